@@ -74,6 +74,8 @@ typedef enum {
 #define PA_DEVERR_SEQ_LEN 4u  /* seq_len < 0 or > max_blocks_per_seq*block_size */
 #define PA_DEVERR_TIMEOUT 8u  /* a bounded wait on an async copy gave up */
 #define PA_DEVERR_PAIR 16u    /* copy_blocks id outside [0, num_blocks) */
+#define PA_DEVERR_QUERY 64u   /* q_starts not ascending within [0, num_tokens], or a sequence of more than max_q_len queries */
+#define PA_DEVERR_PATH 128u   /* a tree path longer than its row, or a node outside its sequence's tree */
 #define PA_DEVERR_INTERNAL 32u /* a sizing invariant of the library failed (a bug; the result is wrong) */
 
 /*
@@ -382,6 +384,180 @@ int pa_decode_noalloc(void* out, pa_dtype out_dtype,
 
 /* Size in bytes of the fixed device array pa_decode_noalloc uses. */
 size_t pa_decode_noalloc_capacity(void);
+
+/*
+ * pa_rope_and_cache - rotary positions of a step's queries and keys, and the
+ * cache write of its keys and values, in one launch.
+ *
+ * For token n at position p = positions[n] and pair i < rotary_dim / 2, with
+ * the angle a = p * inv_freq[i] (the product of the integer and the float32
+ * value; reduced exactly, so far positions keep their precision up to
+ * |p| < 2^31):
+ *     (x, y) -> rope_scale * (x cos a - y sin a, y cos a + x sin a)
+ * where (x, y) are columns (2i, 2i + 1) of a head (interleaved != 0) or
+ * (i, i + rotary_dim / 2) (interleaved == 0); columns from rotary_dim on pass
+ * unchanged.  Computed in float32; q_out and 16-bit caches are rounded to
+ * their type once, 8-bit caches quantise the float32 value of the rotated key
+ * (as pa_reshape_and_cache quantises its source).  The queries go to q_out,
+ * the rotated keys and the values into cache slot slot_mapping[n].
+ * A token with slot_mapping[n] < 0 is padding: nothing is written for it, not
+ * its row of q_out either.  A slot outside the pool sets PA_DEVERR_SLOT and
+ * the token is skipped in the same way.
+ *
+ *   q, q_out       [num_tokens][num_heads][head_dim] at q_stride / q_out_stride
+ *                  elements per token; q_out may be q itself (in place) but
+ *                  must not overlap it otherwise
+ *   k, v, caches, slot_mapping, scales, opt   as pa_reshape_and_cache_ex
+ *   positions      int64 [num_tokens]
+ *   inv_freq       float32 [rotary_dim / 2]
+ *   rotary_dim     even, 2 <= rotary_dim <= head_dim
+ *   rope_scale     factor on both cos and sin (1 for the plain rotation)
+ */
+int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, int num_heads,
+                      const void* k, const void* v, pa_dtype src_dtype, int64_t k_stride, int64_t v_stride,
+                      void* k_cache, void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                      const int64_t* positions, const int64_t* slot_mapping, const float* inv_freq,
+                      int rotary_dim, int interleaved, float rope_scale,
+                      int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                      const float* k_inv_scale, const float* v_inv_scale,
+                      const pa_cache_write_options* opt, void* stream);
+
+/*
+ * pa_attend - attention of ragged query rows over the paged cache, with
+ * modifiers of the scores: prompt chunks, decode steps, trees of drafted
+ * tokens.
+ *
+ * Sequence s has L = q_starts[s+1] - q_starts[s] queries, rows q_starts[s] ..
+ * of q; its cache holds T = seq_lens[s] tokens, the queries' own among them:
+ * query i sits at position P = T - L + i.  For query head h:
+ *     z_t = scale * q . k_t
+ *     z_t = softcap * tanh(z_t / softcap)          when softcap > 0
+ *     z_t = z_t - slopes[h] * |P - t|              when slopes is given
+ *     out = sum_t softmax(z)_t v_t                 over the visible t < T
+ * Visible are
+ *     t <= P, and with a window only t > P - window;
+ *     and also every t < prefix_lens[s] when prefix_lens is given;
+ *   or, when tree_mask is given (the queries are the nodes of a tree of
+ *   drafted tokens, their rows in the cache at T - L .. T - 1),
+ *     every t < T - L, and t = T - L + j when bit j of the query's mask row
+ *     is set (its own bit is not implied).
+ * What a masked position holds does not matter (infinities and NaN too, in K
+ * and in V).  A query that sees nothing, or whose position is negative
+ * (T < L), gets out = 0.  Rows of out from q_starts[num_seqs] on, and before
+ * q_starts[0], are left as they were.
+ *
+ *   out            [num_tokens][num_heads][head_dim], out_dtype F32/F16/BF16,
+ *                  16-byte aligned
+ *   q              the same at q_stride elements per token, q_dtype F16/BF16
+ *   caches, scales, block_tables, seq_lens     as pa_decode
+ *   q_starts       int32 [num_seqs + 1]; NULL: one query per sequence, row s
+ *   max_q_len      at least the largest L; a sequence with more queries, or a
+ *                  range outside [0, num_tokens], sets PA_DEVERR_QUERY and is
+ *                  skipped
+ *   num_heads      1 <= num_heads / num_kv_heads <= 64
+ *   num_seqs       at most 4096
+ *   workspace      >= pa_attend_workspace_bytes(...) bytes, 256-byte aligned,
+ *                  zero-filled before its first use (a completed call leaves
+ *                  it ready for the next; after PA_DEVERR_TIMEOUT zero it
+ *                  again).  Calls that share a workspace must not overlap.
+ *
+ * Options (struct_size as for pa_decode_options):
+ *   softcap        >= 0; 0 = off
+ *   slopes         float32 [num_heads], or NULL
+ *   window         >= 0; 0 = off.  Not together with prefix_lens or tree_mask
+ *   prefix_lens    int32 [num_seqs], or NULL (values above T count as T)
+ *   tree_mask      uint64 [num_tokens][tree_words], or NULL; bit j % 64 of word
+ *                  j / 64.  max_q_len <= 64 * tree_words.  Not together with
+ *                  slopes, window or prefix_lens
+ *   mass           float32 [num_seqs][num_kv_heads][...], or NULL: one query
+ *                  per sequence only (max_q_len 1); mass[s][kvh][t] += the sum
+ *                  over the group's query heads of softmax(z)_t, for every t <
+ *                  T (what a position beyond T holds is left as it was).
+ *                  mass_stride_seq / mass_stride_head elements apart, rows of
+ *                  at least max_blocks_per_seq * block_size elements
+ *   k_zero_point / v_zero_point   as pa_decode_options
+ *   pdl            as pa_decode_options, but nothing at all is read before the
+ *                  kernel before this call has finished
+ */
+typedef struct pa_attend_options {
+  size_t struct_size;
+  const int32_t* k_zero_point;
+  const int32_t* v_zero_point;
+  float softcap;
+  const float* slopes;
+  int32_t window;
+  const int32_t* prefix_lens;
+  const uint64_t* tree_mask;
+  int32_t tree_words;
+  float* mass;
+  int64_t mass_stride_seq;
+  int64_t mass_stride_head;
+  int32_t pdl;
+} pa_attend_options;
+
+int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype, int64_t q_stride,
+              const void* k_cache, const void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+              const float* k_scale, const float* v_scale,
+              const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+              const int32_t* q_starts, int max_q_len, int num_tokens,
+              int num_seqs, int num_heads, int num_kv_heads, int head_dim, float scale, int block_size,
+              void* workspace, size_t workspace_bytes, const pa_attend_options* opt, void* stream);
+
+/* Bytes of workspace pa_attend needs for these sizes on the current device
+ * ((size_t)-1 when they are rejected or no device is usable); accumulate
+ * nonzero: with the mass option. */
+size_t pa_attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                 int max_blocks_per_seq, int max_q_len, pa_dtype kv_dtype, int accumulate);
+
+/*
+ * pa_commit_tree - keeps the accepted path of each sequence's drafted tree:
+ * the cache rows (K and V, every KV head) of positions T - L + path[s][i] move
+ * to positions T - L + i, i < path_lens[s], and new_lens[s] = T - L +
+ * path_lens[s].  Every row of a sequence is read before any is written, so the
+ * path may name the nodes in any order.  The blocks of the span T - L .. T - 1
+ * must belong to one sequence alone (copy-on-write gives them before the draft
+ * is written).  L as in pa_attend.  A path longer than max_path or than L, a
+ * node outside [0, L) or T < L sets PA_DEVERR_PATH: nothing of that sequence
+ * moves and new_lens[s] = seq_lens[s].
+ *   path           int32 [num_seqs][max_path], 1 <= max_path <= 256
+ *   path_lens      int32 [num_seqs]
+ *   new_lens       int32 [num_seqs] (not seq_lens itself)
+ */
+int pa_commit_tree(void* k_cache, void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                   const int32_t* q_starts, const int32_t* path, const int32_t* path_lens, int max_path,
+                   int32_t* new_lens, int num_seqs, int num_kv_heads, int head_dim, int block_size, void* stream);
+
+/*
+ * pa_evict - cuts sequences back to `budget` cached tokens by the attention
+ * weight that pa_attend's mass option has added up.
+ *
+ * A sequence of T = seq_lens[s] <= budget tokens keeps them all.  A longer one
+ * keeps, per KV head, its first `sinks` and its last `recent` positions and,
+ * of the others, the budget - sinks - recent with the largest mass (equal ones:
+ * the lower position first; NaN counts below everything).  With the kept
+ * positions ascending, row i of the K and V caches through dst_tables[s]
+ * receives row kept[s][h][i] through block_tables[s], mass_out[s][h][i] =
+ * mass[s][h][kept[s][h][i]], and new_lens[s] = min(T, budget).  Entries of kept
+ * and mass_out from new_lens[s] on, and the source blocks, are left as they
+ * were.  The destination blocks must be none of the source blocks of the call
+ * (fresh ones, as for copy-on-write), so shared source blocks stay intact.
+ *
+ *   mass           float32 [num_seqs][num_kv_heads] rows, strides as pa_attend
+ *   dst_tables     int32 [num_seqs][max_dst_blocks], max_dst_blocks*block_size >=
+ *                  min(budget, max_blocks_per_seq*block_size); entries beyond
+ *                  ceil(new_lens[s] / block_size) are not read
+ *   kept           int32 [num_seqs][num_kv_heads][budget]
+ *   mass_out       float32 [num_seqs][num_kv_heads][budget]
+ *   new_lens       int32 [num_seqs] (not seq_lens itself)
+ *   budget >= 1, recent >= 0, sinks >= 0, recent + sinks <= budget
+ */
+int pa_evict(void* k_cache, void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+             const float* mass, int64_t mass_stride_seq, int64_t mass_stride_head,
+             const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+             const int32_t* dst_tables, int max_dst_blocks, int32_t* kept, float* mass_out, int32_t* new_lens,
+             int num_seqs, int num_kv_heads, int head_dim, int block_size, int budget, int recent, int sinks,
+             void* stream);
 
 /* Human-readable name of a pa_status value (static string). */
 const char* pa_status_string(int status);

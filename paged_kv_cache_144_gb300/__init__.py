@@ -1,4 +1,4 @@
-"""GB300 (sm_103a) paged decode attention: decode, cache write and CoW block copy.
+"""GB300 (sm_103a) paged attention: decode, cache write, CoW block copy and the operators around them.
 
 The compute path is libpagedattn.so (hand-written CUDA kernels behind the C ABI
 in include/pa.h); this package holds its build script, the ctypes binding and
@@ -17,6 +17,10 @@ from ._lib import (  # noqa: F401
     pa_debug_set_decode_wait,
     decode, reshape_and_cache, copy_blocks, decode_workspace_bytes, new_workspace, get_device_error,
     dtype_code,
+)
+from ._lib import PA_DEVERR_QUERY, PA_DEVERR_PATH, AttendOptions  # noqa: F401
+from ._ops import (  # noqa: F401
+    rope_frequencies, rope_and_cache, attend, attend_tree, attend_accumulate, attend_workspace_bytes, commit_tree, evict,
 )
 from .block_manager import BlockManager  # noqa: F401
 from .step_graph import StepGraph  # noqa: F401

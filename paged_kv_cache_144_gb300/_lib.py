@@ -19,6 +19,7 @@ PA_OK = 0
 PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_DTYPE, PA_ERR_UNSUPPORTED = -1, -2, -3, -4
 PA_ERR_WORKSPACE, PA_ERR_CUDA, PA_ERR_ALIGN = -5, -6, -7
 PA_DEVERR_BLOCK_ID, PA_DEVERR_SLOT, PA_DEVERR_SEQ_LEN, PA_DEVERR_TIMEOUT, PA_DEVERR_PAIR = 1, 2, 4, 8, 16
+PA_DEVERR_QUERY, PA_DEVERR_PATH = 64, 128
 SIZE_MAX = ctypes.c_size_t(-1).value
 
 _vp, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -44,6 +45,18 @@ class CacheWriteOptions(ctypes.Structure):
         super().__init__(struct_size=ctypes.sizeof(CacheWriteOptions), **kw)
 
 
+class AttendOptions(ctypes.Structure):
+    """pa_attend_options (include/pa.h)."""
+    _fields_ = [("struct_size", ctypes.c_size_t), ("k_zero_point", ctypes.c_void_p),
+                ("v_zero_point", ctypes.c_void_p), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("window", ctypes.c_int32), ("prefix_lens", ctypes.c_void_p), ("tree_mask", ctypes.c_void_p),
+                ("tree_words", ctypes.c_int32), ("mass", ctypes.c_void_p), ("mass_stride_seq", ctypes.c_int64),
+                ("mass_stride_head", ctypes.c_int64), ("pdl", ctypes.c_int32)]
+
+    def __init__(self, **kw):
+        super().__init__(struct_size=ctypes.sizeof(AttendOptions), **kw)
+
+
 _SIGNATURES = {
     "pa_decode_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32]),
     "pa_decode_workspace_bytes_ex": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
@@ -57,6 +70,16 @@ _SIGNATURES = {
     "pa_reshape_and_cache_ex": (_i32, [_vp, _vp, _i32, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i32, _i32,
                                        _i32, _vp, _vp, ctypes.POINTER(CacheWriteOptions), _vp]),
     "pa_copy_blocks": (_i32, [_vp, _vp, _i64, _sz, _vp, _i32, _vp]),
+    "pa_rope_and_cache": (_i32, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _i64, _i64, _vp, _vp, _i32, _i64, _vp,
+                                 _vp, _vp, _i32, _i32, _f32, _i32, _i32, _i32, _i32, _vp, _vp,
+                                 ctypes.POINTER(CacheWriteOptions), _vp]),
+    "pa_attend": (_i32, [_vp, _i32, _vp, _i32, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32,
+                         _i32, _i32, _i32, _i32, _f32, _i32, _vp, _sz, ctypes.POINTER(AttendOptions), _vp]),
+    "pa_attend_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "pa_commit_tree": (_i32, [_vp, _vp, _i32, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
+                              _vp]),
+    "pa_evict": (_i32, [_vp, _vp, _i32, _i64, _vp, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32,
+                        _i32, _i32, _i32, _i32, _i32, _vp]),
     "pa_status_string": (ctypes.c_char_p, [_i32]),
     "pa_get_device_error": (_i32, [_vp, ctypes.POINTER(ctypes.c_uint)]),
     "pa_version": (_i32, []),

@@ -26,6 +26,10 @@ LIB_PATH = os.path.join(PKG_DIR, "libpagedattn.so")
 SOURCES = [
     "pa_api.cu",
     "pa_cache.cu",
+    "pa_ops_api.cu",
+    "pa_rope.cu",
+    "pa_attend.cu",
+    "pa_evict.cu",
     "pa_decode_dispatch.cu",
     "pa_decode_f16.cu",
     "pa_decode_bf16.cu",

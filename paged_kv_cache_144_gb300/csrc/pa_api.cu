@@ -20,8 +20,10 @@ __device__ unsigned int g_device_error = 0u;
 
 constexpr int kMaxDevices = 64;
 
+}  // namespace
+
 // Device address of g_device_error on the current device (nullptr on failure).
-unsigned int* device_error_word() {
+unsigned int* pa::device_error_word() {
   static unsigned int* addr[kMaxDevices] = {};
   static std::mutex mu;
   int dev = 0;
@@ -35,14 +37,21 @@ unsigned int* device_error_word() {
   return addr[dev];
 }
 
+namespace {
 // Text of the last CUDA error a call on this thread returned PA_ERR_CUDA for.
 thread_local char g_last_error[512] = "";
+}  // namespace
 
-int cuda_status(cudaError_t e, const char* where) {
+int pa::cuda_status(cudaError_t e, const char* where) {
   if (e == cudaSuccess) return PA_OK;
   snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%s)", where, cudaGetErrorString(e), cudaGetErrorName(e));
   return PA_ERR_CUDA;
 }
+
+namespace {
+
+using pa::cuda_status;
+using pa::device_error_word;
 
 constexpr int kMaxSeqs = 16384;  // prefix sums of the batch live in shared memory
 constexpr int kMaxQueryRows = 64;  // q_len * G: up to four 16-row consumer warps share a ring
@@ -60,7 +69,9 @@ int dtype_bytes(int dt) {
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 pa::tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -73,6 +84,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
+
+namespace {
+
+using pa::tensor_map_encoder;
 
 // 3-D view of a cache pool: {128 bytes of a row, rows, 128-byte halves of a
 // row}, with num_blocks*Hkv*B rows of head_dim elements.  One TMA box =

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -24,6 +25,11 @@ constexpr int kBoxRowQuantum = 8;
 
 // Integer tuning override from the environment (read once per name), or -1.
 int tuning_override(const char* name);
+
+// Shared by the translation units that hold entry points.
+unsigned int* device_error_word();                       // of the current device (nullptr on failure)
+int cuda_status(cudaError_t e, const char* where);       // PA_OK or PA_ERR_CUDA with the error's text recorded
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // nullptr when the driver has none
 
 struct ReshapeArgs {
   const void* k;

@@ -1,0 +1,249 @@
+// pa_rope.cu - rotary positions of a step's queries and keys fused with the
+// cache write of its keys and values.
+//
+// Mathematics: pair i of a head at position p turns by the angle a = p *
+// inv_freq[i].  In units of a full turn, t = inv_freq / 2 pi is held as a
+// signed 64-bit fraction of a turn (its distance from the nearest whole turn
+// times 2^64); p * t then wraps modulo one turn by itself in 64-bit integer
+// arithmetic, so the reduction of a far position's angle is exact and needs no
+// 64-bit floating point per token.  The top 32 bits of the product are the
+// angle, 2^-33 turns at most from it, and go to sincospif.
+//
+// Work: a CTA takes kTokens tokens; its threads first compute the tokens'
+// rotary_dim / 2 angles once (shared memory), then move the token's heads
+// 8 elements (16 bytes) at a time: a unit is one 16-byte chunk of a head
+// (interleaved pairs lie inside it) or, in the half layout, the two chunks that
+// hold both halves of 8 pairs, so one thread reads and writes both elements of
+// every pair it turns and q may be turned in place.
+#include "pa_common.cuh"
+#include "pa_ops.h"
+
+namespace pa {
+namespace {
+
+enum Mode { kCopy = 0, kToFp8 = 1, kToInt8 = 2 };
+// kHalfAny: half layout whose rotary_dim / 2 is no multiple of 8, so the second halves are not
+// 16-byte chunks: one pair (or one passed column) per unit, 2-byte accesses.
+enum Layout { kInterleaved = 0, kHalf = 1, kHalfAny = 2 };
+
+constexpr int kThreads = 128;
+constexpr int kTokens = 2;
+
+struct Dst {  // where a head's row goes
+  uint8_t* row;
+  float inv;  // 8-bit caches
+  int zp;     // INT8
+  bool cache;
+};
+
+// 8 consecutive values from column c on
+template <typename SRC, int MODE>
+__device__ __forceinline__ void store8(const Dst& d, int c, const float (&x)[8]) {
+  constexpr bool BF = std::is_same<SRC, bf16_t>::value;
+  if (MODE == kCopy || !d.cache) {
+    uint4 w;
+    w.x = pack2<BF>(x[0], x[1]);
+    w.y = pack2<BF>(x[2], x[3]);
+    w.z = pack2<BF>(x[4], x[5]);
+    w.w = pack2<BF>(x[6], x[7]);
+    *reinterpret_cast<uint4*>(d.row + 2 * c) = w;
+  } else {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], d.inv);
+    uint32_t w[2];
+    if constexpr (MODE == kToFp8) {
+      w[0] = e4m3x2_code(y[0], y[1]) | (e4m3x2_code(y[2], y[3]) << 16);
+      w[1] = e4m3x2_code(y[4], y[5]) | (e4m3x2_code(y[6], y[7]) << 16);
+    } else {
+      w[0] = w[1] = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i >> 2] |= (static_cast<uint32_t>(int8_code(y[i], d.zp)) & 0xffu) << (8 * (i & 3));
+    }
+    *reinterpret_cast<uint2*>(d.row + c) = make_uint2(w[0], w[1]);
+  }
+}
+
+template <typename SRC, int MODE>
+__device__ __forceinline__ void store1(const Dst& d, int c, float x) {
+  if (MODE == kCopy || !d.cache) {
+    reinterpret_cast<uint16_t*>(d.row)[c] =
+        static_cast<uint16_t>(pack2<std::is_same<SRC, bf16_t>::value>(x, 0.f) & 0xffffu);
+  } else if constexpr (MODE == kToFp8) {
+    d.row[c] = static_cast<uint8_t>(e4m3x2_code(__fmul_rn(x, d.inv), 0.f) & 0xffu);
+  } else {
+    d.row[c] = static_cast<uint8_t>(int8_code(__fmul_rn(x, d.inv), d.zp));
+  }
+}
+
+template <typename SRC>
+__device__ __forceinline__ void load8(const uint8_t* row, int c, float (&x)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(row + 2 * c);
+  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = widen2<SRC>(r[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+template <typename SRC, int MODE, int D, int LAYOUT>
+__global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ float2 cs[kTokens][D / 2];
+  const ReshapeArgs& w = a.w;
+  const int half = a.rotary_dim >> 1;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kTokens;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(kTokens), w.num_tokens - n0));
+
+  for (int x = threadIdx.x; x < nt * half; x += kThreads) {
+    const int t = x / half, i = x - t * half;
+    const double turns = static_cast<double>(__ldg(a.inv_freq + i)) * 0.15915494309189533577;  // 1 / 2 pi
+    const double frac = turns - rint(turns);
+    const unsigned long long step = static_cast<unsigned long long>(__double2ll_rn(frac * 18446744073709551616.0));
+    const unsigned long long phase = step * static_cast<unsigned long long>(a.positions[n0 + t]);
+    const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
+    float sn, c;
+    sincospif(half_turns, &sn, &c);
+    cs[t][i] = make_float2(c * a.rope_scale, sn * a.rope_scale);
+  }
+  __syncthreads();
+
+  const int Hq = a.num_heads, Hk = w.num_kv_heads;
+  // units of a turned head, and of a copied one (V)
+  const int turned = LAYOUT == kInterleaved ? D / 8
+                     : LAYOUT == kHalf      ? (half >> 3) + (D - a.rotary_dim) / 8
+                                            : half + (D - a.rotary_dim);
+  const int copied = D / 8;
+  const int units = (Hq + Hk) * turned + Hk * copied;
+  const int kvb = MODE == kCopy ? 2 : 1;
+  for (int x = threadIdx.x; x < nt * units; x += kThreads) {
+    const int t = x / units;
+    int u = x - t * units;
+    const int64_t n = n0 + t;
+    const int64_t slot = w.slot_mapping[n];
+    if (slot < 0) continue;  // padding token
+    if (slot >= w.num_blocks * w.block_size) {
+      if (u == 0) raise_error(w.err, PA_DEVERR_SLOT);
+      continue;
+    }
+    int head, which;  // which: 0 = q, 1 = k, 2 = v
+    if (u < (Hq + Hk) * turned) {
+      head = u / turned;
+      u -= head * turned;
+      which = head < Hq ? 0 : 1;
+      head -= which ? Hq : 0;
+    } else {
+      u -= (Hq + Hk) * turned;
+      head = u / copied;
+      u -= head * copied;
+      which = 2;
+    }
+    const uint8_t* src;
+    Dst d;
+    d.cache = which != 0;
+    d.inv = 1.f;
+    d.zp = 0;
+    if (which == 0) {
+      src = static_cast<const uint8_t*>(a.q) + (n * a.q_stride + static_cast<int64_t>(head) * D) * 2;
+      d.row = static_cast<uint8_t*>(a.q_out) + (n * a.q_out_stride + static_cast<int64_t>(head) * D) * 2;
+    } else {
+      src = static_cast<const uint8_t*>(which == 1 ? w.k : w.v) +
+            (n * (which == 1 ? w.k_stride : w.v_stride) + static_cast<int64_t>(head) * D) * 2;
+      const int64_t blk = slot / w.block_size, off = slot - blk * w.block_size;
+      d.row = static_cast<uint8_t*>(which == 1 ? w.k_cache : w.v_cache) +
+              ((blk * Hk + head) * w.block_size + off) * D * kvb;
+      if constexpr (MODE != kCopy) d.inv = __ldg((which == 1 ? w.k_inv_scale : w.v_inv_scale) + head);
+      if constexpr (MODE == kToInt8) d.zp = __ldg((which == 1 ? w.k_zero_point : w.v_zero_point) + head);
+    }
+    float lo[8];
+    if (which == 2) {
+      load8<SRC>(src, 8 * u, lo);
+      store8<SRC, MODE>(d, 8 * u, lo);
+    } else if constexpr (LAYOUT == kInterleaved) {
+      load8<SRC>(src, 8 * u, lo);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (4 * u + i < half) {
+          const float2 f = cs[t][4 * u + i];
+          const float p = lo[2 * i], q = lo[2 * i + 1];
+          lo[2 * i] = p * f.x - q * f.y;
+          lo[2 * i + 1] = q * f.x + p * f.y;
+        }
+      }
+      store8<SRC, MODE>(d, 8 * u, lo);
+    } else if constexpr (LAYOUT == kHalf) {
+      if (u < (half >> 3)) {
+        float hi[8];
+        load8<SRC>(src, 8 * u, lo);
+        load8<SRC>(src, half + 8 * u, hi);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = cs[t][8 * u + i];
+          const float p = lo[i], q = hi[i];
+          lo[i] = p * f.x - q * f.y;
+          hi[i] = q * f.x + p * f.y;
+        }
+        store8<SRC, MODE>(d, 8 * u, lo);
+        store8<SRC, MODE>(d, half + 8 * u, hi);
+      } else {
+        const int c = a.rotary_dim + 8 * (u - (half >> 3));
+        load8<SRC>(src, c, lo);
+        store8<SRC, MODE>(d, c, lo);
+      }
+    } else {
+      if (u < half) {
+        const float2 f = cs[t][u];
+        const float p = load_scalar<SRC>(src, u), q = load_scalar<SRC>(src, half + u);
+        store1<SRC, MODE>(d, u, p * f.x - q * f.y);
+        store1<SRC, MODE>(d, half + u, q * f.x + p * f.y);
+      } else {
+        const int c = a.rotary_dim + (u - half);
+        store1<SRC, MODE>(d, c, load_scalar<SRC>(src, c));
+      }
+    }
+  }
+}
+
+template <typename SRC, int MODE, int D>
+cudaError_t launch_layout(const RopeArgs& a, cudaStream_t stream) {
+  void (*kern)(RopeArgs) = a.interleaved               ? rope_and_cache_kernel<SRC, MODE, D, kInterleaved>
+                           : (a.rotary_dim % 16 == 0) ? rope_and_cache_kernel<SRC, MODE, D, kHalf>
+                                                      : rope_and_cache_kernel<SRC, MODE, D, kHalfAny>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.w.num_tokens + kTokens - 1) / kTokens));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.w.pdl ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename SRC>
+cudaError_t launch_src(const RopeArgs& a, cudaStream_t stream) {
+  const int mode = a.w.kv_dtype == PA_FP8_E4M3 ? kToFp8 : (a.w.kv_dtype == PA_INT8 ? kToInt8 : kCopy);
+  if (a.w.head_dim == 128) {
+    if (mode == kToFp8) return launch_layout<SRC, kToFp8, 128>(a, stream);
+    if (mode == kToInt8) return launch_layout<SRC, kToInt8, 128>(a, stream);
+    return launch_layout<SRC, kCopy, 128>(a, stream);
+  }
+  if (mode == kToFp8) return launch_layout<SRC, kToFp8, 64>(a, stream);
+  if (mode == kToInt8) return launch_layout<SRC, kToInt8, 64>(a, stream);
+  return launch_layout<SRC, kCopy, 64>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream) {
+  (void)cudaGetLastError();
+  return a.w.src_dtype == PA_F16 ? launch_src<f16_t>(a, stream) : launch_src<bf16_t>(a, stream);
+}
+
+}  // namespace pa
