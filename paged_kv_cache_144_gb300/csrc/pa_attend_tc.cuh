@@ -1,0 +1,956 @@
+// pa_attend_tc.cuh - attention of ragged query rows over the paged cache on
+// the 5th-generation tensor cores (tcgen05), sm_103a.
+//
+// Mathematics.  The queries of one sequence and the G heads that share a KV
+// head form R = L * G rows; S = Q K^T over 128 cached positions at a time, the
+// modifiers and masks of include/pa.h on each score, the running maximum m and
+// sum l of the softmax per row in base 2, O = O + P V.  m only follows the
+// maximum once it is kSlack above it (weights up to 2^kSlack are exact in
+// float32), so O is rarely rescaled.
+//
+// Layout on the SM.  One persistent CTA per SM, 12 warps:
+//   warp 0     TMA producer: K and V tiles of 128 positions, one box per cache
+//              block, into rings of stages
+//   warp 1     issues every tcgen05.mma and owns the TMEM (512 columns: S0, S1,
+//              O0, O1 of 128 lanes x 128 columns; the weights P overwrite S)
+//   warps 2-3  bring the query rows of streams 0 and 1 into shared memory
+//   warps 4-7, 8-11   softmax of streams 0 and 1, one row per thread: the row
+//              maximum and sum need no exchange between threads
+// Two streams alternate, so the tensor cores compute for one while the other's
+// softmax runs.  With more than 128 rows per (sequence, KV head) the streams
+// are two row tiles over the same K/V tiles ("paired": every K/V byte read
+// from L2 serves 256 rows); with up to 128 rows they take the positions' tiles
+// in turn ("alternating") and their results are joined like any other split.
+//
+// Shared-memory tiles are stored as 8-row groups of [128-byte half][8 rows][128
+// bytes] with the 128-byte swizzle, which one 4-D TMA box per block writes for
+// any block size; it is the K-major operand layout of S = Q K^T (row groups
+// NH * 1024 bytes apart) and the MN-major one of P V as it is.
+//
+// Work split.  A segment is (sequence, KV head, row tile).  All segments'
+// position tiles in order, each segment charged kFragCost tiles more for what
+// a fragment costs besides them, are cut into equal contiguous ranges, one per
+// CTA.  A fragment that is not its whole segment leaves (m, l, O) in the
+// workspace and counts itself in; the one that arrives last joins them in
+// order, so the result does not depend on who that is.
+//
+// Rounding.  P enters P V as 16 bits (bf16 with a bf16 cache, else f16 with
+// weights scaled by 2^7, so that small ones stay above its smallest value):
+// half a step of the type, below the rounding of a 16-bit output.  When the
+// split flag is set (float32 outputs; also whenever the memory traffic bounds
+// the call, where the second product is free) P is two such values, hi + lo,
+// and its rounding is that of 16 bits more.
+//
+// A position's V row is multiplied by P = 0 in rows that do not see it, which
+// is not enough when it holds NaN or infinity: rows past the sequence's end (or
+// before the window) are zeroed in shared memory, and a result row that is
+// not finite is computed again by one warp from the definition (attend_row).
+//
+// Every wait on a barrier ends after kDefaultWaitLimitNs with
+// PA_DEVERR_TIMEOUT.
+#pragma once
+
+#include "pa_attend.cuh"
+
+namespace pa {
+
+constexpr int kTile = 128;      // positions per tile, rows per stream
+constexpr int kFragCost = 1;    // tiles charged per fragment
+constexpr float kSlack = 8.f;   // log2 by which the maximum may lag
+constexpr int kTcThreads = 384;
+
+// ----------------------------------------------------------------- tcgen05 wrappers
+
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_addr, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+// 16 columns
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 4-D tiled TMA load global -> shared, completion counted on `bar`.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle: start address, leading
+// and stride byte offsets in 16-byte units, descriptor version 1.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (static_cast<uint64_t>(sbo >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+// Instruction descriptor: float32 accumulators, 16-bit operands, M = 128.
+constexpr uint32_t mma_idesc(bool bf16, bool b_mn_major, int n) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+// ----------------------------------------------------------------- geometry
+
+struct TcParams {
+  AttendParams a;
+  int paired;        // more than 128 rows per (sequence, KV head): the streams are two row tiles
+  int split_p;       // P as hi + lo
+  int rec_rows;      // rows of a record
+  int slots;         // records of one stream per CTA: paired 2, alternating 4
+  int* counters;     // arrivals: paired: by the segment's first CTA; alternating: by s * H_kv + kvh
+  float* records;
+  float* scores;     // mass: scores [S][H_q][score_stride] in the log2 domain
+  int score_stride;
+};
+
+// Position tiles [lo, hi) of row tile m of a sequence.
+struct TileRange {
+  int lo, hi;
+};
+__device__ __forceinline__ TileRange tile_range(const AttendParams& p, const SeqView& v, int prefix, int rows_per_tile, int m) {
+  TileRange r;
+  const int i0 = m * rows_per_tile / p.group;                       // first query with a row in the tile
+  const int i1 = min(v.L, (m * rows_per_tile + rows_per_tile - 1) / p.group + 1) - 1;  // last one
+  const int last = v.T - v.L + i1;
+  if (v.L <= 0 || last < 0) {
+    r.lo = r.hi = 0;
+    return r;
+  }
+  const int first = max(0, v.T - v.L + i0);
+  const int lo = p.window > 0 ? max(0, first + 1 - p.window) : 0;
+  const int hi = p.tree_mask ? v.T : max(last + 1, prefix);
+  r.lo = lo / kTile;
+  r.hi = (hi + kTile - 1) / kTile;
+  return r;
+}
+
+struct Frag {
+  int s, kvh, m;      // segment
+  SeqView v;
+  int prefix;         // visible prefix length
+  int t0, t1;         // its position tiles
+  int lo;             // first position any row of the segment sees
+  int seg_start;      // cost position of the segment
+  int seg_tiles;
+  bool whole;
+  int idx;            // ordinal in the CTA
+};
+
+// Walks the fragments of one CTA's range of cost positions.
+struct FragIter {
+  int u, u1, U, nw;
+  int s, seg_cost_sum;  // sequence, its cost per KV head
+  int m, m_pos;         // row tile being looked at and its position within the head (scan state)
+  int kvh;
+  int s_state;          // sequence the scan state belongs to (-1: none)
+  int idx;
+};
+
+__device__ __forceinline__ int seg_cost(int tiles) { return tiles > 0 ? tiles + kFragCost : 0; }
+
+// A warp's iterator and its current fragment live in shared memory, not in its registers.
+struct WarpFrag {
+  FragIter it;
+  Frag f;
+};
+
+__device__ __forceinline__ bool advance_frag(FragIter& it, Frag& f, const int* prefix, const TcParams& p) {
+  const AttendParams& a = p.a;
+  const int rpt = p.paired ? 2 * kTile : kTile;
+  while (it.u < it.u1) {
+    while (prefix[it.s + 1] <= it.u) ++it.s;  // last sequence starting at or before u (u < U: one exists)
+    const int per = (prefix[it.s + 1] - prefix[it.s]) / a.num_kv_heads;
+    const int r = it.u - prefix[it.s];
+    const int kvh = r / per;
+    const int off = r - kvh * per;
+    const SeqView v = seq_view(a, it.s, false);
+    const int pre = seq_prefix(a, it.s, v.T);
+    if (it.s_state != it.s || it.kvh != kvh || off < it.m_pos) {
+      it.m = 0;
+      it.m_pos = 0;
+      it.s_state = it.s;
+      it.kvh = kvh;
+    }
+    TileRange tr = tile_range(a, v, pre, rpt, it.m);
+    while (off >= it.m_pos + seg_cost(tr.hi - tr.lo)) {
+      it.m_pos += seg_cost(tr.hi - tr.lo);
+      ++it.m;
+      tr = tile_range(a, v, pre, rpt, it.m);
+    }
+    const int n = tr.hi - tr.lo;
+    const int seg_start = prefix[it.s] + kvh * per + it.m_pos;
+    const int fend = min(it.u1, seg_start + n + kFragCost);
+    const int ja = max(0, it.u - seg_start - kFragCost), jb = fend - seg_start - kFragCost;
+    it.u = fend;
+    if (jb <= ja) continue;  // the range ends inside the segment's overhead
+    f.s = it.s;
+    f.kvh = kvh;
+    f.m = it.m;
+    f.v = v;
+    f.prefix = pre;
+    f.t0 = tr.lo + ja;
+    f.t1 = tr.lo + jb;
+    f.lo = a.window > 0 ? max(0, max(0, v.T - v.L + it.m * rpt / a.group) + 1 - a.window) : 0;
+    f.seg_start = seg_start;
+    f.seg_tiles = n;
+    f.whole = ja == 0 && jb == n;
+    f.idx = it.idx++;
+    return true;
+  }
+  return false;
+}
+
+// The warp's next fragment (all lanes call it); false at the end of the CTA's range.
+__device__ __forceinline__ bool next_frag(WarpFrag* w, const int* prefix, const TcParams& p) {
+  FragIter it = w->it;
+  Frag f;
+  const bool more = advance_frag(it, f, prefix, p);
+  __syncwarp();  // every lane has read the old state
+  if ((threadIdx.x & 31) == 0) {
+    w->it = it;
+    if (more) w->f = f;
+  }
+  __syncwarp();
+  return more;
+}
+
+// CTA whose range holds cost position x.
+__device__ __forceinline__ int cta_of(int x, int U, int nw) {
+  return static_cast<int>((static_cast<long long>(x + 1) * nw - 1) / U);
+}
+__device__ __forceinline__ int range_start(int c, int U, int nw) {
+  return static_cast<int>(static_cast<long long>(c) * U / nw);
+}
+// Tiles of a segment (its cost position, its tiles) in CTA c's range.
+__device__ __forceinline__ int tiles_in(int c, int U, int nw, int seg_start, int seg_tiles) {
+  const int b = max(0, range_start(c, U, nw) - seg_start - kFragCost);
+  return min(seg_tiles, range_start(c + 1, U, nw) - seg_start - kFragCost) - b;
+}
+// Which of a CTA's records its fragment of a segment fills: 0: the CTA's first fragment, 1: a later one (both cut), 2 and
+// 3: whole segments in turn (alternating streams: two contributions of one CTA).
+__device__ __forceinline__ int slot_kind_of(bool whole, int idx) { return whole ? 2 + (idx & 1) : (idx == 0 ? 0 : 1); }
+// The same for CTA c of a cut segment, seen from outside: a range that starts before the segment holds a fragment before it.
+__device__ __forceinline__ int cut_slot_kind(int c, int c0, int U, int nw, int seg_start) {
+  return c > c0 || range_start(c, U, nw) >= seg_start ? 0 : 1;
+}
+
+template <typename KVT, int D>
+struct TcTraits {
+  static constexpr bool BF16 = std::is_same<KVT, bf16_t>::value;
+  static constexpr int NH = D * 2 / 128;           // 128-byte halves per 16-bit row
+  static constexpr int GROUP = NH * 1024;          // bytes of 8 rows
+  static constexpr int TILE_BYTES = kTile / 8 * GROUP;
+  static constexpr int NST = D == 128 ? 2 : 4;     // stages of K and of V
+  static constexpr int OFF_Q = 0;                  // two tiles
+  static constexpr int OFF_K = 2 * TILE_BYTES;
+  static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_V + NST * TILE_BYTES;
+  // barriers (8 bytes each)
+  static constexpr int KF = 0, KE = KF + NST, VF = KE + NST, VE = VF + NST, QF = VE + NST, QE = QF + 2, SF = QE + 2,
+                       PF = SF + 2, OD = PF + 2, RB = OD + 2, NBAR = RB + 2;
+  static constexpr int OFF_MISC = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;  // tmem address, flags, scan scratch
+  static constexpr int OFF_ROWQ = OFF_MISC + 256;                         // attend_row: D floats per softmax warp
+  static constexpr int OFF_FRAG = OFF_ROWQ + 8 * D * 4;                   // WarpFrag per warp, one more for warp 1
+  static constexpr int OFF_PREFIX = OFF_FRAG + (13 * static_cast<int>(sizeof(WarpFrag)) + 15) / 16 * 16;
+  static size_t smem_bytes(int num_seqs) { return 1024 + OFF_PREFIX + static_cast<size_t>(num_seqs + 1) * 4; }
+};
+
+// attend_row out of line: it runs only for rows whose result is not finite
+template <typename KVT, int D>
+__device__ __noinline__ float2 attend_row_again(const AttendParams& p, int s, const SeqView& v, int i, int h, float* qs) {
+  return attend_row<KVT, D>(p, s, v, i, h, qs);
+}
+
+// ----------------------------------------------------------------- kernel
+
+template <typename KVT, int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                 const __grid_constant__ TcParams p) {
+  using Tr = TcTraits<KVT, D>;
+  constexpr int NST = Tr::NST;
+  const AttendParams& a = p.a;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const sm = smem_raw + (base - raw);
+  const uint32_t bars = base + Tr::OFF_BAR;
+  int* const misc = reinterpret_cast<int*>(sm + Tr::OFF_MISC);
+  int* const prefix = reinterpret_cast<int*>(sm + Tr::OFF_PREFIX);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = a.num_seqs;
+  auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+  auto wait = [&](int i, uint32_t parity) -> bool {
+    if (mbar_wait_bounded(bar(i), parity, kDefaultWaitLimitNs)) return true;
+    raise_error(a.err, PA_DEVERR_TIMEOUT);
+    return false;
+  };
+
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmap_k);
+    prefetch_tensormap(&tmap_v);
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(bar(Tr::KF + i), 1);
+      mbar_init(bar(Tr::KE + i), 1);
+      mbar_init(bar(Tr::VF + i), 1);
+      mbar_init(bar(Tr::VE + i), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(Tr::QF + t), 1);
+      mbar_init(bar(Tr::QE + t), 1);
+      mbar_init(bar(Tr::SF + t), 1);
+      mbar_init(bar(Tr::PF + t), 4);
+      mbar_init(bar(Tr::OD + t), 1);
+      mbar_init(bar(Tr::RB + t), 4);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(base + Tr::OFF_MISC, 512);
+  griddep_wait();
+
+  // ---- cost positions before each sequence (every CTA computes the same)
+  {
+    const int rpt = p.paired ? 2 * kTile : kTile;
+    int carry = 0;
+    constexpr int NW = kTcThreads / 32;
+    int* const wsum = misc + 8;
+    for (int s0 = 0; s0 < S; s0 += p.paired ? NW : kTcThreads) {
+      int cost = 0, s;
+      if (p.paired) {  // a warp per sequence, its lanes over the row tiles
+        s = s0 + warp;
+        if (s < S) {
+          const SeqView v = seq_view(a, s, blockIdx.x == 0 && lane == 0);
+          const int pre = seq_prefix(a, s, v.T);
+          const int nm = (v.L * a.group + rpt - 1) / rpt;
+          for (int m = lane; m < nm; m += 32) {
+            const TileRange tr = tile_range(a, v, pre, rpt, m);
+            cost += seg_cost(tr.hi - tr.lo);
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
+        cost *= a.num_kv_heads;
+        if (lane == 0) wsum[warp] = cost;
+        __syncthreads();
+        int before = carry, all = 0;
+        for (int w = 0; w < NW; ++w) {
+          before += w < warp ? wsum[w] : 0;
+          all += wsum[w];
+        }
+        if (lane == 0 && s < S) prefix[s] = before;
+        carry += all;
+      } else {
+        s = s0 + threadIdx.x;
+        if (s < S) {
+          const SeqView v = seq_view(a, s, blockIdx.x == 0);
+          const TileRange tr = tile_range(a, v, seq_prefix(a, s, v.T), rpt, 0);
+          cost = seg_cost(tr.hi - tr.lo) * a.num_kv_heads;
+        }
+        int x = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (lane == 31) wsum[warp] = x;
+        __syncthreads();
+        int before = carry, all = 0;
+        for (int w = 0; w < NW; ++w) {
+          before += w < warp ? wsum[w] : 0;
+          all += wsum[w];
+        }
+        if (s < S) prefix[s] = before + x - cost;
+        carry += all;
+      }
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) prefix[S] = carry;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  const int U = prefix[S];
+  const int want = (U + kFragCost) / (kFragCost + 1);  // at least one tile per CTA
+  const int nw = min(static_cast<int>(gridDim.x), max(want, 1));
+  FragIter it;
+  it.U = U;
+  it.nw = nw;
+  it.idx = 0;
+  it.s = 0;
+  it.s_state = -1;
+  it.m = it.m_pos = it.kvh = 0;
+  it.u = it.u1 = 0;
+  if (static_cast<int>(blockIdx.x) < nw && U > 0) {
+    it.u = range_start(blockIdx.x, U, nw);
+    it.u1 = range_start(blockIdx.x + 1, U, nw);
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {  // last sequence with prefix <= u
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= it.u) lo = mid; else hi = mid - 1;
+    }
+    it.s = lo;
+  }
+  WarpFrag* const wf = reinterpret_cast<WarpFrag*>(sm + Tr::OFF_FRAG) + warp;
+  if (lane == 0) wf->it = it;
+  if (threadIdx.x == 32) wf[11].it = it;  // warp 1 walks two of them
+  __syncwarp();
+  const Frag& f = wf->f;
+
+  // The softmax threads hold a row's 128 scores each: registers move to their warps (88 * 128 + 208 * 256 = 168 * 384).
+  if (warp < 4) {
+  regs_dec<88>();
+  if (warp == 0) {
+    // ================================================================= TMA producer
+    const int BR = min(a.block_size, kTile);            // rows per box
+    const int nbox = kTile / BR;
+    const uint32_t box_bytes = static_cast<uint32_t>(BR / 8) * Tr::GROUP;
+    int kt = 0;  // tiles issued
+    while (next_frag(wf, prefix, p)) {
+      const int nblk = (f.v.T + a.block_size - 1) >> a.block_shift;
+      const int blk_lo = f.lo >> a.block_shift;
+      const int32_t* table = a.block_tables + static_cast<int64_t>(f.s) * a.max_blocks_per_seq;
+      bool ok = true;
+      for (int j = f.t0; j < f.t1 && ok; ++j, ++kt) {
+        const int st = kt % NST;
+        const uint32_t ph = static_cast<uint32_t>(kt / NST) & 1u;
+        const int blk = ((j * kTile) >> a.block_shift) + (nbox > 1 ? lane : 0);
+        const bool mine = lane < nbox && blk >= blk_lo && blk < nblk;
+        int pb = 0;
+        if (mine) {
+          pb = __ldg(table + blk);
+          if (pb < 0 || pb >= a.num_blocks) {
+            raise_error(a.err, PA_DEVERR_BLOCK_ID);
+            pb = 0;
+          }
+        }
+        const int row = nbox > 1 ? 0 : ((j * kTile) & (a.block_size - 1));
+        const int z = (pb * a.num_kv_heads + f.kvh) * (a.block_size >> 3) + (row >> 3);
+        const uint32_t bytes = box_bytes * static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine)));
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          const int full = (which ? Tr::VF : Tr::KF) + st, empty = (which ? Tr::VE : Tr::KE) + st;
+          if (!wait(empty, ph ^ 1u)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
+          __syncwarp();
+          if (mine)
+            tma_load_4d(base + (which ? Tr::OFF_V : Tr::OFF_K) + st * Tr::TILE_BYTES + lane * box_bytes,
+                        which ? &tmap_v : &tmap_k, 0, 0, 0, z, bar(full));
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (!ok) break;
+    }
+    // nothing of ours, and no arrival of the tensor cores, may land after the CTA has left: wait until each stage's
+    // last tile has been used (or, after a wait that ran out, has at least arrived)
+    for (int i = 0; i < NST; ++i) {
+      const int n = kt / NST + (i < kt % NST ? 1 : 0);
+      if (n > 0) {
+        const uint32_t ph = static_cast<uint32_t>(n - 1) & 1u;
+        if (!wait(Tr::KE + i, ph)) wait(Tr::KF + i, ph);
+        if (!wait(Tr::VE + i, ph)) wait(Tr::VF + i, ph);
+      }
+    }
+  } else if (warp == 1) {
+    // ================================================================= MMA issuer
+    constexpr uint32_t kIdQK = mma_idesc(Tr::BF16, false, kTile);
+    constexpr uint32_t kIdPV = mma_idesc(Tr::BF16, true, D);
+    WarpFrag* const wq = wf + 11;  // fragments whose S products are next
+    const Frag& fq = wq->f;
+    bool have_q = next_frag(wq, prefix, p);
+    int jq = have_q ? fq.t0 : 0, tq_frag = 0;   // tile of the next S product; its index within the fragment
+    int ktq = 0;            // its tile count
+    int nq = 0;             // S products issued (job number; stream = nq & 1)
+    uint32_t q_use[2] = {0u, 0u};
+    bool ok = true;
+    // one S = Q K^T
+    auto issue_qk = [&]() -> bool {
+      const int t = nq & 1;
+      const int st = ktq % NST;
+      const bool first_of_stream = p.paired ? tq_frag == 0 : tq_frag < 2;
+      const bool last_of_stream = p.paired ? jq + 1 >= fq.t1 : jq + 2 >= fq.t1;
+      if (first_of_stream && !wait(Tr::QF + t, q_use[t] & 1u)) return false;
+      if (!wait(Tr::KF + st, static_cast<uint32_t>(ktq / NST) & 1u)) return false;
+      tc_fence_after();
+      const bool last_use = !p.paired || t == 1;   // of this K tile
+      if (lane == 0) {
+        const uint32_t qa = base + Tr::OFF_Q + t * Tr::TILE_BYTES, kb = base + Tr::OFF_K + st * Tr::TILE_BYTES;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t o = (s >> 2) * 1024 + (s & 3) * 32;
+          tc_mma_ss(tmem + t * 128, smem_desc(qa + o, 16, Tr::GROUP), smem_desc(kb + o, 16, Tr::GROUP), kIdQK, s > 0);
+        }
+        tc_commit(bar(Tr::SF + t));
+        if (last_use) tc_commit(bar(Tr::KE + st));
+        if (last_of_stream) tc_commit(bar(Tr::QE + t));
+      }
+      __syncwarp();
+      if (last_of_stream) ++q_use[t];
+      ++nq;
+      if (last_use) {
+        ++ktq;
+        ++jq;
+        ++tq_frag;
+        if (jq == fq.t1) {
+          have_q = next_frag(wq, prefix, p);
+          jq = have_q ? fq.t0 : 0;
+          tq_frag = 0;
+        }
+      }
+      return true;
+    };
+    ok = !have_q || issue_qk();
+    if (ok && have_q) ok = issue_qk();
+    int nv = 0, ktv = 0;   // P V products issued, their tile count
+    uint32_t pf[2] = {0u, 0u};
+    while (ok && next_frag(wf, prefix, p)) {
+      const int per_tile = p.paired ? 2 : 1;
+      for (int j = f.t0; ok && j < f.t1; ++j, ++ktv) {
+        const int st = ktv % NST;
+        for (int e = 0; ok && e < per_tile; ++e, ++nv) {
+          const int t = nv & 1;
+          const bool first = p.paired ? j == f.t0 : j - f.t0 < 2;  // the stream's first tile of the fragment
+          if (e == 0) {
+            if (!wait(Tr::VF + st, static_cast<uint32_t>(ktv / NST) & 1u)) { ok = false; break; }
+            // rows outside the sequence (or before the window) may hold anything, or were not loaded
+            const int n_hi = f.v.T - j * kTile, n_lo = f.lo - j * kTile;
+            if (n_hi < kTile || n_lo > 0) {
+              const uint32_t vt = base + Tr::OFF_V + st * Tr::TILE_BYTES;
+              for (int x = lane; x < kTile * Tr::NH * 8; x += 32) {
+                const int r = x / (Tr::NH * 8), c = x % (Tr::NH * 8);
+                if (r >= n_hi || r < n_lo) sts128_zero(vt + (r >> 3) * Tr::GROUP + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16);
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+            }
+          }
+          if (!wait(Tr::PF + t, pf[t] & 1u)) { ok = false; break; }
+          ++pf[t];
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t vb = base + Tr::OFF_V + st * Tr::TILE_BYTES;
+#pragma unroll
+            for (int s = 0; s < kTile / 16; ++s)
+              tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, smem_desc(vb + s * 2 * Tr::GROUP, 1024, Tr::GROUP),
+                        kIdPV, !(first && s == 0));
+            if (p.split_p) {
+#pragma unroll
+              for (int s = 0; s < kTile / 16; ++s)
+                tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 64 + s * 8,
+                          smem_desc(vb + s * 2 * Tr::GROUP, 1024, Tr::GROUP), kIdPV, 1);
+            }
+            tc_commit(bar(Tr::OD + t));
+            if (e == per_tile - 1) tc_commit(bar(Tr::VE + st));
+          }
+          __syncwarp();
+          if (have_q) ok = issue_qk();
+        }
+      }
+    }
+  } else {
+    // ================================================================= query rows of one stream
+    const int t = warp - 2;
+    int uses = 0, parity = 0;
+    constexpr int CH = D / 8;  // 16-byte chunks of a row
+    while (next_frag(wf, prefix, p)) {
+      const int n = f.t1 - f.t0;
+      const bool used = p.paired || n - (t ^ parity) > 0;
+      if (!p.paired) parity ^= n & 1;
+      if (!used) continue;
+      if (uses > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses - 1) & 1u)) break;
+      ++uses;
+      const int row0 = p.paired ? f.m * 2 * kTile + t * kTile : 0;
+      const int R = f.v.L * a.group;
+      const int rows = min(kTile, (max(0, min(kTile, R - row0)) + 31) & ~31);  // whole warps of rows; the rest is not read back
+      for (int x0 = 0; x0 < rows * CH; x0 += 32 * 8) {
+        uint4 w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int x = x0 + 32 * k + lane;
+          const int r = x / CH, c = x % CH;
+          w[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (row0 + r < R && x < rows * CH) {
+            const int i = (row0 + r) / a.group, g = (row0 + r) - i * a.group;
+            w[k] = __ldg(reinterpret_cast<const uint4*>(
+                static_cast<const uint8_t*>(a.q) +
+                ((static_cast<int64_t>(f.v.row0) + i) * a.q_stride + static_cast<int64_t>(f.kvh * a.group + g) * D + c * 8) * 2));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int x = x0 + 32 * k + lane;
+          const int r = x / CH, c = x % CH;
+          if (x < rows * CH)
+            *reinterpret_cast<uint4*>(sm + Tr::OFF_Q + t * Tr::TILE_BYTES + (r >> 3) * Tr::GROUP + (c >> 3) * 1024 +
+                                      (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[k];
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Tr::QF + t));
+    }
+  }
+  } else {
+    regs_inc<208>();
+    // ================================================================= softmax, one row per thread
+    const int t = (warp - 4) >> 2;
+    const int wq = warp & 3;                       // TMEM lanes 32 wq ..
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * 128 + lanes;
+    float* const rowq = reinterpret_cast<float*>(sm + Tr::OFF_ROWQ) + (warp - 4) * D;
+    constexpr float kLog2e = 1.4426950408889634f;
+    // f16 weights carry a factor 2^7 (m is lowered by it), so that weights down to 2^-31 of the largest are normal
+    constexpr float kLift = Tr::BF16 ? 0.f : 7.f;
+    int jobs = 0, parity = 0;
+
+    // queries at negative positions (more queries than tokens) see nothing
+    for (int s = blockIdx.x; s < S; s += gridDim.x) {
+      const SeqView v = seq_view(a, s, false);
+      const int64_t n = static_cast<int64_t>(min(v.L, max(0, v.L - v.T))) * a.num_heads * D;
+      for (int64_t x = threadIdx.x - 128; x < n; x += 256)
+        store_out(a.out, a.out_dtype, static_cast<int64_t>(v.row0) * a.num_heads * D + x, 0.f);
+      if (a.mass && v.T == 0 && v.L == 1)
+        for (int h = threadIdx.x - 128; h < a.num_heads; h += 256)
+          a.row_stats[static_cast<int64_t>(s) * a.num_heads + h] = make_float2(-INFINITY, 0.f);
+    }
+
+    // the four warps of the stream wait for one another (bounded, unlike a named barrier)
+    uint32_t syncs = 0u;
+    auto stream_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Tr::RB + t));
+      return wait(Tr::RB + t, syncs++ & 1u);
+    };
+    bool ok = true;
+    while (ok && next_frag(wf, prefix, p)) {
+      const int n = f.t1 - f.t0;
+      const int e = p.paired ? t : (t ^ parity);    // which of the fragment's contributions this stream makes
+      const int step = p.paired ? 1 : 2;
+      const int j0 = f.t0 + (p.paired ? 0 : e);
+      if (!p.paired) parity ^= n & 1;
+      if (j0 >= f.t1) continue;
+      const int row0 = p.paired ? f.m * 2 * kTile + t * kTile : 0;
+      const int R = f.v.L * a.group;
+      const int r = row0 + wq * 32 + lane;
+      const bool valid = r < R;
+      const bool warp_on = row0 + wq * 32 < R;
+      const int qi = valid ? r / a.group : 0;
+      const int h = f.kvh * a.group + (valid ? r - qi * a.group : 0);
+      RowBounds rb = row_bounds(a, f.v, f.prefix, qi);
+      if (!valid) rb.lo = rb.hi = 0;
+      const int first = f.v.T - f.v.L;              // tree: position of node 0
+      const uint64_t* tree = a.tree_mask ? a.tree_mask + (static_cast<int64_t>(f.v.row0) + qi) * a.tree_words : nullptr;
+      const float slope2 = a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
+      const float sc = a.scale;
+      const float sc2 = sc * kLog2e;
+      const float capk = a.softcap > 0.f ? 2.f * kLog2e * sc / a.softcap : 0.f, cap2 = a.softcap * kLog2e;
+      float m = -INFINITY, l = 0.f;
+      float* const score_row = a.mass && valid ? p.scores + (static_cast<int64_t>(f.s) * a.num_heads + h) * p.score_stride : nullptr;
+
+      for (int j = j0; ok && j < f.t1; j += step, ++jobs) {
+        if (!wait(Tr::SF + t, static_cast<uint32_t>(jobs) & 1u)) { ok = false; break; }
+        tc_fence_after();
+        if (warp_on) {
+          const int tb = j * kTile;
+          float z[kTile];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, z + 32 * c);
+          tmem_wait_ld();
+          if (a.softcap > 0.f) {
+#pragma unroll
+            for (int c = 0; c < kTile; ++c) z[c] = cap2 - __fdividef(2.f * cap2, 1.f + fast_exp2(z[c] * capk));
+          } else {
+#pragma unroll
+            for (int c = 0; c < kTile; c += 2) {
+              const float2 x = fmul2(make_float2(z[c], z[c + 1]), make_float2(sc2, sc2));
+              z[c] = x.x;
+              z[c + 1] = x.y;
+            }
+          }
+          if (a.slopes) {
+            const float d0 = static_cast<float>(tb - rb.pos);
+#pragma unroll
+            for (int c = 0; c < kTile; ++c) z[c] = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), z[c]);
+          }
+          const bool full = rb.lo <= tb && rb.hi >= tb + kTile && (!tree || tb + kTile <= first);
+          if (!__all_sync(0xffffffffu, full || !valid)) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int b0 = tb + 32 * c;
+              // bits [lo, hi) of this 32-position chunk
+              const int lo = max(0, min(32, rb.lo - b0)), hi = max(0, min(32, rb.hi - b0));
+              uint32_t see = (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & (lo >= 32 ? 0u : 0xffffffffu << lo);
+              if (tree && b0 + 32 > first) {
+                // positions first + k need bit k; those before first are all visible
+                uint32_t bits = 0u;
+                if (valid) {
+                  const int k0 = b0 - first;        // node of the chunk's first position (may be negative)
+                  const int kk = max(k0, 0);
+                  const int w = kk >> 6, sh = kk & 63;
+                  uint64_t x = w < a.tree_words ? tree[w] >> sh : 0ull;
+                  if (sh > 32 && w + 1 < a.tree_words) x |= tree[w + 1] << (64 - sh);
+                  bits = k0 >= 0 ? static_cast<uint32_t>(x)
+                                 : (static_cast<uint32_t>(x) << (-k0)) | ((1u << (-k0)) - 1u);
+                }
+                see &= bits;
+              }
+#pragma unroll
+              for (int k = 0; k < 32; ++k) z[32 * c + k] = (see >> k) & 1u ? z[32 * c + k] : -INFINITY;
+            }
+          }
+          if (score_row) {
+#pragma unroll
+            for (int c = 0; c < kTile; c += 4)
+              *reinterpret_cast<float4*>(score_row + tb + c) = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
+          }
+          float mx0 = fmaxf(z[0], z[1]), mx1 = fmaxf(z[2], z[3]);
+#pragma unroll
+          for (int c = 4; c < kTile; c += 4) {
+            mx0 = fmaxf(mx0, fmaxf(z[c], z[c + 1]));
+            mx1 = fmaxf(mx1, fmaxf(z[c + 2], z[c + 3]));
+          }
+          const float mx = fmaxf(mx0, mx1);
+          const bool raise = valid && mx > (m == -INFINITY ? m : m + kSlack);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float mn = raise ? mx : m;
+            const float alpha = raise ? fast_exp2(m - mn) : 1.f;   // nothing seen yet: 2^-inf = 0
+            m = mn;
+            l *= alpha;
+            if (j != j0) {
+              // the product before this one must have left O
+              if (!wait(Tr::OD + t, static_cast<uint32_t>(jobs - 1) & 1u)) ok = false;
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld16(to + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] *= alpha;
+                tmem_st16(to + c, reinterpret_cast<const uint32_t*>(o));
+              }
+              tmem_wait_st();
+            }
+          }
+          const float ms = m == -INFINITY ? 0.f : m - kLift;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float p0 = fast_exp2(z[32 * c + 2 * k] - ms), p1 = fast_exp2(z[32 * c + 2 * k + 1] - ms);
+              l0 += p0;
+              l1 += p1;
+              hi[k] = pack2<Tr::BF16>(p0, p1);
+              if (p.split_p) {
+                const float2 q = unpack2<Tr::BF16>(hi[k]);
+                lo[k] = pack2<Tr::BF16>(p0 - q.x, p1 - q.y);
+              }
+            }
+            tmem_st16(ts + 16 * c, hi);
+            if (p.split_p) tmem_st16(ts + 64 + 16 * c, lo);
+          }
+          l += l0 + l1;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Tr::PF + t));
+      }
+      if (!ok) break;
+
+      // ---- the stream's part of the fragment is done
+      if (!wait(Tr::OD + t, static_cast<uint32_t>(jobs - 1) & 1u)) { ok = false; break; }
+      tc_fence_after();
+      const float me = m == -INFINITY ? m : m - kLift;  // O and l are relative to 2^me
+      const int contributions = p.paired ? 1 : min(2, n);
+      if (f.whole && contributions == 1) {
+        if (warp_on) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          bool bad = l != l;
+          const int64_t o0 = ((static_cast<int64_t>(f.v.row0) + qi) * a.num_heads + h) * D;
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(to + c, o);
+            tmem_wait_ld();
+            if (valid) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                float4 w = make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
+                bad |= !(fabsf(w.x) < INFINITY) || !(fabsf(w.y) < INFINITY) || !(fabsf(w.z) < INFINITY) || !(fabsf(w.w) < INFINITY);
+                store_out4(a.out, a.out_dtype, o0 + c + k, w, true);
+              }
+            }
+          }
+          float2 stats = make_float2(me, l);
+          unsigned again = __ballot_sync(0xffffffffu, bad && valid);
+          while (again) {
+            const int k = __ffs(again) - 1;
+            again &= again - 1;
+            const float2 ml = attend_row_again<KVT, D>(a, f.s, f.v, __shfl_sync(0xffffffffu, qi, k), __shfl_sync(0xffffffffu, h, k), rowq);
+            (void)ml;
+          }
+          if (a.mass && valid) a.row_stats[static_cast<int64_t>(f.s) * a.num_heads + h] = stats;
+        }
+        continue;
+      }
+      // ---- record, then count in; the last contribution joins them all
+      const int slot_kind = slot_kind_of(f.whole, f.idx);
+      const int rec_floats = p.rec_rows * (D + 2);
+      auto record = [&](int cta, int kind, int c) {
+        return p.records + (static_cast<int64_t>(cta) * p.slots * 2 + kind * 2 + c) * rec_floats;
+      };
+      {
+        float* const rec = record(blockIdx.x, slot_kind, e);
+        const int lr = wq * 32 + lane;
+        if (warp_on) {
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(to + c, o);
+            tmem_wait_ld();
+            if (valid) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<float4*>(rec + lr * D + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            }
+          }
+          if (valid) *reinterpret_cast<float2*>(rec + p.rec_rows * D + 2 * lr) = make_float2(me, l);
+        }
+      }
+      __threadfence();
+      if (!(ok = stream_sync())) break;
+      const int c0 = cta_of(f.seg_start + kFragCost, U, nw), c1 = cta_of(f.seg_start + kFragCost + f.seg_tiles - 1, U, nw);
+      int total = 0;  // contributions to this stream's rows (paired: its own row tile; alternating: both streams)
+      for (int c = c0; c <= c1; ++c) total += p.paired ? 1 : min(2, tiles_in(c, U, nw, f.seg_start, f.seg_tiles));
+      // paired: the streams' rows are joined apart (the segment that leaves a CTA unfinished is its last one); alternating:
+      // the segment's only rows
+      int* const counter = p.paired ? p.counters + 2 * c0 + t : p.counters + f.s * a.num_kv_heads + f.kvh;
+      // (two words in turn: a warp still reading one is not overtaken by the next fragment's arrival)
+      volatile int* const arrived = misc + 4 + 2 * (f.idx & 1) + t;
+      if ((threadIdx.x & 127) == 0) *arrived = atom_add_acq_rel_gpu(counter, 1);
+      if (!(ok = stream_sync())) break;
+      const bool last = *arrived == total - 1;
+      if (last) {
+        __threadfence();
+        const int nrows = min(kTile, R - row0);
+        for (int lr = wq; lr < nrows; lr += 4) {
+          float M = -INFINITY;
+          for (int c = c0; c <= c1; ++c) {
+            const int k = tiles_in(c, U, nw, f.seg_start, f.seg_tiles);
+            const int kind = f.whole ? slot_kind : cut_slot_kind(c, c0, U, nw, f.seg_start);
+            for (int x = 0; x < (p.paired ? 1 : min(2, k)); ++x)
+              M = fmaxf(M, __ldcg(record(c, kind, p.paired ? t : x) + p.rec_rows * D + 2 * lr));
+          }
+          float L = 0.f;
+          float acc[D / 32];
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) acc[q] = 0.f;
+          for (int c = c0; c <= c1; ++c) {
+            const int k = tiles_in(c, U, nw, f.seg_start, f.seg_tiles);
+            const int kind = f.whole ? slot_kind : cut_slot_kind(c, c0, U, nw, f.seg_start);
+            for (int x = 0; x < (p.paired ? 1 : min(2, k)); ++x) {
+              const float* rec = record(c, kind, p.paired ? t : x);
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(rec + p.rec_rows * D + 2 * lr));
+              const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+              L = fmaf(w, ml.y, L);
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                const float o = __ldcg(rec + lr * D + lane + 32 * q);
+                acc[q] = fmaf(w, o, acc[q]);
+              }
+            }
+          }
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          const int i = (row0 + lr) / a.group, hh = f.kvh * a.group + (row0 + lr) - i * a.group;
+          const int64_t o0 = ((static_cast<int64_t>(f.v.row0) + i) * a.num_heads + hh) * D;
+          bool bad = L != L;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            const float o = acc[q] * inv;
+            bad |= !(fabsf(o) < INFINITY);
+            store_out(a.out, a.out_dtype, o0 + lane + 32 * q, o);
+          }
+          if (__any_sync(0xffffffffu, bad)) attend_row_again<KVT, D>(a, f.s, f.v, i, hh, rowq);
+          if (a.mass && lane == 0) a.row_stats[static_cast<int64_t>(f.s) * a.num_heads + hh] = make_float2(M, L);
+        }
+        if ((threadIdx.x & 127) == 0) *counter = 0;  // ready for the next call
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace pa

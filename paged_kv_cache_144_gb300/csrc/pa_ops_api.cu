@@ -175,6 +175,10 @@ PA_EXPORT int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q
   if (ps != PA_OK) return ps;
   if (q_stride < static_cast<int64_t>(num_heads) * head_dim) return PA_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(out) || q_stride % 8 != 0) return PA_ERR_ALIGN;
+  // the work of a call is counted in tiles of 128 positions per row tile, in 32 bits
+  if ((static_cast<int64_t>(num_tokens) * (num_heads / num_kv_heads) / 128 + num_seqs) * num_kv_heads * (cap / 128 + 2) >=
+      (int64_t{1} << 31))
+    return PA_ERR_SHAPE;
   const size_t need = pa::attend_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
                                                  max_blocks_per_seq, max_q_len, kv_dtype, o.mass != nullptr);
   if (need == static_cast<size_t>(-1)) return PA_ERR_CUDA;
