@@ -38,6 +38,8 @@ SOURCES = [
     "pa_decode_rows16.cu",
     "pa_decode_append16.cu",
     "pa_decode_append8.cu",
+    "pa_decode_attend16.cu",
+    "pa_decode_attend8.cu",
 ]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -85,15 +85,11 @@ PFN_cuTensorMapEncodeTiled_v12000 pa::tensor_map_encoder() {
   return fn;
 }
 
-namespace {
-
-using pa::tensor_map_encoder;
-
 // 3-D view of a cache pool: {128 bytes of a row, rows, 128-byte halves of a
 // row}, with num_blocks*Hkv*B rows of head_dim elements.  One TMA box =
 // box_rows whole rows with the 128-byte swizzle, landing in shared memory as
 // [half][row][128 bytes], so that each half-plane is swizzled by row.
-bool encode_cache_map(CUtensorMap* map, const void* cache, int64_t num_blocks, int num_kv_heads,
+bool pa::encode_cache_map(CUtensorMap* map, const void* cache, int64_t num_blocks, int num_kv_heads,
                       int block_size, int head_dim, int elem_bytes, int box_rows) {
   if (box_rows % pa::kBoxRowQuantum != 0 || box_rows > 256) return false;
   auto enc = tensor_map_encoder();
@@ -112,6 +108,10 @@ bool encode_cache_map(CUtensorMap* map, const void* cache, int64_t num_blocks, i
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+namespace {
+
+using pa::encode_cache_map;
 
 // Compiled maximum of A rows (q_len * G (query, head) pairs) serving `rows`.
 int gmax_for_rows(int rows) { return rows <= 1 ? 1 : (rows <= 4 ? 4 : (rows <= 8 ? 8 : 16)); }

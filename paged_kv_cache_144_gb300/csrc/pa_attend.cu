@@ -1,44 +1,129 @@
 // pa_attend.cu - attention of ragged query rows over the paged cache with
 // score modifiers, and the accumulation of each cached position's weight.
+#include <cstring>
+
 #include "pa_attend_tc.cuh"
 
 namespace pa {
 namespace {
 
+// Rows (queries x query heads per KV head) up to which the decode kernel's variants serve a call.
+constexpr int kFewRows = 64;
+// Units charged per fragment in their balanced split, as in pa_decode.
+constexpr int kDecodeFragCost = 3;
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Arrival counters live at the start of the workspace, which is zero between calls.  Up to kCounters of them fit the fixed
+// area that calls of any shape share; a call with more clears them itself first (its batch is large enough not to notice).
+constexpr size_t kCounters = 1 << 16;
 
 // How a call of these sizes runs, and what it keeps in the workspace.
 struct Plan {
+  enum Kind { kRows, kFew, kTensor } kind;
+  int paired;                 // kTensor: two row tiles per K/V tile
+  DecodeKey key;              // kFew: the decode kernel's variant and geometry
+  DecodeGeometry geo;
   int ctas;
-  int paired;
   int rec_rows, slots;
-  size_t counters, records, stats, scores, bytes;  // offsets of the parts, total
+  size_t num_counters;
+  size_t records, pending, stats, scores, bytes;  // offsets of the parts, total
   int score_stride;
 };
 
-bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int cap, int max_q_len, bool accumulate,
-               Plan* pl) {
+bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+               int max_q_len, int q_dtype, int kv_dtype, bool tree, bool accumulate, Plan* pl) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return false;
-  const int64_t rows = static_cast<int64_t>(max_q_len) * (num_heads / num_kv_heads);
+  const int group = num_heads / num_kv_heads;
+  const int64_t rows = static_cast<int64_t>(max_q_len) * group;
+  const bool q8 = kv_dtype == PA_FP8_E4M3 || kv_dtype == PA_INT8;
   pl->ctas = sms;
   pl->paired = rows > kTile ? 1 : 0;
-  pl->rec_rows = pl->paired ? kTile : static_cast<int>((rows + 7) / 8 * 8);
-  pl->slots = pl->paired ? 2 : 4;
-  size_t at = 0;
-  pl->counters = at;
-  at += up256((pl->paired ? 2 * static_cast<size_t>(sms) : static_cast<size_t>(num_seqs) * num_kv_heads) * sizeof(int));
+  pl->kind = rows <= kFewRows ? Plan::kFew : (q8 ? Plan::kRows : Plan::kTensor);
+  size_t records = 0, pending = 0;
+  pl->num_counters = 0;
+  if (pl->kind == Plan::kFew) {
+    const int gm = max_q_len == 1 && group <= 8 && !tree ? 8 : 16;
+    pl->key.q_dtype = q_dtype;
+    pl->key.kv_dtype = kv_dtype;
+    pl->key.head_dim = head_dim;
+    pl->key.gmax = gm;
+    pl->key.unit_rows = q8 && block_size >= 16 && gm == 8 ? 64 : 32;
+    pl->key.append = 2;
+    pl->key.row_groups = gm == 16 ? static_cast<int>((rows + 15) / 16) : 1;
+    if (!decode_geometry(pl->key, num_seqs, &pl->geo)) return false;
+    const size_t warps = static_cast<size_t>(pl->geo.ctas) * pl->geo.warps_per_cta;
+    pl->num_counters = static_cast<size_t>(num_seqs) * num_kv_heads * pl->geo.row_groups;
+    records = 2 * warps * pl->geo.record_floats * sizeof(float);
+    pending = 2 * warps * sizeof(int);
+  } else if (pl->kind == Plan::kTensor) {
+    pl->rec_rows = pl->paired ? kTile : static_cast<int>((rows + 7) / 8 * 8);
+    pl->slots = pl->paired ? 2 : 4;
+    pl->num_counters = pl->paired ? 2 * static_cast<size_t>(sms) : static_cast<size_t>(num_seqs) * num_kv_heads;
+    records = static_cast<size_t>(sms) * pl->slots * 2 * pl->rec_rows * (head_dim + 2) * sizeof(float);
+  }
+  size_t at = up256((pl->num_counters > kCounters ? pl->num_counters : kCounters) * sizeof(int));
   pl->records = at;
-  at += up256(static_cast<size_t>(sms) * pl->slots * 2 * pl->rec_rows * (head_dim + 2) * sizeof(float));
+  at += up256(records);
+  pl->pending = at;
+  at += up256(pending);
   pl->stats = at;
-  pl->score_stride = (cap + kTile - 1) / kTile * kTile;
+  pl->score_stride = (max_blocks_per_seq * block_size + kTile - 1) / kTile * kTile;
   if (accumulate) at += up256(static_cast<size_t>(num_seqs) * num_heads * sizeof(float2));
   pl->scores = at;
   if (accumulate) at += up256(static_cast<size_t>(num_seqs) * num_heads * pl->score_stride * sizeof(float));
   pl->bytes = at;
   return true;
+}
+
+// The decode kernel's variants with score modifiers.
+cudaError_t launch_few(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream) {
+  DecodeParams p;
+  memset(&p, 0, sizeof(p));
+  p.out = a.out;
+  p.out_dtype = a.out_dtype;
+  p.q = a.q;
+  p.q_stride = a.q_stride;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.k_zero_point = a.k_zero_point;
+  p.v_zero_point = a.v_zero_point;
+  p.block_tables = a.block_tables;
+  p.max_blocks_per_seq = a.max_blocks_per_seq;
+  p.seq_lens = a.seq_lens;
+  p.num_blocks = a.num_blocks;
+  p.num_seqs = a.num_seqs;
+  p.num_heads = a.num_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.group = a.group;
+  p.qk_scale_log2 = a.scale * 1.4426950408889634f;
+  p.block_size = a.block_size;
+  p.block_shift = a.block_shift;
+  p.frag_cost = kDecodeFragCost;
+  p.window = a.window;
+  p.q_len = 1;
+  p.k_cache = const_cast<void*>(a.k_cache);
+  p.v_cache = const_cast<void*>(a.v_cache);
+  p.seg_counters = reinterpret_cast<int*>(ws);
+  p.part_records = reinterpret_cast<float*>(ws + pl.records);
+  p.pending = reinterpret_cast<int*>(ws + pl.pending);
+  p.pending_cap = 2;
+  p.err = a.err;
+  p.stages = pl.geo.stages;
+  p.row_groups = pl.geo.row_groups;
+  p.stage_bytes = pl.geo.stage_bytes;
+  p.wait_limit_ns = kDefaultWaitLimitNs;
+  p.att = a;
+  const int eb = a.kv_dtype == PA_FP8_E4M3 || a.kv_dtype == PA_INT8 ? 1 : 2;
+  const int box = a.block_size < pl.geo.unit_rows ? a.block_size : pl.geo.unit_rows;
+  CUtensorMap tk, tv;
+  if (!encode_cache_map(&tk, a.k_cache, a.num_blocks, a.num_kv_heads, a.block_size, a.head_dim, eb, box) ||
+      !encode_cache_map(&tv, a.v_cache, a.num_blocks, a.num_kv_heads, a.block_size, a.head_dim, eb, box))
+    return cudaErrorInvalidValue;
+  return launch_decode(pl.key, pl.geo, p, tk, tv, stream, a.pdl);
 }
 
 // 4-D view of a 16-bit pool: {64 elements, 8 rows, 128-byte halves of a row, groups of 8 rows}; one box = box_rows
@@ -67,10 +152,8 @@ cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaSt
   p.split_p = (!pl.paired || a.out_dtype == PA_F32) ? 1 : 0;
   p.rec_rows = pl.rec_rows;
   p.slots = pl.slots;
-  p.counters = reinterpret_cast<int*>(ws + pl.counters);
+  p.counters = reinterpret_cast<int*>(ws);
   p.records = reinterpret_cast<float*>(ws + pl.records);
-  p.scores = reinterpret_cast<float*>(ws + pl.scores);
-  p.score_stride = pl.score_stride;
   CUtensorMap tk, tv;
   const int64_t rows = a.num_blocks * a.num_kv_heads * a.block_size;
   const int box = a.block_size < kTile ? a.block_size : kTile;
@@ -99,56 +182,18 @@ constexpr int kRowWarps = 4;
 // One warp per (query, head).
 template <typename KVT, int D>
 __global__ void __launch_bounds__(kRowWarps * 32) attend_rows_kernel(const AttendParams p) {
-  __shared__ float qs[kRowWarps][D];
   griddep_wait();
   const int s = blockIdx.y;
   const SeqView v = seq_view(p, s, blockIdx.x == 0 && threadIdx.x == 0);
   for (int64_t x = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
        x < static_cast<int64_t>(v.L) * p.num_heads; x += static_cast<int64_t>(gridDim.x) * kRowWarps) {
     const int h = static_cast<int>(x % p.num_heads), i = static_cast<int>(x / p.num_heads);
-    const float2 ml = attend_row<KVT, D>(p, s, v, i, h, qs[threadIdx.x >> 5]);
-    if (p.mass && (threadIdx.x & 31) == 0) p.row_stats[static_cast<int64_t>(s) * p.num_heads + h] = ml;
+    attend_row<KVT, D>(p, s, v, i, h);
   }
-}
-
-// mass[s][kvh][t] += sum over the group of softmax weights: one thread per
-// position, the scores computed again from q and K.
-template <typename KVT, int D>
-__global__ void __launch_bounds__(128) attend_mass_kernel(const AttendParams p) {
-  const int s = blockIdx.z, kvh = blockIdx.y;
-  const SeqView v = seq_view(p, s, false);
-  const int t = blockIdx.x * 128 + threadIdx.x;
-  if (t >= v.T || v.L != 1) return;
-  const RowBounds rb = row_bounds(p, v, seq_prefix(p, s, v.T), 0);
-  if (t < rb.lo || t >= rb.hi) return;
-  float ks = 1.f;
-  int kz = 0;
-  if constexpr (elem<KVT>::bytes == 1) ks = __ldg(p.k_scale + kvh);
-  if constexpr (std::is_same<KVT, i8_t>::value) kz = __ldg(p.k_zero_point + kvh);
-  int pb = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq + (t >> p.block_shift));
-  if (pb < 0 || pb >= p.num_blocks) pb = 0;
-  const uint8_t* kr = static_cast<const uint8_t*>(p.k_cache) +
-                      ((static_cast<int64_t>(pb) * p.num_kv_heads + kvh) * p.block_size + (t & (p.block_size - 1))) *
-                          (D * elem<KVT>::bytes);
-  float sum = 0.f;
-  for (int g = 0; g < p.group; ++g) {
-    const int h = kvh * p.group + g;
-    const int64_t e = static_cast<int64_t>(v.row0) * p.q_stride + static_cast<int64_t>(h) * D;
-    float x = 0.f;
-    for (int c = 0; c < D; ++c)
-      x = fmaf(p.q_dtype == PA_BF16 ? load_scalar<bf16_t>(p.q, e + c) : load_scalar<f16_t>(p.q, e + c),
-               cache_elem<KVT>(kr, c, kz), x);
-    x *= p.scale * ks;
-    if (p.softcap > 0.f) x = cap_score(x, p.softcap, 2.f * 1.4426950408889634f / p.softcap);
-    if (p.slopes) x -= __ldg(p.slopes + h) * static_cast<float>(abs(rb.pos - t));
-    const float2 ml = p.row_stats[static_cast<int64_t>(s) * p.num_heads + h];
-    sum += exp2f(x * 1.4426950408889634f - ml.x) / ml.y;
-  }
-  p.mass[s * p.mass_stride_seq + kvh * p.mass_stride_head + t] += sum;
 }
 
 // mass[s][kvh][t] += sum over the group of exp2(score - max) / sum, from the stored scores: one thread per position.
-__global__ void __launch_bounds__(256) attend_add_mass_kernel(const AttendParams p, const float* scores, int score_stride) {
+__global__ void __launch_bounds__(256) attend_add_mass_kernel(const AttendParams p) {
   const int s = blockIdx.z, kvh = blockIdx.y;
   const SeqView v = seq_view(p, s, false);
   if (v.L != 1) return;
@@ -159,7 +204,7 @@ __global__ void __launch_bounds__(256) attend_add_mass_kernel(const AttendParams
   for (int g = 0; g < p.group; ++g) {
     const int64_t row = static_cast<int64_t>(s) * p.num_heads + kvh * p.group + g;
     const float2 ml = p.row_stats[row];
-    sum += exp2f(scores[row * score_stride + t] - ml.x) / ml.y;
+    sum += exp2f(p.scores[row * p.score_stride + t] - ml.x) / ml.y;
   }
   p.mass[s * p.mass_stride_seq + kvh * p.mass_stride_head + t] += sum;
 }
@@ -169,48 +214,55 @@ cudaError_t launch_t(const AttendParams& p, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.max_q_len) * p.num_heads;
   const int64_t gx = (rows + kRowWarps - 1) / kRowWarps;
   attend_rows_kernel<KVT, D><<<dim3(static_cast<unsigned>(gx < 4096 ? gx : 4096), p.num_seqs), kRowWarps * 32, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && p.mass) {
-    const int cap = p.max_blocks_per_seq << p.block_shift;
-    attend_mass_kernel<KVT, D><<<dim3((cap + 127) / 128, p.num_kv_heads, p.num_seqs), 128, 0, stream>>>(p);
-    e = cudaGetLastError();
-  }
-  return e;
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                               int max_blocks_per_seq, int max_q_len, int kv_dtype, bool accumulate) {
-  Plan pl;
-  if (!make_plan(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq * block_size, max_q_len, accumulate, &pl))
-    return static_cast<size_t>(-1);
-  return pl.bytes;
+  // with and without a tree, with either query type: the larger need
+  size_t most = 0;
+  for (int tree = 0; tree < 2; ++tree) {
+    Plan pl;
+    if (!make_plan(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, max_q_len,
+                   kv_dtype == PA_F16 ? PA_F16 : PA_BF16, kv_dtype, tree != 0, accumulate, &pl))
+      return static_cast<size_t>(-1);
+    most = pl.bytes > most ? pl.bytes : most;
+  }
+  return most;
 }
 
-cudaError_t launch_attend(AttendParams p, void* workspace, cudaStream_t stream) {
+int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   (void)cudaGetLastError();
   Plan pl;
-  if (!make_plan(p.num_seqs, p.num_heads, p.num_kv_heads, p.head_dim, p.max_blocks_per_seq * p.block_size, p.max_q_len,
-                 p.mass != nullptr, &pl))
-    return cudaErrorInvalidDevice;
+  if (!make_plan(p.num_seqs, p.num_heads, p.num_kv_heads, p.head_dim, p.block_size, p.max_blocks_per_seq, p.max_q_len,
+                 p.q_dtype, p.kv_dtype, p.tree_mask != nullptr, p.mass != nullptr, &pl))
+    return cuda_status(cudaErrorInvalidDevice, "pa_attend plan");
+  if (!workspace || workspace_bytes < pl.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return PA_ERR_WORKSPACE;
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   p.row_stats = reinterpret_cast<float2*>(ws + pl.stats);
+  p.scores = reinterpret_cast<float*>(ws + pl.scores);
+  p.score_stride = pl.score_stride;
   cudaError_t e = cudaSuccess;
-  if (p.kv_dtype == PA_F16 || p.kv_dtype == PA_BF16) {
-    if (p.kv_dtype == PA_F16)
-      e = p.head_dim == 128 ? launch_tc<f16_t, 128>(p, pl, ws, stream) : launch_tc<f16_t, 64>(p, pl, ws, stream);
-    else
-      e = p.head_dim == 128 ? launch_tc<bf16_t, 128>(p, pl, ws, stream) : launch_tc<bf16_t, 64>(p, pl, ws, stream);
-    if (e == cudaSuccess && p.mass) {
-      const int cap = p.max_blocks_per_seq << p.block_shift;
-      attend_add_mass_kernel<<<dim3((cap + 255) / 256, p.num_kv_heads, p.num_seqs), 256, 0, stream>>>(
-          p, reinterpret_cast<const float*>(ws + pl.scores), pl.score_stride);
-      e = cudaGetLastError();
-    }
-    return e;
+  if (pl.num_counters > kCounters) e = cudaMemsetAsync(ws, 0, pl.num_counters * sizeof(int), stream);
+  if (e != cudaSuccess) return cuda_status(e, "pa_attend counters");
+  if (pl.kind == Plan::kFew) {
+    e = launch_few(p, pl, ws, stream);
+  } else if (pl.kind == Plan::kRows) {
+    e = p.kv_dtype == PA_FP8_E4M3 ? launch_t<e4m3_t, 128>(p, stream) : launch_t<i8_t, 128>(p, stream);
+  } else if (p.kv_dtype == PA_F16) {
+    e = p.head_dim == 128 ? launch_tc<f16_t, 128>(p, pl, ws, stream) : launch_tc<f16_t, 64>(p, pl, ws, stream);
+  } else {
+    e = p.head_dim == 128 ? launch_tc<bf16_t, 128>(p, pl, ws, stream) : launch_tc<bf16_t, 64>(p, pl, ws, stream);
   }
-  return p.kv_dtype == PA_FP8_E4M3 ? launch_t<e4m3_t, 128>(p, stream) : launch_t<i8_t, 128>(p, stream);
+  if (e == cudaSuccess && p.mass) {
+    const int cap = p.max_blocks_per_seq << p.block_shift;
+    attend_add_mass_kernel<<<dim3((cap + 255) / 256, p.num_kv_heads, p.num_seqs), 256, 0, stream>>>(p);
+    e = cudaGetLastError();
+  }
+  return cuda_status(e, "pa_attend launch");
 }
 
 }  // namespace pa

@@ -83,10 +83,10 @@ __device__ __forceinline__ float cache_elem(const uint8_t* row, int c, int zp) {
 // One (query row, head) by one warp: the running maximum and sum in log2
 // domain over 32 positions at a time, one per lane; then each visible
 // position's V row, one column per lane and step.  Positions that are not
-// visible are never read from V.  qs: 128 floats of shared memory of this warp.
-// Returns (m, l) of the row.
+// visible are never read from V.  The query sits in registers, D / 32 columns
+// per lane.  Returns (m, l) of the row.
 template <typename KVT, int D>
-__device__ float2 attend_row(const AttendParams& p, int s, const SeqView& v, int i, int h, float* qs) {
+__device__ float2 attend_row(const AttendParams& p, int s, const SeqView& v, int i, int h) {
   const int lane = threadIdx.x & 31;
   const int kvh = h / p.group;
   const int64_t n = static_cast<int64_t>(v.row0) + i;
@@ -102,12 +102,13 @@ __device__ float2 attend_row(const AttendParams& p, int s, const SeqView& v, int
     kz = __ldg(p.k_zero_point + kvh);
     vz = __ldg(p.v_zero_point + kvh);
   }
-  __syncwarp();
-  for (int c = lane; c < D; c += 32) {
-    const int64_t e = n * p.q_stride + static_cast<int64_t>(h) * D + c;
-    qs[c] = p.q_dtype == PA_BF16 ? load_scalar<bf16_t>(p.q, e) : load_scalar<f16_t>(p.q, e);
+  float q[D / 32];
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    const int64_t e = n * p.q_stride + static_cast<int64_t>(h) * D + lane + 32 * j;
+    q[j] = p.q_dtype == PA_BF16 ? load_scalar<bf16_t>(p.q, e) : load_scalar<f16_t>(p.q, e);
   }
-  __syncwarp();
+  __syncwarp();  // what other lanes stored to this row before is overwritten below
   const float slope = p.slopes ? __ldg(p.slopes + h) : 0.f;
   const float capk = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
   const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq;
@@ -133,10 +134,14 @@ __device__ float2 attend_row(const AttendParams& p, int s, const SeqView& v, int
       see = (p.tree_mask[n * p.tree_words + (j >> 6)] >> (j & 63)) & 1ull;
     }
     float z = -INFINITY;
+    const uint8_t* kr = see ? row_of(p.k_cache, t) : static_cast<const uint8_t*>(p.k_cache);
+    float x = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+#pragma unroll 1
+      for (int c = 0; c < 32; ++c) x = fmaf(__shfl_sync(0xffffffffu, q[j], c), cache_elem<KVT>(kr, c + 32 * j, kz), x);
+    }
     if (see) {
-      const uint8_t* kr = row_of(p.k_cache, t);
-      float x = 0.f;
-      for (int c = 0; c < D; ++c) x = fmaf(qs[c], cache_elem<KVT>(kr, c, kz), x);
       x *= p.scale * ks;
       if (p.softcap > 0.f) x = cap_score(x, p.softcap, capk);
       if (p.slopes) x -= slope * static_cast<float>(abs(rb.pos - t));
@@ -171,6 +176,23 @@ __device__ float2 attend_row(const AttendParams& p, int s, const SeqView& v, int
     store_out(p.out, p.out_dtype, (n * p.num_heads + h) * D + lane + 32 * j, o);
   }
   return make_float2(m, l);
+}
+
+// Out of line: in the other kernels it runs only for rows whose result is not finite.
+template <typename KVT, int D>
+__device__ __noinline__ void attend_row_again(const AttendParams& p, int s, const SeqView& v, int i, int h) {
+  attend_row<KVT, D>(p, s, v, i, h);
+}
+
+// The 32 visibility bits of positions b0 .. b0 + 31 in a drafted tree's mask row (words tree[0 .. words)): bit
+// position - first from position `first` on, ones before it.
+__device__ __forceinline__ uint32_t tree_bits(const uint64_t* tree, int words, int first, int b0) {
+  const int k0 = b0 - first;  // node of the first position (may be negative)
+  if (k0 <= -32) return 0xffffffffu;
+  const int kk = max(k0, 0), w = kk >> 6, sh = kk & 63;
+  uint64_t x = w < words ? tree[w] >> sh : 0ull;
+  if (sh > 32 && w + 1 < words) x |= tree[w + 1] << (64 - sh);
+  return k0 >= 0 ? static_cast<uint32_t>(x) : (static_cast<uint32_t>(x) << (-k0)) | ((1u << (-k0)) - 1u);
 }
 
 }  // namespace pa

@@ -161,8 +161,6 @@ struct TcParams {
   int slots;         // records of one stream per CTA: paired 2, alternating 4
   int* counters;     // arrivals: paired: by the segment's first CTA; alternating: by s * H_kv + kvh
   float* records;
-  float* scores;     // mass: scores [S][H_q][score_stride] in the log2 domain
-  int score_stride;
 };
 
 // Position tiles [lo, hi) of row tile m of a sequence.
@@ -311,17 +309,10 @@ struct TcTraits {
   static constexpr int KF = 0, KE = KF + NST, VF = KE + NST, VE = VF + NST, QF = VE + NST, QE = QF + 2, SF = QE + 2,
                        PF = SF + 2, OD = PF + 2, RB = OD + 2, NBAR = RB + 2;
   static constexpr int OFF_MISC = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;  // tmem address, flags, scan scratch
-  static constexpr int OFF_ROWQ = OFF_MISC + 256;                         // attend_row: D floats per softmax warp
-  static constexpr int OFF_FRAG = OFF_ROWQ + 8 * D * 4;                   // WarpFrag per warp, one more for warp 1
+  static constexpr int OFF_FRAG = OFF_MISC + 256;                         // WarpFrag per warp, one more for warp 1
   static constexpr int OFF_PREFIX = OFF_FRAG + (13 * static_cast<int>(sizeof(WarpFrag)) + 15) / 16 * 16;
   static size_t smem_bytes(int num_seqs) { return 1024 + OFF_PREFIX + static_cast<size_t>(num_seqs + 1) * 4; }
 };
-
-// attend_row out of line: it runs only for rows whose result is not finite
-template <typename KVT, int D>
-__device__ __noinline__ float2 attend_row_again(const AttendParams& p, int s, const SeqView& v, int i, int h, float* qs) {
-  return attend_row<KVT, D>(p, s, v, i, h, qs);
-}
 
 // ----------------------------------------------------------------- kernel
 
@@ -662,7 +653,6 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     const int wq = warp & 3;                       // TMEM lanes 32 wq ..
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * 128 + lanes;
-    float* const rowq = reinterpret_cast<float*>(sm + Tr::OFF_ROWQ) + (warp - 4) * D;
     constexpr float kLog2e = 1.4426950408889634f;
     // f16 weights carry a factor 2^7 (m is lowered by it), so that weights down to 2^-31 of the largest are normal
     constexpr float kLift = Tr::BF16 ? 0.f : 7.f;
@@ -710,7 +700,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const float sc2 = sc * kLog2e;
       const float capk = a.softcap > 0.f ? 2.f * kLog2e * sc / a.softcap : 0.f, cap2 = a.softcap * kLog2e;
       float m = -INFINITY, l = 0.f;
-      float* const score_row = a.mass && valid ? p.scores + (static_cast<int64_t>(f.s) * a.num_heads + h) * p.score_stride : nullptr;
+      float* const score_row = a.mass && valid ? a.scores + (static_cast<int64_t>(f.s) * a.num_heads + h) * a.score_stride : nullptr;
 
       for (int j = j0; ok && j < f.t1; j += step, ++jobs) {
         if (!wait(Tr::SF + t, static_cast<uint32_t>(jobs) & 1u)) { ok = false; break; }
@@ -745,20 +735,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
               // bits [lo, hi) of this 32-position chunk
               const int lo = max(0, min(32, rb.lo - b0)), hi = max(0, min(32, rb.hi - b0));
               uint32_t see = (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & (lo >= 32 ? 0u : 0xffffffffu << lo);
-              if (tree && b0 + 32 > first) {
-                // positions first + k need bit k; those before first are all visible
-                uint32_t bits = 0u;
-                if (valid) {
-                  const int k0 = b0 - first;        // node of the chunk's first position (may be negative)
-                  const int kk = max(k0, 0);
-                  const int w = kk >> 6, sh = kk & 63;
-                  uint64_t x = w < a.tree_words ? tree[w] >> sh : 0ull;
-                  if (sh > 32 && w + 1 < a.tree_words) x |= tree[w + 1] << (64 - sh);
-                  bits = k0 >= 0 ? static_cast<uint32_t>(x)
-                                 : (static_cast<uint32_t>(x) << (-k0)) | ((1u << (-k0)) - 1u);
-                }
-                see &= bits;
-              }
+              if (tree && valid) see &= tree_bits(tree, a.tree_words, first, b0);
 #pragma unroll
               for (int k = 0; k < 32; ++k) z[32 * c + k] = (see >> k) & 1u ? z[32 * c + k] : -INFINITY;
             }
@@ -854,8 +831,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           while (again) {
             const int k = __ffs(again) - 1;
             again &= again - 1;
-            const float2 ml = attend_row_again<KVT, D>(a, f.s, f.v, __shfl_sync(0xffffffffu, qi, k), __shfl_sync(0xffffffffu, h, k), rowq);
-            (void)ml;
+            attend_row_again<KVT, D>(a, f.s, f.v, __shfl_sync(0xffffffffu, qi, k), __shfl_sync(0xffffffffu, h, k));
           }
           if (a.mass && valid) a.row_stats[static_cast<int64_t>(f.s) * a.num_heads + h] = stats;
         }
@@ -938,7 +914,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             bad |= !(fabsf(o) < INFINITY);
             store_out(a.out, a.out_dtype, o0 + lane + 32 * q, o);
           }
-          if (__any_sync(0xffffffffu, bad)) attend_row_again<KVT, D>(a, f.s, f.v, i, hh, rowq);
+          if (__any_sync(0xffffffffu, bad)) attend_row_again<KVT, D>(a, f.s, f.v, i, hh);
           if (a.mass && lane == 0) a.row_stats[static_cast<int64_t>(f.s) * a.num_heads + hh] = make_float2(M, L);
         }
         if ((threadIdx.x & 127) == 0) *counter = 0;  // ready for the next call

@@ -64,6 +64,10 @@
 //    same recurrence after its own unit loop, one row per lane, writes
 //    out[s, kvh*G .. kvh*G+G-1] and resets the counter.  Nothing waits on
 //    another warp, so the kernel cannot deadlock.
+//  * The variants of pa_attend (AP = 2) add the score modifiers, masks, ragged
+//    query rows and stored scores of include/pa.h; every difference is behind
+//    `if constexpr`, so the decode's own variants compile to what they were.
+//    They see the call through DecodeParams::att.
 //  * Every wait on an mbarrier is bounded by %globaltimer; on expiry the warp
 //    records PA_DEVERR_TIMEOUT, waits (bounded) for its own copies and
 //    returns.
@@ -71,6 +75,7 @@
 
 #include <type_traits>
 
+#include "pa_attend.cuh"
 #include "pa_common.cuh"
 #include "pa_kernels.h"
 
@@ -149,6 +154,7 @@ __device__ __forceinline__ int clamped_len(const DecodeParams& p, int s, bool re
 // partitions.
 struct WorkIter {
   int s, kvh, j, jend, j0, T;
+  int L;          // pa_attend: queries of the sequence
   int nu;         // units of the segment that are attended (from unit ulo on)
   int ulo;        // first attended unit of the sequence
   int lo;         // first attended position (sliding window), 0 without one
@@ -176,8 +182,8 @@ __device__ __forceinline__ int find_seq(const int* prefix, int S, long long u) {
 
 // First attended position of a sequence of length T: that of its first
 // query (position T - q_len) under a sliding window, else 0.
-__device__ __forceinline__ int window_lo(const DecodeParams& p, int T) {
-  const int first = T - p.q_len + 1;
+__device__ __forceinline__ int window_lo(const DecodeParams& p, int T, int q_len) {
+  const int first = T - q_len + 1;
   return (p.window > 0 && first > p.window) ? first - p.window : 0;
 }
 
@@ -198,6 +204,8 @@ __device__ __forceinline__ int window_lo(const DecodeParams& p, int T) {
 // a sequence with prefix[it.s] <= it.u (the ring's positions only grow): the
 // sequence of it.u is found by scanning forward from it, one or two
 // shared-memory reads per fragment, not a search over the whole batch.
+// (ATT: the variants of pa_attend keep each sequence's query count after the lengths.)
+template <bool ATT>
 __device__ __forceinline__ bool frag_balanced(WorkIter& it, const int* prefix, const DecodeParams& p, int ur_shift) {
   const int Hkv = p.num_kv_heads;
   const int beta = p.frag_cost;
@@ -220,7 +228,8 @@ __device__ __forceinline__ bool frag_balanced(WorkIter& it, const int* prefix, c
     it.s = s;
     it.nu = nu;
     it.T = prefix[p.num_seqs + 1 + s];  // clamped length, cached by the prologue
-    it.lo = window_lo(p, it.T);
+    if constexpr (ATT) it.L = prefix[2 * p.num_seqs + 1 + s];
+    it.lo = window_lo(p, it.T, ATT ? it.L : p.q_len);
     it.ulo = it.lo >> ur_shift;
     it.kvh = kvh;
     it.j0 = it.ulo + ja;
@@ -256,7 +265,7 @@ __device__ __forceinline__ void frag_fixed(WorkIter& it, const int* prefix, cons
   it.kvh = rr / parts;
   const int part = rr % parts;
   it.T = prefix[p.num_seqs + 1 + s];  // clamped length, cached by the prologue
-  it.lo = window_lo(p, it.T);
+  it.lo = window_lo(p, it.T, p.q_len);
   it.ulo = it.lo >> ur_shift;
   const int nu_all = (it.T + (1 << ur_shift) - 1) >> ur_shift;
   it.nu = nu_all - it.ulo;
@@ -267,6 +276,7 @@ __device__ __forceinline__ void frag_fixed(WorkIter& it, const int* prefix, cons
   it.slot = (parts == 1) ? -1 : it.r;
 }
 
+template <bool ATT>
 __device__ __forceinline__ void iter_next_fragment(WorkIter& it, const int* prefix, const DecodeParams& p,
                                                    bool fixed, int ur_shift) {
   it.frag_idx++;
@@ -276,7 +286,7 @@ __device__ __forceinline__ void iter_next_fragment(WorkIter& it, const int* pref
     frag_fixed(it, prefix, p, ur_shift);
   } else {
     it.u = it.fend;
-    if (!frag_balanced(it, prefix, p, ur_shift)) it.valid = false;
+    if (!frag_balanced<ATT>(it, prefix, p, ur_shift)) it.valid = false;
   }
 }
 
@@ -316,10 +326,11 @@ struct MergeSlots {
 // depend on which warp merges.  The rows leave through shared memory
 // (swizzled by 16-byte chunk) as whole rows, 16 bytes per lane.
 template <int GM, int D, int REC>
-__device__ __forceinline__ void merge_segment(const float* records, const MergeSlots& ms, int nfr, int lane, int R,
+__device__ __forceinline__ bool merge_segment(const float* records, const MergeSlots& ms, int nfr, int lane, int R,
                                               int G, int num_heads, float vs, float voff, void* out, int out_dtype,
                                               int64_t seq_row0, int row0, uint32_t buf, float* bufp,
-                                              int cap, uint32_t mbar, uint32_t& mpar, unsigned int* err) {
+                                              int cap, uint32_t mbar, uint32_t& mpar, unsigned int* err,
+                                              float2* stats = nullptr) {
   constexpr int PER = GM * D / 32;  // accumulator elements per lane
   static_assert(REC % 4 == 0, "records are whole 16-byte chunks");
   static_assert(32 % GM == 0 && D % 32 == 0 && GM * D <= REC, "one row per lane; output staging fits a record");
@@ -363,11 +374,15 @@ __device__ __forceinline__ void merge_segment(const float* records, const MergeS
   // chunk (d / 4) ^ (g % 8), so that both the writes and the row reads below
   // spread over the banks
   const float inv = L > 0.f ? vs / L : 0.f, off = L > 0.f ? voff : 0.f;  // a row that saw nothing: 0
+  bool bad = L != L;  // a row that is not finite (pa_attend computes it again)
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int d = (lane + 32 * j) / GM;
-    bufp[g * D + ((((d >> 2) ^ (g & 7)) << 2) | (d & 3))] = fmaf(o[j], inv, -off);
+    const float x = fmaf(o[j], inv, -off);
+    bad |= !(fabsf(x) < INFINITY);
+    bufp[g * D + ((((d >> 2) ^ (g & 7)) << 2) | (d & 3))] = x;
   }
+  if (stats != nullptr && lane < R) stats[lane] = make_float2(M, L);
   __syncwarp();
   const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
   for (int r = 0; r < R; ++r) {
@@ -382,6 +397,7 @@ __device__ __forceinline__ void merge_segment(const float* records, const MergeS
   // the next merge's bulk copies overwrite this staging area
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
+  return bad && g < R;
 }
 
 template <typename QT, typename KVT, int D, int GM, int UR_, int AP>
@@ -409,11 +425,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   const int BOX = unit_in_block ? UR : B;
   const int upb_shift = unit_in_block ? p.block_shift - Tr::UR_SHIFT : 0;  // log2(units per block)
   const int bpu_shift = unit_in_block ? 0 : Tr::UR_SHIFT - p.block_shift;  // log2(blocks per unit)
-  const bool fixed = p.partition_units > 0;
+  constexpr bool ATT = AP == 2;  // a pa_attend call: score modifiers, ragged queries
+  const bool fixed = !ATT && p.partition_units > 0;
 
   const int NS = p.stages;  // pipeline depth per ring
-  // fused append (AP): stages also carry the new K/V rows
-  constexpr bool append = AP != 0;
+  // fused append (AP = 1): stages also carry the new K/V rows
+  constexpr bool append = AP == 1;
   // Several queries per sequence (16-row variants): the R = q_len * G rows of
   // a segment are served by NC = ceil(R / 16) consumer warps that share one
   // ring, warp k of the ring taking rows 16k .. 16k + 15 of every unit; the
@@ -428,7 +445,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   // scan scratch, then the producer's block-table ring (16 ints per ring)
   int* prefix = reinterpret_cast<int*>(base + RW * wsm);
   int* lens = prefix + (S + 1);
-  int* scan_tmp = lens + S;
+  int* scan_tmp = lens + (ATT ? 2 * S : S);  // pa_attend: each sequence's query count follows its length
   // 8-bit caches: the per-KV-head K scale, V scale and (INT8) zero-point
   // constants, staged once per CTA so that no fragment waits on them
   float* hp_ks = reinterpret_cast<float*>(scan_tmp + NWARP);
@@ -436,12 +453,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   uint32_t* hp_zk = reinterpret_cast<uint32_t*>(hp_vs + kMaxHeadParams);
   uint32_t* hp_zv = hp_zk + kMaxHeadParams;
   constexpr int kHeadWords = Tr::B8 ? 4 * kMaxHeadParams : 0;
-  const uint32_t table_ring_u32 = base_u32 + RW * wsm + align_up_c((2 * S + 1 + NWARP + kHeadWords) * 4, 16);
+  const uint32_t table_ring_u32 = base_u32 + RW * wsm + align_up_c(((ATT ? 3 : 2) * S + 1 + NWARP + kHeadWords) * 4, 16);
 
   // A kernel launched after this one with programmatic serialization (the
   // next step's cache write) may be scheduled now; it waits for this grid
   // before it touches memory.
   griddep_launch_dependents();
+  if constexpr (ATT) griddep_wait();  // pa_attend reads nothing early
   if (threadIdx.x == 0) {
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
@@ -469,7 +487,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       if (s < S) {
         const int T = clamped_len(p, s, blockIdx.x == 0);
         lens[s] = T;
-        const int nu = ((T + UR - 1) >> Tr::UR_SHIFT) - (window_lo(p, T) >> Tr::UR_SHIFT);
+        int nu;
+        if constexpr (ATT) {
+          const int L = seq_view(p.att, s, blockIdx.x == 0).L;
+          lens[S + s] = L;
+          nu = L > 0 ? ((T + UR - 1) >> Tr::UR_SHIFT) - (window_lo(p, T, L) >> Tr::UR_SHIFT) : 0;
+        } else {
+          nu = ((T + UR - 1) >> Tr::UR_SHIFT) - (window_lo(p, T, p.q_len) >> Tr::UR_SHIFT);
+        }
         // fixed: partitions; balanced: cost positions (units + fragment overhead)
         units = (fixed ? (nu + p.partition_units - 1) / p.partition_units : (nu > 0 ? nu + p.frag_cost : 0)) * Hkv;
       }
@@ -514,6 +539,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   // ---- 3. the share of ring c (global ring id gc)
   const int nw_total = gridDim.x * RW;
   const long long U = prefix[S];  // partitions (fixed) or cost positions (balanced) of the batch
+  // pa_attend: row of q and out of the sequence's first query (q_starts validated above; unused otherwise)
+  auto first_row = [&](int s) -> int64_t { return p.att.q_starts ? __ldg(p.att.q_starts + s) : s; };
   const int min_share = kMinUnitsPerWarp + (fixed ? 0 : p.frag_cost);
   long long want = (U + min_share - 1) / min_share;
   const int nw_eff = fixed ? nw_total : static_cast<int>(want < 1 ? 1 : (want < nw_total ? want : nw_total));
@@ -530,7 +557,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       w.u = gc * U / nw_eff;
       w.u1 = (gc + 1) * U / nw_eff;
       w.s = find_seq(prefix, S, w.u);
-      w.valid = frag_balanced(w, prefix, p, Tr::UR_SHIFT);
+      w.valid = frag_balanced<ATT>(w, prefix, p, Tr::UR_SHIFT);
     }
   };
 
@@ -565,7 +592,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       cp_async_commit();
       rs_pf = (rs_pf + 1) & 3;
       ++pf;
-      if (++ah.j == ah.jend) iter_next_fragment(ah, prefix, p, fixed, Tr::UR_SHIFT);
+      if (++ah.j == ah.jend) iter_next_fragment<ATT>(ah, prefix, p, fixed, Tr::UR_SHIFT);
     };
     while (ah.valid && pf < kTablePrefetch) fetch_tables();
     int nq = 0;  // several queries: query loads issued into this lane's ring buffer
@@ -586,7 +613,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       const int nbox = unit_in_block ? 1 : min(1 << bpu_shift, it.nblk - bj0);
       const int box0 = first_box(it, bj0);
       const int row_in_block = unit_in_block ? (it.j - (bj0 << upb_shift)) * UR : 0;
-      const int qlen = GM > 8 ? p.q_len : 1;  // only 16-row variants serve several queries
+      const int qlen = GM > 8 ? (ATT ? it.L : p.q_len) : 1;  // only 16-row variants serve several queries
       const uint32_t qbytes = new_frag ? static_cast<uint32_t>(qlen * G * D * 2) : 0u;
       // this unit's entries were fetched pf - 1 units before the newest fetch
       if (pf >= 3) {
@@ -634,10 +661,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         // rows (query i, head g) of the group, query-major: [q_len][G][D],
         // into the stage (one query) or the ring's query buffer (several)
         const uint32_t qdst = kMQ ? cbase + OFF_QBUF : kdst + 2 * Tr::TILE;
+        const int64_t qrow0 = ATT ? first_row(it.s) : 0;
         for (int i = 0; i < qlen; ++i) {
-          const uint8_t* qsrc =
-              static_cast<const uint8_t*>(p.q) +
-              (static_cast<int64_t>(it.s) * p.q_stride + (static_cast<int64_t>(i) * p.num_heads + it.kvh * G) * D) * 2;
+          const int64_t qelem =
+              ATT ? (qrow0 + i) * p.q_stride + static_cast<int64_t>(it.kvh) * G * D
+                  : static_cast<int64_t>(it.s) * p.q_stride + (static_cast<int64_t>(i) * p.num_heads + it.kvh * G) * D;
+          const uint8_t* qsrc = static_cast<const uint8_t*>(p.q) + qelem * 2;
           bulk_load(qdst + i * G * D * 2, qsrc, G * D * 2, bar);
         }
         ++nq;
@@ -653,7 +682,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         pph ^= 1;
       }
       if (ah.valid) fetch_tables();
-      if (++it.j == it.jend) iter_next_fragment(it, prefix, p, fixed, Tr::UR_SHIFT);
+      if (++it.j == it.jend) iter_next_fragment<ATT>(it, prefix, p, fixed, Tr::UR_SHIFT);
     };
     // Everything above reads only seq_lens and block_tables.  Under a
     // programmatic dependent launch the grid before this one on the stream
@@ -671,8 +700,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     // empty sequences attend to nothing: their outputs are zero
     for (int s = blockIdx.x * 32 + lane; s < S; s += gridDim.x * 32) {
       if (lens[s] == 0) {
-        const int64_t n = static_cast<int64_t>(p.q_len) * p.num_heads * D;
-        for (int64_t i = 0; i < n; ++i) store_out(p.out, p.out_dtype, static_cast<int64_t>(s) * n + i, 0.f);
+        const int64_t n = static_cast<int64_t>(ATT ? lens[S + s] : p.q_len) * p.num_heads * D;
+        const int64_t o0 = ATT ? first_row(s) * p.num_heads * D : static_cast<int64_t>(s) * n;
+        for (int64_t i = 0; i < n; ++i) store_out(p.out, p.out_dtype, o0 + i, 0.f);
       }
     }
     // 8-bit caches: the per-head constants every consumer needs (read after
@@ -748,6 +778,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 
   // ===================================================================== consumer
   constexpr bool MB = Tr::MMA_BF16;
+  // INT8 V as 1152 + code with the bias taken off the output; pa_attend takes the zero point off each code instead: the
+  // bias is ~1000 times an average of many values, and its float32 rounding would show in 16-bit outputs
+  constexpr bool kBiasV = std::is_same<KVT, i8_t>::value && !ATT;
   const int c = warp - 1;
   const int ring_id = c / NC;  // the ring this warp consumes
   const int rg = c - ring_id * NC;  // its 16-row group of the segment's rows (several queries)
@@ -834,10 +867,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   // compile the single-query case, whose rows share one set of bounds.
   constexpr int NH = GM > 8 ? 2 : 1;
   constexpr bool MQ = GM > 8;
-  const int QL = MQ ? p.q_len : 1;
-  const int R = QL * G;                          // rows of the segment
-  const int row0 = MQ ? 16 * rg : 0;             // this warp's first row of them
-  const int Rw = MQ ? min(16, R - row0) : R;     // and how many it owns
+  int QL = MQ ? p.q_len : 1;                     // (pa_attend: of the fragment's sequence)
+  const int row0 = MQ ? 16 * rg : 0;             // this warp's first row of the segment's QL * G
+  int Rw = MQ ? min(16, QL * G - row0) : G;      // and how many it owns
   uint32_t qa0[Tr::KS], qa1[Tr::KS];  // A operand, row g (zero when g >= R)
   uint32_t qb0[Tr::KS], qb1[Tr::KS];  // A operand, row g + 8 (NH == 2)
   // softmax state rows of this lane: g and g + 8 (several queries), else
@@ -847,6 +879,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   float acc[Tr::KS][NH][4];           // O^T: rows = head_dim columns, cols = A rows 8h + 2t, 8h + 2t + 1
   int hi_abs[NH], lo_abs[NH];         // last / first position row g + 8h may see (MQ)
   float score_scale = p.qk_scale_log2;
+  // pa_attend: cap, slopes (log2 domain) and positions of this lane's softmax rows, their mask rows and stored scores
+  constexpr float kLog2e = 1.4426950408889634f;
+  [[maybe_unused]] float capk = 0.f, cap2 = 0.f, slope2[NR];
+  [[maybe_unused]] int qpos[NR];
+  [[maybe_unused]] const uint64_t* tree[NR];
+  [[maybe_unused]] float* score_row[NR];
   uint32_t zpk2 = 0u, zpv2 = 0u;  // INT8: f16x2(1152 + zero point) of this KV head
 
   // One unit: S^T = Q K^T, online-softmax update, O^T += V^T P^T.
@@ -902,9 +940,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float x = sc[mt][e] * score_scale;
+          const int tok = 16 * mt + 8 * (e >> 1) + (k8bit ? sigma(gid) : gid);
+          if constexpr (ATT) {
+            if (p.att.softcap > 0.f) x = cap2 - __fdividef(2.f * cap2, 1.f + fast_exp2(sc[mt][e] * capk));
+            if (p.att.slopes) x -= slope2[e & 1] * static_cast<float>(qpos[0] - (j * UR + tok));
+          }
           if constexpr (!FULL) {
-            const int tok = 16 * mt + 8 * (e >> 1) + (k8bit ? sigma(gid) : gid);
             x = (tok < n_valid && tok >= lo_rel) ? x : -INFINITY;
+          }
+          if constexpr (ATT) {
+            if (score_row[e & 1] && tok < n_valid && tok >= lo_rel) score_row[e & 1][j * UR + tok] = x;
           }
           sc[mt][e] = x;
           if (e & 1) {
@@ -996,6 +1041,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           hr = hi_abs[h] - j * UR;
           lr = lo_abs[h] - j * UR;
         }
+        [[maybe_unused]] uint32_t bits = 0xffffffffu;  // pa_attend: what the row's tree mask leaves of the unit
+        if constexpr (ATT) {
+          if (tree[h]) bits = tree_bits(tree[h], p.att.tree_words, it.T - QL, j * UR);
+        }
 #pragma unroll
         for (int nt = 0; nt < Tr::NT; ++nt) {
 #pragma unroll
@@ -1005,6 +1054,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
               const int tok = nt * 8 + (k8bit ? sigma(2 * tig + e) : 2 * tig + e);
               bool ok = tok < n_valid && tok >= lo_rel;
               if constexpr (MQ) ok = ok && tok <= hr && tok >= lr;
+              if constexpr (ATT) {
+                if (p.att.softcap > 0.f) x = cap2 - __fdividef(2.f * cap2, 1.f + fast_exp2(sc[nt][2 * h + e] * capk));
+                if (p.att.slopes) x -= slope2[h] * fabsf(static_cast<float>(qpos[h] - (j * UR + tok)));
+                ok = ok && ((bits >> tok) & 1u);
+                if (score_row[h] && ok) score_row[h][j * UR + tok] = x;
+              }
               x = ok ? x : -INFINITY;
             }
             sc[nt][2 * h + e] = x;
@@ -1094,7 +1149,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           const uint32_t lo01 = prmt(x0, x1, 0x5140u), lo23 = prmt(x0, x1, 0x7362u);
           const uint32_t hi01 = prmt(y0, y1, 0x5140u), hi23 = prmt(y0, y1, 0x7362u);
           uint32_t d0l, d1l, d2l, d3l, d0h, d1h, d2h, d3h;
-          if constexpr (std::is_same<KVT, i8_t>::value) {
+          if constexpr (kBiasV) {
             // 1152 + code: the output subtracts (1152 + zp) * v_scale once
             widen4_i8_biased(lo01, d0l, d1l);
             widen4_i8_biased(lo23, d2l, d3l);
@@ -1178,6 +1233,18 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     __syncwarp();
   };
 
+  // pa_attend, several queries: the warp's rows of a segment from the definition
+  [[maybe_unused]] auto again = [&](int s, int kvh, int T, int L, int64_t rows0, int n) {
+    if constexpr (ATT && MQ) {
+      SeqView v;
+      v.T = T;
+      v.L = L;
+      v.row0 = static_cast<int>(rows0);
+      for (int r = 0; r < n; ++r)
+        attend_row_again<KVT, D>(p.att, s, v, (row0 + r) / G, kvh * G + (row0 + r) % G);
+    }
+  };
+
   // Merge of split segment x = s * H_kv + kvh by the warp that arrived last,
   // after the unit loop (list in the workspace): an inlined merge inside the
   // loop costs the loop registers, and the arrival itself does not wait: its
@@ -1223,15 +1290,26 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     }
     float vs = 1.f, voff = 0.f;
     if constexpr (k8bit) vs = hp_vs[kvh];
-    if constexpr (std::is_same<KVT, i8_t>::value) voff = v_bias_offset(hp_zv[kvh], vs);
-    const int64_t seq_row0 = static_cast<int64_t>(s) * QL * p.num_heads + static_cast<int64_t>(kvh) * G;
+    if constexpr (kBiasV) voff = v_bias_offset(hp_zv[kvh], vs);
+    const int mL = ATT && MQ ? lens[S + s] : QL;  // pa_attend: queries and rows of this sequence
+    const int mR = ATT && MQ ? min(16, mL * G - row0) : Rw;
+    const int64_t mrow = ATT ? first_row(s) : static_cast<int64_t>(s) * QL;
+    const int64_t seq_row0 = mrow * p.num_heads + static_cast<int64_t>(kvh) * G;
     // the ring's stages are idle after the unit loop (every warp of the ring
     // has passed the ring barrier): warp rg stages its records in its share
     const int share = (NS * STG) / NC / (Tr::REC * 4) * (Tr::REC * 4);
-    merge_segment<GM, D, Tr::REC>(p.part_records, ms, nfr, lane, Rw, G, p.num_heads, vs, voff, p.out, p.out_dtype, seq_row0,
+    float2* stats = nullptr;
+    if constexpr (ATT) {
+      if (p.att.mass) stats = p.att.row_stats + static_cast<int64_t>(s) * p.num_heads + kvh * G + row0;
+    }
+    [[maybe_unused]] const bool bad =
+        merge_segment<GM, D, Tr::REC>(p.part_records, ms, nfr, lane, mR, G, p.num_heads, vs, voff, p.out, p.out_dtype, seq_row0,
                                   row0, wbase_u32 + Tr::OFF_STAGES + rg * share,
                                   reinterpret_cast<float*>(const_cast<uint8_t*>(wbase) + Tr::OFF_STAGES + rg * share),
-                                  share / (Tr::REC * 4), wbase_u32 + Tr::OFF_MERGE + 8 * rg, merge_par, p.err);
+                                  share / (Tr::REC * 4), wbase_u32 + Tr::OFF_MERGE + 8 * rg, merge_par, p.err, stats);
+    if constexpr (ATT && MQ) {
+      if (__any_sync(0xffffffffu, bad)) again(s, kvh, lens[s], mL, mrow, mR);
+    }
     if (lane == 0) p.seg_counters[x * NC + rg] = 0;
   };
 
@@ -1251,6 +1329,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     // subnormals, an absolute error below 2^-38 of the largest element.
     constexpr bool q_rescale = k8bit && std::is_same<QT, bf16_t>::value;
     int qexp = 0;
+    [[maybe_unused]] int64_t row_base = 0;  // pa_attend: the sequence's first row of q and out
+    if constexpr (ATT) {
+      row_base = first_row(it.s);
+      if constexpr (MQ) {
+        QL = it.L;
+        Rw = min(16, QL * G - row0);  // may be negative: the ring's warps serve the longest sequence
+      }
+    }
     {
       // the query group rode on the fragment's first stage (into the ring's
       // query buffer with several queries)
@@ -1283,7 +1369,37 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           const int qi = row < Rw ? (row0 + row) / G : QL - 1;
           hi_abs[h] = it.T - QL + qi;
           lo_abs[h] = p.window > 0 ? hi_abs[h] - p.window + 1 : 0;
+          if constexpr (ATT) {
+            qpos[h] = hi_abs[h];
+            const bool mine = row < Rw;
+            if (p.att.tree_mask || p.att.prefix_lens) {
+              SeqView v;
+              v.T = it.T;
+              v.L = QL;
+              const RowBounds rb = row_bounds(p.att, v, seq_prefix(p.att, it.s, it.T), qi);
+              hi_abs[h] = rb.hi - 1;  // nothing at a negative position: -1
+            }
+            const int head = it.kvh * G + (mine ? (row0 + row) % G : 0);
+            slope2[h] = p.att.slopes ? __ldg(p.att.slopes + head) * kLog2e : 0.f;
+            tree[h] = p.att.tree_mask && mine ? p.att.tree_mask + (row_base + qi) * p.att.tree_words : nullptr;
+            score_row[h] = p.att.mass && mine
+                               ? p.att.scores + (static_cast<int64_t>(it.s) * p.num_heads + head) * p.att.score_stride
+                               : nullptr;
+          }
         }
+      }
+    }
+    if constexpr (ATT && !MQ) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 2 * tig + e;
+        const bool mine = row < G;
+        const int head = it.kvh * G + (mine ? row : 0);
+        qpos[e] = it.T - 1;
+        slope2[e] = p.att.slopes ? __ldg(p.att.slopes + head) * kLog2e : 0.f;
+        score_row[e] = p.att.mass && mine
+                           ? p.att.scores + (static_cast<int64_t>(it.s) * p.num_heads + head) * p.att.score_stride
+                           : nullptr;
       }
     }
     if constexpr (MQ) {
@@ -1327,6 +1443,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     score_scale = p.qk_scale_log2;
     if constexpr (k8bit) score_scale *= hp_ks[it.kvh];
     if constexpr (q_rescale) score_scale *= __int_as_float((127 - qexp) << 23);
+    if constexpr (ATT) {
+      if (p.att.softcap > 0.f) {
+        cap2 = p.att.softcap * kLog2e;
+        capk = score_scale * 2.f / p.att.softcap;  // score_scale holds log2(e)
+      }
+    }
     if constexpr (std::is_same<KVT, i8_t>::value) {
       zpk2 = hp_zk[it.kvh];
       zpv2 = hp_zv[it.kvh];
@@ -1395,14 +1517,15 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       }
       float vs = 1.f, voff = 0.f;  // out = acc * vs / l - voff (INT8: V entered as 1152 + code)
       if constexpr (k8bit) vs = hp_vs[it.kvh];
-      if constexpr (std::is_same<KVT, i8_t>::value) voff = v_bias_offset(hp_zv[it.kvh], vs);
+      if constexpr (kBiasV) voff = v_bias_offset(hp_zv[it.kvh], vs);
       // output row of A row r: out[s][r / G][kvh * G + r % G]
-      const int64_t seq_row0 = static_cast<int64_t>(it.s) * QL * p.num_heads + static_cast<int64_t>(it.kvh) * G;
+      const int64_t seq_row0 = (ATT ? row_base : static_cast<int64_t>(it.s) * QL) * p.num_heads + static_cast<int64_t>(it.kvh) * G;
       auto out_row = [&](int r) -> int64_t {
         if constexpr (!MQ) return seq_row0 + r;  // one query: row = head
         return seq_row0 + static_cast<int64_t>((row0 + r) / G) * p.num_heads + (row0 + r) % G;
       };
       if (it.slot < 0) {
+        [[maybe_unused]] bool bad = false;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           const int r0 = 8 * h + 2 * tig, r1 = r0 + 1;
@@ -1423,9 +1546,26 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const int d = dim_of(i, hf);
-              if (w0) store_out(p.out, p.out_dtype, o0 + d, fmaf(acc[i][h][2 * hf], i0, -b0));
-              if (w1) store_out(p.out, p.out_dtype, o1 + d, fmaf(acc[i][h][2 * hf + 1], i1, -b1));
+              const float x0 = fmaf(acc[i][h][2 * hf], i0, -b0), x1 = fmaf(acc[i][h][2 * hf + 1], i1, -b1);
+              if (w0) store_out(p.out, p.out_dtype, o0 + d, x0);
+              if (w1) store_out(p.out, p.out_dtype, o1 + d, x1);
+              if constexpr (ATT && MQ) bad = bad || (w0 && !(fabsf(x0) < INFINITY)) || (w1 && !(fabsf(x1) < INFINITY));
             }
+          }
+          if constexpr (ATT && MQ) bad = bad || (w0 && l0 != l0) || (w1 && l1 != l1);
+        }
+        if constexpr (ATT) {
+          if (p.att.mass) {  // (max, sum) of the rows this lane holds
+#pragma unroll
+            for (int h = 0; h < NR; ++h) {
+              const int row = MQ ? gid + 8 * h : 2 * tig + h;
+              if ((MQ ? tig : gid) == 0 && row < Rw)
+                p.att.row_stats[static_cast<int64_t>(it.s) * p.num_heads + it.kvh * G + row0 + row] = make_float2(m[h], lt[h]);
+            }
+          }
+          // a row that is not finite may owe it to a V row it does not see
+          if constexpr (MQ) {
+            if (__any_sync(0xffffffffu, bad)) again(it.s, it.kvh, it.T, QL, row_base, Rw);
           }
         }
       } else {
@@ -1487,7 +1627,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       }
     }
     ++it.j;
-    iter_next_fragment(it, prefix, p, fixed, Tr::UR_SHIFT);
+    iter_next_fragment<ATT>(it, prefix, p, fixed, Tr::UR_SHIFT);
   }
 
   // ---- the split merges this warp won
@@ -1522,7 +1662,7 @@ struct DecodeVariant {
   static size_t smem_bytes(int num_seqs, int warps, int rings, int stages, int stage) {
     constexpr int head_words = Tr::B8 ? 4 * kMaxHeadParams : 0;
     return 1024 + static_cast<size_t>(rings) * (Tr::warp_smem(stages, stage) + Tr::qbuf_bytes(warps / rings)) +
-           static_cast<size_t>(align_up_c((2 * num_seqs + 1 + warps + 1 + head_words) * 4, 16)) +
+           static_cast<size_t>(align_up_c(((AP == 2 ? 3 : 2) * num_seqs + 1 + warps + 1 + head_words) * 4, 16)) +
            static_cast<size_t>(rings) * 64;
   }
 
@@ -1548,7 +1688,7 @@ struct DecodeVariant {
     constexpr bool mq = GM > 8;
     if (nc < 1 || (!mq && nc != 1) || nc > 4) return false;
     // several queries: K and V only (the query rows have a buffer per ring)
-    const int stage = mq ? align_up_c(2 * Tr::TILE, 1024) : (AP ? Tr::STAGE_APPEND : Tr::STAGE);
+    const int stage = mq ? align_up_c(2 * Tr::TILE, 1024) : (AP == 1 ? Tr::STAGE_APPEND : Tr::STAGE);
     const int env_ns = tuning_override("PA_DECODE_STAGES");
     const int env_w = tuning_override("PA_DECODE_WARPS");
     int best_w = 0, best_occ = 0, best_ns = 0;

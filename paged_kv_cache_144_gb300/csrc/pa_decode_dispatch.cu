@@ -66,7 +66,7 @@ bool decode_geometry(const DecodeKey& key, int num_seqs, DecodeGeometry* geo) {
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const uint64_t k = (static_cast<uint64_t>(dev & 0xff) << 56) | (static_cast<uint64_t>(key.q_dtype & 0xf) << 52) |
                      (static_cast<uint64_t>(key.kv_dtype & 0xf) << 48) |
-                     (static_cast<uint64_t>(key.head_dim & 0xfff) << 36) |
+                     (static_cast<uint64_t>(key.head_dim & 0x7ff) << 36) | (static_cast<uint64_t>(key.append >> 1) << 47) |
                      (static_cast<uint64_t>(key.gmax & 0xf) << 32) | (static_cast<uint64_t>(key.unit_rows & 0xff) << 24) |
                      (static_cast<uint64_t>(key.append & 1) << 23) | (static_cast<uint64_t>(key.row_groups & 7) << 20) |
                      static_cast<uint64_t>(num_seqs & 0xfffff);

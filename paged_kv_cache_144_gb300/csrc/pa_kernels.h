@@ -30,6 +30,8 @@ int tuning_override(const char* name);
 unsigned int* device_error_word();                       // of the current device (nullptr on failure)
 int cuda_status(cudaError_t e, const char* where);       // PA_OK or PA_ERR_CUDA with the error's text recorded
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // nullptr when the driver has none
+bool encode_cache_map(CUtensorMap* map, const void* cache, int64_t num_blocks, int num_kv_heads, int block_size,
+                      int head_dim, int elem_bytes, int box_rows);
 
 struct ReshapeArgs {
   const void* k;
@@ -57,6 +59,50 @@ struct ReshapeArgs {
 cudaError_t launch_reshape_and_cache(const ReshapeArgs& a, cudaStream_t stream);
 cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, int64_t num_blocks, int64_t block_bytes,
                                const int32_t* pairs, int num_pairs, unsigned int* err, cudaStream_t stream);
+
+// One pa_attend call.
+struct AttendParams {
+  void* out;
+  int out_dtype;
+  const void* q;
+  int q_dtype;
+  int64_t q_stride;  // elements between consecutive query rows
+  const void* k_cache;
+  const void* v_cache;
+  int kv_dtype;
+  int64_t num_blocks;
+  const float* k_scale;         // 8-bit caches only
+  const float* v_scale;         // 8-bit caches only
+  const int32_t* k_zero_point;  // INT8 only
+  const int32_t* v_zero_point;  // INT8 only
+  const int32_t* block_tables;
+  int max_blocks_per_seq;
+  const int32_t* seq_lens;
+  const int32_t* q_starts;  // nullptr: one query per sequence
+  int max_q_len;
+  int num_tokens;  // rows of q and out
+  int num_seqs;
+  int num_heads;
+  int num_kv_heads;
+  int group;
+  int head_dim;
+  float scale;
+  int block_size;
+  int block_shift;
+  float softcap;             // 0: off
+  const float* slopes;       // nullptr: off
+  int window;                // 0: off
+  const int32_t* prefix_lens;
+  const uint64_t* tree_mask;
+  int tree_words;
+  float* mass;
+  int64_t mass_stride_seq, mass_stride_head;
+  float2* row_stats;  // mass: (max, sum) of each (sequence, head) row, in the scores' log2 domain
+  float* scores;      // mass: the scores [S][H_q][score_stride] of every attended position, log2 domain
+  int score_stride;
+  unsigned int* err;
+  bool pdl;
+};
 
 // Everything the decode kernel reads besides the two tensor maps.
 struct DecodeParams {
@@ -103,6 +149,7 @@ struct DecodeParams {
   uint64_t wait_limit_ns;       // limit of every wait on a pipeline barrier (PA_DEVERR_TIMEOUT after it)
   int withhold_copies;          // testing hook: the producer issues no copy, so every consumer wait runs out
   int early_kv;                 // K/V of units without a sequence's newest row may be copied before the wait
+  AttendParams att;             // variants with score modifiers only: the pa_attend call
 };
 
 // Compile-time variant of the decode kernel.
@@ -112,7 +159,7 @@ struct DecodeKey {
   int head_dim;   // 64 / 128
   int gmax;       // 1 / 4 / 8 (query heads per KV head, rounded up)
   int unit_rows;  // 16 / 32 / 64 rows per work unit
-  int append;     // 1: fused append (each stage also stages the new K/V rows)
+  int append;     // 1: fused append (each stage also stages the new K/V rows); 2: score modifiers (pa_attend)
   int row_groups; // consumer warps sharing a ring (1; up to 4 for the 16-row variants)
 };
 

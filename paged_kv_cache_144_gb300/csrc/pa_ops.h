@@ -23,48 +23,8 @@ struct RopeArgs {
 
 cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream);
 
-struct AttendParams {
-  void* out;
-  int out_dtype;
-  const void* q;
-  int q_dtype;
-  int64_t q_stride;  // elements between consecutive query rows
-  const void* k_cache;
-  const void* v_cache;
-  int kv_dtype;
-  int64_t num_blocks;
-  const float* k_scale;         // 8-bit caches only
-  const float* v_scale;         // 8-bit caches only
-  const int32_t* k_zero_point;  // INT8 only
-  const int32_t* v_zero_point;  // INT8 only
-  const int32_t* block_tables;
-  int max_blocks_per_seq;
-  const int32_t* seq_lens;
-  const int32_t* q_starts;  // nullptr: one query per sequence
-  int max_q_len;
-  int num_tokens;  // rows of q and out
-  int num_seqs;
-  int num_heads;
-  int num_kv_heads;
-  int group;
-  int head_dim;
-  float scale;
-  int block_size;
-  int block_shift;
-  float softcap;             // 0: off
-  const float* slopes;       // nullptr: off
-  int window;                // 0: off
-  const int32_t* prefix_lens;
-  const uint64_t* tree_mask;
-  int tree_words;
-  float* mass;
-  int64_t mass_stride_seq, mass_stride_head;
-  float2* row_stats;  // mass: (max, sum) of each (sequence, head) row, in the scores' log2 domain
-  unsigned int* err;
-  bool pdl;
-};
-
-cudaError_t launch_attend(AttendParams p, void* workspace, cudaStream_t stream);
+// A pa_status: PA_ERR_WORKSPACE before anything is enqueued, or that of the launches.
+int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 // (size_t)-1 when the device cannot be asked
 size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                               int max_blocks_per_seq, int max_q_len, int kv_dtype, bool accumulate);

@@ -175,15 +175,11 @@ PA_EXPORT int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q
   if (ps != PA_OK) return ps;
   if (q_stride < static_cast<int64_t>(num_heads) * head_dim) return PA_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(out) || q_stride % 8 != 0) return PA_ERR_ALIGN;
-  // the work of a call is counted in tiles of 128 positions per row tile, in 32 bits
+  // the work of a call is counted in tiles of 128 positions per row tile, or in units of 32 positions, in 32 bits
   if ((static_cast<int64_t>(num_tokens) * (num_heads / num_kv_heads) / 128 + num_seqs) * num_kv_heads * (cap / 128 + 2) >=
       (int64_t{1} << 31))
     return PA_ERR_SHAPE;
-  const size_t need = pa::attend_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
-                                                 max_blocks_per_seq, max_q_len, kv_dtype, o.mass != nullptr);
-  if (need == static_cast<size_t>(-1)) return PA_ERR_CUDA;
-  if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
-    return PA_ERR_WORKSPACE;
+  if (static_cast<int64_t>(num_seqs) * num_kv_heads * (cap / 32 + 4) >= (int64_t{1} << 31)) return PA_ERR_SHAPE;
   unsigned int* err = pa::device_error_word();
   if (!err) return PA_ERR_CUDA;
   pa::AttendParams p;
@@ -226,7 +222,7 @@ PA_EXPORT int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q
   p.mass_stride_head = o.mass_stride_head;
   p.err = err;
   p.pdl = o.pdl != 0;
-  return pa::cuda_status(pa::launch_attend(p, workspace, static_cast<cudaStream_t>(stream)), "pa_attend launch");
+  return pa::launch_attend(p, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 PA_EXPORT int pa_commit_tree(void* k_cache, void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
