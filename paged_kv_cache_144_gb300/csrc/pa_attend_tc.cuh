@@ -73,18 +73,25 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// One lane of the warp, always the same one, chosen in a way that leaves the branch on it warp-uniform to the compiler.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// Operand descriptors are passed as their low words: the high word is the same for all.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
       : "memory");
 }
 // 32 columns of this warp's 32 lanes
@@ -120,6 +127,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
 template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -138,12 +157,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Shared-memory operand descriptor, 128-byte swizzle: start address, leading
-// and stride byte offsets in 16-byte units, descriptor version 1.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(sbo >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
-}
+// Shared-memory operand descriptor, 128-byte swizzle: start address and leading byte offset (between 128-byte halves; used
+// by the MN-major operand) in 16-byte units in the low word; stride byte offset (between 8-row groups), descriptor
+// version 1 and the swizzle in the high word.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr & 0x3ffffu) >> 4) | ((1024u >> 4) << 16); }
+constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
 
 // Instruction descriptor: float32 accumulators, 16-bit operands, M = 128.
 constexpr uint32_t mma_idesc(bool bf16, bool b_mn_major, int n) {
@@ -511,6 +529,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     // ================================================================= MMA issuer
     constexpr uint32_t kIdQK = mma_idesc(Tr::BF16, false, kTile);
     constexpr uint32_t kIdPV = mma_idesc(Tr::BF16, true, D);
+    constexpr uint32_t kDescHi = desc_hi(Tr::GROUP);
     WarpFrag* const wq = wf + 11;  // fragments whose S products are next
     const Frag& fq = wq->f;
     bool have_q = next_frag(wq, prefix, p);
@@ -529,12 +548,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       if (!wait(Tr::KF + st, static_cast<uint32_t>(ktq / NST) & 1u)) return false;
       tc_fence_after();
       const bool last_use = !p.paired || t == 1;   // of this K tile
-      if (lane == 0) {
-        const uint32_t qa = base + Tr::OFF_Q + t * Tr::TILE_BYTES, kb = base + Tr::OFF_K + st * Tr::TILE_BYTES;
+      if (elect_one()) {
+        const uint32_t qa = desc_lo(base + Tr::OFF_Q + t * Tr::TILE_BYTES), kb = desc_lo(base + Tr::OFF_K + st * Tr::TILE_BYTES);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          const uint32_t o = (s >> 2) * 1024 + (s & 3) * 32;
-          tc_mma_ss(tmem + t * 128, smem_desc(qa + o, 16, Tr::GROUP), smem_desc(kb + o, 16, Tr::GROUP), kIdQK, s > 0);
+          const uint32_t o = ((s >> 2) * 1024 + (s & 3) * 32) >> 4;
+          tc_mma_ss(tmem + t * 128, qa + o, kb + o, kDescHi, kIdQK, s > 0);
         }
         tc_commit(bar(Tr::SF + t));
         if (last_use) tc_commit(bar(Tr::KE + st));
@@ -583,17 +602,16 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           if (!wait(Tr::PF + t, pf[t] & 1u)) { ok = false; break; }
           ++pf[t];
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t vb = base + Tr::OFF_V + st * Tr::TILE_BYTES;
+          if (elect_one()) {
+            const uint32_t vb = desc_lo(base + Tr::OFF_V + st * Tr::TILE_BYTES);
+            tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128, vb, kDescHi, kIdPV, !first);
 #pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
-              tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, smem_desc(vb + s * 2 * Tr::GROUP, 1024, Tr::GROUP),
-                        kIdPV, !(first && s == 0));
+            for (int s = 1; s < kTile / 16; ++s)
+              tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, vb + s * (2 * Tr::GROUP >> 4), kDescHi, kIdPV, true);
             if (p.split_p) {
 #pragma unroll
               for (int s = 0; s < kTile / 16; ++s)
-                tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 64 + s * 8,
-                          smem_desc(vb + s * 2 * Tr::GROUP, 1024, Tr::GROUP), kIdPV, 1);
+                tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 64 + s * 8, vb + s * (2 * Tr::GROUP >> 4), kDescHi, kIdPV, true);
             }
             tc_commit(bar(Tr::OD + t));
             if (e == per_tile - 1) tc_commit(bar(Tr::VE + st));
@@ -696,9 +714,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int first = f.v.T - f.v.L;              // tree: position of node 0
       const uint64_t* tree = a.tree_mask ? a.tree_mask + (static_cast<int64_t>(f.v.row0) + qi) * a.tree_words : nullptr;
       const float slope2 = a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
-      const float sc = a.scale;
-      const float sc2 = sc * kLog2e;
-      const float capk = a.softcap > 0.f ? 2.f * kLog2e * sc / a.softcap : 0.f, cap2 = a.softcap * kLog2e;
+      const float sc2 = a.scale * kLog2e;
+      const float capk = a.softcap > 0.f ? 2.f * sc2 / a.softcap : 0.f, cap2 = a.softcap * kLog2e;
+      // (a negative scale would turn the maximum of raw products into a minimum)
+      const bool modified = a.softcap > 0.f || a.slopes || a.mass || !(sc2 >= 0.f);
       float m = -INFINITY, l = 0.f;
       float* const score_row = a.mass && valid ? a.scores + (static_cast<int64_t>(f.s) * a.num_heads + h) * a.score_stride : nullptr;
 
@@ -711,24 +730,30 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, z + 32 * c);
           tmem_wait_ld();
-          if (a.softcap > 0.f) {
+          const bool full = rb.lo <= tb && rb.hi >= tb + kTile && (!tree || tb + kTile <= first);
+          const bool masked = !__all_sync(0xffffffffu, full || !valid);
+          // z: scores in the log2 domain, or (the plain case) raw products that the exponent's FMA scales by mul
+          float mul = sc2;
+          if (masked || modified) {
+            mul = 1.f;
+            if (a.softcap > 0.f) {
 #pragma unroll
-            for (int c = 0; c < kTile; ++c) z[c] = cap2 - __fdividef(2.f * cap2, 1.f + fast_exp2(z[c] * capk));
-          } else {
+              for (int c = 0; c < kTile; ++c) z[c] = cap2 - __fdividef(2.f * cap2, 1.f + fast_exp2(z[c] * capk));
+            } else {
 #pragma unroll
-            for (int c = 0; c < kTile; c += 2) {
-              const float2 x = fmul2(make_float2(z[c], z[c + 1]), make_float2(sc2, sc2));
-              z[c] = x.x;
-              z[c + 1] = x.y;
+              for (int c = 0; c < kTile; c += 2) {
+                const float2 x = fmul2(make_float2(z[c], z[c + 1]), make_float2(sc2, sc2));
+                z[c] = x.x;
+                z[c + 1] = x.y;
+              }
+            }
+            if (a.slopes) {
+              const float d0 = static_cast<float>(tb - rb.pos);
+#pragma unroll
+              for (int c = 0; c < kTile; ++c) z[c] = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), z[c]);
             }
           }
-          if (a.slopes) {
-            const float d0 = static_cast<float>(tb - rb.pos);
-#pragma unroll
-            for (int c = 0; c < kTile; ++c) z[c] = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), z[c]);
-          }
-          const bool full = rb.lo <= tb && rb.hi >= tb + kTile && (!tree || tb + kTile <= first);
-          if (!__all_sync(0xffffffffu, full || !valid)) {
+          if (masked) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int b0 = tb + 32 * c;
@@ -745,17 +770,54 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             for (int c = 0; c < kTile; c += 4)
               *reinterpret_cast<float4*>(score_row + tb + c) = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
           }
-          float mx0 = fmaxf(z[0], z[1]), mx1 = fmaxf(z[2], z[3]);
+          // Weights of the tile against the reference maximum ms, summed and stored as the 16-bit operand of P V (hi, then
+          // lo in the split form); returns the tile's largest score.
+          float lt = 0.f;
+          auto weights_as = [&](auto split, float ms) -> float {
+            constexpr bool kSplit = decltype(split)::value;
+            float2 sum = make_float2(0.f, 0.f);
+            float mx = z[0];
+            const float2 mul2 = make_float2(mul, mul), neg = make_float2(-ms, -ms);
 #pragma unroll
-          for (int c = 4; c < kTile; c += 4) {
-            mx0 = fmaxf(mx0, fmaxf(z[c], z[c + 1]));
-            mx1 = fmaxf(mx1, fmaxf(z[c + 2], z[c + 3]));
+            for (int c = 0; c < 4; ++c) {
+              uint32_t hi[16], lo[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float z0 = z[32 * c + 2 * k], z1 = z[32 * c + 2 * k + 1];
+                mx = fmax3(mx, z0, z1);
+                const float2 x = ffma2(make_float2(z0, z1), mul2, neg);
+                const float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                sum = fadd2(sum, w);
+                hi[k] = pack2<Tr::BF16>(w.x, w.y);
+                if constexpr (kSplit) {
+                  const float2 q = unpack2<Tr::BF16>(hi[k]);
+                  lo[k] = pack2<Tr::BF16>(w.x - q.x, w.y - q.y);
+                }
+              }
+              tmem_st16(ts + 16 * c, hi);
+              if constexpr (kSplit) tmem_st16(ts + 64 + 16 * c, lo);
+            }
+            lt = sum.x + sum.y;
+            return mx * mul;
+          };
+          auto weights = [&](float ms) { return p.split_p ? weights_as(std::true_type{}, ms) : weights_as(std::false_type{}, ms); };
+          // Against the maximum so far first: after a row's first tiles it seldom moves by more than kSlack, and neither the
+          // exponentials nor the maximum of this tile wait for the other.
+          float mx;
+          bool raise;
+          if (j == j0) {
+            float x = fmaxf(z[0], z[1]);
+#pragma unroll
+            for (int c = 2; c < kTile; c += 2) x = fmax3(x, z[c], z[c + 1]);
+            mx = x * mul;
+            raise = true;
+          } else {
+            mx = weights(m == -INFINITY ? 0.f : m - kLift);
+            raise = mx > (m == -INFINITY ? m : m + kSlack);
           }
-          const float mx = fmaxf(mx0, mx1);
-          const bool raise = valid && mx > (m == -INFINITY ? m : m + kSlack);
-          if (__any_sync(0xffffffffu, raise)) {
-            const float mn = raise ? mx : m;
-            const float alpha = raise ? fast_exp2(m - mn) : 1.f;   // nothing seen yet: 2^-inf = 0
+          if (__any_sync(0xffffffffu, raise && valid)) {
+            const float mn = raise ? fmaxf(m, mx) : m;
+            const float alpha = raise && mn != -INFINITY ? fast_exp2(m - mn) : 1.f;   // nothing seen before: 2^-inf = 0
             m = mn;
             l *= alpha;
             if (j != j0) {
@@ -771,29 +833,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 for (int k = 0; k < 16; ++k) o[k] *= alpha;
                 tmem_st16(to + c, reinterpret_cast<const uint32_t*>(o));
               }
-              tmem_wait_st();
             }
+            weights(m == -INFINITY ? 0.f : m - kLift);
           }
-          const float ms = m == -INFINITY ? 0.f : m - kLift;
-          float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float p0 = fast_exp2(z[32 * c + 2 * k] - ms), p1 = fast_exp2(z[32 * c + 2 * k + 1] - ms);
-              l0 += p0;
-              l1 += p1;
-              hi[k] = pack2<Tr::BF16>(p0, p1);
-              if (p.split_p) {
-                const float2 q = unpack2<Tr::BF16>(hi[k]);
-                lo[k] = pack2<Tr::BF16>(p0 - q.x, p1 - q.y);
-              }
-            }
-            tmem_st16(ts + 16 * c, hi);
-            if (p.split_p) tmem_st16(ts + 64 + 16 * c, lo);
-          }
-          l += l0 + l1;
+          l += lt;
           tmem_wait_st();
         }
         tc_fence_before();
