@@ -41,7 +41,7 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
   const int64_t rows = static_cast<int64_t>(max_q_len) * group;
   const bool q8 = kv_dtype == PA_FP8_E4M3 || kv_dtype == PA_INT8;
   pl->ctas = sms;
-  pl->paired = rows > kTile ? 1 : 0;
+  pl->paired = rows > stream_rows(group) ? 1 : 0;
   pl->kind = rows <= kFewRows ? Plan::kFew : (q8 ? Plan::kRows : Plan::kTensor);
   size_t records = 0, pending = 0;
   pl->num_counters = 0;
@@ -142,6 +142,21 @@ bool encode_tile_map(CUtensorMap* map, const void* cache, int64_t rows, int head
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 4-D view of the query rows: {64 elements, heads, tokens, 128-byte halves of a row}; one box = 128 / group tokens by the
+// group's heads, landing as [half][token, head][128 bytes], swizzled by row; zero past the last token.
+bool encode_query_map(CUtensorMap* map, const AttendParams& a) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint32_t halves = static_cast<cuuint32_t>(a.head_dim / 64);
+  cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(a.num_heads), static_cast<cuuint64_t>(a.num_tokens), halves};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.head_dim) * 2, static_cast<cuuint64_t>(a.q_stride) * 2, 128};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.group), static_cast<cuuint32_t>(kTile / a.group), halves};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(a.q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename KVT, int D>
 cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream) {
   using Tr = TcTraits<KVT, D>;
@@ -154,10 +169,11 @@ cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaSt
   p.slots = pl.slots;
   p.counters = reinterpret_cast<int*>(ws);
   p.records = reinterpret_cast<float*>(ws + pl.records);
-  CUtensorMap tk, tv;
+  CUtensorMap tk, tv, tq;
   const int64_t rows = a.num_blocks * a.num_kv_heads * a.block_size;
   const int box = a.block_size < kTile ? a.block_size : kTile;
-  if (!encode_tile_map(&tk, a.k_cache, rows, D, box) || !encode_tile_map(&tv, a.v_cache, rows, D, box))
+  if (!encode_tile_map(&tk, a.k_cache, rows, D, box) || !encode_tile_map(&tv, a.v_cache, rows, D, box) ||
+      !encode_query_map(&tq, a))
     return cudaErrorInvalidValue;
   auto kern = attend_tc_kernel<KVT, D>;
   const size_t smem = Tr::smem_bytes(a.num_seqs);
@@ -173,7 +189,7 @@ cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaSt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kern, tk, tv, p);
+  e = cudaLaunchKernelEx(&cfg, kern, tk, tv, tq, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -9,11 +9,11 @@
 // float32), so O is rarely rescaled.
 //
 // Layout on the SM.  One persistent CTA per SM, 12 warps:
-//   warp 0     TMA producer: K and V tiles of 128 positions, one box per cache
-//              block, into rings of stages
+//   warps 0, 3 TMA producers of the K and of the V tiles of 128 positions, one
+//              box per cache block, into rings of stages
 //   warp 1     issues every tcgen05.mma and owns the TMEM (512 columns: S0, S1,
 //              O0, O1 of 128 lanes x 128 columns; the weights P overwrite S)
-//   warps 2-3  bring the query rows of streams 0 and 1 into shared memory
+//   warp 2     brings the query rows of both streams into shared memory
 //   warps 4-7, 8-11   softmax of streams 0 and 1, one row per thread: the row
 //              maximum and sum need no exchange between threads
 // Two streams alternate, so the tensor cores compute for one while the other's
@@ -79,12 +79,13 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
   return p != 0;
 }
-// Operand descriptors are passed as their low words: the high word is the same for all.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
+// Operand descriptors are passed as their two words: the high word holds no address and is a constant.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                          bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
       : "memory");
 }
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
@@ -139,6 +140,35 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
       : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
   return d;
 }
+// 32 consecutive outputs from element i (a multiple of 32) of one row by one thread: whole 32-byte sectors (`wide`: the
+// buffer is 32-byte aligned), or 16 bytes at a time.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+__device__ __forceinline__ void store_row32(void* out, int dtype, int64_t i, const float* v, bool wide) {
+  if (dtype == PA_F32) {
+#pragma unroll
+    for (int k = 0; k < 32; k += 8) store32(static_cast<float*>(out) + i + k, reinterpret_cast<const uint32_t*>(v + k), wide);
+  } else {
+    uint32_t w[16];
+    if (dtype == PA_BF16) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) w[k] = pack2<true>(v[2 * k], v[2 * k + 1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) w[k] = pack2<false>(v[2 * k], v[2 * k + 1]);
+    }
+    store32(static_cast<uint16_t*>(out) + i, w, wide);
+    store32(static_cast<uint16_t*>(out) + i + 16, w + 8, wide);
+  }
+}
 template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -180,6 +210,9 @@ struct TcParams {
   int* counters;     // arrivals: paired: by the segment's first CTA; alternating: by s * H_kv + kvh
   float* records;
 };
+
+// Rows of one stream's tile: whole queries, as one TMA box of 128 / G queries by G heads brings them.
+__host__ __device__ __forceinline__ int stream_rows(int group) { return kTile / group * group; }
 
 // Position tiles [lo, hi) of row tile m of a sequence.
 struct TileRange {
@@ -234,7 +267,7 @@ struct WarpFrag {
 
 __device__ __forceinline__ bool advance_frag(FragIter& it, Frag& f, const int* prefix, const TcParams& p) {
   const AttendParams& a = p.a;
-  const int rpt = p.paired ? 2 * kTile : kTile;
+  const int rpt = stream_rows(a.group) * (p.paired ? 2 : 1);
   while (it.u < it.u1) {
     while (prefix[it.s + 1] <= it.u) ++it.s;  // last sequence starting at or before u (u < U: one exists)
     const int per = (prefix[it.s + 1] - prefix[it.s]) / a.num_kv_heads;
@@ -337,6 +370,7 @@ struct TcTraits {
 template <typename KVT, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                 const __grid_constant__ CUtensorMap tmap_q,
                  const __grid_constant__ TcParams p) {
   using Tr = TcTraits<KVT, D>;
   constexpr int NST = Tr::NST;
@@ -360,6 +394,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   if (threadIdx.x == 0) {
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
+    prefetch_tensormap(&tmap_q);
     for (int i = 0; i < NST; ++i) {
       mbar_init(bar(Tr::KF + i), 1);
       mbar_init(bar(Tr::KE + i), 1);
@@ -381,7 +416,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
 
   // ---- cost positions before each sequence (every CTA computes the same)
   {
-    const int rpt = p.paired ? 2 * kTile : kTile;
+    const int rpt = stream_rows(a.group) * (p.paired ? 2 : 1);
     int carry = 0;
     constexpr int NW = kTcThreads / 32;
     int* const wsum = misc + 8;
@@ -471,49 +506,48 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   // The softmax threads hold a row's 128 scores each: registers move to their warps (88 * 128 + 208 * 256 = 168 * 384).
   if (warp < 4) {
   regs_dec<88>();
-  if (warp == 0) {
-    // ================================================================= TMA producer
+  if (warp == 0 || warp == 3) {
+    // ================================================================= TMA producers: K (warp 0), V (warp 3)
+    const bool is_v = warp == 3;
     const int BR = min(a.block_size, kTile);            // rows per box
     const int nbox = kTile / BR;
     const uint32_t box_bytes = static_cast<uint32_t>(BR / 8) * Tr::GROUP;
+    const uint32_t ring = base + (is_v ? Tr::OFF_V : Tr::OFF_K);
+    const int FULL = is_v ? Tr::VF : Tr::KF, EMPTY = is_v ? Tr::VE : Tr::KE;
     int kt = 0;  // tiles issued
-    while (next_frag(wf, prefix, p)) {
+    bool ok = true;
+    while (ok && next_frag(wf, prefix, p)) {
       const int nblk = (f.v.T + a.block_size - 1) >> a.block_shift;
       const int blk_lo = f.lo >> a.block_shift;
+      const int t1 = f.t1, kvh = f.kvh;
       const int32_t* table = a.block_tables + static_cast<int64_t>(f.s) * a.max_blocks_per_seq;
-      bool ok = true;
-      for (int j = f.t0; j < f.t1 && ok; ++j, ++kt) {
+      // this lane's block of tile j (its table entry), or -1
+      auto entry = [&](int j) -> int {
+        const int blk = ((j * kTile) >> a.block_shift) + (nbox > 1 ? lane : 0);
+        if (lane >= nbox || blk < blk_lo || blk >= nblk) return -1;
+        const int pb = __ldg(table + blk);
+        if (pb >= 0 && pb < a.num_blocks) return pb;
+        raise_error(a.err, PA_DEVERR_BLOCK_ID);
+        return 0;
+      };
+      int next = entry(f.t0);
+      for (int j = f.t0; j < t1; ++j, ++kt) {
         const int st = kt % NST;
         const uint32_t ph = static_cast<uint32_t>(kt / NST) & 1u;
-        const int blk = ((j * kTile) >> a.block_shift) + (nbox > 1 ? lane : 0);
-        const bool mine = lane < nbox && blk >= blk_lo && blk < nblk;
-        int pb = 0;
-        if (mine) {
-          pb = __ldg(table + blk);
-          if (pb < 0 || pb >= a.num_blocks) {
-            raise_error(a.err, PA_DEVERR_BLOCK_ID);
-            pb = 0;
-          }
+        const int pb = next;
+        const uint32_t bytes = box_bytes * static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, pb >= 0)));
+        if (!__all_sync(0xffffffffu, wait(EMPTY + st, ph ^ 1u))) {
+          ok = false;
+          break;
         }
+        if (lane == 0) mbar_arrive_expect_tx(bar(FULL + st), bytes);
+        __syncwarp();
         const int row = nbox > 1 ? 0 : ((j * kTile) & (a.block_size - 1));
-        const int z = (pb * a.num_kv_heads + f.kvh) * (a.block_size >> 3) + (row >> 3);
-        const uint32_t bytes = box_bytes * static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine)));
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          const int full = (which ? Tr::VF : Tr::KF) + st, empty = (which ? Tr::VE : Tr::KE) + st;
-          if (!wait(empty, ph ^ 1u)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
-          __syncwarp();
-          if (mine)
-            tma_load_4d(base + (which ? Tr::OFF_V : Tr::OFF_K) + st * Tr::TILE_BYTES + lane * box_bytes,
-                        which ? &tmap_v : &tmap_k, 0, 0, 0, z, bar(full));
-        }
-        ok = __all_sync(0xffffffffu, ok);
+        if (pb >= 0)
+          tma_load_4d(ring + st * Tr::TILE_BYTES + lane * box_bytes, is_v ? &tmap_v : &tmap_k, 0, 0, 0,
+                      (pb * a.num_kv_heads + kvh) * (a.block_size >> 3) + (row >> 3), bar(FULL + st));
+        if (j + 1 < t1) next = entry(j + 1);  // read while the next stage is waited for
       }
-      if (!ok) break;
     }
     // nothing of ours, and no arrival of the tensor cores, may land after the CTA has left: wait until each stage's
     // last tile has been used (or, after a wait that ran out, has at least arrived)
@@ -521,15 +555,15 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int n = kt / NST + (i < kt % NST ? 1 : 0);
       if (n > 0) {
         const uint32_t ph = static_cast<uint32_t>(n - 1) & 1u;
-        if (!wait(Tr::KE + i, ph)) wait(Tr::KF + i, ph);
-        if (!wait(Tr::VE + i, ph)) wait(Tr::VF + i, ph);
+        if (!wait(EMPTY + i, ph)) wait(FULL + i, ph);
       }
     }
   } else if (warp == 1) {
     // ================================================================= MMA issuer
     constexpr uint32_t kIdQK = mma_idesc(Tr::BF16, false, kTile);
     constexpr uint32_t kIdPV = mma_idesc(Tr::BF16, true, D);
-    constexpr uint32_t kDescHi = desc_hi(Tr::GROUP);
+    constexpr uint32_t kDescHi = desc_hi(Tr::GROUP), kQDescHi = desc_hi(1024);
+    const uint32_t q_half = static_cast<uint32_t>(stream_rows(a.group)) * 128;  // the query tile is [half][row][128 bytes]
     WarpFrag* const wq = wf + 11;  // fragments whose S products are next
     const Frag& fq = wq->f;
     bool have_q = next_frag(wq, prefix, p);
@@ -552,8 +586,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         const uint32_t qa = desc_lo(base + Tr::OFF_Q + t * Tr::TILE_BYTES), kb = desc_lo(base + Tr::OFF_K + st * Tr::TILE_BYTES);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          const uint32_t o = ((s >> 2) * 1024 + (s & 3) * 32) >> 4;
-          tc_mma_ss(tmem + t * 128, qa + o, kb + o, kDescHi, kIdQK, s > 0);
+          const uint32_t oq = ((s >> 2) * q_half + (s & 3) * 32) >> 4, ok = ((s >> 2) * 1024 + (s & 3) * 32) >> 4;
+          tc_mma_ss(tmem + t * 128, qa + oq, kQDescHi, kb + ok, kDescHi, kIdQK, s > 0);
         }
         tc_commit(bar(Tr::SF + t));
         if (last_use) tc_commit(bar(Tr::KE + st));
@@ -622,47 +656,34 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       }
     }
   } else {
-    // ================================================================= query rows of one stream
-    const int t = warp - 2;
-    int uses = 0, parity = 0;
-    constexpr int CH = D / 8;  // 16-byte chunks of a row
-    while (next_frag(wf, prefix, p)) {
+    // ================================================================= query rows of both streams
+    // (rows past the sequence's last are another sequence's, or zero past the last token: their results are not stored)
+    int uses[2] = {0, 0}, parity = 0;
+    const int per_box = kTile / a.group;
+    const uint32_t bytes = static_cast<uint32_t>(per_box * a.group) * D * 2;
+    bool ok = true;
+    while (ok && next_frag(wf, prefix, p)) {
       const int n = f.t1 - f.t0;
-      const bool used = p.paired || n - (t ^ parity) > 0;
-      if (!p.paired) parity ^= n & 1;
-      if (!used) continue;
-      if (uses > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses - 1) & 1u)) break;
-      ++uses;
-      const int row0 = p.paired ? f.m * 2 * kTile + t * kTile : 0;
-      const int R = f.v.L * a.group;
-      const int rows = min(kTile, (max(0, min(kTile, R - row0)) + 31) & ~31);  // whole warps of rows; the rest is not read back
-      for (int x0 = 0; x0 < rows * CH; x0 += 32 * 8) {
-        uint4 w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int x = x0 + 32 * k + lane;
-          const int r = x / CH, c = x % CH;
-          w[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (row0 + r < R && x < rows * CH) {
-            const int i = (row0 + r) / a.group, g = (row0 + r) - i * a.group;
-            w[k] = __ldg(reinterpret_cast<const uint4*>(
-                static_cast<const uint8_t*>(a.q) +
-                ((static_cast<int64_t>(f.v.row0) + i) * a.q_stride + static_cast<int64_t>(f.kvh * a.group + g) * D + c * 8) * 2));
-          }
+      for (int e = 0; ok && e < 2; ++e) {
+        const int t = p.paired ? e : e ^ parity;  // in the order in which the streams need them
+        if (!p.paired && n <= e) continue;
+        if (uses[t] > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses[t] - 1) & 1u)) {
+          ok = false;
+          break;
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int x = x0 + 32 * k + lane;
-          const int r = x / CH, c = x % CH;
-          if (x < rows * CH)
-            *reinterpret_cast<uint4*>(sm + Tr::OFF_Q + t * Tr::TILE_BYTES + (r >> 3) * Tr::GROUP + (c >> 3) * 1024 +
-                                      (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[k];
+        ++uses[t];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(Tr::QF + t), bytes);
+          tma_load_4d(base + Tr::OFF_Q + t * Tr::TILE_BYTES, &tmap_q, 0, f.kvh * a.group,
+                      f.v.row0 + (p.paired ? (f.m * 2 + t) * per_box : 0), 0, bar(Tr::QF + t));
         }
+        __syncwarp();
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Tr::QF + t));
+      if (!p.paired) parity ^= n & 1;
     }
+    for (int t = 0; t < 2; ++t)
+      if (uses[t] > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses[t] - 1) & 1u))
+        wait(Tr::QF + t, static_cast<uint32_t>(uses[t] - 1) & 1u);
   }
   } else {
     regs_inc<208>();
@@ -702,11 +723,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int j0 = f.t0 + (p.paired ? 0 : e);
       if (!p.paired) parity ^= n & 1;
       if (j0 >= f.t1) continue;
-      const int row0 = p.paired ? f.m * 2 * kTile + t * kTile : 0;
-      const int R = f.v.L * a.group;
+      const int rps = stream_rows(a.group);
+      const int row0 = p.paired ? (f.m * 2 + t) * rps : 0;
+      const int rows = min(rps, f.v.L * a.group - row0);  // of this stream (none: the segment's last rows are the other's)
       const int r = row0 + wq * 32 + lane;
-      const bool valid = r < R;
-      const bool warp_on = row0 + wq * 32 < R;
+      const bool valid = wq * 32 + lane < rows;
+      const bool warp_on = wq * 32 < rows;
       const int qi = valid ? r / a.group : 0;
       const int h = f.kvh * a.group + (valid ? r - qi * a.group : 0);
       RowBounds rb = row_bounds(a, f.v, f.prefix, qi);
@@ -855,6 +877,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           const float inv = l > 0.f ? 1.f / l : 0.f;
           bool bad = l != l;
           const int64_t o0 = ((static_cast<int64_t>(f.v.row0) + qi) * a.num_heads + h) * D;
+          const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
 #pragma unroll
           for (int c = 0; c < D; c += 32) {
             float o[32];
@@ -862,11 +885,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             tmem_wait_ld();
             if (valid) {
 #pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                float4 w = make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
-                bad |= !(fabsf(w.x) < INFINITY) || !(fabsf(w.y) < INFINITY) || !(fabsf(w.z) < INFINITY) || !(fabsf(w.w) < INFINITY);
-                store_out4(a.out, a.out_dtype, o0 + c + k, w, true);
+              for (int k = 0; k < 32; ++k) {
+                o[k] *= inv;
+                bad |= !(fabsf(o[k]) < INFINITY);
               }
+              store_row32(a.out, a.out_dtype, o0 + c, o, wide);
             }
           }
           float2 stats = make_float2(me, l);
@@ -919,8 +942,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const bool last = *arrived == total - 1;
       if (last) {
         __threadfence();
-        const int nrows = min(kTile, R - row0);
-        for (int lr = wq; lr < nrows; lr += 4) {
+        for (int lr = wq; lr < rows; lr += 4) {
           float M = -INFINITY;
           for (int c = c0; c <= c1; ++c) {
             const int k = tiles_in(c, U, nw, f.seg_start, f.seg_tiles);

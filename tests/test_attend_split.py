@@ -28,6 +28,7 @@ PRELUDE = r"""
 #include <vector>
 using std::max; using std::min;
 #define __device__
+#define __host__
 #define __forceinline__ inline
 template <typename T> T __ldg(const T* p) { return *p; }
 struct AttendParams {
@@ -65,8 +66,8 @@ int main() {
     const uint64_t word = 0;
     if (trial % 5 == 2) a.prefix_lens = pre.data();
     if (trial % 5 == 3) a.tree_mask = &word;
-    p.paired = static_cast<long long>(a.max_q_len) * a.group > kTile;
-    const int rpt = p.paired ? 2 * kTile : kTile;
+    p.paired = static_cast<long long>(a.max_q_len) * a.group > stream_rows(a.group);
+    const int rpt = stream_rows(a.group) * (p.paired ? 2 : 1);
     std::vector<int> prefix(S + 1, 0);
     std::map<std::tuple<int, int, int>, std::set<int>> todo;   // tiles of every segment
     for (int s = 0; s < S; ++s) {
@@ -146,7 +147,7 @@ def test_work_split(tmp_path):
         tc = f.read()
     code = PRELUDE.replace("FRAG_COST", re.search(r"kFragCost = (\d+);", tc).group(1))
     code += _between(common, "struct SeqView", "// softcap * tanh")
-    code += _between(tc, "struct TileRange", "// A warp's iterator").replace("struct WarpFrag", "struct Unused")
+    code += _between(tc, "__host__ __device__ __forceinline__ int stream_rows", "// A warp's iterator").replace("struct WarpFrag", "struct Unused")
     code += _between(tc, "__device__ __forceinline__ bool advance_frag", "// The warp's next fragment")
     code += _between(tc, "// CTA whose range holds", "template <typename KVT, int D>")
     code += MAIN
