@@ -53,8 +53,11 @@ class AttendOptions(ctypes.Structure):
                 ("tree_words", ctypes.c_int32), ("mass", ctypes.c_void_p), ("mass_stride_seq", ctypes.c_int64),
                 ("mass_stride_head", ctypes.c_int64), ("pdl", ctypes.c_int32)]
 
-    def __init__(self, **kw):
-        super().__init__(struct_size=ctypes.sizeof(AttendOptions), **kw)
+    def __init__(self, *args, **kw):
+        if args:                                   # every field in order, struct_size first
+            super().__init__(*args)
+        else:
+            super().__init__(struct_size=ctypes.sizeof(AttendOptions), **kw)
 
 
 _SIGNATURES = {

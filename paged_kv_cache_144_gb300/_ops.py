@@ -14,77 +14,99 @@ from . import _lib
 from ._lib import (PA_ERR_SHAPE, SIZE_MAX, AttendOptions, CacheWriteOptions, PagedAttnError, _check, _ptr, dtype_code,
                    load)
 
-_torch = None
+_OPT_SIZE = ctypes.sizeof(AttendOptions)
+
+_torch = _CODES = _raw_stream = _get_device = None
+_I32 = _I64 = _F32 = None
 
 
 def _t():
-    global _torch
+    """torch and the few names of it that a call looks up (the per-step path), bound once."""
+    global _torch, _CODES, _raw_stream, _get_device, _I32, _I64, _F32
     if _torch is None:
         import torch
+        _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+        _raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        dtype_code(torch.empty(0))
+        _CODES = _lib._DTYPE_CODES
         _torch = torch
     return _torch
 
 
-def _device_of(first, named, stream):
-    """The one device of all tensors; a (device guard or None, stream handle) pair for the call."""
-    torch = _t()
-    if not first.is_cuda:
+def _code(t):
+    c = _CODES.get(t.dtype)
+    if c is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return c
+
+
+def _on_one_device(first, *rest):
+    """The index of the CUDA device that holds all these tensors (None: an argument left out)."""
+    d = first.get_device()
+    if d < 0:
         raise ValueError("q/k_cache must be a CUDA tensor")
-    dev = first.device
-    for name, t in named:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, the device of the call's other tensors")
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream must be on {dev}")
+    for t in rest:
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"every tensor of a call must be on cuda:{d}, one is on {t.device}")
+    return d
+
+
+def _issue(fn, dev, stream, *args):
+    """Calls fn(*args, stream handle) with `dev` current."""
+    if stream is None:
+        handle = _raw_stream(dev)
+    elif stream.device_index == dev:
         handle = stream.cuda_stream
     else:
-        handle = torch.cuda.current_stream(dev).cuda_stream
-    guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-    return guard, handle
-
-
-def _call(fn, guard, *args):
-    if guard is None:
-        _check(fn.__name__, fn(*args))
+        raise ValueError(f"stream must be on cuda:{dev}")
+    if _get_device() == dev:
+        st = fn(*args, handle)
     else:
-        with guard:
-            _check(fn.__name__, fn(*args))
+        with _torch.cuda.device(dev):
+            st = fn(*args, handle)
+    if st:
+        _check(fn.__name__, st)
 
 
-def _need(name, t, dtype, *shape):
-    """A contiguous tensor of this dtype of exactly these sizes (None: any)."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _need(name, t, dtype, shape):
+    """A contiguous tensor of this dtype and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)} with strides "
+                         f"{t.stride()}")
 
 
-def _rows(name, t, heads, dim):
-    """[N, heads, dim] with contiguous rows; returns the stride between tokens."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must have shape [N, {heads}, {dim}], not {tuple(t.shape)}")
-    if t.stride(2) != 1 or t.stride(1) != dim:
-        raise ValueError(f"{name} rows must be contiguous per token")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dim)
+def _table(name, t, rows, dtype):
+    """A contiguous [rows, any] tensor; returns its width."""
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 2 or shape[0] != rows or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} [{rows}, any], not {t.dtype} {tuple(shape)}")
+    return shape[1]
 
 
-def _cache(k_cache, v_cache, num_kv_heads, block_size):
-    if (k_cache.dim() != 4 or k_cache.shape[1] != num_kv_heads or k_cache.shape[2] != block_size or
-            not k_cache.is_contiguous()):
-        raise ValueError(f"k_cache must be contiguous [blocks, {num_kv_heads}, {block_size}, d], not "
-                         f"{tuple(k_cache.shape)}")
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or not v_cache.is_contiguous():
+def _row_stride(name, t, tokens, heads, dim):
+    """[tokens, heads, dim] with contiguous rows; returns the stride between tokens."""
+    a, b, c = t.stride()
+    if t.shape != (tokens, heads, dim) or c != 1 or (b != dim and heads > 1):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}] with contiguous rows per token, not "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    return a if tokens > 1 else max(a, heads * dim)
+
+
+def _cache(k_cache, v_cache, block_size):
+    """(blocks, KV heads, head size) of the two pools."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[2] != block_size or not k_cache.is_contiguous():
+        raise ValueError(f"k_cache must be contiguous [blocks, H_kv, {block_size}, d], not {tuple(shape)}")
+    if v_cache.shape != shape or v_cache.dtype is not k_cache.dtype or not v_cache.is_contiguous():
         raise ValueError("v_cache must be contiguous, of the shape and type of k_cache")
+    return shape[0], shape[1], shape[3]
 
 
-def _heads_params(num_kv_heads, **named):
-    torch = _t()
-    for name, t in named.items():
-        if t is not None:
-            _need(name, t, torch.int32 if "zero" in name else torch.float32, num_kv_heads)
+def _heads_params(num_kv_heads, scales, zero_points):
+    for dtype, named in ((_F32, scales), (_I32, zero_points)):
+        for t in named:
+            if t is not None:
+                _need("a per-KV-head scale" if dtype is _F32 else "a zero point", t, dtype, (num_kv_heads,))
 
 
 def rope_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, original_positions=None, low_factor=1.0,
@@ -127,36 +149,36 @@ def rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq,
     The turned q goes to q_out (default: q itself), the turned k and v into their slots; tokens with a negative slot
     are padding and left alone.  Returns q_out.
     """
-    torch = _t()
+    _torch or _t()
     if q_out is None:
         q_out = q
-    guard, handle = _device_of(q, (("k", k), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache),
-                                   ("positions", positions), ("slot_mapping", slot_mapping), ("inv_freq", inv_freq),
-                                   ("q_out", q_out), ("k_inv_scale", k_inv_scale), ("v_inv_scale", v_inv_scale),
-                                   ("k_zero_point", k_zero_point), ("v_zero_point", v_zero_point)), stream)
+    dev = _on_one_device(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, q_out, k_inv_scale, v_inv_scale,
+                         k_zero_point, v_zero_point)
     N, Hq, D = q.shape
-    Hkv = k.shape[1]
-    _cache(k_cache, v_cache, Hkv, block_size)
-    if k_cache.shape[3] != D or k.shape[0] != N or v.shape[0] != N or q_out.shape[0] != N:
-        raise ValueError("q, k, v, q_out and the caches must agree in tokens and head size")
-    if k.dtype != q.dtype or v.dtype != q.dtype or q_out.dtype != q.dtype:
+    blocks, Hkv, dim = _cache(k_cache, v_cache, block_size)
+    if dim != D:
+        raise ValueError("q and the caches must have one head size")
+    dt = q.dtype
+    if k.dtype is not dt or v.dtype is not dt or q_out.dtype is not dt:
         raise ValueError("q, k, v and q_out must have one type")
-    qs, qos = _rows("q", q, Hq, D), _rows("q_out", q_out, Hq, D)
-    ks, vs = _rows("k", k, Hkv, D), _rows("v", v, Hkv, D)
-    _need("positions", positions, torch.int64, N)
-    _need("slot_mapping", slot_mapping, torch.int64, N)
-    _need("inv_freq", inv_freq, torch.float32, None)
-    _heads_params(Hkv, k_inv_scale=k_inv_scale, v_inv_scale=v_inv_scale, k_zero_point=k_zero_point,
-                  v_zero_point=v_zero_point)
-    opt = None
+    qs = _row_stride("q", q, N, Hq, D)
+    qos = qs if q_out is q else _row_stride("q_out", q_out, N, Hq, D)
+    ks, vs = _row_stride("k", k, N, Hkv, D), _row_stride("v", v, N, Hkv, D)
+    tokens = (N,)
+    _need("positions", positions, _I64, tokens)
+    _need("slot_mapping", slot_mapping, _I64, tokens)
+    _need("inv_freq", inv_freq, _F32, inv_freq.shape[:1])
+    opt = ki = vi = None
+    if k_inv_scale is not None or v_inv_scale is not None:
+        _heads_params(Hkv, (k_inv_scale, v_inv_scale), (k_zero_point, v_zero_point))
+        ki, vi = _ptr(k_inv_scale), _ptr(v_inv_scale)
     if k_zero_point is not None or v_zero_point is not None or pdl:
         opt = ctypes.byref(CacheWriteOptions(k_zero_point=_ptr(k_zero_point), v_zero_point=_ptr(v_zero_point),
                                              pdl=1 if pdl else 0))
-    _call(load().pa_rope_and_cache, guard, q_out.data_ptr(), qos, q.data_ptr(), qs, Hq, k.data_ptr(), v.data_ptr(),
-          dtype_code(q), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), dtype_code(k_cache), k_cache.shape[0],
-          positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0],
-          1 if interleaved else 0, float(rope_scale), N, Hkv, D, int(block_size), _ptr(k_inv_scale),
-          _ptr(v_inv_scale), opt, handle)
+    _issue(load().pa_rope_and_cache, dev, stream, q_out.data_ptr(), qos, q.data_ptr(), qs, Hq, k.data_ptr(), v.data_ptr(),
+           _code(q), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), _code(k_cache), blocks, positions.data_ptr(),
+           slot_mapping.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, rope_scale, N,
+           Hkv, D, int(block_size), ki, vi, opt)
     return q_out
 
 
@@ -173,58 +195,58 @@ def attend_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_si
 def _attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_len, num_kv_heads, scale, block_size,
             workspace, k_scale, v_scale, k_zero_point, v_zero_point, softcap, slopes, window, prefix_lens, tree_mask,
             mass, pdl, stream):
-    torch = _t()
-    guard, handle = _device_of(q, (("out", out), ("k_cache", k_cache), ("v_cache", v_cache),
-                                   ("block_tables", block_tables), ("seq_lens", seq_lens), ("q_starts", q_starts),
-                                   ("workspace", workspace), ("k_scale", k_scale), ("v_scale", v_scale),
-                                   ("k_zero_point", k_zero_point), ("v_zero_point", v_zero_point), ("slopes", slopes),
-                                   ("prefix_lens", prefix_lens), ("tree_mask", tree_mask), ("mass", mass)), stream)
+    _torch or _t()
+    dev = _on_one_device(q, out, k_cache, v_cache, block_tables, seq_lens, q_starts, workspace, k_scale, v_scale,
+                         k_zero_point, v_zero_point, slopes, prefix_lens, tree_mask, mass)
     N, Hq, D = q.shape
-    qs = _rows("q", q, Hq, D)
-    _cache(k_cache, v_cache, num_kv_heads, block_size)
-    if k_cache.shape[3] != D:
-        raise ValueError("q and the caches must have one head size")
+    qs = _row_stride("q", q, N, Hq, D)
+    blocks, Hkv, dim = _cache(k_cache, v_cache, block_size)
+    if dim != D or Hkv != num_kv_heads:
+        raise ValueError("the caches must have q's head size and num_kv_heads heads")
     if out.shape != q.shape or not out.is_contiguous():
         raise ValueError(f"out must be contiguous of shape {tuple(q.shape)}")
     S = seq_lens.shape[0]
-    _need("block_tables", block_tables, torch.int32, S, None)
-    _need("seq_lens", seq_lens, torch.int32, S)
+    width = _table("block_tables", block_tables, S, _I32)
+    _need("seq_lens", seq_lens, _I32, (S,))
+    starts = None
     if q_starts is not None:
-        _need("q_starts", q_starts, torch.int32, S + 1)
-    _heads_params(num_kv_heads, k_scale=k_scale, v_scale=v_scale, k_zero_point=k_zero_point, v_zero_point=v_zero_point)
+        _need("q_starts", q_starts, _I32, (S + 1,))
+        starts = q_starts.data_ptr()
+    if k_scale is not None or v_scale is not None:
+        _heads_params(Hkv, (k_scale, v_scale), (k_zero_point, v_zero_point))
     ws, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    words = mseq = mhead = 0
-    if slopes is not None:
-        _need("slopes", slopes, torch.float32, Hq)
-    if prefix_lens is not None:
-        _need("prefix_lens", prefix_lens, torch.int32, S)
-    if tree_mask is not None:
-        if tree_mask.dtype not in (torch.int64, getattr(torch, "uint64", torch.int64)):
-            raise ValueError("tree_mask must be int64 (or uint64) words")
-        _need("tree_mask", tree_mask, tree_mask.dtype, N, None)
-        words = tree_mask.shape[1]
-    if mass is not None:
-        mseq, mhead = _mass_strides("mass", mass, S, num_kv_heads)
-        if mass.shape[2] < block_tables.shape[1] * block_size:
-            raise ValueError("mass rows must hold block_tables.shape[1] * block_size positions")
-    opt = AttendOptions(k_zero_point=_ptr(k_zero_point), v_zero_point=_ptr(v_zero_point), softcap=float(softcap),
-                        slopes=_ptr(slopes), window=int(window), prefix_lens=_ptr(prefix_lens),
-                        tree_mask=_ptr(tree_mask), tree_words=words, mass=_ptr(mass), mass_stride_seq=mseq,
-                        mass_stride_head=mhead, pdl=1 if pdl else 0)
-    _call(load().pa_attend, guard, out.data_ptr(), dtype_code(out), q.data_ptr(), dtype_code(q), qs,
-          k_cache.data_ptr(), v_cache.data_ptr(), dtype_code(k_cache), k_cache.shape[0], _ptr(k_scale), _ptr(v_scale),
-          block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), _ptr(q_starts), int(max_q_len), N, S,
-          Hq, int(num_kv_heads), D, float(scale), int(block_size), ws, wb, ctypes.byref(opt), handle)
+    opt = None
+    if softcap or window or pdl or k_zero_point is not None or v_zero_point is not None or slopes is not None or \
+            prefix_lens is not None or tree_mask is not None or mass is not None:
+        words = mseq = mhead = 0
+        if slopes is not None:
+            _need("slopes", slopes, _F32, (Hq,))
+        if prefix_lens is not None:
+            _need("prefix_lens", prefix_lens, _I32, (S,))
+        if tree_mask is not None:
+            if tree_mask.dtype not in (_I64, getattr(_torch, "uint64", _I64)):
+                raise ValueError("tree_mask must be int64 (or uint64) words")
+            words = _table("tree_mask", tree_mask, N, tree_mask.dtype)
+        if mass is not None:
+            mseq, mhead = _mass_strides("mass", mass, S, Hkv)
+            if mass.shape[2] < width * block_size:
+                raise ValueError("mass rows must hold block_tables.shape[1] * block_size positions")
+        opt = ctypes.byref(AttendOptions(_OPT_SIZE, _ptr(k_zero_point), _ptr(v_zero_point), softcap, _ptr(slopes), int(window),
+                                         _ptr(prefix_lens), _ptr(tree_mask), words, _ptr(mass), mseq, mhead,
+                                         1 if pdl else 0))
+    _issue(load().pa_attend, dev, stream, out.data_ptr(), _code(out), q.data_ptr(), _code(q), qs, k_cache.data_ptr(),
+           v_cache.data_ptr(), _code(k_cache), blocks, _ptr(k_scale), _ptr(v_scale), block_tables.data_ptr(), width,
+           seq_lens.data_ptr(), starts, int(max_q_len), N, S, Hq, Hkv, D, scale, int(block_size), ws, wb, opt)
     return out
 
 
 def _mass_strides(name, mass, seqs, heads):
-    if mass.dtype != _t().float32 or mass.dim() != 3 or mass.shape[0] != seqs or mass.shape[1] != heads:
-        raise ValueError(f"{name} must be float32 [{seqs}, {heads}, positions], not {mass.dtype} {tuple(mass.shape)}")
-    if mass.stride(2) != 1 and mass.shape[2] > 1:
-        raise ValueError(f"{name} rows must be contiguous")
-    h = mass.stride(1) if heads > 1 else max(mass.stride(1), mass.shape[2])
-    return (mass.stride(0) if seqs > 1 else max(mass.stride(0), h * heads)), h
+    shape, (a, b, c) = mass.shape, mass.stride()
+    if mass.dtype is not _F32 or len(shape) != 3 or shape[0] != seqs or shape[1] != heads or (c != 1 and shape[2] > 1):
+        raise ValueError(f"{name} must be float32 [{seqs}, {heads}, positions] with contiguous rows, not {mass.dtype} "
+                         f"{tuple(shape)} with strides {mass.stride()}")
+    h = b if heads > 1 else max(b, shape[2])
+    return (a if seqs > 1 else max(a, h * heads)), h
 
 
 def attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_len, num_kv_heads, scale, block_size, *,
@@ -275,22 +297,19 @@ def commit_tree(k_cache, v_cache, block_tables, seq_lens, q_starts, path, path_l
                 stream=None):
     """Move the accepted path's cache rows (nodes path[s, :path_lens[s]]) to the front of each tree's span and write
     the sequences' new lengths (pa_commit_tree).  Returns new_lens."""
-    torch = _t()
-    guard, handle = _device_of(k_cache, (("v_cache", v_cache), ("block_tables", block_tables), ("seq_lens", seq_lens),
-                                         ("q_starts", q_starts), ("path", path), ("path_lens", path_lens),
-                                         ("new_lens", new_lens)), stream)
+    _torch or _t()
+    dev = _on_one_device(k_cache, v_cache, block_tables, seq_lens, q_starts, path, path_lens, new_lens)
+    blocks, Hkv, D = _cache(k_cache, v_cache, block_size)
     S = seq_lens.shape[0]
-    Hkv, D = k_cache.shape[1], k_cache.shape[3]
-    _cache(k_cache, v_cache, Hkv, block_size)
-    _need("block_tables", block_tables, torch.int32, S, None)
-    _need("seq_lens", seq_lens, torch.int32, S)
-    _need("q_starts", q_starts, torch.int32, S + 1)
-    _need("path", path, torch.int32, S, None)
-    _need("path_lens", path_lens, torch.int32, S)
-    _need("new_lens", new_lens, torch.int32, S)
-    _call(load().pa_commit_tree, guard, k_cache.data_ptr(), v_cache.data_ptr(), dtype_code(k_cache), k_cache.shape[0],
-          block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), q_starts.data_ptr(), path.data_ptr(),
-          path_lens.data_ptr(), path.shape[1], new_lens.data_ptr(), S, Hkv, D, int(block_size), handle)
+    seqs = (S,)
+    width, deep = _table("block_tables", block_tables, S, _I32), _table("path", path, S, _I32)
+    _need("seq_lens", seq_lens, _I32, seqs)
+    _need("q_starts", q_starts, _I32, (S + 1,))
+    _need("path_lens", path_lens, _I32, seqs)
+    _need("new_lens", new_lens, _I32, seqs)
+    _issue(load().pa_commit_tree, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), _code(k_cache), blocks,
+           block_tables.data_ptr(), width, seq_lens.data_ptr(), q_starts.data_ptr(), path.data_ptr(),
+           path_lens.data_ptr(), deep, new_lens.data_ptr(), S, Hkv, D, int(block_size))
     return new_lens
 
 
@@ -302,24 +321,20 @@ def evict(k_cache, v_cache, mass, block_tables, seq_lens, dst_tables, kept, mass
     Writes kept int32 / mass_out float32 [S, H_kv, budget] and new_lens int32 [S].  dst_tables must name fresh blocks.
     Returns kept.
     """
-    torch = _t()
-    guard, handle = _device_of(k_cache, (("v_cache", v_cache), ("mass", mass), ("block_tables", block_tables),
-                                         ("seq_lens", seq_lens), ("dst_tables", dst_tables), ("kept", kept),
-                                         ("mass_out", mass_out), ("new_lens", new_lens)), stream)
+    _torch or _t()
+    dev = _on_one_device(k_cache, v_cache, mass, block_tables, seq_lens, dst_tables, kept, mass_out, new_lens)
+    blocks, Hkv, D = _cache(k_cache, v_cache, block_size)
     S = seq_lens.shape[0]
-    Hkv, D = k_cache.shape[1], k_cache.shape[3]
-    _cache(k_cache, v_cache, Hkv, block_size)
-    _need("block_tables", block_tables, torch.int32, S, None)
-    _need("seq_lens", seq_lens, torch.int32, S)
-    _need("dst_tables", dst_tables, torch.int32, S, None)
-    _need("kept", kept, torch.int32, S, Hkv, budget)
-    _need("mass_out", mass_out, torch.float32, S, Hkv, budget)
-    _need("new_lens", new_lens, torch.int32, S)
+    seqs, lists = (S,), (S, Hkv, budget)
+    width, dst_width = _table("block_tables", block_tables, S, _I32), _table("dst_tables", dst_tables, S, _I32)
+    _need("seq_lens", seq_lens, _I32, seqs)
+    _need("kept", kept, _I32, lists)
+    _need("mass_out", mass_out, _F32, lists)
+    _need("new_lens", new_lens, _I32, seqs)
     mseq, mhead = _mass_strides("mass", mass, S, Hkv)
-    if mass.shape[2] < block_tables.shape[1] * block_size:
+    if mass.shape[2] < width * block_size:
         raise ValueError("mass rows must hold block_tables.shape[1] * block_size positions")
-    _call(load().pa_evict, guard, k_cache.data_ptr(), v_cache.data_ptr(), dtype_code(k_cache), k_cache.shape[0],
-          mass.data_ptr(), mseq, mhead, block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
-          dst_tables.data_ptr(), dst_tables.shape[1], kept.data_ptr(), mass_out.data_ptr(), new_lens.data_ptr(), S,
-          Hkv, D, int(block_size), int(budget), int(recent), int(sinks), handle)
+    _issue(load().pa_evict, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), _code(k_cache), blocks, mass.data_ptr(),
+           mseq, mhead, block_tables.data_ptr(), width, seq_lens.data_ptr(), dst_tables.data_ptr(), dst_width,
+           kept.data_ptr(), mass_out.data_ptr(), new_lens.data_ptr(), S, Hkv, D, int(block_size), int(budget), int(recent), int(sinks))
     return kept

@@ -208,21 +208,36 @@ __global__ void __launch_bounds__(kRowWarps * 32) attend_rows_kernel(const Atten
   }
 }
 
-// mass[s][kvh][t] += sum over the group of exp2(score - max) / sum, from the stored scores: one thread per position.
-__global__ void __launch_bounds__(256) attend_add_mass_kernel(const AttendParams p) {
+// mass[s][kvh][t] += sum over the group of exp2(score - max) / sum, from the stored scores: four positions per thread (the
+// score rows are 16-byte aligned; the mass rows need not be).
+constexpr int kMassThreads = 128;
+__global__ void __launch_bounds__(kMassThreads) attend_add_mass_kernel(const AttendParams p) {
+  griddep_wait();
   const int s = blockIdx.z, kvh = blockIdx.y;
   const SeqView v = seq_view(p, s, false);
   if (v.L != 1) return;
   const RowBounds rb = row_bounds(p, v, seq_prefix(p, s, v.T), 0);
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t < rb.lo || t >= rb.hi) return;
-  float sum = 0.f;
+  const int t = (blockIdx.x * kMassThreads + threadIdx.x) * 4;
+  if (t + 4 <= rb.lo || t >= rb.hi) return;
+  const int64_t row0 = static_cast<int64_t>(s) * p.num_heads + kvh * p.group;
+  const float* const sc = p.scores + row0 * p.score_stride + t;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
   for (int g = 0; g < p.group; ++g) {
-    const int64_t row = static_cast<int64_t>(s) * p.num_heads + kvh * p.group + g;
-    const float2 ml = p.row_stats[row];
-    sum += exp2f(p.scores[row * p.score_stride + t] - ml.x) / ml.y;
+    const float2 ml = p.row_stats[row0 + g];
+    const float4 x = *reinterpret_cast<const float4*>(sc + static_cast<int64_t>(g) * p.score_stride);
+    const float inv = __frcp_rn(ml.y);
+    sum.x = fmaf(exp2f(x.x - ml.x), inv, sum.x);
+    sum.y = fmaf(exp2f(x.y - ml.x), inv, sum.y);
+    sum.z = fmaf(exp2f(x.z - ml.x), inv, sum.z);
+    sum.w = fmaf(exp2f(x.w - ml.x), inv, sum.w);
   }
-  p.mass[s * p.mass_stride_seq + kvh * p.mass_stride_head + t] += sum;
+  // (scores outside [lo, hi) were not stored: whatever stands there is not used)
+  float* const mass = p.mass + s * p.mass_stride_seq + kvh * p.mass_stride_head + t;
+  const float add[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (t + k >= rb.lo && t + k < rb.hi) mass[k] += add[k];
 }
 
 template <typename KVT, int D>
@@ -275,8 +290,17 @@ int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaS
   }
   if (e == cudaSuccess && p.mass) {
     const int cap = p.max_blocks_per_seq << p.block_shift;
-    attend_add_mass_kernel<<<dim3((cap + 255) / 256, p.num_kv_heads, p.num_seqs), 256, 0, stream>>>(p);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((cap + 4 * kMassThreads - 1) / (4 * kMassThreads), p.num_kv_heads, p.num_seqs);
+    cfg.blockDim = dim3(kMassThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attend_add_mass_kernel, p);
+    if (e == cudaSuccess) e = cudaGetLastError();
   }
   return cuda_status(e, "pa_attend launch");
 }
