@@ -84,20 +84,21 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const Commi
 
 // ------------------------------------------------------------------ eviction: selection
 //
-// One CTA per (sequence, KV head).  A weight's key is an unsigned integer with
-// the same order (NaN: 0, below minus infinity; minus zero counts as zero).
-// The key of rank `need` among the middle positions is found digit by digit, 8
-// bits a pass, from histograms in shared memory; then each warp takes a
-// contiguous part of the positions, counts what it keeps, and after one scan
-// over the warps writes its kept positions: those above the key, and the first
-// `ties` equal to it.
-//
-// Weights share few leading digits (a handful of exponents), so lanes of one
-// warp would queue at the same counter: every lane has a column of counters of
-// its own, on its own bank.
+// One CTA per (sequence, KV head), each warp a contiguous part of its
+// positions.  A weight's key is an unsigned integer with the same order (NaN:
+// 0, below minus infinity; minus zero counts as zero).  The key of rank `need`
+// among the middle positions is narrowed down 11 bits at a time by a histogram
+// in shared memory; as soon as the keys that share the leading digits fit the
+// CTA, one per thread, its remaining bits follow from one count over the CTA
+// each (and none are needed when all of those are kept).  Then each warp
+// counts what it keeps, and after one scan over the warps writes its kept
+// positions in order: those above the key, and the first `ties` equal to it.
+// Up to 32768 positions the weights are read once and stay in registers; more
+// are read again (from L2) in each pass.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelUnroll = 8;  // weights a thread has in flight
+constexpr int kSelHeld = 32;  // weights a thread holds, or has in flight
+constexpr int kBins = 2048;
 
 __device__ __forceinline__ uint32_t weight_key(float x) {
   if (x != x) return 0u;
@@ -125,137 +126,152 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     }
     return;
   }
+  __shared__ int hist[kBins];
+  __shared__ uint32_t few[kSelThreads];
+  __shared__ int wsum[2][kSelWarps];
+  __shared__ int pick[3], num_few;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lo = a.sinks, hi = T - a.recent;  // the middle positions
   int need = a.budget - a.sinks - a.recent;   // < hi - lo
   const bool any = need > 0;
-  extern __shared__ int hist[];               // [256][32]
-  __shared__ int bin[256];
-  __shared__ int pick[2];
-  uint32_t prefix = 0u, mask = 0u;
-  if (any) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256 * 32; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int t0 = lo + static_cast<int>(threadIdx.x); t0 < hi; t0 += kSelThreads * kSelUnroll) {
-        float x[kSelUnroll];
-#pragma unroll
-        for (int k = 0; k < kSelUnroll; ++k) {
-          const int t = t0 + k * kSelThreads;
-          x[k] = t < hi ? __ldg(mass + t) : 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < kSelUnroll; ++k) {
-          const uint32_t key = weight_key(x[k]);
-          if (t0 + k * kSelThreads < hi && (key & mask) == prefix) atomicAdd(&hist[((key >> shift) & 255u) * 32 + lane], 1);
-        }
-      }
-      __syncthreads();
-      for (int b = warp; b < 256; b += kSelWarps) {  // a bin's 32 columns
-        int c = hist[b * 32 + lane];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-        if (lane == 0) bin[b] = c;
-      }
-      __syncthreads();
-      if (warp == 0) {
-        // lane i holds the bins 255 - 8 i .. 248 - 8 i: the digit is the first, from above, that brings the count to `need`
-        int c[8], sum = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          c[k] = bin[255 - 8 * lane - k];
-          sum += c[k];
-        }
-        int before = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, before, o);
-          if (lane >= o) before += y;
-        }
-        before -= sum;
-        if (before < need && need <= before + sum) {
-          int left = need - before;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (left > 0 && left <= c[k]) {
-              pick[0] = 255 - 8 * lane - k;
-              pick[1] = left;
-            }
-            left -= c[k];
-          }
-        }
-      }
-      __syncthreads();
-      prefix |= static_cast<uint32_t>(pick[0]) << shift;
-      mask |= 255u << shift;
-      need = pick[1];
-    }
-  }
-  const int ties = need;  // how many of the middle positions equal to the key are kept
-  // each warp: positions [w0, w1), a multiple of 32 long
+  // this warp's positions [w0, w1): a multiple of 32, lane l holding w0 + 32 k + l
   const int part = ((T + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int w0 = min(T, warp * part), w1 = min(T, w0 + part);
-  auto classify = [&](int t, float x, bool* equal) -> bool {
+  const bool held = part <= 32 * kSelHeld;
+  float x[kSelHeld];
+  auto fetch = [&](int t0) {
+#pragma unroll
+    for (int k = 0; k < kSelHeld; ++k) {
+      const int t = t0 + 32 * k + lane;
+      x[k] = t < w1 ? __ldg(mass + t) : 0.f;
+    }
+  };
+  if (held) fetch(w0);
+  // body(k, t) over the warp's positions, weights in x[k]
+  auto each = [&](auto body) {
+    for (int t0 = w0; t0 < w1; t0 += 32 * kSelHeld) {
+      if (!held) fetch(t0);
+#pragma unroll
+      for (int k = 0; k < kSelHeld; ++k)
+        if (t0 + 32 * k < w1) body(k, t0 + 32 * k + lane);
+    }
+  };
+  // the key: everything above `key` is kept, and `ties` of those equal to it
+  uint32_t key = 0u;
+  int ties = 0;
+  if (any) {
+    uint32_t prefix = 0u, mask = 0u;
+    int shift = 21;
+    for (int digit = 0; digit < 3; ++digit) {
+      const uint32_t dmask = digit < 2 ? 0x7ffu : 0x3ffu;
+      for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      each([&](int k, int t) {
+        const uint32_t y = weight_key(x[k]);
+        if (t >= lo && t < hi && (y & mask) == prefix) atomicAdd(&hist[(y >> shift) & dmask], 1);
+      });
+      __syncthreads();
+      // thread i holds bins kBins - 1 - 2 i and the one below: the digit is the first from above that brings the count to need
+      {
+        const int b = kBins - 1 - 2 * static_cast<int>(threadIdx.x);
+        const int c0 = hist[b], c1 = hist[b - 1];
+        int upto = c0 + c1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        if (lane == 31) wsum[0][warp] = upto;
+        __syncthreads();
+        int w = lane < warp ? wsum[0][lane] : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+        const int before = w + upto - c0 - c1;
+        if (before < need && need <= before + c0 + c1) {
+          const bool first = need <= before + c0;
+          pick[0] = first ? b : b - 1;
+          pick[1] = need - before - (first ? 0 : c0);  // still to be found in the bin
+          pick[2] = first ? c0 : c1;                   // its size
+        }
+        if (threadIdx.x == 0) num_few = 0;
+        __syncthreads();
+      }
+      prefix |= static_cast<uint32_t>(pick[0]) << shift;
+      mask |= dmask << shift;
+      need = pick[1];
+      const int size = pick[2];
+      if (need == size) {  // all of them: everything from prefix on (need < the middle's count, so prefix > 0 here)
+        key = prefix - 1u;
+        ties = 0;
+        break;
+      }
+      if (digit == 2) {
+        key = prefix;
+        ties = need;
+        break;
+      }
+      if (size <= kSelThreads) {
+        each([&](int k, int t) {
+          const uint32_t y = weight_key(x[k]);
+          if (t >= lo && t < hi && (y & mask) == prefix) few[atomicAdd(&num_few, 1)] = y;
+        });
+        __syncthreads();
+        const uint32_t y = static_cast<int>(threadIdx.x) < size ? few[threadIdx.x] : 0u;
+        const bool mine = static_cast<int>(threadIdx.x) < size;
+        // the largest value v of the remaining bits with at least `need` keys >= prefix | v
+        for (int b = shift - 1; b >= 0; --b) {
+          const uint32_t with = prefix | (1u << b);
+          if (__syncthreads_count(mine && y >= with) >= need) prefix = with;
+        }
+        key = prefix;
+        ties = need - __syncthreads_count(mine && y > key);
+        break;
+      }
+      shift = digit == 0 ? 10 : 0;
+    }
+  }
+  auto classify = [&](int t, float v, bool* equal) -> bool {
     *equal = false;
     if (t >= w1) return false;
     if (t < lo || t >= hi) return true;
     if (!any) return false;
-    const uint32_t k = weight_key(x);
-    *equal = k == prefix;
-    return k > prefix;
+    const uint32_t y = weight_key(v);
+    *equal = y == key;
+    return y > key;
   };
   int sure = 0, equal = 0;
-  for (int t0 = w0; t0 < w1; t0 += 32 * kSelUnroll) {
-    float x[kSelUnroll];
-#pragma unroll
-    for (int k = 0; k < kSelUnroll; ++k) {
-      const int t = t0 + 32 * k + lane;
-      x[k] = t < w1 ? __ldg(mass + t) : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < kSelUnroll; ++k) {
-      bool e;
-      const bool y = classify(t0 + 32 * k + lane, x[k], &e);
-      sure += __popc(__ballot_sync(0xffffffffu, y));
-      equal += __popc(__ballot_sync(0xffffffffu, e));
-    }
-  }
-  __shared__ int wsure[kSelWarps], wequal[kSelWarps];
+  each([&](int k, int t) {
+    bool e;
+    const bool y = classify(t, x[k], &e);
+    sure += __popc(__ballot_sync(0xffffffffu, y));
+    equal += __popc(__ballot_sync(0xffffffffu, e));
+  });
+  __syncthreads();  // wsum is free
   if (lane == 0) {
-    wsure[warp] = sure;
-    wequal[warp] = equal;
+    wsum[0][warp] = sure;
+    wsum[1][warp] = equal;
   }
   __syncthreads();
-  int s0 = lane < warp ? wsure[lane] : 0, e0 = lane < warp ? wequal[lane] : 0;
+  int s0 = lane < warp ? wsum[0][lane] : 0, e0 = lane < warp ? wsum[1][lane] : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s0 += __shfl_xor_sync(0xffffffffu, s0, o);
     e0 += __shfl_xor_sync(0xffffffffu, e0, o);
   }
-  for (int t0 = w0; t0 < w1; t0 += 32 * kSelUnroll) {
-    float x[kSelUnroll];
-#pragma unroll
-    for (int k = 0; k < kSelUnroll; ++k) {
-      const int t = t0 + 32 * k + lane;
-      x[k] = t < w1 ? __ldg(mass + t) : 0.f;
+  const unsigned below = (1u << lane) - 1u;
+  each([&](int k, int t) {
+    bool e;
+    const bool y = classify(t, x[k], &e);
+    const unsigned by = __ballot_sync(0xffffffffu, y), be = __ballot_sync(0xffffffffu, e);
+    const int eq = e0 + __popc(be & below);  // equal ones before this position
+    if (y || (e && eq < ties)) {
+      const int at = s0 + __popc(by & below) + min(eq, ties);
+      kept[at] = t;
+      mass_out[at] = x[k];
     }
-#pragma unroll
-    for (int k = 0; k < kSelUnroll; ++k) {
-      const int t = t0 + 32 * k + lane;
-      bool e;
-      const bool y = classify(t, x[k], &e);
-      const unsigned by = __ballot_sync(0xffffffffu, y), be = __ballot_sync(0xffffffffu, e);
-      const unsigned below = (1u << lane) - 1u;
-      const int eq = e0 + __popc(be & below);  // equal ones before this position
-      if (y || (e && eq < ties)) {
-        const int at = s0 + __popc(by & below) + min(eq, ties);
-        kept[at] = t;
-        mass_out[at] = x[k];
-      }
-      s0 += __popc(by);
-      e0 += __popc(be);
-    }
-  }
+    s0 += __popc(by);
+    e0 += __popc(be);
+  });
 }
 
 // ------------------------------------------------------------------ eviction: row moves
@@ -318,7 +334,7 @@ cudaError_t launch_commit_tree(const CommitArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   (void)cudaGetLastError();
-  evict_select_kernel<<<dim3(a.num_kv_heads, a.num_seqs), kSelThreads, 256 * 32 * sizeof(int), stream>>>(a);
+  evict_select_kernel<<<dim3(a.num_kv_heads, a.num_seqs), kSelThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the moves may be set up while the selection runs; they wait for it before they read
