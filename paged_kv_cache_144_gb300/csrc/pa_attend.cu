@@ -21,7 +21,9 @@ constexpr size_t kCounters = 1 << 16;
 // How a call of these sizes runs, and what it keeps in the workspace.
 struct Plan {
   enum Kind { kRows, kFew, kTensor } kind;
-  int paired;                 // kTensor: two row tiles per K/V tile
+  int cg;                     // kTensor: CTAs that share a tile (1, or a cluster of 2)
+  int paired;                 // kTensor: the streams are two row tiles
+  int seg_rows;               // kTensor: rows of a segment
   DecodeKey key;              // kFew: the decode kernel's variant and geometry
   DecodeGeometry geo;
   int ctas;
@@ -41,7 +43,10 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
   const int64_t rows = static_cast<int64_t>(max_q_len) * group;
   const bool q8 = kv_dtype == PA_FP8_E4M3 || kv_dtype == PA_INT8;
   pl->ctas = sms;
-  pl->paired = rows > stream_rows(group) ? 1 : 0;
+  const int rps = stream_rows(group);
+  pl->cg = head_dim == 128 && rows > rps && tuning_override("PA_ATTEND_CG") != 1 ? 2 : 1;
+  pl->paired = rows > static_cast<int64_t>(rps) * pl->cg ? 1 : 0;
+  pl->seg_rows = rps * pl->cg * (pl->paired ? 2 : 1);
   pl->kind = rows <= kFewRows ? Plan::kFew : (q8 ? Plan::kRows : Plan::kTensor);
   size_t records = 0, pending = 0;
   pl->num_counters = 0;
@@ -60,9 +65,10 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
     records = 2 * warps * pl->geo.record_floats * sizeof(float);
     pending = 2 * warps * sizeof(int);
   } else if (pl->kind == Plan::kTensor) {
-    pl->rec_rows = pl->paired ? kTile : static_cast<int>((rows + 7) / 8 * 8);
+    pl->ctas = sms / pl->cg * pl->cg;
+    pl->rec_rows = rows < rps ? static_cast<int>((rows + 7) / 8 * 8) : kTile;
     pl->slots = pl->paired ? 2 : 4;
-    pl->num_counters = pl->paired ? 2 * static_cast<size_t>(sms) : static_cast<size_t>(num_seqs) * num_kv_heads;
+    pl->num_counters = pl->paired ? 2 * static_cast<size_t>(sms) : static_cast<size_t>(num_seqs) * num_kv_heads * pl->cg;
     records = static_cast<size_t>(sms) * pl->slots * 2 * pl->rec_rows * (head_dim + 2) * sizeof(float);
   }
   size_t at = up256((pl->num_counters > kCounters ? pl->num_counters : kCounters) * sizeof(int));
@@ -128,14 +134,14 @@ cudaError_t launch_few(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaS
 
 // 4-D view of a 16-bit pool: {64 elements, 8 rows, 128-byte halves of a row, groups of 8 rows}; one box = box_rows
 // rows, landing as [group][half][8 rows][128 bytes], swizzled by row.
-bool encode_tile_map(CUtensorMap* map, const void* cache, int64_t rows, int head_dim, int box_rows) {
+bool encode_tile_map(CUtensorMap* map, const void* cache, int64_t rows, int head_dim, int box_rows, int box_halves) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t row_bytes = static_cast<cuuint64_t>(head_dim) * 2;
   const cuuint32_t halves = static_cast<cuuint32_t>(row_bytes / 128);
   cuuint64_t dims[4] = {64, 8, halves, static_cast<cuuint64_t>(rows / 8)};
   cuuint64_t strides[3] = {row_bytes, 128, 8 * row_bytes};
-  cuuint32_t box[4] = {64, 8, halves, static_cast<cuuint32_t>(box_rows / 8)};
+  cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(box_halves), static_cast<cuuint32_t>(box_rows / 8)};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(cache), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -157,12 +163,13 @@ bool encode_query_map(CUtensorMap* map, const AttendParams& a) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename KVT, int D>
+template <typename KVT, int D, int CG>
 cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream) {
-  using Tr = TcTraits<KVT, D>;
+  using Tr = TcTraits<KVT, D, CG>;
   TcParams p;
   p.a = a;
   p.paired = pl.paired;
+  p.seg_rows = pl.seg_rows;
   // the second product is free where memory traffic bounds the call, and wanted where the output keeps its precision
   p.split_p = (!pl.paired || a.out_dtype == PA_F32) ? 1 : 0;
   p.rec_rows = pl.rec_rows;
@@ -171,11 +178,11 @@ cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaSt
   p.records = reinterpret_cast<float*>(ws + pl.records);
   CUtensorMap tk, tv, tq;
   const int64_t rows = a.num_blocks * a.num_kv_heads * a.block_size;
-  const int box = a.block_size < kTile ? a.block_size : kTile;
-  if (!encode_tile_map(&tk, a.k_cache, rows, D, box) || !encode_tile_map(&tv, a.v_cache, rows, D, box) ||
-      !encode_query_map(&tq, a))
+  auto box = [&](int most) { return a.block_size < most ? a.block_size : most; };
+  if (!encode_tile_map(&tk, a.k_cache, rows, D, box(Tr::KROWS), Tr::NH) ||
+      !encode_tile_map(&tv, a.v_cache, rows, D, box(kTile), Tr::VH) || !encode_query_map(&tq, a))
     return cudaErrorInvalidValue;
-  auto kern = attend_tc_kernel<KVT, D>;
+  auto kern = attend_tc_kernel<KVT, D, CG>;
   const size_t smem = Tr::smem_bytes(a.num_seqs);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -184,11 +191,14 @@ cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaSt
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.pdl ? 1 : 0;
+  cfg.numAttrs = a.pdl ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, tk, tv, tq, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -284,9 +294,13 @@ int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaS
   } else if (pl.kind == Plan::kRows) {
     e = p.kv_dtype == PA_FP8_E4M3 ? launch_t<e4m3_t, 128>(p, stream) : launch_t<i8_t, 128>(p, stream);
   } else if (p.kv_dtype == PA_F16) {
-    e = p.head_dim == 128 ? launch_tc<f16_t, 128>(p, pl, ws, stream) : launch_tc<f16_t, 64>(p, pl, ws, stream);
+    e = p.head_dim == 64 ? launch_tc<f16_t, 64, 1>(p, pl, ws, stream)
+        : pl.cg == 1     ? launch_tc<f16_t, 128, 1>(p, pl, ws, stream)
+                         : launch_tc<f16_t, 128, 2>(p, pl, ws, stream);
   } else {
-    e = p.head_dim == 128 ? launch_tc<bf16_t, 128>(p, pl, ws, stream) : launch_tc<bf16_t, 64>(p, pl, ws, stream);
+    e = p.head_dim == 64 ? launch_tc<bf16_t, 64, 1>(p, pl, ws, stream)
+        : pl.cg == 1     ? launch_tc<bf16_t, 128, 1>(p, pl, ws, stream)
+                         : launch_tc<bf16_t, 128, 2>(p, pl, ws, stream);
   }
   if (e == cudaSuccess && p.mass) {
     const int cap = p.max_blocks_per_seq << p.block_shift;

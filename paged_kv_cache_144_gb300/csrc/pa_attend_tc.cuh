@@ -61,17 +61,71 @@ constexpr int kTcThreads = 384;
 
 // ----------------------------------------------------------------- tcgen05 wrappers
 
+// CG: CTAs that share a tensor-core operation (1, or the 2 of a cluster).
+template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_addr, uint32_t cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr), "r"(cols) : "memory");
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr), "r"(cols) : "memory");
 }
+template <int CG>
 __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols) {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+  if constexpr (CG == 1) {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+  } else {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+  }
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Arrives on `bar` (in both CTAs of a pair, at the same offset) when this thread's tensor-core operations so far are done.
+template <int CG>
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+// Barriers between the CTAs of a pair: arrive on the pair's first CTA, wait with the cluster's scope.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void arrive_first_cta(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_bounded_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // One lane of the warp, always the same one, chosen in a way that leaves the branch on it warp-uniform to the compiler.
 __device__ __forceinline__ bool elect_one() {
@@ -80,20 +134,28 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 // Operand descriptors are passed as their two words: the high word holds no address and is a constant.
+template <int CG>
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                           bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
-      : "memory");
+#define PA_MMA_SS(CGS)                                                                                                   \
+  asm volatile(                                                                                                          \
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t" \
+      "tcgen05.mma.cta_group::" CGS ".kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),                                       \
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))                     \
+      : "memory")
+  if constexpr (CG == 1) PA_MMA_SS("1"); else PA_MMA_SS("2");
+#undef PA_MMA_SS
 }
+template <int CG>
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
-      : "memory");
+#define PA_MMA_TS(CGS)                                                                                            \
+  asm volatile(                                                                                                   \
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"                       \
+      "tcgen05.mma.cta_group::" CGS ".kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),                             \
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))                              \
+      : "memory")
+  if constexpr (CG == 1) PA_MMA_TS("1"); else PA_MMA_TS("2");
+#undef PA_MMA_TS
 }
 // 32 columns of this warp's 32 lanes
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
@@ -193,17 +255,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr & 0x3ffffu) >> 4) | ((1024u >> 4) << 16); }
 constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
 
-// Instruction descriptor: float32 accumulators, 16-bit operands, M = 128.
-constexpr uint32_t mma_idesc(bool bf16, bool b_mn_major, int n) {
+// Instruction descriptor: float32 accumulators, 16-bit operands, M = 128 per CTA.
+constexpr uint32_t mma_idesc(bool bf16, bool b_mn_major, int n, int cg) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
-         (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(8 * cg) << 24);
 }
 
 // ----------------------------------------------------------------- geometry
 
 struct TcParams {
   AttendParams a;
-  int paired;        // more than 128 rows per (sequence, KV head): the streams are two row tiles
+  int paired;        // the streams are two row tiles (else: one, its position tiles in turn)
+  int seg_rows;      // rows of a segment: stream_rows x CTAs of a group x (paired: 2)
   int split_p;       // P as hi + lo
   int rec_rows;      // rows of a record
   int slots;         // records of one stream per CTA: paired 2, alternating 4
@@ -267,7 +330,7 @@ struct WarpFrag {
 
 __device__ __forceinline__ bool advance_frag(FragIter& it, Frag& f, const int* prefix, const TcParams& p) {
   const AttendParams& a = p.a;
-  const int rpt = stream_rows(a.group) * (p.paired ? 2 : 1);
+  const int rpt = p.seg_rows;
   while (it.u < it.u1) {
     while (prefix[it.s + 1] <= it.u) ++it.s;  // last sequence starting at or before u (u < U: one exists)
     const int per = (prefix[it.s + 1] - prefix[it.s]) / a.num_kv_heads;
@@ -345,20 +408,27 @@ __device__ __forceinline__ int cut_slot_kind(int c, int c0, int U, int nw, int s
   return c > c0 || range_start(c, U, nw) >= seg_start ? 0 : 1;
 }
 
-template <typename KVT, int D>
+template <typename KVT, int D, int CG>
 struct TcTraits {
   static constexpr bool BF16 = std::is_same<KVT, bf16_t>::value;
   static constexpr int NH = D * 2 / 128;           // 128-byte halves per 16-bit row
-  static constexpr int GROUP = NH * 1024;          // bytes of 8 rows
-  static constexpr int TILE_BYTES = kTile / 8 * GROUP;
-  static constexpr int NST = D == 128 ? 2 : 4;     // stages of K and of V
+  static constexpr int TILE_BYTES = kTile * D * 2;  // a tile of K, V or Q
+  // A pair of CTAs halves every K and V tile: each holds 64 of a K tile's positions, and one 128-byte half of all of a
+  // V tile's rows.
+  static_assert(CG == 1 || NH == 2, "a pair of CTAs shares tiles of 256-byte rows");
+  static constexpr int KROWS = kTile / CG;         // rows of a K stage
+  static constexpr int VH = NH / CG;               // halves of a V stage
+  static constexpr int KGROUP = NH * 1024, VGROUP = VH * 1024;  // bytes of 8 rows
+  static constexpr int STAGE = TILE_BYTES / CG;    // bytes of a K or V stage
+  static constexpr int NST = (D == 128 ? 2 : 4) * CG;  // stages of K and of V
   static constexpr int OFF_Q = 0;                  // two tiles
   static constexpr int OFF_K = 2 * TILE_BYTES;
-  static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
-  static constexpr int OFF_BAR = OFF_V + NST * TILE_BYTES;
+  static constexpr int OFF_V = OFF_K + NST * STAGE;
+  static constexpr int OFF_BAR = OFF_V + NST * STAGE;
   // barriers (8 bytes each)
   static constexpr int KF = 0, KE = KF + NST, VF = KE + NST, VE = VF + NST, QF = VE + NST, QE = QF + 2, SF = QE + 2,
-                       PF = SF + 2, OD = PF + 2, RB = OD + 2, NBAR = RB + 2;
+                       PF = SF + 2, OD = PF + 2, RB = OD + 2,
+                       KP = RB + 2, VP = KP + NST, QP = VP + NST, NBAR = QP + 2;  // KP, VP, QP: the peer's has arrived
   static constexpr int OFF_MISC = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;  // tmem address, flags, scan scratch
   static constexpr int OFF_FRAG = OFF_MISC + 256;                         // WarpFrag per warp, one more for warp 1
   static constexpr int OFF_PREFIX = OFF_FRAG + (13 * static_cast<int>(sizeof(WarpFrag)) + 15) / 16 * 16;
@@ -367,12 +437,12 @@ struct TcTraits {
 
 // ----------------------------------------------------------------- kernel
 
-template <typename KVT, int D>
+template <typename KVT, int D, int CG>
 __global__ void __launch_bounds__(kTcThreads, 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const __grid_constant__ CUtensorMap tmap_q,
                  const __grid_constant__ TcParams p) {
-  using Tr = TcTraits<KVT, D>;
+  using Tr = TcTraits<KVT, D, CG>;
   constexpr int NST = Tr::NST;
   const AttendParams& a = p.a;
   extern __shared__ uint8_t smem_raw[];
@@ -384,9 +454,17 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   int* const prefix = reinterpret_cast<int*>(sm + Tr::OFF_PREFIX);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = a.num_seqs;
+  const int rank = CG == 1 ? 0 : static_cast<int>(cluster_rank());  // CTA of its group; the first issues the products
+  const int group_id = static_cast<int>(blockIdx.x) / CG, groups = static_cast<int>(gridDim.x) / CG;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   auto wait = [&](int i, uint32_t parity) -> bool {
     if (mbar_wait_bounded(bar(i), parity, kDefaultWaitLimitNs)) return true;
+    raise_error(a.err, PA_DEVERR_TIMEOUT);
+    return false;
+  };
+  // the same for what the other CTA of a pair arrives on
+  auto wait_pair = [&](int i, uint32_t parity) -> bool {
+    if (mbar_wait_bounded_cluster(bar(i), parity, kDefaultWaitLimitNs)) return true;
     raise_error(a.err, PA_DEVERR_TIMEOUT);
     return false;
   };
@@ -400,23 +478,26 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       mbar_init(bar(Tr::KE + i), 1);
       mbar_init(bar(Tr::VF + i), 1);
       mbar_init(bar(Tr::VE + i), 1);
+      mbar_init(bar(Tr::KP + i), 1);
+      mbar_init(bar(Tr::VP + i), 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(Tr::QF + t), 1);
       mbar_init(bar(Tr::QE + t), 1);
       mbar_init(bar(Tr::SF + t), 1);
-      mbar_init(bar(Tr::PF + t), 4);
+      mbar_init(bar(Tr::PF + t), 4 * CG);
+      mbar_init(bar(Tr::QP + t), 1);
       mbar_init(bar(Tr::OD + t), 1);
       mbar_init(bar(Tr::RB + t), 4);
     }
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(base + Tr::OFF_MISC, 512);
+  if (warp == 1) tmem_alloc<CG>(base + Tr::OFF_MISC, 512);
   griddep_wait();
 
   // ---- cost positions before each sequence (every CTA computes the same)
   {
-    const int rpt = stream_rows(a.group) * (p.paired ? 2 : 1);
+    const int rpt = p.seg_rows;
     int carry = 0;
     constexpr int NW = kTcThreads / 32;
     int* const wsum = misc + 8;
@@ -474,11 +555,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();  // the peer's barriers exist
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
   const int U = prefix[S];
   const int want = (U + kFragCost) / (kFragCost + 1);  // at least one tile per CTA
-  const int nw = min(static_cast<int>(gridDim.x), max(want, 1));
+  const int nw = min(groups, max(want, 1));
   FragIter it;
   it.U = U;
   it.nw = nw;
@@ -487,9 +569,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   it.s_state = -1;
   it.m = it.m_pos = it.kvh = 0;
   it.u = it.u1 = 0;
-  if (static_cast<int>(blockIdx.x) < nw && U > 0) {
-    it.u = range_start(blockIdx.x, U, nw);
-    it.u1 = range_start(blockIdx.x + 1, U, nw);
+  if (group_id < nw && U > 0) {
+    it.u = range_start(group_id, U, nw);
+    it.u1 = range_start(group_id + 1, U, nw);
     int lo = 0, hi = S - 1;
     while (lo < hi) {  // last sequence with prefix <= u
       const int mid = (lo + hi + 1) >> 1;
@@ -503,15 +585,33 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   __syncwarp();
   const Frag& f = wf->f;
 
+  // row tile of stream t in this CTA within its sequence
+  auto row_tile = [&](int m, int t) { return p.paired ? (m * 2 + t) * CG + rank : m * CG + rank; };
+
+  // V rows of a stage outside the sequence (or before the window) may hold anything, or were not loaded: zero for the
+  // products (one warp; n_hi, n_lo: the first row past the end, the first visible one)
+  auto clear_v = [&](int st, int n_hi, int n_lo) {
+    if (n_hi >= kTile && n_lo <= 0) return;
+    const uint32_t vt = base + Tr::OFF_V + st * Tr::STAGE;
+    for (int x = lane; x < kTile * Tr::VH * 8; x += 32) {
+      const int r = x / (Tr::VH * 8), c = x % (Tr::VH * 8);
+      if (r >= n_hi || r < n_lo) sts128_zero(vt + (r >> 3) * Tr::VGROUP + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+  };
+
   // The softmax threads hold a row's 128 scores each: registers move to their warps (88 * 128 + 208 * 256 = 168 * 384).
   if (warp < 4) {
   regs_dec<88>();
   if (warp == 0 || warp == 3) {
     // ================================================================= TMA producers: K (warp 0), V (warp 3)
     const bool is_v = warp == 3;
-    const int BR = min(a.block_size, kTile);            // rows per box
-    const int nbox = kTile / BR;
-    const uint32_t box_bytes = static_cast<uint32_t>(BR / 8) * Tr::GROUP;
+    const int TR = is_v ? kTile : Tr::KROWS;            // rows of a stage
+    const int row_off = is_v ? 0 : rank * Tr::KROWS;    // its first position within the tile
+    const int BR = min(a.block_size, TR);               // rows per box
+    const int nbox = TR / BR;
+    const uint32_t box_bytes = static_cast<uint32_t>(BR / 8) * (is_v ? Tr::VGROUP : Tr::KGROUP);
     const uint32_t ring = base + (is_v ? Tr::OFF_V : Tr::OFF_K);
     const int FULL = is_v ? Tr::VF : Tr::KF, EMPTY = is_v ? Tr::VE : Tr::KE;
     int kt = 0;  // tiles issued
@@ -523,7 +623,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int32_t* table = a.block_tables + static_cast<int64_t>(f.s) * a.max_blocks_per_seq;
       // this lane's block of tile j (its table entry), or -1
       auto entry = [&](int j) -> int {
-        const int blk = ((j * kTile) >> a.block_shift) + (nbox > 1 ? lane : 0);
+        const int blk = ((j * kTile + row_off) >> a.block_shift) + (nbox > 1 ? lane : 0);
         if (lane >= nbox || blk < blk_lo || blk >= nblk) return -1;
         const int pb = __ldg(table + blk);
         if (pb >= 0 && pb < a.num_blocks) return pb;
@@ -542,9 +642,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
         if (lane == 0) mbar_arrive_expect_tx(bar(FULL + st), bytes);
         __syncwarp();
-        const int row = nbox > 1 ? 0 : ((j * kTile) & (a.block_size - 1));
+        const int row = nbox > 1 ? 0 : ((j * kTile + row_off) & (a.block_size - 1));
         if (pb >= 0)
-          tma_load_4d(ring + st * Tr::TILE_BYTES + lane * box_bytes, is_v ? &tmap_v : &tmap_k, 0, 0, 0,
+          tma_load_4d(ring + st * Tr::STAGE + lane * box_bytes, is_v ? &tmap_v : &tmap_k, 0, 0, is_v && CG == 2 ? rank : 0,
                       (pb * a.num_kv_heads + kvh) * (a.block_size >> 3) + (row >> 3), bar(FULL + st));
         if (j + 1 < t1) next = entry(j + 1);  // read while the next stage is waited for
       }
@@ -558,11 +658,26 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         if (!wait(EMPTY + i, ph)) wait(FULL + i, ph);
       }
     }
+  } else if (warp == 1 && rank != 0) {
+    // ================================================================= the second CTA of a pair: says what has arrived
+    int kt = 0;
+    bool ok = true;
+    while (ok && next_frag(wf, prefix, p)) {
+      for (int j = f.t0; ok && j < f.t1; ++j, ++kt) {
+        const int st = kt % NST;
+        const uint32_t ph = static_cast<uint32_t>(kt / NST) & 1u;
+        if (!(ok = wait(Tr::KF + st, ph))) break;
+        if (lane == 0) arrive_first_cta(bar(Tr::KP + st));
+        if (!(ok = wait(Tr::VF + st, ph))) break;
+        clear_v(st, f.v.T - j * kTile, f.lo - j * kTile);
+        if (lane == 0) arrive_first_cta(bar(Tr::VP + st));
+      }
+    }
   } else if (warp == 1) {
     // ================================================================= MMA issuer
-    constexpr uint32_t kIdQK = mma_idesc(Tr::BF16, false, kTile);
-    constexpr uint32_t kIdPV = mma_idesc(Tr::BF16, true, D);
-    constexpr uint32_t kDescHi = desc_hi(Tr::GROUP), kQDescHi = desc_hi(1024);
+    constexpr uint32_t kIdQK = mma_idesc(Tr::BF16, false, kTile, CG);
+    constexpr uint32_t kIdPV = mma_idesc(Tr::BF16, true, D, CG);
+    constexpr uint32_t kKDescHi = desc_hi(Tr::KGROUP), kVDescHi = desc_hi(Tr::VGROUP), kQDescHi = desc_hi(1024);
     const uint32_t q_half = static_cast<uint32_t>(stream_rows(a.group)) * 128;  // the query tile is [half][row][128 bytes]
     WarpFrag* const wq = wf + 11;  // fragments whose S products are next
     const Frag& fq = wq->f;
@@ -578,20 +693,25 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int st = ktq % NST;
       const bool first_of_stream = p.paired ? tq_frag == 0 : tq_frag < 2;
       const bool last_of_stream = p.paired ? jq + 1 >= fq.t1 : jq + 2 >= fq.t1;
+      const uint32_t kph = static_cast<uint32_t>(ktq / NST) & 1u;
       if (first_of_stream && !wait(Tr::QF + t, q_use[t] & 1u)) return false;
-      if (!wait(Tr::KF + st, static_cast<uint32_t>(ktq / NST) & 1u)) return false;
+      if (!wait(Tr::KF + st, kph)) return false;
+      if constexpr (CG == 2) {
+        if (first_of_stream && !wait_pair(Tr::QP + t, q_use[t] & 1u)) return false;
+        if (!wait_pair(Tr::KP + st, kph)) return false;
+      }
       tc_fence_after();
       const bool last_use = !p.paired || t == 1;   // of this K tile
       if (elect_one()) {
-        const uint32_t qa = desc_lo(base + Tr::OFF_Q + t * Tr::TILE_BYTES), kb = desc_lo(base + Tr::OFF_K + st * Tr::TILE_BYTES);
+        const uint32_t qa = desc_lo(base + Tr::OFF_Q + t * Tr::TILE_BYTES), kb = desc_lo(base + Tr::OFF_K + st * Tr::STAGE);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           const uint32_t oq = ((s >> 2) * q_half + (s & 3) * 32) >> 4, ok = ((s >> 2) * 1024 + (s & 3) * 32) >> 4;
-          tc_mma_ss(tmem + t * 128, qa + oq, kQDescHi, kb + ok, kDescHi, kIdQK, s > 0);
+          tc_mma_ss<CG>(tmem + t * 128, qa + oq, kQDescHi, kb + ok, kKDescHi, kIdQK, s > 0);
         }
-        tc_commit(bar(Tr::SF + t));
-        if (last_use) tc_commit(bar(Tr::KE + st));
-        if (last_of_stream) tc_commit(bar(Tr::QE + t));
+        tc_commit<CG>(bar(Tr::SF + t));
+        if (last_use) tc_commit<CG>(bar(Tr::KE + st));
+        if (last_of_stream) tc_commit<CG>(bar(Tr::QE + t));
       }
       __syncwarp();
       if (last_of_stream) ++q_use[t];
@@ -621,34 +741,27 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           const bool first = p.paired ? j == f.t0 : j - f.t0 < 2;  // the stream's first tile of the fragment
           if (e == 0) {
             if (!wait(Tr::VF + st, static_cast<uint32_t>(ktv / NST) & 1u)) { ok = false; break; }
-            // rows outside the sequence (or before the window) may hold anything, or were not loaded
-            const int n_hi = f.v.T - j * kTile, n_lo = f.lo - j * kTile;
-            if (n_hi < kTile || n_lo > 0) {
-              const uint32_t vt = base + Tr::OFF_V + st * Tr::TILE_BYTES;
-              for (int x = lane; x < kTile * Tr::NH * 8; x += 32) {
-                const int r = x / (Tr::NH * 8), c = x % (Tr::NH * 8);
-                if (r >= n_hi || r < n_lo) sts128_zero(vt + (r >> 3) * Tr::GROUP + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16);
-              }
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
+            clear_v(st, f.v.T - j * kTile, f.lo - j * kTile);
+            if constexpr (CG == 2) {
+              if (!wait_pair(Tr::VP + st, static_cast<uint32_t>(ktv / NST) & 1u)) { ok = false; break; }
             }
           }
-          if (!wait(Tr::PF + t, pf[t] & 1u)) { ok = false; break; }
+          if (!(CG == 2 ? wait_pair(Tr::PF + t, pf[t] & 1u) : wait(Tr::PF + t, pf[t] & 1u))) { ok = false; break; }
           ++pf[t];
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t vb = desc_lo(base + Tr::OFF_V + st * Tr::TILE_BYTES);
-            tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128, vb, kDescHi, kIdPV, !first);
+            const uint32_t vb = desc_lo(base + Tr::OFF_V + st * Tr::STAGE);
+            tc_mma_ts<CG>(tmem + 256 + t * 128, tmem + t * 128, vb, kVDescHi, kIdPV, !first);
 #pragma unroll
             for (int s = 1; s < kTile / 16; ++s)
-              tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, vb + s * (2 * Tr::GROUP >> 4), kDescHi, kIdPV, true);
+              tc_mma_ts<CG>(tmem + 256 + t * 128, tmem + t * 128 + s * 8, vb + s * (2 * Tr::VGROUP >> 4), kVDescHi, kIdPV, true);
             if (p.split_p) {
 #pragma unroll
               for (int s = 0; s < kTile / 16; ++s)
-                tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 64 + s * 8, vb + s * (2 * Tr::GROUP >> 4), kDescHi, kIdPV, true);
+                tc_mma_ts<CG>(tmem + 256 + t * 128, tmem + t * 128 + 64 + s * 8, vb + s * (2 * Tr::VGROUP >> 4), kVDescHi, kIdPV, true);
             }
-            tc_commit(bar(Tr::OD + t));
-            if (e == per_tile - 1) tc_commit(bar(Tr::VE + st));
+            tc_commit<CG>(bar(Tr::OD + t));
+            if (e == per_tile - 1) tc_commit<CG>(bar(Tr::VE + st));
           }
           __syncwarp();
           if (have_q) ok = issue_qk();
@@ -675,9 +788,13 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(Tr::QF + t), bytes);
           tma_load_4d(base + Tr::OFF_Q + t * Tr::TILE_BYTES, &tmap_q, 0, f.kvh * a.group,
-                      f.v.row0 + (p.paired ? (f.m * 2 + t) * per_box : 0), 0, bar(Tr::QF + t));
+                      f.v.row0 + row_tile(f.m, t) * per_box, 0, bar(Tr::QF + t));
         }
         __syncwarp();
+        if (CG == 2 && rank != 0) {
+          if (!(ok = wait(Tr::QF + t, static_cast<uint32_t>(uses[t] - 1) & 1u))) break;
+          if (lane == 0) arrive_first_cta(bar(Tr::QP + t));
+        }
       }
       if (!p.paired) parity ^= n & 1;
     }
@@ -724,7 +841,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       if (!p.paired) parity ^= n & 1;
       if (j0 >= f.t1) continue;
       const int rps = stream_rows(a.group);
-      const int row0 = p.paired ? (f.m * 2 + t) * rps : 0;
+      const int row0 = row_tile(f.m, t) * rps;
       const int rows = min(rps, f.v.L * a.group - row0);  // of this stream (none: the segment's last rows are the other's)
       const int r = row0 + wq * 32 + lane;
       const bool valid = wq * 32 + lane < rows;
@@ -863,7 +980,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(Tr::PF + t));
+        if (lane == 0) {
+          if constexpr (CG == 2) arrive_first_cta(bar(Tr::PF + t)); else mbar_arrive(bar(Tr::PF + t));
+        }
       }
       if (!ok) break;
 
@@ -907,7 +1026,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int slot_kind = slot_kind_of(f.whole, f.idx);
       const int rec_floats = p.rec_rows * (D + 2);
       auto record = [&](int cta, int kind, int c) {
-        return p.records + (static_cast<int64_t>(cta) * p.slots * 2 + kind * 2 + c) * rec_floats;
+        return p.records + (static_cast<int64_t>(cta) * p.slots * 2 + kind * 2 + c) * rec_floats;  // cta: of the grid
       };
       {
         float* const rec = record(blockIdx.x, slot_kind, e);
@@ -934,7 +1053,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       for (int c = c0; c <= c1; ++c) total += p.paired ? 1 : min(2, tiles_in(c, U, nw, f.seg_start, f.seg_tiles));
       // paired: the streams' rows are joined apart (the segment that leaves a CTA unfinished is its last one); alternating:
       // the segment's only rows
-      int* const counter = p.paired ? p.counters + 2 * c0 + t : p.counters + f.s * a.num_kv_heads + f.kvh;
+      int* const counter = p.paired ? p.counters + (2 * c0 + t) * CG + rank
+                                    : p.counters + (f.s * a.num_kv_heads + f.kvh) * CG + rank;
       // (two words in turn: a warp still reading one is not overtaken by the next fragment's arrival)
       volatile int* const arrived = misc + 4 + 2 * (f.idx & 1) + t;
       if ((threadIdx.x & 127) == 0) *arrived = atom_add_acq_rel_gpu(counter, 1);
@@ -948,7 +1068,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             const int k = tiles_in(c, U, nw, f.seg_start, f.seg_tiles);
             const int kind = f.whole ? slot_kind : cut_slot_kind(c, c0, U, nw, f.seg_start);
             for (int x = 0; x < (p.paired ? 1 : min(2, k)); ++x)
-              M = fmaxf(M, __ldcg(record(c, kind, p.paired ? t : x) + p.rec_rows * D + 2 * lr));
+              M = fmaxf(M, __ldcg(record(c * CG + rank, kind, p.paired ? t : x) + p.rec_rows * D + 2 * lr));
           }
           float L = 0.f;
           float acc[D / 32];
@@ -958,7 +1078,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             const int k = tiles_in(c, U, nw, f.seg_start, f.seg_tiles);
             const int kind = f.whole ? slot_kind : cut_slot_kind(c, c0, U, nw, f.seg_start);
             for (int x = 0; x < (p.paired ? 1 : min(2, k)); ++x) {
-              const float* rec = record(c, kind, p.paired ? t : x);
+              const float* rec = record(c * CG + rank, kind, p.paired ? t : x);
               const float2 ml = __ldcg(reinterpret_cast<const float2*>(rec + p.rec_rows * D + 2 * lr));
               const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
               L = fmaf(w, ml.y, L);
@@ -988,9 +1108,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();  // nobody uses the peer's shared memory or TMEM any more
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc<CG>(tmem, 512);
   }
 }
 

@@ -35,7 +35,7 @@ struct AttendParams {
   const int32_t* seq_lens; const int32_t* q_starts; const int32_t* prefix_lens; const uint64_t* tree_mask;
   int max_blocks_per_seq, block_shift, num_tokens, max_q_len, group, num_kv_heads, num_seqs, window; unsigned* err;
 };
-struct TcParams { AttendParams a; int paired; };
+struct TcParams { AttendParams a; int paired, seg_rows; };
 static unsigned bits;
 inline void raise_error(unsigned*, unsigned b) { bits |= b; }
 enum { PA_DEVERR_SEQ_LEN = 4, PA_DEVERR_QUERY = 64 };
@@ -66,8 +66,9 @@ int main() {
     const uint64_t word = 0;
     if (trial % 5 == 2) a.prefix_lens = pre.data();
     if (trial % 5 == 3) a.tree_mask = &word;
-    p.paired = static_cast<long long>(a.max_q_len) * a.group > stream_rows(a.group);
-    const int rpt = stream_rows(a.group) * (p.paired ? 2 : 1);
+    const int ctas = rnd(1, 2);   // of a group
+    p.paired = static_cast<long long>(a.max_q_len) * a.group > stream_rows(a.group) * ctas;
+    const int rpt = p.seg_rows = stream_rows(a.group) * ctas * (p.paired ? 2 : 1);
     std::vector<int> prefix(S + 1, 0);
     std::map<std::tuple<int, int, int>, std::set<int>> todo;   // tiles of every segment
     for (int s = 0; s < S; ++s) {
@@ -149,7 +150,7 @@ def test_work_split(tmp_path):
     code += _between(common, "struct SeqView", "// softcap * tanh")
     code += _between(tc, "__host__ __device__ __forceinline__ int stream_rows", "// A warp's iterator").replace("struct WarpFrag", "struct Unused")
     code += _between(tc, "__device__ __forceinline__ bool advance_frag", "// The warp's next fragment")
-    code += _between(tc, "// CTA whose range holds", "template <typename KVT, int D>")
+    code += _between(tc, "// CTA whose range holds", "template <typename KVT, int D, int CG>")
     code += MAIN
     src = tmp_path / "split.cpp"
     src.write_text(code)
