@@ -69,7 +69,7 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
     pl->rec_rows = rows < rps ? static_cast<int>((rows + 7) / 8 * 8) : kTile;
     pl->slots = pl->paired ? 2 : 4;
     pl->num_counters = pl->paired ? 2 * static_cast<size_t>(sms) : static_cast<size_t>(num_seqs) * num_kv_heads * pl->cg;
-    records = static_cast<size_t>(sms) * pl->slots * 2 * pl->rec_rows * (head_dim + 2) * sizeof(float);
+    records = static_cast<size_t>(sms) * pl->slots * 2 * pl->rec_rows * (head_dim + 2) * sizeof(float);  // (32-byte multiples)
   }
   size_t at = up256((pl->num_counters > kCounters ? pl->num_counters : kCounters) * sizeof(int));
   pl->records = at;

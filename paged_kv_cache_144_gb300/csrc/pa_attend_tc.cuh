@@ -9,11 +9,11 @@
 // float32), so O is rarely rescaled.
 //
 // Layout on the SM.  One persistent CTA per SM, 12 warps:
-//   warps 0, 3 TMA producers of the K and of the V tiles of 128 positions, one
-//              box per cache block, into rings of stages
-//   warp 1     issues every tcgen05.mma and owns the TMEM (512 columns: S0, S1,
-//              O0, O1 of 128 lanes x 128 columns; the weights P overwrite S)
-//   warp 2     brings the query rows of both streams into shared memory
+//   warp 0     TMA producer: K and V tiles of 128 positions, one box per cache
+//              block, into rings of stages
+//   warps 1-2  issue the tcgen05.mma of streams 0 and 1 (TMEM, 512 columns: S0,
+//              S1, O0, O1 of 128 lanes x 128 columns; the weights P overwrite S)
+//   warp 3     brings both streams' query rows (TMA), zeroes V rows
 //   warps 4-7, 8-11   softmax of streams 0 and 1, one row per thread: the row
 //              maximum and sum need no exchange between threads
 // Two streams alternate, so the tensor cores compute for one while the other's
@@ -101,7 +101,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void arrive_first_cta(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar)
+      "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar)
       : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
@@ -229,6 +229,26 @@ __device__ __forceinline__ void store_row32(void* out, int dtype, int64_t i, con
     }
     store32(static_cast<uint16_t*>(out) + i, w, wide);
     store32(static_cast<uint16_t*>(out) + i + 16, w + 8, wide);
+  }
+}
+// V = 2 or 4 consecutive floats of a record, and the same columns of an output row
+template <int V>
+__device__ __forceinline__ void load_columns(const float* src, float* v) {
+  if constexpr (V == 4) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+  } else {
+    const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+    v[0] = x.x, v[1] = x.y;
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_columns(void* out, int dtype, int64_t i, const float* v) {
+  if constexpr (V == 4) {
+    store_out4(out, dtype, i, make_float4(v[0], v[1], v[2], v[3]), true);
+  } else {
+    store_out(out, dtype, i, v[0]);
+    store_out(out, dtype, i + 1, v[1]);
   }
 }
 template <int N>
@@ -428,12 +448,89 @@ struct TcTraits {
   // barriers (8 bytes each)
   static constexpr int KF = 0, KE = KF + NST, VF = KE + NST, VE = VF + NST, QF = VE + NST, QE = QF + 2, SF = QE + 2,
                        PF = SF + 2, OD = PF + 2, RB = OD + 2,
-                       KP = RB + 2, VP = KP + NST, QP = VP + NST, NBAR = QP + 2;  // KP, VP, QP: the peer's has arrived
+                       KP = RB + 2, VP = KP + NST, QP = VP + NST,  // the peer's has arrived
+                       VL = QP + 2, NBAR = VL + NST;               // a V tile with rows to be zeroed has arrived
   static constexpr int OFF_MISC = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;  // tmem address, flags, scan scratch
-  static constexpr int OFF_FRAG = OFF_MISC + 256;                         // WarpFrag per warp, one more for warp 1
-  static constexpr int OFF_PREFIX = OFF_FRAG + (13 * static_cast<int>(sizeof(WarpFrag)) + 15) / 16 * 16;
+  static constexpr int OFF_FRAG = OFF_MISC + 256;                         // WarpFrag per warp
+  static constexpr int OFF_PREFIX = OFF_FRAG + (12 * static_cast<int>(sizeof(WarpFrag)) + 15) / 16 * 16;
   static size_t smem_bytes(int num_seqs) { return 1024 + OFF_PREFIX + static_cast<size_t>(num_seqs + 1) * 4; }
 };
+
+// Where contribution c of a fragment with this slot kind lies.
+template <int D>
+__device__ __forceinline__ float* record_at(const TcParams& p, int cta, int kind, int c) {
+  return p.records + (static_cast<int64_t>(cta) * p.slots * 2 + kind * 2 + c) * (p.rec_rows * (D + 2));
+}
+
+// Joins the contributions of CTA groups c0 .. c1 to rows 32 wq .. 32 wq + 31 of a stream's row tile, in order, and writes the
+// rows out; run by one warp of the contribution that arrived last.  Each lane takes one row's maximum and weights; then
+// kJoin rows at a time, D / 32 columns per lane, with the loads of a record's rows all under way at once (one row at a time the
+// latency of each load showed: 100 us at the end of a 600 us call); more rows would take registers
+// from the main loop.
+constexpr int kJoin = 4;
+template <typename KVT, int D, int CG>
+__device__ __forceinline__ void join_rows(const TcParams& p, const Frag& f, int U, int nw, int c0, int c1, int rank, int t, int wq,
+                                       int row0, int rows, int slot_kind) {
+  const AttendParams& a = p.a;
+  const int lane = threadIdx.x & 31;
+  constexpr int V = D / 32;  // columns per lane
+  auto each_record = [&](auto body) {
+    for (int c = c0; c <= c1; ++c) {
+      const int n = p.paired ? 1 : min(2, tiles_in(c, U, nw, f.seg_start, f.seg_tiles));
+      const int kind = f.whole ? slot_kind : cut_slot_kind(c, c0, U, nw, f.seg_start);
+      for (int x = 0; x < n; ++x) body(record_at<D>(p, c * CG + rank, kind, p.paired ? t : x));
+    }
+  };
+  const int lr = min(wq * 32 + lane, rows - 1);
+  float M = -INFINITY, L = 0.f;
+  each_record([&](const float* rec) { M = fmaxf(M, __ldcg(rec + p.rec_rows * D + 2 * lr)); });
+  each_record([&](const float* rec) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(rec + p.rec_rows * D + 2 * lr));
+    L = fmaf(ml.x == -INFINITY ? 0.f : exp2f(ml.x - M), ml.y, L);
+  });
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32 && wq * 32 + r0 < rows; r0 += kJoin) {
+    float acc[kJoin][V];
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) {
+#pragma unroll
+      for (int q = 0; q < V; ++q) acc[k][q] = 0.f;
+    }
+    each_record([&](const float* rec) {
+      const float m = __ldcg(rec + p.rec_rows * D + 2 * lr);
+      const float w = m == -INFINITY ? 0.f : exp2f(m - M);
+      const float* const src = rec + static_cast<int64_t>(wq * 32 + r0) * D + lane * V;
+      float o[kJoin][V];
+#pragma unroll
+      for (int k = 0; k < kJoin; ++k) {
+        if (wq * 32 + r0 + k < rows) load_columns<V>(src + k * D, o[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kJoin; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, r0 + k);
+#pragma unroll
+        for (int q = 0; q < V; ++q) acc[k][q] = fmaf(wk, o[k][q], acc[k][q]);
+      }
+    });
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) {
+      const int row = wq * 32 + r0 + k;
+      const float ik = __shfl_sync(0xffffffffu, inv, r0 + k), Lk = __shfl_sync(0xffffffffu, L, r0 + k);
+      if (row >= rows) continue;
+      const int i = (row0 + row) / a.group, h = f.kvh * a.group + (row0 + row) - i * a.group;
+      const int64_t o0 = ((static_cast<int64_t>(f.v.row0) + i) * a.num_heads + h) * D + lane * V;
+      bool bad = Lk != Lk;
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        acc[k][q] *= ik;
+        bad |= !(fabsf(acc[k][q]) < INFINITY);
+      }
+      store_columns<V>(a.out, a.out_dtype, o0, acc[k]);
+      if (__any_sync(0xffffffffu, bad)) attend_row_again<KVT, D>(a, f.s, f.v, i, h);
+    }
+  }
+}
 
 // ----------------------------------------------------------------- kernel
 
@@ -475,9 +572,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     prefetch_tensormap(&tmap_q);
     for (int i = 0; i < NST; ++i) {
       mbar_init(bar(Tr::KF + i), 1);
-      mbar_init(bar(Tr::KE + i), 1);
+      mbar_init(bar(Tr::KE + i), p.paired ? 2 : 1);  // paired: both streams read every tile
       mbar_init(bar(Tr::VF + i), 1);
-      mbar_init(bar(Tr::VE + i), 1);
+      mbar_init(bar(Tr::VE + i), p.paired ? 2 : 1);
+      mbar_init(bar(Tr::VL + i), 1);
       mbar_init(bar(Tr::KP + i), 1);
       mbar_init(bar(Tr::VP + i), 1);
     }
@@ -581,7 +679,6 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   }
   WarpFrag* const wf = reinterpret_cast<WarpFrag*>(sm + Tr::OFF_FRAG) + warp;
   if (lane == 0) wf->it = it;
-  if (threadIdx.x == 32) wf[11].it = it;  // warp 1 walks two of them
   __syncwarp();
   const Frag& f = wf->f;
 
@@ -590,8 +687,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
 
   // V rows of a stage outside the sequence (or before the window) may hold anything, or were not loaded: zero for the
   // products (one warp; n_hi, n_lo: the first row past the end, the first visible one)
+  auto partial = [&](int j) { return f.v.T - j * kTile < kTile || f.lo > j * kTile; };
   auto clear_v = [&](int st, int n_hi, int n_lo) {
-    if (n_hi >= kTile && n_lo <= 0) return;
     const uint32_t vt = base + Tr::OFF_V + st * Tr::STAGE;
     for (int x = lane; x < kTile * Tr::VH * 8; x += 32) {
       const int r = x / (Tr::VH * 8), c = x % (Tr::VH * 8);
@@ -604,174 +701,65 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   // The softmax threads hold a row's 128 scores each: registers move to their warps (88 * 128 + 208 * 256 = 168 * 384).
   if (warp < 4) {
   regs_dec<88>();
-  if (warp == 0 || warp == 3) {
-    // ================================================================= TMA producers: K (warp 0), V (warp 3)
-    const bool is_v = warp == 3;
-    const int TR = is_v ? kTile : Tr::KROWS;            // rows of a stage
-    const int row_off = is_v ? 0 : rank * Tr::KROWS;    // its first position within the tile
-    const int BR = min(a.block_size, TR);               // rows per box
-    const int nbox = TR / BR;
-    const uint32_t box_bytes = static_cast<uint32_t>(BR / 8) * (is_v ? Tr::VGROUP : Tr::KGROUP);
-    const uint32_t ring = base + (is_v ? Tr::OFF_V : Tr::OFF_K);
-    const int FULL = is_v ? Tr::VF : Tr::KF, EMPTY = is_v ? Tr::VE : Tr::KE;
-    int kt = 0;  // tiles issued
+  if (warp == 0) {
+    // ================================================================= TMA producer
+    // V of a tile, then K of the next: the order in which their stages come free
+    const uint32_t k_box = static_cast<uint32_t>(min(a.block_size, Tr::KROWS) / 8) * Tr::KGROUP;
+    const uint32_t v_box = static_cast<uint32_t>(min(a.block_size, kTile) / 8) * Tr::VGROUP;
+    const int k_boxes = Tr::KROWS / min(a.block_size, Tr::KROWS), v_boxes = kTile / min(a.block_size, kTile);
+    const int k_off = rank * Tr::KROWS;  // first position of this CTA's part of a K tile
+    int kk = 0, kv = 0;                  // K and V tiles issued
     bool ok = true;
-    while (ok && next_frag(wf, prefix, p)) {
+    // this lane's block of the rows from position t0 on (its table entry), or -1
+    auto entry = [&](int t0, int boxes) -> int {
+      const int blk = (t0 >> a.block_shift) + (boxes > 1 ? lane : 0);
       const int nblk = (f.v.T + a.block_size - 1) >> a.block_shift;
-      const int blk_lo = f.lo >> a.block_shift;
-      const int t1 = f.t1, kvh = f.kvh;
-      const int32_t* table = a.block_tables + static_cast<int64_t>(f.s) * a.max_blocks_per_seq;
-      // this lane's block of tile j (its table entry), or -1
-      auto entry = [&](int j) -> int {
-        const int blk = ((j * kTile + row_off) >> a.block_shift) + (nbox > 1 ? lane : 0);
-        if (lane >= nbox || blk < blk_lo || blk >= nblk) return -1;
-        const int pb = __ldg(table + blk);
-        if (pb >= 0 && pb < a.num_blocks) return pb;
-        raise_error(a.err, PA_DEVERR_BLOCK_ID);
-        return 0;
-      };
-      int next = entry(f.t0);
-      for (int j = f.t0; j < t1; ++j, ++kt) {
-        const int st = kt % NST;
-        const uint32_t ph = static_cast<uint32_t>(kt / NST) & 1u;
-        const int pb = next;
-        const uint32_t bytes = box_bytes * static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, pb >= 0)));
-        if (!__all_sync(0xffffffffu, wait(EMPTY + st, ph ^ 1u))) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(bar(FULL + st), bytes);
-        __syncwarp();
-        const int row = nbox > 1 ? 0 : ((j * kTile + row_off) & (a.block_size - 1));
-        if (pb >= 0)
-          tma_load_4d(ring + st * Tr::STAGE + lane * box_bytes, is_v ? &tmap_v : &tmap_k, 0, 0, is_v && CG == 2 ? rank : 0,
-                      (pb * a.num_kv_heads + kvh) * (a.block_size >> 3) + (row >> 3), bar(FULL + st));
-        if (j + 1 < t1) next = entry(j + 1);  // read while the next stage is waited for
+      if (lane >= boxes || blk < (f.lo >> a.block_shift) || blk >= nblk) return -1;
+      const int pb = __ldg(a.block_tables + static_cast<int64_t>(f.s) * a.max_blocks_per_seq + blk);
+      if (pb >= 0 && pb < a.num_blocks) return pb;
+      raise_error(a.err, PA_DEVERR_BLOCK_ID);
+      return 0;
+    };
+    auto issue = [&](bool is_v, int count, int pb, int t0, int boxes, uint32_t box, bool part) -> bool {
+      const int st = count % NST;
+      const uint32_t ph = static_cast<uint32_t>(count / NST) & 1u;
+      const uint32_t bytes = box * static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, pb >= 0)));
+      if (!__all_sync(0xffffffffu, wait((is_v ? Tr::VE : Tr::KE) + st, ph ^ 1u))) return false;
+      // a V tile with rows to be zeroed is announced by the warp that does so
+      const uint32_t full = bar((is_v ? (part ? Tr::VL : Tr::VF) : Tr::KF) + st);
+      if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+      __syncwarp();
+      const int row = boxes > 1 ? 0 : (t0 & (a.block_size - 1));
+      if (pb >= 0)
+        tma_load_4d(base + (is_v ? Tr::OFF_V : Tr::OFF_K) + st * Tr::STAGE + lane * box, is_v ? &tmap_v : &tmap_k, 0, 0,
+                    is_v && CG == 2 ? rank : 0, (pb * a.num_kv_heads + f.kvh) * (a.block_size >> 3) + (row >> 3), full);
+      return true;
+    };
+    while (ok && next_frag(wf, prefix, p)) {
+      const int t1 = f.t1;
+      int kb = entry(f.t0 * kTile + k_off, k_boxes), vb = entry(f.t0 * kTile, v_boxes);
+      if (!(ok = issue(false, kk++, kb, f.t0 * kTile + k_off, k_boxes, k_box, false))) break;
+      for (int j = f.t0; j < t1; ++j) {
+        // table entries a tile ahead of the wait for their stage
+        const int kn = j + 1 < t1 ? entry((j + 1) * kTile + k_off, k_boxes) : -1;
+        const int vn = j + 1 < t1 ? entry((j + 1) * kTile, v_boxes) : -1;
+        if (!(ok = issue(true, kv++, vb, j * kTile, v_boxes, v_box, partial(j)))) break;
+        if (j + 1 < t1 && !(ok = issue(false, kk++, kn, (j + 1) * kTile + k_off, k_boxes, k_box, false))) break;
+        vb = vn;
       }
     }
     // nothing of ours, and no arrival of the tensor cores, may land after the CTA has left: wait until each stage's
-    // last tile has been used (or, after a wait that ran out, has at least arrived)
+    // last tile has been used (after a wait that ran out, at least until it has arrived)
     for (int i = 0; i < NST; ++i) {
-      const int n = kt / NST + (i < kt % NST ? 1 : 0);
-      if (n > 0) {
-        const uint32_t ph = static_cast<uint32_t>(n - 1) & 1u;
-        if (!wait(EMPTY + i, ph)) wait(FULL + i, ph);
-      }
+      const int nk = kk / NST + (i < kk % NST ? 1 : 0), nv = kv / NST + (i < kv % NST ? 1 : 0);
+      if (nk > 0 && !wait(Tr::KE + i, static_cast<uint32_t>(nk - 1) & 1u)) wait(Tr::KF + i, static_cast<uint32_t>(nk - 1) & 1u);
+      if (nv > 0 && !wait(Tr::VE + i, static_cast<uint32_t>(nv - 1) & 1u)) wait(Tr::VF + i, static_cast<uint32_t>(nv - 1) & 1u);
     }
-  } else if (warp == 1 && rank != 0) {
-    // ================================================================= the second CTA of a pair: says what has arrived
-    int kt = 0;
-    bool ok = true;
-    while (ok && next_frag(wf, prefix, p)) {
-      for (int j = f.t0; ok && j < f.t1; ++j, ++kt) {
-        const int st = kt % NST;
-        const uint32_t ph = static_cast<uint32_t>(kt / NST) & 1u;
-        if (!(ok = wait(Tr::KF + st, ph))) break;
-        if (lane == 0) arrive_first_cta(bar(Tr::KP + st));
-        if (!(ok = wait(Tr::VF + st, ph))) break;
-        clear_v(st, f.v.T - j * kTile, f.lo - j * kTile);
-        if (lane == 0) arrive_first_cta(bar(Tr::VP + st));
-      }
-    }
-  } else if (warp == 1) {
-    // ================================================================= MMA issuer
-    constexpr uint32_t kIdQK = mma_idesc(Tr::BF16, false, kTile, CG);
-    constexpr uint32_t kIdPV = mma_idesc(Tr::BF16, true, D, CG);
-    constexpr uint32_t kKDescHi = desc_hi(Tr::KGROUP), kVDescHi = desc_hi(Tr::VGROUP), kQDescHi = desc_hi(1024);
-    const uint32_t q_half = static_cast<uint32_t>(stream_rows(a.group)) * 128;  // the query tile is [half][row][128 bytes]
-    WarpFrag* const wq = wf + 11;  // fragments whose S products are next
-    const Frag& fq = wq->f;
-    bool have_q = next_frag(wq, prefix, p);
-    int jq = have_q ? fq.t0 : 0, tq_frag = 0;   // tile of the next S product; its index within the fragment
-    int ktq = 0;            // its tile count
-    int nq = 0;             // S products issued (job number; stream = nq & 1)
-    uint32_t q_use[2] = {0u, 0u};
-    bool ok = true;
-    // one S = Q K^T
-    auto issue_qk = [&]() -> bool {
-      const int t = nq & 1;
-      const int st = ktq % NST;
-      const bool first_of_stream = p.paired ? tq_frag == 0 : tq_frag < 2;
-      const bool last_of_stream = p.paired ? jq + 1 >= fq.t1 : jq + 2 >= fq.t1;
-      const uint32_t kph = static_cast<uint32_t>(ktq / NST) & 1u;
-      if (first_of_stream && !wait(Tr::QF + t, q_use[t] & 1u)) return false;
-      if (!wait(Tr::KF + st, kph)) return false;
-      if constexpr (CG == 2) {
-        if (first_of_stream && !wait_pair(Tr::QP + t, q_use[t] & 1u)) return false;
-        if (!wait_pair(Tr::KP + st, kph)) return false;
-      }
-      tc_fence_after();
-      const bool last_use = !p.paired || t == 1;   // of this K tile
-      if (elect_one()) {
-        const uint32_t qa = desc_lo(base + Tr::OFF_Q + t * Tr::TILE_BYTES), kb = desc_lo(base + Tr::OFF_K + st * Tr::STAGE);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t oq = ((s >> 2) * q_half + (s & 3) * 32) >> 4, ok = ((s >> 2) * 1024 + (s & 3) * 32) >> 4;
-          tc_mma_ss<CG>(tmem + t * 128, qa + oq, kQDescHi, kb + ok, kKDescHi, kIdQK, s > 0);
-        }
-        tc_commit<CG>(bar(Tr::SF + t));
-        if (last_use) tc_commit<CG>(bar(Tr::KE + st));
-        if (last_of_stream) tc_commit<CG>(bar(Tr::QE + t));
-      }
-      __syncwarp();
-      if (last_of_stream) ++q_use[t];
-      ++nq;
-      if (last_use) {
-        ++ktq;
-        ++jq;
-        ++tq_frag;
-        if (jq == fq.t1) {
-          have_q = next_frag(wq, prefix, p);
-          jq = have_q ? fq.t0 : 0;
-          tq_frag = 0;
-        }
-      }
-      return true;
-    };
-    ok = !have_q || issue_qk();
-    if (ok && have_q) ok = issue_qk();
-    int nv = 0, ktv = 0;   // P V products issued, their tile count
-    uint32_t pf[2] = {0u, 0u};
-    while (ok && next_frag(wf, prefix, p)) {
-      const int per_tile = p.paired ? 2 : 1;
-      for (int j = f.t0; ok && j < f.t1; ++j, ++ktv) {
-        const int st = ktv % NST;
-        for (int e = 0; ok && e < per_tile; ++e, ++nv) {
-          const int t = nv & 1;
-          const bool first = p.paired ? j == f.t0 : j - f.t0 < 2;  // the stream's first tile of the fragment
-          if (e == 0) {
-            if (!wait(Tr::VF + st, static_cast<uint32_t>(ktv / NST) & 1u)) { ok = false; break; }
-            clear_v(st, f.v.T - j * kTile, f.lo - j * kTile);
-            if constexpr (CG == 2) {
-              if (!wait_pair(Tr::VP + st, static_cast<uint32_t>(ktv / NST) & 1u)) { ok = false; break; }
-            }
-          }
-          if (!(CG == 2 ? wait_pair(Tr::PF + t, pf[t] & 1u) : wait(Tr::PF + t, pf[t] & 1u))) { ok = false; break; }
-          ++pf[t];
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t vb = desc_lo(base + Tr::OFF_V + st * Tr::STAGE);
-            tc_mma_ts<CG>(tmem + 256 + t * 128, tmem + t * 128, vb, kVDescHi, kIdPV, !first);
-#pragma unroll
-            for (int s = 1; s < kTile / 16; ++s)
-              tc_mma_ts<CG>(tmem + 256 + t * 128, tmem + t * 128 + s * 8, vb + s * (2 * Tr::VGROUP >> 4), kVDescHi, kIdPV, true);
-            if (p.split_p) {
-#pragma unroll
-              for (int s = 0; s < kTile / 16; ++s)
-                tc_mma_ts<CG>(tmem + 256 + t * 128, tmem + t * 128 + 64 + s * 8, vb + s * (2 * Tr::VGROUP >> 4), kVDescHi, kIdPV, true);
-            }
-            tc_commit<CG>(bar(Tr::OD + t));
-            if (e == per_tile - 1) tc_commit<CG>(bar(Tr::VE + st));
-          }
-          __syncwarp();
-          if (have_q) ok = issue_qk();
-        }
-      }
-    }
-  } else {
-    // ================================================================= query rows of both streams
+  } else if (warp == 3) {
+    // ================================================================= query rows, V rows to be zeroed
     // (rows past the sequence's last are another sequence's, or zero past the last token: their results are not stored)
-    int uses[2] = {0, 0}, parity = 0;
+    int uses[2] = {0, 0}, parity = 0, kv = 0;
+    uint32_t vl = 0u;  // phases of VL used, per stage (a bit each)
     const int per_box = kTile / a.group;
     const uint32_t bytes = static_cast<uint32_t>(per_box * a.group) * D * 2;
     bool ok = true;
@@ -797,10 +785,103 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
       }
       if (!p.paired) parity ^= n & 1;
+      for (int j = f.t0; ok && j < f.t1; ++j, ++kv) {
+        if (!partial(j)) continue;
+        const int st = kv % NST;
+        if (!(ok = wait(Tr::VL + st, (vl >> st) & 1u))) break;
+        vl ^= 1u << st;
+        clear_v(st, f.v.T - j * kTile, f.lo - j * kTile);
+        if (lane == 0) mbar_arrive(bar(Tr::VF + st));
+      }
     }
     for (int t = 0; t < 2; ++t)
       if (uses[t] > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses[t] - 1) & 1u))
         wait(Tr::QF + t, static_cast<uint32_t>(uses[t] - 1) & 1u);
+  } else if (rank != 0) {
+    // ================================================================= the second CTA of a pair: says what has arrived
+    // (warp 1: K, warp 2: V)
+    const bool is_v = warp == 2;
+    int kt = 0;
+    bool ok = true;
+    while (ok && next_frag(wf, prefix, p)) {
+      for (int j = f.t0; ok && j < f.t1; ++j, ++kt) {
+        const int st = kt % NST;
+        if (!(ok = wait((is_v ? Tr::VF : Tr::KF) + st, static_cast<uint32_t>(kt / NST) & 1u))) break;
+        if (lane == 0) arrive_first_cta(bar((is_v ? Tr::VP : Tr::KP) + st));
+      }
+    }
+  } else {
+    // ================================================================= MMA issuers, one per stream
+    // (issuing, and committing to a barrier, keeps a thread as long as the products before it: two threads keep the
+    // tensor cores fed from both streams)
+    const int t = warp - 1;
+    constexpr uint32_t kIdQK = mma_idesc(Tr::BF16, false, kTile, CG);
+    constexpr uint32_t kIdPV = mma_idesc(Tr::BF16, true, D, CG);
+    constexpr uint32_t kKDescHi = desc_hi(Tr::KGROUP), kVDescHi = desc_hi(Tr::VGROUP), kQDescHi = desc_hi(1024);
+    const uint32_t q_half = static_cast<uint32_t>(stream_rows(a.group)) * 128;  // the query tile is [half][row][128 bytes]
+    const uint32_t s_tm = tmem + t * 128, o_tm = tmem + 256 + t * 128;
+    int uses = 0, parity = 0, kt = 0;  // query tiles used; tiles before this fragment
+    uint32_t pf = 0u;
+    bool ok = true;
+    while (ok && next_frag(wf, prefix, p)) {
+      const int t0 = f.t0, t1 = f.t1;
+      const int step = p.paired ? 1 : 2;
+      const int j0 = t0 + (p.paired ? 0 : t ^ parity);
+      if (!p.paired) parity ^= (t1 - t0) & 1;
+      const int kt0 = kt - t0;  // tile j has count kt0 + j
+      kt += t1 - t0;
+      if (j0 >= t1) continue;
+      // one S = Q K^T
+      auto issue_qk = [&](int j) -> bool {
+        const int st = (kt0 + j) % NST;
+        const uint32_t ph = static_cast<uint32_t>((kt0 + j) / NST) & 1u;
+        if (!wait(Tr::KF + st, ph)) return false;
+        if (CG == 2 && !wait_pair(Tr::KP + st, ph)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t qa = desc_lo(base + Tr::OFF_Q + t * Tr::TILE_BYTES), kb = desc_lo(base + Tr::OFF_K + st * Tr::STAGE);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t oq = ((s >> 2) * q_half + (s & 3) * 32) >> 4, ok = ((s >> 2) * 1024 + (s & 3) * 32) >> 4;
+            tc_mma_ss<CG>(s_tm, qa + oq, kQDescHi, kb + ok, kKDescHi, kIdQK, s > 0);
+          }
+          tc_commit<CG>(bar(Tr::SF + t));
+          tc_commit<CG>(bar(Tr::KE + st));
+          if (j + step >= t1) tc_commit<CG>(bar(Tr::QE + t));
+        }
+        __syncwarp();
+        return true;
+      };
+      const uint32_t qph = static_cast<uint32_t>(uses++) & 1u;
+      if (!(ok = wait(Tr::QF + t, qph))) break;
+      if (CG == 2 && !(ok = wait_pair(Tr::QP + t, qph))) break;
+      if (!(ok = issue_qk(j0))) break;
+      for (int j = j0; j < t1; j += step) {
+        const int st = (kt0 + j) % NST;
+        const uint32_t ph = static_cast<uint32_t>((kt0 + j) / NST) & 1u;
+        if (!(ok = wait(Tr::VF + st, ph))) break;
+        if (CG == 2 && !(ok = wait_pair(Tr::VP + st, ph))) break;
+        if (!(ok = CG == 2 ? wait_pair(Tr::PF + t, pf & 1u) : wait(Tr::PF + t, pf & 1u))) break;
+        ++pf;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t vb = desc_lo(base + Tr::OFF_V + st * Tr::STAGE);
+          tc_mma_ts<CG>(o_tm, s_tm, vb, kVDescHi, kIdPV, j != j0);
+#pragma unroll
+          for (int s = 1; s < kTile / 16; ++s)
+            tc_mma_ts<CG>(o_tm, s_tm + s * 8, vb + s * (2 * Tr::VGROUP >> 4), kVDescHi, kIdPV, true);
+          if (p.split_p) {
+#pragma unroll
+            for (int s = 0; s < kTile / 16; ++s)
+              tc_mma_ts<CG>(o_tm, s_tm + 64 + s * 8, vb + s * (2 * Tr::VGROUP >> 4), kVDescHi, kIdPV, true);
+          }
+          tc_commit<CG>(bar(Tr::OD + t));
+          tc_commit<CG>(bar(Tr::VE + st));
+        }
+        __syncwarp();
+        if (j + step < t1 && !(ok = issue_qk(j + step))) break;
+      }
+    }
   }
   } else {
     regs_inc<208>();
@@ -820,9 +901,6 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int64_t n = static_cast<int64_t>(min(v.L, max(0, v.L - v.T))) * a.num_heads * D;
       for (int64_t x = threadIdx.x - 128; x < n; x += 256)
         store_out(a.out, a.out_dtype, static_cast<int64_t>(v.row0) * a.num_heads * D + x, 0.f);
-      if (a.mass && v.T == 0 && v.L == 1)
-        for (int h = threadIdx.x - 128; h < a.num_heads; h += 256)
-          a.row_stats[static_cast<int64_t>(s) * a.num_heads + h] = make_float2(-INFINITY, 0.f);
     }
 
     // the four warps of the stream wait for one another (bounded, unlike a named barrier)
@@ -856,9 +934,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const float sc2 = a.scale * kLog2e;
       const float capk = a.softcap > 0.f ? 2.f * sc2 / a.softcap : 0.f, cap2 = a.softcap * kLog2e;
       // (a negative scale would turn the maximum of raw products into a minimum)
-      const bool modified = a.softcap > 0.f || a.slopes || a.mass || !(sc2 >= 0.f);
+      const bool modified = a.softcap > 0.f || a.slopes || !(sc2 >= 0.f);
       float m = -INFINITY, l = 0.f;
-      float* const score_row = a.mass && valid ? a.scores + (static_cast<int64_t>(f.s) * a.num_heads + h) * a.score_stride : nullptr;
 
       for (int j = j0; ok && j < f.t1; j += step, ++jobs) {
         if (!wait(Tr::SF + t, static_cast<uint32_t>(jobs) & 1u)) { ok = false; break; }
@@ -903,11 +980,6 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
 #pragma unroll
               for (int k = 0; k < 32; ++k) z[32 * c + k] = (see >> k) & 1u ? z[32 * c + k] : -INFINITY;
             }
-          }
-          if (score_row) {
-#pragma unroll
-            for (int c = 0; c < kTile; c += 4)
-              *reinterpret_cast<float4*>(score_row + tb + c) = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
           }
           // Weights of the tile against the reference maximum ms, summed and stored as the 16-bit operand of P V (hi, then
           // lo in the split form); returns the tile's largest score.
@@ -1011,25 +1083,19 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
               store_row32(a.out, a.out_dtype, o0 + c, o, wide);
             }
           }
-          float2 stats = make_float2(me, l);
           unsigned again = __ballot_sync(0xffffffffu, bad && valid);
           while (again) {
             const int k = __ffs(again) - 1;
             again &= again - 1;
             attend_row_again<KVT, D>(a, f.s, f.v, __shfl_sync(0xffffffffu, qi, k), __shfl_sync(0xffffffffu, h, k));
           }
-          if (a.mass && valid) a.row_stats[static_cast<int64_t>(f.s) * a.num_heads + h] = stats;
         }
         continue;
       }
       // ---- record, then count in; the last contribution joins them all
       const int slot_kind = slot_kind_of(f.whole, f.idx);
-      const int rec_floats = p.rec_rows * (D + 2);
-      auto record = [&](int cta, int kind, int c) {
-        return p.records + (static_cast<int64_t>(cta) * p.slots * 2 + kind * 2 + c) * rec_floats;  // cta: of the grid
-      };
       {
-        float* const rec = record(blockIdx.x, slot_kind, e);
+        float* const rec = record_at<D>(p, blockIdx.x, slot_kind, e);
         const int lr = wq * 32 + lane;
         if (warp_on) {
 #pragma unroll
@@ -1039,8 +1105,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             tmem_wait_ld();
             if (valid) {
 #pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<float4*>(rec + lr * D + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+              for (int k = 0; k < 32; k += 8) store32(rec + lr * D + c + k, reinterpret_cast<const uint32_t*>(o + k), true);
             }
           }
           if (valid) *reinterpret_cast<float2*>(rec + p.rec_rows * D + 2 * lr) = make_float2(me, l);
@@ -1062,46 +1127,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const bool last = *arrived == total - 1;
       if (last) {
         __threadfence();
-        for (int lr = wq; lr < rows; lr += 4) {
-          float M = -INFINITY;
-          for (int c = c0; c <= c1; ++c) {
-            const int k = tiles_in(c, U, nw, f.seg_start, f.seg_tiles);
-            const int kind = f.whole ? slot_kind : cut_slot_kind(c, c0, U, nw, f.seg_start);
-            for (int x = 0; x < (p.paired ? 1 : min(2, k)); ++x)
-              M = fmaxf(M, __ldcg(record(c * CG + rank, kind, p.paired ? t : x) + p.rec_rows * D + 2 * lr));
-          }
-          float L = 0.f;
-          float acc[D / 32];
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) acc[q] = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            const int k = tiles_in(c, U, nw, f.seg_start, f.seg_tiles);
-            const int kind = f.whole ? slot_kind : cut_slot_kind(c, c0, U, nw, f.seg_start);
-            for (int x = 0; x < (p.paired ? 1 : min(2, k)); ++x) {
-              const float* rec = record(c * CG + rank, kind, p.paired ? t : x);
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(rec + p.rec_rows * D + 2 * lr));
-              const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-              L = fmaf(w, ml.y, L);
-#pragma unroll
-              for (int q = 0; q < D / 32; ++q) {
-                const float o = __ldcg(rec + lr * D + lane + 32 * q);
-                acc[q] = fmaf(w, o, acc[q]);
-              }
-            }
-          }
-          const float inv = L > 0.f ? 1.f / L : 0.f;
-          const int i = (row0 + lr) / a.group, hh = f.kvh * a.group + (row0 + lr) - i * a.group;
-          const int64_t o0 = ((static_cast<int64_t>(f.v.row0) + i) * a.num_heads + hh) * D;
-          bool bad = L != L;
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            const float o = acc[q] * inv;
-            bad |= !(fabsf(o) < INFINITY);
-            store_out(a.out, a.out_dtype, o0 + lane + 32 * q, o);
-          }
-          if (__any_sync(0xffffffffu, bad)) attend_row_again<KVT, D>(a, f.s, f.v, i, hh);
-          if (a.mass && lane == 0) a.row_stats[static_cast<int64_t>(f.s) * a.num_heads + hh] = make_float2(M, L);
-        }
+        if (warp_on) join_rows<KVT, D, CG>(p, f, U, nw, c0, c1, rank, t, wq, row0, rows, slot_kind);
         if ((threadIdx.x & 127) == 0) *counter = 0;  // ready for the next call
       }
     }

@@ -150,7 +150,7 @@ def test_work_split(tmp_path):
     code += _between(common, "struct SeqView", "// softcap * tanh")
     code += _between(tc, "__host__ __device__ __forceinline__ int stream_rows", "// A warp's iterator").replace("struct WarpFrag", "struct Unused")
     code += _between(tc, "__device__ __forceinline__ bool advance_frag", "// The warp's next fragment")
-    code += _between(tc, "// CTA whose range holds", "template <typename KVT, int D, int CG>")
+    code += _between(tc, "// CTA whose range holds", "template <")
     code += MAIN
     src = tmp_path / "split.cpp"
     src.write_text(code)
