@@ -163,15 +163,13 @@ bool encode_query_map(CUtensorMap* map, const AttendParams& a) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename KVT, int D, int CG>
-cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream) {
+template <typename KVT, int D, int CG, bool SPLIT>
+cudaError_t launch_tc_as(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream) {
   using Tr = TcTraits<KVT, D, CG>;
   TcParams p;
   p.a = a;
   p.paired = pl.paired;
   p.seg_rows = pl.seg_rows;
-  // the second product is free where memory traffic bounds the call, and wanted where the output keeps its precision
-  p.split_p = (!pl.paired || a.out_dtype == PA_F32) ? 1 : 0;
   p.rec_rows = pl.rec_rows;
   p.slots = pl.slots;
   p.counters = reinterpret_cast<int*>(ws);
@@ -182,7 +180,7 @@ cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaSt
   if (!encode_tile_map(&tk, a.k_cache, rows, D, box(Tr::KROWS), Tr::NH) ||
       !encode_tile_map(&tv, a.v_cache, rows, D, box(kTile), Tr::VH) || !encode_query_map(&tq, a))
     return cudaErrorInvalidValue;
-  auto kern = attend_tc_kernel<KVT, D, CG>;
+  auto kern = attend_tc_kernel<KVT, D, CG, SPLIT>;
   const size_t smem = Tr::smem_bytes(a.num_seqs);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -216,6 +214,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) attend_rows_kernel(const Atten
     const int h = static_cast<int>(x % p.num_heads), i = static_cast<int>(x / p.num_heads);
     attend_row<KVT, D>(p, s, v, i, h);
   }
+}
+
+template <typename KVT, int D, int CG>
+cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream) {
+  // the second product is free where memory traffic bounds the call, and wanted where the output keeps its precision
+  return !pl.paired || a.out_dtype == PA_F32 ? launch_tc_as<KVT, D, CG, true>(a, pl, ws, stream)
+                                             : launch_tc_as<KVT, D, CG, false>(a, pl, ws, stream);
 }
 
 // mass[s][kvh][t] += sum over the group of exp2(score - max) / sum, from the stored scores: four positions per thread (the

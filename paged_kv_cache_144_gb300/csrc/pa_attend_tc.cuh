@@ -16,8 +16,10 @@
 //   warp 3     brings both streams' query rows (TMA), zeroes V rows
 //   warps 4-7, 8-11   softmax of streams 0 and 1, one row per thread: the row
 //              maximum and sum need no exchange between threads
-// Two streams alternate, so the tensor cores compute for one while the other's
-// softmax runs.  With more than 128 rows per (sequence, KV head) the streams
+// The streams' turns, and the two halves (64 positions) of each stream's tile,
+// keep the tensor cores and the softmax busy at once: while the weights of one
+// half are computed, the other half's are multiplied and the next tile's scores
+// take their columns.  With more than 128 rows per (sequence, KV head) the streams
 // are two row tiles over the same K/V tiles ("paired": every K/V byte read
 // from L2 serves 256 rows); with up to 128 rows they take the positions' tiles
 // in turn ("alternating") and their results are joined like any other split.
@@ -36,10 +38,10 @@
 //
 // Rounding.  P enters P V as 16 bits (bf16 with a bf16 cache, else f16 with
 // weights scaled by 2^7, so that small ones stay above its smallest value):
-// half a step of the type, below the rounding of a 16-bit output.  When the
-// split flag is set (float32 outputs; also whenever the memory traffic bounds
-// the call, where the second product is free) P is two such values, hi + lo,
-// and its rounding is that of 16 bits more.
+// half a step of the type, below the rounding of a 16-bit output.  In the SPLIT
+// form (float32 outputs; also with few rows, where memory traffic bounds the
+// call and the second product is free) P is two such values, hi + lo, and its
+// rounding that of as many bits more.
 //
 // A position's V row is multiplied by P = 0 in rows that do not see it, which
 // is not enough when it holds NaN or infinity: rows past the sequence's end (or
@@ -55,6 +57,7 @@
 namespace pa {
 
 constexpr int kTile = 128;      // positions per tile, rows per stream
+constexpr int kHalfTile = kTile / 2;
 constexpr int kFragCost = 1;    // tiles charged per fragment
 constexpr float kSlack = 8.f;   // log2 by which the maximum may lag
 constexpr int kTcThreads = 384;
@@ -287,7 +290,6 @@ struct TcParams {
   AttendParams a;
   int paired;        // the streams are two row tiles (else: one, its position tiles in turn)
   int seg_rows;      // rows of a segment: stream_rows x CTAs of a group x (paired: 2)
-  int split_p;       // P as hi + lo
   int rec_rows;      // rows of a record
   int slots;         // records of one stream per CTA: paired 2, alternating 4
   int* counters;     // arrivals: paired: by the segment's first CTA; alternating: by s * H_kv + kvh
@@ -447,7 +449,7 @@ struct TcTraits {
   static constexpr int OFF_BAR = OFF_V + NST * STAGE;
   // barriers (8 bytes each)
   static constexpr int KF = 0, KE = KF + NST, VF = KE + NST, VE = VF + NST, QF = VE + NST, QE = QF + 2, SF = QE + 2,
-                       PF = SF + 2, OD = PF + 2, RB = OD + 2,
+                       PF = SF + 4, OH = PF + 4, OD = OH + 2, RB = OD + 2,  // SF, PF: per half of a tile; OH, OD: its halves
                        KP = RB + 2, VP = KP + NST, QP = VP + NST,  // the peer's has arrived
                        VL = QP + 2, NBAR = VL + NST;               // a V tile with rows to be zeroed has arrived
   static constexpr int OFF_MISC = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;  // tmem address, flags, scan scratch
@@ -534,7 +536,7 @@ __device__ __forceinline__ void join_rows(const TcParams& p, const Frag& f, int 
 
 // ----------------------------------------------------------------- kernel
 
-template <typename KVT, int D, int CG>
+template <typename KVT, int D, int CG, bool SPLIT>
 __global__ void __launch_bounds__(kTcThreads, 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const __grid_constant__ CUtensorMap tmap_q,
@@ -583,7 +585,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       mbar_init(bar(Tr::QF + t), 1);
       mbar_init(bar(Tr::QE + t), 1);
       mbar_init(bar(Tr::SF + t), 1);
+      mbar_init(bar(Tr::SF + 2 + t), 1);
       mbar_init(bar(Tr::PF + t), 4 * CG);
+      mbar_init(bar(Tr::PF + 2 + t), 4 * CG);
+      mbar_init(bar(Tr::OH + t), 1);
       mbar_init(bar(Tr::QP + t), 1);
       mbar_init(bar(Tr::OD + t), 1);
       mbar_init(bar(Tr::RB + t), 4);
@@ -815,7 +820,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     // (issuing, and committing to a barrier, keeps a thread as long as the products before it: two threads keep the
     // tensor cores fed from both streams)
     const int t = warp - 1;
-    constexpr uint32_t kIdQK = mma_idesc(Tr::BF16, false, kTile, CG);
+    constexpr uint32_t kIdQK = mma_idesc(Tr::BF16, false, kHalfTile, CG);
     constexpr uint32_t kIdPV = mma_idesc(Tr::BF16, true, D, CG);
     constexpr uint32_t kKDescHi = desc_hi(Tr::KGROUP), kVDescHi = desc_hi(Tr::VGROUP), kQDescHi = desc_hi(1024);
     const uint32_t q_half = static_cast<uint32_t>(stream_rows(a.group)) * 128;  // the query tile is [half][row][128 bytes]
@@ -831,23 +836,28 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int kt0 = kt - t0;  // tile j has count kt0 + j
       kt += t1 - t0;
       if (j0 >= t1) continue;
-      // one S = Q K^T
-      auto issue_qk = [&](int j) -> bool {
+      // S = Q K^T of half a tile, into its half of the stream's columns (a pair of CTAs: 32 positions of each CTA's 64)
+      auto issue_qk = [&](int j, int half) -> bool {
         const int st = (kt0 + j) % NST;
         const uint32_t ph = static_cast<uint32_t>((kt0 + j) / NST) & 1u;
-        if (!wait(Tr::KF + st, ph)) return false;
-        if (CG == 2 && !wait_pair(Tr::KP + st, ph)) return false;
+        if (half == 0) {
+          if (!wait(Tr::KF + st, ph)) return false;
+          if (CG == 2 && !wait_pair(Tr::KP + st, ph)) return false;
+        }
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t qa = desc_lo(base + Tr::OFF_Q + t * Tr::TILE_BYTES), kb = desc_lo(base + Tr::OFF_K + st * Tr::STAGE);
+          const uint32_t qa = desc_lo(base + Tr::OFF_Q + t * Tr::TILE_BYTES);
+          const uint32_t kb = desc_lo(base + Tr::OFF_K + st * Tr::STAGE) + half * (kHalfTile / CG / 8 * Tr::KGROUP >> 4);
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
             const uint32_t oq = ((s >> 2) * q_half + (s & 3) * 32) >> 4, ok = ((s >> 2) * 1024 + (s & 3) * 32) >> 4;
-            tc_mma_ss<CG>(s_tm, qa + oq, kQDescHi, kb + ok, kKDescHi, kIdQK, s > 0);
+            tc_mma_ss<CG>(s_tm + half * kHalfTile, qa + oq, kQDescHi, kb + ok, kKDescHi, kIdQK, s > 0);
           }
-          tc_commit<CG>(bar(Tr::SF + t));
-          tc_commit<CG>(bar(Tr::KE + st));
-          if (j + step >= t1) tc_commit<CG>(bar(Tr::QE + t));
+          tc_commit<CG>(bar(Tr::SF + 2 * half + t));
+          if (half) {
+            tc_commit<CG>(bar(Tr::KE + st));
+            if (j + step >= t1) tc_commit<CG>(bar(Tr::QE + t));
+          }
         }
         __syncwarp();
         return true;
@@ -855,31 +865,33 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const uint32_t qph = static_cast<uint32_t>(uses++) & 1u;
       if (!(ok = wait(Tr::QF + t, qph))) break;
       if (CG == 2 && !(ok = wait_pair(Tr::QP + t, qph))) break;
-      if (!(ok = issue_qk(j0))) break;
-      for (int j = j0; j < t1; j += step) {
+      if (!(ok = issue_qk(j0, 0) && issue_qk(j0, 1))) break;
+      for (int j = j0; ok && j < t1; j += step, ++pf) {
         const int st = (kt0 + j) % NST;
         const uint32_t ph = static_cast<uint32_t>((kt0 + j) / NST) & 1u;
         if (!(ok = wait(Tr::VF + st, ph))) break;
         if (CG == 2 && !(ok = wait_pair(Tr::VP + st, ph))) break;
-        if (!(ok = CG == 2 ? wait_pair(Tr::PF + t, pf & 1u) : wait(Tr::PF + t, pf & 1u))) break;
-        ++pf;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t vb = desc_lo(base + Tr::OFF_V + st * Tr::STAGE);
-          tc_mma_ts<CG>(o_tm, s_tm, vb, kVDescHi, kIdPV, j != j0);
 #pragma unroll
-          for (int s = 1; s < kTile / 16; ++s)
-            tc_mma_ts<CG>(o_tm, s_tm + s * 8, vb + s * (2 * Tr::VGROUP >> 4), kVDescHi, kIdPV, true);
-          if (p.split_p) {
+        for (int half = 0; half < 2; ++half) {
+          if (!(ok = CG == 2 ? wait_pair(Tr::PF + 2 * half + t, pf & 1u) : wait(Tr::PF + 2 * half + t, pf & 1u))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t vb = desc_lo(base + Tr::OFF_V + st * Tr::STAGE);
+            const uint32_t pa = s_tm + half * kHalfTile;
 #pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
-              tc_mma_ts<CG>(o_tm, s_tm + 64 + s * 8, vb + s * (2 * Tr::VGROUP >> 4), kVDescHi, kIdPV, true);
+            for (int x = 0; x < (SPLIT ? 2 : 1) * (kHalfTile / 16); ++x) {
+              const int s = x % (kHalfTile / 16), lo = x / (kHalfTile / 16);
+              // 16 positions of the half: in a pair of CTAs its columns are positions 32 half .. and 64 + 32 half ..
+              const int row = CG == 1 ? half * kHalfTile + s * 16 : (s >> 1) * kHalfTile + half * 32 + (s & 1) * 16;
+              tc_mma_ts<CG>(o_tm, pa + lo * (kHalfTile / 2) + s * 8, vb + (row / 8 * Tr::VGROUP >> 4), kVDescHi, kIdPV,
+                            x > 0 || half != 0 || j != j0);
+            }
+            tc_commit<CG>(bar((half ? Tr::OD : Tr::OH) + t));
+            if (half) tc_commit<CG>(bar(Tr::VE + st));
           }
-          tc_commit<CG>(bar(Tr::OD + t));
-          tc_commit<CG>(bar(Tr::VE + st));
+          __syncwarp();
+          if (j + step < t1 && !(ok = issue_qk(j + step, half))) break;
         }
-        __syncwarp();
-        if (j + step < t1 && !(ok = issue_qk(j + step))) break;
       }
     }
   }
@@ -893,6 +905,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     constexpr float kLog2e = 1.4426950408889634f;
     // f16 weights carry a factor 2^7 (m is lowered by it), so that weights down to 2^-31 of the largest are normal
     constexpr float kLift = Tr::BF16 ? 0.f : 7.f;
+    constexpr float kMost = Tr::BF16 ? 256.f : 32768.f;  // 2^(kLift + kSlack): 64 weights of at most 2^kLift stay below it
     int jobs = 0, parity = 0;
 
     // queries at negative positions (more queries than tokens) see nothing
@@ -938,122 +951,129 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       float m = -INFINITY, l = 0.f;
 
       for (int j = j0; ok && j < f.t1; j += step, ++jobs) {
-        if (!wait(Tr::SF + t, static_cast<uint32_t>(jobs) & 1u)) { ok = false; break; }
-        tc_fence_after();
-        if (warp_on) {
-          const int tb = j * kTile;
-          float z[kTile];
+        // Half a tile at a time: while one half's weights are computed, the tensor cores multiply the other's and compute the
+        // next tile's scores in its place.
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(Tr::SF + 2 * half + t, static_cast<uint32_t>(jobs) & 1u)) { ok = false; break; }
+          tc_fence_after();
+          if (warp_on) {
+            // positions of the half: 32 from tb, 32 from tb + gap on
+            const int tb = j * kTile + half * (CG == 1 ? kHalfTile : 32);
+            constexpr int kGap = CG == 1 ? 32 : kHalfTile;
+            const uint32_t ps = ts + half * kHalfTile;  // the half's scores; its weights replace them (hi, then lo)
+            float z[kHalfTile];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, z + 32 * c);
-          tmem_wait_ld();
-          const bool full = rb.lo <= tb && rb.hi >= tb + kTile && (!tree || tb + kTile <= first);
-          const bool masked = !__all_sync(0xffffffffu, full || !valid);
-          // z: scores in the log2 domain, or (the plain case) raw products that the exponent's FMA scales by mul
-          float mul = sc2;
-          if (masked || modified) {
-            mul = 1.f;
-            if (a.softcap > 0.f) {
+            for (int c = 0; c < kHalfTile; c += 32) tmem_ld32(ps + c, z + c);
+            tmem_wait_ld();
+            const bool full = rb.lo <= tb && rb.hi >= tb + kGap + 32 && (!tree || tb + kGap + 32 <= first);
+            const bool masked = !__all_sync(0xffffffffu, full || !valid);
+            // z: scores in the log2 domain, or (the plain case) raw products that the exponent's FMA scales by mul
+            float mul = sc2;
+            if (masked || modified) {
+              mul = 1.f;
+              if (a.softcap > 0.f) {
 #pragma unroll
-              for (int c = 0; c < kTile; ++c) z[c] = cap2 - __fdividef(2.f * cap2, 1.f + fast_exp2(z[c] * capk));
-            } else {
+                for (int c = 0; c < kHalfTile; ++c) z[c] = cap2 - __fdividef(2.f * cap2, 1.f + fast_exp2(z[c] * capk));
+              } else {
 #pragma unroll
-              for (int c = 0; c < kTile; c += 2) {
-                const float2 x = fmul2(make_float2(z[c], z[c + 1]), make_float2(sc2, sc2));
-                z[c] = x.x;
-                z[c + 1] = x.y;
-              }
-            }
-            if (a.slopes) {
-              const float d0 = static_cast<float>(tb - rb.pos);
-#pragma unroll
-              for (int c = 0; c < kTile; ++c) z[c] = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), z[c]);
-            }
-          }
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int b0 = tb + 32 * c;
-              // bits [lo, hi) of this 32-position chunk
-              const int lo = max(0, min(32, rb.lo - b0)), hi = max(0, min(32, rb.hi - b0));
-              uint32_t see = (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & (lo >= 32 ? 0u : 0xffffffffu << lo);
-              if (tree && valid) see &= tree_bits(tree, a.tree_words, first, b0);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) z[32 * c + k] = (see >> k) & 1u ? z[32 * c + k] : -INFINITY;
-            }
-          }
-          // Weights of the tile against the reference maximum ms, summed and stored as the 16-bit operand of P V (hi, then
-          // lo in the split form); returns the tile's largest score.
-          float lt = 0.f;
-          auto weights_as = [&](auto split, float ms) -> float {
-            constexpr bool kSplit = decltype(split)::value;
-            float2 sum = make_float2(0.f, 0.f);
-            float mx = z[0];
-            const float2 mul2 = make_float2(mul, mul), neg = make_float2(-ms, -ms);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t hi[16], lo[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float z0 = z[32 * c + 2 * k], z1 = z[32 * c + 2 * k + 1];
-                mx = fmax3(mx, z0, z1);
-                const float2 x = ffma2(make_float2(z0, z1), mul2, neg);
-                const float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                sum = fadd2(sum, w);
-                hi[k] = pack2<Tr::BF16>(w.x, w.y);
-                if constexpr (kSplit) {
-                  const float2 q = unpack2<Tr::BF16>(hi[k]);
-                  lo[k] = pack2<Tr::BF16>(w.x - q.x, w.y - q.y);
+                for (int c = 0; c < kHalfTile; c += 2) {
+                  const float2 x = fmul2(make_float2(z[c], z[c + 1]), make_float2(sc2, sc2));
+                  z[c] = x.x;
+                  z[c + 1] = x.y;
                 }
               }
-              tmem_st16(ts + 16 * c, hi);
-              if constexpr (kSplit) tmem_st16(ts + 64 + 16 * c, lo);
-            }
-            lt = sum.x + sum.y;
-            return mx * mul;
-          };
-          auto weights = [&](float ms) { return p.split_p ? weights_as(std::true_type{}, ms) : weights_as(std::false_type{}, ms); };
-          // Against the maximum so far first: after a row's first tiles it seldom moves by more than kSlack, and neither the
-          // exponentials nor the maximum of this tile wait for the other.
-          float mx;
-          bool raise;
-          if (j == j0) {
-            float x = fmaxf(z[0], z[1]);
+              if (a.slopes) {
+                const float d0 = static_cast<float>(tb - rb.pos);
 #pragma unroll
-            for (int c = 2; c < kTile; c += 2) x = fmax3(x, z[c], z[c + 1]);
-            mx = x * mul;
-            raise = true;
-          } else {
-            mx = weights(m == -INFINITY ? 0.f : m - kLift);
-            raise = mx > (m == -INFINITY ? m : m + kSlack);
-          }
-          if (__any_sync(0xffffffffu, raise && valid)) {
-            const float mn = raise ? fmaxf(m, mx) : m;
-            const float alpha = raise && mn != -INFINITY ? fast_exp2(m - mn) : 1.f;   // nothing seen before: 2^-inf = 0
-            m = mn;
-            l *= alpha;
-            if (j != j0) {
-              // the product before this one must have left O
-              if (!wait(Tr::OD + t, static_cast<uint32_t>(jobs - 1) & 1u)) ok = false;
-              tc_fence_after();
-#pragma unroll
-              for (int c = 0; c < D; c += 16) {
-                float o[16];
-                tmem_ld16(to + c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] *= alpha;
-                tmem_st16(to + c, reinterpret_cast<const uint32_t*>(o));
+                for (int c = 0; c < kHalfTile; ++c)
+                  z[c] = fmaf(-slope2, fabsf(d0 + static_cast<float>((c >> 5) * kGap + (c & 31))), z[c]);
               }
             }
-            weights(m == -INFINITY ? 0.f : m - kLift);
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < kHalfTile / 32; ++c) {
+                const int b0 = tb + kGap * c;
+                // bits [lo, hi) of this 32-position chunk
+                const int lo = max(0, min(32, rb.lo - b0)), hi = max(0, min(32, rb.hi - b0));
+                uint32_t see = (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & (lo >= 32 ? 0u : 0xffffffffu << lo);
+                if (tree && valid) see &= tree_bits(tree, a.tree_words, first, b0);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) z[32 * c + k] = (see >> k) & 1u ? z[32 * c + k] : -INFINITY;
+              }
+            }
+            // Weights against the maximum so far first: after a row's first positions it seldom moves by kSlack (a sum of
+            // weights above kMost tells; one below it means no weight is large).  Only then, and for a row that has seen
+            // nothing yet, is this half's maximum found, O rescaled and the weights computed again.
+            const bool fresh = j == j0 && half == 0;  // nothing multiplied for this fragment yet
+            float lt;
+#pragma unroll 1
+            for (bool again = fresh;; again = true) {
+              if (again) {
+                float x = fmaxf(z[0], z[1]);
+#pragma unroll
+                for (int c = 2; c < kHalfTile; c += 2) x = fmax3(x, z[c], z[c + 1]);
+                const float mn = fmaxf(m, x * mul);
+                const float alpha = mn != -INFINITY ? fast_exp2(m - mn) : 1.f;   // nothing seen before: 2^-inf = 0
+                m = mn;
+                l *= alpha;
+                if (!fresh) {
+                  // the products before this half must have left O
+                  if (!wait((half ? Tr::OH : Tr::OD) + t, static_cast<uint32_t>(half ? jobs : jobs - 1) & 1u)) ok = false;
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int c = 0; c < D; c += 16) {
+                    float o[16];
+                    tmem_ld16(to + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] *= alpha;
+                    tmem_st16(to + c, reinterpret_cast<const uint32_t*>(o));
+                  }
+                }
+              }
+              const float ms = m == -INFINITY ? 0.f : m - kLift;
+              const float2 mul2 = make_float2(mul, mul), neg = make_float2(-ms, -ms);
+              float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+              for (int c = 0; c < kHalfTile / 32; ++c) {
+                float2 w[16];
+                uint32_t hi[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) w[k] = ffma2(make_float2(z[32 * c + 2 * k], z[32 * c + 2 * k + 1]), mul2, neg);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) w[k] = make_float2(fast_exp2(w[k].x), fast_exp2(w[k].y));
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                  sum0 = fadd2(sum0, w[k]);
+                  sum1 = fadd2(sum1, w[k + 1]);
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) hi[k] = pack2<Tr::BF16>(w[k].x, w[k].y);
+                tmem_st16(ps + 16 * c, hi);
+                if constexpr (SPLIT) {
+                  uint32_t lo[16];
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) {
+                    const float2 q = unpack2<Tr::BF16>(hi[k]);
+                    lo[k] = pack2<Tr::BF16>(w[k].x - q.x, w[k].y - q.y);
+                  }
+                  tmem_st16(ps + kHalfTile / 2 + 16 * c, lo);
+                }
+              }
+              sum0 = fadd2(sum0, sum1);
+              lt = sum0.x + sum0.y;
+              if (again || !__any_sync(0xffffffffu, valid && (lt > kMost || m == -INFINITY))) break;
+            }
+            l += lt;
+            tmem_wait_st();
           }
-          l += lt;
-          tmem_wait_st();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 2) arrive_first_cta(bar(Tr::PF + t)); else mbar_arrive(bar(Tr::PF + t));
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            const uint32_t pf = bar(Tr::PF + 2 * half + t);
+            if constexpr (CG == 2) arrive_first_cta(pf); else mbar_arrive(pf);
+          }
         }
       }
       if (!ok) break;
