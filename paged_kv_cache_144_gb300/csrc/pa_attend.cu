@@ -20,7 +20,7 @@ constexpr size_t kCounters = 1 << 16;
 
 // How a call of these sizes runs, and what it keeps in the workspace.
 struct Plan {
-  enum Kind { kRows, kFew, kTensor } kind;
+  enum Kind { kFew, kTensor } kind;
   int cg;                     // kTensor: CTAs that share a tile (1, or a cluster of 2)
   int paired;                 // kTensor: the streams are two row tiles
   int seg_rows;               // kTensor: rows of a segment
@@ -44,10 +44,11 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
   const bool q8 = kv_dtype == PA_FP8_E4M3 || kv_dtype == PA_INT8;
   pl->ctas = sms;
   const int rps = stream_rows(group);
-  pl->cg = head_dim == 128 && rows > rps && tuning_override("PA_ATTEND_CG") != 1 ? 2 : 1;
+  pl->cg = q8 || (head_dim == 128 && rows > rps) ? 2 : 1;
   pl->paired = rows > static_cast<int64_t>(rps) * pl->cg ? 1 : 0;
   pl->seg_rows = rps * pl->cg * (pl->paired ? 2 : 1);
-  pl->kind = rows <= kFewRows ? Plan::kFew : (q8 ? Plan::kRows : Plan::kTensor);
+  const int few = tuning_override("PA_ATTEND_FEW_ROWS");
+  pl->kind = rows <= (few >= 0 && few <= kFewRows ? few : kFewRows) || accumulate ? Plan::kFew : Plan::kTensor;
   size_t records = 0, pending = 0;
   pl->num_counters = 0;
   if (pl->kind == Plan::kFew) {
@@ -64,7 +65,7 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
     pl->num_counters = static_cast<size_t>(num_seqs) * num_kv_heads * pl->geo.row_groups;
     records = 2 * warps * pl->geo.record_floats * sizeof(float);
     pending = 2 * warps * sizeof(int);
-  } else if (pl->kind == Plan::kTensor) {
+  } else {
     pl->ctas = sms / pl->cg * pl->cg;
     pl->rec_rows = rows < rps ? static_cast<int>((rows + 7) / 8 * 8) : kTile;
     pl->slots = pl->paired ? 2 : 4;
@@ -148,6 +149,19 @@ bool encode_tile_map(CUtensorMap* map, const void* cache, int64_t rows, int head
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2-D view of an 8-bit pool: {row bytes, rows}; one box = box_rows rows of box_bytes bytes, as they are.
+bool encode_code_map(CUtensorMap* map, const void* cache, int64_t rows, int row_bytes, int box_rows, int box_bytes) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(cache), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 4-D view of the query rows: {64 elements, heads, tokens, 128-byte halves of a row}; one box = 128 / group tokens by the
 // group's heads, landing as [half][token, head][128 bytes], swizzled by row; zero past the last token.
 bool encode_query_map(CUtensorMap* map, const AttendParams& a) {
@@ -170,6 +184,7 @@ cudaError_t launch_tc_as(const AttendParams& a, const Plan& pl, uint8_t* ws, cud
   p.a = a;
   p.paired = pl.paired;
   p.seg_rows = pl.seg_rows;
+  p.max_segments = static_cast<float>(a.num_seqs) * a.num_kv_heads * ((a.max_q_len * a.group + pl.seg_rows - 1) / pl.seg_rows);
   p.rec_rows = pl.rec_rows;
   p.slots = pl.slots;
   p.counters = reinterpret_cast<int*>(ws);
@@ -177,16 +192,18 @@ cudaError_t launch_tc_as(const AttendParams& a, const Plan& pl, uint8_t* ws, cud
   CUtensorMap tk, tv, tq;
   const int64_t rows = a.num_blocks * a.num_kv_heads * a.block_size;
   auto box = [&](int most) { return a.block_size < most ? a.block_size : most; };
-  if (!encode_tile_map(&tk, a.k_cache, rows, D, box(Tr::KROWS), Tr::NH) ||
-      !encode_tile_map(&tv, a.v_cache, rows, D, box(kTile), Tr::VH) || !encode_query_map(&tq, a))
-    return cudaErrorInvalidValue;
+  const bool maps = Tr::B8 ? encode_code_map(&tk, a.k_cache, rows, D, box(Tr::KROWS), D) &&
+                                 encode_code_map(&tv, a.v_cache, rows, D, box(kTile), D / CG)
+                           : encode_tile_map(&tk, a.k_cache, rows, D, box(Tr::KROWS), Tr::NH) &&
+                                 encode_tile_map(&tv, a.v_cache, rows, D, box(kTile), Tr::VH);
+  if (!maps || !encode_query_map(&tq, a)) return cudaErrorInvalidValue;
   auto kern = attend_tc_kernel<KVT, D, CG, SPLIT>;
   const size_t smem = Tr::smem_bytes(a.num_seqs);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.ctas);
-  cfg.blockDim = dim3(kTcThreads);
+  cfg.blockDim = dim3(Tr::THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -199,21 +216,6 @@ cudaError_t launch_tc_as(const AttendParams& a, const Plan& pl, uint8_t* ws, cud
   cfg.numAttrs = a.pdl ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, tk, tv, tq, p);
   return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-constexpr int kRowWarps = 4;
-
-// One warp per (query, head).
-template <typename KVT, int D>
-__global__ void __launch_bounds__(kRowWarps * 32) attend_rows_kernel(const AttendParams p) {
-  griddep_wait();
-  const int s = blockIdx.y;
-  const SeqView v = seq_view(p, s, blockIdx.x == 0 && threadIdx.x == 0);
-  for (int64_t x = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-       x < static_cast<int64_t>(v.L) * p.num_heads; x += static_cast<int64_t>(gridDim.x) * kRowWarps) {
-    const int h = static_cast<int>(x % p.num_heads), i = static_cast<int>(x / p.num_heads);
-    attend_row<KVT, D>(p, s, v, i, h);
-  }
 }
 
 template <typename KVT, int D, int CG>
@@ -255,14 +257,6 @@ __global__ void __launch_bounds__(kMassThreads) attend_add_mass_kernel(const Att
     if (t + k >= rb.lo && t + k < rb.hi) mass[k] += add[k];
 }
 
-template <typename KVT, int D>
-cudaError_t launch_t(const AttendParams& p, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.max_q_len) * p.num_heads;
-  const int64_t gx = (rows + kRowWarps - 1) / kRowWarps;
-  attend_rows_kernel<KVT, D><<<dim3(static_cast<unsigned>(gx < 4096 ? gx : 4096), p.num_seqs), kRowWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
@@ -296,8 +290,10 @@ int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaS
   if (e != cudaSuccess) return cuda_status(e, "pa_attend counters");
   if (pl.kind == Plan::kFew) {
     e = launch_few(p, pl, ws, stream);
-  } else if (pl.kind == Plan::kRows) {
-    e = p.kv_dtype == PA_FP8_E4M3 ? launch_t<e4m3_t, 128>(p, stream) : launch_t<i8_t, 128>(p, stream);
+  } else if (p.kv_dtype == PA_FP8_E4M3) {
+    e = launch_tc<e4m3_t, 128, 2>(p, pl, ws, stream);
+  } else if (p.kv_dtype == PA_INT8) {
+    e = launch_tc<i8_t, 128, 2>(p, pl, ws, stream);
   } else if (p.kv_dtype == PA_F16) {
     e = p.head_dim == 64 ? launch_tc<f16_t, 64, 1>(p, pl, ws, stream)
         : pl.cg == 1     ? launch_tc<f16_t, 128, 1>(p, pl, ws, stream)

@@ -29,6 +29,13 @@
 // any block size; it is the K-major operand layout of S = Q K^T (row groups
 // NH * 1024 bytes apart) and the MN-major one of P V as it is.
 //
+// 8-bit caches (pairs of CTAs only): the producer brings the codes as they are
+// and four more warps (12-15) widen them to f16 in the operands' layout, exactly
+// (the K scale multiplies the scores, the V scale the output), zero V rows on
+// the way and bring bf16 queries into f16's range: each row is multiplied by the
+// power of two that puts its largest element at 2^14 .. 2^15, its scores by the
+// inverse, as in the decode kernel.
+//
 // Work split.  A segment is (sequence, KV head, row tile).  All segments'
 // position tiles in order, each segment charged kFragCost tiles more for what
 // a fragment costs besides them, are cut into equal contiguous ranges, one per
@@ -60,7 +67,6 @@ constexpr int kTile = 128;      // positions per tile, rows per stream
 constexpr int kHalfTile = kTile / 2;
 constexpr int kFragCost = 1;    // tiles charged per fragment
 constexpr float kSlack = 8.f;   // log2 by which the maximum may lag
-constexpr int kTcThreads = 384;
 
 // ----------------------------------------------------------------- tcgen05 wrappers
 
@@ -290,6 +296,7 @@ struct TcParams {
   AttendParams a;
   int paired;        // the streams are two row tiles (else: one, its position tiles in turn)
   int seg_rows;      // rows of a segment: stream_rows x CTAs of a group x (paired: 2)
+  float max_segments;  // an upper bound
   int rec_rows;      // rows of a record
   int slots;         // records of one stream per CTA: paired 2, alternating 4
   int* counters;     // arrivals: paired: by the segment's first CTA; alternating: by s * H_kv + kvh
@@ -433,6 +440,13 @@ __device__ __forceinline__ int cut_slot_kind(int c, int c0, int U, int nw, int s
 template <typename KVT, int D, int CG>
 struct TcTraits {
   static constexpr bool BF16 = std::is_same<KVT, bf16_t>::value;
+  static constexpr bool B8 = elem<KVT>::bytes == 1;
+  static_assert(!B8 || (CG == 2 && D == 128), "8-bit caches: pairs of CTAs, head_dim 128");
+  static constexpr int THREADS = B8 ? 512 : 384;
+  // The softmax threads hold 64 scores each: registers move to their warps from the others (at launch 65536 / THREADS,
+  // rounded down to a multiple of 8, each).
+  static constexpr int REGS_LOW = B8 ? 72 : 88, REGS_HIGH = B8 ? 184 : 208;
+  static_assert((THREADS - 256) * REGS_LOW + 256 * REGS_HIGH <= THREADS * (65536 / THREADS / 8 * 8), "register split");
   static constexpr int NH = D * 2 / 128;           // 128-byte halves per 16-bit row
   static constexpr int TILE_BYTES = kTile * D * 2;  // a tile of K, V or Q
   // A pair of CTAs halves every K and V tile: each holds 64 of a K tile's positions, and one 128-byte half of all of a
@@ -442,19 +456,26 @@ struct TcTraits {
   static constexpr int VH = NH / CG;               // halves of a V stage
   static constexpr int KGROUP = NH * 1024, VGROUP = VH * 1024;  // bytes of 8 rows
   static constexpr int STAGE = TILE_BYTES / CG;    // bytes of a K or V stage
-  static constexpr int NST = (D == 128 ? 2 : 4) * CG;  // stages of K and of V
+  static constexpr int NST = B8 ? 3 : (D == 128 ? 2 : 4) * CG;  // stages of K and of V
+  // 8-bit caches: stages of codes as they come, [rows][128 / CG bytes] for V
+  static constexpr int NR = B8 ? 2 : 0, RAW = B8 ? STAGE / 2 : 0;
   static constexpr int OFF_Q = 0;                  // two tiles
   static constexpr int OFF_K = 2 * TILE_BYTES;
   static constexpr int OFF_V = OFF_K + NST * STAGE;
-  static constexpr int OFF_BAR = OFF_V + NST * STAGE;
+  static constexpr int OFF_RK = OFF_V + NST * STAGE;
+  static constexpr int OFF_RV = OFF_RK + NR * RAW;
+  static constexpr int OFF_QX = OFF_RV + NR * RAW;  // bf16 queries: 2^-exponent per row, [stream][use & 1][128]
+  static constexpr int OFF_BAR = OFF_QX + (B8 ? 4 * kTile * 4 : 0);
   // barriers (8 bytes each)
   static constexpr int KF = 0, KE = KF + NST, VF = KE + NST, VE = VF + NST, QF = VE + NST, QE = QF + 2, SF = QE + 2,
                        PF = SF + 4, OH = PF + 4, OD = OH + 2, RB = OD + 2,  // SF, PF: per half of a tile; OH, OD: its halves
                        KP = RB + 2, VP = KP + NST, QP = VP + NST,  // the peer's has arrived
-                       VL = QP + 2, NBAR = VL + NST;               // a V tile with rows to be zeroed has arrived
+                       VL = QP + 2,                                // a V tile with rows to be zeroed has arrived
+                       RKF = VL + NST, RKE = RKF + NR, RVF = RKE + NR, RVE = RVF + NR, QL = RVE + NR,  // 8-bit caches
+                       NBAR = QL + 2;
   static constexpr int OFF_MISC = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;  // tmem address, flags, scan scratch
   static constexpr int OFF_FRAG = OFF_MISC + 256;                         // WarpFrag per warp
-  static constexpr int OFF_PREFIX = OFF_FRAG + (12 * static_cast<int>(sizeof(WarpFrag)) + 15) / 16 * 16;
+  static constexpr int OFF_PREFIX = OFF_FRAG + (THREADS / 32 * static_cast<int>(sizeof(WarpFrag)) + 15) / 16 * 16;
   static size_t smem_bytes(int num_seqs) { return 1024 + OFF_PREFIX + static_cast<size_t>(num_seqs + 1) * 4; }
 };
 
@@ -465,71 +486,97 @@ __device__ __forceinline__ float* record_at(const TcParams& p, int cta, int kind
 }
 
 // Joins the contributions of CTA groups c0 .. c1 to rows 32 wq .. 32 wq + 31 of a stream's row tile, in order, and writes the
-// rows out; run by one warp of the contribution that arrived last.  Each lane takes one row's maximum and weights; then
-// kJoin rows at a time, D / 32 columns per lane, with the loads of a record's rows all under way at once (one row at a time the
-// latency of each load showed: 100 us at the end of a 600 us call); more rows would take registers
-// from the main loop.
-constexpr int kJoin = 4;
+// rows out; run by one warp of the contribution that arrived last.  Each lane takes one row's maximum, sum and weights; then
+// kJoin rows at a time, D / 32 columns per lane.  This runs at the end of most CTAs, where nothing hides the latency of its
+// loads (one row and record after the other they took 100 us at the end of a 600 us call): those of kJoin rows of kRecs
+// records are under way at once, which the registers of the softmax warps allow.
+constexpr int kJoin = 4, kRecs = 3;
 template <typename KVT, int D, int CG>
 __device__ __forceinline__ void join_rows(const TcParams& p, const Frag& f, int U, int nw, int c0, int c1, int rank, int t, int wq,
-                                       int row0, int rows, int slot_kind) {
+                                          int row0, int rows, int slot_kind) {
   const AttendParams& a = p.a;
   const int lane = threadIdx.x & 31;
   constexpr int V = D / 32;  // columns per lane
-  auto each_record = [&](auto body) {
-    for (int c = c0; c <= c1; ++c) {
-      const int n = p.paired ? 1 : min(2, tiles_in(c, U, nw, f.seg_start, f.seg_tiles));
-      const int kind = f.whole ? slot_kind : cut_slot_kind(c, c0, U, nw, f.seg_start);
-      for (int x = 0; x < n; ++x) body(record_at<D>(p, c * CG + rank, kind, p.paired ? t : x));
-    }
+  // contribution k: CTA group c0 + k (paired), or c0 + k / 2, stream k % 2 (alternating: the second may be missing)
+  const int total = (c1 - c0 + 1) * (p.paired ? 1 : 2);
+  auto record_of = [&](int k) -> const float* {
+    const int c = c0 + (p.paired ? k : k >> 1);
+    if (k >= total || (!p.paired && (k & 1) >= tiles_in(c, U, nw, f.seg_start, f.seg_tiles))) return nullptr;
+    const int kind = f.whole ? slot_kind : cut_slot_kind(c, c0, U, nw, f.seg_start);
+    return record_at<D>(p, c * CG + rank, kind, p.paired ? t : k & 1);
   };
   const int lr = min(wq * 32 + lane, rows - 1);
+  auto stats_of = [&](const float* rec) {
+    return rec ? __ldcg(reinterpret_cast<const float2*>(rec + p.rec_rows * D + 2 * lr)) : make_float2(-INFINITY, 0.f);
+  };
   float M = -INFINITY, L = 0.f;
-  each_record([&](const float* rec) { M = fmaxf(M, __ldcg(rec + p.rec_rows * D + 2 * lr)); });
-  each_record([&](const float* rec) {
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(rec + p.rec_rows * D + 2 * lr));
+#pragma unroll 4
+  for (int k = 0; k < total; ++k) M = fmaxf(M, stats_of(record_of(k)).x);
+#pragma unroll 4
+  for (int k = 0; k < total; ++k) {
+    const float2 ml = stats_of(record_of(k));
     L = fmaf(ml.x == -INFINITY ? 0.f : exp2f(ml.x - M), ml.y, L);
-  });
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll 1
-  for (int r0 = 0; r0 < 32 && wq * 32 + r0 < rows; r0 += kJoin) {
-    float acc[kJoin][V];
+  }
+  float inv = L > 0.f ? 1.f / L : 0.f;
+  if constexpr (elem<KVT>::bytes == 1) inv *= __ldg(a.v_scale + f.kvh);
+  for (int g = 0; g < total; g += kRecs) {
+    // (more than kRecs records: the rows are gone through again, from the sums so far)
+    const float* rec[kRecs];
+    float w[kRecs];
 #pragma unroll
-    for (int k = 0; k < kJoin; ++k) {
-#pragma unroll
-      for (int q = 0; q < V; ++q) acc[k][q] = 0.f;
+    for (int x = 0; x < kRecs; ++x) {
+      rec[x] = record_of(g + x);
+      const float m = stats_of(rec[x]).x;
+      w[x] = m == -INFINITY ? 0.f : exp2f(m - M);
     }
-    each_record([&](const float* rec) {
-      const float m = __ldcg(rec + p.rec_rows * D + 2 * lr);
-      const float w = m == -INFINITY ? 0.f : exp2f(m - M);
-      const float* const src = rec + static_cast<int64_t>(wq * 32 + r0) * D + lane * V;
-      float o[kJoin][V];
+    float* const sums = record_at<D>(p, c0 * CG + rank, f.whole ? slot_kind : cut_slot_kind(c0, c0, U, nw, f.seg_start),
+                                     p.paired ? t : 0);  // of this warp's rows, in place of the first record's
+    const bool last = g + kRecs >= total;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32 && wq * 32 + r0 < rows; r0 += kJoin) {
+      float o[kRecs][kJoin][V], acc[kJoin][V];
 #pragma unroll
-      for (int k = 0; k < kJoin; ++k) {
-        if (wq * 32 + r0 + k < rows) load_columns<V>(src + k * D, o[k]);
+      for (int x = 0; x < kRecs; ++x) {
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k) {
+          if (rec[x] && wq * 32 + r0 + k < rows) {
+            load_columns<V>(rec[x] + static_cast<int64_t>(wq * 32 + r0 + k) * D + lane * V, o[x][k]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < V; ++q) o[x][k][q] = 0.f;
+          }
+        }
       }
 #pragma unroll
       for (int k = 0; k < kJoin; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, r0 + k);
+        const int row = wq * 32 + r0 + k;
 #pragma unroll
-        for (int q = 0; q < V; ++q) acc[k][q] = fmaf(wk, o[k][q], acc[k][q]);
+        for (int q = 0; q < V; ++q) acc[k][q] = 0.f;
+        if (g > 0 && row < rows) load_columns<V>(sums + static_cast<int64_t>(row) * D + lane * V, acc[k]);
+#pragma unroll
+        for (int x = 0; x < kRecs; ++x) {
+          const float wk = __shfl_sync(0xffffffffu, w[x], r0 + k);
+#pragma unroll
+          for (int q = 0; q < V; ++q) acc[k][q] = fmaf(wk, o[x][k][q], acc[k][q]);
+        }
+        const float ik = __shfl_sync(0xffffffffu, inv, r0 + k), Lk = __shfl_sync(0xffffffffu, L, r0 + k);
+        if (row >= rows) continue;
+        if (!last) {
+#pragma unroll
+          for (int q = 0; q < V; ++q) sums[static_cast<int64_t>(row) * D + lane * V + q] = acc[k][q];
+          continue;
+        }
+        const int i = (row0 + row) / a.group, h = f.kvh * a.group + (row0 + row) - i * a.group;
+        const int64_t o0 = ((static_cast<int64_t>(f.v.row0) + i) * a.num_heads + h) * D + lane * V;
+        bool bad = Lk != Lk;
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          acc[k][q] *= ik;
+          bad |= !(fabsf(acc[k][q]) < INFINITY);
+        }
+        store_columns<V>(a.out, a.out_dtype, o0, acc[k]);
+        if (__any_sync(0xffffffffu, bad)) attend_row_again<KVT, D>(a, f.s, f.v, i, h);
       }
-    });
-#pragma unroll
-    for (int k = 0; k < kJoin; ++k) {
-      const int row = wq * 32 + r0 + k;
-      const float ik = __shfl_sync(0xffffffffu, inv, r0 + k), Lk = __shfl_sync(0xffffffffu, L, r0 + k);
-      if (row >= rows) continue;
-      const int i = (row0 + row) / a.group, h = f.kvh * a.group + (row0 + row) - i * a.group;
-      const int64_t o0 = ((static_cast<int64_t>(f.v.row0) + i) * a.num_heads + h) * D + lane * V;
-      bool bad = Lk != Lk;
-#pragma unroll
-      for (int q = 0; q < V; ++q) {
-        acc[k][q] *= ik;
-        bad |= !(fabsf(acc[k][q]) < INFINITY);
-      }
-      store_columns<V>(a.out, a.out_dtype, o0, acc[k]);
-      if (__any_sync(0xffffffffu, bad)) attend_row_again<KVT, D>(a, f.s, f.v, i, h);
     }
   }
 }
@@ -537,7 +584,7 @@ __device__ __forceinline__ void join_rows(const TcParams& p, const Frag& f, int 
 // ----------------------------------------------------------------- kernel
 
 template <typename KVT, int D, int CG, bool SPLIT>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(TcTraits<KVT, D, CG>::THREADS, 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const __grid_constant__ CUtensorMap tmap_q,
                  const __grid_constant__ TcParams p) {
@@ -554,6 +601,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = a.num_seqs;
   const int rank = CG == 1 ? 0 : static_cast<int>(cluster_rank());  // CTA of its group; the first issues the products
+  const bool q_widen = Tr::B8 && a.q_dtype == PA_BF16;  // bf16 queries become f16
   const int group_id = static_cast<int>(blockIdx.x) / CG, groups = static_cast<int>(gridDim.x) / CG;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   auto wait = [&](int i, uint32_t parity) -> bool {
@@ -573,16 +621,23 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     prefetch_tensormap(&tmap_v);
     prefetch_tensormap(&tmap_q);
     for (int i = 0; i < NST; ++i) {
-      mbar_init(bar(Tr::KF + i), 1);
+      mbar_init(bar(Tr::KF + i), Tr::B8 ? 4 : 1);  // (8-bit caches: the widening warps)
       mbar_init(bar(Tr::KE + i), p.paired ? 2 : 1);  // paired: both streams read every tile
-      mbar_init(bar(Tr::VF + i), 1);
+      mbar_init(bar(Tr::VF + i), Tr::B8 ? 4 : 1);
       mbar_init(bar(Tr::VE + i), p.paired ? 2 : 1);
       mbar_init(bar(Tr::VL + i), 1);
       mbar_init(bar(Tr::KP + i), 1);
       mbar_init(bar(Tr::VP + i), 1);
     }
+    for (int i = 0; i < Tr::NR; ++i) {
+      mbar_init(bar(Tr::RKF + i), 1);
+      mbar_init(bar(Tr::RKE + i), 4);
+      mbar_init(bar(Tr::RVF + i), 1);
+      mbar_init(bar(Tr::RVE + i), 4);
+    }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(Tr::QF + t), 1);
+      mbar_init(bar(Tr::QF + t), q_widen ? 4 : 1);
+      mbar_init(bar(Tr::QL + t), 1);
       mbar_init(bar(Tr::QE + t), 1);
       mbar_init(bar(Tr::SF + t), 1);
       mbar_init(bar(Tr::SF + 2 + t), 1);
@@ -602,9 +657,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   {
     const int rpt = p.seg_rows;
     int carry = 0;
-    constexpr int NW = kTcThreads / 32;
+    constexpr int NW = Tr::THREADS / 32;
     int* const wsum = misc + 8;
-    for (int s0 = 0; s0 < S; s0 += p.paired ? NW : kTcThreads) {
+    for (int s0 = 0; s0 < S; s0 += p.paired ? NW : Tr::THREADS) {
       int cost = 0, s;
       if (p.paired) {  // a warp per sequence, its lanes over the row tiles
         s = s0 + warp;
@@ -663,7 +718,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
   const int U = prefix[S];
   const int want = (U + kFragCost) / (kFragCost + 1);  // at least one tile per CTA
-  const int nw = min(groups, max(want, 1));
+  // A segment cut n ways costs its tiles / n and its join n records of about 1.6 tiles' time: with few segments, fewer CTAs
+  // than there are (n near the root of 0.6 tiles).
+  const int balanced = static_cast<int>(sqrtf(0.6f * static_cast<float>(U) * p.max_segments));
+  const int nw = min(groups, max(min(want, balanced), 1));
   FragIter it;
   it.U = U;
   it.nw = nw;
@@ -703,14 +761,14 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     __syncwarp();
   };
 
-  // The softmax threads hold a row's 128 scores each: registers move to their warps (88 * 128 + 208 * 256 = 168 * 384).
   if (warp < 4) {
-  regs_dec<88>();
+  regs_dec<Tr::REGS_LOW>();
   if (warp == 0) {
     // ================================================================= TMA producer
     // V of a tile, then K of the next: the order in which their stages come free
-    const uint32_t k_box = static_cast<uint32_t>(min(a.block_size, Tr::KROWS) / 8) * Tr::KGROUP;
-    const uint32_t v_box = static_cast<uint32_t>(min(a.block_size, kTile) / 8) * Tr::VGROUP;
+    constexpr int kCode = Tr::B8 ? 2 : 1;  // 8-bit codes take half the bytes
+    const uint32_t k_box = static_cast<uint32_t>(min(a.block_size, Tr::KROWS) / 8) * Tr::KGROUP / kCode;
+    const uint32_t v_box = static_cast<uint32_t>(min(a.block_size, kTile) / 8) * Tr::VGROUP / kCode;
     const int k_boxes = Tr::KROWS / min(a.block_size, Tr::KROWS), v_boxes = kTile / min(a.block_size, kTile);
     const int k_off = rank * Tr::KROWS;  // first position of this CTA's part of a K tile
     int kk = 0, kv = 0;                  // K and V tiles issued
@@ -726,18 +784,25 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       return 0;
     };
     auto issue = [&](bool is_v, int count, int pb, int t0, int boxes, uint32_t box, bool part) -> bool {
-      const int st = count % NST;
-      const uint32_t ph = static_cast<uint32_t>(count / NST) & 1u;
+      constexpr int RING = Tr::B8 ? Tr::NR : NST;
+      const int st = count % RING;
+      const uint32_t ph = static_cast<uint32_t>(count / RING) & 1u;
       const uint32_t bytes = box * static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, pb >= 0)));
-      if (!__all_sync(0xffffffffu, wait((is_v ? Tr::VE : Tr::KE) + st, ph ^ 1u))) return false;
+      const int empty = Tr::B8 ? (is_v ? Tr::RVE : Tr::RKE) : (is_v ? Tr::VE : Tr::KE);
+      if (!__all_sync(0xffffffffu, wait(empty + st, ph ^ 1u))) return false;
       // a V tile with rows to be zeroed is announced by the warp that does so
-      const uint32_t full = bar((is_v ? (part ? Tr::VL : Tr::VF) : Tr::KF) + st);
+      const uint32_t full = bar((Tr::B8 ? (is_v ? Tr::RVF : Tr::RKF) : is_v ? (part ? Tr::VL : Tr::VF) : Tr::KF) + st);
       if (lane == 0) mbar_arrive_expect_tx(full, bytes);
       __syncwarp();
       const int row = boxes > 1 ? 0 : (t0 & (a.block_size - 1));
-      if (pb >= 0)
-        tma_load_4d(base + (is_v ? Tr::OFF_V : Tr::OFF_K) + st * Tr::STAGE + lane * box, is_v ? &tmap_v : &tmap_k, 0, 0,
-                    is_v && CG == 2 ? rank : 0, (pb * a.num_kv_heads + f.kvh) * (a.block_size >> 3) + (row >> 3), full);
+      if (pb >= 0) {
+        if constexpr (Tr::B8)
+          tma_load_2d(base + (is_v ? Tr::OFF_RV : Tr::OFF_RK) + st * Tr::RAW + lane * box, is_v ? &tmap_v : &tmap_k,
+                      is_v ? rank * (D / CG) : 0, (pb * a.num_kv_heads + f.kvh) * a.block_size + row, full);
+        else
+          tma_load_4d(base + (is_v ? Tr::OFF_V : Tr::OFF_K) + st * Tr::STAGE + lane * box, is_v ? &tmap_v : &tmap_k, 0, 0,
+                      is_v && CG == 2 ? rank : 0, (pb * a.num_kv_heads + f.kvh) * (a.block_size >> 3) + (row >> 3), full);
+      }
       return true;
     };
     while (ok && next_frag(wf, prefix, p)) {
@@ -760,6 +825,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       if (nk > 0 && !wait(Tr::KE + i, static_cast<uint32_t>(nk - 1) & 1u)) wait(Tr::KF + i, static_cast<uint32_t>(nk - 1) & 1u);
       if (nv > 0 && !wait(Tr::VE + i, static_cast<uint32_t>(nv - 1) & 1u)) wait(Tr::VF + i, static_cast<uint32_t>(nv - 1) & 1u);
     }
+    for (int i = 0; i < Tr::NR; ++i) {
+      const int nk = kk / (Tr::B8 ? Tr::NR : 1) + (i < kk % (Tr::B8 ? Tr::NR : 1) ? 1 : 0), nv = kv / (Tr::B8 ? Tr::NR : 1) + (i < kv % (Tr::B8 ? Tr::NR : 1) ? 1 : 0);
+      if (nk > 0) wait(Tr::RKF + i, static_cast<uint32_t>(nk - 1) & 1u);
+      if (nv > 0) wait(Tr::RVF + i, static_cast<uint32_t>(nv - 1) & 1u);
+    }
   } else if (warp == 3) {
     // ================================================================= query rows, V rows to be zeroed
     // (rows past the sequence's last are another sequence's, or zero past the last token: their results are not stored)
@@ -779,9 +849,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
         ++uses[t];
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar(Tr::QF + t), bytes);
+          const uint32_t full = bar((q_widen ? Tr::QL : Tr::QF) + t);
+          mbar_arrive_expect_tx(full, bytes);
           tma_load_4d(base + Tr::OFF_Q + t * Tr::TILE_BYTES, &tmap_q, 0, f.kvh * a.group,
-                      f.v.row0 + row_tile(f.m, t) * per_box, 0, bar(Tr::QF + t));
+                      f.v.row0 + row_tile(f.m, t) * per_box, 0, full);
         }
         __syncwarp();
         if (CG == 2 && rank != 0) {
@@ -791,7 +862,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       }
       if (!p.paired) parity ^= n & 1;
       for (int j = f.t0; ok && j < f.t1; ++j, ++kv) {
-        if (!partial(j)) continue;
+        if (Tr::B8 || !partial(j)) continue;
         const int st = kv % NST;
         if (!(ok = wait(Tr::VL + st, (vl >> st) & 1u))) break;
         vl ^= 1u << st;
@@ -801,7 +872,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     }
     for (int t = 0; t < 2; ++t)
       if (uses[t] > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses[t] - 1) & 1u))
-        wait(Tr::QF + t, static_cast<uint32_t>(uses[t] - 1) & 1u);
+        wait((q_widen ? Tr::QL : Tr::QF) + t, static_cast<uint32_t>(uses[t] - 1) & 1u);
   } else if (rank != 0) {
     // ================================================================= the second CTA of a pair: says what has arrived
     // (warp 1: K, warp 2: V)
@@ -895,8 +966,123 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       }
     }
   }
+  } else if (Tr::B8 && warp >= 12) {
+    regs_dec<Tr::REGS_LOW>();
+    // ================================================================= 8-bit caches: codes to f16
+    if constexpr (Tr::B8) {
+      const int tid = static_cast<int>(threadIdx.x) - 384;
+      int kt = 0, parity = 0, uses[2] = {0, 0};
+      bool ok = true;
+      // 16 codes to two 16-byte chunks of f16
+      auto widen16 = [&](const uint4& w, uint32_t zp2, uint4& lo, uint4& hi) {
+        widen4<KVT>(w.x, zp2, lo.x, lo.y);
+        widen4<KVT>(w.y, zp2, lo.z, lo.w);
+        widen4<KVT>(w.z, zp2, hi.x, hi.y);
+        widen4<KVT>(w.w, zp2, hi.z, hi.w);
+      };
+      auto done = [&](int full, int raw_empty) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(full));
+          if (raw_empty >= 0) mbar_arrive(bar(raw_empty));
+        }
+      };
+      const int rps = stream_rows(a.group);
+      while (ok && next_frag(wf, prefix, p)) {
+        uint32_t zk2 = 0u, zv2 = 0u;
+        if constexpr (std::is_same<KVT, i8_t>::value) {
+          const uint32_t zk = __half_as_ushort(__float2half_rn(1152.f + static_cast<float>(__ldg(a.k_zero_point + f.kvh))));
+          const uint32_t zv = __half_as_ushort(__float2half_rn(1152.f + static_cast<float>(__ldg(a.v_zero_point + f.kvh))));
+          zk2 = zk | (zk << 16);
+          zv2 = zv | (zv << 16);
+        }
+        const int n = f.t1 - f.t0;
+        for (int e = 0; ok && q_widen && e < 2; ++e) {
+          const int t = p.paired ? e : e ^ parity;
+          if (!p.paired && n <= e) continue;
+          if (!(ok = wait(Tr::QL + t, static_cast<uint32_t>(uses[t]) & 1u))) break;
+          // one query row per thread: its largest element decides the power of two
+          float* const qx = reinterpret_cast<float*>(sm + Tr::OFF_QX) + (t * 2 + (uses[t] & 1)) * kTile;
+          ++uses[t];
+          if (tid < rps) {
+            auto chunk = [&](int c) -> uint4* {
+              const uint32_t row = static_cast<uint32_t>(c >> 3) * rps * 128 + tid * 128;  // (tiles are 1024-byte aligned)
+              return reinterpret_cast<uint4*>(sm + Tr::OFF_Q + t * Tr::TILE_BYTES + row + (((c & 7) ^ ((row >> 7) & 7)) << 4));
+            };
+            float top = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 w = *chunk(c);
+              const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                top = fmaxf(top, fmaxf(__uint_as_float((r[i] << 16) & 0x7fffffffu), __uint_as_float(r[i] & 0x7fff0000u)));
+            }
+            const int ebits = (__float_as_int(top) >> 23) & 0xff;
+            const int e2 = top > 0.f ? min(100, max(-100, 141 - ebits)) : 0;
+            const float mul = __int_as_float((127 + e2) << 23);
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+              uint4* const at = chunk(c);
+              const uint4 w = *at;
+              const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+              uint32_t h[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 x = widen2<bf16_t>(r[i]);
+                h[i] = pack2<false>(x.x * mul, x.y * mul);
+              }
+              *at = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            qx[tid] = __int_as_float((127 - e2) << 23);
+          }
+          done(Tr::QF + t, -1);
+        }
+        if (!p.paired) parity ^= n & 1;
+        for (int j = f.t0; ok && j < f.t1; ++j, ++kt) {
+          const int st = kt % NST, r = kt % Tr::NR;
+          const uint32_t eph = (static_cast<uint32_t>(kt / NST) & 1u) ^ 1u, rph = static_cast<uint32_t>(kt / Tr::NR) & 1u;
+          constexpr int PER = Tr::RAW / 16 / 128;  // 16-byte chunks of codes per thread
+          {
+            if (!(ok = wait(Tr::RKF + r, rph) && wait(Tr::KE + st, eph))) break;
+            uint4 w[PER];
+#pragma unroll
+            for (int k = 0; k < PER; ++k) w[k] = lds128(base + Tr::OFF_RK + r * Tr::RAW + (k * 128 + tid) * 16);
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+              const int x = k * 128 + tid, row = x >> 3, c = 2 * (x & 7);
+              uint4 lo, hi;
+              widen16(w[k], zk2, lo, hi);
+              uint8_t* const to = sm + Tr::OFF_K + st * Tr::STAGE + (row >> 3) * Tr::KGROUP + (c >> 3) * 1024 + (row & 7) * 128;
+              *reinterpret_cast<uint4*>(to + (((c & 7) ^ (row & 7)) << 4)) = lo;
+              *reinterpret_cast<uint4*>(to + ((((c & 7) + 1) ^ (row & 7)) << 4)) = hi;
+            }
+            done(Tr::KF + st, Tr::RKE + r);
+          }
+          {
+            if (!(ok = wait(Tr::RVF + r, rph) && wait(Tr::VE + st, eph))) break;
+            const int n_hi = f.v.T - j * kTile, n_lo = f.lo - j * kTile;
+            uint4 w[PER];
+#pragma unroll
+            for (int k = 0; k < PER; ++k) w[k] = lds128(base + Tr::OFF_RV + r * Tr::RAW + (k * 128 + tid) * 16);
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+              const int x = k * 128 + tid, row = x >> 2, c = 2 * (x & 3);
+              uint4 lo, hi;
+              widen16(w[k], zv2, lo, hi);
+              if (row >= n_hi || row < n_lo) lo = hi = make_uint4(0u, 0u, 0u, 0u);  // outside the sequence or the window
+              uint8_t* const to = sm + Tr::OFF_V + st * Tr::STAGE + (row >> 3) * Tr::VGROUP + (row & 7) * 128;
+              *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) = lo;
+              *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) << 4)) = hi;
+            }
+            done(Tr::VF + st, Tr::RVE + r);
+          }
+        }
+      }
+    }
   } else {
-    regs_inc<208>();
+    regs_inc<Tr::REGS_HIGH>();
     // ================================================================= softmax, one row per thread
     const int t = (warp - 4) >> 2;
     const int wq = warp & 3;                       // TMEM lanes 32 wq ..
@@ -906,7 +1092,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     // f16 weights carry a factor 2^7 (m is lowered by it), so that weights down to 2^-31 of the largest are normal
     constexpr float kLift = Tr::BF16 ? 0.f : 7.f;
     constexpr float kMost = Tr::BF16 ? 256.f : 32768.f;  // 2^(kLift + kSlack): 64 weights of at most 2^kLift stay below it
-    int jobs = 0, parity = 0;
+    int jobs = 0, parity = 0, q_uses = 0;
 
     // queries at negative positions (more queries than tokens) see nothing
     for (int s = blockIdx.x; s < S; s += gridDim.x) {
@@ -944,8 +1130,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int first = f.v.T - f.v.L;              // tree: position of node 0
       const uint64_t* tree = a.tree_mask ? a.tree_mask + (static_cast<int64_t>(f.v.row0) + qi) * a.tree_words : nullptr;
       const float slope2 = a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
-      const float sc2 = a.scale * kLog2e;
-      const float capk = a.softcap > 0.f ? 2.f * sc2 / a.softcap : 0.f, cap2 = a.softcap * kLog2e;
+      float sc2 = a.scale * kLog2e;
+      if constexpr (Tr::B8) sc2 *= __ldg(a.k_scale + f.kvh);
+      float capk = a.softcap > 0.f ? 2.f * sc2 / a.softcap : 0.f;
+      const float cap2 = a.softcap * kLog2e;
       // (a negative scale would turn the maximum of raw products into a minimum)
       const bool modified = a.softcap > 0.f || a.slopes || !(sc2 >= 0.f);
       float m = -INFINITY, l = 0.f;
@@ -957,6 +1145,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         for (int half = 0; half < 2; ++half) {
           if (!wait(Tr::SF + 2 * half + t, static_cast<uint32_t>(jobs) & 1u)) { ok = false; break; }
           tc_fence_after();
+          if (q_widen && j == j0 && half == 0) {  // the row's power of two (written before its first scores were computed)
+            const float x = reinterpret_cast<const float*>(sm + Tr::OFF_QX)[(t * 2 + (q_uses & 1)) * kTile + wq * 32 + lane];
+            sc2 *= x;
+            capk *= x;
+            ++q_uses;
+          }
           if (warp_on) {
             // positions of the half: 32 from tb, 32 from tb + gap on
             const int tb = j * kTile + half * (CG == 1 ? kHalfTile : 32);
@@ -1085,7 +1279,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int contributions = p.paired ? 1 : min(2, n);
       if (f.whole && contributions == 1) {
         if (warp_on) {
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          float inv = l > 0.f ? 1.f / l : 0.f;
+          if constexpr (Tr::B8) inv *= __ldg(a.v_scale + f.kvh);
           bool bad = l != l;
           const int64_t o0 = ((static_cast<int64_t>(f.v.row0) + qi) * a.num_heads + h) * D;
           const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;

@@ -266,3 +266,31 @@ def test_bad_inputs_are_reported_and_skipped():
     got, err = run_attend(c)
     assert err == pa.PA_DEVERR_BLOCK_ID
     assert torch.all((got[:2] - ref[:2]).abs() <= c.tolerance("f32", ref, wabs)[:2])
+
+
+@pytest.mark.parametrize("kv,q", [("e4m3", "bf16"), ("e4m3", "f16"), ("i8", "bf16"), ("i8", "f16")])
+@pytest.mark.parametrize("qlens,lens", [([30, 17], [30, 200]), ([120, 1], [700, 900]), ([300, 257], [300, 1100])])
+def test_chunks_over_8_bit_caches(kv, q, qlens, lens):
+    """Rows below, at and above those of one pair of CTAs; queries of very different magnitude in one tile."""
+    c = AttendCase(lens, qlens, kv=kv, q=q, heads=8, kv_heads=2, seed=30)
+    c.q_wide[: qlens[0] // 2] *= 2.0 ** -9
+    c.q_wide[3:4] = 0
+    check_attend(c, "f32")
+    check_attend(c, c.qt)
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(3, 1), (10, 2), (48, 1)])
+@pytest.mark.parametrize("kv", ["bf16", "f16", "e4m3"])
+def test_chunk_head_groups(heads, kv_heads, kv):
+    """Groups whose queries do not fill 128 rows: tiles of whole queries."""
+    c = AttendCase([400, 190], [129, 60], heads=heads, kv_heads=kv_heads, kv=kv, seed=31)
+    check_attend(c)
+
+
+def test_few_long_segments_are_cut_and_joined():
+    """One KV head over a long context: a segment in many pieces, joined in order."""
+    c = AttendCase([20000], [40], heads=4, kv_heads=1, seed=32)
+    first, _, _ = check_attend(c)
+    again, _ = run_attend(c)
+    assert torch.equal(first, again)
+    check_attend(AttendCase([20000], [90], heads=4, kv_heads=1, dim=64, kv="f16", seed=33))
