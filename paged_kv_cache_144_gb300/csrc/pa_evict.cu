@@ -82,215 +82,15 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const Commi
     if (at[j] >= 0) *reinterpret_cast<uint4*>(cache + at[j]) = held[j];
 }
 
-// ------------------------------------------------------------------ eviction: selection
-//
-// One CTA per (sequence, KV head), each warp a contiguous part of its
-// positions.  A weight's key is an unsigned integer with the same order (NaN:
-// 0, below minus infinity; minus zero counts as zero).  The key of rank `need`
-// among the middle positions is narrowed down 11 bits at a time by a histogram
-// in shared memory; as soon as the keys that share the leading digits fit the
-// CTA, one per thread, its remaining bits follow from one count over the CTA
-// each (and none are needed when all of those are kept).  Then each warp
-// counts what it keeps, and after one scan over the warps writes its kept
-// positions in order: those above the key, and the first `ties` equal to it.
-// Up to 32768 positions the weights are read once and stay in registers; more
-// are read again (from L2) in each pass.
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelHeld = 32;  // weights a thread holds, or has in flight
-constexpr int kBins = 2048;
-
-__device__ __forceinline__ uint32_t weight_key(float x) {
-  if (x != x) return 0u;
-  const uint32_t u = __float_as_uint(x + 0.f);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
-}
-
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  griddep_launch_dependents();
-  const int kvh = blockIdx.x, s = blockIdx.y;
-  const int cap = a.max_blocks_per_seq << a.block_shift;
-  int T = a.seq_lens[s];
-  if (T < 0 || T > cap) {
-    if (kvh == 0 && threadIdx.x == 0) raise_error(a.err, PA_DEVERR_SEQ_LEN);
-    T = T < 0 ? 0 : cap;
-  }
-  const float* mass = a.mass + s * a.mass_stride_seq + kvh * a.mass_stride_head;
-  int32_t* kept = a.kept + (static_cast<int64_t>(s) * a.num_kv_heads + kvh) * a.budget;
-  float* mass_out = a.mass_out + (static_cast<int64_t>(s) * a.num_kv_heads + kvh) * a.budget;
-  if (kvh == 0 && threadIdx.x == 0) a.new_lens[s] = min(T, a.budget);
-  if (T <= a.budget) {
-    for (int t = threadIdx.x; t < T; t += kSelThreads) {
-      kept[t] = t;
-      mass_out[t] = mass[t];
-    }
-    return;
-  }
-  __shared__ int hist[kBins];
-  __shared__ uint32_t few[kSelThreads];
-  __shared__ int wsum[2][kSelWarps];
-  __shared__ int pick[3], num_few;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int lo = a.sinks, hi = T - a.recent;  // the middle positions
-  int need = a.budget - a.sinks - a.recent;   // < hi - lo
-  const bool any = need > 0;
-  // this warp's positions [w0, w1): a multiple of 32, lane l holding w0 + 32 k + l
-  const int part = ((T + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-  const int w0 = min(T, warp * part), w1 = min(T, w0 + part);
-  const bool held = part <= 32 * kSelHeld;
-  float x[kSelHeld];
-  auto fetch = [&](int t0) {
-#pragma unroll
-    for (int k = 0; k < kSelHeld; ++k) {
-      const int t = t0 + 32 * k + lane;
-      x[k] = t < w1 ? __ldg(mass + t) : 0.f;
-    }
-  };
-  if (held) fetch(w0);
-  // body(k, t) over the warp's positions, weights in x[k]
-  auto each = [&](auto body) {
-    for (int t0 = w0; t0 < w1; t0 += 32 * kSelHeld) {
-      if (!held) fetch(t0);
-#pragma unroll
-      for (int k = 0; k < kSelHeld; ++k)
-        if (t0 + 32 * k < w1) body(k, t0 + 32 * k + lane);
-    }
-  };
-  // the key: everything above `key` is kept, and `ties` of those equal to it
-  uint32_t key = 0u;
-  int ties = 0;
-  if (any) {
-    uint32_t prefix = 0u, mask = 0u;
-    int shift = 21;
-    for (int digit = 0; digit < 3; ++digit) {
-      const uint32_t dmask = digit < 2 ? 0x7ffu : 0x3ffu;
-      for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      each([&](int k, int t) {
-        const uint32_t y = weight_key(x[k]);
-        if (t >= lo && t < hi && (y & mask) == prefix) atomicAdd(&hist[(y >> shift) & dmask], 1);
-      });
-      __syncthreads();
-      // thread i holds bins kBins - 1 - 2 i and the one below: the digit is the first from above that brings the count to need
-      {
-        const int b = kBins - 1 - 2 * static_cast<int>(threadIdx.x);
-        const int c0 = hist[b], c1 = hist[b - 1];
-        int upto = c0 + c1;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += y;
-        }
-        if (lane == 31) wsum[0][warp] = upto;
-        __syncthreads();
-        int w = lane < warp ? wsum[0][lane] : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-        const int before = w + upto - c0 - c1;
-        if (before < need && need <= before + c0 + c1) {
-          const bool first = need <= before + c0;
-          pick[0] = first ? b : b - 1;
-          pick[1] = need - before - (first ? 0 : c0);  // still to be found in the bin
-          pick[2] = first ? c0 : c1;                   // its size
-        }
-        if (threadIdx.x == 0) num_few = 0;
-        __syncthreads();
-      }
-      prefix |= static_cast<uint32_t>(pick[0]) << shift;
-      mask |= dmask << shift;
-      need = pick[1];
-      const int size = pick[2];
-      if (need == size) {  // all of them: everything from prefix on (need < the middle's count, so prefix > 0 here)
-        key = prefix - 1u;
-        ties = 0;
-        break;
-      }
-      if (digit == 2) {
-        key = prefix;
-        ties = need;
-        break;
-      }
-      if (size <= kSelThreads) {
-        each([&](int k, int t) {
-          const uint32_t y = weight_key(x[k]);
-          if (t >= lo && t < hi && (y & mask) == prefix) few[atomicAdd(&num_few, 1)] = y;
-        });
-        __syncthreads();
-        const uint32_t y = static_cast<int>(threadIdx.x) < size ? few[threadIdx.x] : 0u;
-        const bool mine = static_cast<int>(threadIdx.x) < size;
-        // the largest value v of the remaining bits with at least `need` keys >= prefix | v
-        for (int b = shift - 1; b >= 0; --b) {
-          const uint32_t with = prefix | (1u << b);
-          if (__syncthreads_count(mine && y >= with) >= need) prefix = with;
-        }
-        key = prefix;
-        ties = need - __syncthreads_count(mine && y > key);
-        break;
-      }
-      shift = digit == 0 ? 10 : 0;
-    }
-  }
-  auto classify = [&](int t, float v, bool* equal) -> bool {
-    *equal = false;
-    if (t >= w1) return false;
-    if (t < lo || t >= hi) return true;
-    if (!any) return false;
-    const uint32_t y = weight_key(v);
-    *equal = y == key;
-    return y > key;
-  };
-  int sure = 0, equal = 0;
-  each([&](int k, int t) {
-    bool e;
-    const bool y = classify(t, x[k], &e);
-    sure += __popc(__ballot_sync(0xffffffffu, y));
-    equal += __popc(__ballot_sync(0xffffffffu, e));
-  });
-  __syncthreads();  // wsum is free
-  if (lane == 0) {
-    wsum[0][warp] = sure;
-    wsum[1][warp] = equal;
-  }
-  __syncthreads();
-  int s0 = lane < warp ? wsum[0][lane] : 0, e0 = lane < warp ? wsum[1][lane] : 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-    e0 += __shfl_xor_sync(0xffffffffu, e0, o);
-  }
-  const unsigned below = (1u << lane) - 1u;
-  each([&](int k, int t) {
-    bool e;
-    const bool y = classify(t, x[k], &e);
-    const unsigned by = __ballot_sync(0xffffffffu, y), be = __ballot_sync(0xffffffffu, e);
-    const int eq = e0 + __popc(be & below);  // equal ones before this position
-    if (y || (e && eq < ties)) {
-      const int at = s0 + __popc(by & below) + min(eq, ties);
-      kept[at] = t;
-      mass_out[at] = x[k];
-    }
-    s0 += __popc(by);
-    e0 += __popc(be);
-  });
-}
-
 // ------------------------------------------------------------------ eviction: row moves
 //
 // A warp moves 32 rows of K and V: its lanes look up one row's source and
 // destination each (one round trip for all 32), then row_bytes / 16 lanes copy
 // a row 16 bytes each, kMoves of them in flight before the first is stored.
-constexpr int kGatherWarps = 4;
 constexpr int kMoves = 8;
 
-__global__ void __launch_bounds__(kGatherWarps * 32) evict_gather_kernel(const EvictArgs a) {
-  griddep_wait();
-  const int s = blockIdx.z, kvh = blockIdx.y;
-  const int cap = a.max_blocks_per_seq << a.block_shift;
-  const int n = min(max(0, min(a.seq_lens[s], cap)), a.budget);
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int s, int kvh, const int32_t* kept, int i0, int n) {
   const int lane = threadIdx.x & 31;
-  const int i0 = (blockIdx.x * kGatherWarps + (threadIdx.x >> 5)) * 32;
-  if (i0 >= n) return;
-  const int32_t* kept = a.kept + (static_cast<int64_t>(s) * a.num_kv_heads + kvh) * a.budget;
   const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
   const int32_t* dtable = a.dst_tables + static_cast<int64_t>(s) * a.max_dst_blocks;
   int64_t src = -1, dst = -1;
@@ -301,7 +101,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) evict_gather_kernel(const E
                     &dst))
       dst = -1;
   }
-  const int shift = a.row_bytes == 256 ? 4 : 3;  // log2 of the 16-byte chunks of a row
+  const int shift = a.row_bytes == 256 ? 4 : (a.row_bytes == 128 ? 3 : 2);  // log2 of the 16-byte chunks of a row
   const int sub = lane >> shift, c = (lane & ((1 << shift) - 1)) * 16, step = 32 >> shift;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
@@ -324,6 +124,209 @@ __global__ void __launch_bounds__(kGatherWarps * 32) evict_gather_kernel(const E
   }
 }
 
+constexpr int kGatherWarps = 4;
+
+__global__ void __launch_bounds__(kGatherWarps * 32) evict_gather_kernel(const EvictArgs a) {
+  griddep_wait();
+  const int s = blockIdx.z, kvh = blockIdx.y;
+  const int cap = a.max_blocks_per_seq << a.block_shift;
+  const int n = min(max(0, min(a.seq_lens[s], cap)), a.budget);
+  const int i0 = (blockIdx.x * kGatherWarps + (threadIdx.x >> 5)) * 32;
+  if (i0 >= n) return;
+  move_rows(a, s, kvh, a.kept + (static_cast<int64_t>(s) * a.num_kv_heads + kvh) * a.budget, i0, n);
+}
+
+// ------------------------------------------------------------------ eviction: selection
+//
+// One CTA per (sequence, KV head), each warp a contiguous part of its
+// positions.  A weight's key is an unsigned integer with the same order: minus
+// zero counts as zero, NaN (1) stands below minus infinity, the always-kept
+// positions stand above everything, and no position (0) below it.  So the kept
+// positions are those of the `budget` largest keys.  The key of that rank is
+// narrowed down 11 bits at a time by a histogram in shared memory; as soon as
+// the keys that share the leading digits fit the CTA, one per thread, its
+// remaining bits follow from one count over the CTA each (and none are needed
+// when all of those are kept).  Then each warp counts what it keeps, and after
+// one scan over the warps writes its kept positions in order: those above the
+// key, and the first `ties` equal to it.  Up to 32768 positions the keys are
+// made once and stay in registers; beyond, the weights are read again (from L2)
+// in each pass.
+// (Moving few rows in the same CTA instead of a second, overlapping launch was
+// slower: 21.9 against 18 us for 256 rows of 32 pairs.)
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelHeld = 32;  // keys a thread holds, or has in flight
+constexpr int kBins = 2048;
+constexpr uint32_t kAlways = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t weight_key(float x) {
+  if (x != x) return 1u;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+  griddep_launch_dependents();
+  const int kvh = blockIdx.x, s = blockIdx.y;
+  const int cap = a.max_blocks_per_seq << a.block_shift;
+  int T = a.seq_lens[s];
+  if (T < 0 || T > cap) {
+    if (kvh == 0 && threadIdx.x == 0) raise_error(a.err, PA_DEVERR_SEQ_LEN);
+    T = T < 0 ? 0 : cap;
+  }
+  const float* mass = a.mass + s * a.mass_stride_seq + kvh * a.mass_stride_head;
+  int32_t* kept = a.kept + (static_cast<int64_t>(s) * a.num_kv_heads + kvh) * a.budget;
+  float* mass_out = a.mass_out + (static_cast<int64_t>(s) * a.num_kv_heads + kvh) * a.budget;
+  if (kvh == 0 && threadIdx.x == 0) a.new_lens[s] = min(T, a.budget);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (T <= a.budget) {
+    for (int t = threadIdx.x; t < T; t += kSelThreads) {
+      kept[t] = t;
+      mass_out[t] = mass[t];
+    }
+    return;
+  }
+  __shared__ int hist[kBins];
+  __shared__ uint32_t few[kSelThreads];
+  __shared__ int wsum[2][kSelWarps];
+  __shared__ int pick[3], num_few;
+  const int lo = a.sinks, hi = T - a.recent;  // outside: always kept
+  // this warp's positions [w0, w1): a multiple of 32, lane l holding w0 + 32 k + l
+  const int part = ((T + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int w0 = min(T, warp * part), w1 = min(T, w0 + part);
+  const bool held = part <= 32 * kSelHeld;
+  uint32_t y[kSelHeld];
+  auto fetch = [&](int t0) {
+    float x[kSelHeld];
+#pragma unroll
+    for (int k = 0; k < kSelHeld; ++k) {
+      const int t = t0 + 32 * k + lane;
+      x[k] = t < w1 ? __ldg(mass + t) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kSelHeld; ++k) {
+      const int t = t0 + 32 * k + lane;
+      y[k] = t >= w1 ? 0u : (t < lo || t >= hi) ? kAlways : weight_key(x[k]);
+    }
+  };
+  if (held) fetch(w0);
+  // body(key, position of the chunk's first lane) over the warp's positions, a chunk of 32 at a time
+  auto each = [&](auto body) {
+#pragma unroll 1
+    for (int t0 = w0; t0 < w1; t0 += 32 * kSelHeld) {
+      if (!held) fetch(t0);
+#pragma unroll
+      for (int k = 0; k < kSelHeld; ++k)
+        if (t0 + 32 * k < w1) body(y[k], t0 + 32 * k);
+    }
+  };
+  // the key: everything above `key` is kept, and `ties` of those equal to it
+  uint32_t key = 0u, prefix = 0u, mask = 0u;
+  int ties = 0, need = a.budget, shift = 21;
+#pragma unroll 1
+  for (int digit = 0; digit < 3; ++digit) {
+    const uint32_t dmask = digit < 2 ? 0x7ffu : 0x3ffu;
+    for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    each([&](uint32_t v, int) {
+      if ((v & mask) == prefix) atomicAdd(&hist[(v >> shift) & dmask], 1);
+    });
+    __syncthreads();
+    // thread i holds bins kBins - 1 - 2 i and the one below: the digit is the first from above that brings the count to need
+    {
+      const int b = kBins - 1 - 2 * static_cast<int>(threadIdx.x);
+      const int c0 = hist[b], c1 = hist[b - 1];
+      int upto = c0 + c1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      if (lane == 31) wsum[0][warp] = upto;
+      __syncthreads();
+      int w = lane < warp ? wsum[0][lane] : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+      const int before = w + upto - c0 - c1;
+      if (before < need && need <= before + c0 + c1) {
+        const bool first = need <= before + c0;
+        pick[0] = first ? b : b - 1;
+        pick[1] = need - before - (first ? 0 : c0);  // still to be found in the bin
+        pick[2] = first ? c0 : c1;                   // its size
+      }
+      if (threadIdx.x == 0) num_few = 0;
+      __syncthreads();
+    }
+    prefix |= static_cast<uint32_t>(pick[0]) << shift;
+    mask |= dmask << shift;
+    need = pick[1];
+    const int size = pick[2];
+    if (need == size) {  // all of them: everything from prefix on (not all positions are kept, so prefix > 0 here)
+      key = prefix - 1u;
+      ties = 0;
+      break;
+    }
+    if (digit == 2) {
+      key = prefix;
+      ties = need;
+      break;
+    }
+    if (size <= kSelThreads) {
+      each([&](uint32_t v, int) {
+        if ((v & mask) == prefix) {
+          const int at = atomicAdd(&num_few, 1);
+          if (at < kSelThreads) few[at] = v;  // (lanes past the end hold 0 and may add to the lowest bin)
+        }
+      });
+      __syncthreads();
+      const bool mine = static_cast<int>(threadIdx.x) < size;
+      const uint32_t v = mine ? few[threadIdx.x] : 0u;
+      // the largest value of the remaining bits with at least `need` keys from it on
+#pragma unroll 1
+      for (int b = shift - 1; b >= 0; --b) {
+        const uint32_t with = prefix | (1u << b);
+        if (__syncthreads_count(mine && v >= with) >= need) prefix = with;
+      }
+      key = prefix;
+      ties = need - __syncthreads_count(mine && v > key);
+      break;
+    }
+    shift = digit == 0 ? 10 : 0;
+  }
+  int sure = 0, equal = 0;
+  each([&](uint32_t v, int) {
+    sure += __popc(__ballot_sync(0xffffffffu, v > key));
+    equal += __popc(__ballot_sync(0xffffffffu, v == key));
+  });
+  __syncthreads();  // wsum is free
+  if (lane == 0) {
+    wsum[0][warp] = sure;
+    wsum[1][warp] = equal;
+  }
+  __syncthreads();
+  int s0 = lane < warp ? wsum[0][lane] : 0, e0 = lane < warp ? wsum[1][lane] : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+    e0 += __shfl_xor_sync(0xffffffffu, e0, o);
+  }
+  const unsigned below = (1u << lane) - 1u;
+  each([&](uint32_t v, int t0) {
+    const bool above = v > key, same = v == key;
+    const unsigned by = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, same);
+    if (by | be) {
+      const int eq = e0 + __popc(be & below);  // equal ones before this position
+      if (above || (same && eq < ties)) {
+        const int at = s0 + __popc(by & below) + min(eq, ties);
+        kept[at] = t0 + lane;
+        mass_out[at] = __ldg(mass + t0 + lane);
+      }
+      s0 += __popc(by);
+      e0 += __popc(be);
+    }
+  });
+}
+
 }  // namespace
 
 cudaError_t launch_commit_tree(const CommitArgs& a, cudaStream_t stream) {
@@ -334,12 +337,12 @@ cudaError_t launch_commit_tree(const CommitArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   (void)cudaGetLastError();
+  const int cap = a.max_blocks_per_seq << a.block_shift;
+  const int rows = a.budget < cap ? a.budget : cap;
   evict_select_kernel<<<dim3(a.num_kv_heads, a.num_seqs), kSelThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the moves may be set up while the selection runs; they wait for it before they read
-  const int cap = a.max_blocks_per_seq << a.block_shift;
-  const int rows = a.budget < cap ? a.budget : cap;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((rows + kGatherWarps * 32 - 1) / (kGatherWarps * 32), a.num_kv_heads, a.num_seqs);
   cfg.blockDim = dim3(kGatherWarps * 32);
