@@ -462,7 +462,8 @@ int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t 
  *                  again).  Calls that share a workspace must not overlap.
  *
  * Options (struct_size as for pa_decode_options):
- *   softcap        >= 0; 0 = off
+ *   softcap        0 = off, or 2^-10 <= softcap <= 512 (the capped score is off by
+ *                  up to about 2^-21 softcap)
  *   slopes         float32 [num_heads], or NULL
  *   window         >= 0; 0 = off.  Not together with prefix_lens or tree_mask
  *   prefix_lens    int32 [num_seqs], or NULL (values above T count as T)

@@ -7,8 +7,18 @@
 namespace pa {
 namespace {
 
-// Rows (queries x query heads per KV head) up to which the decode kernel's variants serve a call.
+// Which kernel serves a call, by its rows (queries x query heads per KV head) and by the table's positions over all
+// sequences and KV heads.  The decode kernel's variants read the cache once per 16 rows; the tensor-core kernel's time hardly
+// depends on the rows below 128, but has about 50 us of start and joins, and widens 8-bit codes.  Measured, head size 128,
+// lengths of 1/2 to 1 of the table, decode kernel / tensor cores, us:
+//   bf16, 2^20 positions: 32 rows 120 / 153, 48 rows 162 / 156, 64 rows 236 / 157;  2^21: 32 rows 241 / 201, 64 rows 456 / 204
+//   bf16, 2^19 positions: 32 rows 72 / 103, 48 rows 90 / 101, 64 rows 127 / 105;  2^16: 64 rows 27 / 63
+//   e4m3, 2^20 positions: 32 rows 135 / 254, 48 rows 192 / 255, 64 rows 281 / 257;  2^19: 64 rows 134 / 131
 constexpr int kFewRows = 64;
+bool few_rows(int64_t rows, int64_t positions, bool q8) {
+  const int64_t row_groups = (rows + 15) / 16;
+  return rows <= 16 || (rows <= kFewRows && positions <= int64_t{1} << ((q8 ? 23 : 22) - row_groups));
+}
 // Units charged per fragment in their balanced split, as in pa_decode.
 constexpr int kDecodeFragCost = 3;
 
@@ -47,8 +57,9 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
   pl->cg = q8 || (head_dim == 128 && rows > rps) ? 2 : 1;
   pl->paired = rows > static_cast<int64_t>(rps) * pl->cg ? 1 : 0;
   pl->seg_rows = rps * pl->cg * (pl->paired ? 2 : 1);
-  const int few = tuning_override("PA_ATTEND_FEW_ROWS");
-  pl->kind = rows <= (few >= 0 && few <= kFewRows ? few : kFewRows) || accumulate ? Plan::kFew : Plan::kTensor;
+  const int few = tuning_override("PA_ATTEND_FEW_ROWS");  // tuning
+  const int64_t positions = static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq * block_size;
+  pl->kind = accumulate || (few >= 0 ? rows <= few : few_rows(rows, positions, q8)) ? Plan::kFew : Plan::kTensor;
   size_t records = 0, pending = 0;
   pl->num_counters = 0;
   if (pl->kind == Plan::kFew) {
@@ -261,12 +272,14 @@ __global__ void __launch_bounds__(kMassThreads) attend_add_mass_kernel(const Att
 
 size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                               int max_blocks_per_seq, int max_q_len, int kv_dtype, bool accumulate) {
-  // with and without a tree, with either query type: the larger need
+  // with and without a tree, with either query type that the caches take: the largest need
   size_t most = 0;
-  for (int tree = 0; tree < 2; ++tree) {
+  for (int i = 0; i < 4; ++i) {
+    const int q_dtype = i & 1 ? PA_BF16 : PA_F16;
+    if ((kv_dtype == PA_F16 || kv_dtype == PA_BF16) && q_dtype != kv_dtype) continue;
     Plan pl;
-    if (!make_plan(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, max_q_len,
-                   kv_dtype == PA_F16 ? PA_F16 : PA_BF16, kv_dtype, tree != 0, accumulate, &pl))
+    if (!make_plan(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, max_q_len, q_dtype,
+                   kv_dtype, (i & 2) != 0, accumulate, &pl))
       return static_cast<size_t>(-1);
     most = pl.bytes > most ? pl.bytes : most;
   }

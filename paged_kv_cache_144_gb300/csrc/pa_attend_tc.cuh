@@ -9,11 +9,13 @@
 // float32), so O is rarely rescaled.
 //
 // Layout on the SM.  One persistent CTA per SM, 12 warps:
-//   warp 0     TMA producer: K and V tiles of 128 positions, one box per cache
-//              block, into rings of stages
+//   warp 0     TMA producer of the K tiles (128 positions, one box per cache
+//              block) into a ring of stages
 //   warps 1-2  issue the tcgen05.mma of streams 0 and 1 (TMEM, 512 columns: S0,
 //              S1, O0, O1 of 128 lanes x 128 columns; the weights P overwrite S)
-//   warp 3     brings both streams' query rows (TMA), zeroes V rows
+//   warp 3     the same for the V tiles and both streams' query rows; zeroes V
+//              rows where it must (V apart from K: with the streams taking turns
+//              a V stage comes free long after the K stage needed next)
 //   warps 4-7, 8-11   softmax of streams 0 and 1, one row per thread: the row
 //              maximum and sum need no exchange between threads
 // The streams' turns, and the two halves (64 positions) of each stream's tile,
@@ -761,85 +763,86 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     __syncwarp();
   };
 
+  // Boxes of this CTA's part of a K or V tile, and its first position.
+  auto tile_rows = [&](bool is_v) { return is_v ? kTile : Tr::KROWS; };
+  auto tile_start = [&](bool is_v, int j) { return j * kTile + (is_v ? 0 : rank * Tr::KROWS); };
+  // This lane's block of tile j (its table entry), or -1.
+  auto tile_block = [&](bool is_v, int j) -> int {
+    const int boxes = tile_rows(is_v) / min(a.block_size, tile_rows(is_v));
+    const int blk = (tile_start(is_v, j) >> a.block_shift) + (boxes > 1 ? lane : 0);
+    const int nblk = (f.v.T + a.block_size - 1) >> a.block_shift;
+    if (lane >= boxes || blk < (f.lo >> a.block_shift) || blk >= nblk) return -1;
+    const int pb = __ldg(a.block_tables + static_cast<int64_t>(f.s) * a.max_blocks_per_seq + blk);
+    if (pb >= 0 && pb < a.num_blocks) return pb;
+    raise_error(a.err, PA_DEVERR_BLOCK_ID);
+    return 0;
+  };
+  // One tile of K or V: its boxes, one lane each (block pb), into the next stage of the ring (8-bit caches: of codes).
+  auto issue_tile = [&](bool is_v, int count, int j, int pb) -> bool {
+    constexpr int RING = Tr::B8 ? Tr::NR : NST;
+    const int box_rows = min(a.block_size, tile_rows(is_v)), boxes = tile_rows(is_v) / box_rows;
+    const uint32_t box = static_cast<uint32_t>(box_rows / 8) * (is_v ? Tr::VGROUP : Tr::KGROUP) / (Tr::B8 ? 2 : 1);
+    const int t0 = tile_start(is_v, j);
+    const int st = count % RING;
+    const uint32_t ph = static_cast<uint32_t>(count / RING) & 1u;
+    const int empty = Tr::B8 ? (is_v ? Tr::RVE : Tr::RKE) : (is_v ? Tr::VE : Tr::KE);
+    if (!__all_sync(0xffffffffu, wait(empty + st, ph ^ 1u))) return false;
+    const uint32_t bytes = box * static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, pb >= 0)));
+    // a V tile with rows to be zeroed is announced once that is done
+    const uint32_t full = bar((Tr::B8 ? (is_v ? Tr::RVF : Tr::RKF) : is_v ? (partial(j) ? Tr::VL : Tr::VF) : Tr::KF) + st);
+    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+    __syncwarp();
+    const int row = boxes > 1 ? 0 : (t0 & (a.block_size - 1));
+    if (pb >= 0) {
+      if constexpr (Tr::B8)
+        tma_load_2d(base + (is_v ? Tr::OFF_RV : Tr::OFF_RK) + st * Tr::RAW + lane * box, is_v ? &tmap_v : &tmap_k,
+                    is_v ? rank * (D / CG) : 0, (pb * a.num_kv_heads + f.kvh) * a.block_size + row, full);
+      else
+        tma_load_4d(base + (is_v ? Tr::OFF_V : Tr::OFF_K) + st * Tr::STAGE + lane * box, is_v ? &tmap_v : &tmap_k, 0, 0,
+                    is_v && CG == 2 ? rank : 0, (pb * a.num_kv_heads + f.kvh) * (a.block_size >> 3) + (row >> 3), full);
+    }
+    return true;
+  };
+  // Nothing of ours, and no arrival of the tensor cores, may land after the CTA has left: wait until each stage's last tile
+  // has been used (after a wait that ran out, at least until it has arrived).
+  auto drain = [&](bool is_v, int count) {
+    for (int i = 0; i < NST; ++i) {
+      const int n = count / NST + (i < count % NST ? 1 : 0);
+      const uint32_t ph = static_cast<uint32_t>(n - 1) & 1u;
+      if (n > 0 && !wait((is_v ? Tr::VE : Tr::KE) + i, ph)) wait((is_v ? Tr::VF : Tr::KF) + i, ph);
+    }
+    for (int i = 0; i < Tr::NR; ++i) {
+      const int n = count / (Tr::B8 ? Tr::NR : 1) + (i < count % (Tr::B8 ? Tr::NR : 1) ? 1 : 0);
+      if (n > 0) wait((is_v ? Tr::RVF : Tr::RKF) + i, static_cast<uint32_t>(n - 1) & 1u);
+    }
+  };
+
   if (warp < 4) {
   regs_dec<Tr::REGS_LOW>();
   if (warp == 0) {
-    // ================================================================= TMA producer
-    // V of a tile, then K of the next: the order in which their stages come free
-    constexpr int kCode = Tr::B8 ? 2 : 1;  // 8-bit codes take half the bytes
-    const uint32_t k_box = static_cast<uint32_t>(min(a.block_size, Tr::KROWS) / 8) * Tr::KGROUP / kCode;
-    const uint32_t v_box = static_cast<uint32_t>(min(a.block_size, kTile) / 8) * Tr::VGROUP / kCode;
-    const int k_boxes = Tr::KROWS / min(a.block_size, Tr::KROWS), v_boxes = kTile / min(a.block_size, kTile);
-    const int k_off = rank * Tr::KROWS;  // first position of this CTA's part of a K tile
-    int kk = 0, kv = 0;                  // K and V tiles issued
+    // ================================================================= K tiles (TMA)
+    int kt = 0;
     bool ok = true;
-    // this lane's block of the rows from position t0 on (its table entry), or -1
-    auto entry = [&](int t0, int boxes) -> int {
-      const int blk = (t0 >> a.block_shift) + (boxes > 1 ? lane : 0);
-      const int nblk = (f.v.T + a.block_size - 1) >> a.block_shift;
-      if (lane >= boxes || blk < (f.lo >> a.block_shift) || blk >= nblk) return -1;
-      const int pb = __ldg(a.block_tables + static_cast<int64_t>(f.s) * a.max_blocks_per_seq + blk);
-      if (pb >= 0 && pb < a.num_blocks) return pb;
-      raise_error(a.err, PA_DEVERR_BLOCK_ID);
-      return 0;
-    };
-    auto issue = [&](bool is_v, int count, int pb, int t0, int boxes, uint32_t box, bool part) -> bool {
-      constexpr int RING = Tr::B8 ? Tr::NR : NST;
-      const int st = count % RING;
-      const uint32_t ph = static_cast<uint32_t>(count / RING) & 1u;
-      const uint32_t bytes = box * static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, pb >= 0)));
-      const int empty = Tr::B8 ? (is_v ? Tr::RVE : Tr::RKE) : (is_v ? Tr::VE : Tr::KE);
-      if (!__all_sync(0xffffffffu, wait(empty + st, ph ^ 1u))) return false;
-      // a V tile with rows to be zeroed is announced by the warp that does so
-      const uint32_t full = bar((Tr::B8 ? (is_v ? Tr::RVF : Tr::RKF) : is_v ? (part ? Tr::VL : Tr::VF) : Tr::KF) + st);
-      if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-      __syncwarp();
-      const int row = boxes > 1 ? 0 : (t0 & (a.block_size - 1));
-      if (pb >= 0) {
-        if constexpr (Tr::B8)
-          tma_load_2d(base + (is_v ? Tr::OFF_RV : Tr::OFF_RK) + st * Tr::RAW + lane * box, is_v ? &tmap_v : &tmap_k,
-                      is_v ? rank * (D / CG) : 0, (pb * a.num_kv_heads + f.kvh) * a.block_size + row, full);
-        else
-          tma_load_4d(base + (is_v ? Tr::OFF_V : Tr::OFF_K) + st * Tr::STAGE + lane * box, is_v ? &tmap_v : &tmap_k, 0, 0,
-                      is_v && CG == 2 ? rank : 0, (pb * a.num_kv_heads + f.kvh) * (a.block_size >> 3) + (row >> 3), full);
-      }
-      return true;
-    };
     while (ok && next_frag(wf, prefix, p)) {
       const int t1 = f.t1;
-      int kb = entry(f.t0 * kTile + k_off, k_boxes), vb = entry(f.t0 * kTile, v_boxes);
-      if (!(ok = issue(false, kk++, kb, f.t0 * kTile + k_off, k_boxes, k_box, false))) break;
-      for (int j = f.t0; j < t1; ++j) {
-        // table entries a tile ahead of the wait for their stage
-        const int kn = j + 1 < t1 ? entry((j + 1) * kTile + k_off, k_boxes) : -1;
-        const int vn = j + 1 < t1 ? entry((j + 1) * kTile, v_boxes) : -1;
-        if (!(ok = issue(true, kv++, vb, j * kTile, v_boxes, v_box, partial(j)))) break;
-        if (j + 1 < t1 && !(ok = issue(false, kk++, kn, (j + 1) * kTile + k_off, k_boxes, k_box, false))) break;
-        vb = vn;
+      int pb = tile_block(false, f.t0);
+      for (int j = f.t0; ok && j < t1; ++j) {
+        ok = issue_tile(false, kt, j, pb);
+        kt += ok ? 1 : 0;
+        if (j + 1 < t1) pb = tile_block(false, j + 1);  // read while the next stage is waited for
       }
     }
-    // nothing of ours, and no arrival of the tensor cores, may land after the CTA has left: wait until each stage's
-    // last tile has been used (after a wait that ran out, at least until it has arrived)
-    for (int i = 0; i < NST; ++i) {
-      const int nk = kk / NST + (i < kk % NST ? 1 : 0), nv = kv / NST + (i < kv % NST ? 1 : 0);
-      if (nk > 0 && !wait(Tr::KE + i, static_cast<uint32_t>(nk - 1) & 1u)) wait(Tr::KF + i, static_cast<uint32_t>(nk - 1) & 1u);
-      if (nv > 0 && !wait(Tr::VE + i, static_cast<uint32_t>(nv - 1) & 1u)) wait(Tr::VF + i, static_cast<uint32_t>(nv - 1) & 1u);
-    }
-    for (int i = 0; i < Tr::NR; ++i) {
-      const int nk = kk / (Tr::B8 ? Tr::NR : 1) + (i < kk % (Tr::B8 ? Tr::NR : 1) ? 1 : 0), nv = kv / (Tr::B8 ? Tr::NR : 1) + (i < kv % (Tr::B8 ? Tr::NR : 1) ? 1 : 0);
-      if (nk > 0) wait(Tr::RKF + i, static_cast<uint32_t>(nk - 1) & 1u);
-      if (nv > 0) wait(Tr::RVF + i, static_cast<uint32_t>(nv - 1) & 1u);
-    }
+    drain(false, kt);
   } else if (warp == 3) {
-    // ================================================================= query rows, V rows to be zeroed
-    // (rows past the sequence's last are another sequence's, or zero past the last token: their results are not stored)
-    int uses[2] = {0, 0}, parity = 0, kv = 0;
+    // ================================================================= query rows and V tiles (TMA), V rows to be zeroed
+    // (query rows past the sequence's last are another sequence's, or zero past the last token: their results are not stored)
+    int uses[2] = {0, 0}, parity = 0, kt = 0;
     uint32_t vl = 0u;  // phases of VL used, per stage (a bit each)
     const int per_box = kTile / a.group;
     const uint32_t bytes = static_cast<uint32_t>(per_box * a.group) * D * 2;
     bool ok = true;
     while (ok && next_frag(wf, prefix, p)) {
-      const int n = f.t1 - f.t0;
+      const int t1 = f.t1, n = t1 - f.t0;
       for (int e = 0; ok && e < 2; ++e) {
         const int t = p.paired ? e : e ^ parity;  // in the order in which the streams need them
         if (!p.paired && n <= e) continue;
@@ -855,21 +858,36 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                       f.v.row0 + row_tile(f.m, t) * per_box, 0, full);
         }
         __syncwarp();
-        if (CG == 2 && rank != 0) {
-          if (!(ok = wait(Tr::QF + t, static_cast<uint32_t>(uses[t] - 1) & 1u))) break;
-          if (lane == 0) arrive_first_cta(bar(Tr::QP + t));
-        }
+      }
+      // the first V tile is under way before the queries are waited for
+      int j = f.t0, pb = -1;
+      if (ok) {
+        ok = issue_tile(true, kt, j, tile_block(true, j));
+        kt += ok ? 1 : 0;
+        if (j + 1 < t1) pb = tile_block(true, j + 1);
+      }
+      for (int e = 0; ok && CG == 2 && rank != 0 && e < 2; ++e) {
+        const int t = p.paired ? e : e ^ parity;
+        if (!p.paired && n <= e) continue;
+        if (!(ok = wait(Tr::QF + t, static_cast<uint32_t>(uses[t] - 1) & 1u))) break;
+        if (lane == 0) arrive_first_cta(bar(Tr::QP + t));
       }
       if (!p.paired) parity ^= n & 1;
-      for (int j = f.t0; ok && j < f.t1; ++j, ++kv) {
-        if (Tr::B8 || !partial(j)) continue;
-        const int st = kv % NST;
-        if (!(ok = wait(Tr::VL + st, (vl >> st) & 1u))) break;
-        vl ^= 1u << st;
-        clear_v(st, f.v.T - j * kTile, f.lo - j * kTile);
-        if (lane == 0) mbar_arrive(bar(Tr::VF + st));
+      while (ok) {
+        if (!Tr::B8 && partial(j)) {
+          const int st = (kt - 1) % NST;
+          if (!(ok = wait(Tr::VL + st, (vl >> st) & 1u))) break;
+          vl ^= 1u << st;
+          clear_v(st, f.v.T - j * kTile, f.lo - j * kTile);
+          if (lane == 0) mbar_arrive(bar(Tr::VF + st));
+        }
+        if (++j >= t1) break;
+        ok = issue_tile(true, kt, j, pb);
+        kt += ok ? 1 : 0;
+        if (j + 1 < t1) pb = tile_block(true, j + 1);
       }
     }
+    drain(true, kt);
     for (int t = 0; t < 2; ++t)
       if (uses[t] > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses[t] - 1) & 1u))
         wait((q_widen ? Tr::QL : Tr::QF) + t, static_cast<uint32_t>(uses[t] - 1) & 1u);

@@ -155,6 +155,8 @@ PA_EXPORT int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q
                                     max_q_len, kv_dtype);
   if (sh != PA_OK) return sh;
   if (num_tokens < 0 || !(o.softcap >= 0.f) || std::isinf(o.softcap) || o.window < 0) return PA_ERR_SHAPE;
+  // outside these the score's float32 form loses too much: its error is about 2^-21 softcap
+  if (o.softcap > 0.f && (o.softcap < 0x1p-10f || o.softcap > 512.f)) return PA_ERR_UNSUPPORTED;
   if (o.window > 0 && (o.prefix_lens || o.tree_mask)) return PA_ERR_UNSUPPORTED;
   if (o.tree_mask && (o.slopes || o.prefix_lens)) return PA_ERR_UNSUPPORTED;
   if (o.tree_mask && (o.tree_words <= 0 || static_cast<int64_t>(o.tree_words) * 64 < max_q_len)) return PA_ERR_SHAPE;

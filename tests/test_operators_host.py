@@ -115,6 +115,11 @@ def test_attend_option_refusals(lib):
     assert _attend(lib, O(mass=A, mass_stride_seq=256, mass_stride_head=256), mq=1) == pa.PA_ERR_SHAPE
 
 
+def test_attend_softcap_range(lib):
+    for cap in (1e-40, 2.0 ** -11, 513.0, 1e6):
+        assert _attend(lib, pa.AttendOptions(softcap=cap)) == pa.PA_ERR_UNSUPPORTED
+
+
 def test_attend_workspace_refusals(lib):
     def n(**kw):
         a = dict(s=3, hq=8, hk=2, d=128, b=16, mb=16, mq=4, kv=pa.PA_BF16, acc=0)
