@@ -138,24 +138,27 @@ __global__ void __launch_bounds__(kGatherWarps * 32) evict_gather_kernel(const E
 
 // ------------------------------------------------------------------ eviction: selection
 //
-// One CTA per (sequence, KV head), each warp a contiguous part of its
-// positions.  A weight's key is an unsigned integer with the same order: minus
-// zero counts as zero, NaN (1) stands below minus infinity, the always-kept
-// positions stand above everything, and no position (0) below it.  So the kept
-// positions are those of the `budget` largest keys.  The key of that rank is
-// narrowed down 11 bits at a time by a histogram in shared memory; as soon as
-// the keys that share the leading digits fit the CTA, one per thread, its
-// remaining bits follow from one count over the CTA each (and none are needed
-// when all of those are kept).  Then each warp counts what it keeps, and after
-// one scan over the warps writes its kept positions in order: those above the
-// key, and the first `ties` equal to it.  Up to 32768 positions the keys are
-// made once and stay in registers; beyond, the weights are read again (from L2)
-// in each pass.
+// One CTA per (sequence, KV head), or a cluster of them when there are few
+// pairs and many positions; each warp has a contiguous part of the positions.  A weight's key is an unsigned integer with the same order: minus
+// zero counts as zero, NaN (1) stands below minus infinity, and the always-kept
+// positions stand above everything.  So the kept positions are those of the
+// `budget` largest keys.  The key of that rank is narrowed down 11 bits at a
+// time by a histogram in shared memory; as soon as the keys that share the
+// leading digits fit the CTA, one per thread, the other positions are left out
+// of the next digits (and none are needed when all of those are kept).  Then
+// each warp counts what it keeps, and after one scan over the warps writes its
+// kept positions in order: those above the key, and the first `ties` equal to
+// it.  The first kSelHeld positions' keys are made once and stay in shared
+// memory; beyond, the weights are read again (from L2) in each pass.  (Keys in
+// registers took the same passes unrolled 32 times, whose code alone, fetched
+// once per launch, cost microseconds.)
+// CTAs of a cluster exchange their histograms and their warps' counts; all of
+// them find the same key.
 // (Moving few rows in the same CTA instead of a second, overlapping launch was
 // slower: 21.9 against 18 us for 256 rows of 32 pairs.)
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelHeld = 32;  // keys a thread holds, or has in flight
+constexpr int kSelHeld = 48 * 1024;
 constexpr int kBins = 2048;
 constexpr uint32_t kAlways = 0xffffffffu;
 
@@ -165,98 +168,127 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ int2 ld_cluster2(const int* p, uint32_t rank) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
   griddep_launch_dependents();
-  const int kvh = blockIdx.x, s = blockIdx.y;
+  uint32_t rank = 0, ctas = 1;
+  if constexpr (CLUSTER) {
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  }
+  const int kvh = blockIdx.x / ctas, s = blockIdx.y;
   const int cap = a.max_blocks_per_seq << a.block_shift;
   int T = a.seq_lens[s];
   if (T < 0 || T > cap) {
-    if (kvh == 0 && threadIdx.x == 0) raise_error(a.err, PA_DEVERR_SEQ_LEN);
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, PA_DEVERR_SEQ_LEN);
     T = T < 0 ? 0 : cap;
   }
   const float* mass = a.mass + s * a.mass_stride_seq + kvh * a.mass_stride_head;
   int32_t* kept = a.kept + (static_cast<int64_t>(s) * a.num_kv_heads + kvh) * a.budget;
   float* mass_out = a.mass_out + (static_cast<int64_t>(s) * a.num_kv_heads + kvh) * a.budget;
-  if (kvh == 0 && threadIdx.x == 0) a.new_lens[s] = min(T, a.budget);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.new_lens[s] = min(T, a.budget);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (T <= a.budget) {
-    for (int t = threadIdx.x; t < T; t += kSelThreads) {
+    for (int t = rank * kSelThreads + threadIdx.x; t < T; t += ctas * kSelThreads) {
       kept[t] = t;
       mass_out[t] = mass[t];
     }
     return;
   }
-  __shared__ int hist[kBins];
+  extern __shared__ __align__(16) uint32_t keys[];  // of the CTA's first kSelHeld positions
+  __shared__ __align__(16) int hists[CLUSTER ? 3 : 1][kBins];  // (the other CTAs may still read the last digit's)
   __shared__ uint32_t few[kSelThreads];
-  __shared__ int wsum[2][kSelWarps];
+  __shared__ int wsum[kSelWarps];
+  __shared__ int2 counts[kSelWarps];
   __shared__ int pick[3], num_few;
   const int lo = a.sinks, hi = T - a.recent;  // outside: always kept
-  // this warp's positions [w0, w1): a multiple of 32, lane l holding w0 + 32 k + l
-  const int part = ((T + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-  const int w0 = min(T, warp * part), w1 = min(T, w0 + part);
-  const bool held = part <= 32 * kSelHeld;
-  uint32_t y[kSelHeld];
-  auto fetch = [&](int t0) {
-    float x[kSelHeld];
-#pragma unroll
-    for (int k = 0; k < kSelHeld; ++k) {
-      const int t = t0 + 32 * k + lane;
-      x[k] = t < w1 ? __ldg(mass + t) : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < kSelHeld; ++k) {
-      const int t = t0 + 32 * k + lane;
-      y[k] = t >= w1 ? 0u : (t < lo || t >= hi) ? kAlways : weight_key(x[k]);
-    }
-  };
-  if (held) fetch(w0);
-  // body(key, position of the chunk's first lane) over the warp's positions, a chunk of 32 at a time
-  auto each = [&](auto body) {
-#pragma unroll 1
-    for (int t0 = w0; t0 < w1; t0 += 32 * kSelHeld) {
-      if (!held) fetch(t0);
-#pragma unroll
-      for (int k = 0; k < kSelHeld; ++k)
-        if (t0 + 32 * k < w1) body(y[k], t0 + 32 * k);
+  // this warp's positions [w0, w1); lane l takes w0 + 32 k + l
+  const int part = (T + ctas * kSelThreads - 1) / (ctas * kSelThreads) * 32;
+  const int c0 = rank * kSelWarps * part, held = c0 + kSelHeld;
+  const int w0 = min(T, c0 + warp * part), w1 = min(T, w0 + part);
+  for (int t = w0 + lane; t < min(w1, held); t += 32)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(keys + (t - c0))), "l"(mass + t) : "memory");
+  for (int i = threadIdx.x; i < (CLUSTER ? 3 : 1) * kBins; i += kSelThreads) hists[0][i] = 0;
+  if (threadIdx.x == 0) num_few = 0;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  auto sync_all = [&] {  // the CTAs that share the positions
+    if constexpr (CLUSTER) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
     }
   };
+  auto key_of = [&](int t, float x) { return t < lo || t >= hi ? kAlways : weight_key(x); };
+  auto key_at = [&](int t) { return t < held ? keys[t - c0] : key_of(t, __ldg(mass + t)); };
   // the key: everything above `key` is kept, and `ties` of those equal to it
-  uint32_t key = 0u, prefix = 0u, mask = 0u;
-  int ties = 0, need = a.budget, shift = 21;
+  uint32_t key = 0u, prefix = 0u, mask = 0u, own = 0u;
+  int ties = 0, need = a.budget;
+  bool small = false, mine = false;  // the keys that are left are one per thread (its own, if `mine`)
 #pragma unroll 1
   for (int digit = 0; digit < 3; ++digit) {
     const uint32_t dmask = digit < 2 ? 0x7ffu : 0x3ffu;
-    for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    each([&](uint32_t v, int) {
-      if ((v & mask) == prefix) atomicAdd(&hist[(v >> shift) & dmask], 1);
-    });
-    __syncthreads();
-    // thread i holds bins kBins - 1 - 2 i and the one below: the digit is the first from above that brings the count to need
-    {
-      const int b = kBins - 1 - 2 * static_cast<int>(threadIdx.x);
-      const int c0 = hist[b], c1 = hist[b - 1];
-      int upto = c0 + c1;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
+    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+    int* const hist = hists[CLUSTER ? digit : 0];
+    if (digit == 0) {
+#pragma unroll 4
+      for (int t = w0 + lane; t < w1; t += 32) {
+        const uint32_t v = key_of(t, t < held ? __uint_as_float(keys[t - c0]) : __ldg(mass + t));
+        if (t < held) keys[t - c0] = v;
+        atomicAdd(&hist[v >> 21], 1);
       }
-      if (lane == 31) wsum[0][warp] = upto;
-      __syncthreads();
-      int w = lane < warp ? wsum[0][lane] : 0;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-      const int before = w + upto - c0 - c1;
-      if (before < need && need <= before + c0 + c1) {
-        const bool first = need <= before + c0;
-        pick[0] = first ? b : b - 1;
-        pick[1] = need - before - (first ? 0 : c0);  // still to be found in the bin
-        pick[2] = first ? c0 : c1;                   // its size
+    } else if (small) {
+      if (mine && (own & mask) == prefix) atomicAdd(&hist[(own >> shift) & dmask], 1);
+    } else {
+#pragma unroll 4
+      for (int t = w0 + lane; t < w1; t += 32) {
+        const uint32_t v = key_at(t);
+        if ((v & mask) == prefix) atomicAdd(&hist[(v >> shift) & dmask], 1);
       }
-      if (threadIdx.x == 0) num_few = 0;
-      __syncthreads();
     }
+    sync_all();
+    // thread i holds bins kBins - 1 - 2 i and the one below: the digit is the first from above that brings the count to need
+    const int b = kBins - 1 - 2 * static_cast<int>(threadIdx.x);
+    int n0 = hist[b], n1 = hist[b - 1];
+    if constexpr (CLUSTER) {
+      for (uint32_t r = 1; r < ctas; ++r) {
+        const int2 n = ld_cluster2(&hist[b - 1], (rank + r) % ctas);
+        n0 += n.y;
+        n1 += n.x;
+      }
+    } else {
+      hist[b] = hist[b - 1] = 0;
+    }
+    int upto = n0 + n1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) wsum[warp] = upto;
+    __syncthreads();
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0) + upto - n0 - n1;
+    if (before < need && need <= before + n0 + n1) {
+      const bool first = need <= before + n0;
+      pick[0] = first ? b : b - 1;
+      pick[1] = need - before - (first ? 0 : n0);  // still to be found in the bin
+      pick[2] = first ? n0 : n1;                   // its size
+    }
+    __syncthreads();
     prefix |= static_cast<uint32_t>(pick[0]) << shift;
     mask |= dmask << shift;
     need = pick[1];
@@ -271,60 +303,57 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       ties = need;
       break;
     }
-    if (size <= kSelThreads) {
-      each([&](uint32_t v, int) {
-        if ((v & mask) == prefix) {
-          const int at = atomicAdd(&num_few, 1);
-          if (at < kSelThreads) few[at] = v;  // (lanes past the end hold 0 and may add to the lowest bin)
-        }
-      });
-      __syncthreads();
-      const bool mine = static_cast<int>(threadIdx.x) < size;
-      const uint32_t v = mine ? few[threadIdx.x] : 0u;
-      // the largest value of the remaining bits with at least `need` keys from it on
-#pragma unroll 1
-      for (int b = shift - 1; b >= 0; --b) {
-        const uint32_t with = prefix | (1u << b);
-        if (__syncthreads_count(mine && v >= with) >= need) prefix = with;
+    if (!small && size <= kSelThreads) {
+#pragma unroll 4
+      for (int t = w0 + lane; t < w1; t += 32) {
+        const uint32_t v = key_at(t);
+        if ((v & mask) == prefix) few[atomicAdd(&num_few, 1)] = v;
       }
-      key = prefix;
-      ties = need - __syncthreads_count(mine && v > key);
-      break;
+      __syncthreads();
+      small = true;
+      mine = static_cast<int>(threadIdx.x) < num_few;
+      own = mine ? few[threadIdx.x] : 0u;
     }
-    shift = digit == 0 ? 10 : 0;
   }
   int sure = 0, equal = 0;
-  each([&](uint32_t v, int) {
-    sure += __popc(__ballot_sync(0xffffffffu, v > key));
-    equal += __popc(__ballot_sync(0xffffffffu, v == key));
-  });
-  __syncthreads();  // wsum is free
-  if (lane == 0) {
-    wsum[0][warp] = sure;
-    wsum[1][warp] = equal;
+#pragma unroll 4
+  for (int t = w0 + lane; t < w1; t += 32) {
+    const uint32_t v = key_at(t);
+    sure += v > key ? 1 : 0;
+    equal += v == key ? 1 : 0;
   }
-  __syncthreads();
-  int s0 = lane < warp ? wsum[0][lane] : 0, e0 = lane < warp ? wsum[1][lane] : 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-    e0 += __shfl_xor_sync(0xffffffffu, e0, o);
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (lane == 0) counts[warp] = make_int2(sure, equal);
+  sync_all();
+  // what the warps before this one, in its CTA and in those before, keep
+  int2 n = lane < warp ? counts[lane] : make_int2(0, 0);
+  for (uint32_t r = 0; CLUSTER && r < rank; ++r) {
+    const int2 v = ld_cluster2(reinterpret_cast<const int*>(counts + lane), r);
+    n.x += v.x;
+    n.y += v.y;
   }
+  int s0 = __reduce_add_sync(0xffffffffu, n.x), e0 = __reduce_add_sync(0xffffffffu, n.y);
+  if constexpr (CLUSTER) cluster_arrive();  // the others' shared memory has been read
   const unsigned below = (1u << lane) - 1u;
-  each([&](uint32_t v, int t0) {
-    const bool above = v > key, same = v == key;
+#pragma unroll 4
+  for (int t0 = w0; t0 < w1; t0 += 32) {
+    const int t = t0 + lane;
+    const uint32_t v = t < w1 ? key_at(t) : 0u;
+    const bool above = v > key, same = t < w1 && v == key;
     const unsigned by = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, same);
-    if (by | be) {
-      const int eq = e0 + __popc(be & below);  // equal ones before this position
-      if (above || (same && eq < ties)) {
-        const int at = s0 + __popc(by & below) + min(eq, ties);
-        kept[at] = t0 + lane;
-        mass_out[at] = __ldg(mass + t0 + lane);
-      }
-      s0 += __popc(by);
-      e0 += __popc(be);
+    const int eq = e0 + __popc(be & below);  // equal ones before this position
+    if (above || (same && eq < ties)) {
+      const int at = s0 + __popc(by & below) + min(eq, ties);
+      kept[at] = t;
+      // the key gives the weight back, but for the always-kept and NaN
+      mass_out[at] = v == kAlways || v == 1u ? __ldg(mass + t)
+                                             : __uint_as_float(v ^ ((v >> 31) ? 0x80000000u : 0xffffffffu));
     }
-  });
+    s0 += __popc(by);
+    e0 += __popc(be);
+  }
+  if constexpr (CLUSTER) cluster_wait();
 }
 
 }  // namespace
@@ -339,8 +368,33 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   (void)cudaGetLastError();
   const int cap = a.max_blocks_per_seq << a.block_shift;
   const int rows = a.budget < cap ? a.budget : cap;
-  evict_select_kernel<<<dim3(a.num_kv_heads, a.num_seqs), kSelThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // CTAs that share a pair: up to 8192 positions each while the device has SMs for all (a CTA fills one), and as many as
+  // hold all keys.  A cluster costs about 4 us to start, so none up to 16384 positions.  Both kernels in us with clusters
+  // of 1 / 2 / 4 / 8, positions x pairs to kept rows: 32768 x 32 to 4096 57 / 52 / 50 / 65, 32768 x 64 to 4096
+  // 77 / 73 / 77 / 101, 16384 x 32 to 1024 30 / 30 / 31 / 40, 131072 x 8 to 4096 212 / 118 / 46 / 42.
+  const int64_t pairs = static_cast<int64_t>(a.num_kv_heads) * a.num_seqs;
+  int ctas = 1;
+  while (cap > 2 * 8192 && ctas < 8 && ((cap / ctas > 8192 && 2 * ctas * pairs <= sms) || cap / ctas > kSelHeld)) ctas *= 2;
+  const int most = cap / ctas + kSelThreads;  // positions of a CTA
+  auto* const select = ctas > 1 ? evict_select_kernel<true> : evict_select_kernel<false>;
+  e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelHeld * 4);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t sel = {};
+  sel.gridDim = dim3(a.num_kv_heads * ctas, a.num_seqs);
+  sel.blockDim = dim3(kSelThreads);
+  sel.dynamicSmemBytes = (most < kSelHeld ? most : kSelHeld) * sizeof(uint32_t);
+  sel.stream = stream;
+  cudaLaunchAttribute cluster[1];
+  cluster[0].id = cudaLaunchAttributeClusterDimension;
+  cluster[0].val.clusterDim.x = ctas;
+  cluster[0].val.clusterDim.y = cluster[0].val.clusterDim.z = 1;
+  sel.attrs = cluster;
+  sel.numAttrs = ctas > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&sel, select, a);
   if (e != cudaSuccess) return e;
   // the moves may be set up while the selection runs; they wait for it before they read
   cudaLaunchConfig_t cfg = {};

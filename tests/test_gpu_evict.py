@@ -233,3 +233,21 @@ def test_a_serving_run_of_the_operators():
     check_attend(e, spoil=False)
     assert pa.get_device_error() == 0
     run_attend(e)
+
+
+@pytest.mark.parametrize("lens", [[40000, 20001], [300, 100000], [131072 + 5]])
+@pytest.mark.parametrize("weights", ["spread", "few values", "equal"])
+def test_evict_of_many_positions_in_clusters(lens, weights):
+    """Positions shared by several CTAs; ties across their borders."""
+    def mass(S, H, W, g):
+        if weights == "equal":
+            return torch.ones((S, H, W))
+        m = torch.rand((S, H, W), generator=g) ** 6
+        return m if weights == "spread" else (m * 40).floor()
+    _evict(lens, 700, 64, 4, heads=2, dim=64, kv="f16", block=64, seed=21, mass=mass)
+    _evict(lens, 301, 0, 0, heads=2, dim=64, kv="f16", block=64, seed=22, mass=mass)
+
+
+def test_evict_of_many_positions_and_pairs():
+    """More pairs than SMs, and tables longer than what one CTA's shared memory holds."""
+    _evict([60000, 5, 777, 90], 40, 3, 2, heads=44, dim=64, kv="f16", block=1024, seed=23)
