@@ -544,6 +544,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   const int min_share = kMinUnitsPerWarp + (fixed ? 0 : p.frag_cost);
   long long want = (U + min_share - 1) / min_share;
   const int nw_eff = fixed ? nw_total : static_cast<int>(want < 1 ? 1 : (want < nw_total ? want : nw_total));
+  // (pa_attend: a batch of few rings has them on as many SMs)
+  auto ring_gc = [&](int ring) -> int { return ATT ? ring * gridDim.x + blockIdx.x : blockIdx.x * RW + ring; };
   auto start_iter = [&](WorkIter& w, int gc) {
     w.frag_idx = 0;
     w.gw = gc;
@@ -569,7 +571,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     // unit is issued, so that a table read never stalls the warp.
     WorkIter it, ah;  // next unit to issue; next unit whose table entries to fetch
     it.valid = false;
-    if (lane < RW) start_iter(it, blockIdx.x * RW + lane);
+    if (lane < RW) start_iter(it, ring_gc(lane));
     ah = it;
     const uint32_t cbase = base_u32 + (lane < RW ? lane : 0) * wsm;
     const uint32_t ring = table_ring_u32 + (lane < RW ? lane : 0) * 64;  // 4 units x 4 entries
@@ -786,7 +788,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   const int rg = c - ring_id * NC;  // its 16-row group of the segment's rows (several queries)
   if (ring_id >= RW) return;
   WorkIter it;
-  start_iter(it, blockIdx.x * RW + ring_id);
+  start_iter(it, ring_gc(ring_id));
   if (!it.valid) return;
   // Under a programmatic dependent launch this CTA may be resident long
   // before the kernel before it has finished; the bounded waits below start
