@@ -91,7 +91,7 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
   pl->pending = at;
   at += up256(pending);
   pl->stats = at;
-  pl->score_stride = (max_blocks_per_seq * block_size + kTile - 1) / kTile * kTile;
+  pl->score_stride = max_blocks_per_seq * block_size;
   if (accumulate) at += up256(static_cast<size_t>(num_seqs) * num_heads * sizeof(float2));
   pl->scores = at;
   if (accumulate) at += up256(static_cast<size_t>(num_seqs) * num_heads * pl->score_stride * sizeof(float));
@@ -238,36 +238,68 @@ cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaSt
                                              : launch_tc_as<KVT, D, CG, false>(a, pl, ws, stream);
 }
 
-// mass[s][kvh][t] += sum over the group of exp2(score - max) / sum, from the stored scores: four positions per thread (the
-// score rows are 16-byte aligned; the mass rows need not be).
-constexpr int kMassThreads = 128;
+// mass[s][kvh][t] += sum over the group of exp2(score - max) / sum, from the stored scores, whose heads stand side by side:
+// kMassKeys positions per thread, a CTA's threads on consecutive ones.
+constexpr int kMassThreads = 128, kMassKeys = 4;
 __global__ void __launch_bounds__(kMassThreads) attend_add_mass_kernel(const AttendParams p) {
   griddep_wait();
-  const int s = blockIdx.z, kvh = blockIdx.y;
+  const int s = blockIdx.z, kvh = blockIdx.y, G = p.group;
   const SeqView v = seq_view(p, s, false);
   if (v.L != 1) return;
   const RowBounds rb = row_bounds(p, v, seq_prefix(p, s, v.T), 0);
-  const int t = (blockIdx.x * kMassThreads + threadIdx.x) * 4;
-  if (t + 4 <= rb.lo || t >= rb.hi) return;
-  const int64_t row0 = static_cast<int64_t>(s) * p.num_heads + kvh * p.group;
-  const float* const sc = p.scores + row0 * p.score_stride + t;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int g = 0; g < p.group; ++g) {
-    const float2 ml = p.row_stats[row0 + g];
-    const float4 x = *reinterpret_cast<const float4*>(sc + static_cast<int64_t>(g) * p.score_stride);
-    const float inv = __frcp_rn(ml.y);
-    sum.x = fmaf(exp2f(x.x - ml.x), inv, sum.x);
-    sum.y = fmaf(exp2f(x.y - ml.x), inv, sum.y);
-    sum.z = fmaf(exp2f(x.z - ml.x), inv, sum.z);
-    sum.w = fmaf(exp2f(x.w - ml.x), inv, sum.w);
-  }
-  // (scores outside [lo, hi) were not stored: whatever stands there is not used)
-  float* const mass = p.mass + s * p.mass_stride_seq + kvh * p.mass_stride_head + t;
-  const float add[4] = {sum.x, sum.y, sum.z, sum.w};
+  const int t0 = blockIdx.x * kMassThreads * kMassKeys;
+  if (t0 + kMassThreads * kMassKeys <= rb.lo || t0 >= rb.hi) return;
+  const int64_t row0 = static_cast<int64_t>(s) * p.num_heads + kvh * G;
+  const float* const sc = p.scores + (static_cast<int64_t>(s) * p.num_kv_heads + kvh) * p.score_stride * G;
+  float* const mass = p.mass + s * p.mass_stride_seq + kvh * p.mass_stride_head;
+  float sum[kMassKeys] = {}, old[kMassKeys];
+  bool in[kMassKeys];  // (scores outside [lo, hi) were not stored)
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (t + k >= rb.lo && t + k < rb.hi) mass[k] += add[k];
+  for (int k = 0; k < kMassKeys; ++k) {
+    const int t = t0 + k * kMassThreads + threadIdx.x;
+    in[k] = t >= rb.lo && t < rb.hi;
+    old[k] = in[k] ? mass[t] : 0.f;
+  }
+  auto add = [&](int k, float z, float2 ml, float inv) { sum[k] = fmaf(exp2f(z - ml.x), inv, sum[k]); };
+  if ((G & 3) == 0) {
+#pragma unroll 2
+    for (int g = 0; g < G; g += 4) {
+      float4 x[kMassKeys];
+#pragma unroll
+      for (int k = 0; k < kMassKeys; ++k) {
+        const int t = t0 + k * kMassThreads + threadIdx.x;
+        if (in[k]) x[k] = *reinterpret_cast<const float4*>(sc + static_cast<int64_t>(t) * G + g);
+      }
+      float2 ml[4];
+      float inv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ml[i] = p.row_stats[row0 + g + i];
+        inv[i] = __frcp_rn(ml[i].y);
+      }
+#pragma unroll
+      for (int k = 0; k < kMassKeys; ++k) {
+        if (!in[k]) continue;
+        add(k, x[k].x, ml[0], inv[0]);
+        add(k, x[k].y, ml[1], inv[1]);
+        add(k, x[k].z, ml[2], inv[2]);
+        add(k, x[k].w, ml[3], inv[3]);
+      }
+    }
+  } else {
+    for (int g = 0; g < G; ++g) {
+      const float2 ml = p.row_stats[row0 + g];
+      const float inv = __frcp_rn(ml.y);
+#pragma unroll
+      for (int k = 0; k < kMassKeys; ++k) {
+        const int t = t0 + k * kMassThreads + threadIdx.x;
+        if (in[k]) add(k, sc[static_cast<int64_t>(t) * G + g], ml, inv);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kMassKeys; ++k)
+    if (in[k]) mass[t0 + k * kMassThreads + threadIdx.x] = old[k] + sum[k];
 }
 
 }  // namespace
@@ -321,7 +353,7 @@ int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaS
   if (e == cudaSuccess && p.mass) {
     const int cap = p.max_blocks_per_seq << p.block_shift;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((cap + 4 * kMassThreads - 1) / (4 * kMassThreads), p.num_kv_heads, p.num_seqs);
+    cfg.gridDim = dim3((cap + kMassKeys * kMassThreads - 1) / (kMassKeys * kMassThreads), p.num_kv_heads, p.num_seqs);
     cfg.blockDim = dim3(kMassThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -578,6 +578,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     int pst = 0, pph = 1, issued = 0;
     int pf = 0, rs_use = 0, rs_pf = 0;  // units fetched ahead; ring slots to read / fill
     uint64_t wait_since = 0;
+    [[maybe_unused]] uint64_t policy = 0;  // pa_attend: K and V pass through L2 and leave it to the stored scores
+    if constexpr (ATT) {
+      if (p.att.mass) {
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+      } else {
+        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+      }
+    }
     // boxes [first_box, nbox) of a unit hold attended rows: blocks wholly
     // before a sliding window are neither looked up nor loaded
     auto first_box = [&](const WorkIter& w, int bj) {
@@ -653,8 +661,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
             pb = 0;
           }
           const int z = (pb * Hkv + it.kvh) * B + row_in_block;
-          tma_load_3d(kdst + i * BOX * Tr::ROW, &tmap_k, 0, z, 0, bar);
-          tma_load_3d(vdst + i * BOX * Tr::ROW, &tmap_v, 0, z, 0, bar);
+          if constexpr (ATT) {
+            tma_load_3d(kdst + i * BOX * Tr::ROW, &tmap_k, 0, z, 0, bar, policy);
+            tma_load_3d(vdst + i * BOX * Tr::ROW, &tmap_v, 0, z, 0, bar, policy);
+          } else {
+            tma_load_3d(kdst + i * BOX * Tr::ROW, &tmap_k, 0, z, 0, bar);
+            tma_load_3d(vdst + i * BOX * Tr::ROW, &tmap_v, 0, z, 0, bar);
+          }
         }
       }
       if (early) {
@@ -887,6 +900,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   [[maybe_unused]] int qpos[NR];
   [[maybe_unused]] const uint64_t* tree[NR];
   [[maybe_unused]] float* score_row[NR];
+  // stored scores of a segment: [position][query head of the group]
+  [[maybe_unused]] auto segment_scores = [&](int s, int kvh) {
+    return p.att.scores + (static_cast<int64_t>(s) * Hkv + kvh) * p.att.score_stride * G;
+  };
   uint32_t zpk2 = 0u, zpv2 = 0u;  // INT8: f16x2(1152 + zero point) of this KV head
 
   // One unit: S^T = Q K^T, online-softmax update, O^T += V^T P^T.
@@ -950,14 +967,30 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           if constexpr (!FULL) {
             x = (tok < n_valid && tok >= lo_rel) ? x : -INFINITY;
           }
-          if constexpr (ATT) {
-            if (score_row[e & 1] && tok < n_valid && tok >= lo_rel) score_row[e & 1][j * UR + tok] = x;
-          }
           sc[mt][e] = x;
           if (e & 1) {
             mx1 = fmaxf(mx1, x);
           } else {
             mx0 = fmaxf(mx0, x);
+          }
+        }
+      }
+      if constexpr (ATT) {
+        if (score_row[0]) {  // both rows of a position stand side by side
+          float* const at = score_row[0] + static_cast<int64_t>(j) * UR * G;
+#pragma unroll
+          for (int mt = 0; mt < NMT; ++mt) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const int tok = 16 * mt + 4 * e + (k8bit ? sigma(gid) : gid);
+              if (tok >= n_valid || tok < lo_rel) continue;
+              if (score_row[1] && (G & 1) == 0) {
+                *reinterpret_cast<float2*>(at + tok * G) = make_float2(sc[mt][e], sc[mt][e + 1]);
+              } else {
+                at[tok * G] = sc[mt][e];
+                if (score_row[1]) at[tok * G + 1] = sc[mt][e + 1];
+              }
+            }
           }
         }
       }
@@ -1060,7 +1093,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                 if (p.att.softcap > 0.f) x = cap2 - __fdividef(2.f * cap2, 1.f + fast_exp2(sc[nt][2 * h + e] * capk));
                 if (p.att.slopes) x -= slope2[h] * fabsf(static_cast<float>(qpos[h] - (j * UR + tok)));
                 ok = ok && ((bits >> tok) & 1u);
-                if (score_row[h] && ok) score_row[h][j * UR + tok] = x;
+                if (score_row[h] && ok) score_row[h][static_cast<int64_t>(j * UR + tok) * G] = x;
               }
               x = ok ? x : -INFINITY;
             }
@@ -1384,9 +1417,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
             const int head = it.kvh * G + (mine ? (row0 + row) % G : 0);
             slope2[h] = p.att.slopes ? __ldg(p.att.slopes + head) * kLog2e : 0.f;
             tree[h] = p.att.tree_mask && mine ? p.att.tree_mask + (row_base + qi) * p.att.tree_words : nullptr;
-            score_row[h] = p.att.mass && mine
-                               ? p.att.scores + (static_cast<int64_t>(it.s) * p.num_heads + head) * p.att.score_stride
-                               : nullptr;
+            score_row[h] = p.att.mass && mine ? segment_scores(it.s, it.kvh) + (row0 + row) % G : nullptr;
           }
         }
       }
@@ -1399,9 +1430,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         const int head = it.kvh * G + (mine ? row : 0);
         qpos[e] = it.T - 1;
         slope2[e] = p.att.slopes ? __ldg(p.att.slopes + head) * kLog2e : 0.f;
-        score_row[e] = p.att.mass && mine
-                           ? p.att.scores + (static_cast<int64_t>(it.s) * p.num_heads + head) * p.att.score_stride
-                           : nullptr;
+        score_row[e] = p.att.mass && mine ? segment_scores(it.s, it.kvh) + row : nullptr;
       }
     }
     if constexpr (MQ) {

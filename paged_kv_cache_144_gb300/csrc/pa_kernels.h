@@ -98,7 +98,7 @@ struct AttendParams {
   float* mass;
   int64_t mass_stride_seq, mass_stride_head;
   float2* row_stats;  // mass: (max, sum) of each (sequence, head) row, in the scores' log2 domain
-  float* scores;      // mass: the scores [S][H_q][score_stride] of every attended position, log2 domain
+  float* scores;      // mass: the scores [S][H_kv][score_stride][G] of every attended position, log2 domain
   int score_stride;
   unsigned int* err;
   bool pdl;
