@@ -190,7 +190,7 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <bool CLUSTER>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictArgs a) {
   griddep_launch_dependents();
   uint32_t rank = 0, ctas = 1;
   if constexpr (CLUSTER) {
