@@ -33,6 +33,8 @@ enum Mode { kCopy = 0, kToFp8 = 1, kToInt8 = 2 };
 // 16-byte chunks: one pair (or one passed column) per unit, 2-byte accesses.
 enum Layout { kInterleaved = 0, kHalf = 1, kHalfAny = 2 };
 
+// (8192 tokens of 32 + 2 x 8 heads, events around the call: 64 / 128 / 256 / 512 threads 46 / 44 / 49 / 66 us, 1 / 2 / 4 units in
+// flight 44.5 / 44 / 48 us)
 constexpr int kThreads = 128;
 constexpr int kTokens = 2;
 constexpr int kUnroll = 2;           // units whose loads a thread has in flight
