@@ -505,8 +505,9 @@ int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype, in
               void* workspace, size_t workspace_bytes, const pa_attend_options* opt, void* stream);
 
 /* Bytes of workspace pa_attend needs for these sizes on the current device
- * ((size_t)-1 when they are rejected or no device is usable); accumulate
- * nonzero: with the mass option. */
+ * ((size_t)-1 when they are rejected or no device is usable), and for calls
+ * with fewer sequences, queries or blocks per sequence; accumulate nonzero:
+ * with the mass option. */
 size_t pa_attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                                  int max_blocks_per_seq, int max_q_len, pa_dtype kv_dtype, int accumulate);
 

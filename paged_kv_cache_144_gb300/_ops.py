@@ -184,7 +184,7 @@ def rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq,
 
 def attend_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, max_q_len,
                            kv_dtype=_lib.PA_BF16, accumulate=False) -> int:
-    """Workspace of attend / attend_tree / attend_accumulate (accumulate=True) for these sizes on the current device."""
+    """Workspace of attend / attend_tree / attend_accumulate (accumulate=True) for up to these sizes on the current device."""
     n = int(load().pa_attend_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
                                              max_blocks_per_seq, max_q_len, kv_dtype, 1 if accumulate else 0))
     if n == SIZE_MAX:

@@ -61,7 +61,8 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
   pl->seg_rows = rps * pl->cg * (pl->paired ? 2 : 1);
   const int few = tuning_override("PA_ATTEND_FEW_ROWS");  // tuning
   const int64_t positions = static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq * block_size;
-  pl->kind = accumulate || (few >= 0 ? rows <= few : few_rows(rows, positions, q8)) ? Plan::kFew : Plan::kTensor;
+  const bool is_few = rows <= kFewRows && (accumulate || (few >= 0 ? rows <= few : few_rows(rows, positions, q8)));
+  pl->kind = is_few ? Plan::kFew : Plan::kTensor;
   size_t records = 0, pending = 0;
   pl->num_counters = 0;
   if (pl->kind == Plan::kFew) {
@@ -238,11 +239,11 @@ cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaSt
                                              : launch_tc_as<KVT, D, CG, false>(a, pl, ws, stream);
 }
 
-// A weight is known only when its row's last position has been seen, so the attention stores the scores and this kernel follows.
+// mass[s][kvh][t] += sum over the group of exp2(score - max) / sum, from the stored scores, whose heads stand side by side:
+// kMassKeys positions per thread, a CTA's threads on consecutive ones.  (A weight is known only when its row's last position
+// has been seen, so the attention stores the scores and this kernel follows.)
 // What bounds it: memory and L2 traffic, 4 G + 8 bytes per position and KV head.  8 heads of 32 x up to 4096 positions, G = 4:
 // 5.5 us; of 8 x 32768, G = 8: 16 us (84 MB, 5.2 TB/s).
-// mass[s][kvh][t] += sum over the group of exp2(score - max) / sum, from the stored scores, whose heads stand side by side:
-// kMassKeys positions per thread, a CTA's threads on consecutive ones.
 constexpr int kMassThreads = 128, kMassKeys = 4;
 __global__ void __launch_bounds__(kMassThreads) attend_add_mass_kernel(const AttendParams p) {
   griddep_wait();
@@ -309,16 +310,24 @@ __global__ void __launch_bounds__(kMassThreads) attend_add_mass_kernel(const Att
 
 size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                               int max_blocks_per_seq, int max_q_len, int kv_dtype, bool accumulate) {
-  // with and without a tree, with either query type that the caches take: the largest need
+  // The largest need with and without a tree, with either query type that the caches take, and of calls with fewer
+  // sequences, queries or blocks: one sequence and one block leave the most room for other parts (they are cut down for the
+  // batch's arrays), and the records' size changes where the rows fill another 16 up to 64, a stream or a pair.
+  const int group = num_heads / num_kv_heads, per_stream = stream_rows(group) / group;
+  const int lens[] = {1,          16 / group, 17 / group + 1,  32 / group,     33 / group + 1,     48 / group, 49 / group + 1,
+                      64 / group, 64 / group + 1, per_stream, per_stream + 1, 2 * per_stream, max_q_len};
   size_t most = 0;
-  for (int i = 0; i < 4; ++i) {
-    const int q_dtype = i & 1 ? PA_BF16 : PA_F16;
+  for (int i = 0; i < 16; ++i) {
+    const int q_dtype = i & 1 ? PA_BF16 : PA_F16, seqs = i & 2 ? 1 : num_seqs, blocks = i & 4 ? 1 : max_blocks_per_seq;
     if ((kv_dtype == PA_F16 || kv_dtype == PA_BF16) && q_dtype != kv_dtype) continue;
-    Plan pl;
-    if (!make_plan(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, max_q_len, q_dtype,
-                   kv_dtype, (i & 2) != 0, accumulate, &pl))
-      return static_cast<size_t>(-1);
-    most = pl.bytes > most ? pl.bytes : most;
+    for (const int len : lens) {
+      if (len < 1 || len > max_q_len) continue;
+      Plan pl;
+      if (!make_plan(seqs, num_heads, num_kv_heads, head_dim, block_size, blocks, len, q_dtype, kv_dtype, (i & 8) != 0,
+                     accumulate, &pl))
+        return static_cast<size_t>(-1);
+      most = pl.bytes > most ? pl.bytes : most;
+    }
   }
   return most;
 }
@@ -336,7 +345,10 @@ int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaS
   p.scores = reinterpret_cast<float*>(ws + pl.scores);
   p.score_stride = pl.score_stride;
   cudaError_t e = cudaSuccess;
-  if (pl.num_counters > kCounters) e = cudaMemsetAsync(ws, 0, pl.num_counters * sizeof(int), stream);
+  if (pl.num_counters > kCounters) {
+    e = cudaMemsetAsync(ws, 0, pl.num_counters * sizeof(int), stream);
+    p.pdl = false;  // the kernel before this one is no longer the stream's last work
+  }
   if (e != cudaSuccess) return cuda_status(e, "pa_attend counters");
   if (pl.kind == Plan::kFew) {
     e = launch_few(p, pl, ws, stream);

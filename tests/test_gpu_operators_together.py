@@ -323,3 +323,68 @@ def test_graph_of_no_sequences_and_empty_batches():
     pa.evict(k, k.clone(), torch.empty((0, 2, 48), device="cuda"), tables, none, tables.clone(),
              torch.empty((0, 2, 4), dtype=torch.int32, device="cuda"), torch.empty((0, 2, 4), device="cuda"), none.clone(), 16, budget=4)
     assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kv,q,dim,heads,kv_heads", [("bf16", "bf16", 128, 8, 2), ("f16", "f16", 64, 6, 2),
+                                                     ("e4m3", "bf16", 128, 40, 8), ("i8", "f16", 128, 64, 1)])
+def test_a_workspace_serves_smaller_calls(kv, q, dim, heads, kv_heads):
+    """Bytes for up to 50 sequences, 150 queries and 20 000 positions are enough for every smaller call."""
+    code = {"bf16": pa.PA_BF16, "f16": pa.PA_F16, "e4m3": pa.PA_FP8_E4M3, "i8": pa.PA_INT8}[kv]
+    for acc in (False, True):
+        most = pa.attend_workspace_bytes(50, heads, kv_heads, dim, 16, 1250, 1 if acc else 150, code, accumulate=acc)
+        for seqs in (1, 2, 7, 33, 50):
+            for blocks in (1, 9, 64, 500, 1250):
+                for L in ((1,) if acc else (1, 2, 3, 4, 5, 6, 7, 8, 12, 16, 17, 21, 32, 33, 64, 65, 100, 128, 129, 150)):
+                    n = pa.attend_workspace_bytes(seqs, heads, kv_heads, dim, 16, blocks, L, code, accumulate=acc)
+                    assert n <= most, (acc, seqs, blocks, L)
+    ws = pa.new_workspace(pa.attend_workspace_bytes(50, heads, kv_heads, dim, 16, 1250, 150, code), "cuda")
+    for seqs, L in ((1, 1), (3, 2), (2, 10), (2, 30), (1, 140)):
+        c = AttendCase([200 + 31 * i for i in range(seqs)], [L] * seqs, kv=kv, q=q, dim=dim, heads=heads, kv_heads=kv_heads,
+                       seed=19 + L)
+        check_attend(c, workspace=ws)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("qlens", [[1, 1], [3, 1], [40, 130]])
+def test_positions_before_a_window_may_hold_anything(kv, qlens):
+    c = AttendCase([170, 300], qlens, kv=kv, seed=20)
+    c.window = 37
+    for s, (t, n) in enumerate(zip(c.lens, qlens)):
+        for pos in range(0, t - n + 1 - 37):               # seen by no query
+            b, o = c.row_of(s, pos)
+            for x in (c.k, c.v):
+                row = torch.full((c.kv_heads, c.dim), float("nan")).to(x.dtype)
+                x.view(torch.uint8)[b, :, o] = row.view(torch.uint8).view(c.kv_heads, -1)
+    c.spoil_tails()
+    clean = AttendCase([170, 300], qlens, kv=kv, seed=20)  # the same numbers, unspoiled
+    clean.window = 37
+    ref, wabs, m = clean.reference()
+    n = sum(qlens)
+    got, err = run_attend(c)
+    assert err == 0
+    assert torch.all((got - ref).abs()[:n] <= c.tolerance("f32", ref, wabs)[:n])
+    if max(qlens) == 1:
+        mass = torch.zeros((2, c.kv_heads, c.tables.shape[1] * c.block), device="cuda")
+        got, err = run_attend(c, mass=mass)
+        assert err == 0
+        assert torch.all((got - ref).abs()[:n] <= c.tolerance("f32", ref, wabs)[:n])
+        assert torch.all((mass.cpu().double() - m).abs() <= 3e-4 * m + 2.0 ** -24)
+
+
+def test_a_captured_call_with_more_counters_than_the_fixed_area():
+    S, H, B, D = 2200, 32, 8, 64
+    g = torch.Generator(device="cuda").manual_seed(21)
+    k, v = (torch.randn((S, H, B, D), generator=g, device="cuda").half() for _ in range(2))
+    tables = torch.randperm(S, generator=g, device="cuda").to(torch.int32).view(S, 1)
+    lens = torch.randint(1, 9, (S,), generator=g, device="cuda", dtype=torch.int32)
+    q = torch.randn((S, H, D), generator=g, device="cuda").half()
+    want, out = torch.zeros((S, H, D), device="cuda"), torch.zeros((S, H, D), device="cuda")
+    ws = pa.new_workspace(pa.attend_workspace_bytes(S, H, H, D, B, 1, 1, pa.PA_F16), "cuda")
+    pa.attend(want, q, k, v, tables, lens, None, 1, H, 0.125, B, workspace=ws)
+    graph = pa.StepGraph(lambda: pa.attend(out, q, k, v, tables, lens, None, 1, H, 0.125, B, workspace=ws, pdl=True))
+    out.zero_()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert pa.get_device_error() == 0
+    assert torch.equal(out, want)
