@@ -447,7 +447,8 @@ int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t 
  * q_starts[0], are left as they were.
  *
  *   out            [num_tokens][num_heads][head_dim], out_dtype F32/F16/BF16,
- *                  16-byte aligned
+ *                  16-byte aligned, not overlapping q (rows are read by
+ *                  several CTAs)
  *   q              the same at q_stride elements per token, q_dtype F16/BF16
  *   caches, scales, block_tables, seq_lens     as pa_decode
  *   q_starts       int32 [num_seqs + 1]; NULL: one query per sequence, row s
@@ -550,7 +551,7 @@ int pa_commit_tree(void* k_cache, void* v_cache, pa_dtype kv_dtype, int64_t num_
  *                  min(budget, max_blocks_per_seq*block_size); entries beyond
  *                  ceil(new_lens[s] / block_size) are not read
  *   kept           int32 [num_seqs][num_kv_heads][budget]
- *   mass_out       float32 [num_seqs][num_kv_heads][budget]
+ *   mass_out       float32 [num_seqs][num_kv_heads][budget], not overlapping mass
  *   new_lens       int32 [num_seqs] (not seq_lens itself)
  *   budget >= 1, recent >= 0, sinks >= 0, recent + sinks <= budget
  */

@@ -205,6 +205,8 @@ def _attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_le
         raise ValueError("the caches must have q's head size and num_kv_heads heads")
     if out.shape != q.shape or not out.is_contiguous():
         raise ValueError(f"out must be contiguous of shape {tuple(q.shape)}")
+    if out.data_ptr() == q.data_ptr() and N:
+        raise ValueError("out must not be q: its rows are read by several CTAs")
     S = seq_lens.shape[0]
     width = _table("block_tables", block_tables, S, _I32)
     _need("seq_lens", seq_lens, _I32, (S,))

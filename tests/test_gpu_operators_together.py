@@ -388,3 +388,9 @@ def test_a_captured_call_with_more_counters_than_the_fixed_area():
     torch.cuda.synchronize()
     assert pa.get_device_error() == 0
     assert torch.equal(out, want)
+
+
+def test_out_may_not_be_q():
+    x = OnGpu(AttendCase([5, 9], [1, 1], pad_rows=0))
+    with pytest.raises(ValueError, match="out must not be q"):
+        pa.attend(x.q, x.q, x.k, x.v, x.tables, x.lens, x.starts, 1, 2, 0.1, 16, workspace=x.ws)
