@@ -394,3 +394,40 @@ def test_out_may_not_be_q():
     x = OnGpu(AttendCase([5, 9], [1, 1], pad_rows=0))
     with pytest.raises(ValueError, match="out must not be q"):
         pa.attend(x.q, x.q, x.k, x.v, x.tables, x.lens, x.starts, 1, 2, 0.1, 16, workspace=x.ws)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("most,group", [(100, 1), (100, 2), (300, 2)])
+def test_most_sequences_on_the_tensor_cores(kv, most, group):
+    """4096 sequences of 0 to 8 tokens, up to 8 of them queries, in a call that allows for many more queries."""
+    S, H, B, D = 4096, 2, 8, 128
+    g = torch.Generator(device="cuda").manual_seed(23)
+    dt = {"bf16": torch.bfloat16, "f16": torch.float16, "e4m3": torch.float8_e4m3fn}[kv]
+    qt = torch.float16 if kv == "f16" else torch.bfloat16
+    k, v = (torch.randn((S + 5, H, B, D), generator=g, device="cuda").to(dt) for _ in range(2))
+    tables = torch.randperm(S + 5, generator=g, device="cuda")[:S].to(torch.int32).view(S, 1)
+    lens = torch.randint(0, 9, (S,), generator=g, device="cuda", dtype=torch.int32)
+    qlens = torch.minimum(lens, torch.randint(0, 9, (S,), generator=g, device="cuda", dtype=torch.int32))
+    starts = torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+    starts[1:] = qlens.cumsum(0)
+    n = int(starts[-1])
+    q = torch.randn((n, H * group, D), generator=g, device="cuda").to(qt)
+    out = torch.full((n + 1, H * group, D), 7.0, device="cuda")
+    scale = torch.tensor([0.8, 1.1], device="cuda") if kv == "e4m3" else None
+    q_all = torch.cat([q, q[:1]])
+    ws = pa.new_workspace(pa.attend_workspace_bytes(S, H * group, H, D, B, 1, most, pa.dtype_code(k)), "cuda")
+    for _ in range(2):
+        pa.attend(out, q_all, k, v, tables, lens, starts, most, H, 0.09, B, workspace=ws, k_scale=scale, v_scale=scale)
+    assert pa.get_device_error() == 0
+    assert torch.all(out[n] == 7.0)
+    seq = torch.repeat_interleave(torch.arange(S, device="cuda"), qlens.long())
+    pos = (lens - qlens).long()[seq] + torch.arange(n, device="cuda") - starts.long()[seq]
+    K, V = (x[tables[:, 0].long()].double() * (1.0 if scale is None else scale.double()[None, :, None, None]) for x in (k, v))
+    K, V = (x[seq].repeat_interleave(group, 1) for x in (K, V))
+    z = torch.einsum("nhd,nhtd->nht", q.double(), K) * 0.09
+    z = z.masked_fill(torch.arange(B, device="cuda") > pos[:, None, None], -float("inf"))
+    p = torch.softmax(z, 2)
+    ref, wabs = torch.einsum("nht,nhtd->nhd", p, V), torch.einsum("nht,nhtd->nhd", p, V.abs())
+    c = AttendCase([1], [1], kv=kv)
+    c.q = q
+    assert torch.all((out[:n].double() - ref).abs() <= c.tolerance("f32", ref, wabs))
