@@ -1,5 +1,7 @@
 // pa_evict.cu - row moves inside the paged cache: the commit of a drafted
 // tree's accepted path, and the eviction by accumulated attention weight.
+#include <type_traits>
+
 #include "pa_common.cuh"
 #include "pa_ops.h"
 
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) evict_gather_kernel(const E
 // What bounds it: the chain of passes and barriers in few CTAs.  4 x 8 pairs of
 // 4096 positions: 6.0 us (9200 cycles: reading the length and the weights 3600,
 // digits 3900, counting and writing 1600); 8 x 8 pairs of 32768 positions: 24 us
-// in one CTA each, 19 us in two.
+// in one CTA each, 18 us in two.
 // CTAs of a cluster exchange their histograms and their warps' counts; all of
 // them find the same key.
 // (Moving few rows in the same CTA instead of a second, overlapping launch was
@@ -242,7 +244,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     }
   };
   auto key_of = [&](int t, float x) { return t < lo || t >= hi ? kAlways : weight_key(x); };
-  auto key_at = [&](int t) { return t < held ? keys[t - c0] : key_of(t, __ldg(mass + t)); };
+  // body(position, key) over the warp's positions; made: the keys stand in shared memory
+  auto each = [&](auto made, auto body) {
+    const int in_shared = min(w1, held);
+    uint32_t* const at = keys - c0;
+#pragma unroll 8
+    for (int t = w0 + lane; t < in_shared; t += 32) {
+      if constexpr (decltype(made)::value) {
+        body(t, at[t]);
+      } else {
+        const uint32_t v = key_of(t, __uint_as_float(at[t]));
+        at[t] = v;
+        body(t, v);
+      }
+    }
+#pragma unroll 1
+    for (int t = max(w0, held) + lane; t < w1; t += 32) body(t, key_of(t, __ldg(mass + t)));
+  };
   // the key: everything above `key` is kept, and `ties` of those equal to it
   uint32_t key = 0u, prefix = 0u, mask = 0u, own = 0u;
   int ties = 0, need = a.budget;
@@ -253,20 +271,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
     int* const hist = hists[CLUSTER ? digit : 0];
     if (digit == 0) {
-#pragma unroll 4
-      for (int t = w0 + lane; t < w1; t += 32) {
-        const uint32_t v = key_of(t, t < held ? __uint_as_float(keys[t - c0]) : __ldg(mass + t));
-        if (t < held) keys[t - c0] = v;
-        atomicAdd(&hist[v >> 21], 1);
-      }
+      each(std::false_type(), [&](int, uint32_t v) { atomicAdd(&hist[v >> 21], 1); });
     } else if (small) {
       if (mine && (own & mask) == prefix) atomicAdd(&hist[(own >> shift) & dmask], 1);
     } else {
-#pragma unroll 4
-      for (int t = w0 + lane; t < w1; t += 32) {
-        const uint32_t v = key_at(t);
+      each(std::true_type(), [&](int, uint32_t v) {
         if ((v & mask) == prefix) atomicAdd(&hist[(v >> shift) & dmask], 1);
-      }
+      });
     }
     sync_all();
     // thread i holds bins kBins - 1 - 2 i and the one below: the digit is the first from above that brings the count to need
@@ -312,11 +323,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
       break;
     }
     if (!small && size <= kSelThreads) {
-#pragma unroll 4
-      for (int t = w0 + lane; t < w1; t += 32) {
-        const uint32_t v = key_at(t);
+      each(std::true_type(), [&](int, uint32_t v) {
         if ((v & mask) == prefix) few[atomicAdd(&num_few, 1)] = v;
-      }
+      });
       __syncthreads();
       small = true;
       mine = static_cast<int>(threadIdx.x) < num_few;
@@ -324,12 +333,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     }
   }
   int sure = 0, equal = 0;
-#pragma unroll 4
-  for (int t = w0 + lane; t < w1; t += 32) {
-    const uint32_t v = key_at(t);
+  each(std::true_type(), [&](int, uint32_t v) {
     sure += v > key ? 1 : 0;
     equal += v == key ? 1 : 0;
-  }
+  });
   sure = __reduce_add_sync(0xffffffffu, sure);
   equal = __reduce_add_sync(0xffffffffu, equal);
   if (lane == 0) counts[warp] = make_int2(sure, equal);
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 #pragma unroll 4
   for (int t0 = w0; t0 < w1; t0 += 32) {
     const int t = t0 + lane;
-    const uint32_t v = t < w1 ? key_at(t) : 0u;
+    const uint32_t v = t >= w1 ? 0u : t < held ? keys[t - c0] : key_of(t, __ldg(mass + t));
     const bool above = v > key, same = t < w1 && v == key;
     const unsigned by = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, same);
     const int eq = e0 + __popc(be & below);  // equal ones before this position
