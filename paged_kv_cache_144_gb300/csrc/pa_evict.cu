@@ -145,27 +145,31 @@ __global__ void __launch_bounds__(kGatherWarps * 32) evict_gather_kernel(const E
 // ------------------------------------------------------------------ eviction: selection
 //
 // One CTA per (sequence, KV head), or a cluster of them when there are few
-// pairs and many positions; each warp has a contiguous part of the positions.  A weight's key is an unsigned integer with the same order: minus
-// zero counts as zero, NaN (1) stands below minus infinity, and the always-kept
-// positions stand above everything.  So the kept positions are those of the
-// `budget` largest keys.  The key of that rank is narrowed down 11 bits at a
-// time by a histogram in shared memory; as soon as the keys that share the
-// leading digits fit the CTA, one per thread, the other positions are left out
-// of the next digits (and none are needed when all of those are kept).  Then
-// each warp counts what it keeps, and after one scan over the warps writes its
-// kept positions in order: those above the key, and the first `ties` equal to
-// it.  The first kSelHeld positions' keys are made once and stay in shared
+// pairs and many positions; each warp has a contiguous part of the positions.
+// A weight's key is an unsigned integer with the same order: minus zero counts
+// as zero, NaN (1) stands below minus infinity, and the always-kept positions
+// stand above everything.  So the kept positions are those of the `budget`
+// largest keys.  The key of that rank is narrowed down 11 bits at a time by a
+// histogram in shared memory; as soon as the keys that share the leading digits
+// fit the CTA, one per thread, the other positions are left out of the next
+// digits (and none are needed when all of those are kept).  Then each warp
+// counts what it keeps, and after one scan over the warps writes its kept
+// positions in order: those above the key, and the first `ties` equal to it.
+// CTAs of a cluster exchange their histograms and their warps' counts; all of
+// them find the same key.
+//
+// The keys of a CTA's first kSelHeld positions are made once and stay in shared
 // memory; beyond, the weights are read again (from L2) in each pass.  (Keys in
 // registers took the same passes unrolled 32 times, whose code alone, fetched
-// once per launch, cost microseconds.)
+// once per launch, cost microseconds: 16.4 against 12.5 us for 4 x 8 pairs of
+// 4096 positions with their moves.)
+//
 // What bounds it: the chain of passes and barriers in few CTAs.  4 x 8 pairs of
 // 4096 positions: 6.0 us (9200 cycles: reading the length and the weights 3600,
 // digits 3900, counting and writing 1600); 8 x 8 pairs of 32768 positions: 24 us
-// in one CTA each, 18 us in two.
-// CTAs of a cluster exchange their histograms and their warps' counts; all of
-// them find the same key.
-// (Moving few rows in the same CTA instead of a second, overlapping launch was
-// slower: 21.9 against 18 us for 256 rows of 32 pairs.)
+// in one CTA each, 18 us in two.  (Moving few rows in the same CTA instead of a
+// second, overlapping launch was slower: 21.9 against 18 us for 256 rows of 32
+// pairs, at the time.)
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelHeld = 48 * 1024;
@@ -383,26 +387,31 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   (void)cudaGetLastError();
   const int cap = a.max_blocks_per_seq << a.block_shift;
   const int rows = a.budget < cap ? a.budget : cap;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   // CTAs that share a pair: up to 8192 positions each while the device has SMs for all (a CTA fills one), and as many as
   // hold all keys.  A cluster costs about 4 us to start, so none up to 16384 positions.  Both kernels in us with clusters
   // of 1 / 2 / 4 / 8, positions x pairs to kept rows: 32768 x 32 to 4096 57 / 52 / 50 / 65, 32768 x 64 to 4096
   // 77 / 73 / 77 / 101, 16384 x 32 to 1024 30 / 30 / 31 / 40, 131072 x 8 to 4096 212 / 118 / 46 / 42.
   const int64_t pairs = static_cast<int64_t>(a.num_kv_heads) * a.num_seqs;
   int ctas = 1;
-  while (cap > 2 * 8192 && ctas < 8 && ((cap / ctas > 8192 && 2 * ctas * pairs <= sms) || cap / ctas > kSelHeld)) ctas *= 2;
+  cudaError_t e = cudaSuccess;
+  if (cap > 2 * 8192) {
+    int dev = 0, sms = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    while (ctas < 8 && ((cap / ctas > 8192 && 2 * ctas * pairs <= sms) || cap / ctas > kSelHeld)) ctas *= 2;
+  }
   const int most = cap / ctas + kSelThreads;  // positions of a CTA
   auto* const select = ctas > 1 ? evict_select_kernel<true> : evict_select_kernel<false>;
-  e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelHeld * 4);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t sel = {};
   sel.gridDim = dim3(a.num_kv_heads * ctas, a.num_seqs);
   sel.blockDim = dim3(kSelThreads);
   sel.dynamicSmemBytes = (most < kSelHeld ? most : kSelHeld) * sizeof(uint32_t);
   sel.stream = stream;
+  if (ctas > 1 || sel.dynamicSmemBytes > 32 * 1024) {  // with the 13 KB that are static, up to 48 KB need no leave
+    e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelHeld * 4);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute cluster[1];
   cluster[0].id = cudaLaunchAttributeClusterDimension;
   cluster[0].val.clusterDim.x = ctas;
