@@ -76,7 +76,7 @@
 // us, single CTAs to pairs 571 -> 555.  Tried and slower: fetching the next
 // half's scores before handing this one over (604 us, registers), computing on
 // the first 32 columns while the rest arrive (559), the two streams set half a
-// tile apart (550 to 555).
+// tile apart (550 to 555), their warps on a scheduler taking turns (630).
 #pragma once
 
 #include "pa_attend.cuh"
