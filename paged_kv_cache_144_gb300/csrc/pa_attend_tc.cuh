@@ -450,7 +450,9 @@ __device__ __forceinline__ int tiles_in(int c, int U, int nw, int seg_start, int
   return min(seg_tiles, range_start(c + 1, U, nw) - seg_start - kFragCost) - b;
 }
 // Which of a CTA's records its fragment of a segment fills: 0: the CTA's first fragment, 1: a later one (both cut), 2 and
-// 3: whole segments in turn (alternating streams: two contributions of one CTA).
+// 3: whole segments in turn (alternating streams: two contributions of one CTA).  Whole segments of a CTA may be many: a slot is
+// written again only when its records have been joined (barriers JD), since a stream that need not join can be several
+// fragments ahead of the one that does.
 __device__ __forceinline__ int slot_kind_of(bool whole, int idx) { return whole ? 2 + (idx & 1) : (idx == 0 ? 0 : 1); }
 // The same for CTA c of a cut segment, seen from outside: a range that starts before the segment holds a fragment before it.
 __device__ __forceinline__ int cut_slot_kind(int c, int c0, int U, int nw, int seg_start) {
@@ -492,7 +494,8 @@ struct TcTraits {
                        KP = RB + 2, VP = KP + NST, QP = VP + NST,  // the peer's has arrived
                        VL = QP + 2,                                // a V tile with rows to be zeroed has arrived
                        RKF = VL + NST, RKE = RKF + NR, RVF = RKE + NR, RVE = RVF + NR, QL = RVE + NR,  // 8-bit caches
-                       NBAR = QL + 2;
+                       JD = QL + 2,  // a whole segment's records have been joined, per slot
+                       NBAR = JD + 2;
   static constexpr int OFF_MISC = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;  // tmem address, flags, scan scratch
   static constexpr int OFF_FRAG = OFF_MISC + 256;                         // WarpFrag per warp
   static constexpr int OFF_PREFIX = OFF_FRAG + (THREADS / 32 * static_cast<int>(sizeof(WarpFrag)) + 15) / 16 * 16;
@@ -667,6 +670,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       mbar_init(bar(Tr::QP + t), 1);
       mbar_init(bar(Tr::OD + t), 1);
       mbar_init(bar(Tr::RB + t), 4);
+      mbar_init(bar(Tr::JD + t), 4);
     }
     fence_mbar_init();
   }
@@ -1129,6 +1133,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     constexpr float kLift = Tr::BF16 ? 0.f : 7.f;
     constexpr float kMost = Tr::BF16 ? 256.f : 32768.f;  // 2^(kLift + kSlack): 64 weights of at most 2^kLift stay below it
     int jobs = 0, parity = 0, q_uses = 0;
+    uint32_t slot_uses = 0u;  // parity of the uses of the whole segments' record slots, a bit each
 
     // queries at negative positions (more queries than tokens) see nothing
     for (int s = blockIdx.x; s < S; s += gridDim.x) {
@@ -1344,7 +1349,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         continue;
       }
       // ---- record, then count in; the last contribution joins them all
-      const int slot_kind = slot_kind_of(f.whole, f.idx);
+      const int slot_kind = slot_kind_of(f.whole, f.idx), slot = slot_kind & 1;
+      if (f.whole) {  // the slot's last segment has been joined (by either stream; at once for the slot's first)
+        if (!(ok = wait(Tr::JD + slot, ((slot_uses >> slot) & 1u) ^ 1u))) break;
+        slot_uses ^= 1u << slot;
+      }
       {
         float* const rec = record_at<D>(p, blockIdx.x, slot_kind, e);
         const int lr = wq * 32 + lane;
@@ -1380,6 +1389,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         __threadfence();
         if (warp_on) join_rows<KVT, D, CG>(p, f, U, nw, c0, c1, rank, t, wq, row0, rows, slot_kind);
         if ((threadIdx.x & 127) == 0) *counter = 0;  // ready for the next call
+        if (f.whole) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Tr::JD + slot));
+        }
       }
     }
   }
