@@ -147,6 +147,12 @@ __device__ float2 attend_row(const AttendParams& p, int s, const SeqView& v, int
       if (p.slopes) x -= slope * static_cast<float>(abs(rb.pos - t));
       z = x * kLog2e;
     }
+    if (__any_sync(0xffffffffu, z != z || z == INFINITY)) {  // no maximum to subtract: every weight is NaN, and so is the row
+      m = INFINITY;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) acc[j] = nanf("");
+      break;
+    }
     float mx = z;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
