@@ -442,7 +442,9 @@ int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t 
  *     every t < T - L, and t = T - L + j when bit j of the query's mask row
  *     is set (its own bit is not implied).
  * What a masked position holds does not matter (infinities and NaN too, in K
- * and in V).  A query that sees nothing, or whose position is negative
+ * and in V).  NaN or infinity at a visible position shows in the rows that see
+ * it and in no other; rows whose tile holds it may take long (each is computed
+ * again on its own, after the rest of the call).  A query that sees nothing, or whose position is negative
  * (T < L), gets out = 0.  Rows of out from q_starts[num_seqs] on, and before
  * q_starts[0], are left as they were.
  *
@@ -581,8 +583,9 @@ int pa_version(void);
 
 /*
  * pa_debug_set_decode_wait - testing hook for the bounded waits of the decode
- * kernel (engineering addition with no counterpart in the pages; process-wide,
- * read at each later pa_decode / pa_decode_ex / pa_decode_noalloc call).
+ * and attention kernels (engineering addition with no counterpart in the pages;
+ * process-wide, read at each later pa_decode / pa_decode_ex /
+ * pa_decode_noalloc call, limit_ns by pa_attend too).
  *   limit_ns         limit of every wait of a consumer warp on its pipeline
  *                    barrier (and of the producer on a consumer's release);
  *                    0 restores the default of 2 s.  A wait that runs out

@@ -288,10 +288,19 @@ PA_EXPORT int pa_decode_launch_config(int num_seqs, int num_heads, int num_kv_he
 
 namespace {
 
-// Wait limit and copy withholding of the next decode launches (testing hook,
+// Wait limit and copy withholding of the next launches (testing hook,
 // pa_debug_set_decode_wait); 0 = the default limit.
 std::atomic<uint64_t> g_wait_limit_ns{0};
 std::atomic<int> g_withhold_copies{0};
+
+}  // namespace
+
+uint64_t pa::wait_limit_ns() {
+  const uint64_t lim = g_wait_limit_ns.load(std::memory_order_relaxed);
+  return lim ? lim : kDefaultWaitLimitNs;
+}
+
+namespace {
 
 // Everything one decode launch needs, validated: the plan, the kernel
 // parameters and the two tensor maps.  Filling it enqueues nothing.
@@ -417,8 +426,7 @@ int prepare_decode(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtyp
   p.pending_cap = plan.pending_cap;
   p.part_records = plan.bytes ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.counters_bytes)
                               : nullptr;
-  const uint64_t lim = g_wait_limit_ns.load(std::memory_order_relaxed);
-  p.wait_limit_ns = lim ? lim : pa::kDefaultWaitLimitNs;
+  p.wait_limit_ns = pa::wait_limit_ns();
   p.withhold_copies = g_withhold_copies.load(std::memory_order_relaxed);
   p.early_kv = (o.early_kv != 0 && o.pdl != 0 && q_len == 1 && !append) ? 1 : 0;
   d->pdl = o.pdl != 0;

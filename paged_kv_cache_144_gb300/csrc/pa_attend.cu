@@ -136,7 +136,7 @@ cudaError_t launch_few(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaS
   p.stages = pl.geo.stages;
   p.row_groups = pl.geo.row_groups;
   p.stage_bytes = pl.geo.stage_bytes;
-  p.wait_limit_ns = kDefaultWaitLimitNs;
+  p.wait_limit_ns = a.wait_limit_ns;
   p.att = a;
   const int eb = a.kv_dtype == PA_FP8_E4M3 || a.kv_dtype == PA_INT8 ? 1 : 2;
   const int box = a.block_size < pl.geo.unit_rows ? a.block_size : pl.geo.unit_rows;

@@ -60,10 +60,11 @@
 // A position's V row is multiplied by P = 0 in rows that do not see it, which
 // is not enough when it holds NaN or infinity: rows past the sequence's end (or
 // before the window) are zeroed in shared memory, and a result row that is
-// not finite is computed again by one warp from the definition (attend_row).
+// not finite is computed again by one warp from the definition (attend_row):
+// once all of the CTA's fragments are done, so that no wait of the pipeline
+// depends on it.
 //
-// Every wait on a barrier ends after kDefaultWaitLimitNs with
-// PA_DEVERR_TIMEOUT.
+// Every wait on a barrier ends after a limit (2 s) with PA_DEVERR_TIMEOUT.
 //
 // What bounds it.  Prompt chunks of 4 x 1-2K queries over 4-8K tokens (32 heads
 // on 8, head size 128): 555 us, 62 % of the measured bf16 matrix rate; 64-node
@@ -502,6 +503,13 @@ struct TcTraits {
   static size_t smem_bytes(int num_seqs) { return 1024 + OFF_PREFIX + static_cast<size_t>(num_seqs + 1) * 4; }
 };
 
+// Word of the shared scratch that notes where rows of the CTA are not finite, and a fragment's bits in it: one for all whole
+// segments, one for each stream's rows of a cut one (slot kind 0 or 1) that this CTA has joined.
+constexpr int kRedo = 40;
+__device__ __forceinline__ int redo_bits(bool whole, int slot_kind, int stream) {
+  return whole ? 16 : 1 << (2 * slot_kind + stream);
+}
+
 // Where contribution c of a fragment with this slot kind lies.
 template <int D>
 __device__ __forceinline__ float* record_at(const TcParams& p, int cta, int kind, int c) {
@@ -514,8 +522,9 @@ __device__ __forceinline__ float* record_at(const TcParams& p, int cta, int kind
 // loads (one row and record after the other they took 100 us at the end of a 600 us call): those of kJoin rows of kRecs
 // records are under way at once, which the registers of the softmax warps allow.
 constexpr int kJoin = 4, kRecs = 3;
+// True: a row is not finite.
 template <typename KVT, int D, int CG>
-__device__ __forceinline__ void join_rows(const TcParams& p, const Frag& f, int U, int nw, int c0, int c1, int rank, int t, int wq,
+__device__ __forceinline__ bool join_rows(const TcParams& p, const Frag& f, int U, int nw, int c0, int c1, int rank, int t, int wq,
                                           int row0, int rows, int slot_kind) {
   const AttendParams& a = p.a;
   const int lane = threadIdx.x & 31;
@@ -542,6 +551,7 @@ __device__ __forceinline__ void join_rows(const TcParams& p, const Frag& f, int 
   }
   float inv = L > 0.f ? 1.f / L : 0.f;
   if constexpr (elem<KVT>::bytes == 1) inv *= __ldg(a.v_scale + f.kvh);
+  bool bad = false;
   for (int g = 0; g < total; g += kRecs) {
     // (more than kRecs records: the rows are gone through again, from the sums so far)
     const float* rec[kRecs];
@@ -591,17 +601,17 @@ __device__ __forceinline__ void join_rows(const TcParams& p, const Frag& f, int 
         }
         const int i = (row0 + row) / a.group, h = f.kvh * a.group + (row0 + row) - i * a.group;
         const int64_t o0 = ((static_cast<int64_t>(f.v.row0) + i) * a.num_heads + h) * D + lane * V;
-        bool bad = Lk != Lk;
+        bad |= Lk != Lk;
 #pragma unroll
         for (int q = 0; q < V; ++q) {
           acc[k][q] *= ik;
           bad |= !(fabsf(acc[k][q]) < INFINITY);
         }
         store_columns<V>(a.out, a.out_dtype, o0, acc[k]);
-        if (__any_sync(0xffffffffu, bad)) attend_row_again<KVT, D>(a, f.s, f.v, i, h);
       }
     }
   }
+  return __any_sync(0xffffffffu, bad);
 }
 
 // ----------------------------------------------------------------- kernel
@@ -627,14 +637,14 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   const bool q_widen = Tr::B8 && a.q_dtype == PA_BF16;  // bf16 queries become f16
   const int group_id = static_cast<int>(blockIdx.x) / CG, groups = static_cast<int>(gridDim.x) / CG;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
-  auto wait = [&](int i, uint32_t parity) -> bool {
-    if (mbar_wait_bounded(bar(i), parity, kDefaultWaitLimitNs)) return true;
+  auto wait = [&](int i, uint32_t parity, bool full = false) -> bool {  // full: the whole limit, whatever the call's
+    if (mbar_wait_bounded(bar(i), parity, full ? kDefaultWaitLimitNs : a.wait_limit_ns)) return true;
     raise_error(a.err, PA_DEVERR_TIMEOUT);
     return false;
   };
   // the same for what the other CTA of a pair arrives on
   auto wait_pair = [&](int i, uint32_t parity) -> bool {
-    if (mbar_wait_bounded_cluster(bar(i), parity, kDefaultWaitLimitNs)) return true;
+    if (mbar_wait_bounded_cluster(bar(i), parity, a.wait_limit_ns)) return true;
     raise_error(a.err, PA_DEVERR_TIMEOUT);
     return false;
   };
@@ -672,6 +682,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       mbar_init(bar(Tr::RB + t), 4);
       mbar_init(bar(Tr::JD + t), 4);
     }
+    misc[kRedo] = 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc<CG>(base + Tr::OFF_MISC, 512);
@@ -746,28 +757,32 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   // than there are (n near the root of 0.6 tiles).
   const int balanced = static_cast<int>(sqrtf(0.6f * static_cast<float>(U) * p.max_segments));
   const int nw = min(groups, max(min(want, balanced), 1));
-  FragIter it;
-  it.U = U;
-  it.nw = nw;
-  it.idx = 0;
-  it.s = 0;
-  it.s_state = -1;
-  it.m = it.m_pos = it.kvh = 0;
-  it.u = it.u1 = 0;
-  if (group_id < nw && U > 0) {
-    it.u = range_start(group_id, U, nw);
-    it.u1 = range_start(group_id + 1, U, nw);
-    int lo = 0, hi = S - 1;
-    while (lo < hi) {  // last sequence with prefix <= u
-      const int mid = (lo + hi + 1) >> 1;
-      if (prefix[mid] <= it.u) lo = mid; else hi = mid - 1;
-    }
-    it.s = lo;
-  }
   WarpFrag* const wf = reinterpret_cast<WarpFrag*>(sm + Tr::OFF_FRAG) + warp;
-  if (lane == 0) wf->it = it;
-  __syncwarp();
   const Frag& f = wf->f;
+  auto start_frags = [&] {  // the warp's iterator at the start of the CTA's range
+    FragIter it;
+    it.U = U;
+    it.nw = nw;
+    it.idx = 0;
+    it.s = 0;
+    it.s_state = -1;
+    it.m = it.m_pos = it.kvh = 0;
+    it.u = it.u1 = 0;
+    if (group_id < nw && U > 0) {
+      it.u = range_start(group_id, U, nw);
+      it.u1 = range_start(group_id + 1, U, nw);
+      int lo = 0, hi = S - 1;
+      while (lo < hi) {  // last sequence with prefix <= u
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= it.u) lo = mid; else hi = mid - 1;
+      }
+      it.s = lo;
+    }
+    __syncwarp();
+    if (lane == 0) wf->it = it;
+    __syncwarp();
+  };
+  start_frags();
 
   // row tile of stream t in this CTA within its sequence
   auto row_tile = [&](int m, int t) { return p.paired ? (m * 2 + t) * CG + rank : m * CG + rank; };
@@ -831,11 +846,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     for (int i = 0; i < NST; ++i) {
       const int n = count / NST + (i < count % NST ? 1 : 0);
       const uint32_t ph = static_cast<uint32_t>(n - 1) & 1u;
-      if (n > 0 && !wait((is_v ? Tr::VE : Tr::KE) + i, ph)) wait((is_v ? Tr::VF : Tr::KF) + i, ph);
+      if (n > 0 && !wait((is_v ? Tr::VE : Tr::KE) + i, ph, true)) wait((is_v ? Tr::VF : Tr::KF) + i, ph, true);
     }
     for (int i = 0; i < Tr::NR; ++i) {
       const int n = count / (Tr::B8 ? Tr::NR : 1) + (i < count % (Tr::B8 ? Tr::NR : 1) ? 1 : 0);
-      if (n > 0) wait((is_v ? Tr::RVF : Tr::RKF) + i, static_cast<uint32_t>(n - 1) & 1u);
+      if (n > 0) wait((is_v ? Tr::RVF : Tr::RKF) + i, static_cast<uint32_t>(n - 1) & 1u, true);
     }
   };
 
@@ -911,8 +926,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       }
       drain(true, kt);
       for (int t = 0; t < 2; ++t)
-        if (uses[t] > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses[t] - 1) & 1u))
-          wait((q_widen ? Tr::QL : Tr::QF) + t, static_cast<uint32_t>(uses[t] - 1) & 1u);
+        if (uses[t] > 0 && !wait(Tr::QE + t, static_cast<uint32_t>(uses[t] - 1) & 1u, true))
+          wait((q_widen ? Tr::QL : Tr::QF) + t, static_cast<uint32_t>(uses[t] - 1) & 1u, true);
     } else if (rank != 0) {
       // ================================================================= the second CTA of a pair: says what has arrived
       // (warp 1: K, warp 2: V)
@@ -1339,12 +1354,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
               store_row32(a.out, a.out_dtype, o0 + c, o, wide);
             }
           }
-          unsigned again = __ballot_sync(0xffffffffu, bad && valid);
-          while (again) {
-            const int k = __ffs(again) - 1;
-            again &= again - 1;
-            attend_row_again<KVT, D>(a, f.s, f.v, __shfl_sync(0xffffffffu, qi, k), __shfl_sync(0xffffffffu, h, k));
-          }
+          if (__any_sync(0xffffffffu, bad && valid) && lane == 0) atomicOr(misc + kRedo, redo_bits(true, 0, t));
         }
         continue;
       }
@@ -1387,11 +1397,33 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const bool last = *arrived == total - 1;
       if (last) {
         __threadfence();
-        if (warp_on) join_rows<KVT, D, CG>(p, f, U, nw, c0, c1, rank, t, wq, row0, rows, slot_kind);
+        if (warp_on && join_rows<KVT, D, CG>(p, f, U, nw, c0, c1, rank, t, wq, row0, rows, slot_kind) && lane == 0)
+          atomicOr(misc + kRedo, redo_bits(f.whole, slot_kind, t));
         if ((threadIdx.x & 127) == 0) *counter = 0;  // ready for the next call
         if (f.whole) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(Tr::JD + slot));
+        }
+      }
+    }
+
+    // ---- rows that are not finite, from the definition: they may owe it to a V row that they do not see.  All fragments
+    // are done, and nothing but the end of the kernel waits for these warps.
+    named_barrier_sync(1, 256);  // the CTA's rows are stored
+    const int redo = *static_cast<volatile int*>(misc + kRedo);
+    if (redo != 0) {
+      start_frags();
+      while (next_frag(wf, prefix, p)) {
+        const int rps = stream_rows(a.group), kind = slot_kind_of(f.whole, f.idx);
+        for (int x = 0; x < (p.paired ? 2 : 1); ++x) {
+          const int bits = redo_bits(f.whole, kind, x) | (p.paired ? 0 : redo_bits(f.whole, kind, 1));
+          if ((redo & bits) == 0) continue;
+          const int first_row = row_tile(f.m, x) * rps, rows = min(rps, f.v.L * a.group - first_row);
+          for (int k = warp - 4; k < rows; k += 8) {
+            const int i = (first_row + k) / a.group, h = f.kvh * a.group + (first_row + k) - i * a.group;
+            if (row_not_finite<D>(a, (static_cast<int64_t>(f.v.row0) + i) * a.num_heads + h))
+              attend_row<KVT, D>(a, f.s, f.v, i, h);
+          }
         }
       }
     }

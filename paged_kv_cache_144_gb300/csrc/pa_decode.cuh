@@ -1272,15 +1272,21 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     __syncwarp();
   };
 
-  // pa_attend, several queries: the warp's rows of a segment from the definition
+  // pa_attend, several queries: those of the warp's rows of a segment that are stored and not finite, from the definition
+  // (a row may owe it to a V row it does not see).  Called after the unit loop only: it takes long, and the ring's producer
+  // and other warps wait for this one's stages until then.
+  [[maybe_unused]] bool redo = false;  // a segment that this warp computed alone has such rows
   [[maybe_unused]] auto again = [&](int s, int kvh, int T, int L, int64_t rows0, int n) {
     if constexpr (ATT && MQ) {
       SeqView v;
       v.T = T;
       v.L = L;
       v.row0 = static_cast<int>(rows0);
-      for (int r = 0; r < n; ++r)
-        attend_row_again<KVT, D>(p.att, s, v, (row0 + r) / G, kvh * G + (row0 + r) % G);
+      __syncwarp();  // the rows are stored
+      for (int r = 0; r < n; ++r) {
+        const int i = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
+        if (row_not_finite<D>(p.att, (rows0 + i) * p.num_heads + h)) attend_row_again<KVT, D>(p.att, s, v, i, h);
+      }
     }
   };
 
@@ -1598,10 +1604,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                 p.att.row_stats[static_cast<int64_t>(it.s) * p.num_heads + it.kvh * G + row0 + row] = make_float2(m[h], lt[h]);
             }
           }
-          // a row that is not finite may owe it to a V row it does not see
-          if constexpr (MQ) {
-            if (__any_sync(0xffffffffu, bad)) again(it.s, it.kvh, it.T, QL, row_base, Rw);
-          }
+          if constexpr (MQ) redo = redo || bad;
         }
       } else {
         float* rec = p.part_records + (static_cast<int64_t>(it.slot) * NC + rg) * Tr::REC;
@@ -1684,6 +1687,15 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     // them after its (acquired) view of global memory
     fence_proxy_async_global();
     for (int i = 0; i < npend; ++i) merge_seg(pend[i]);
+  }
+  if constexpr (ATT && MQ) {
+    if (__any_sync(0xffffffffu, redo)) {
+      start_iter(it, ring_gc(ring_id));
+      while (it.valid) {
+        if (it.slot < 0) again(it.s, it.kvh, it.T, it.L, first_row(it.s), min(16, it.L * G - row0));
+        iter_next_fragment<ATT>(it, prefix, p, fixed, Tr::UR_SHIFT);
+      }
+    }
   }
 }
 

@@ -27,6 +27,7 @@ constexpr int kBoxRowQuantum = 8;
 int tuning_override(const char* name);
 
 // Shared by the translation units that hold entry points.
+uint64_t wait_limit_ns();                                // of pipeline waits (2 s, or what the testing hook has set)
 unsigned int* device_error_word();                       // of the current device (nullptr on failure)
 int cuda_status(cudaError_t e, const char* where);       // PA_OK or PA_ERR_CUDA with the error's text recorded
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // nullptr when the driver has none
@@ -102,6 +103,7 @@ struct AttendParams {
   int score_stride;
   unsigned int* err;
   bool pdl;
+  uint64_t wait_limit_ns;  // limit of every wait on a pipeline barrier
 };
 
 // Everything the decode kernel reads besides the two tensor maps.

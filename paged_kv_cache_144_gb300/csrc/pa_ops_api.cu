@@ -224,6 +224,7 @@ PA_EXPORT int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q
   p.mass_stride_head = o.mass_stride_head;
   p.err = err;
   p.pdl = o.pdl != 0;
+  p.wait_limit_ns = pa::wait_limit_ns();
   return pa::launch_attend(p, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
