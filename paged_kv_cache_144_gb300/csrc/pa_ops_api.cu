@@ -57,6 +57,13 @@ int check_attend_shape(int num_seqs, int num_heads, int num_kv_heads, int head_d
   return PA_OK;
 }
 
+// Whether the bytes [out, out + out_bytes) meet one of `rows` rows of row_bytes, stride bytes apart from q on.
+bool overlaps_rows(const void* out, int64_t out_bytes, const void* q, int64_t rows, int64_t row_bytes, int64_t stride) {
+  const int64_t o = static_cast<int64_t>(reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(q));
+  const int64_t first = o < row_bytes ? 0 : (o - row_bytes) / stride + 1;  // the first row that ends behind out's start
+  return first < rows && first * stride < o + out_bytes;
+}
+
 }  // namespace
 
 PA_EXPORT int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, int num_heads,
@@ -182,6 +189,9 @@ PA_EXPORT int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q
       (int64_t{1} << 31))
     return PA_ERR_SHAPE;
   if (static_cast<int64_t>(num_seqs) * num_kv_heads * (cap / 32 + 4) >= (int64_t{1} << 31)) return PA_ERR_SHAPE;
+  const int64_t row = static_cast<int64_t>(num_heads) * head_dim;
+  if (overlaps_rows(out, num_tokens * row * (out_dtype == PA_F32 ? 4 : 2), q, num_tokens, row * 2, q_stride * 2))
+    return PA_ERR_SHAPE;
   unsigned int* err = pa::device_error_word();
   if (!err) return PA_ERR_CUDA;
   pa::AttendParams p;
