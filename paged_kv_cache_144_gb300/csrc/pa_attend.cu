@@ -30,6 +30,15 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // area that calls of any shape share; a call with more clears them itself first (its batch is large enough not to notice).
 constexpr size_t kCounters = 1 << 16;
 
+// Sequences for which the decode kernel's launch shape is computed: the next power of two.  (Its per-sequence arrays take shared
+// memory from the rings, so warps, and the workspace that their records take, fall as a batch grows, in steps; with few
+// different shapes attend_workspace_bytes can look at all of them.)
+int shape_seqs(int num_seqs) {
+  int n = 1;
+  while (n < num_seqs) n *= 2;
+  return n;
+}
+
 // How a call of these sizes runs, and what it keeps in the workspace.
 struct Plan {
   enum Kind { kFew, kTensor } kind;
@@ -45,8 +54,9 @@ struct Plan {
   int score_stride;
 };
 
+// prefer: the kernel to plan for where both may serve such a call, or -1: the one that does.
 bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
-               int max_q_len, int q_dtype, int kv_dtype, bool tree, bool accumulate, Plan* pl) {
+               int max_q_len, int q_dtype, int kv_dtype, bool tree, bool accumulate, int prefer, Plan* pl) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -61,7 +71,8 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
   pl->seg_rows = rps * pl->cg * (pl->paired ? 2 : 1);
   const int few = tuning_override("PA_ATTEND_FEW_ROWS");  // tuning
   const int64_t positions = static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq * block_size;
-  const bool is_few = rows <= kFewRows && (accumulate || (few >= 0 ? rows <= few : few_rows(rows, positions, q8)));
+  const bool chosen = prefer >= 0 ? prefer == Plan::kFew : few >= 0 ? rows <= few : few_rows(rows, positions, q8);
+  const bool is_few = rows <= kFewRows && (accumulate || chosen);
   pl->kind = is_few ? Plan::kFew : Plan::kTensor;
   size_t records = 0, pending = 0;
   pl->num_counters = 0;
@@ -74,7 +85,7 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
     pl->key.unit_rows = q8 && block_size >= 16 && gm == 8 ? 64 : 32;
     pl->key.append = 2;
     pl->key.row_groups = gm == 16 ? static_cast<int>((rows + 15) / 16) : 1;
-    if (!decode_geometry(pl->key, num_seqs, &pl->geo)) return false;
+    if (!decode_geometry(pl->key, shape_seqs(num_seqs), &pl->geo)) return false;
     const size_t warps = static_cast<size_t>(pl->geo.ctas) * pl->geo.warps_per_cta;
     pl->num_counters = static_cast<size_t>(num_seqs) * num_kv_heads * pl->geo.row_groups;
     records = 2 * warps * pl->geo.record_floats * sizeof(float);
@@ -310,23 +321,29 @@ __global__ void __launch_bounds__(kMassThreads) attend_add_mass_kernel(const Att
 
 size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                               int max_blocks_per_seq, int max_q_len, int kv_dtype, bool accumulate) {
-  // The largest need with and without a tree, with either query type that the caches take, and of calls with fewer
-  // sequences, queries or blocks: one sequence and one block leave the most room for other parts (they are cut down for the
-  // batch's arrays), and the records' size changes where the rows fill another 16 up to 64, a stream or a pair.
+  // The largest need on either kernel, with and without a tree, with either query type that the caches take, and of calls with
+  // fewer sequences, queries or blocks: records change with the batch's power of two (shape_seqs; all else grows with the
+  // batch and its blocks), and where the rows fill another 16 up to 64, a stream or a pair.
   const int group = num_heads / num_kv_heads, per_stream = stream_rows(group) / group;
-  const int lens[] = {1,          16 / group, 17 / group + 1,  32 / group,     33 / group + 1,     48 / group, 49 / group + 1,
-                      64 / group, 64 / group + 1, per_stream, per_stream + 1, 2 * per_stream, max_q_len};
+  const int lens[] = {1,          16 / group,     16 / group + 1, 32 / group,     32 / group + 1, 48 / group, 48 / group + 1,
+                      64 / group, 64 / group + 1, per_stream,     per_stream + 1, 2 * per_stream, max_q_len};
+  constexpr int kLens = sizeof(lens) / sizeof(lens[0]);
   size_t most = 0;
-  for (int i = 0; i < 16; ++i) {
-    const int q_dtype = i & 1 ? PA_BF16 : PA_F16, seqs = i & 2 ? 1 : num_seqs, blocks = i & 4 ? 1 : max_blocks_per_seq;
+  for (int i = 0; i < 8; ++i) {
+    const int q_dtype = i & 1 ? PA_BF16 : PA_F16, prefer = i & 2 ? Plan::kFew : Plan::kTensor;
     if ((kv_dtype == PA_F16 || kv_dtype == PA_BF16) && q_dtype != kv_dtype) continue;
-    for (const int len : lens) {
-      if (len < 1 || len > max_q_len) continue;
-      Plan pl;
-      if (!make_plan(seqs, num_heads, num_kv_heads, head_dim, block_size, blocks, len, q_dtype, kv_dtype, (i & 8) != 0,
-                     accumulate, &pl))
-        return static_cast<size_t>(-1);
-      most = pl.bytes > most ? pl.bytes : most;
+    for (int x = 0; x < kLens; ++x) {
+      const int len = lens[x];
+      bool again = len < 1 || len > max_q_len;
+      for (int y = 0; y < x; ++y) again = again || lens[y] == len;
+      if (again) continue;
+      for (int seqs = num_seqs > 1 ? num_seqs : 1; seqs >= 1; seqs = shape_seqs(seqs) / 2) {
+        Plan pl;
+        if (!make_plan(seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, len, q_dtype, kv_dtype,
+                       (i & 4) != 0, accumulate, prefer, &pl))
+          return static_cast<size_t>(-1);
+        most = pl.bytes > most ? pl.bytes : most;
+      }
     }
   }
   return most;
@@ -336,7 +353,7 @@ int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaS
   (void)cudaGetLastError();
   Plan pl;
   if (!make_plan(p.num_seqs, p.num_heads, p.num_kv_heads, p.head_dim, p.block_size, p.max_blocks_per_seq, p.max_q_len,
-                 p.q_dtype, p.kv_dtype, p.tree_mask != nullptr, p.mass != nullptr, &pl))
+                 p.q_dtype, p.kv_dtype, p.tree_mask != nullptr, p.mass != nullptr, -1, &pl))
     return cuda_status(cudaErrorInvalidDevice, "pa_attend plan");
   if (!workspace || workspace_bytes < pl.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PA_ERR_WORKSPACE;
