@@ -391,8 +391,9 @@ size_t pa_decode_noalloc_capacity(void);
  *
  * For token n at position p = positions[n] and pair i < rotary_dim / 2, with
  * the angle a = p * inv_freq[i] (the product of the integer and the float32
- * value; reduced exactly, so far positions keep their precision up to
- * |p| < 2^31):
+ * value, off by at most 2^-26 + |p| 2^-54.6 turns for inv_freq[i] <= 1: far
+ * positions keep their precision, negative ones turn the other way;
+ * |p| <= 2^31):
  *     (x, y) -> rope_scale * (x cos a - y sin a, y cos a + x sin a)
  * where (x, y) are columns (2i, 2i + 1) of a head (interleaved != 0) or
  * (i, i + rotary_dim / 2) (interleaved == 0); columns from rotary_dim on pass

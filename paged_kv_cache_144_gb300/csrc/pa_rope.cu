@@ -5,9 +5,11 @@
 // inv_freq[i].  In units of a full turn, t = inv_freq / 2 pi is held as a
 // signed 64-bit fraction of a turn (its distance from the nearest whole turn
 // times 2^64); p * t then wraps modulo one turn by itself in 64-bit integer
-// arithmetic, so the reduction of a far position's angle is exact and needs no
-// 64-bit floating point per token.  The top 32 bits of the product are the
-// angle, 2^-33 turns at most from it, and go to sincospif.
+// arithmetic, so the reduction of a far position's angle loses nothing and needs
+// no 64-bit floating point per token.  The top 32 bits of the product, rounded
+// to a float32, go to sincospif: 2^-26 turns at most from p * t.  t itself is a
+// product in 53 bits, off by at most 2^-54.6 turns for frequencies up to 1,
+// which p multiplies: 2^-23.6 turns (5e-7 radians) at |p| = 2^31.
 //
 // Work: a CTA takes kTokens tokens and a slice of their heads (a few tokens
 // alone would not fill the device: the heads are then spread over more CTAs).
