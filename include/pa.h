@@ -204,8 +204,14 @@ int pa_decode(void* out, pa_dtype out_dtype,
  *            caches, the scales and the new rows, and writes out, the cache
  *            and the workspace, only after that kernel has finished.  So with
  *            pdl on, seq_lens and block_tables must not be written by the
- *            kernel launched just before this call (host copies and earlier
- *            kernels are fine).  0: an ordinary launch.  Either way the decode
+ *            kernel launched just before this call.  Where that kernel was
+ *            itself launched with pdl, it lets this call start before the
+ *            kernel before it has finished: the rule then holds for that one
+ *            too, and so on back to the last ordinary launch (that one
+ *            included) or copy on the stream; what came before it is fine.  A
+ *            step that writes lengths, tables or cache rows (pa_commit_tree,
+ *            pa_copy_blocks) goes before an ordinary launch.  0: an ordinary
+ *            launch.  Either way the decode
  *            lets a kernel launched after it with programmatic serialization
  *            (pa_reshape_and_cache_ex with pdl) be scheduled at once; that
  *            kernel waits for the decode before it touches memory.
@@ -214,7 +220,8 @@ int pa_decode(void* out, pa_dtype out_dtype,
  *            the caller guarantees that the kernel launched just before this
  *            call writes no row of k_cache / v_cache except the newest one of
  *            each sequence (position seq_lens[s]-1), as pa_reshape_and_cache
- *            of the same step does.  The decode then starts copying the K/V
+ *            of the same step does, and that the kernels before it which the
+ *            rule of pdl names write none either.  The decode then starts copying the K/V
  *            rows of its first units that hold none of those positions before
  *            that kernel has finished; q, the scales and the newest rows are
  *            still read only after it.  Ignored otherwise.  A caller that
@@ -309,7 +316,9 @@ int pa_reshape_and_cache(const void* k, const void* v, pa_dtype src_dtype,
  *            launched just before it on `stream` has finished, so only the
  *            launch overlaps that kernel.  0: an ordinary launch.  Either way
  *            a decode launched after the write with pdl may start its set-up
- *            at once (it reads the cache only after the write has finished).
+ *            at once (it reads the cache only after the write has finished),
+ *            which with pdl here may be before the kernel before the write has
+ *            finished (see pa_decode_ex).
  *            Engineering addition with no counterpart in the pages.
  */
 typedef struct pa_cache_write_options {
@@ -527,7 +536,10 @@ size_t pa_attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, 
  * moves and new_lens[s] = seq_lens[s].
  *   path           int32 [num_seqs][max_path], 1 <= max_path <= 256
  *   path_lens      int32 [num_seqs]
- *   new_lens       int32 [num_seqs] (not seq_lens itself)
+ *   new_lens       int32 [num_seqs] (not seq_lens itself).  A pa_decode with
+ *                  pdl reads its lengths early: with new_lens as its seq_lens,
+ *                  an ordinary launch has to stand between (the next step's
+ *                  cache write without pdl)
  */
 int pa_commit_tree(void* k_cache, void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
                    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,

@@ -290,9 +290,10 @@ def decode(out, q, k_cache, v_cache, block_tables, seq_lens, num_kv_heads, scale
     written into their cache slots (quantised with k_inv_scale / v_inv_scale for 8-bit caches) and
     attended in the same launch (pa_decode_ex).
     pdl=True: programmatic dependent launch (pa_decode_ex): the set-up overlaps the kernel launched just
-    before on the stream, so seq_lens and block_tables must not be written by that kernel.
-    early_kv=True (with pdl, one query, no fused append): that kernel also writes no cache row but each
-    sequence's newest one (the step's cache write), so K/V copies of the other rows start before it ends.
+    before on the stream, so seq_lens and block_tables must not be written by that kernel, nor, as long as
+    those were launched with pdl themselves, by the ones before it up to the last ordinary launch.
+    early_kv=True (with pdl, one query, no fused append): those kernels also write no cache row but each
+    sequence's newest one (the step's cache write), so K/V copies of the other rows start before they end.
     """
     _require_cuda_all((("out", out), ("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
                        ("seq_lens", seq_lens), ("k_scale", k_scale), ("v_scale", v_scale),
@@ -362,7 +363,8 @@ def reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, block_size, *, k_inv
 
     INT8 caches (torch.int8) also take int32 per-KV-head zero points (pa_reshape_and_cache_ex).
     pdl=True: programmatic dependent launch (pa_reshape_and_cache_ex): the kernel waits for the kernel before
-    it on the stream before touching memory, so only its launch overlaps that kernel's end.
+    it on the stream before touching memory, so only its launch overlaps that kernel's end.  A decode with pdl
+    right after it may then start early as well: after copy_blocks or commit_tree, leave pdl off here.
     """
     _require_cuda_all((("k_cache", k_cache), ("v_cache", v_cache), ("slot_mapping", slot_mapping),
                        ("k_inv_scale", k_inv_scale), ("v_inv_scale", v_inv_scale), ("k_zero_point", k_zero_point),

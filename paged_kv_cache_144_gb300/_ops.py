@@ -147,7 +147,7 @@ def rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq,
 
     q [N, H_q, d], k / v [N, H_kv, d]; positions and slot_mapping int64 [N]; inv_freq float32 [rotary_dim / 2].
     The turned q goes to q_out (default: q itself), the turned k and v into their slots; tokens with a negative slot
-    are padding and left alone.  Returns q_out.
+    are padding and left alone.  pdl as in reshape_and_cache.  Returns q_out.
     """
     _torch or _t()
     if q_out is None:
@@ -298,7 +298,11 @@ def attend_accumulate(out, q, k_cache, v_cache, block_tables, seq_lens, mass, nu
 def commit_tree(k_cache, v_cache, block_tables, seq_lens, q_starts, path, path_lens, new_lens, block_size, *,
                 stream=None):
     """Move the accepted path's cache rows (nodes path[s, :path_lens[s]]) to the front of each tree's span and write
-    the sequences' new lengths (pa_commit_tree).  Returns new_lens."""
+    the sequences' new lengths (pa_commit_tree).  Returns new_lens.
+
+    A decode with pdl reads its lengths before the kernels just before it have finished: launch the cache write
+    between this call and it without pdl.
+    """
     _torch or _t()
     dev = _on_one_device(k_cache, v_cache, block_tables, seq_lens, q_starts, path, path_lens, new_lens)
     blocks, Hkv, D = _cache(k_cache, v_cache, block_size)
