@@ -591,7 +591,8 @@ int pa_get_device_error(void* stream, unsigned int* error_bits);
  * thread ("" if none); a static thread-local string. */
 const char* pa_last_error_detail(void);
 
-/* Library ABI version (major*100 + minor). */
+/* Library ABI version (major*100 + minor); 101: pa_rope_and_cache, pa_attend,
+ * pa_commit_tree, pa_evict. */
 int pa_version(void);
 
 /*

@@ -217,7 +217,7 @@ int make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int b
 
 }  // namespace
 
-PA_EXPORT int pa_version(void) { return 100; }
+PA_EXPORT int pa_version(void) { return 101; }
 
 PA_EXPORT const char* pa_last_error_detail(void) { return g_last_error; }
 
