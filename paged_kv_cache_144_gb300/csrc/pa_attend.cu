@@ -30,13 +30,22 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // area that calls of any shape share; a call with more clears them itself first (its batch is large enough not to notice).
 constexpr size_t kCounters = 1 << 16;
 
-// Sequences for which the decode kernel's launch shape is computed: the next power of two.  (Its per-sequence arrays take shared
-// memory from the rings, so warps, and the workspace that their records take, fall as a batch grows, in steps; with few
-// different shapes attend_workspace_bytes can look at all of them.)
-int shape_seqs(int num_seqs) {
+// Batches for which the decode kernel's launch shape is computed: powers of two up to 64, then steps of an eighth of the next
+// power of two, 64 at least; a batch takes the next one's shape.  (Its per-sequence arrays take shared memory from the rings, so
+// warps, and the workspace that their records take, fall as a batch grows, in steps; with few different shapes
+// attend_workspace_bytes can look at all of them.)
+int shape_step(int num_seqs) {
   int n = 1;
   while (n < num_seqs) n *= 2;
-  return n;
+  return n <= 64 ? n : (n / 8 > 64 ? n / 8 : 64);
+}
+int shape_seqs(int num_seqs) {
+  const int step = shape_step(num_seqs);
+  return (num_seqs + step - 1) / step * step;
+}
+int smaller_shape(int num_seqs) {  // the next smaller of them, or 0
+  const int n = shape_seqs(num_seqs);
+  return n <= 64 ? n / 2 : n - shape_step(n);
 }
 
 // How a call of these sizes runs, and what it keeps in the workspace.
@@ -322,8 +331,8 @@ __global__ void __launch_bounds__(kMassThreads) attend_add_mass_kernel(const Att
 size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                               int max_blocks_per_seq, int max_q_len, int kv_dtype, bool accumulate) {
   // The largest need on either kernel, with and without a tree, with either query type that the caches take, and of calls with
-  // fewer sequences, queries or blocks: records change with the batch's power of two (shape_seqs; all else grows with the
-  // batch and its blocks), and where the rows fill another 16 up to 64, a stream or a pair.
+  // fewer sequences, queries or blocks: records change with the launch shape (shape_seqs; all else grows with the batch and its
+  // blocks), and where the rows fill another 16 up to 64, a stream or a pair.
   const int group = num_heads / num_kv_heads, per_stream = stream_rows(group) / group;
   const int lens[] = {1,          16 / group,     16 / group + 1, 32 / group,     32 / group + 1, 48 / group, 48 / group + 1,
                       64 / group, 64 / group + 1, per_stream,     per_stream + 1, 2 * per_stream, max_q_len};
@@ -337,7 +346,7 @@ size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int
       bool again = len < 1 || len > max_q_len;
       for (int y = 0; y < x; ++y) again = again || lens[y] == len;
       if (again) continue;
-      for (int seqs = num_seqs > 1 ? num_seqs : 1; seqs >= 1; seqs = shape_seqs(seqs) / 2) {
+      for (int seqs = num_seqs > 1 ? num_seqs : 1; seqs >= 1; seqs = smaller_shape(seqs)) {
         Plan pl;
         if (!make_plan(seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, len, q_dtype, kv_dtype,
                        (i & 4) != 0, accumulate, prefer, &pl))
