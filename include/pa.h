@@ -457,10 +457,17 @@ int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t 
  * again on its own, after the rest of the call).  A query that sees nothing, or whose position is negative
  * (T < L), gets out = 0.  Rows of out from q_starts[num_seqs] on, and before
  * q_starts[0], are left as they were.
+ * Precision: scores, maxima and sums are float32.  A weight enters its product
+ * with v as two 16-bit values (an error of at most 2^-16 of it), but in calls with a
+ * 16-bit out whose max_q_len * G rows exceed one row tile - 128 / G * G rows,
+ * twice that with 8-bit caches or head_dim 128 - as one, off by up to 2^-8
+ * (bf16 caches) or 2^-11 (others) of it: up to the size of a rounding of out
+ * itself.  Ask for a float32 out where a prompt's rows have to be as exact as a
+ * decode step's.
  *
  *   out            [num_tokens][num_heads][head_dim], out_dtype F32/F16/BF16,
  *                  16-byte aligned, not overlapping q (rows are read by
- *                  several CTAs)
+ *                  several CTAs; PA_ERR_SHAPE)
  *   q              the same at q_stride elements per token, q_dtype F16/BF16
  *   caches, scales, block_tables, seq_lens     as pa_decode
  *   q_starts       int32 [num_seqs + 1]; NULL: one query per sequence, row s
@@ -488,7 +495,8 @@ int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t 
  *                  over the group's query heads of softmax(z)_t, for every t <
  *                  T (what a position beyond T holds is left as it was).
  *                  mass_stride_seq / mass_stride_head elements apart, rows of
- *                  at least max_blocks_per_seq * block_size elements
+ *                  at least max_blocks_per_seq * block_size elements.  A weight
+ *                  is off by up to 3e-4 of it; the totals are float32
  *   k_zero_point / v_zero_point   as pa_decode_options
  *   pdl            as pa_decode_options, but nothing at all is read before the
  *                  kernel before this call has finished
@@ -520,7 +528,9 @@ int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype, in
 /* Bytes of workspace pa_attend needs for these sizes on the current device
  * ((size_t)-1 when they are rejected or no device is usable), and for calls
  * with fewer sequences, queries or blocks per sequence; accumulate nonzero:
- * with the mass option. */
+ * with the mass option, which keeps the scores: 4 bytes for every query head and
+ * position of the tables, 4 * num_seqs * num_heads * max_blocks_per_seq *
+ * block_size (2 GB for 256 sequences of 32768 at 64 heads). */
 size_t pa_attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                                  int max_blocks_per_seq, int max_q_len, pa_dtype kv_dtype, int accumulate);
 

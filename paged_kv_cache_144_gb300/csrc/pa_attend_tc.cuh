@@ -68,7 +68,7 @@
 //
 // What bounds it.  Prompt chunks of 4 x 1-2K queries over 4-8K tokens (32 heads
 // on 8, head size 128): 555 us, 62 % of the measured bf16 matrix rate; 64-node
-// trees over 8 x 32K (64 heads on 8): 431 us, 65 %.  Without the softmax's work
+// trees over 8 x 32K (64 heads on 8): 435 us, 65 %.  Without the softmax's work
 // the same loop takes 357 and 277 us, without its loads either 324 and 252: the
 // tensor cores wait for weights.  Half a tile costs a softmax warp about 1490
 // cycles, 760 of them arithmetic (two warps share each scheduler's exponential
@@ -1144,7 +1144,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * 128 + lanes;
     constexpr float kLog2e = 1.4426950408889634f;
-    // f16 weights carry a factor 2^7 (m is lowered by it), so that weights down to 2^-31 of the largest are normal
+    // f16 weights carry a factor 2^7 (m is lowered by it), so that weights down to 2^-21 of the largest are normal and none
+    // above 2^-32 becomes zero
     constexpr float kLift = Tr::BF16 ? 0.f : 7.f;
     constexpr float kMost = Tr::BF16 ? 256.f : 32768.f;  // 2^(kLift + kSlack): 64 weights of at most 2^kLift stay below it
     int jobs = 0, parity = 0, q_uses = 0;

@@ -90,9 +90,10 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const Commi
 // destination each (one round trip for all 32), then row_bytes / 16 lanes copy
 // a row 16 bytes each, kMoves of them in flight before the first is stored.
 // What bounds it: memory traffic.  4096 rows of 8 x 8 pairs, 256 bytes each, K
-// and V: 41 us for 268 MB read and written, 6.5 TB/s (a plain copy's rate); 512
-// rows of 4 x 8 pairs: 9 us from a cold cache, its chain of dependent reads (kept
-// position, table, row).
+// and V: 42 us for 268 MB read and written, of which DRAM moves 222 MB in that
+// time (5.2 TB/s; the last writes leave L2 later).  256 or 512 rows of 4 x 8
+// pairs: 11 us from a cold cache, its chain of dependent reads (kept position,
+// table, row).
 constexpr int kMoves = 8;
 
 __device__ __forceinline__ void move_rows(const EvictArgs& a, int s, int kvh, const int32_t* kept, int i0, int n) {
@@ -162,12 +163,11 @@ __global__ void __launch_bounds__(kGatherWarps * 32) evict_gather_kernel(const E
 // memory; beyond, the weights are read again (from L2) in each pass.  (Keys in
 // registers took the same passes unrolled 32 times, whose code alone, fetched
 // once per launch, cost microseconds: 16.4 against 12.5 us for 4 x 8 pairs of
-// 4096 positions with their moves.)
+// 300 to 1100 positions with their moves.)
 //
 // What bounds it: the chain of passes and barriers in few CTAs.  4 x 8 pairs of
-// 4096 positions: 6.0 us (9200 cycles: reading the length and the weights 3600,
-// digits 3900, counting and writing 1600); 8 x 8 pairs of 32768 positions: 24 us
-// in one CTA each, 18 us in two.  (Moving few rows in the same CTA instead of a
+// 300 to 1100 positions: 7.2 us, of 4096: 8.3 us; 8 x 8 pairs of 32768 positions:
+// 24 us in one CTA each, 18 us in two.  (Moving few rows in the same CTA instead of a
 // second, overlapping launch was slower: 21.9 against 18 us for 256 rows of 32
 // pairs, at the time.)
 constexpr int kSelThreads = 1024;
