@@ -53,8 +53,10 @@ typedef enum {
   PA_F16 = 1,
   PA_BF16 = 2,
   PA_FP8_E4M3 = 3, /* OCP E4M3: 1 sign, 4 exponent (bias 7), 3 mantissa; max 448 */
-  PA_INT8 = 4      /* signed 8-bit code with a per-KV-head scale and zero point:
+  PA_INT8 = 4,     /* signed 8-bit code with a per-KV-head scale and zero point:
                       value = (code - zero_point) * scale */
+  PA_INT4 = 5      /* 4-bit codes 0 .. 15 with a scale and a zero per token and KV head
+                      (float16): value = code * scale + zero.  See "4-bit caches" */
 } pa_dtype;
 
 typedef enum {
@@ -77,6 +79,23 @@ typedef enum {
 #define PA_DEVERR_QUERY 64u   /* q_starts not ascending within [0, num_tokens], or a sequence of more than max_q_len queries */
 #define PA_DEVERR_PATH 128u   /* a tree path longer than its row, or a node outside its sequence's tree */
 #define PA_DEVERR_INTERNAL 32u /* a sizing invariant of the library failed (a bug; the result is wrong) */
+
+/*
+ * 4-bit caches (PA_INT4; head_dim 128)
+ *   A pool is [num_blocks][num_kv_heads] tiles of block_size * (head_dim / 2 + 4)
+ *   bytes: first the codes of the tile's rows, head_dim / 2 bytes each, then each
+ *   row's pair (scale, zero) of float16.  The 32-bit word w of a row's codes
+ *   (little endian) holds its values 8 w .. 8 w + 7: value 8 w + 2 j + e in bits
+ *   16 e + 4 j .. 16 e + 4 j + 3.
+ *   Written by pa_norm_rope_and_cache, pa_rope_and_cache and
+ *   pa_reshape_and_cache: zero = float16(smallest value of the row), scale =
+ *   float16((largest - zero) / 15), code = (x - zero) / scale rounded to the
+ *   nearest of 0 .. 15 (ties to even; 0 where scale is 0).  The bounds are clipped
+ *   to +-2^15; NaN does not count for them and takes code 0.  Any finite pair may
+ *   be stored by the caller.
+ *   Read by pa_attend and pa_read_cache.  pa_copy_blocks copies its blocks
+ *   (block_bytes = num_kv_heads tiles).  The other calls refuse it.
+ */
 
 /*
  * pa_decode_workspace_bytes
@@ -417,7 +436,8 @@ size_t pa_decode_noalloc_capacity(void);
  *   q, q_out       [num_tokens][num_heads][head_dim] at q_stride / q_out_stride
  *                  elements per token; q_out may be q itself (in place) but
  *                  must not overlap it otherwise
- *   k, v, caches, slot_mapping, scales, opt   as pa_reshape_and_cache_ex
+ *   k, v, caches, slot_mapping, scales, opt   as pa_reshape_and_cache_ex (and
+ *                  4-bit caches)
  *   positions      int64 [num_tokens]
  *   inv_freq       float32 [rotary_dim / 2]
  *   rotary_dim     even, 2 <= rotary_dim <= head_dim
@@ -431,6 +451,64 @@ int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t 
                       int num_tokens, int num_kv_heads, int head_dim, int block_size,
                       const float* k_inv_scale, const float* v_inv_scale,
                       const pa_cache_write_options* opt, void* stream);
+
+/*
+ * pa_norm_rope_and_cache - pa_rope_and_cache with a norm of the queries and keys
+ * of each head before they are turned, in the same pass.
+ *
+ * A row x (head_dim values of one token and head) of q, and of k, becomes
+ *     y_c = x_c * (sum_i x_i^2 / head_dim + eps)^(-1/2) * (weight[c] + weight_offset)
+ * in float32 (a row whose squares overflow float32 becomes 0 where it is finite);
+ * y is turned as pa_rope_and_cache turns x, without a rounding
+ * in between, and stored as there.  q_weight or k_weight NULL: that tensor is not
+ * normalised.  rotary_dim may be 0: nothing is turned, and positions and inv_freq
+ * may be NULL.
+ *
+ *   norm           q_weight, k_weight  [head_dim], weight_dtype F32/F16/BF16
+ *                  weight_offset       added to every weight (1 where models store
+ *                                      weight - 1)
+ *                  eps                 >= 0, finite
+ *   the rest as pa_rope_and_cache
+ */
+typedef struct pa_norm_options {
+  size_t struct_size;
+  const void* q_weight;
+  const void* k_weight;
+  int32_t weight_dtype;
+  float weight_offset;
+  float eps;
+} pa_norm_options;
+
+int pa_norm_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, int num_heads,
+                           const void* k, const void* v, pa_dtype src_dtype, int64_t k_stride, int64_t v_stride,
+                           void* k_cache, void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                           const int64_t* positions, const int64_t* slot_mapping, const float* inv_freq,
+                           int rotary_dim, int interleaved, float rope_scale,
+                           int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                           const pa_norm_options* norm, const float* k_inv_scale, const float* v_inv_scale,
+                           const pa_cache_write_options* opt, void* stream);
+
+/*
+ * pa_read_cache - cached rows as values: for every token n and KV head h,
+ *     k_out[n][h][:] = the K row at slot slot_mapping[n], widened (and, for 8- and
+ *     4-bit caches, dequantised) in float32 and rounded once to out_dtype;
+ * v_out likewise.  The opposite of pa_reshape_and_cache: for what takes a
+ * sequence's rows out of the pool (another type of cache, another process, a
+ * dense kernel over a prompt).  slot < 0 is padding: its rows of k_out and v_out
+ * are left as they were; a slot outside the pool sets PA_DEVERR_SLOT and leaves
+ * them too.  Slots may repeat.
+ *
+ *   k_out, v_out   [num_tokens][num_kv_heads][head_dim] at k_out_stride /
+ *                  v_out_stride elements per token, out_dtype F32/F16/BF16,
+ *                  16-byte aligned rows, apart from each other and from the caches
+ *   caches, scales as pa_decode
+ *   opt            k_zero_point / v_zero_point (INT8) and pdl, as
+ *                  pa_reshape_and_cache_ex
+ */
+int pa_read_cache(void* k_out, void* v_out, pa_dtype out_dtype, int64_t k_out_stride, int64_t v_out_stride,
+                  const void* k_cache, const void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                  const float* k_scale, const float* v_scale, const int64_t* slot_mapping, int num_tokens,
+                  int num_kv_heads, int head_dim, int block_size, const pa_cache_write_options* opt, void* stream);
 
 /*
  * pa_attend - attention of ragged query rows over the paged cache, with

@@ -14,7 +14,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libpagedattn.so")
 HEADER = os.path.join(os.path.dirname(PKG_DIR), "include", "pa.h")
 
-PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3, PA_INT8 = 0, 1, 2, 3, 4
+PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3, PA_INT8, PA_INT4 = 0, 1, 2, 3, 4, 5
 PA_OK = 0
 PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_DTYPE, PA_ERR_UNSUPPORTED = -1, -2, -3, -4
 PA_ERR_WORKSPACE, PA_ERR_CUDA, PA_ERR_ALIGN = -5, -6, -7
@@ -43,6 +43,15 @@ class CacheWriteOptions(ctypes.Structure):
 
     def __init__(self, **kw):
         super().__init__(struct_size=ctypes.sizeof(CacheWriteOptions), **kw)
+
+
+class NormOptions(ctypes.Structure):
+    """pa_norm_options (include/pa.h)."""
+    _fields_ = [("struct_size", ctypes.c_size_t), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("weight_dtype", ctypes.c_int32), ("weight_offset", ctypes.c_float), ("eps", ctypes.c_float)]
+
+    def __init__(self, **kw):
+        super().__init__(struct_size=ctypes.sizeof(NormOptions), **kw)
 
 
 class AttendOptions(ctypes.Structure):
@@ -76,6 +85,11 @@ _SIGNATURES = {
     "pa_rope_and_cache": (_i32, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _i64, _i64, _vp, _vp, _i32, _i64, _vp,
                                  _vp, _vp, _i32, _i32, _f32, _i32, _i32, _i32, _i32, _vp, _vp,
                                  ctypes.POINTER(CacheWriteOptions), _vp]),
+    "pa_norm_rope_and_cache": (_i32, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _i64, _i64, _vp, _vp, _i32, _i64, _vp,
+                                      _vp, _vp, _i32, _i32, _f32, _i32, _i32, _i32, _i32, ctypes.POINTER(NormOptions),
+                                      _vp, _vp, ctypes.POINTER(CacheWriteOptions), _vp]),
+    "pa_read_cache": (_i32, [_vp, _vp, _i32, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                             ctypes.POINTER(CacheWriteOptions), _vp]),
     "pa_attend": (_i32, [_vp, _i32, _vp, _i32, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32,
                          _i32, _i32, _i32, _i32, _f32, _i32, _vp, _sz, ctypes.POINTER(AttendOptions), _vp]),
     "pa_attend_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32]),
@@ -231,6 +245,20 @@ def dtype_code(t) -> int:
     return code
 
 
+def cache_dtype_code(cache) -> int:
+    """The type of a cache pool: 4-bit pools are uint8 [blocks, H_kv, tile bytes] (int4_cache_shape), the others
+    [blocks, H_kv, block_size, d] of their own type."""
+    if cache.dim() == 3 and cache.dtype is _torch().uint8:
+        return PA_INT4
+    return dtype_code(cache)
+
+
+def int4_cache_shape(num_blocks, num_kv_heads, block_size, head_dim=128):
+    """Shape of a 4-bit pool (torch.uint8): per block and KV head the codes of block_size rows, then their (scale, zero)
+    float16 pairs."""
+    return (int(num_blocks), int(num_kv_heads), int(block_size) * (int(head_dim) // 2 + 4))
+
+
 def _ptr(t):
     # a plain integer: the signatures declare void*, so ctypes converts it
     return None if t is None else t.data_ptr()
@@ -361,7 +389,8 @@ def reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, block_size, *, k_inv
                       k_zero_point=None, v_zero_point=None, stream=None, pdl=False):
     """Write rows k[n], v[n] ([N, H_kv, d]) to cache slots slot_mapping[n] (pa_reshape_and_cache).
 
-    INT8 caches (torch.int8) also take int32 per-KV-head zero points (pa_reshape_and_cache_ex).
+    INT8 caches (torch.int8) also take int32 per-KV-head zero points (pa_reshape_and_cache_ex).  4-bit caches
+    (int4_cache_shape) take neither scales nor zero points: each row gets its own.
     pdl=True: programmatic dependent launch (pa_reshape_and_cache_ex): the kernel waits for the kernel before
     it on the stream before touching memory, so only its launch overlaps that kernel's end.  A decode with pdl
     right after it may then start early as well: after copy_blocks or commit_tree, leave pdl off here.
@@ -375,8 +404,13 @@ def reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, block_size, *, k_inv
     for t in (k, v):
         if t.stride(2) != 1 or t.stride(1) != D:
             raise ValueError("k/v rows must be contiguous per token")
+    code = cache_dtype_code(k_cache)
+    if code == PA_INT4:
+        for t in (k_cache, v_cache):
+            if t.dtype is not k_cache.dtype or tuple(t.shape) != int4_cache_shape(k_cache.shape[0], Hkv, block_size, D):
+                raise ValueError("4-bit caches must be uint8 of int4_cache_shape(blocks, H_kv, block_size, d)")
     args = (_ptr(k), _ptr(v), dtype_code(k), k.stride(0), v.stride(0),
-            _ptr(k_cache), _ptr(v_cache), dtype_code(k_cache), k_cache.shape[0],
+            _ptr(k_cache), _ptr(v_cache), code, k_cache.shape[0],
             _ptr(slot_mapping), N, Hkv, D, int(block_size), _ptr(k_inv_scale), _ptr(v_inv_scale))
     if k_zero_point is not None or v_zero_point is not None or pdl:
         opt = CacheWriteOptions(k_zero_point=_ptr(k_zero_point), v_zero_point=_ptr(v_zero_point),

@@ -1,5 +1,5 @@
-"""Torch marshalling of the operators around the cache (include/pa.h): rotary positions with the cache write,
-attention with score modifiers, drafted trees, eviction by attention weight.
+"""Torch marshalling of the operators around the cache (include/pa.h): norms and rotary positions with the cache write,
+rows read back, attention with score modifiers, drafted trees, eviction by attention weight.
 
 Argument checks and pointers only, as in ``_lib``: every step runs in the library's kernels.  All tensors of a call
 are on one device; the call runs on that device, on `stream` or its current stream.
@@ -11,21 +11,21 @@ import ctypes
 import math
 
 from . import _lib
-from ._lib import (PA_ERR_SHAPE, SIZE_MAX, AttendOptions, CacheWriteOptions, PagedAttnError, _check, _ptr, dtype_code,
-                   load)
+from ._lib import (PA_ERR_SHAPE, PA_INT4, SIZE_MAX, AttendOptions, CacheWriteOptions, NormOptions, PagedAttnError, _check,
+                   _ptr, dtype_code, int4_cache_shape, load)
 
 _OPT_SIZE = ctypes.sizeof(AttendOptions)
 
 _torch = _CODES = _raw_stream = _get_device = None
-_I32 = _I64 = _F32 = None
+_I32 = _I64 = _F32 = _U8 = None
 
 
 def _t():
     """torch and the few names of it that a call looks up (the per-step path), bound once."""
-    global _torch, _CODES, _raw_stream, _get_device, _I32, _I64, _F32
+    global _torch, _CODES, _raw_stream, _get_device, _I32, _I64, _F32, _U8
     if _torch is None:
         import torch
-        _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+        _I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
         _raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         dtype_code(torch.empty(0))
         _CODES = _lib._DTYPE_CODES
@@ -95,11 +95,22 @@ def _row_stride(name, t, tokens, heads, dim):
 def _cache(k_cache, v_cache, block_size):
     """(blocks, KV heads, head size) of the two pools."""
     shape = k_cache.shape
-    if len(shape) != 4 or shape[2] != block_size or not k_cache.is_contiguous():
-        raise ValueError(f"k_cache must be contiguous [blocks, H_kv, {block_size}, d], not {tuple(shape)}")
+    if len(shape) == 3 and k_cache.dtype is _U8:  # 4 bits
+        dim = 2 * (shape[2] // block_size - 4) if block_size > 0 else 0
+        if dim <= 0 or shape != int4_cache_shape(shape[0], shape[1], block_size, dim) or not k_cache.is_contiguous():
+            raise ValueError(f"a 4-bit k_cache must be contiguous, of int4_cache_shape(blocks, H_kv, {block_size}), not "
+                             f"{tuple(shape)}")
+    else:
+        if len(shape) != 4 or shape[2] != block_size or not k_cache.is_contiguous():
+            raise ValueError(f"k_cache must be contiguous [blocks, H_kv, {block_size}, d], not {tuple(shape)}")
+        dim = shape[3]
     if v_cache.shape != shape or v_cache.dtype is not k_cache.dtype or not v_cache.is_contiguous():
         raise ValueError("v_cache must be contiguous, of the shape and type of k_cache")
-    return shape[0], shape[1], shape[3]
+    return shape[0], shape[1], dim
+
+
+def _cache_code(k_cache):
+    return PA_INT4 if k_cache.dtype is _U8 and k_cache.dim() == 3 else _code(k_cache)
 
 
 def _heads_params(num_kv_heads, scales, zero_points):
@@ -140,20 +151,16 @@ def rope_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, orig
     return f.float()
 
 
-def rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, block_size, *, q_out=None,
-                   interleaved=False, rope_scale=1.0, k_inv_scale=None, v_inv_scale=None, k_zero_point=None,
-                   v_zero_point=None, pdl=False, stream=None):
-    """Rotary positions of q and k, and the cache write of k and v (pa_rope_and_cache).
-
-    q [N, H_q, d], k / v [N, H_kv, d]; positions and slot_mapping int64 [N]; inv_freq float32 [rotary_dim / 2].
-    The turned q goes to q_out (default: q itself), the turned k and v into their slots; tokens with a negative slot
-    are padding and left alone.  pdl as in reshape_and_cache.  Returns q_out.
-    """
-    _torch or _t()
+def _write_rotated(norm, q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, block_size, q_out, interleaved,
+                   rope_scale, k_inv_scale, v_inv_scale, k_zero_point, v_zero_point, pdl, stream):
+    """rope_and_cache (norm None) and norm_rope_and_cache (norm: q_weight, k_weight, eps, weight_offset)."""
     if q_out is None:
         q_out = q
+    qw = kw = None
+    if norm is not None:
+        qw, kw = norm[:2]
     dev = _on_one_device(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, q_out, k_inv_scale, v_inv_scale,
-                         k_zero_point, v_zero_point)
+                         k_zero_point, v_zero_point, qw, kw)
     N, Hq, D = q.shape
     blocks, Hkv, dim = _cache(k_cache, v_cache, block_size)
     if dim != D:
@@ -165,9 +172,19 @@ def rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq,
     qos = qs if q_out is q else _row_stride("q_out", q_out, N, Hq, D)
     ks, vs = _row_stride("k", k, N, Hkv, D), _row_stride("v", v, N, Hkv, D)
     tokens = (N,)
-    _need("positions", positions, _I64, tokens)
     _need("slot_mapping", slot_mapping, _I64, tokens)
-    _need("inv_freq", inv_freq, _F32, inv_freq.shape[:1])
+    pos = freq = None
+    pairs = 0
+    if inv_freq is not None:
+        _need("inv_freq", inv_freq, _F32, inv_freq.shape[:1])
+        pairs = inv_freq.shape[0]
+    if positions is not None:
+        _need("positions", positions, _I64, tokens)
+        pos = positions.data_ptr()
+    elif pairs:
+        raise ValueError("inv_freq needs positions")
+    if pairs:
+        freq = inv_freq.data_ptr()
     opt = ki = vi = None
     if k_inv_scale is not None or v_inv_scale is not None:
         _heads_params(Hkv, (k_inv_scale, v_inv_scale), (k_zero_point, v_zero_point))
@@ -175,11 +192,77 @@ def rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq,
     if k_zero_point is not None or v_zero_point is not None or pdl:
         opt = ctypes.byref(CacheWriteOptions(k_zero_point=_ptr(k_zero_point), v_zero_point=_ptr(v_zero_point),
                                              pdl=1 if pdl else 0))
-    _issue(load().pa_rope_and_cache, dev, stream, q_out.data_ptr(), qos, q.data_ptr(), qs, Hq, k.data_ptr(), v.data_ptr(),
-           _code(q), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), _code(k_cache), blocks, positions.data_ptr(),
-           slot_mapping.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, rope_scale, N,
-           Hkv, D, int(block_size), ki, vi, opt)
+    args = (q_out.data_ptr(), qos, q.data_ptr(), qs, Hq, k.data_ptr(), v.data_ptr(), _code(q), ks, vs, k_cache.data_ptr(),
+            v_cache.data_ptr(), _cache_code(k_cache), blocks, pos, slot_mapping.data_ptr(), freq, 2 * pairs,
+            1 if interleaved else 0, rope_scale, N, Hkv, D, int(block_size))
+    if norm is None:
+        _issue(load().pa_rope_and_cache, dev, stream, *args, ki, vi, opt)
+        return q_out
+    wd = 0
+    for name, w in (("q_weight", qw), ("k_weight", kw)):
+        if w is not None:
+            _need(name, w, w.dtype, (D,))
+            wd = _code(w)
+    if qw is not None and kw is not None and qw.dtype is not kw.dtype:
+        raise ValueError("q_weight and k_weight must have one type")
+    _issue(load().pa_norm_rope_and_cache, dev, stream, *args,
+           ctypes.byref(NormOptions(q_weight=_ptr(qw), k_weight=_ptr(kw), weight_dtype=wd, weight_offset=norm[3],
+                                    eps=norm[2])), ki, vi, opt)
     return q_out
+
+
+def rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, block_size, *, q_out=None,
+                   interleaved=False, rope_scale=1.0, k_inv_scale=None, v_inv_scale=None, k_zero_point=None,
+                   v_zero_point=None, pdl=False, stream=None):
+    """Rotary positions of q and k, and the cache write of k and v (pa_rope_and_cache).
+
+    q [N, H_q, d], k / v [N, H_kv, d]; positions and slot_mapping int64 [N]; inv_freq float32 [rotary_dim / 2].
+    The turned q goes to q_out (default: q itself), the turned k and v into their slots; tokens with a negative slot
+    are padding and left alone.  pdl as in reshape_and_cache.  Returns q_out.
+    """
+    _torch or _t()
+    return _write_rotated(None, q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, block_size, q_out,
+                          interleaved, rope_scale, k_inv_scale, v_inv_scale, k_zero_point, v_zero_point, pdl, stream)
+
+
+def norm_rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, block_size, *, q_weight=None,
+                        k_weight=None, eps=1e-6, weight_offset=0.0, q_out=None, interleaved=False, rope_scale=1.0,
+                        k_inv_scale=None, v_inv_scale=None, k_zero_point=None, v_zero_point=None, pdl=False, stream=None):
+    """rope_and_cache with a norm of each head's query and key row first (pa_norm_rope_and_cache):
+    x / sqrt(mean(x^2) + eps) * (weight + weight_offset), in float32 and not rounded before the turn.
+
+    q_weight / k_weight [d] (float32, float16 or bfloat16); None: that tensor is not normalised.  positions and inv_freq
+    may be None: nothing is turned.  4-bit caches (int4_cache_shape) need no scales.  Returns q_out.
+    """
+    _torch or _t()
+    return _write_rotated((q_weight, k_weight, float(eps), float(weight_offset)), q, k, v, k_cache, v_cache, positions,
+                          slot_mapping, inv_freq, block_size, q_out, interleaved, rope_scale, k_inv_scale, v_inv_scale,
+                          k_zero_point, v_zero_point, pdl, stream)
+
+
+def read_cache(k_out, v_out, k_cache, v_cache, slot_mapping, block_size, *, k_scale=None, v_scale=None,
+               k_zero_point=None, v_zero_point=None, pdl=False, stream=None):
+    """Cached rows as values (pa_read_cache): k_out[n, h] and v_out[n, h] (float32, float16 or bfloat16 [N, H_kv, d])
+    receive the rows at slot_mapping[n] (int64 [N]; negative: left as they were), dequantised.  Returns (k_out, v_out).
+    """
+    _torch or _t()
+    dev = _on_one_device(k_cache, v_cache, k_out, v_out, slot_mapping, k_scale, v_scale, k_zero_point, v_zero_point)
+    blocks, Hkv, D = _cache(k_cache, v_cache, block_size)
+    if k_out.dtype is not v_out.dtype:
+        raise ValueError("k_out and v_out must have one type")
+    N = k_out.shape[0]
+    ks, vs = _row_stride("k_out", k_out, N, Hkv, D), _row_stride("v_out", v_out, N, Hkv, D)
+    _need("slot_mapping", slot_mapping, _I64, (N,))
+    opt = None
+    if k_scale is not None or v_scale is not None:
+        _heads_params(Hkv, (k_scale, v_scale), (k_zero_point, v_zero_point))
+    if k_zero_point is not None or v_zero_point is not None or pdl:
+        opt = ctypes.byref(CacheWriteOptions(k_zero_point=_ptr(k_zero_point), v_zero_point=_ptr(v_zero_point),
+                                             pdl=1 if pdl else 0))
+    _issue(load().pa_read_cache, dev, stream, k_out.data_ptr(), v_out.data_ptr(), _code(k_out), ks, vs,
+           k_cache.data_ptr(), v_cache.data_ptr(), _cache_code(k_cache), blocks, _ptr(k_scale), _ptr(v_scale),
+           slot_mapping.data_ptr(), N, Hkv, D, int(block_size), opt)
+    return k_out, v_out
 
 
 def attend_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, max_q_len,
@@ -237,7 +320,7 @@ def _attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_le
                                          _ptr(prefix_lens), _ptr(tree_mask), words, _ptr(mass), mseq, mhead,
                                          1 if pdl else 0))
     _issue(load().pa_attend, dev, stream, out.data_ptr(), _code(out), q.data_ptr(), _code(q), qs, k_cache.data_ptr(),
-           v_cache.data_ptr(), _code(k_cache), blocks, _ptr(k_scale), _ptr(v_scale), block_tables.data_ptr(), width,
+           v_cache.data_ptr(), _cache_code(k_cache), blocks, _ptr(k_scale), _ptr(v_scale), block_tables.data_ptr(), width,
            seq_lens.data_ptr(), starts, int(max_q_len), N, S, Hq, Hkv, D, scale, int(block_size), ws, wb, opt)
     return out
 
@@ -313,7 +396,7 @@ def commit_tree(k_cache, v_cache, block_tables, seq_lens, q_starts, path, path_l
     _need("q_starts", q_starts, _I32, (S + 1,))
     _need("path_lens", path_lens, _I32, seqs)
     _need("new_lens", new_lens, _I32, seqs)
-    _issue(load().pa_commit_tree, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), _code(k_cache), blocks,
+    _issue(load().pa_commit_tree, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), _cache_code(k_cache), blocks,
            block_tables.data_ptr(), width, seq_lens.data_ptr(), q_starts.data_ptr(), path.data_ptr(),
            path_lens.data_ptr(), deep, new_lens.data_ptr(), S, Hkv, D, int(block_size))
     return new_lens
@@ -340,7 +423,7 @@ def evict(k_cache, v_cache, mass, block_tables, seq_lens, dst_tables, kept, mass
     mseq, mhead = _mass_strides("mass", mass, S, Hkv)
     if mass.shape[2] < width * block_size:
         raise ValueError("mass rows must hold block_tables.shape[1] * block_size positions")
-    _issue(load().pa_evict, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), _code(k_cache), blocks, mass.data_ptr(),
+    _issue(load().pa_evict, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), _cache_code(k_cache), blocks, mass.data_ptr(),
            mseq, mhead, block_tables.data_ptr(), width, seq_lens.data_ptr(), dst_tables.data_ptr(), dst_width,
            kept.data_ptr(), mass_out.data_ptr(), new_lens.data_ptr(), S, Hkv, D, int(block_size), int(budget), int(recent), int(sinks))
     return kept

@@ -28,6 +28,8 @@ SOURCES = [
     "pa_cache.cu",
     "pa_ops_api.cu",
     "pa_rope.cu",
+    "pa_norm.cu",
+    "pa_read.cu",
     "pa_attend.cu",
     "pa_evict.cu",
     "pa_decode_dispatch.cu",

@@ -9,7 +9,7 @@
 #include <mutex>
 
 #include "pa_common.cuh"
-#include "pa_kernels.h"
+#include "pa_ops.h"
 
 #define PA_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -494,7 +494,9 @@ PA_EXPORT int pa_reshape_and_cache_ex(const void* k, const void* v, pa_dtype src
   if (!k || !v || !k_cache || !v_cache || !slot_mapping) return PA_ERR_NULL;
   if (src_dtype != PA_F16 && src_dtype != PA_BF16) return PA_ERR_DTYPE;
   const bool quant = kv_dtype == PA_FP8_E4M3 || kv_dtype == PA_INT8;
-  if (kv_dtype != src_dtype && !quant) return PA_ERR_DTYPE;
+  if (kv_dtype != src_dtype && !quant && kv_dtype != PA_INT4) return PA_ERR_DTYPE;
+  if (kv_dtype == PA_INT4 && (head_dim != 128 || block_size < 8 || block_size > 1024 || (block_size & (block_size - 1)) != 0))
+    return PA_ERR_UNSUPPORTED;
   if (quant && (!k_inv_scale || !v_inv_scale)) return PA_ERR_NULL;
   if (kv_dtype == PA_INT8 && (!o.k_zero_point || !o.v_zero_point)) return PA_ERR_NULL;
   const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
@@ -526,6 +528,13 @@ PA_EXPORT int pa_reshape_and_cache_ex(const void* k, const void* v, pa_dtype src
   a.k_zero_point = o.k_zero_point;
   a.v_zero_point = o.v_zero_point;
   a.pdl = o.pdl != 0;
+  if (kv_dtype == PA_INT4) {  // the norms' kernel, without queries, norms and positions
+    pa::NormArgs n;
+    memset(&n, 0, sizeof(n));
+    n.r.w = a;
+    return cuda_status(pa::launch_norm_rope_and_cache(n, static_cast<cudaStream_t>(stream)),
+                       "pa_reshape_and_cache launch");
+  }
   return cuda_status(pa::launch_reshape_and_cache(a, static_cast<cudaStream_t>(stream)),
                      "pa_reshape_and_cache launch");
 }

@@ -203,12 +203,16 @@ struct f16_t {};
 struct bf16_t {};
 struct e4m3_t {};
 struct i8_t {};  // INT8 code with a per-KV-head scale and zero point
+struct i4_t {};  // 4-bit code with a scale and a zero of its row's own (tiles of codes, then pairs: include/pa.h)
 
 template <typename T> struct elem;
 template <> struct elem<f16_t> { static constexpr int bytes = 2; using storage = uint16_t; };
 template <> struct elem<bf16_t> { static constexpr int bytes = 2; using storage = uint16_t; };
 template <> struct elem<e4m3_t> { static constexpr int bytes = 1; using storage = uint8_t; };
 template <> struct elem<i8_t> { static constexpr int bytes = 1; using storage = int8_t; };
+
+// Bytes of a 4-bit row: its codes, and its (scale, zero) pair.
+__host__ __device__ constexpr int int4_row_bytes(int head_dim) { return head_dim / 2 + 4; }
 
 // Widen two packed 16-bit values (one 32-bit word) to a float2 (x = low half).
 template <typename T> __device__ __forceinline__ float2 widen2(uint32_t w);

@@ -23,6 +23,38 @@ struct RopeArgs {
 
 cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream);
 
+struct NormArgs {
+  RopeArgs r;  // rotary_dim 0: no positions; num_heads 0: no queries
+  const void* q_weight;  // nullptr: that tensor is not normalised
+  const void* k_weight;
+  int weight_dtype;
+  float weight_offset;
+  float eps;
+};
+// Also the write into a 4-bit cache (no weights).
+cudaError_t launch_norm_rope_and_cache(const NormArgs& a, cudaStream_t stream);
+
+struct ReadArgs {
+  void* k_out;
+  void* v_out;
+  int out_dtype;
+  int64_t k_stride, v_stride;
+  const void* k_cache;
+  const void* v_cache;
+  int kv_dtype;
+  int64_t num_blocks;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* k_zero_point;
+  const int32_t* v_zero_point;
+  const int64_t* slots;
+  int64_t num_tokens;
+  int num_kv_heads, head_dim, block_size, block_shift;
+  unsigned int* err;
+  bool pdl;
+};
+cudaError_t launch_read_cache(const ReadArgs& a, cudaStream_t stream);
+
 // A pa_status: PA_ERR_WORKSPACE before anything is enqueued, or that of the launches.
 int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 // (size_t)-1 when the device cannot be asked

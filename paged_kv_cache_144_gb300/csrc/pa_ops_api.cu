@@ -1,6 +1,6 @@
 // pa_ops_api.cu - the extern "C" entry points of the operators around the
-// cache (rotary cache write, attention with score modifiers, tree commit,
-// eviction): argument validation and dispatch.  No call here allocates device
+// cache (rotary cache write with and without norms, rows read back, attention
+// with score modifiers, tree commit, eviction): argument validation and dispatch.  No call here allocates device
 // memory.
 #include <cmath>
 #include <cstring>
@@ -20,7 +20,11 @@ constexpr int kMaxPath = 256;          // rows a CTA of the commit holds in regi
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool is8bit(int dt) { return dt == PA_FP8_E4M3 || dt == PA_INT8; }
-bool cache_dtype(int dt) { return dt == PA_F16 || dt == PA_BF16 || is8bit(dt); }
+bool cache_dtype(int dt) { return dt == PA_F16 || dt == PA_BF16 || is8bit(dt) || dt == PA_INT4; }
+// A tile of a 4-bit cache is whole 16-byte pieces, and its rows a word per 8 values of 128.
+bool int4_shape(int head_dim, int block_size) {
+  return head_dim == 128 && block_size >= 8 && block_size <= 1024 && (block_size & (block_size - 1)) == 0;
+}
 
 // The cache's shape, shared by every call here.
 int check_cache(int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int kv_dtype) {
@@ -29,6 +33,7 @@ int check_cache(int num_kv_heads, int head_dim, int block_size, int max_blocks_p
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (num_kv_heads > kMaxHeads) return PA_ERR_UNSUPPORTED;
   if (is8bit(kv_dtype) && (head_dim != 128 || num_kv_heads > pa::kMaxHeadParams)) return PA_ERR_UNSUPPORTED;
+  if (kv_dtype == PA_INT4 && head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (block_size < 8 || block_size > 1024 || (block_size & (block_size - 1)) != 0) return PA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(max_blocks_per_seq) * block_size >= (int64_t{1} << 26)) return PA_ERR_SHAPE;
   return PA_OK;
@@ -66,13 +71,15 @@ bool overlaps_rows(const void* out, int64_t out_bytes, const void* q, int64_t ro
 
 }  // namespace
 
-PA_EXPORT int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, int num_heads,
-                                const void* k, const void* v, pa_dtype src_dtype, int64_t k_stride, int64_t v_stride,
-                                void* k_cache, void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
-                                const int64_t* positions, const int64_t* slot_mapping, const float* inv_freq,
-                                int rotary_dim, int interleaved, float rope_scale, int num_tokens, int num_kv_heads,
-                                int head_dim, int block_size, const float* k_inv_scale, const float* v_inv_scale,
-                                const pa_cache_write_options* opt, void* stream) {
+namespace {
+
+// pa_rope_and_cache (norm == nullptr) and pa_norm_rope_and_cache.
+int write_rotated(const char* where, const pa_norm_options* norm, void* q_out, int64_t q_out_stride, const void* q,
+                  int64_t q_stride, int num_heads, const void* k, const void* v, pa_dtype src_dtype, int64_t k_stride,
+                  int64_t v_stride, void* k_cache, void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                  const int64_t* positions, const int64_t* slot_mapping, const float* inv_freq, int rotary_dim,
+                  int interleaved, float rope_scale, int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                  const float* k_inv_scale, const float* v_inv_scale, const pa_cache_write_options* opt, void* stream) {
   pa_cache_write_options o;
   memset(&o, 0, sizeof(o));
   if (opt) {
@@ -83,12 +90,17 @@ PA_EXPORT int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q
     return PA_ERR_SHAPE;
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (num_heads > kMaxHeads || num_kv_heads > kMaxHeads) return PA_ERR_UNSUPPORTED;
-  if (rotary_dim < 2 || rotary_dim > head_dim || rotary_dim % 2 != 0) return PA_ERR_SHAPE;
+  if (rotary_dim < (norm ? 0 : 2) || rotary_dim > head_dim || rotary_dim % 2 != 0) return PA_ERR_SHAPE;
+  if (norm && !(norm->eps >= 0.f && norm->eps < INFINITY)) return PA_ERR_SHAPE;
   if (num_tokens == 0) return PA_OK;
-  if (!q_out || !q || !k || !v || !k_cache || !v_cache || !positions || !slot_mapping || !inv_freq)
-    return PA_ERR_NULL;
+  if (!q_out || !q || !k || !v || !k_cache || !v_cache || !slot_mapping) return PA_ERR_NULL;
+  if (rotary_dim > 0 && (!positions || !inv_freq)) return PA_ERR_NULL;
   if (src_dtype != PA_F16 && src_dtype != PA_BF16) return PA_ERR_DTYPE;
-  if (kv_dtype != src_dtype && !is8bit(kv_dtype)) return PA_ERR_DTYPE;
+  if (kv_dtype != src_dtype && !is8bit(kv_dtype) && kv_dtype != PA_INT4) return PA_ERR_DTYPE;
+  if (norm && (norm->q_weight || norm->k_weight) && norm->weight_dtype != PA_F32 && norm->weight_dtype != PA_F16 &&
+      norm->weight_dtype != PA_BF16)
+    return PA_ERR_DTYPE;
+  if (kv_dtype == PA_INT4 && !int4_shape(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
   if (is8bit(kv_dtype) && (!k_inv_scale || !v_inv_scale)) return PA_ERR_NULL;
   if (kv_dtype == PA_INT8 && (!o.k_zero_point || !o.v_zero_point)) return PA_ERR_NULL;
   const int64_t qrow = static_cast<int64_t>(num_heads) * head_dim, row = static_cast<int64_t>(num_kv_heads) * head_dim;
@@ -97,9 +109,16 @@ PA_EXPORT int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(k_cache) ||
       !aligned16(v_cache) || q_stride % 8 != 0 || q_out_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0)
     return PA_ERR_ALIGN;
+  if (norm) {
+    const uintptr_t most = norm->weight_dtype == PA_F32 ? 3u : 1u;
+    if (((reinterpret_cast<uintptr_t>(norm->q_weight) | reinterpret_cast<uintptr_t>(norm->k_weight)) & most) != 0)
+      return PA_ERR_ALIGN;
+  }
   unsigned int* err = pa::device_error_word();
   if (!err) return PA_ERR_CUDA;
-  pa::RopeArgs a;
+  pa::NormArgs n;
+  memset(&n, 0, sizeof(n));
+  pa::RopeArgs& a = n.r;
   a.q_out = q_out;
   a.q_out_stride = q_out_stride;
   a.q = q;
@@ -131,7 +150,114 @@ PA_EXPORT int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q
   w.k_zero_point = o.k_zero_point;
   w.v_zero_point = o.v_zero_point;
   w.pdl = o.pdl != 0;
-  return pa::cuda_status(pa::launch_rope_and_cache(a, static_cast<cudaStream_t>(stream)), "pa_rope_and_cache launch");
+  if (!norm && kv_dtype != PA_INT4)
+    return pa::cuda_status(pa::launch_rope_and_cache(a, static_cast<cudaStream_t>(stream)), where);
+  if (norm) {
+    n.q_weight = norm->q_weight;
+    n.k_weight = norm->k_weight;
+    n.weight_dtype = norm->weight_dtype;
+    n.weight_offset = norm->weight_offset;
+    n.eps = norm->eps;
+  }
+  return pa::cuda_status(pa::launch_norm_rope_and_cache(n, static_cast<cudaStream_t>(stream)), where);
+}
+
+}  // namespace
+
+PA_EXPORT int pa_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, int num_heads,
+                                const void* k, const void* v, pa_dtype src_dtype, int64_t k_stride, int64_t v_stride,
+                                void* k_cache, void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                                const int64_t* positions, const int64_t* slot_mapping, const float* inv_freq,
+                                int rotary_dim, int interleaved, float rope_scale, int num_tokens, int num_kv_heads,
+                                int head_dim, int block_size, const float* k_inv_scale, const float* v_inv_scale,
+                                const pa_cache_write_options* opt, void* stream) {
+  return write_rotated("pa_rope_and_cache launch", nullptr, q_out, q_out_stride, q, q_stride, num_heads, k, v, src_dtype,
+                       k_stride, v_stride, k_cache, v_cache, kv_dtype, num_blocks, positions, slot_mapping, inv_freq,
+                       rotary_dim, interleaved, rope_scale, num_tokens, num_kv_heads, head_dim, block_size, k_inv_scale,
+                       v_inv_scale, opt, stream);
+}
+
+PA_EXPORT int pa_norm_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, int num_heads,
+                                     const void* k, const void* v, pa_dtype src_dtype, int64_t k_stride,
+                                     int64_t v_stride, void* k_cache, void* v_cache, pa_dtype kv_dtype,
+                                     int64_t num_blocks, const int64_t* positions, const int64_t* slot_mapping,
+                                     const float* inv_freq, int rotary_dim, int interleaved, float rope_scale,
+                                     int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                                     const pa_norm_options* norm, const float* k_inv_scale, const float* v_inv_scale,
+                                     const pa_cache_write_options* opt, void* stream) {
+  if (!norm) return PA_ERR_NULL;
+  if (norm->struct_size < sizeof(size_t)) return PA_ERR_SHAPE;
+  pa_norm_options n;
+  memset(&n, 0, sizeof(n));
+  memcpy(&n, norm, norm->struct_size < sizeof(n) ? norm->struct_size : sizeof(n));
+  return write_rotated("pa_norm_rope_and_cache launch", &n, q_out, q_out_stride, q, q_stride, num_heads, k, v, src_dtype,
+                       k_stride, v_stride, k_cache, v_cache, kv_dtype, num_blocks, positions, slot_mapping, inv_freq,
+                       rotary_dim, interleaved, rope_scale, num_tokens, num_kv_heads, head_dim, block_size, k_inv_scale,
+                       v_inv_scale, opt, stream);
+}
+
+PA_EXPORT int pa_read_cache(void* k_out, void* v_out, pa_dtype out_dtype, int64_t k_out_stride, int64_t v_out_stride,
+                            const void* k_cache, const void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                            const float* k_scale, const float* v_scale, const int64_t* slot_mapping, int num_tokens,
+                            int num_kv_heads, int head_dim, int block_size, const pa_cache_write_options* opt,
+                            void* stream) {
+  pa_cache_write_options o;
+  memset(&o, 0, sizeof(o));
+  if (opt) {
+    if (opt->struct_size < sizeof(size_t)) return PA_ERR_SHAPE;
+    memcpy(&o, opt, opt->struct_size < sizeof(o) ? opt->struct_size : sizeof(o));
+  }
+  if (num_tokens < 0 || num_kv_heads <= 0) return PA_ERR_SHAPE;
+  if (!cache_dtype(kv_dtype)) return PA_ERR_DTYPE;
+  // (8-bit rows of 64 too: the writes make them)
+  if ((head_dim != 64 && head_dim != 128) || num_kv_heads > kMaxHeads) return PA_ERR_UNSUPPORTED;
+  if (kv_dtype == PA_INT4 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (block_size < 8 || block_size > 1024 || (block_size & (block_size - 1)) != 0) return PA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PA_OK;
+  if (!k_out || !v_out || !slot_mapping) return PA_ERR_NULL;
+  if (out_dtype != PA_F32 && out_dtype != PA_F16 && out_dtype != PA_BF16) return PA_ERR_DTYPE;
+  if (is8bit(kv_dtype) && (!k_scale || !v_scale)) return PA_ERR_NULL;
+  if (kv_dtype == PA_INT8 && (!o.k_zero_point || !o.v_zero_point)) return PA_ERR_NULL;
+  const int ps = check_pool(k_cache, v_cache, num_blocks, num_kv_heads, block_size);
+  if (ps != PA_OK) return ps;
+  const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (k_out_stride < row || v_out_stride < row) return PA_ERR_SHAPE;
+  const int64_t piece = out_dtype == PA_F32 ? 4 : 8;  // elements of 16 bytes
+  if (!aligned16(k_out) || !aligned16(v_out) || k_out_stride % piece != 0 || v_out_stride % piece != 0) return PA_ERR_ALIGN;
+  const int64_t bytes = out_dtype == PA_F32 ? 4 : 2;
+  if (k_out == v_out ||
+      overlaps_rows(k_out, ((num_tokens - 1) * k_out_stride + row) * bytes, v_out, num_tokens, row * bytes,
+                    v_out_stride * bytes)) {
+    // (rows of one buffer may alternate: K and V side by side in each token's row)
+    const int64_t apart = static_cast<int64_t>(reinterpret_cast<intptr_t>(v_out) - reinterpret_cast<intptr_t>(k_out));
+    const int64_t stride = k_out_stride * bytes, at = ((apart % stride) + stride) % stride;
+    if (k_out_stride != v_out_stride || at < row * bytes || at + row * bytes > stride) return PA_ERR_SHAPE;
+  }
+  pa::ReadArgs a;
+  memset(&a, 0, sizeof(a));
+  a.err = pa::device_error_word();
+  if (!a.err) return PA_ERR_CUDA;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.out_dtype = out_dtype;
+  a.k_stride = k_out_stride;
+  a.v_stride = v_out_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.kv_dtype = kv_dtype;
+  a.num_blocks = num_blocks;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.k_zero_point = o.k_zero_point;
+  a.v_zero_point = o.v_zero_point;
+  a.slots = slot_mapping;
+  a.num_tokens = num_tokens;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.block_size = block_size;
+  a.block_shift = shift_of(block_size);
+  a.pdl = o.pdl != 0;
+  return pa::cuda_status(pa::launch_read_cache(a, static_cast<cudaStream_t>(stream)), "pa_read_cache launch");
 }
 
 PA_EXPORT size_t pa_attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
@@ -245,6 +371,7 @@ PA_EXPORT int pa_commit_tree(void* k_cache, void* v_cache, pa_dtype kv_dtype, in
                              void* stream) {
   const int sh = check_cache(num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype);
   if (sh != PA_OK) return sh;
+  if (kv_dtype == PA_INT4) return PA_ERR_UNSUPPORTED;
   if (num_seqs < 0 || max_path < 1) return PA_ERR_SHAPE;
   if (max_path > kMaxPath || num_seqs > 65535) return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
@@ -281,6 +408,7 @@ PA_EXPORT int pa_evict(void* k_cache, void* v_cache, pa_dtype kv_dtype, int64_t 
                        int head_dim, int block_size, int budget, int recent, int sinks, void* stream) {
   const int sh = check_cache(num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype);
   if (sh != PA_OK) return sh;
+  if (kv_dtype == PA_INT4) return PA_ERR_UNSUPPORTED;
   const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * block_size;
   if (num_seqs < 0 || budget < 1 || budget >= (1 << 26) || recent < 0 || sinks < 0 || max_dst_blocks < 1 ||
       static_cast<int64_t>(recent) + sinks > budget)
