@@ -523,7 +523,7 @@ int pa_read_cache(void* k_out, void* v_out, pa_dtype out_dtype, int64_t k_out_st
  *     z_t = z_t - slopes[h] * |P - t|              when slopes is given
  *     out = sum_t softmax(z)_t v_t                 over the visible t < T
  * Visible are
- *     t <= P, and with a window only t > P - window;
+ *     t <= P, and with a window only t > P - window or t < sinks;
  *     and also every t < prefix_lens[s] when prefix_lens is given;
  *   or, when tree_mask is given (the queries are the nodes of a tree of
  *   drafted tokens, their rows in the cache at T - L .. T - 1),
@@ -563,7 +563,9 @@ int pa_read_cache(void* k_out, void* v_out, pa_dtype out_dtype, int64_t k_out_st
  *   softcap        0 = off, or 2^-10 <= softcap <= 512 (the capped score is off by
  *                  up to about 2^-21 softcap)
  *   slopes         float32 [num_heads], or NULL
- *   window         >= 0; 0 = off.  Not together with prefix_lens or tree_mask
+ *   window         >= 0; 0 = off.  Not together with prefix_lens or tree_mask.
+ *                  Entries of block_tables whose blocks no query of the sequence
+ *                  sees are not read
  *   prefix_lens    int32 [num_seqs], or NULL (values above T count as T)
  *   tree_mask      uint64 [num_tokens][tree_words], or NULL; bit j % 64 of word
  *                  j / 64.  max_q_len <= 64 * tree_words.  Not together with
@@ -578,6 +580,10 @@ int pa_read_cache(void* k_out, void* v_out, pa_dtype out_dtype, int64_t k_out_st
  *   k_zero_point / v_zero_point   as pa_decode_options
  *   pdl            as pa_decode_options, but nothing at all is read before the
  *                  kernel before this call has finished
+ *   sinks          >= 0: with a window, the first `sinks` positions of each
+ *                  sequence stay visible (t <= P still holds).  Their distance
+ *                  to the query is the real one, |P - t|.  Without a window it
+ *                  changes nothing.  Not together with prefix_lens or tree_mask
  */
 typedef struct pa_attend_options {
   size_t struct_size;
@@ -593,6 +599,7 @@ typedef struct pa_attend_options {
   int64_t mass_stride_seq;
   int64_t mass_stride_head;
   int32_t pdl;
+  int32_t sinks;
 } pa_attend_options;
 
 int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype, int64_t q_stride,

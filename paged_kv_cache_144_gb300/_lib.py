@@ -60,7 +60,7 @@ class AttendOptions(ctypes.Structure):
                 ("v_zero_point", ctypes.c_void_p), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
                 ("window", ctypes.c_int32), ("prefix_lens", ctypes.c_void_p), ("tree_mask", ctypes.c_void_p),
                 ("tree_words", ctypes.c_int32), ("mass", ctypes.c_void_p), ("mass_stride_seq", ctypes.c_int64),
-                ("mass_stride_head", ctypes.c_int64), ("pdl", ctypes.c_int32)]
+                ("mass_stride_head", ctypes.c_int64), ("pdl", ctypes.c_int32), ("sinks", ctypes.c_int32)]
 
     def __init__(self, *args, **kw):
         if args:                                   # every field in order, struct_size first

@@ -276,7 +276,7 @@ def attend_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_si
 
 
 def _attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_len, num_kv_heads, scale, block_size,
-            workspace, k_scale, v_scale, k_zero_point, v_zero_point, softcap, slopes, window, prefix_lens, tree_mask,
+            workspace, k_scale, v_scale, k_zero_point, v_zero_point, softcap, slopes, window, sinks, prefix_lens, tree_mask,
             mass, pdl, stream):
     _torch or _t()
     dev = _on_one_device(q, out, k_cache, v_cache, block_tables, seq_lens, q_starts, workspace, k_scale, v_scale,
@@ -301,7 +301,7 @@ def _attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_le
         _heads_params(Hkv, (k_scale, v_scale), (k_zero_point, v_zero_point))
     ws, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     opt = None
-    if softcap or window or pdl or k_zero_point is not None or v_zero_point is not None or slopes is not None or \
+    if softcap or window or sinks or pdl or k_zero_point is not None or v_zero_point is not None or slopes is not None or \
             prefix_lens is not None or tree_mask is not None or mass is not None:
         words = mseq = mhead = 0
         if slopes is not None:
@@ -318,7 +318,7 @@ def _attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_le
                 raise ValueError("mass rows must hold block_tables.shape[1] * block_size positions")
         opt = ctypes.byref(AttendOptions(_OPT_SIZE, _ptr(k_zero_point), _ptr(v_zero_point), softcap, _ptr(slopes), int(window),
                                          _ptr(prefix_lens), _ptr(tree_mask), words, _ptr(mass), mseq, mhead,
-                                         1 if pdl else 0))
+                                         1 if pdl else 0, int(sinks)))
     _issue(load().pa_attend, dev, stream, out.data_ptr(), _code(out), q.data_ptr(), _code(q), qs, k_cache.data_ptr(),
            v_cache.data_ptr(), _cache_code(k_cache), blocks, _ptr(k_scale), _ptr(v_scale), block_tables.data_ptr(), width,
            seq_lens.data_ptr(), starts, int(max_q_len), N, S, Hq, Hkv, D, scale, int(block_size), ws, wb, opt)
@@ -336,18 +336,18 @@ def _mass_strides(name, mass, seqs, heads):
 
 def attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_len, num_kv_heads, scale, block_size, *,
            workspace=None, k_scale=None, v_scale=None, k_zero_point=None, v_zero_point=None, softcap=0.0, slopes=None,
-           window=0, prefix_lens=None, pdl=False, stream=None):
+           window=0, prefix_lens=None, sinks=0, pdl=False, stream=None):
     """Attention of ragged query rows (prompt chunks, decode steps) over the paged cache (pa_attend).
 
     q, out [N, H_q, d]: sequence s owns rows q_starts[s] .. q_starts[s + 1] - 1 (q_starts int32 [S + 1]; None: one
     query per sequence), its newest positions; max_q_len >= the most queries of one sequence.
     softcap > 0: scores softcap * tanh(score / softcap).  slopes [H_q]: - slopes[h] * distance is added.
-    window > 0: the last `window` positions only.  prefix_lens int32 [S]: the first positions are seen by all queries.
+    window > 0: the last `window` positions only, and the first `sinks`.  prefix_lens int32 [S]: the first positions are seen by all queries.
     workspace: new_workspace(attend_workspace_bytes(...)), not shared by calls that may overlap.
     """
     return _attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_len, num_kv_heads, scale,
                    block_size, workspace, k_scale, v_scale, k_zero_point, v_zero_point, softcap, slopes, window,
-                   prefix_lens, None, None, pdl, stream)
+                   sinks, prefix_lens, None, None, pdl, stream)
 
 
 def attend_tree(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_len, tree_mask, num_kv_heads, scale,
@@ -362,20 +362,20 @@ def attend_tree(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_
     if tree_mask is None:
         raise ValueError("attend_tree needs tree_mask")
     return _attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_len, num_kv_heads, scale,
-                   block_size, workspace, k_scale, v_scale, k_zero_point, v_zero_point, softcap, None, 0, None,
+                   block_size, workspace, k_scale, v_scale, k_zero_point, v_zero_point, softcap, None, 0, 0, None,
                    tree_mask, None, pdl, stream)
 
 
 def attend_accumulate(out, q, k_cache, v_cache, block_tables, seq_lens, mass, num_kv_heads, scale, block_size, *,
                       workspace=None, k_scale=None, v_scale=None, k_zero_point=None, v_zero_point=None, softcap=0.0,
-                      slopes=None, window=0, prefix_lens=None, pdl=False, stream=None):
+                      slopes=None, window=0, prefix_lens=None, sinks=0, pdl=False, stream=None):
     """One decode step (q [S, H_q, d]) that also adds each position's attention weight, summed over the KV head's
     query heads, to mass[s, kv_head, position] (float32; pa_attend with the mass option)."""
     if mass is None:
         raise ValueError("attend_accumulate needs mass")
     return _attend(out, q, k_cache, v_cache, block_tables, seq_lens, None, 1, num_kv_heads, scale, block_size,
-                   workspace, k_scale, v_scale, k_zero_point, v_zero_point, softcap, slopes, window, prefix_lens, None,
-                   mass, pdl, stream)
+                   workspace, k_scale, v_scale, k_zero_point, v_zero_point, softcap, slopes, window, sinks, prefix_lens,
+                   None, mass, pdl, stream)
 
 
 def commit_tree(k_cache, v_cache, block_tables, seq_lens, q_starts, path, path_lens, new_lens, block_size, *,

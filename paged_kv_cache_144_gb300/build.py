@@ -31,6 +31,10 @@ SOURCES = [
     "pa_norm.cu",
     "pa_read.cu",
     "pa_attend.cu",
+    "pa_attend_tc_f16.cu",
+    "pa_attend_tc_bf16.cu",
+    "pa_attend_tc_fp8.cu",
+    "pa_attend_tc_int8.cu",
     "pa_evict.cu",
     "pa_decode_dispatch.cu",
     "pa_decode_f16.cu",
@@ -42,6 +46,8 @@ SOURCES = [
     "pa_decode_append8.cu",
     "pa_decode_attend16.cu",
     "pa_decode_attend8.cu",
+    "pa_decode_sinks16.cu",
+    "pa_decode_sinks8.cu",
 ]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

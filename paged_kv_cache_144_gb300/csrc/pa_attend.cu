@@ -2,6 +2,7 @@
 // score modifiers, and the accumulation of each cached position's weight.
 #include <cstring>
 
+#include "pa_attend_plan.h"
 #include "pa_attend_tc.cuh"
 
 namespace pa {
@@ -48,24 +49,10 @@ int smaller_shape(int num_seqs) {  // the next smaller of them, or 0
   return n <= 64 ? n / 2 : n - shape_step(n);
 }
 
-// How a call of these sizes runs, and what it keeps in the workspace.
-struct Plan {
-  enum Kind { kFew, kTensor } kind;
-  int cg;                     // kTensor: CTAs that share a tile (1, or a cluster of 2)
-  int paired;                 // kTensor: the streams are two row tiles
-  int seg_rows;               // kTensor: rows of a segment
-  DecodeKey key;              // kFew: the decode kernel's variant and geometry
-  DecodeGeometry geo;
-  int ctas;
-  int rec_rows, slots;
-  size_t num_counters;
-  size_t records, pending, stats, scores, bytes;  // offsets of the parts, total
-  int score_stride;
-};
-
-// prefer: the kernel to plan for where both may serve such a call, or -1: the one that does.
+// prefer: the kernel to plan for where both may serve such a call, or -1: the one that does.  span: positions of a sequence that
+// count for that choice.
 bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
-               int max_q_len, int q_dtype, int kv_dtype, bool tree, bool accumulate, int prefer, Plan* pl) {
+               int max_q_len, int q_dtype, int kv_dtype, bool tree, bool accumulate, bool sinks, int64_t span, int prefer, Plan* pl) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -79,7 +66,7 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
   pl->paired = rows > static_cast<int64_t>(rps) * pl->cg ? 1 : 0;
   pl->seg_rows = rps * pl->cg * (pl->paired ? 2 : 1);
   const int few = tuning_override("PA_ATTEND_FEW_ROWS");  // tuning
-  const int64_t positions = static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq * block_size;
+  const int64_t positions = static_cast<int64_t>(num_seqs) * num_kv_heads * span;
   const bool chosen = prefer >= 0 ? prefer == Plan::kFew : few >= 0 ? rows <= few : few_rows(rows, positions, q8);
   const bool is_few = rows <= kFewRows && (accumulate || chosen);
   pl->kind = is_few ? Plan::kFew : Plan::kTensor;
@@ -92,7 +79,7 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
     pl->key.head_dim = head_dim;
     pl->key.gmax = gm;
     pl->key.unit_rows = q8 && block_size >= 16 && gm == 8 ? 64 : 32;
-    pl->key.append = 2;
+    pl->key.append = sinks ? 3 : 2;
     pl->key.row_groups = gm == 16 ? static_cast<int>((rows + 15) / 16) : 1;
     if (!decode_geometry(pl->key, shape_seqs(num_seqs), &pl->geo)) return false;
     const size_t warps = static_cast<size_t>(pl->geo.ctas) * pl->geo.warps_per_cta;
@@ -167,98 +154,6 @@ cudaError_t launch_few(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaS
   return launch_decode(pl.key, pl.geo, p, tk, tv, stream, a.pdl);
 }
 
-// 4-D view of a 16-bit pool: {64 elements, 8 rows, 128-byte halves of a row, groups of 8 rows}; one box = box_rows
-// rows, landing as [group][half][8 rows][128 bytes], swizzled by row.
-bool encode_tile_map(CUtensorMap* map, const void* cache, int64_t rows, int head_dim, int box_rows, int box_halves) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
-  const cuuint64_t row_bytes = static_cast<cuuint64_t>(head_dim) * 2;
-  const cuuint32_t halves = static_cast<cuuint32_t>(row_bytes / 128);
-  cuuint64_t dims[4] = {64, 8, halves, static_cast<cuuint64_t>(rows / 8)};
-  cuuint64_t strides[3] = {row_bytes, 128, 8 * row_bytes};
-  cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(box_halves), static_cast<cuuint32_t>(box_rows / 8)};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(cache), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 2-D view of an 8-bit pool: {row bytes, rows}; one box = box_rows rows of box_bytes bytes, as they are.
-bool encode_code_map(CUtensorMap* map, const void* cache, int64_t rows, int row_bytes, int box_rows, int box_bytes) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes), static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(cache), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 4-D view of the query rows: {64 elements, heads, tokens, 128-byte halves of a row}; one box = 128 / group tokens by the
-// group's heads, landing as [half][token, head][128 bytes], swizzled by row; zero past the last token.
-bool encode_query_map(CUtensorMap* map, const AttendParams& a) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
-  const cuuint32_t halves = static_cast<cuuint32_t>(a.head_dim / 64);
-  cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(a.num_heads), static_cast<cuuint64_t>(a.num_tokens), halves};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.head_dim) * 2, static_cast<cuuint64_t>(a.q_stride) * 2, 128};
-  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.group), static_cast<cuuint32_t>(kTile / a.group), halves};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(a.q), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <typename KVT, int D, int CG, bool SPLIT>
-cudaError_t launch_tc_as(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream) {
-  using Tr = TcTraits<KVT, D, CG>;
-  TcParams p;
-  p.a = a;
-  p.paired = pl.paired;
-  p.seg_rows = pl.seg_rows;
-  p.max_segments = static_cast<float>(a.num_seqs) * a.num_kv_heads * ((a.max_q_len * a.group + pl.seg_rows - 1) / pl.seg_rows);
-  p.rec_rows = pl.rec_rows;
-  p.slots = pl.slots;
-  p.counters = reinterpret_cast<int*>(ws);
-  p.records = reinterpret_cast<float*>(ws + pl.records);
-  CUtensorMap tk, tv, tq;
-  const int64_t rows = a.num_blocks * a.num_kv_heads * a.block_size;
-  auto box = [&](int most) { return a.block_size < most ? a.block_size : most; };
-  const bool maps = Tr::B8 ? encode_code_map(&tk, a.k_cache, rows, D, box(Tr::KROWS), D) &&
-                                 encode_code_map(&tv, a.v_cache, rows, D, box(kTile), D / CG)
-                           : encode_tile_map(&tk, a.k_cache, rows, D, box(Tr::KROWS), Tr::NH) &&
-                                 encode_tile_map(&tv, a.v_cache, rows, D, box(kTile), Tr::VH);
-  if (!maps || !encode_query_map(&tq, a)) return cudaErrorInvalidValue;
-  auto kern = attend_tc_kernel<KVT, D, CG, SPLIT>;
-  const size_t smem = Tr::smem_bytes(a.num_seqs);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pl.ctas);
-  cfg.blockDim = dim3(Tr::THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.pdl ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, tk, tv, tq, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-template <typename KVT, int D, int CG>
-cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream) {
-  // the second product is free where memory traffic bounds the call, and wanted where the output keeps its precision
-  return !pl.paired || a.out_dtype == PA_F32 ? launch_tc_as<KVT, D, CG, true>(a, pl, ws, stream)
-                                             : launch_tc_as<KVT, D, CG, false>(a, pl, ws, stream);
-}
-
 // mass[s][kvh][t] += sum over the group of exp2(score - max) / sum, from the stored scores, whose heads stand side by side:
 // kMassKeys positions per thread, a CTA's threads on consecutive ones.  (A weight is known only when its row's last position
 // has been seen, so the attention stores the scores and this kernel follows.)
@@ -272,16 +167,16 @@ __global__ void __launch_bounds__(kMassThreads) attend_add_mass_kernel(const Att
   if (v.L != 1) return;
   const RowBounds rb = row_bounds(p, v, seq_prefix(p, s, v.T), 0);
   const int t0 = blockIdx.x * kMassThreads * kMassKeys;
-  if (t0 + kMassThreads * kMassKeys <= rb.lo || t0 >= rb.hi) return;
+  if ((t0 + kMassThreads * kMassKeys <= rb.lo && t0 >= rb.sinks) || t0 >= rb.hi) return;
   const int64_t row0 = static_cast<int64_t>(s) * p.num_heads + kvh * G;
   const float* const sc = p.scores + (static_cast<int64_t>(s) * p.num_kv_heads + kvh) * p.score_stride * G;
   float* const mass = p.mass + s * p.mass_stride_seq + kvh * p.mass_stride_head;
   float sum[kMassKeys] = {}, old[kMassKeys];
-  bool in[kMassKeys];  // (scores outside [lo, hi) were not stored)
+  bool in[kMassKeys];  // (scores that the row does not see were not stored)
 #pragma unroll
   for (int k = 0; k < kMassKeys; ++k) {
     const int t = t0 + k * kMassThreads + threadIdx.x;
-    in[k] = t >= rb.lo && t < rb.hi;
+    in[k] = (t >= rb.lo || t < rb.sinks) && t < rb.hi;
     old[k] = in[k] ? mass[t] : 0.f;
   }
   auto add = [&](int k, float z, float2 ml, float inv) { sum[k] = fmaf(exp2f(z - ml.x), inv, sum[k]); };
@@ -330,7 +225,7 @@ __global__ void __launch_bounds__(kMassThreads) attend_add_mass_kernel(const Att
 
 size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                               int max_blocks_per_seq, int max_q_len, int kv_dtype, bool accumulate) {
-  // The largest need on either kernel, with and without a tree, with either query type that the caches take, and of calls with
+  // The largest need on either kernel, with and without a tree or sinks, with either query type that the caches take, and of calls with
   // fewer sequences, queries or blocks: records change with the launch shape (shape_seqs; all else grows with the batch and its
   // blocks), and where the rows fill another 16 up to 64, a stream or a pair.
   const int group = num_heads / num_kv_heads, per_stream = stream_rows(group) / group;
@@ -338,7 +233,7 @@ size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int
                       64 / group, 64 / group + 1, per_stream,     per_stream + 1, 2 * per_stream, max_q_len};
   constexpr int kLens = sizeof(lens) / sizeof(lens[0]);
   size_t most = 0;
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 16; ++i) {
     const int q_dtype = i & 1 ? PA_BF16 : PA_F16, prefer = i & 2 ? Plan::kFew : Plan::kTensor;
     if ((kv_dtype == PA_F16 || kv_dtype == PA_BF16) && q_dtype != kv_dtype) continue;
     for (int x = 0; x < kLens; ++x) {
@@ -349,7 +244,7 @@ size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int
       for (int seqs = num_seqs > 1 ? num_seqs : 1; seqs >= 1; seqs = smaller_shape(seqs)) {
         Plan pl;
         if (!make_plan(seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, len, q_dtype, kv_dtype,
-                       (i & 4) != 0, accumulate, prefer, &pl))
+                       (i & 4) != 0, accumulate, (i & 8) != 0, 1, prefer, &pl))
           return static_cast<size_t>(-1);
         most = pl.bytes > most ? pl.bytes : most;
       }
@@ -361,8 +256,11 @@ size_t attend_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int
 int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   (void)cudaGetLastError();
   Plan pl;
+  int64_t span = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
+  if (p.sinks > 0 && span > static_cast<int64_t>(p.window) + p.sinks + p.max_q_len)
+    span = static_cast<int64_t>(p.window) + p.sinks + p.max_q_len;
   if (!make_plan(p.num_seqs, p.num_heads, p.num_kv_heads, p.head_dim, p.block_size, p.max_blocks_per_seq, p.max_q_len,
-                 p.q_dtype, p.kv_dtype, p.tree_mask != nullptr, p.mass != nullptr, -1, &pl))
+                 p.q_dtype, p.kv_dtype, p.tree_mask != nullptr, p.mass != nullptr, p.sinks > 0, span, -1, &pl))
     return cuda_status(cudaErrorInvalidDevice, "pa_attend plan");
   if (!workspace || workspace_bytes < pl.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PA_ERR_WORKSPACE;
@@ -379,17 +277,13 @@ int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaS
   if (pl.kind == Plan::kFew) {
     e = launch_few(p, pl, ws, stream);
   } else if (p.kv_dtype == PA_FP8_E4M3) {
-    e = launch_tc<e4m3_t, 128, 2>(p, pl, ws, stream);
+    e = launch_tc_fp8(p, pl, ws, stream);
   } else if (p.kv_dtype == PA_INT8) {
-    e = launch_tc<i8_t, 128, 2>(p, pl, ws, stream);
+    e = launch_tc_int8(p, pl, ws, stream);
   } else if (p.kv_dtype == PA_F16) {
-    e = p.head_dim == 64 ? launch_tc<f16_t, 64, 1>(p, pl, ws, stream)
-        : pl.cg == 1     ? launch_tc<f16_t, 128, 1>(p, pl, ws, stream)
-                         : launch_tc<f16_t, 128, 2>(p, pl, ws, stream);
+    e = launch_tc_f16(p, pl, ws, stream);
   } else {
-    e = p.head_dim == 64 ? launch_tc<bf16_t, 64, 1>(p, pl, ws, stream)
-        : pl.cg == 1     ? launch_tc<bf16_t, 128, 1>(p, pl, ws, stream)
-                         : launch_tc<bf16_t, 128, 2>(p, pl, ws, stream);
+    e = launch_tc_bf16(p, pl, ws, stream);
   }
   if (e == cudaSuccess && p.mass) {
     const int cap = p.max_blocks_per_seq << p.block_shift;

@@ -38,14 +38,25 @@ __device__ __forceinline__ SeqView seq_view(const AttendParams& p, int s, bool r
   return v;
 }
 
-// Bounds [lo, hi) of what query i sees; with a tree, positions from `first` on
-// also need their bit.
+// First positions that stay visible under a window.  (The functions that cut the work are also compiled on their own, with
+// parameters that have none.)
+template <typename P>
+__device__ __forceinline__ auto sinks_of(const P& p, int) -> decltype(p.sinks) {
+  return p.sinks;
+}
+template <typename P>
+__device__ __forceinline__ int sinks_of(const P&, long) {
+  return 0;
+}
+// Bounds [lo, hi) of what query i sees, and below lo the first `sinks` positions;
+// with a tree, positions from `first` on also need their bit.
 struct RowBounds {
-  int pos, lo, hi;
+  int pos, lo, hi, sinks;
 };
 __device__ __forceinline__ RowBounds row_bounds(const AttendParams& p, const SeqView& v, int prefix, int i) {
   RowBounds b;
   b.pos = v.T - v.L + i;
+  b.sinks = 0;
   if (b.pos < 0) {  // more queries than tokens: nothing
     b.lo = b.hi = 0;
   } else if (p.tree_mask) {
@@ -54,8 +65,20 @@ __device__ __forceinline__ RowBounds row_bounds(const AttendParams& p, const Seq
   } else {
     b.lo = p.window > 0 ? max(0, b.pos + 1 - p.window) : 0;
     b.hi = max(b.pos + 1, prefix);
+    b.sinks = min(sinks_of(p, 0), b.lo);
   }
   return b;
+}
+// Units (of 1 << shift positions) that queries from position lo on attend when the first `sinks` positions are visible too:
+// the first su, and after a gap of `skip` of them the rest.  Unit number v of those attended is unit v, or v + skip from su on.
+struct UnitGap {
+  int su, skip;
+};
+__device__ __forceinline__ UnitGap unit_gap(int sinks, int lo, int shift) {
+  UnitGap g;
+  g.su = (min(sinks, lo) + (1 << shift) - 1) >> shift;
+  g.skip = max(0, (lo >> shift) - g.su);
+  return g;
 }
 __device__ __forceinline__ int seq_prefix(const AttendParams& p, int s, int T) {
   return p.prefix_lens ? max(0, min(__ldg(p.prefix_lens + s), T)) : 0;
@@ -126,9 +149,10 @@ __device__ __forceinline__ void attend_row(const AttendParams& p, int s, const S
   float m = -INFINITY, l = 0.f, acc[D / 32];
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
-  for (int t0 = rb.lo & ~31; t0 < rb.hi; t0 += 32) {
+  for (int t0 = rb.sinks > 0 ? 0 : rb.lo & ~31; t0 < rb.hi; t0 += 32) {
+    if (t0 >= rb.sinks && t0 + 32 <= rb.lo) t0 = rb.lo & ~31;
     const int t = t0 + lane;
-    bool see = t >= rb.lo && t < rb.hi;
+    bool see = (t >= rb.lo || t < rb.sinks) && t < rb.hi;
     if (see && p.tree_mask && t >= first) {
       const int j = t - first;
       see = (p.tree_mask[n * p.tree_words + (j >> 6)] >> (j & 63)) & 1ull;

@@ -327,7 +327,8 @@ struct TcParams {
 // Rows of one stream's tile: whole queries, as one TMA box of 128 / G queries by G heads brings them.
 __host__ __device__ __forceinline__ int stream_rows(int group) { return kTile / group * group; }
 
-// Position tiles [lo, hi) of row tile m of a sequence.
+// Position tiles [lo, hi) of row tile m of a sequence.  The tiles of sinks that lie before the window's first tile are
+// numbered as the last ones before it (first_of in the kernel).
 struct TileRange {
   int lo, hi;
 };
@@ -343,7 +344,7 @@ __device__ __forceinline__ TileRange tile_range(const AttendParams& p, const Seq
   const int first = max(0, v.T - v.L + i0);
   const int lo = p.window > 0 ? max(0, first + 1 - p.window) : 0;
   const int hi = p.tree_mask ? v.T : max(last + 1, prefix);
-  r.lo = lo / kTile;
+  r.lo = lo / kTile - min(lo / kTile, (min(sinks_of(p, 0), lo) + kTile - 1) / kTile);
   r.hi = (hi + kTile - 1) / kTile;
   return r;
 }
@@ -352,8 +353,10 @@ struct Frag {
   int s, kvh, m;      // segment
   SeqView v;
   int prefix;         // visible prefix length
-  int t0, t1;         // its position tiles
-  int lo;             // first position any row of the segment sees
+  int t0, t1;         // its position tiles (numbers: TileRange)
+  int seg_lo;         // the segment's first one
+  int lo;             // first position any row of the segment sees, but for the sinks
+  int sinks;          // positions before lo that its rows see
   int seg_start;      // cost position of the segment
   int seg_tiles;
   bool whole;
@@ -414,7 +417,9 @@ __device__ __forceinline__ bool advance_frag(FragIter& it, Frag& f, const int* p
     f.prefix = pre;
     f.t0 = tr.lo + ja;
     f.t1 = tr.lo + jb;
+    f.seg_lo = tr.lo;
     f.lo = a.window > 0 ? max(0, max(0, v.T - v.L + it.m * rpt / a.group) + 1 - a.window) : 0;
+    f.sinks = min(sinks_of(a, 0), f.lo);
     f.seg_start = seg_start;
     f.seg_tiles = n;
     f.whole = ja == 0 && jb == n;
@@ -616,7 +621,7 @@ __device__ __forceinline__ bool join_rows(const TcParams& p, const Frag& f, int 
 
 // ----------------------------------------------------------------- kernel
 
-template <typename KVT, int D, int CG, bool SPLIT>
+template <typename KVT, int D, int CG, bool SPLIT, bool SINKS>
 __global__ void __launch_bounds__(TcTraits<KVT, D, CG>::THREADS, 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const __grid_constant__ CUtensorMap tmap_q,
@@ -788,13 +793,18 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   auto row_tile = [&](int m, int t) { return p.paired ? (m * 2 + t) * CG + rank : m * CG + rank; };
 
   // V rows of a stage outside the sequence (or before the window) may hold anything, or were not loaded: zero for the
-  // products (one warp; n_hi, n_lo: the first row past the end, the first visible one)
-  auto partial = [&](int j) { return f.v.T - j * kTile < kTile || f.lo > j * kTile; };
-  auto clear_v = [&](int st, int n_hi, int n_lo) {
+  // products (one warp; n_hi, n_lo, n_sinks: the first row past the end, of the window, behind the sinks)
+  // position of tile number j's first row
+  auto first_of = [&](int j) { return (!SINKS || j >= f.lo / kTile ? j : j - f.seg_lo) * kTile; };
+  auto partial = [&](int j) {
+    const int t = first_of(j);
+    return f.v.T - t < kTile || (f.lo > t && !(SINKS && f.sinks >= t + kTile));
+  };
+  auto clear_v = [&](int st, int n_hi, int n_lo, int n_sinks) {
     const uint32_t vt = base + Tr::OFF_V + st * Tr::STAGE;
     for (int x = lane; x < kTile * Tr::VH * 8; x += 32) {
       const int r = x / (Tr::VH * 8), c = x % (Tr::VH * 8);
-      if (r >= n_hi || r < n_lo) sts128_zero(vt + (r >> 3) * Tr::VGROUP + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16);
+      if (r >= n_hi || (r < n_lo && !(SINKS && r < n_sinks))) sts128_zero(vt + (r >> 3) * Tr::VGROUP + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -802,13 +812,14 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
 
   // Boxes of this CTA's part of a K or V tile, and its first position.
   auto tile_rows = [&](bool is_v) { return is_v ? kTile : Tr::KROWS; };
-  auto tile_start = [&](bool is_v, int j) { return j * kTile + (is_v ? 0 : rank * Tr::KROWS); };
+  auto tile_start = [&](bool is_v, int j) { return first_of(j) + (is_v ? 0 : rank * Tr::KROWS); };
   // This lane's block of tile j (its table entry), or -1.
   auto tile_block = [&](bool is_v, int j) -> int {
     const int boxes = tile_rows(is_v) / min(a.block_size, tile_rows(is_v));
     const int blk = (tile_start(is_v, j) >> a.block_shift) + (boxes > 1 ? lane : 0);
     const int nblk = (f.v.T + a.block_size - 1) >> a.block_shift;
-    if (lane >= boxes || blk < (f.lo >> a.block_shift) || blk >= nblk) return -1;
+    const int sblk = SINKS ? (f.sinks + a.block_size - 1) >> a.block_shift : 0;  // blocks of sinks
+    if (lane >= boxes || (blk < (f.lo >> a.block_shift) && blk >= sblk) || blk >= nblk) return -1;
     const int pb = __ldg(a.block_tables + static_cast<int64_t>(f.s) * a.max_blocks_per_seq + blk);
     if (pb >= 0 && pb < a.num_blocks) return pb;
     raise_error(a.err, PA_DEVERR_BLOCK_ID);
@@ -915,7 +926,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             const int st = (kt - 1) % NST;
             if (!(ok = wait(Tr::VL + st, (vl >> st) & 1u))) break;
             vl ^= 1u << st;
-            clear_v(st, f.v.T - j * kTile, f.lo - j * kTile);
+            const int t = first_of(j);
+            clear_v(st, f.v.T - t, f.lo - t, f.sinks - t);
             if (lane == 0) mbar_arrive(bar(Tr::VF + st));
           }
           if (++j >= t1) break;
@@ -1117,7 +1129,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           }
           {
             if (!(ok = wait(Tr::RVF + r, rph) && wait(Tr::VE + st, eph))) break;
-            const int n_hi = f.v.T - j * kTile, n_lo = f.lo - j * kTile;
+            const int t = first_of(j), n_hi = f.v.T - t, n_lo = f.lo - t, n_sinks = f.sinks - t;
             uint4 w[PER];
 #pragma unroll
             for (int k = 0; k < PER; ++k) w[k] = lds128(base + Tr::OFF_RV + r * Tr::RAW + (k * 128 + tid) * 16);
@@ -1126,7 +1138,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
               const int x = k * 128 + tid, row = x >> 2, c = 2 * (x & 3);
               uint4 lo, hi;
               widen16(w[k], zv2, lo, hi);
-              if (row >= n_hi || row < n_lo) lo = hi = make_uint4(0u, 0u, 0u, 0u);  // outside the sequence or the window
+              if (row >= n_hi || (row < n_lo && !(SINKS && row < n_sinks))) lo = hi = make_uint4(0u, 0u, 0u, 0u);  // outside the sequence or the window
               uint8_t* const to = sm + Tr::OFF_V + st * Tr::STAGE + (row >> 3) * Tr::VGROUP + (row & 7) * 128;
               *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) = lo;
               *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) << 4)) = hi;
@@ -1210,14 +1222,15 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           }
           if (warp_on) {
             // positions of the half: 32 from tb, 32 from tb + gap on
-            const int tb = j * kTile + half * (CG == 1 ? kHalfTile : 32);
+            const int tb = first_of(j) + half * (CG == 1 ? kHalfTile : 32);
             constexpr int kGap = CG == 1 ? 32 : kHalfTile;
             const uint32_t ps = ts + half * kHalfTile;  // the half's scores; its weights replace them (hi, then lo)
             float z[kHalfTile];
 #pragma unroll
             for (int c = 0; c < kHalfTile; c += 32) tmem_ld32(ps + c, z + c);
             tmem_wait_ld();
-            const bool full = rb.lo <= tb && rb.hi >= tb + kGap + 32 && (!tree || tb + kGap + 32 <= first);
+            const bool full = (rb.lo <= tb || (SINKS && min(a.sinks, rb.lo) >= tb + kGap + 32)) && rb.hi >= tb + kGap + 32 &&
+                              (!tree || tb + kGap + 32 <= first);
             const bool masked = !__all_sync(0xffffffffu, full || !valid);
             // z: scores in the log2 domain, or (the plain case) raw products that the exponent's FMA scales by mul
             float mul = sc2;
@@ -1247,7 +1260,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 const int b0 = tb + kGap * c;
                 // bits [lo, hi) of this 32-position chunk
                 const int lo = max(0, min(32, rb.lo - b0)), hi = max(0, min(32, rb.hi - b0));
-                uint32_t see = (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & (lo >= 32 ? 0u : 0xffffffffu << lo);
+                uint32_t from = lo >= 32 ? 0u : 0xffffffffu << lo;
+                if constexpr (SINKS) {
+                  const int sk = min(32, min(a.sinks, rb.lo) - b0);
+                  if (sk > 0) from |= sk >= 32 ? 0xffffffffu : (1u << sk) - 1u;
+                }
+                uint32_t see = (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & from;
                 if (tree && valid) see &= tree_bits(tree, a.tree_words, first, b0);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) z[32 * c + k] = (see >> k) & 1u ? z[32 * c + k] : -INFINITY;

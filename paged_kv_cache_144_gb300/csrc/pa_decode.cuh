@@ -64,7 +64,7 @@
 //    same recurrence after its own unit loop, one row per lane, writes
 //    out[s, kvh*G .. kvh*G+G-1] and resets the counter.  Nothing waits on
 //    another warp, so the kernel cannot deadlock.
-//  * The variants of pa_attend (AP = 2) add the score modifiers, masks, ragged
+//  * The variants of pa_attend (AP = 2; 3: with sinks) add the score modifiers, masks, ragged
 //    query rows and stored scores of include/pa.h; every difference is behind
 //    `if constexpr`, so the decode's own variants compile to what they were.
 //    They see the call through DecodeParams::att.  Against the decode's own
@@ -159,6 +159,8 @@ __device__ __forceinline__ int clamped_len(const DecodeParams& p, int s, bool re
 struct WorkIter {
   int s, kvh, j, jend, j0, T;
   int L;          // pa_attend: queries of the sequence
+  int su, skip;   // with sinks: attended units before the gap that they leave, and its units (unit_gap)
+  int sinks;      // positions before lo that are attended too
   int nu;         // units of the segment that are attended (from unit ulo on)
   int ulo;        // first attended unit of the sequence
   int lo;         // first attended position (sliding window), 0 without one
@@ -209,7 +211,7 @@ __device__ __forceinline__ int window_lo(const DecodeParams& p, int T, int q_len
 // sequence of it.u is found by scanning forward from it, one or two
 // shared-memory reads per fragment, not a search over the whole batch.
 // (ATT: the variants of pa_attend keep each sequence's query count after the lengths.)
-template <bool ATT>
+template <bool ATT, bool SINKS>
 __device__ __forceinline__ bool frag_balanced(WorkIter& it, const int* prefix, const DecodeParams& p, int ur_shift) {
   const int Hkv = p.num_kv_heads;
   const int beta = p.frag_cost;
@@ -234,11 +236,20 @@ __device__ __forceinline__ bool frag_balanced(WorkIter& it, const int* prefix, c
     it.T = prefix[p.num_seqs + 1 + s];  // clamped length, cached by the prologue
     if constexpr (ATT) it.L = prefix[2 * p.num_seqs + 1 + s];
     it.lo = window_lo(p, it.T, ATT ? it.L : p.q_len);
-    it.ulo = it.lo >> ur_shift;
     it.kvh = kvh;
-    it.j0 = it.ulo + ja;
+    if constexpr (SINKS) {
+      it.sinks = min(p.att.sinks, it.lo);
+      const UnitGap g = unit_gap(it.sinks, it.lo, ur_shift);
+      it.su = g.su;
+      it.skip = g.skip;
+      it.j0 = ja + (ja >= g.su ? g.skip : 0);
+      it.jend = jb + (jb > g.su ? g.skip : 0);
+    } else {
+      it.ulo = it.lo >> ur_shift;
+      it.j0 = it.ulo + ja;
+      it.jend = it.ulo + jb;
+    }
     it.j = it.j0;
-    it.jend = it.ulo + jb;
     it.fend = fend;
     const bool whole = ja == 0 && jb == nu;
     it.slot = whole ? -1 : it.gw * 2 + (it.frag_idx == 0 ? 0 : 1);
@@ -280,7 +291,15 @@ __device__ __forceinline__ void frag_fixed(WorkIter& it, const int* prefix, cons
   it.slot = (parts == 1) ? -1 : it.r;
 }
 
-template <bool ATT>
+// To the fragment's next unit; false behind its last one.
+template <bool SINKS>
+__device__ __forceinline__ bool next_unit(WorkIter& it) {
+  if (++it.j == it.jend) return false;
+  if constexpr (SINKS) it.j += it.j == it.su ? it.skip : 0;
+  return true;
+}
+
+template <bool ATT, bool SINKS>
 __device__ __forceinline__ void iter_next_fragment(WorkIter& it, const int* prefix, const DecodeParams& p,
                                                    bool fixed, int ur_shift) {
   it.frag_idx++;
@@ -290,7 +309,7 @@ __device__ __forceinline__ void iter_next_fragment(WorkIter& it, const int* pref
     frag_fixed(it, prefix, p, ur_shift);
   } else {
     it.u = it.fend;
-    if (!frag_balanced<ATT>(it, prefix, p, ur_shift)) it.valid = false;
+    if (!frag_balanced<ATT, SINKS>(it, prefix, p, ur_shift)) it.valid = false;
   }
 }
 
@@ -429,7 +448,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   const int BOX = unit_in_block ? UR : B;
   const int upb_shift = unit_in_block ? p.block_shift - Tr::UR_SHIFT : 0;  // log2(units per block)
   const int bpu_shift = unit_in_block ? 0 : Tr::UR_SHIFT - p.block_shift;  // log2(blocks per unit)
-  constexpr bool ATT = AP == 2;  // a pa_attend call: score modifiers, ragged queries
+  constexpr bool ATT = AP >= 2;  // a pa_attend call: score modifiers, ragged queries
+  constexpr bool SINKS = AP == 3;  // first positions may stay visible before a window
   const bool fixed = !ATT && p.partition_units > 0;
 
   const int NS = p.stages;  // pipeline depth per ring
@@ -495,7 +515,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         if constexpr (ATT) {
           const int L = seq_view(p.att, s, blockIdx.x == 0).L;
           lens[S + s] = L;
-          nu = L > 0 ? ((T + UR - 1) >> Tr::UR_SHIFT) - (window_lo(p, T, L) >> Tr::UR_SHIFT) : 0;
+          const int lo = window_lo(p, T, L);
+          const int skip = SINKS ? unit_gap(p.att.sinks, lo, Tr::UR_SHIFT).skip : lo >> Tr::UR_SHIFT;
+          nu = L > 0 ? ((T + UR - 1) >> Tr::UR_SHIFT) - skip : 0;
         } else {
           nu = ((T + UR - 1) >> Tr::UR_SHIFT) - (window_lo(p, T, p.q_len) >> Tr::UR_SHIFT);
         }
@@ -563,7 +585,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       w.u = gc * U / nw_eff;
       w.u1 = (gc + 1) * U / nw_eff;
       w.s = find_seq(prefix, S, w.u);
-      w.valid = frag_balanced<ATT>(w, prefix, p, Tr::UR_SHIFT);
+      w.valid = frag_balanced<ATT, SINKS>(w, prefix, p, Tr::UR_SHIFT);
     }
   };
 
@@ -591,22 +613,27 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       }
     }
     // boxes [first_box, nbox) of a unit hold attended rows: blocks wholly
-    // before a sliding window are neither looked up nor loaded
+    // before a sliding window are neither looked up nor loaded, but those of its sinks
     auto first_box = [&](const WorkIter& w, int bj) {
       return unit_in_block ? 0 : max(0, (w.lo >> p.block_shift) - bj);
+    };
+    [[maybe_unused]] auto sink_boxes = [&](const WorkIter& w, int bj) {  // the first ones of a unit, up to first_box
+      return ((w.sinks + B - 1) >> p.block_shift) - bj;
     };
     auto fetch_tables = [&]() {
       const int bj = unit_in_block ? (ah.j >> upb_shift) : (ah.j << bpu_shift);
       const int nb = unit_in_block ? 1 : min(1 << bpu_shift, ah.nblk - bj);
       const int i0 = first_box(ah, bj);
       const int32_t* src = p.block_tables + static_cast<int64_t>(ah.s) * p.max_blocks_per_seq + bj;
+      int i1 = 0;
+      if constexpr (SINKS) i1 = sink_boxes(ah, bj);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i >= i0 && i < nb) cp_async4(ring + (rs_pf * 4 + i) * 4, src + i);
+        if ((i >= i0 || i < i1) && i < nb) cp_async4(ring + (rs_pf * 4 + i) * 4, src + i);
       cp_async_commit();
       rs_pf = (rs_pf + 1) & 3;
       ++pf;
-      if (++ah.j == ah.jend) iter_next_fragment<ATT>(ah, prefix, p, fixed, Tr::UR_SHIFT);
+      if (!next_unit<SINKS>(ah)) iter_next_fragment<ATT, SINKS>(ah, prefix, p, fixed, Tr::UR_SHIFT);
     };
     while (ah.valid && pf < kTablePrefetch) fetch_tables();
     int nq = 0;  // several queries: query loads issued into this lane's ring buffer
@@ -626,6 +653,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       const int bj0 = unit_in_block ? (it.j >> upb_shift) : (it.j << bpu_shift);
       const int nbox = unit_in_block ? 1 : min(1 << bpu_shift, it.nblk - bj0);
       const int box0 = first_box(it, bj0);
+      int box1 = 0;  // boxes of sinks
+      if constexpr (SINKS) box1 = max(0, min(min(box0, nbox), sink_boxes(it, bj0)));
       const int row_in_block = unit_in_block ? (it.j - (bj0 << upb_shift)) * UR : 0;
       const int qlen = GM > 8 ? (ATT ? it.L : p.q_len) : 1;  // only 16-row variants serve several queries
       const uint32_t qbytes = new_frag ? static_cast<uint32_t>(qlen * G * D * 2) : 0u;
@@ -640,7 +669,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       int phys[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        phys[i] = (i >= box0 && i < nbox) ? static_cast<int>(lds32(ring + (rs_use * 4 + i) * 4)) : 0;
+        phys[i] = ((i >= box0 || i < box1) && i < nbox) ? static_cast<int>(lds32(ring + (rs_use * 4 + i) * 4)) : 0;
       rs_use = (rs_use + 1) & 3;
       --pf;
       // fused append: this unit holds position T-1; its new rows ride along
@@ -650,7 +679,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         st_shared_s32(kdst + Tr::OFF_NEW + 4 * D, (pb >= 0 && pb < p.num_blocks) ? pb : -1);
       }
       const uint32_t nbytes = has_new ? static_cast<uint32_t>(4 * D) : 0u;
-      const uint32_t bytes = 2u * (nbox - box0) * BOX * Tr::ROW + qbytes + nbytes;
+      const int boxes = SINKS ? max(nbox - box0, 0) + box1 : nbox - box0;
+      const uint32_t bytes = 2u * boxes * BOX * Tr::ROW + qbytes + nbytes;
       if (early) {
         mbar_expect_tx(bar, bytes);  // armed only: the query copy and the arrival follow the wait
       } else {
@@ -658,7 +688,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (i >= box0 && i < nbox) {
+        if ((i >= box0 || i < box1) && i < nbox) {
           int pb = phys[i];
           if (pb < 0 || pb >= p.num_blocks) {
             raise_error(p.err, PA_DEVERR_BLOCK_ID);
@@ -701,7 +731,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         pph ^= 1;
       }
       if (ah.valid) fetch_tables();
-      if (++it.j == it.jend) iter_next_fragment<ATT>(it, prefix, p, fixed, Tr::UR_SHIFT);
+      if (!next_unit<SINKS>(it)) iter_next_fragment<ATT, SINKS>(it, prefix, p, fixed, Tr::UR_SHIFT);
     };
     // Everything above reads only seq_lens and block_tables.  Under a
     // programmatic dependent launch the grid before this one on the stream
@@ -912,7 +942,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 
   // One unit: S^T = Q K^T, online-softmax update, O^T += V^T P^T.
   // FULL: all UR rows valid.
-  auto unit_step = [&](auto full_tag, uint32_t kt, int n_valid, int lo_rel, int j) {
+  // sink_rel: with sinks: rows below it are attended too (at most lo_rel).
+  auto unit_step = [&](auto full_tag, uint32_t kt, int n_valid, int lo_rel, [[maybe_unused]] int sink_rel, int j) {
     constexpr bool FULL = decltype(full_tag)::value;
     const uint32_t vt = kt + Tr::TILE;
     // P^T as the B operand of each 16-token k-step of O^T += V^T P^T, split hi + lo
@@ -969,7 +1000,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
             if (p.att.slopes) x -= slope2[e & 1] * static_cast<float>(qpos[0] - (j * UR + tok));
           }
           if constexpr (!FULL) {
-            x = (tok < n_valid && tok >= lo_rel) ? x : -INFINITY;
+            x = (tok < n_valid && (tok >= lo_rel || (SINKS && tok < sink_rel))) ? x : -INFINITY;
           }
           sc[mt][e] = x;
           if (e & 1) {
@@ -987,7 +1018,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
               const int tok = 16 * mt + 4 * e + (k8bit ? sigma(gid) : gid);
-              if (tok >= n_valid || tok < lo_rel) continue;
+              if (tok >= n_valid || (tok < lo_rel && !(SINKS && tok < sink_rel))) continue;
               if (score_row[1] && (G & 1) == 0) {
                 *reinterpret_cast<float2*>(at + tok * G) = make_float2(sc[mt][e], sc[mt][e + 1]);
               } else {
@@ -1093,6 +1124,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
               const int tok = nt * 8 + (k8bit ? sigma(2 * tig + e) : 2 * tig + e);
               bool ok = tok < n_valid && tok >= lo_rel;
               if constexpr (MQ) ok = ok && tok <= hr && tok >= lr;
+              if constexpr (SINKS) ok = ok || (tok < p.att.sinks - j * UR && tok < n_valid && tok <= hr);
               if constexpr (ATT) {
                 if (p.att.softcap > 0.f) x = cap2 - __fdividef(2.f * cap2, 1.f + fast_exp2(sc[nt][2 * h + e] * capk));
                 if (p.att.slopes) x -= slope2[h] * fabsf(static_cast<float>(qpos[h] - (j * UR + tok)));
@@ -1149,11 +1181,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     // rows past the end of the sequence, and rows before a sliding window,
     // may hold anything (or were not loaded): zero them in V
     if constexpr (!FULL) {
-      const int nlo = max(lo_rel, 0);
+      const int s0 = SINKS ? min(max(sink_rel, 0), UR) : 0;  // (sinks before the window stay; it may start behind their unit)
+      const int nlo = max((SINKS ? min(lo_rel, UR) : lo_rel) - s0, 0);
       const int nz = (UR - n_valid + nlo) * Tr::NSUB * 8;
       for (int k = lane; k < nz; k += 32) {
         const int rr = k / (Tr::NSUB * 8);
-        const int r = rr < nlo ? rr : n_valid + (rr - nlo);
+        const int r = rr < nlo ? s0 + rr : n_valid + (rr - nlo);
         const int ch = k % (Tr::NSUB * 8);
         sts128_zero(vt + chunk_off(r, ch));
       }
@@ -1512,17 +1545,18 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       const uint32_t stage_u32 = wbase_u32 + Tr::OFF_STAGES + cst * STG;
       if (append && it.j == ((it.T - 1) >> Tr::UR_SHIFT)) append_row(cst);
       const int n_valid = min(UR, it.T - it.j * UR);
-      const int lo_rel = it.lo - it.j * UR;  // positions before the window (> 0 only in its first unit)
+      const int lo_rel = it.lo - it.j * UR;  // positions before the window (> 0 only in its first unit, and in sinks' units)
+      const int sink_rel = SINKS ? it.sinks - it.j * UR : 0;
       if constexpr (MQ) {
         // one (masked) copy of the unit step: two inlined copies do not fit the
         // registers of the 16-row variants
         (void)full_lo;
         (void)full_hi;
-        unit_step(std::false_type{}, stage_u32, n_valid, lo_rel, it.j);
-      } else if (n_valid == UR && lo_rel <= 0) {
-        unit_step(std::true_type{}, stage_u32, UR, 0, it.j);
+        unit_step(std::false_type{}, stage_u32, n_valid, lo_rel, sink_rel, it.j);
+      } else if (n_valid == UR && (lo_rel <= 0 || (SINKS && sink_rel >= UR))) {
+        unit_step(std::true_type{}, stage_u32, UR, 0, 0, it.j);
       } else {
-        unit_step(std::false_type{}, stage_u32, n_valid, lo_rel, it.j);
+        unit_step(std::false_type{}, stage_u32, n_valid, lo_rel, sink_rel, it.j);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(wbase_u32 + Tr::OFF_EMPTY + 8 * cst);  // the stage may be refilled
@@ -1530,8 +1564,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         cst = 0;
         cpar ^= 1;
       }
-      if (it.j + 1 == it.jend) break;
-      ++it.j;
+      if (!next_unit<SINKS>(it)) break;
       if (!mbar_wait_bounded(wbase_u32 + Tr::OFF_FULL + 8 * cst, cpar, p.wait_limit_ns)) {
         if (lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
         timed_out = true;
@@ -1664,8 +1697,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         arr_acq = final_frag;
       }
     }
-    ++it.j;
-    iter_next_fragment<ATT>(it, prefix, p, fixed, Tr::UR_SHIFT);
+    iter_next_fragment<ATT, SINKS>(it, prefix, p, fixed, Tr::UR_SHIFT);
   }
 
   // ---- the split merges this warp won
@@ -1693,7 +1725,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       start_iter(it, ring_gc(ring_id));
       while (it.valid) {
         if (it.slot < 0) again(it.s, it.kvh, it.T, it.L, first_row(it.s), min(16, it.L * G - row0));
-        iter_next_fragment<ATT>(it, prefix, p, fixed, Tr::UR_SHIFT);
+        iter_next_fragment<ATT, SINKS>(it, prefix, p, fixed, Tr::UR_SHIFT);
       }
     }
   }
@@ -1709,7 +1741,7 @@ struct DecodeVariant {
   static size_t smem_bytes(int num_seqs, int warps, int rings, int stages, int stage) {
     constexpr int head_words = Tr::B8 ? 4 * kMaxHeadParams : 0;
     return 1024 + static_cast<size_t>(rings) * (Tr::warp_smem(stages, stage) + Tr::qbuf_bytes(warps / rings)) +
-           static_cast<size_t>(align_up_c(((AP == 2 ? 3 : 2) * num_seqs + 1 + warps + 1 + head_words) * 4, 16)) +
+           static_cast<size_t>(align_up_c(((AP >= 2 ? 3 : 2) * num_seqs + 1 + warps + 1 + head_words) * 4, 16)) +
            static_cast<size_t>(rings) * 64;
   }
 

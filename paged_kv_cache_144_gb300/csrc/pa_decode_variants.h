@@ -67,10 +67,22 @@
   X(f16_t, i8_t, 128, 8, 32, 2) X(f16_t, i8_t, 128, 8, 64, 2) X(bf16_t, e4m3_t, 128, 16, 32, 2) \
   X(bf16_t, i8_t, 128, 16, 32, 2) X(f16_t, e4m3_t, 128, 16, 32, 2) X(f16_t, i8_t, 128, 16, 32, 2)
 
+// the same with sinks
+#define PA_DECODE_VARIANTS_SINKS16(X) \
+  X(f16_t, f16_t, 64, 8, 32, 3) X(f16_t, f16_t, 128, 8, 32, 3) X(bf16_t, bf16_t, 64, 8, 32, 3) \
+  X(bf16_t, bf16_t, 128, 8, 32, 3) X(f16_t, f16_t, 64, 16, 32, 3) X(f16_t, f16_t, 128, 16, 32, 3) \
+  X(bf16_t, bf16_t, 64, 16, 32, 3) X(bf16_t, bf16_t, 128, 16, 32, 3)
+#define PA_DECODE_VARIANTS_SINKS8(X) \
+  X(bf16_t, e4m3_t, 128, 8, 32, 3) X(bf16_t, e4m3_t, 128, 8, 64, 3) X(f16_t, e4m3_t, 128, 8, 32, 3) \
+  X(f16_t, e4m3_t, 128, 8, 64, 3) X(bf16_t, i8_t, 128, 8, 32, 3) X(bf16_t, i8_t, 128, 8, 64, 3) \
+  X(f16_t, i8_t, 128, 8, 32, 3) X(f16_t, i8_t, 128, 8, 64, 3) X(bf16_t, e4m3_t, 128, 16, 32, 3) \
+  X(bf16_t, i8_t, 128, 16, 32, 3) X(f16_t, e4m3_t, 128, 16, 32, 3) X(f16_t, i8_t, 128, 16, 32, 3)
+
 #define PA_DECODE_VARIANTS(X) \
   PA_DECODE_VARIANTS_F16(X) PA_DECODE_VARIANTS_BF16(X) PA_DECODE_VARIANTS_FP8(X) PA_DECODE_VARIANTS_INT8(X) \
   PA_DECODE_VARIANTS_ROWS16(X) PA_DECODE_VARIANTS_APPEND16(X) PA_DECODE_VARIANTS_APPEND8(X) \
-  PA_DECODE_VARIANTS_ATTEND16(X) PA_DECODE_VARIANTS_ATTEND8(X)
+  PA_DECODE_VARIANTS_ATTEND16(X) PA_DECODE_VARIANTS_ATTEND8(X) PA_DECODE_VARIANTS_SINKS16(X) \
+  PA_DECODE_VARIANTS_SINKS8(X)
 
 // Each variant translation unit defines these two plain functions; the
 // dispatcher sees only the declarations, so every kernel is instantiated and

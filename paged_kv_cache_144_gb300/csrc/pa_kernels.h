@@ -93,6 +93,7 @@ struct AttendParams {
   float softcap;             // 0: off
   const float* slopes;       // nullptr: off
   int window;                // 0: off
+  int sinks;                 // with a window: first positions that stay visible
   const int32_t* prefix_lens;
   const uint64_t* tree_mask;
   int tree_words;
@@ -161,7 +162,7 @@ struct DecodeKey {
   int head_dim;   // 64 / 128
   int gmax;       // 1 / 4 / 8 (query heads per KV head, rounded up)
   int unit_rows;  // 16 / 32 / 64 rows per work unit
-  int append;     // 1: fused append (each stage also stages the new K/V rows); 2: score modifiers (pa_attend)
+  int append;     // 1: fused append (each stage also stages the new K/V rows); 2: score modifiers (pa_attend); 3: with sinks
   int row_groups; // consumer warps sharing a ring (1; up to 4 for the 16-row variants)
 };
 

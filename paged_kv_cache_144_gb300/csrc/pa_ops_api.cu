@@ -291,6 +291,8 @@ PA_EXPORT int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q
   // outside these the score's float32 form loses too much: its error is about 2^-21 softcap
   if (o.softcap > 0.f && (o.softcap < 0x1p-10f || o.softcap > 512.f)) return PA_ERR_UNSUPPORTED;
   if (o.window > 0 && (o.prefix_lens || o.tree_mask)) return PA_ERR_UNSUPPORTED;
+  if (o.sinks < 0) return PA_ERR_SHAPE;
+  if (o.sinks > 0 && (o.prefix_lens || o.tree_mask)) return PA_ERR_UNSUPPORTED;
   if (o.tree_mask && (o.slopes || o.prefix_lens)) return PA_ERR_UNSUPPORTED;
   if (o.tree_mask && (o.tree_words <= 0 || static_cast<int64_t>(o.tree_words) * 64 < max_q_len)) return PA_ERR_SHAPE;
   if (o.mass && max_q_len != 1) return PA_ERR_UNSUPPORTED;
@@ -352,6 +354,7 @@ PA_EXPORT int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q
   p.softcap = o.softcap;
   p.slopes = o.slopes;
   p.window = o.window;
+  p.sinks = o.window > 0 ? (o.sinks < cap ? o.sinks : static_cast<int>(cap)) : 0;  // (without a window everything is seen)
   p.prefix_lens = o.prefix_lens;
   p.tree_mask = o.tree_mask;
   p.tree_words = o.tree_words;
