@@ -91,8 +91,8 @@ typedef enum {
  *   pa_reshape_and_cache: zero = float16(smallest value of the row), scale =
  *   float16((largest - zero) / 15), code = (x - zero) / scale rounded to the
  *   nearest of 0 .. 15 (ties to even; 0 where scale is 0).  The bounds are clipped
- *   to +-2^15; NaN does not count for them and takes code 0.  Any finite pair may
- *   be stored by the caller.
+ *   to +-2^15; NaN does not count for them and takes code 0.  A caller may store
+ *   other pairs, whose 16 values are finite float16 numbers.
  *   Read by pa_attend and pa_read_cache.  pa_copy_blocks copies its blocks
  *   (block_bytes = num_kv_heads tiles).  The other calls refuse it.
  */

@@ -35,6 +35,7 @@ SOURCES = [
     "pa_attend_tc_bf16.cu",
     "pa_attend_tc_fp8.cu",
     "pa_attend_tc_int8.cu",
+    "pa_attend_tc_int4.cu",
     "pa_evict.cu",
     "pa_decode_dispatch.cu",
     "pa_decode_f16.cu",
@@ -46,6 +47,7 @@ SOURCES = [
     "pa_decode_append8.cu",
     "pa_decode_attend16.cu",
     "pa_decode_attend8.cu",
+    "pa_decode_int4.cu",
     "pa_decode_sinks16.cu",
     "pa_decode_sinks8.cu",
 ]

@@ -59,7 +59,8 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
     return false;
   const int group = num_heads / num_kv_heads;
   const int64_t rows = static_cast<int64_t>(max_q_len) * group;
-  const bool q8 = kv_dtype == PA_FP8_E4M3 || kv_dtype == PA_INT8;
+  const bool q4 = kv_dtype == PA_INT4;
+  const bool q8 = kv_dtype == PA_FP8_E4M3 || kv_dtype == PA_INT8 || q4;
   pl->ctas = sms;
   const int rps = stream_rows(group);
   pl->cg = q8 || (head_dim == 128 && rows > rps) ? 2 : 1;
@@ -79,7 +80,7 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
     pl->key.head_dim = head_dim;
     pl->key.gmax = gm;
     pl->key.unit_rows = q8 && block_size >= 16 && gm == 8 ? 64 : 32;
-    pl->key.append = sinks ? 3 : 2;
+    pl->key.append = sinks || q4 ? 3 : 2;
     pl->key.row_groups = gm == 16 ? static_cast<int>((rows + 15) / 16) : 1;
     if (!decode_geometry(pl->key, shape_seqs(num_seqs), &pl->geo)) return false;
     const size_t warps = static_cast<size_t>(pl->geo.ctas) * pl->geo.warps_per_cta;
@@ -147,7 +148,8 @@ cudaError_t launch_few(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaS
   p.att = a;
   const int eb = a.kv_dtype == PA_FP8_E4M3 || a.kv_dtype == PA_INT8 ? 1 : 2;
   const int box = a.block_size < pl.geo.unit_rows ? a.block_size : pl.geo.unit_rows;
-  CUtensorMap tk, tv;
+  CUtensorMap tk = {}, tv = {};  // (4-bit caches: bulk copies, no maps)
+  if (a.kv_dtype == PA_INT4) return launch_decode(pl.key, pl.geo, p, tk, tv, stream, a.pdl);
   if (!encode_cache_map(&tk, a.k_cache, a.num_blocks, a.num_kv_heads, a.block_size, a.head_dim, eb, box) ||
       !encode_cache_map(&tv, a.v_cache, a.num_blocks, a.num_kv_heads, a.block_size, a.head_dim, eb, box))
     return cudaErrorInvalidValue;
@@ -276,6 +278,8 @@ int launch_attend(AttendParams p, void* workspace, size_t workspace_bytes, cudaS
   if (e != cudaSuccess) return cuda_status(e, "pa_attend counters");
   if (pl.kind == Plan::kFew) {
     e = launch_few(p, pl, ws, stream);
+  } else if (p.kv_dtype == PA_INT4) {
+    e = launch_tc_int4(p, pl, ws, stream);
   } else if (p.kv_dtype == PA_FP8_E4M3) {
     e = launch_tc_fp8(p, pl, ws, stream);
   } else if (p.kv_dtype == PA_INT8) {

@@ -91,10 +91,13 @@ __device__ __forceinline__ float cap_score(float x, float cap, float two_log2e_o
   return cap - __fdividef(2.f * cap, 1.f + fast_exp2(x * two_log2e_over_cap));
 }
 
-// One cache element, widened and (INT8) with its zero point subtracted; scales stay outside.
+// One cache element, widened and (INT8) with its zero point subtracted; scales, and a 4-bit row's zero, stay outside.
 template <typename KVT>
 __device__ __forceinline__ float cache_elem(const uint8_t* row, int c, int zp) {
-  if constexpr (std::is_same<KVT, e4m3_t>::value) {
+  if constexpr (std::is_same<KVT, i4_t>::value) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(row)[c >> 3];
+    return static_cast<float>((w >> (16 * (c & 1) + 4 * ((c & 7) >> 1))) & 15u);
+  } else if constexpr (std::is_same<KVT, e4m3_t>::value) {
     return widen2_e4m3(row[c]).x;
   } else if constexpr (std::is_same<KVT, i8_t>::value) {
     return static_cast<float>(static_cast<int>(reinterpret_cast<const int8_t*>(row)[c]) - zp);
@@ -136,19 +139,35 @@ __device__ __forceinline__ void attend_row(const AttendParams& p, int s, const S
   const float capk = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
   const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq;
   const int first = v.T - v.L;
-  auto row_of = [&](const void* cache, int t) -> const uint8_t* {
+  // the row of position t; pair: a 4-bit row's scale and zero (else 1 and 0)
+  auto row_of = [&](const void* cache, int t, float2* pair) -> const uint8_t* {
     int pb = __ldg(table + (t >> p.block_shift));
     if (pb < 0 || pb >= p.num_blocks) {
       raise_error(p.err, PA_DEVERR_BLOCK_ID);
       pb = 0;
+    }
+    if constexpr (std::is_same<KVT, i4_t>::value) {
+      const uint8_t* const tile = static_cast<const uint8_t*>(cache) + (static_cast<int64_t>(pb) * p.num_kv_heads + kvh) *
+                                                                           (p.block_size * int4_row_bytes(D));
+      const int r = t & (p.block_size - 1);
+      *pair = widen2<f16_t>(*reinterpret_cast<const uint32_t*>(tile + p.block_size * (D / 2) + 4 * r));
+      return tile + r * (D / 2);
     }
     return static_cast<const uint8_t*>(cache) +
            ((static_cast<int64_t>(pb) * p.num_kv_heads + kvh) * p.block_size + (t & (p.block_size - 1))) *
                (D * elem<KVT>::bytes);
   };
   float m = -INFINITY, l = 0.f, acc[D / 32];
+  [[maybe_unused]] float qsum = 0.f;  // what a 4-bit row's zero multiplies
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
+  for (int j = 0; j < D / 32; ++j) {
+    acc[j] = 0.f;
+    qsum += q[j];
+  }
+  if constexpr (std::is_same<KVT, i4_t>::value) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) qsum += __shfl_xor_sync(0xffffffffu, qsum, o);
+  }
   for (int t0 = rb.sinks > 0 ? 0 : rb.lo & ~31; t0 < rb.hi; t0 += 32) {
     if (t0 >= rb.sinks && t0 + 32 <= rb.lo) t0 = rb.lo & ~31;
     const int t = t0 + lane;
@@ -158,7 +177,8 @@ __device__ __forceinline__ void attend_row(const AttendParams& p, int s, const S
       see = (p.tree_mask[n * p.tree_words + (j >> 6)] >> (j & 63)) & 1ull;
     }
     float z = -INFINITY;
-    const uint8_t* kr = see ? row_of(p.k_cache, t) : static_cast<const uint8_t*>(p.k_cache);
+    float2 kp = make_float2(1.f, 0.f);
+    const uint8_t* kr = see ? row_of(p.k_cache, t, &kp) : static_cast<const uint8_t*>(p.k_cache);
     float x = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
@@ -166,6 +186,7 @@ __device__ __forceinline__ void attend_row(const AttendParams& p, int s, const S
       for (int c = 0; c < 32; ++c) x = fmaf(__shfl_sync(0xffffffffu, q[j], c), cache_elem<KVT>(kr, c + 32 * j, kz), x);
     }
     if (see) {
+      if constexpr (std::is_same<KVT, i4_t>::value) x = fmaf(x, kp.x, kp.y * qsum);
       x *= p.scale * ks;
       if (p.softcap > 0.f) x = cap_score(x, p.softcap, capk);
       if (p.slopes) x -= slope * static_cast<float>(abs(rb.pos - t));
@@ -192,9 +213,14 @@ __device__ __forceinline__ void attend_row(const AttendParams& p, int s, const S
       const int k = __ffs(left) - 1;
       left &= left - 1;
       const float w = __shfl_sync(0xffffffffu, e, k);
-      const uint8_t* vr = row_of(p.v_cache, t0 + k);
+      float2 vp = make_float2(1.f, 0.f);
+      const uint8_t* vr = row_of(p.v_cache, t0 + k, &vp);
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(w, cache_elem<KVT>(vr, lane + 32 * j, vz), acc[j]);
+      for (int j = 0; j < D / 32; ++j) {
+        float y = cache_elem<KVT>(vr, lane + 32 * j, vz);
+        if constexpr (std::is_same<KVT, i4_t>::value) y = fmaf(y, vp.x, vp.y);
+        acc[j] = fmaf(w, y, acc[j]);
+      }
     }
     bool lost = true;
 #pragma unroll

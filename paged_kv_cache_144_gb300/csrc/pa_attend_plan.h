@@ -25,5 +25,6 @@ cudaError_t launch_tc_f16(const AttendParams& a, const Plan& pl, uint8_t* ws, cu
 cudaError_t launch_tc_bf16(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream);
 cudaError_t launch_tc_fp8(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream);
 cudaError_t launch_tc_int8(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream);
+cudaError_t launch_tc_int4(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream);
 
 }  // namespace pa

@@ -36,6 +36,10 @@
 // any block size; it is the K-major operand layout of S = Q K^T (row groups
 // NH * 1024 bytes apart) and the MN-major one of P V as it is.
 //
+// 4-bit caches (pairs of CTAs only): as 8-bit ones; the producer brings a block's
+// tile in one bulk copy, and the widening warps round each value, code * scale +
+// zero, to f16.
+//
 // 8-bit caches (pairs of CTAs only): the producer brings the codes as they are
 // and four more warps (12-15) widen them to f16 in the operands' layout, exactly
 // (the K scale multiplies the scores, the V scale the output), zero V rows on
@@ -468,12 +472,13 @@ __device__ __forceinline__ int cut_slot_kind(int c, int c0, int U, int nw, int s
 template <typename KVT, int D, int CG>
 struct TcTraits {
   static constexpr bool BF16 = std::is_same<KVT, bf16_t>::value;
-  static constexpr bool B8 = elem<KVT>::bytes == 1;
-  static_assert(!B8 || (CG == 2 && D == 128), "8-bit caches: pairs of CTAs, head_dim 128");
-  static constexpr int THREADS = B8 ? 512 : 384;
+  static constexpr bool B8 = elem<KVT>::bytes == 1, B4 = std::is_same<KVT, i4_t>::value;
+  static constexpr bool CODES = B8 || B4;  // widened to f16 on the way
+  static_assert(!CODES || (CG == 2 && D == 128), "8- and 4-bit caches: pairs of CTAs, head_dim 128");
+  static constexpr int THREADS = CODES ? 512 : 384;
   // The softmax threads hold 64 scores each: registers move to their warps from the others (at launch 65536 / THREADS,
   // rounded down to a multiple of 8, each).
-  static constexpr int REGS_LOW = B8 ? 72 : 88, REGS_HIGH = B8 ? 184 : 208;
+  static constexpr int REGS_LOW = CODES ? 72 : 88, REGS_HIGH = CODES ? 184 : 208;
   static_assert((THREADS - 256) * REGS_LOW + 256 * REGS_HIGH <= THREADS * (65536 / THREADS / 8 * 8), "register split");
   static constexpr int NH = D * 2 / 128;           // 128-byte halves per 16-bit row
   static constexpr int TILE_BYTES = kTile * D * 2;  // a tile of K, V or Q
@@ -484,16 +489,19 @@ struct TcTraits {
   static constexpr int VH = NH / CG;               // halves of a V stage
   static constexpr int KGROUP = NH * 1024, VGROUP = VH * 1024;  // bytes of 8 rows
   static constexpr int STAGE = TILE_BYTES / CG;    // bytes of a K or V stage
-  static constexpr int NST = B8 ? 3 : (D == 128 ? 2 : 4) * CG;  // stages of K and of V
-  // 8-bit caches: stages of codes as they come, [rows][128 / CG bytes] for V
-  static constexpr int NR = B8 ? 2 : 0, RAW = B8 ? STAGE / 2 : 0;
+  static constexpr int NST = CODES ? 3 : (D == 128 ? 2 : 4) * CG;  // stages of K and of V
+  // 8-bit caches: stages of codes as they come, [rows][128 / CG bytes] for V; 4-bit: [box][rows of codes, their pairs]
+  static constexpr int NR = CODES ? 2 : 0;
+  static constexpr int RAW_K = B8 ? STAGE / 2 : B4 ? KROWS * int4_row_bytes(D) : 0;
+  static constexpr int RAW_V = B8 ? STAGE / 2 : B4 ? kTile * int4_row_bytes(D) : 0;
+  static_assert(RAW_K % 128 == 0 && RAW_V % 128 == 0, "alignment");
   static constexpr int OFF_Q = 0;                  // two tiles
   static constexpr int OFF_K = 2 * TILE_BYTES;
   static constexpr int OFF_V = OFF_K + NST * STAGE;
   static constexpr int OFF_RK = OFF_V + NST * STAGE;
-  static constexpr int OFF_RV = OFF_RK + NR * RAW;
-  static constexpr int OFF_QX = OFF_RV + NR * RAW;  // bf16 queries: 2^-exponent per row, [stream][use & 1][128]
-  static constexpr int OFF_BAR = OFF_QX + (B8 ? 4 * kTile * 4 : 0);
+  static constexpr int OFF_RV = OFF_RK + NR * RAW_K;
+  static constexpr int OFF_QX = OFF_RV + NR * RAW_V;  // bf16 queries: 2^-exponent per row, [stream][use & 1][128]
+  static constexpr int OFF_BAR = OFF_QX + (CODES ? 4 * kTile * 4 : 0);
   // barriers (8 bytes each)
   static constexpr int KF = 0, KE = KF + NST, VF = KE + NST, VE = VF + NST, QF = VE + NST, QE = QF + 2, SF = QE + 2,
                        PF = SF + 4, OH = PF + 4, OD = OH + 2, RB = OD + 2,  // SF, PF: per half of a tile; OH, OD: its halves
@@ -639,7 +647,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = a.num_seqs;
   const int rank = CG == 1 ? 0 : static_cast<int>(cluster_rank());  // CTA of its group; the first issues the products
-  const bool q_widen = Tr::B8 && a.q_dtype == PA_BF16;  // bf16 queries become f16
+  const bool q_widen = Tr::CODES && a.q_dtype == PA_BF16;  // bf16 queries become f16
   const int group_id = static_cast<int>(blockIdx.x) / CG, groups = static_cast<int>(gridDim.x) / CG;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   auto wait = [&](int i, uint32_t parity, bool full = false) -> bool {  // full: the whole limit, whatever the call's
@@ -655,13 +663,15 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   };
 
   if (threadIdx.x == 0) {
-    prefetch_tensormap(&tmap_k);
-    prefetch_tensormap(&tmap_v);
+    if constexpr (!Tr::B4) {
+      prefetch_tensormap(&tmap_k);
+      prefetch_tensormap(&tmap_v);
+    }
     prefetch_tensormap(&tmap_q);
     for (int i = 0; i < NST; ++i) {
-      mbar_init(bar(Tr::KF + i), Tr::B8 ? 4 : 1);  // (8-bit caches: the widening warps)
+      mbar_init(bar(Tr::KF + i), Tr::CODES ? 4 : 1);  // (8-bit caches: the widening warps)
       mbar_init(bar(Tr::KE + i), p.paired ? 2 : 1);  // paired: both streams read every tile
-      mbar_init(bar(Tr::VF + i), Tr::B8 ? 4 : 1);
+      mbar_init(bar(Tr::VF + i), Tr::CODES ? 4 : 1);
       mbar_init(bar(Tr::VE + i), p.paired ? 2 : 1);
       mbar_init(bar(Tr::VL + i), 1);
       mbar_init(bar(Tr::KP + i), 1);
@@ -827,23 +837,35 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   };
   // One tile of K or V: its boxes, one lane each (block pb), into the next stage of the ring (8-bit caches: of codes).
   auto issue_tile = [&](bool is_v, int count, int j, int pb) -> bool {
-    constexpr int RING = Tr::B8 ? Tr::NR : NST;
+    constexpr int RING = Tr::CODES ? Tr::NR : NST;
     const int box_rows = min(a.block_size, tile_rows(is_v)), boxes = tile_rows(is_v) / box_rows;
-    const uint32_t box = static_cast<uint32_t>(box_rows / 8) * (is_v ? Tr::VGROUP : Tr::KGROUP) / (Tr::B8 ? 2 : 1);
+    const uint32_t box = Tr::B4 ? static_cast<uint32_t>(box_rows * int4_row_bytes(D))
+                                : static_cast<uint32_t>(box_rows / 8) * (is_v ? Tr::VGROUP : Tr::KGROUP) / (Tr::B8 ? 2 : 1);
     const int t0 = tile_start(is_v, j);
     const int st = count % RING;
     const uint32_t ph = static_cast<uint32_t>(count / RING) & 1u;
-    const int empty = Tr::B8 ? (is_v ? Tr::RVE : Tr::RKE) : (is_v ? Tr::VE : Tr::KE);
+    const int empty = Tr::CODES ? (is_v ? Tr::RVE : Tr::RKE) : (is_v ? Tr::VE : Tr::KE);
     if (!__all_sync(0xffffffffu, wait(empty + st, ph ^ 1u))) return false;
     const uint32_t bytes = box * static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, pb >= 0)));
     // a V tile with rows to be zeroed is announced once that is done
-    const uint32_t full = bar((Tr::B8 ? (is_v ? Tr::RVF : Tr::RKF) : is_v ? (partial(j) ? Tr::VL : Tr::VF) : Tr::KF) + st);
+    const uint32_t full = bar((Tr::CODES ? (is_v ? Tr::RVF : Tr::RKF) : is_v ? (partial(j) ? Tr::VL : Tr::VF) : Tr::KF) + st);
     if (lane == 0) mbar_arrive_expect_tx(full, bytes);
     __syncwarp();
     const int row = boxes > 1 ? 0 : (t0 & (a.block_size - 1));
     if (pb >= 0) {
-      if constexpr (Tr::B8)
-        tma_load_2d(base + (is_v ? Tr::OFF_RV : Tr::OFF_RK) + st * Tr::RAW + lane * box, is_v ? &tmap_v : &tmap_k,
+      if constexpr (Tr::B4) {
+        // (V: whole rows, of which each CTA of the pair widens its half)
+        const uint8_t* const tile = static_cast<const uint8_t*>(is_v ? a.v_cache : a.k_cache) +
+                                    (static_cast<int64_t>(pb) * a.num_kv_heads + f.kvh) * (a.block_size * int4_row_bytes(D));
+        const uint32_t to = base + (is_v ? Tr::OFF_RV + st * Tr::RAW_V : Tr::OFF_RK + st * Tr::RAW_K) + lane * box;
+        if (box_rows == a.block_size) {
+          bulk_load(to, tile, box, full);
+        } else {  // part of a longer block: its codes, and its pairs
+          bulk_load(to, tile + row * (D / 2), box_rows * (D / 2), full);
+          bulk_load(to + box_rows * (D / 2), tile + a.block_size * (D / 2) + row * 4, box_rows * 4, full);
+        }
+      } else if constexpr (Tr::B8)
+        tma_load_2d(base + (is_v ? Tr::OFF_RV + st * Tr::RAW_V : Tr::OFF_RK + st * Tr::RAW_K) + lane * box, is_v ? &tmap_v : &tmap_k,
                     is_v ? rank * (D / CG) : 0, (pb * a.num_kv_heads + f.kvh) * a.block_size + row, full);
       else
         tma_load_4d(base + (is_v ? Tr::OFF_V : Tr::OFF_K) + st * Tr::STAGE + lane * box, is_v ? &tmap_v : &tmap_k, 0, 0,
@@ -860,7 +882,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       if (n > 0 && !wait((is_v ? Tr::VE : Tr::KE) + i, ph, true)) wait((is_v ? Tr::VF : Tr::KF) + i, ph, true);
     }
     for (int i = 0; i < Tr::NR; ++i) {
-      const int n = count / (Tr::B8 ? Tr::NR : 1) + (i < count % (Tr::B8 ? Tr::NR : 1) ? 1 : 0);
+      const int n = count / (Tr::CODES ? Tr::NR : 1) + (i < count % (Tr::CODES ? Tr::NR : 1) ? 1 : 0);
       if (n > 0) wait((is_v ? Tr::RVF : Tr::RKF) + i, static_cast<uint32_t>(n - 1) & 1u, true);
     }
   };
@@ -922,7 +944,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
         if (!p.paired) parity ^= n & 1;
         while (ok) {
-          if (!Tr::B8 && partial(j)) {
+          if (!Tr::CODES && partial(j)) {
             const int st = (kt - 1) % NST;
             if (!(ok = wait(Tr::VL + st, (vl >> st) & 1u))) break;
             vl ^= 1u << st;
@@ -1033,15 +1055,35 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
       }
     }
-  } else if (Tr::B8 && warp >= 12) {
+  } else if (Tr::CODES && warp >= 12) {
     regs_dec<Tr::REGS_LOW>();
-    // ================================================================= 8-bit caches: codes to f16
-    if constexpr (Tr::B8) {
+    // ================================================================= 8- and 4-bit caches: codes to f16
+    if constexpr (Tr::CODES) {
       const int tid = static_cast<int>(threadIdx.x) - 384;
       int kt = 0, parity = 0, uses[2] = {0, 0};
       bool ok = true;
+      // 4 bits: rows 16-byte piece c of row r of a stage, its pair, and 8 codes to a 16-byte chunk of f16: code (exact) * scale +
+      // zero, rounded once
+      [[maybe_unused]] auto codes_at = [&](int r, int box_rows) { return r * (D / 2) + 4 * (r & ~(box_rows - 1)); };
+      [[maybe_unused]] auto pair_at = [&](int r, int box_rows) { return 4 * r + (D / 2) * ((r & ~(box_rows - 1)) + box_rows); };
+      [[maybe_unused]] auto widen8 = [&](uint32_t w, uint32_t pair) {
+        const uint32_t s2 = prmt(pair, pair, 0x1010u), z2 = prmt(pair, pair, 0x3232u);
+        uint4 o;
+        auto two = [&](uint32_t x) {  // f16x2 64 + code -> value
+          uint32_t y;
+          asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tfma.rn.f16x2 %0, t, %3, %4;\n\t}"
+              : "=r"(y)
+              : "r"(x), "r"(0x54005400u), "r"(s2), "r"(z2));
+          return y;
+        };
+        o.x = two(nibbles_f16_64<0>(w));
+        o.y = two(nibbles_f16_64<1>(w));
+        o.z = two(nibbles_f16_64<2>(w));
+        o.w = two(nibbles_f16_64<3>(w));
+        return o;
+      };
       // 16 codes to two 16-byte chunks of f16
-      auto widen16 = [&](const uint4& w, uint32_t zp2, uint4& lo, uint4& hi) {
+      [[maybe_unused]] auto widen16 = [&](const uint4& w, uint32_t zp2, uint4& lo, uint4& hi) {
         widen4<KVT>(w.x, zp2, lo.x, lo.y);
         widen4<KVT>(w.y, zp2, lo.z, lo.w);
         widen4<KVT>(w.z, zp2, hi.x, hi.y);
@@ -1110,40 +1152,93 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         for (int j = f.t0; ok && j < f.t1; ++j, ++kt) {
           const int st = kt % NST, r = kt % Tr::NR;
           const uint32_t eph = (static_cast<uint32_t>(kt / NST) & 1u) ^ 1u, rph = static_cast<uint32_t>(kt / Tr::NR) & 1u;
-          constexpr int PER = Tr::RAW / 16 / 128;  // 16-byte chunks of codes per thread
-          {
-            if (!(ok = wait(Tr::RKF + r, rph) && wait(Tr::KE + st, eph))) break;
-            uint4 w[PER];
+          if constexpr (Tr::B4) {
+            // two pieces of 32 codes per thread, of K and of V (its half of the columns)
+            {
+              if (!(ok = wait(Tr::RKF + r, rph) && wait(Tr::KE + st, eph))) break;
+              const uint32_t raw = base + Tr::OFF_RK + r * Tr::RAW_K;
+              const int box_rows = min(a.block_size, Tr::KROWS);
+              uint4 w[2];
+              uint32_t pair[2];
 #pragma unroll
-            for (int k = 0; k < PER; ++k) w[k] = lds128(base + Tr::OFF_RK + r * Tr::RAW + (k * 128 + tid) * 16);
+              for (int k = 0; k < 2; ++k) {
+                const int x = k * 128 + tid, row = x >> 2;
+                w[k] = lds128(raw + codes_at(row, box_rows) + (x & 3) * 16);
+                pair[k] = lds32(raw + pair_at(row, box_rows));
+              }
 #pragma unroll
-            for (int k = 0; k < PER; ++k) {
-              const int x = k * 128 + tid, row = x >> 3, c = 2 * (x & 7);
-              uint4 lo, hi;
-              widen16(w[k], zk2, lo, hi);
-              uint8_t* const to = sm + Tr::OFF_K + st * Tr::STAGE + (row >> 3) * Tr::KGROUP + (c >> 3) * 1024 + (row & 7) * 128;
-              *reinterpret_cast<uint4*>(to + (((c & 7) ^ (row & 7)) << 4)) = lo;
-              *reinterpret_cast<uint4*>(to + ((((c & 7) + 1) ^ (row & 7)) << 4)) = hi;
+              for (int k = 0; k < 2; ++k) {
+                const int x = k * 128 + tid, row = x >> 2, c = 4 * (x & 3);
+                uint8_t* const to = sm + Tr::OFF_K + st * Tr::STAGE + (row >> 3) * Tr::KGROUP + (c >> 3) * 1024 + (row & 7) * 128;
+                const uint32_t words[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  *reinterpret_cast<uint4*>(to + ((((c & 7) + i) ^ (row & 7)) << 4)) = widen8(words[i], pair[k]);
+              }
+              done(Tr::KF + st, Tr::RKE + r);
             }
-            done(Tr::KF + st, Tr::RKE + r);
-          }
-          {
-            if (!(ok = wait(Tr::RVF + r, rph) && wait(Tr::VE + st, eph))) break;
-            const int t = first_of(j), n_hi = f.v.T - t, n_lo = f.lo - t, n_sinks = f.sinks - t;
-            uint4 w[PER];
+            {
+              if (!(ok = wait(Tr::RVF + r, rph) && wait(Tr::VE + st, eph))) break;
+              const int t = first_of(j), n_hi = f.v.T - t, n_lo = f.lo - t, n_sinks = f.sinks - t;
+              const uint32_t raw = base + Tr::OFF_RV + r * Tr::RAW_V;
+              const int box_rows = min(a.block_size, kTile);
+              uint4 w[2];
+              uint32_t pair[2];
 #pragma unroll
-            for (int k = 0; k < PER; ++k) w[k] = lds128(base + Tr::OFF_RV + r * Tr::RAW + (k * 128 + tid) * 16);
+              for (int k = 0; k < 2; ++k) {
+                const int x = k * 128 + tid, row = x >> 1;
+                w[k] = lds128(raw + codes_at(row, box_rows) + rank * 32 + (x & 1) * 16);
+                pair[k] = lds32(raw + pair_at(row, box_rows));
+              }
 #pragma unroll
-            for (int k = 0; k < PER; ++k) {
-              const int x = k * 128 + tid, row = x >> 2, c = 2 * (x & 3);
-              uint4 lo, hi;
-              widen16(w[k], zv2, lo, hi);
-              if (row >= n_hi || (row < n_lo && !(SINKS && row < n_sinks))) lo = hi = make_uint4(0u, 0u, 0u, 0u);  // outside the sequence or the window
-              uint8_t* const to = sm + Tr::OFF_V + st * Tr::STAGE + (row >> 3) * Tr::VGROUP + (row & 7) * 128;
-              *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) = lo;
-              *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) << 4)) = hi;
+              for (int k = 0; k < 2; ++k) {
+                const int x = k * 128 + tid, row = x >> 1, c = 4 * (x & 1);
+                const bool out = row >= n_hi || (row < n_lo && !(SINKS && row < n_sinks));  // of the sequence or the window
+                uint8_t* const to = sm + Tr::OFF_V + st * Tr::STAGE + (row >> 3) * Tr::VGROUP + (row & 7) * 128;
+                const uint32_t words[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  *reinterpret_cast<uint4*>(to + (((c + i) ^ (row & 7)) << 4)) =
+                      out ? make_uint4(0u, 0u, 0u, 0u) : widen8(words[i], pair[k]);
+              }
+              done(Tr::VF + st, Tr::RVE + r);
             }
-            done(Tr::VF + st, Tr::RVE + r);
+          } else {
+            constexpr int PER = Tr::RAW_K / 16 / 128;  // 16-byte chunks of codes per thread
+            {
+              if (!(ok = wait(Tr::RKF + r, rph) && wait(Tr::KE + st, eph))) break;
+              uint4 w[PER];
+#pragma unroll
+              for (int k = 0; k < PER; ++k) w[k] = lds128(base + Tr::OFF_RK + r * Tr::RAW_K + (k * 128 + tid) * 16);
+#pragma unroll
+              for (int k = 0; k < PER; ++k) {
+                const int x = k * 128 + tid, row = x >> 3, c = 2 * (x & 7);
+                uint4 lo, hi;
+                widen16(w[k], zk2, lo, hi);
+                uint8_t* const to = sm + Tr::OFF_K + st * Tr::STAGE + (row >> 3) * Tr::KGROUP + (c >> 3) * 1024 + (row & 7) * 128;
+                *reinterpret_cast<uint4*>(to + (((c & 7) ^ (row & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4*>(to + ((((c & 7) + 1) ^ (row & 7)) << 4)) = hi;
+              }
+              done(Tr::KF + st, Tr::RKE + r);
+            }
+            {
+              if (!(ok = wait(Tr::RVF + r, rph) && wait(Tr::VE + st, eph))) break;
+              const int t = first_of(j), n_hi = f.v.T - t, n_lo = f.lo - t, n_sinks = f.sinks - t;
+              uint4 w[PER];
+#pragma unroll
+              for (int k = 0; k < PER; ++k) w[k] = lds128(base + Tr::OFF_RV + r * Tr::RAW_V + (k * 128 + tid) * 16);
+#pragma unroll
+              for (int k = 0; k < PER; ++k) {
+                const int x = k * 128 + tid, row = x >> 2, c = 2 * (x & 3);
+                uint4 lo, hi;
+                widen16(w[k], zv2, lo, hi);
+                if (row >= n_hi || (row < n_lo && !(SINKS && row < n_sinks))) lo = hi = make_uint4(0u, 0u, 0u, 0u);  // outside the sequence or the window
+                uint8_t* const to = sm + Tr::OFF_V + st * Tr::STAGE + (row >> 3) * Tr::VGROUP + (row & 7) * 128;
+                *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) << 4)) = hi;
+              }
+              done(Tr::VF + st, Tr::RVE + r);
+            }
           }
         }
       }

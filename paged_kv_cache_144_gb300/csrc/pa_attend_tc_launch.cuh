@@ -65,10 +65,11 @@ cudaError_t launch_tc_as(const AttendParams& a, const Plan& pl, uint8_t* ws, cud
   p.slots = pl.slots;
   p.counters = reinterpret_cast<int*>(ws);
   p.records = reinterpret_cast<float*>(ws + pl.records);
-  CUtensorMap tk, tv, tq;
+  CUtensorMap tk = {}, tv = {}, tq;  // (4-bit caches: bulk copies, no maps of K and V)
   const int64_t rows = a.num_blocks * a.num_kv_heads * a.block_size;
   auto box = [&](int most) { return a.block_size < most ? a.block_size : most; };
-  const bool maps = Tr::B8 ? encode_code_map(&tk, a.k_cache, rows, D, box(Tr::KROWS), D) &&
+  const bool maps = Tr::B4   ? true
+                    : Tr::B8 ? encode_code_map(&tk, a.k_cache, rows, D, box(Tr::KROWS), D) &&
                                  encode_code_map(&tv, a.v_cache, rows, D, box(kTile), D / CG)
                            : encode_tile_map(&tk, a.k_cache, rows, D, box(Tr::KROWS), Tr::NH) &&
                                  encode_tile_map(&tv, a.v_cache, rows, D, box(kTile), Tr::VH);
@@ -99,9 +100,10 @@ cudaError_t launch_tc(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaSt
   // the second product is free where memory traffic bounds the call, and wanted where the output keeps its precision
   const bool split = !pl.paired || a.out_dtype == PA_F32;
   // (sinks apart: their masks and tile numbers cost a call without them 5 % of its time)
-  if (a.sinks > 0)
+  if (a.sinks > 0 || std::is_same<KVT, i4_t>::value)
     return split ? launch_tc_as<KVT, D, CG, true, true>(a, pl, ws, stream) : launch_tc_as<KVT, D, CG, false, true>(a, pl, ws, stream);
-  return split ? launch_tc_as<KVT, D, CG, true, false>(a, pl, ws, stream) : launch_tc_as<KVT, D, CG, false, false>(a, pl, ws, stream);
+  if constexpr (!std::is_same<KVT, i4_t>::value)
+    return split ? launch_tc_as<KVT, D, CG, true, false>(a, pl, ws, stream) : launch_tc_as<KVT, D, CG, false, false>(a, pl, ws, stream);
 }
 
 }  // namespace

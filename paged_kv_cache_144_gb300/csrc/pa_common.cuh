@@ -130,6 +130,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// The same with an L2 cache policy (createpolicy).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 // 4-byte asynchronous copy global -> shared (no register destination).
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -210,6 +218,7 @@ template <> struct elem<f16_t> { static constexpr int bytes = 2; using storage =
 template <> struct elem<bf16_t> { static constexpr int bytes = 2; using storage = uint16_t; };
 template <> struct elem<e4m3_t> { static constexpr int bytes = 1; using storage = uint8_t; };
 template <> struct elem<i8_t> { static constexpr int bytes = 1; using storage = int8_t; };
+template <> struct elem<i4_t> { static constexpr int bytes = 0; };  // (half a byte: rows of their own layout)
 
 // Bytes of a 4-bit row: its codes, and its (scale, zero) pair.
 __host__ __device__ constexpr int int4_row_bytes(int head_dim) { return head_dim / 2 + 4; }
@@ -313,6 +322,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return r;
 }
 
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+  return r;
+}
+
 // atomic add with release semantics at GPU scope: this thread's earlier
 // writes (and those ordered before it by a warp barrier) become visible to
 // whoever observes the new value and then acquires (fence_acq_rel_gpu)
@@ -389,6 +404,19 @@ __device__ __forceinline__ void widen4_i8_biased(uint32_t w, uint32_t& lo, uint3
   const uint32_t u = w ^ 0x80808080u;
   lo = prmt(u, 0x64646464u, 0x5140u);
   hi = prmt(u, 0x64646464u, 0x7362u);
+}
+
+// Nibble J of each 16-bit half of w (4-bit codes) as f16x2 64 + code or bf16x2 16 + code, exact: the code lands on the
+// mantissa bits that count in ones above 64 (16).
+template <int J>
+__device__ __forceinline__ uint32_t nibbles_f16_64(uint32_t w) {
+  const uint32_t x = J == 0 ? w << 4 : w >> (4 * J - 4);
+  return (x & 0x00f000f0u) | 0x54005400u;
+}
+template <int J>
+__device__ __forceinline__ uint32_t nibbles_bf16_16(uint32_t w) {
+  const uint32_t x = J == 0 ? w << 3 : w >> (4 * J - 3);
+  return (x & 0x00780078u) | 0x41804180u;
 }
 
 // float32 y (= x * inv_scale, already rounded to float32) -> INT8 code:

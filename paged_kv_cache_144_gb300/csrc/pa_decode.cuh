@@ -64,6 +64,12 @@
 //    same recurrence after its own unit loop, one row per lane, writes
 //    out[s, kvh*G .. kvh*G+G-1] and resets the counter.  Nothing waits on
 //    another warp, so the kernel cannot deadlock.
+//  * 4-bit caches (pa_attend only): a tile of one block, codes then pairs, comes
+//    in one bulk copy.  Codes enter the products as they are, one mask and one
+//    shift per two of them (64 + code in f16 for K, 16 + code in bf16 for V, in
+//    the order of a word's nibbles); a row's scale multiplies its score, or its
+//    weight, and what the zeros and the added constants contribute is kept apart
+//    in float32 (q_sum, z_sum).
 //  * The variants of pa_attend (AP = 2; 3: with sinks) add the score modifiers, masks, ragged
 //    query rows and stored scores of include/pa.h; every difference is behind
 //    `if constexpr`, so the decode's own variants compile to what they were.
@@ -102,15 +108,17 @@ __host__ __device__ constexpr int align_up_c(int x, int a) { return (x + a - 1) 
 template <typename QT, typename KVT, int D, int GM, int UR_>
 struct DecodeTraits {
   static constexpr int KVB = elem<KVT>::bytes;
-  static constexpr int ROW = D * KVB;  // bytes of one cache row
-  static_assert(ROW == 128 || ROW == 256, "cache rows must be 128 or 256 bytes");
-  static constexpr int UR = UR_;                 // rows per work unit (32; 64 for 8-bit caches)
-  static_assert(UR == 32 || (UR == 64 && KVB == 1), "unit rows");
+  static constexpr bool B4 = std::is_same<KVT, i4_t>::value;  // 4-bit cache: rows of 64 bytes of codes, and 4 of their pair
+  static constexpr int ROW = B4 ? int4_row_bytes(D) : D * KVB;  // bytes of one cache row
+  static_assert(B4 || ROW == 128 || ROW == 256, "cache rows must be 128 or 256 bytes");
+  static constexpr int UR = UR_;                 // rows per work unit (32; 64 for 8- and 4-bit caches)
+  static_assert(UR == 32 || (UR == 64 && KVB <= 1), "unit rows");
   static constexpr int UR_SHIFT = UR == 64 ? 6 : 5;
-  static constexpr int NSUB = ROW / 128;         // 128-byte halves per row
+  static constexpr int NSUB = B4 ? 1 : ROW / 128;  // 128-byte halves per row
   static constexpr int TILE = UR * ROW;          // bytes of one unit of K (or V)
   static constexpr int QRAW = GM * D * 2;        // bytes of one raw query group
-  static constexpr int STAGE = align_up_c(2 * TILE + QRAW, 1024);  // K tile + V tile + raw q
+  static constexpr int ALIGN = B4 ? 128 : 1024;  // of a stage (the swizzle of the others' tiles)
+  static constexpr int STAGE = align_up_c(2 * TILE + QRAW, ALIGN);  // K tile + V tile + raw q
   // fused append: each stage can also stage the new K and V rows (16-bit
   // source format) and the physical block that receives them
   static constexpr int OFF_NEW = 2 * TILE + QRAW;
@@ -122,8 +130,8 @@ struct DecodeTraits {
   static constexpr int NT = UR / 8;              // 8-token n-tiles of a unit
   static constexpr int NSB = UR / 16;            // 16-token sub-tiles (one PV k-step each)
   static constexpr bool B8 = KVB == 1;          // FP8-e4m3 or INT8 cache
-  static constexpr bool MMA_BF16 = !B8 && std::is_same<KVT, bf16_t>::value;  // else f16
-  static_assert(!B8 || D == 128, "8-bit caches: head_dim 128");
+  static constexpr bool MMA_BF16 = KVB == 2 && std::is_same<KVT, bf16_t>::value;  // else f16
+  static_assert(KVB == 2 || D == 128, "8- and 4-bit caches: head_dim 128");
   // per-consumer shared memory: [full[MAX_NS] | empty[MAX_NS] | NS stages]
   static constexpr int OFF_FULL = 0;
   static constexpr int OFF_EMPTY = OFF_FULL + MAX_NS * 8;
@@ -428,7 +436,8 @@ __global__ void __launch_bounds__((DecodeTraits<QT, KVT, D, GM, UR_>::MAX_W + 1)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                     const DecodeParams p) {
   using Tr = DecodeTraits<QT, KVT, D, GM, UR_>;
-  constexpr bool k8bit = elem<KVT>::bytes == 1;
+  constexpr bool k8bit = elem<KVT>::bytes == 1, k4bit = Tr::B4;
+  static_assert(!k4bit || AP == 3, "4-bit caches: pa_attend");
   constexpr int UR = Tr::UR;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -484,7 +493,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   // before it touches memory.
   griddep_launch_dependents();
   if constexpr (ATT) griddep_wait();  // pa_attend reads nothing early
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && !k4bit) {
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
   }
@@ -695,7 +704,22 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
             pb = 0;
           }
           const int z = (pb * Hkv + it.kvh) * B + row_in_block;
-          if constexpr (ATT) {
+          if constexpr (k4bit) {
+            // a tile is one piece, codes then pairs; of a block longer than a unit, the unit's part of each
+            const int64_t at = (static_cast<int64_t>(pb) * Hkv + it.kvh) * (B * Tr::ROW);
+            const uint8_t* const ks = static_cast<const uint8_t*>(p.k_cache) + at;
+            const uint8_t* const vs = static_cast<const uint8_t*>(p.v_cache) + at;
+            if (BOX == B) {
+              bulk_load(kdst + i * BOX * Tr::ROW, ks, BOX * Tr::ROW, bar, policy);
+              bulk_load(vdst + i * BOX * Tr::ROW, vs, BOX * Tr::ROW, bar, policy);
+            } else {
+              const int codes = row_in_block * (D / 2), pairs = B * (D / 2) + row_in_block * 4;
+              bulk_load(kdst, ks + codes, UR * (D / 2), bar, policy);
+              bulk_load(kdst + UR * (D / 2), ks + pairs, UR * 4, bar, policy);
+              bulk_load(vdst, vs + codes, UR * (D / 2), bar, policy);
+              bulk_load(vdst + UR * (D / 2), vs + pairs, UR * 4, bar, policy);
+            }
+          } else if constexpr (ATT) {
             tma_load_3d(kdst + i * BOX * Tr::ROW, &tmap_k, 0, z, 0, bar, policy);
             tma_load_3d(vdst + i * BOX * Tr::ROW, &tmap_v, 0, z, 0, bar, policy);
           } else {
@@ -827,6 +851,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 
   // ===================================================================== consumer
   constexpr bool MB = Tr::MMA_BF16;
+  constexpr bool PB = MB || k4bit;  // the type of the weights
   // INT8 V as 1152 + code with the bias taken off the output; pa_attend takes the zero point off each code instead: the
   // bias is ~1000 times an average of many values, and its float32 rounding would show in 16-bit outputs
   constexpr bool kBiasV = std::is_same<KVT, i8_t>::value && !ATT;
@@ -870,8 +895,17 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   // 8-bit tiles: n-position j of an 8-token n-tile holds token j ^ 4(j & 1),
   // which keeps both the K and the V loads below free of bank conflicts.
   auto sigma = [](int j) { return j ^ ((j & 1) << 2); };
+  // 4-bit tiles: it holds token tau(j): rows are 64 bytes, so two rows that one 128-byte access reads together are an even and
+  // an odd one.
+  auto tau = [](int j) { return j ^ ((j >> 1) & 1); };
+  auto token_at = [&](int j) { return k4bit ? tau(j) : k8bit ? sigma(j) : j; };
+  // 4-bit tiles: where rows 8 x .. 8 x + 7 lie: boxes of BOX rows, codes then pairs
+  auto codes_of = [&](int x) { return static_cast<uint32_t>(512 * x + 4 * ((8 * x) & ~(BOX - 1))); };
+  auto pairs_of = [&](int x) { return static_cast<uint32_t>(32 * x + 64 * (((8 * x) & ~(BOX - 1)) + BOX)); };
   uint32_t kb8[2], vb8[2][Tr::KS / 2];
-  if constexpr (!k8bit) {
+  if constexpr (k4bit) {
+    // (addresses are a few additions where they are used)
+  } else if constexpr (!k8bit) {
     const int lt = (lane & 7) + ((lane >> 4) << 3);
     const int lhi = (lane >> 3) & 1;
 #pragma unroll
@@ -906,6 +940,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   }
   // head_dim column of accumulator row (m-tile i, half hf) of O^T
   auto dim_of = [&](int i, int hf) -> int {
+    if constexpr (k4bit) return 16 * gid + 2 * i + hf;
     if constexpr (!k8bit) return 16 * i + gid + 8 * hf;
     return 32 * (i >> 1) + 4 * gid + 2 * (i & 1) + hf;
   };
@@ -939,6 +974,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     return p.att.scores + (static_cast<int64_t>(s) * Hkv + kvh) * p.att.score_stride * G;
   };
   uint32_t zpk2 = 0u, zpv2 = 0u;  // INT8: f16x2(1152 + zero point) of this KV head
+  // 4-bit caches.  K enters S as 64 + code (f16), so a score is scale S + (zero - 64 scale) sum(q); V enters O as 16 + code
+  // (bf16) with the weights times the row's scale, so O lacks sum(weight (zero - 16 scale)): both in float32.
+  [[maybe_unused]] float q_sum[NR], z_sum[NR];  // of this lane's softmax rows
 
   // One unit: S^T = Q K^T, online-softmax update, O^T += V^T P^T.
   // FULL: all UR rows valid.
@@ -956,7 +994,30 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       float sc[NMT][4];
 #pragma unroll
       for (int mt = 0; mt < NMT; ++mt) sc[mt][0] = sc[mt][1] = sc[mt][2] = sc[mt][3] = 0.f;
-      if constexpr (!k8bit) {
+      if constexpr (k4bit) {
+#pragma unroll
+        for (int mt = 0; mt < NMT; ++mt) {
+          // 32 values of tokens tau(g) and 8 + tau(g): word r holds those of k-steps 2 r and 2 r + 1
+          const uint4 w0 = lds128(kt + codes_of(2 * mt) + tau(gid) * 64 + tig * 16);
+          const uint4 w1 = lds128(kt + codes_of(2 * mt + 1) + tau(gid) * 64 + tig * 16);
+          const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w};
+          const uint32_t x1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            mma16816<false>(sc[mt], nibbles_f16_64<0>(x0[r]), nibbles_f16_64<0>(x1[r]), nibbles_f16_64<1>(x0[r]),
+                            nibbles_f16_64<1>(x1[r]), qa0[2 * r], qa1[2 * r]);
+            mma16816<false>(sc[mt], nibbles_f16_64<2>(x0[r]), nibbles_f16_64<2>(x1[r]), nibbles_f16_64<3>(x0[r]),
+                            nibbles_f16_64<3>(x1[r]), qa0[2 * r + 1], qa1[2 * r + 1]);
+          }
+          const float2 p0 = widen2<f16_t>(lds32(kt + pairs_of(2 * mt) + tau(gid) * 4));
+          const float2 p1 = widen2<f16_t>(lds32(kt + pairs_of(2 * mt + 1) + tau(gid) * 4));
+          const float z0 = fmaf(-64.f, p0.x, p0.y), z1 = fmaf(-64.f, p1.x, p1.y);
+          sc[mt][0] = fmaf(sc[mt][0], p0.x, z0 * q_sum[0]);
+          sc[mt][1] = fmaf(sc[mt][1], p0.x, z0 * q_sum[1]);
+          sc[mt][2] = fmaf(sc[mt][2], p1.x, z1 * q_sum[0]);
+          sc[mt][3] = fmaf(sc[mt][3], p1.x, z1 * q_sum[1]);
+        }
+      } else if constexpr (!k8bit) {
 #pragma unroll
         for (int mt = 0; mt < NMT; ++mt) {
 #pragma unroll
@@ -994,7 +1055,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float x = sc[mt][e] * score_scale;
-          const int tok = 16 * mt + 8 * (e >> 1) + (k8bit ? sigma(gid) : gid);
+          const int tok = 16 * mt + 8 * (e >> 1) + token_at(gid);
           if constexpr (ATT) {
             if (p.att.softcap > 0.f) x = cap2 - __fdividef(2.f * cap2, 1.f + fast_exp2(sc[mt][e] * capk));
             if (p.att.slopes) x -= slope2[e & 1] * static_cast<float>(qpos[0] - (j * UR + tok));
@@ -1017,7 +1078,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           for (int mt = 0; mt < NMT; ++mt) {
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-              const int tok = 16 * mt + 4 * e + (k8bit ? sigma(gid) : gid);
+              const int tok = 16 * mt + 4 * e + token_at(gid);
               if (tok >= n_valid || (tok < lo_rel && !(SINKS && tok < sink_rel))) continue;
               if (score_row[1] && (G & 1) == 0) {
                 *reinterpret_cast<float2*>(at + tok * G) = make_float2(sc[mt][e], sc[mt][e + 1]);
@@ -1042,6 +1103,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         m[1] = mn1;
         l[0] *= a0;
         l[1] *= a1;
+        if constexpr (k4bit) {
+          z_sum[0] *= a0;
+          z_sum[1] *= a1;
+        }
 #pragma unroll
         for (int i = 0; i < Tr::KS; ++i) {
           acc[i][0][0] *= a0;
@@ -1054,25 +1119,61 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       // (2t + 8, 2t + 9) of P^T, the token order the V loads use
 #pragma unroll
       for (int mt = 0; mt < NMT; ++mt) {
-        const float p0 = fast_exp2(sc[mt][0] - m[0]);
-        const float p1 = fast_exp2(sc[mt][1] - m[1]);
-        const float p2 = fast_exp2(sc[mt][2] - m[0]);
-        const float p3 = fast_exp2(sc[mt][3] - m[1]);
+        float p0 = fast_exp2(sc[mt][0] - m[0]);
+        float p1 = fast_exp2(sc[mt][1] - m[1]);
+        float p2 = fast_exp2(sc[mt][2] - m[0]);
+        float p3 = fast_exp2(sc[mt][3] - m[1]);
         l[0] += p0 + p2;
         l[1] += p1 + p3;
-        const uint32_t h01 = pack2<MB>(p0, p1), h23 = pack2<MB>(p2, p3);
-        const float2 f01 = unpack2<MB>(h01), f23 = unpack2<MB>(h23);
+        if constexpr (k4bit) {
+          float2 v0 = widen2<f16_t>(lds32(vt + pairs_of(2 * mt) + tau(gid) * 4));
+          float2 v1 = widen2<f16_t>(lds32(vt + pairs_of(2 * mt + 1) + tau(gid) * 4));
+          if constexpr (!FULL) {  // (a row that is not attended may hold anything)
+            auto in = [&](int tok) { return tok < n_valid && (tok >= lo_rel || tok < sink_rel); };
+            if (!in(16 * mt + tau(gid))) v0 = make_float2(0.f, 0.f);
+            if (!in(16 * mt + 8 + tau(gid))) v1 = make_float2(0.f, 0.f);
+          }
+          const float z0 = fmaf(-16.f, v0.x, v0.y), z1 = fmaf(-16.f, v1.x, v1.y);
+          z_sum[0] = fmaf(p0, z0, fmaf(p2, z1, z_sum[0]));
+          z_sum[1] = fmaf(p1, z0, fmaf(p3, z1, z_sum[1]));
+          p0 *= v0.x;
+          p1 *= v0.x;
+          p2 *= v1.x;
+          p3 *= v1.x;
+        }
+        const uint32_t h01 = pack2<PB>(p0, p1), h23 = pack2<PB>(p2, p3);
+        const float2 f01 = unpack2<PB>(h01), f23 = unpack2<PB>(h23);
         ph[mt][0][0] = movmatrix_trans(h01);
         ph[mt][0][1] = movmatrix_trans(h23);
-        pl[mt][0][0] = movmatrix_trans(pack2<MB>(p0 - f01.x, p1 - f01.y));
-        pl[mt][0][1] = movmatrix_trans(pack2<MB>(p2 - f23.x, p3 - f23.y));
+        pl[mt][0][0] = movmatrix_trans(pack2<PB>(p0 - f01.x, p1 - f01.y));
+        pl[mt][0][1] = movmatrix_trans(pack2<PB>(p2 - f23.x, p3 - f23.y));
       }
     } else {
       float sc[Tr::NT][4];
 #pragma unroll
       for (int nt = 0; nt < Tr::NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
       // ---- scores
-      if constexpr (!k8bit) {
+      if constexpr (k4bit) {
+#pragma unroll
+        for (int nt = 0; nt < Tr::NT; ++nt) {
+          const uint4 w = lds128(kt + codes_of(nt) + tau(gid) * 64 + tig * 16);
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            mma16816<false>(sc[nt], qa0[2 * r], NH == 2 ? qb0[2 * r] : 0u, qa1[2 * r], NH == 2 ? qb1[2 * r] : 0u,
+                            nibbles_f16_64<0>(ws[r]), nibbles_f16_64<1>(ws[r]));
+            mma16816<false>(sc[nt], qa0[2 * r + 1], NH == 2 ? qb0[2 * r + 1] : 0u, qa1[2 * r + 1],
+                            NH == 2 ? qb1[2 * r + 1] : 0u, nibbles_f16_64<2>(ws[r]), nibbles_f16_64<3>(ws[r]));
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 kp = widen2<f16_t>(lds32(kt + pairs_of(nt) + tau(2 * tig + e) * 4));
+            const float z = fmaf(-64.f, kp.x, kp.y);
+#pragma unroll
+            for (int h = 0; h < NH; ++h) sc[nt][2 * h + e] = fmaf(sc[nt][2 * h + e], kp.x, z * q_sum[h]);
+          }
+        }
+      } else if constexpr (!k8bit) {
 #pragma unroll
         for (int sb = 0; sb < Tr::NSB; ++sb) {
 #pragma unroll
@@ -1121,7 +1222,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           for (int e = 0; e < 2; ++e) {
             float x = sc[nt][2 * h + e] * score_scale;
             if constexpr (!FULL) {
-              const int tok = nt * 8 + (k8bit ? sigma(2 * tig + e) : 2 * tig + e);
+              const int tok = nt * 8 + token_at(2 * tig + e);
               bool ok = tok < n_valid && tok >= lo_rel;
               if constexpr (MQ) ok = ok && tok <= hr && tok >= lr;
               if constexpr (SINKS) ok = ok || (tok < p.att.sinks - j * UR && tok < n_valid && tok <= hr);
@@ -1151,6 +1252,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           const float alpha = (MQ && mn == -INFINITY) ? 1.f : fast_exp2(m[h] - mn);
           m[h] = mn;
           l[h] *= alpha;
+          if constexpr (k4bit) z_sum[h] *= alpha;
           const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * tig);      // row 8h + 2t
           const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * tig + 4);  // row 8h + 2t + 1
 #pragma unroll
@@ -1168,19 +1270,31 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         const float ms = (MQ && m[h] == -INFINITY) ? 0.f : m[h];  // exp2(-inf - ms) = 0 for an empty row
 #pragma unroll
         for (int nt = 0; nt < Tr::NT; ++nt) {
-          const float p0 = fast_exp2(sc[nt][2 * h] - ms);
-          const float p1 = fast_exp2(sc[nt][2 * h + 1] - ms);
+          float p0 = fast_exp2(sc[nt][2 * h] - ms);
+          float p1 = fast_exp2(sc[nt][2 * h + 1] - ms);
           l[h] += p0 + p1;
-          const uint32_t hp = pack2<MB>(p0, p1);
-          const float2 hf = unpack2<MB>(hp);
+          if constexpr (k4bit) {
+            float2 v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int tok = nt * 8 + tau(2 * tig + e);
+              v[e] = widen2<f16_t>(lds32(vt + pairs_of(nt) + tau(2 * tig + e) * 4));
+              if (tok >= n_valid || (tok < lo_rel && tok >= sink_rel)) v[e] = make_float2(0.f, 0.f);  // not attended
+            }
+            z_sum[h] = fmaf(p0, fmaf(-16.f, v[0].x, v[0].y), fmaf(p1, fmaf(-16.f, v[1].x, v[1].y), z_sum[h]));
+            p0 *= v[0].x;
+            p1 *= v[1].x;
+          }
+          const uint32_t hp = pack2<PB>(p0, p1);
+          const float2 hf = unpack2<PB>(hp);
           ph[nt >> 1][h][nt & 1] = hp;
-          pl[nt >> 1][h][nt & 1] = pack2<MB>(p0 - hf.x, p1 - hf.y);
+          pl[nt >> 1][h][nt & 1] = pack2<PB>(p0 - hf.x, p1 - hf.y);
         }
       }
     }
     // rows past the end of the sequence, and rows before a sliding window,
-    // may hold anything (or were not loaded): zero them in V
-    if constexpr (!FULL) {
+    // may hold anything (or were not loaded): zero them in V (4 bits: codes are finite, and such a row's pair counts as zero)
+    if constexpr (!FULL && !k4bit) {
       const int s0 = SINKS ? min(max(sink_rel, 0), UR) : 0;  // (sinks before the window stay; it may start behind their unit)
       const int nlo = max((SINKS ? min(lo_rel, UR) : lo_rel) - s0, 0);
       const int nz = (UR - n_valid + nlo) * Tr::NSUB * 8;
@@ -1194,7 +1308,43 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       __syncwarp();
     }
     // ---- O^T += V^T P^T
-    if constexpr (!k8bit) {
+    if constexpr (k4bit) {
+#pragma unroll
+      for (int sb = 0; sb < Tr::NSB; ++sb) {
+        // 16 values of tokens tau(2t), tau(2t + 1) of the two 8-row groups; a nibble of two tokens' words side by side is an
+        // operand register: even values from the words' lower halves, odd ones from the upper
+        uint2 v[2][2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) v[x][e] = lds64(vt + codes_of(2 * sb + x) + tau(2 * tig + e) * 64 + gid * 8);
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t even[2], odd[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t a = w ? v[x][0].y : v[x][0].x, b = w ? v[x][1].y : v[x][1].x;
+            even[x] = prmt(a, b, 0x5410u);
+            odd[x] = prmt(a, b, 0x7632u);
+          }
+          auto product = [&](auto nibble) {
+            constexpr int J = decltype(nibble)::value;
+            const uint32_t a0 = nibbles_bf16_16<J>(even[0]), a1 = nibbles_bf16_16<J>(odd[0]);
+            const uint32_t a2 = nibbles_bf16_16<J>(even[1]), a3 = nibbles_bf16_16<J>(odd[1]);
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              mma16816<true>(acc[4 * w + J][h], a0, a1, a2, a3, ph[sb][h][0], ph[sb][h][1]);
+              mma16816<true>(acc[4 * w + J][h], a0, a1, a2, a3, pl[sb][h][0], pl[sb][h][1]);
+            }
+          };
+          product(std::integral_constant<int, 0>());
+          product(std::integral_constant<int, 1>());
+          product(std::integral_constant<int, 2>());
+          product(std::integral_constant<int, 3>());
+        }
+      }
+    } else if constexpr (!k8bit) {
 #pragma unroll
       for (int sb = 0; sb < Tr::NSB; ++sb) {
 #pragma unroll
@@ -1260,7 +1410,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     if (lane < 2 * CH) {
       const int which = lane / CH, ch = lane % CH;  // 0: K, 1: V
       uint4 w;
-      if constexpr (!k8bit) {
+      if constexpr (!k8bit) {  // (no 4-bit form: pa_decode only)
         w = *reinterpret_cast<const uint4*>(staged + which * 2 * D + ch * 16);
       } else {
         // 16 source values -> 16 cache bytes
@@ -1405,7 +1555,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     // rounding of every element within 2^28 of the group's largest (bf16 has 8
     // significant bits, f16 11); smaller elements can lose bits as f16
     // subnormals, an absolute error below 2^-38 of the largest element.
-    constexpr bool q_rescale = k8bit && std::is_same<QT, bf16_t>::value;
+    constexpr bool q_rescale = (k8bit || k4bit) && std::is_same<QT, bf16_t>::value;
     int qexp = 0;
     [[maybe_unused]] int64_t row_base = 0;  // pa_attend: the sequence's first row of q and out
     if constexpr (ATT) {
@@ -1426,8 +1576,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 #pragma unroll
         for (int s = 0; s < Tr::KS; ++s) {
           // columns of k-step s held by this lane: (d, d+1) for a0/a1, (d2, d2+1) for a2/a3
-          const int d = k8bit ? (MQ ? 16 * (4 * (s >> 2) + tig) + 4 * (s & 3) : 32 * tig + 4 * s) : 16 * s + 2 * tig;
-          const int d2 = k8bit ? d + 2 : d + 8;
+          const int d = k4bit ? 32 * tig + 4 * s : k8bit ? (MQ ? 16 * (4 * (s >> 2) + tig) + 4 * (s & 3) : 32 * tig + 4 * s) : 16 * s + 2 * tig;
+          const int d2 = k8bit || k4bit ? d + 2 : d + 8;
           uint32_t w0 = 0u, w1 = 0u;
           if (row_ok) {
             w0 = *reinterpret_cast<const uint32_t*>(qr + ((row0 + row) * D + d) * 2);
@@ -1514,6 +1664,27 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         }
       }
     }
+    if constexpr (k4bit) {
+      // the sums of query rows g (and g + 8), as they enter the products; one query: then of this lane's rows 2t, 2t + 1
+      auto sum_row = [&](const uint32_t(&a)[Tr::KS], const uint32_t(&b)[Tr::KS]) {
+        float x = 0.f;
+#pragma unroll
+        for (int s = 0; s < Tr::KS; ++s) {
+          const float2 f = widen2<f16_t>(a[s]), g = widen2<f16_t>(b[s]);
+          x += (f.x + f.y) + (g.x + g.y);
+        }
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        return x + __shfl_xor_sync(0xffffffffu, x, 2);
+      };
+      const float sg = sum_row(qa0, qa1);
+      if constexpr (MQ) {
+        q_sum[0] = sg;
+        q_sum[1] = sum_row(qb0, qb1);
+      } else {
+        q_sum[0] = __shfl_sync(0xffffffffu, sg, 8 * tig);
+        q_sum[1] = __shfl_sync(0xffffffffu, sg, 8 * tig + 4);
+      }
+    }
     score_scale = p.qk_scale_log2;
     if constexpr (k8bit) score_scale *= hp_ks[it.kvh];
     if constexpr (q_rescale) score_scale *= __int_as_float((127 - qexp) << 23);
@@ -1531,6 +1702,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     for (int h = 0; h < NR; ++h) {
       m[h] = -INFINITY;
       l[h] = 0.f;
+      if constexpr (k4bit) z_sum[h] = 0.f;
     }
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
@@ -1587,6 +1759,33 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           lt[h] = l[h];
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) lt[h] += __shfl_xor_sync(0xffffffffu, lt[h], off);
+        }
+      }
+      if constexpr (k4bit) {  // the rows' share of the zeros joins their products
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          float z0, z1;  // of rows 8h + 2t, 8h + 2t + 1
+          if constexpr (MQ) {
+            float z = z_sum[h] + __shfl_xor_sync(0xffffffffu, z_sum[h], 1);
+            z += __shfl_xor_sync(0xffffffffu, z, 2);
+            z0 = __shfl_sync(0xffffffffu, z, 8 * tig);
+            z1 = __shfl_sync(0xffffffffu, z, 8 * tig + 4);
+          } else {
+            z0 = z_sum[0];
+            z1 = z_sum[1];
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+              z0 += __shfl_xor_sync(0xffffffffu, z0, off);
+              z1 += __shfl_xor_sync(0xffffffffu, z1, off);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < Tr::KS; ++i) {
+            acc[i][h][0] += z0;
+            acc[i][h][1] += z1;
+            acc[i][h][2] += z0;
+            acc[i][h][3] += z1;
+          }
         }
       }
       float vs = 1.f, voff = 0.f;  // out = acc * vs / l - voff (INT8: V entered as 1152 + code)
@@ -1767,7 +1966,7 @@ struct DecodeVariant {
     constexpr bool mq = GM > 8;
     if (nc < 1 || (!mq && nc != 1) || nc > 4) return false;
     // several queries: K and V only (the query rows have a buffer per ring)
-    const int stage = mq ? align_up_c(2 * Tr::TILE, 1024) : (AP == 1 ? Tr::STAGE_APPEND : Tr::STAGE);
+    const int stage = mq ? align_up_c(2 * Tr::TILE, Tr::ALIGN) : (AP == 1 ? Tr::STAGE_APPEND : Tr::STAGE);
     const int env_ns = tuning_override("PA_DECODE_STAGES");
     const int env_w = tuning_override("PA_DECODE_WARPS");
     int best_w = 0, best_occ = 0, best_ns = 0;

@@ -305,7 +305,7 @@ PA_EXPORT int pa_attend(void* out, pa_dtype out_dtype, const void* q, pa_dtype q
   if (!out || !q || !block_tables || !seq_lens) return PA_ERR_NULL;
   if (out_dtype != PA_F32 && out_dtype != PA_F16 && out_dtype != PA_BF16) return PA_ERR_DTYPE;
   if (q_dtype != PA_F16 && q_dtype != PA_BF16) return PA_ERR_DTYPE;
-  if (kv_dtype != q_dtype && !is8bit(kv_dtype)) return PA_ERR_DTYPE;
+  if (kv_dtype != q_dtype && !is8bit(kv_dtype) && kv_dtype != PA_INT4) return PA_ERR_DTYPE;
   if (is8bit(kv_dtype) && (!k_scale || !v_scale)) return PA_ERR_NULL;
   if (kv_dtype == PA_INT8 && (!o.k_zero_point || !o.v_zero_point)) return PA_ERR_NULL;
   const int ps = check_pool(k_cache, v_cache, num_blocks, num_kv_heads, block_size);
