@@ -406,17 +406,22 @@ __device__ __forceinline__ void widen4_i8_biased(uint32_t w, uint32_t& lo, uint3
   hi = prmt(u, 0x64646464u, 0x7362u);
 }
 
-// Nibble J of each 16-bit half of w (4-bit codes) as f16x2 64 + code or bf16x2 16 + code, exact: the code lands on the
-// mantissa bits that count in ones above 64 (16).
+// The nibbles of each 16-bit half of w (4-bit codes) as f16x2 without a conversion: in an otherwise empty half, code c in
+// bits 0 .. 3 is the subnormal c 2^-24, in bits 4 .. 7 c 2^-20.  One mask per pair, one shift per word: nibbles 0 and 2 are
+// in units of 2^-24, 1 and 3 of 2^-20, which whoever multiplies them makes up for.  (Products with subnormal f16 operands
+// are exact on the tensor cores.)
+__device__ __forceinline__ void nibbles4(uint32_t w, uint32_t (&n)[4]) {
+  const uint32_t u = w >> 8;
+  n[0] = w & 0x000f000fu;
+  n[1] = w & 0x00f000f0u;
+  n[2] = u & 0x000f000fu;
+  n[3] = u & 0x00f000f0u;
+}
+// Nibble J of each half as f16x2 64 + code, exact.
 template <int J>
 __device__ __forceinline__ uint32_t nibbles_f16_64(uint32_t w) {
   const uint32_t x = J == 0 ? w << 4 : w >> (4 * J - 4);
   return (x & 0x00f000f0u) | 0x54005400u;
-}
-template <int J>
-__device__ __forceinline__ uint32_t nibbles_bf16_16(uint32_t w) {
-  const uint32_t x = J == 0 ? w << 3 : w >> (4 * J - 3);
-  return (x & 0x00780078u) | 0x41804180u;
 }
 
 // float32 y (= x * inv_scale, already rounded to float32) -> INT8 code:

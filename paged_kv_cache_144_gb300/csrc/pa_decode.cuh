@@ -65,11 +65,12 @@
 //    out[s, kvh*G .. kvh*G+G-1] and resets the counter.  Nothing waits on
 //    another warp, so the kernel cannot deadlock.
 //  * 4-bit caches (pa_attend only): a tile of one block, codes then pairs, comes
-//    in one bulk copy.  Codes enter the products as they are, one mask and one
-//    shift per two of them (64 + code in f16 for K, 16 + code in bf16 for V, in
-//    the order of a word's nibbles); a row's scale multiplies its score, or its
-//    weight, and what the zeros and the added constants contribute is kept apart
-//    in float32 (q_sum, z_sum).
+//    in one bulk copy.  Codes enter the products as f16 subnormals, in the order
+//    of a word's nibbles: five instructions for eight of them, and no constant
+//    added that would have to be taken off again (with 64 + code and 16 + code the
+//    average of 32768 rows lost four bits to it: error 3.6e-3 against 1.7e-3 in a
+//    bf16 output).  A row's scale multiplies its score, or its weight; what the
+//    zeros contribute is added up apart in float32 (q_sum, z_sum).
 //  * The variants of pa_attend (AP = 2; 3: with sinks) add the score modifiers, masks, ragged
 //    query rows and stored scores of include/pa.h; every difference is behind
 //    `if constexpr`, so the decode's own variants compile to what they were.
@@ -91,6 +92,7 @@
 
 namespace pa {
 
+constexpr float kCodeUnit = 16777216.f;        // 4-bit codes enter the products in units of 2^-24
 constexpr int kMinUnitsPerWarp = 2;            // smallest balanced share (small batches spread wide)
 constexpr int kStageBytesPerWarp = 24 * 1024;  // default K/V pipeline bytes per consumer warp
 constexpr int kTablePrefetch = 3;              // units whose table entries the producer fetches ahead
@@ -851,7 +853,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 
   // ===================================================================== consumer
   constexpr bool MB = Tr::MMA_BF16;
-  constexpr bool PB = MB || k4bit;  // the type of the weights
   // INT8 V as 1152 + code with the bias taken off the output; pa_attend takes the zero point off each code instead: the
   // bias is ~1000 times an average of many values, and its float32 rounding would show in 16-bit outputs
   constexpr bool kBiasV = std::is_same<KVT, i8_t>::value && !ATT;
@@ -974,9 +975,21 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     return p.att.scores + (static_cast<int64_t>(s) * Hkv + kvh) * p.att.score_stride * G;
   };
   uint32_t zpk2 = 0u, zpv2 = 0u;  // INT8: f16x2(1152 + zero point) of this KV head
-  // 4-bit caches.  K enters S as 64 + code (f16), so a score is scale S + (zero - 64 scale) sum(q); V enters O as 16 + code
-  // (bf16) with the weights times the row's scale, so O lacks sum(weight (zero - 16 scale)): both in float32.
+  // 4-bit caches.  Codes enter both products alone: a score is scale S + zero sum(q); O takes the weights times the row's
+  // scale, and lacks sum(weight zero), which is added up apart in float32.  Scaled weights go to f16 times 2^(29 - vexp), which
+  // is 2^15 over a power of two above the scales seen so far, so that none exceeds f16 and those down to 2^-39 of the largest
+  // count; O follows when a larger scale comes, as it follows the maximum.  vexp: that scale's f16 exponent field (-1: none).
   [[maybe_unused]] float q_sum[NR], z_sum[NR];  // of this lane's softmax rows
+  [[maybe_unused]] int vexp = -1;
+  // the larger of the scales' bits so far and those of pair word w
+  [[maybe_unused]] auto scale_bits = [](int most, uint32_t w) { return max(most, static_cast<int>(w & 0x7fffu)); };
+  // vexp for scales up to these bits of any lane; returns what O is multiplied by
+  [[maybe_unused]] auto larger_scale = [&](int bits) {
+    const int e = max(vexp, __reduce_max_sync(0xffffffffu, bits) >> 10), down = vexp - e;
+    vexp = e;
+    return __int_as_float((127 + down) << 23);
+  };
+  [[maybe_unused]] auto weight_unit = [&] { return __int_as_float((127 + 29 - vexp) << 23); };
 
   // One unit: S^T = Q K^T, online-softmax update, O^T += V^T P^T.
   // FULL: all UR rows valid.
@@ -1004,18 +1017,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           const uint32_t x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            mma16816<false>(sc[mt], nibbles_f16_64<0>(x0[r]), nibbles_f16_64<0>(x1[r]), nibbles_f16_64<1>(x0[r]),
-                            nibbles_f16_64<1>(x1[r]), qa0[2 * r], qa1[2 * r]);
-            mma16816<false>(sc[mt], nibbles_f16_64<2>(x0[r]), nibbles_f16_64<2>(x1[r]), nibbles_f16_64<3>(x0[r]),
-                            nibbles_f16_64<3>(x1[r]), qa0[2 * r + 1], qa1[2 * r + 1]);
+            uint32_t n0[4], n1[4];
+            nibbles4(x0[r], n0);
+            nibbles4(x1[r], n1);
+            mma16816<false>(sc[mt], n0[0], n1[0], n0[1], n1[1], qa0[2 * r], qa1[2 * r]);
+            mma16816<false>(sc[mt], n0[2], n1[2], n0[3], n1[3], qa0[2 * r + 1], qa1[2 * r + 1]);
           }
           const float2 p0 = widen2<f16_t>(lds32(kt + pairs_of(2 * mt) + tau(gid) * 4));
           const float2 p1 = widen2<f16_t>(lds32(kt + pairs_of(2 * mt + 1) + tau(gid) * 4));
-          const float z0 = fmaf(-64.f, p0.x, p0.y), z1 = fmaf(-64.f, p1.x, p1.y);
-          sc[mt][0] = fmaf(sc[mt][0], p0.x, z0 * q_sum[0]);
-          sc[mt][1] = fmaf(sc[mt][1], p0.x, z0 * q_sum[1]);
-          sc[mt][2] = fmaf(sc[mt][2], p1.x, z1 * q_sum[0]);
-          sc[mt][3] = fmaf(sc[mt][3], p1.x, z1 * q_sum[1]);
+          const float s0 = p0.x * kCodeUnit, s1 = p1.x * kCodeUnit;
+          sc[mt][0] = fmaf(sc[mt][0], s0, p0.y * q_sum[0]);
+          sc[mt][1] = fmaf(sc[mt][1], s0, p0.y * q_sum[1]);
+          sc[mt][2] = fmaf(sc[mt][2], s1, p1.y * q_sum[0]);
+          sc[mt][3] = fmaf(sc[mt][3], s1, p1.y * q_sum[1]);
         }
       } else if constexpr (!k8bit) {
 #pragma unroll
@@ -1095,10 +1109,27 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
       }
+      // 4-bit: the V rows' pairs (of one that is not attended, which may hold anything: zero), their largest scale
+      [[maybe_unused]] uint32_t vpair[NMT][2];
+      [[maybe_unused]] int vbits = 0;
+      if constexpr (k4bit) {
+#pragma unroll
+        for (int mt = 0; mt < NMT; ++mt) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            vpair[mt][x] = lds32(vt + pairs_of(2 * mt + x) + tau(gid) * 4);
+            if constexpr (!FULL) {
+              const int tok = 16 * mt + 8 * x + tau(gid);
+              if (tok >= n_valid || (tok < lo_rel && tok >= sink_rel)) vpair[mt][x] = 0u;
+            }
+            vbits = scale_bits(vbits, vpair[mt][x]);
+          }
+        }
+      }
       // every row sees a token in every unit it processes: the new maxima are finite
-      if (__any_sync(0xffffffffu, mx0 > m[0] || mx1 > m[1])) {
+      if (__any_sync(0xffffffffu, mx0 > m[0] || mx1 > m[1] || (k4bit && (vbits >> 10) > vexp))) {
         const float mn0 = fmaxf(m[0], mx0), mn1 = fmaxf(m[1], mx1);
-        const float a0 = fast_exp2(m[0] - mn0), a1 = fast_exp2(m[1] - mn1);
+        float a0 = fast_exp2(m[0] - mn0), a1 = fast_exp2(m[1] - mn1);
         m[0] = mn0;
         m[1] = mn1;
         l[0] *= a0;
@@ -1106,6 +1137,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         if constexpr (k4bit) {
           z_sum[0] *= a0;
           z_sum[1] *= a1;
+          const float f = larger_scale(vbits);
+          a0 *= f;
+          a1 *= f;
         }
 #pragma unroll
         for (int i = 0; i < Tr::KS; ++i) {
@@ -1115,6 +1149,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           acc[i][0][3] *= a1;
         }
       }
+      [[maybe_unused]] float wunit = 0.f;
+      if constexpr (k4bit) wunit = weight_unit();
       // P, then its transposes: m-rows g (g + 8) of S become k-rows 2t, 2t + 1
       // (2t + 8, 2t + 9) of P^T, the token order the V loads use
 #pragma unroll
@@ -1126,27 +1162,21 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         l[0] += p0 + p2;
         l[1] += p1 + p3;
         if constexpr (k4bit) {
-          float2 v0 = widen2<f16_t>(lds32(vt + pairs_of(2 * mt) + tau(gid) * 4));
-          float2 v1 = widen2<f16_t>(lds32(vt + pairs_of(2 * mt + 1) + tau(gid) * 4));
-          if constexpr (!FULL) {  // (a row that is not attended may hold anything)
-            auto in = [&](int tok) { return tok < n_valid && (tok >= lo_rel || tok < sink_rel); };
-            if (!in(16 * mt + tau(gid))) v0 = make_float2(0.f, 0.f);
-            if (!in(16 * mt + 8 + tau(gid))) v1 = make_float2(0.f, 0.f);
-          }
-          const float z0 = fmaf(-16.f, v0.x, v0.y), z1 = fmaf(-16.f, v1.x, v1.y);
-          z_sum[0] = fmaf(p0, z0, fmaf(p2, z1, z_sum[0]));
-          z_sum[1] = fmaf(p1, z0, fmaf(p3, z1, z_sum[1]));
-          p0 *= v0.x;
-          p1 *= v0.x;
-          p2 *= v1.x;
-          p3 *= v1.x;
+          const float2 v0 = widen2<f16_t>(vpair[mt][0]), v1 = widen2<f16_t>(vpair[mt][1]);
+          z_sum[0] = fmaf(p0, v0.y, fmaf(p2, v1.y, z_sum[0]));
+          z_sum[1] = fmaf(p1, v0.y, fmaf(p3, v1.y, z_sum[1]));
+          const float s0 = v0.x * wunit, s1 = v1.x * wunit;
+          p0 *= s0;
+          p1 *= s0;
+          p2 *= s1;
+          p3 *= s1;
         }
-        const uint32_t h01 = pack2<PB>(p0, p1), h23 = pack2<PB>(p2, p3);
-        const float2 f01 = unpack2<PB>(h01), f23 = unpack2<PB>(h23);
+        const uint32_t h01 = pack2<MB>(p0, p1), h23 = pack2<MB>(p2, p3);
+        const float2 f01 = unpack2<MB>(h01), f23 = unpack2<MB>(h23);
         ph[mt][0][0] = movmatrix_trans(h01);
         ph[mt][0][1] = movmatrix_trans(h23);
-        pl[mt][0][0] = movmatrix_trans(pack2<PB>(p0 - f01.x, p1 - f01.y));
-        pl[mt][0][1] = movmatrix_trans(pack2<PB>(p2 - f23.x, p3 - f23.y));
+        pl[mt][0][0] = movmatrix_trans(pack2<MB>(p0 - f01.x, p1 - f01.y));
+        pl[mt][0][1] = movmatrix_trans(pack2<MB>(p2 - f23.x, p3 - f23.y));
       }
     } else {
       float sc[Tr::NT][4];
@@ -1160,17 +1190,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            mma16816<false>(sc[nt], qa0[2 * r], NH == 2 ? qb0[2 * r] : 0u, qa1[2 * r], NH == 2 ? qb1[2 * r] : 0u,
-                            nibbles_f16_64<0>(ws[r]), nibbles_f16_64<1>(ws[r]));
-            mma16816<false>(sc[nt], qa0[2 * r + 1], NH == 2 ? qb0[2 * r + 1] : 0u, qa1[2 * r + 1],
-                            NH == 2 ? qb1[2 * r + 1] : 0u, nibbles_f16_64<2>(ws[r]), nibbles_f16_64<3>(ws[r]));
+            uint32_t n[4];
+            nibbles4(ws[r], n);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              mma16816<false>(sc[nt], qa0[2 * r + x], NH == 2 ? qb0[2 * r + x] : 0u, qa1[2 * r + x],
+                              NH == 2 ? qb1[2 * r + x] : 0u, n[2 * x], n[2 * x + 1]);
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float2 kp = widen2<f16_t>(lds32(kt + pairs_of(nt) + tau(2 * tig + e) * 4));
-            const float z = fmaf(-64.f, kp.x, kp.y);
+            const float ks = kp.x * kCodeUnit;
 #pragma unroll
-            for (int h = 0; h < NH; ++h) sc[nt][2 * h + e] = fmaf(sc[nt][2 * h + e], kp.x, z * q_sum[h]);
+            for (int h = 0; h < NH; ++h) sc[nt][2 * h + e] = fmaf(sc[nt][2 * h + e], ks, kp.y * q_sum[h]);
           }
         }
       } else if constexpr (!k8bit) {
@@ -1243,7 +1275,25 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       }
       bool up = mx[0] > m[0];
       if constexpr (NH == 2) up |= mx[1] > m[1];
+      // 4-bit: the V rows' pairs (of one that is not attended, which may hold anything: zero), their largest scale
+      [[maybe_unused]] uint32_t vpair[Tr::NT][2];
+      [[maybe_unused]] int vbits = 0;
+      if constexpr (k4bit) {
+#pragma unroll
+        for (int nt = 0; nt < Tr::NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int tok = nt * 8 + tau(2 * tig + e);
+            vpair[nt][e] = lds32(vt + pairs_of(nt) + tau(2 * tig + e) * 4);
+            if (tok >= n_valid || (tok < lo_rel && tok >= sink_rel)) vpair[nt][e] = 0u;
+            vbits = scale_bits(vbits, vpair[nt][e]);
+          }
+        }
+        up |= (vbits >> 10) > vexp;
+      }
       if (__any_sync(0xffffffffu, up)) {
+        [[maybe_unused]] float down = 1.f;
+        if constexpr (k4bit) down = larger_scale(vbits);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           const float mn = fmaxf(m[h], mx[h]);
@@ -1253,8 +1303,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           m[h] = mn;
           l[h] *= alpha;
           if constexpr (k4bit) z_sum[h] *= alpha;
-          const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * tig);      // row 8h + 2t
-          const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * tig + 4);  // row 8h + 2t + 1
+          float a0 = __shfl_sync(0xffffffffu, alpha, 8 * tig);      // row 8h + 2t
+          float a1 = __shfl_sync(0xffffffffu, alpha, 8 * tig + 4);  // row 8h + 2t + 1
+          if constexpr (k4bit) {
+            a0 *= down;
+            a1 *= down;
+          }
 #pragma unroll
           for (int i = 0; i < Tr::KS; ++i) {
             acc[i][h][0] *= a0;
@@ -1264,6 +1318,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           }
         }
       }
+      [[maybe_unused]] float wunit = 0.f;
+      if constexpr (k4bit) wunit = weight_unit();
       // P^T as the B operand of each 16-token k-step, per row half, split hi + lo
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
@@ -1274,21 +1330,15 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           float p1 = fast_exp2(sc[nt][2 * h + 1] - ms);
           l[h] += p0 + p1;
           if constexpr (k4bit) {
-            float2 v[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int tok = nt * 8 + tau(2 * tig + e);
-              v[e] = widen2<f16_t>(lds32(vt + pairs_of(nt) + tau(2 * tig + e) * 4));
-              if (tok >= n_valid || (tok < lo_rel && tok >= sink_rel)) v[e] = make_float2(0.f, 0.f);  // not attended
-            }
-            z_sum[h] = fmaf(p0, fmaf(-16.f, v[0].x, v[0].y), fmaf(p1, fmaf(-16.f, v[1].x, v[1].y), z_sum[h]));
-            p0 *= v[0].x;
-            p1 *= v[1].x;
+            const float2 v0 = widen2<f16_t>(vpair[nt][0]), v1 = widen2<f16_t>(vpair[nt][1]);
+            z_sum[h] = fmaf(p0, v0.y, fmaf(p1, v1.y, z_sum[h]));
+            p0 *= v0.x * wunit;
+            p1 *= v1.x * wunit;
           }
-          const uint32_t hp = pack2<PB>(p0, p1);
-          const float2 hf = unpack2<PB>(hp);
+          const uint32_t hp = pack2<MB>(p0, p1);
+          const float2 hf = unpack2<MB>(hp);
           ph[nt >> 1][h][nt & 1] = hp;
-          pl[nt >> 1][h][nt & 1] = pack2<PB>(p0 - hf.x, p1 - hf.y);
+          pl[nt >> 1][h][nt & 1] = pack2<MB>(p0 - hf.x, p1 - hf.y);
         }
       }
     }
@@ -1328,20 +1378,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
             even[x] = prmt(a, b, 0x5410u);
             odd[x] = prmt(a, b, 0x7632u);
           }
-          auto product = [&](auto nibble) {
-            constexpr int J = decltype(nibble)::value;
-            const uint32_t a0 = nibbles_bf16_16<J>(even[0]), a1 = nibbles_bf16_16<J>(odd[0]);
-            const uint32_t a2 = nibbles_bf16_16<J>(even[1]), a3 = nibbles_bf16_16<J>(odd[1]);
+          uint32_t n0[4], n1[4], n2[4], n3[4];
+          nibbles4(even[0], n0);
+          nibbles4(odd[0], n1);
+          nibbles4(even[1], n2);
+          nibbles4(odd[1], n3);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-              mma16816<true>(acc[4 * w + J][h], a0, a1, a2, a3, ph[sb][h][0], ph[sb][h][1]);
-              mma16816<true>(acc[4 * w + J][h], a0, a1, a2, a3, pl[sb][h][0], pl[sb][h][1]);
+              mma16816<false>(acc[4 * w + j][h], n0[j], n1[j], n2[j], n3[j], ph[sb][h][0], ph[sb][h][1]);
+              mma16816<false>(acc[4 * w + j][h], n0[j], n1[j], n2[j], n3[j], pl[sb][h][0], pl[sb][h][1]);
             }
-          };
-          product(std::integral_constant<int, 0>());
-          product(std::integral_constant<int, 1>());
-          product(std::integral_constant<int, 2>());
-          product(std::integral_constant<int, 3>());
+          }
         }
       }
     } else if constexpr (!k8bit) {
@@ -1555,7 +1604,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     // rounding of every element within 2^28 of the group's largest (bf16 has 8
     // significant bits, f16 11); smaller elements can lose bits as f16
     // subnormals, an absolute error below 2^-38 of the largest element.
-    constexpr bool q_rescale = (k8bit || k4bit) && std::is_same<QT, bf16_t>::value;
+    // 4-bit caches: f16 queries too, since the codes' units (nibbles4) put half of each row's elements 2^4 below the others: exact
+    // within 2^24 of the largest.
+    constexpr bool q_rescale = (k8bit && std::is_same<QT, bf16_t>::value) || k4bit;
     int qexp = 0;
     [[maybe_unused]] int64_t row_base = 0;  // pa_attend: the sequence's first row of q and out
     if constexpr (ATT) {
@@ -1635,6 +1686,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     if constexpr (q_rescale) {
       // largest |q| of the group (bf16 halves read as floats), over the warp
       auto amax2 = [](float a, uint32_t w) {
+        if constexpr (std::is_same<QT, f16_t>::value) {
+          const float2 f = widen2<f16_t>(w);
+          return fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
         return fmaxf(a, fmaxf(__uint_as_float((w << 16) & 0x7fffffffu), __uint_as_float(w & 0x7fff0000u)));
       };
       float qmax = 0.f;
@@ -1650,28 +1705,30 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       const int ebits = (__float_as_int(qmax) >> 23) & 0xff;
       qexp = qmax > 0.f ? min(100, max(-100, 141 - ebits)) : 0;
       const float mul = __int_as_float((127 + qexp) << 23);
-      auto narrow = [&](uint32_t w) {
-        const float2 f = widen2<bf16_t>(w);
-        return pack2<false>(f.x * mul, f.y * mul);
+      const float mul1 = k4bit ? mul * 0.0625f : mul;  // (4-bit: the codes of these columns are in units of 2^-20, not 2^-24)
+      auto narrow = [](uint32_t w, float by) {
+        const float2 f = widen2<QT>(w);
+        return pack2<false>(f.x * by, f.y * by);
       };
 #pragma unroll
       for (int s = 0; s < Tr::KS; ++s) {
-        qa0[s] = narrow(qa0[s]);
-        qa1[s] = narrow(qa1[s]);
+        qa0[s] = narrow(qa0[s], mul);
+        qa1[s] = narrow(qa1[s], mul1);
         if constexpr (NH == 2) {
-          qb0[s] = narrow(qb0[s]);
-          qb1[s] = narrow(qb1[s]);
+          qb0[s] = narrow(qb0[s], mul);
+          qb1[s] = narrow(qb1[s], mul1);
         }
       }
     }
     if constexpr (k4bit) {
+      vexp = -1;
       // the sums of query rows g (and g + 8), as they enter the products; one query: then of this lane's rows 2t, 2t + 1
       auto sum_row = [&](const uint32_t(&a)[Tr::KS], const uint32_t(&b)[Tr::KS]) {
         float x = 0.f;
 #pragma unroll
         for (int s = 0; s < Tr::KS; ++s) {
           const float2 f = widen2<f16_t>(a[s]), g = widen2<f16_t>(b[s]);
-          x += (f.x + f.y) + (g.x + g.y);
+          x += fmaf(16.f, g.x + g.y, f.x + f.y);
         }
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         return x + __shfl_xor_sync(0xffffffffu, x, 2);
@@ -1781,10 +1838,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           }
 #pragma unroll
           for (int i = 0; i < Tr::KS; ++i) {
-            acc[i][h][0] += z0;
-            acc[i][h][1] += z1;
-            acc[i][h][2] += z0;
-            acc[i][h][3] += z1;
+            // O in units of the codes (2^-24, odd nibbles 2^-20) and of the weights
+            const float f = __int_as_float((127 + ((i & 1) ? 20 : 24) - 29 + vexp) << 23);
+            acc[i][h][0] = fmaf(acc[i][h][0], f, z0);
+            acc[i][h][1] = fmaf(acc[i][h][1], f, z1);
+            acc[i][h][2] = fmaf(acc[i][h][2], f, z0);
+            acc[i][h][3] = fmaf(acc[i][h][3], f, z1);
           }
         }
       }

@@ -1,12 +1,16 @@
 """Attend cases with sinks and with 4-bit caches: AttendCase (operator_cases) with both, and the call that runs them.
 
 A 4-bit value is code * scale + zero.  In calls of few rows (at most 64 rows of queries x query heads per KV head, on the
-decode kernel) the codes enter the products exactly, and the weights, times the row's scale, as two bfloat16 values: off by
-at most 2^-17 of them; a value enters as 16 + code, so its error is at most (16 + 15) scale 2^-17, below 2^-12 of the largest
-value of its row.  In calls of many rows K and V are rounded to float16 once: half a step, 2^-11 of a value, at most.  A
-score then is off by the sum of 128 independent errors q_i k_i 2^-11, uniform: a standard deviation of 2^-11 / sqrt(3) *
-sqrt(sum q_i^2 k_i^2) / sqrt(128), about 2.9e-4 for standard normal q and k; six of these in the score, and twice that in a
-weight, relative to it.
+decode kernel) the codes enter the products exactly, and the weights, times the row's scale, as two float16 values: 22 bits,
+as AttendCase.tolerance has it.  But the codes' part and the zeros' part of an output are summed apart and may cancel: each
+is at most R = 3 times the largest value (zero is the row's smallest value, code * scale at most the difference to the
+largest).  The first is off by 2^-22 R for its weights; either by 2^-23 R for each addition to its accumulator (the tensor
+cores cut off, two products per 16 positions; a float32 addition per 8), of which there are at most min(T, 2048) / 8 in a
+warp: longer sequences are split over the device, here to shares far below that.
+
+In calls of many rows K and V are rounded to float16 once: half a step, 2^-11 of a value, at most.  A score then is off by
+the sum of 128 independent errors q_i k_i 2^-11, uniform: a standard deviation of 2^-11 / sqrt(3) * sqrt(sum q_i^2 k_i^2) /
+sqrt(128), about 2.9e-4 for standard normal q and k; six of these in the score, and twice that in a weight, relative to it.
 """
 
 from __future__ import annotations
@@ -74,7 +78,8 @@ class Case(AttendCase):
         group = self.heads // self.kv_heads
         mult = max(1.0, float(self.q.float().abs().max()) / 4.5)
         if max(self.qlens) * group <= 16:                  # always on the decode kernel
-            return tol + 2.0 ** -12 * wabs.amax(-1, keepdim=True) * 2
+            steps = 1 + 2 * min(max(self.lens), 2048) // 8
+            return tol + (2.0 ** -22 + steps * 2.0 ** -23) * 3 * float(self.v64.abs().max())
         return tol + (2 * 6 * 2.9e-4 * mult + 2.0 ** -11) * wabs
 
 
