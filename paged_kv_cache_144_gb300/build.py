@@ -31,6 +31,7 @@ SOURCES = [
     "pa_norm.cu",
     "pa_read.cu",
     "pa_attend.cu",
+    "pa_attend_int4.cu",
     "pa_attend_tc_f16.cu",
     "pa_attend_tc_bf16.cu",
     "pa_attend_tc_fp8.cu",

@@ -82,7 +82,8 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
     pl->key.unit_rows = q8 && block_size >= 16 && gm == 8 ? 64 : 32;
     pl->key.append = sinks || q4 ? 3 : 2;
     pl->key.row_groups = gm == 16 ? static_cast<int>((rows + 15) / 16) : 1;
-    if (!decode_geometry(pl->key, shape_seqs(num_seqs), &pl->geo)) return false;
+    const bool direct = q4 && gm == 8;  // attend_int4_kernel
+    if (!(direct ? int4_geometry(num_seqs, &pl->geo) : decode_geometry(pl->key, shape_seqs(num_seqs), &pl->geo))) return false;
     const size_t warps = static_cast<size_t>(pl->geo.ctas) * pl->geo.warps_per_cta;
     pl->num_counters = static_cast<size_t>(num_seqs) * num_kv_heads * pl->geo.row_groups;
     records = 2 * warps * pl->geo.record_floats * sizeof(float);
@@ -149,7 +150,8 @@ cudaError_t launch_few(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaS
   const int eb = a.kv_dtype == PA_FP8_E4M3 || a.kv_dtype == PA_INT8 ? 1 : 2;
   const int box = a.block_size < pl.geo.unit_rows ? a.block_size : pl.geo.unit_rows;
   CUtensorMap tk = {}, tv = {};  // (4-bit caches: bulk copies, no maps)
-  if (a.kv_dtype == PA_INT4) return launch_decode(pl.key, pl.geo, p, tk, tv, stream, a.pdl);
+  if (a.kv_dtype == PA_INT4)
+    return pl.key.gmax == 8 ? launch_int4(pl.geo, p, a.q_dtype, stream, a.pdl) : launch_decode(pl.key, pl.geo, p, tk, tv, stream, a.pdl);
   if (!encode_cache_map(&tk, a.k_cache, a.num_blocks, a.num_kv_heads, a.block_size, a.head_dim, eb, box) ||
       !encode_cache_map(&tv, a.v_cache, a.num_blocks, a.num_kv_heads, a.block_size, a.head_dim, eb, box))
     return cudaErrorInvalidValue;

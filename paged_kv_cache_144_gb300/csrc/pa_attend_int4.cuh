@@ -1,0 +1,686 @@
+// pa_attend_int4.cuh - one query per sequence over a 4-bit cache, up to 8 query
+// heads per KV head.
+//
+// Mathematics: that of paged_decode_kernel (pa_decode.cuh), whose split of the
+// batch, recurrence, records and merge this kernel shares: scores and weights in
+// the fragments of mma.sync m16n8k16, S = K Q^T with 16 positions per m-tile, O^T
+// += V^T P^T with the weights transposed in registers.  A value is code * scale +
+// zero with a pair of the row's own, so a score is scale (q . codes) + zero
+// sum(q), and an output the product of the codes with the weights times the
+// rows' scales, plus sum(weight zero); the zeros' parts are float32 sums.
+//
+// Codes enter both products as f16 subnormals (nibbles4): five instructions for
+// eight codes, no constant to be taken off the sums again.  The order of a word's
+// nibbles and of a lane's words is that of the operands: a lane takes 32
+// consecutive columns of a K row, 16 of a V row.  The weights times the scales go
+// to f16 in units that follow the largest scale seen (weight_unit).
+//
+// How it is laid out.  Every warp brings its own units of 64 positions into its
+// own ring of stages by asynchronous copies, 16 bytes per lane, one unit ahead,
+// and waits for nobody else: no producer, no barrier until the end.  (With a
+// producer warp and one bulk copy per block, as the other caches have it, the
+// producer was what everybody waited for: 8 x 32768 positions of 8 KV heads took
+// 106 us with seven consumer warps and with ten.)  What a warp needs of its
+// fragment stands in shared memory, so that a unit's operands keep their
+// registers.  The records of a split segment are joined by the whole CTA whose
+// arrival was the last, after its units: their loads are what counts, and one
+// warp per segment had too few under way (28 -> 34 us for 32 x up to 4096).
+//
+// What bounds it.  8 x 32768 positions, 8 KV heads of 8 query heads, blocks of 16
+// (device time, caches cold): 72 us; 5.4 TB/s (79 % of a plain copy) while it
+// streams, 6 us before the first unit has arrived, 6 us from the first warp's end
+// to the last record joined.  G = 1 and 4 take the same.  32 x up to 4096: 28 us.
+// Instructions bound the streaming: about 1000 per unit, half of them on the
+// integer pipe, which takes two cycles for each (41 % of all issue slots, 40 % of
+// that pipe, tensor pipe 22 %).  Tried, same case: units of 32 with 16 or 12 warps
+// 77 and 78 us, units of 64 with 10 warps (a few spills) 80, three stages (six
+// warps of 64, eleven of 32) 90 and 82, operands loaded straight to registers 80;
+// weights as two f16 values (float32 and float16 outputs) 74.
+#pragma once
+
+#include "pa_decode.cuh"
+
+namespace pa {
+
+struct Int4Traits {
+  static constexpr int D = 128, GM = 8;
+  static constexpr int UR = 64, UR_SHIFT = 6;     // positions of a unit
+  static constexpr int MT = UR / 16;              // 16-position m-tiles of S, k-steps of O
+  static constexpr int WARPS = 8;
+  static constexpr int REC = align_up_c(GM * (D + 2), 4);  // floats of a record, as in DecodeTraits
+  static constexpr int NS = 2;                    // stages: the current unit and those under way
+  // a stage: codes of K, of V, pairs of K, of V
+  static constexpr int OFF_V = UR * 64, OFF_KP = 2 * UR * 64, OFF_VP = OFF_KP + UR * 4;
+  static constexpr int STAGE = OFF_VP + UR * 4;
+  // shared memory of a warp: its stages, query rows, its place in the work
+  static constexpr int OFF_Q = NS * STAGE;
+  static constexpr int Q_BYTES = GM * D * 2;      // of a fragment's query rows: NS of them, by turns
+  static constexpr int NFRAG = NS + 1;            // fragments that a warp is in or has units of under way
+  static constexpr int OFF_FRAG = OFF_Q + NS * Q_BYTES;  // Int4Frag [NFRAG], then the WorkIter
+  static constexpr int WARP_SMEM = align_up_c(OFF_FRAG + NFRAG * 64 + static_cast<int>(sizeof(WorkIter)), 128);
+  static size_t smem_bytes(int num_seqs) {
+    return static_cast<size_t>(WARPS) * WARP_SMEM + (static_cast<size_t>(3) * num_seqs + 1 + WARPS + 1 + 3 * 2 * WARPS) * 4;
+  }
+};
+
+// What a warp needs of a fragment while it runs through its units: in shared memory, not in its registers.
+struct Int4Frag {
+  int T, lo, sinks, jend;      // attended: t < T, and t >= lo or t < sinks; end of the units
+  int su, skip, s, kvh;        // unit number su is followed by skip units that are not attended; segment
+  int nblk, slot, nu, rows0;   // blocks of the sequence; record (-1: the whole segment); units of the segment; query row
+  int j0, pad[3];              // first unit
+};
+static_assert(sizeof(Int4Frag) == 64, "Int4Traits::WARP_SMEM");
+
+// BX: blocks of a unit (its positions over the block size, or 1: a unit is part of one block).  SPLIT: weights enter P V as
+// two f16 values, hi + lo, else as one.
+template <typename QT, int BX, bool SPLIT>
+__global__ void __launch_bounds__(Int4Traits::WARPS * 32, 1) attend_int4_kernel(const DecodeParams p) {
+  using Tr = Int4Traits;
+  constexpr int D = Tr::D, GM = Tr::GM, UR = Tr::UR, MT = Tr::MT, W = Tr::WARPS, KS = D / 16;
+  constexpr bool ATT = true, SINKS = true;
+  constexpr float kLog2e = 1.4426950408889634f;
+  extern __shared__ __align__(128) uint8_t sm[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int S = p.num_seqs, Hkv = p.num_kv_heads, G = p.group, B = p.block_size;
+  int* const prefix = reinterpret_cast<int*>(sm + W * Tr::WARP_SMEM);
+  int* const lens = prefix + (S + 1);
+  int* const scan = lens + 2 * S;
+  int* const won = scan + W;  // what this CTA merges: the number of segments, then (segment, first share, records) of each
+  griddep_launch_dependents();
+  griddep_wait();
+  // the block tables on their way to L2 while the lengths are read
+  if (const int64_t bytes = static_cast<int64_t>(S) * p.max_blocks_per_seq * 4; bytes <= kTableL2Bytes) {
+    const char* const tables = reinterpret_cast<const char*>(p.block_tables);
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i * 128 < bytes;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+      prefetch_l2(tables + i * 128);
+  }
+  if (threadIdx.x == 0) won[0] = 0;
+
+  // ---- cost positions before each sequence (every CTA computes the same), lengths and query counts
+  int carry = 0;
+  for (int b0 = 0; b0 < S; b0 += blockDim.x) {
+    const int s = b0 + threadIdx.x;
+    int units = 0;
+    if (s < S) {
+      const SeqView v = seq_view(p.att, s, blockIdx.x == 0);
+      lens[s] = v.T;
+      lens[S + s] = v.L;
+      const int nu = v.L > 0 ? ((v.T + UR - 1) >> Tr::UR_SHIFT) - unit_gap(p.att.sinks, window_lo(p, v.T, v.L), Tr::UR_SHIFT).skip : 0;
+      units = (nu > 0 ? nu + p.frag_cost : 0) * Hkv;
+    }
+    int x = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < W; ++w) {
+      before += w < warp ? scan[w] : 0;
+      all += scan[w];
+    }
+    if (s < S) prefix[s] = carry + before + x - units;
+    carry += all;
+    __syncthreads();
+  }
+  uint8_t* const mine = sm + warp * Tr::WARP_SMEM;
+  const uint32_t mine_u32 = smem_u32(mine);
+  if (threadIdx.x == 0) prefix[S] = carry;
+  __syncthreads();
+  auto first_row = [&](int s) -> int64_t { return p.att.q_starts ? __ldg(p.att.q_starts + s) : s; };
+  // empty sequences attend to nothing: their outputs are zero
+  for (int s = blockIdx.x * W + warp; s < S; s += gridDim.x * W) {
+    if (lens[s] != 0 || lens[S + s] == 0) continue;
+    const int64_t n = static_cast<int64_t>(p.num_heads) * D, o0 = first_row(s) * n;
+    for (int64_t i = lane; i < n; i += 32) store_out(p.out, p.out_dtype, o0 + i, 0.f);
+  }
+
+  // ---- this warp's share
+  const long long U = prefix[S];
+  const int nw_total = gridDim.x * W, min_share = kMinUnitsPerWarp + p.frag_cost;
+  const long long want = (U + min_share - 1) / min_share;
+  const int nw_eff = static_cast<int>(want < 1 ? 1 : (want < nw_total ? want : nw_total));
+  // A CTA's warps take neighbouring shares, so that a segment's records come from few CTAs and its merge falls to another CTA
+  // than the next one's (else a slow SM is the last at every segment); few shares go to as many SMs.
+  const int w_eff = (nw_eff + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  const int gc = warp < w_eff ? static_cast<int>(blockIdx.x) * w_eff + warp : nw_total;
+  Int4Frag* const frags = reinterpret_cast<Int4Frag*>(mine + Tr::OFF_FRAG);  // by turns
+  WorkIter* const walk = reinterpret_cast<WorkIter*>(frags + Tr::NFRAG);
+  // notes fragment w as frags[i]
+  auto note = [&](const WorkIter& w, int i) {
+    if (lane == 0) {
+      *walk = w;
+      if (w.valid) frags[i] = Int4Frag{w.T, w.lo, w.sinks, w.jend, w.su, w.skip, w.s, w.kvh, w.nblk, w.slot, w.nu,
+                                       static_cast<int>(first_row(w.s)), w.j0, {0, 0, 0}};
+    }
+    __syncwarp();
+  };
+  int j = 0;  // the current unit
+  bool any;   // there is one
+  {
+    WorkIter w;
+    w.frag_idx = 0;
+    w.gw = gc;
+    w.valid = false;
+    if (U > 0 && gc < nw_eff) {
+      w.u = gc * U / nw_eff;
+      w.u1 = (gc + 1) * U / nw_eff;
+      w.s = find_seq(prefix, S, w.u);
+      w.valid = frag_balanced<ATT, SINKS>(w, prefix, p, Tr::UR_SHIFT);
+    }
+    any = w.valid;
+    if (any) {
+      note(w, 0);
+      j = w.j;
+    }
+  }
+  int cur = 0;  // its fragment, of frags
+
+  // ---- loads.  Box b of a unit: block (unit's first block + b); lane b looks its table entry up.
+  constexpr int BR = UR / BX;  // rows of a box
+  const uint32_t tile_bytes = static_cast<uint32_t>(B) * int4_row_bytes(D);
+  const uint8_t* const k_cache = static_cast<const uint8_t*>(p.k_cache);
+  const uint8_t* const v_cache = static_cast<const uint8_t*>(p.v_cache);
+  // table entry of this lane's box (or block 0: what is not attended counts for nothing)
+  auto entry_of = [&](const Int4Frag& f, int u) -> int {
+    const int blk = BX == 1 ? (u << Tr::UR_SHIFT) >> p.block_shift : u * BX + lane;
+    const bool in = (BX == 1 || lane < BX) && blk < f.nblk &&
+                    (blk >= (f.lo >> p.block_shift) || blk < ((f.sinks + B - 1) >> p.block_shift));
+    return in ? __ldg(p.block_tables + static_cast<int64_t>(f.s) * p.max_blocks_per_seq + blk) : 0;
+  };
+  // the tile of this lane's box
+  auto tile_of = [&](const Int4Frag& f, int entry) -> int {
+    if (entry < 0 || entry >= p.num_blocks) {
+      raise_error(p.err, PA_DEVERR_BLOCK_ID);
+      entry = 0;
+    }
+    return entry * Hkv + f.kvh;
+  };
+  // A stage holds the codes of two rows per 128 bytes, in 16-byte chunks: chunk c of row r is chunk (4 (r & 1) + c) ^ 2 ((r / 2)
+  // & 3), so that the reads below spread over the banks: of K 16 bytes of row g, of V 8 bytes of row 2t or 2t + 1.
+  const uint32_t k_at = static_cast<uint32_t>((gid >> 1) * 128 + ((((gid & 1) << 2) | tig) ^ ((gid >> 1) << 1)) * 16);
+  const uint32_t v_at = static_cast<uint32_t>(Tr::OFF_V + tig * 128 + ((gid >> 1) ^ (tig << 1)) * 16 + (gid & 1) * 8);  // row 2t + 1: ^ 64
+  // copies unit u of fragment f (this lane's box: `tile`) into a stage: each lane 16 bytes of row g of every 8, and a row's pair
+  auto fetch_unit = [&](uint32_t stage, int tile, int u) {
+    const uint32_t r0 = BX == 1 ? (u << Tr::UR_SHIFT) & (B - 1) : 0;  // first row of the unit in its block
+#pragma unroll
+    for (int b = 0; b < BX; ++b) {
+      // (a shuffle from one lane: the address but for the lane's part is the warp's)
+      const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, tile, b))) * tile_bytes;
+      const uint32_t off = lane * 16 + r0 * 64;
+#pragma unroll
+      for (int y = 0; y < BR / 8; ++y) {
+        cp_async16(stage + k_at + (b * BR + 8 * y) * 64, k_cache + at + off + y * 512);
+        cp_async16(stage + Tr::OFF_V + k_at + (b * BR + 8 * y) * 64, v_cache + at + off + y * 512);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < UR / 32; ++x) {
+      const int row = 32 * x + lane;
+      const uint64_t at =
+          static_cast<uint64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, tile, row / BR))) * tile_bytes + B * 64;
+      const uint32_t off = (r0 + (row & (BR - 1))) * 4;
+      cp_async4(stage + Tr::OFF_KP + row * 4, k_cache + at + off);
+      cp_async4(stage + Tr::OFF_VP + row * 4, v_cache + at + off);
+    }
+  };
+  // the query rows of a fragment, into query buffer i
+  auto fetch_q = [&](const Int4Frag& f, int i) {
+    const uint8_t* const q = static_cast<const uint8_t*>(p.q) + (f.rows0 * p.q_stride + static_cast<int64_t>(f.kvh) * G * D) * 2;
+    const uint32_t to = mine_u32 + Tr::OFF_Q + i * Tr::Q_BYTES;
+    for (int x = lane; x < G * (D * 2 / 16); x += 32) cp_async16(to + x * 16, q + x * 16);
+  };
+
+  // ---- state of a fragment
+  uint32_t qa0[KS], qa1[KS];   // B operand of S: row g, columns 32 t + 4 s (+ 1), and + 2 (+ 3)
+  float q_sum[2], z_sum[2];    // of rows 2t, 2t + 1
+  float m[2], l[2];
+  float acc[KS][4];            // O^T: columns 16 g + 2 i (+ 1: elements 2, 3) of rows 2t, 2t + 1
+  float score_unit = 0.f;      // what a K scale is multiplied by: units of the codes and the queries, the softmax's scale
+  const float cap2 = p.att.softcap * kLog2e, capk = p.att.softcap > 0.f ? 2.f / p.att.softcap : 0.f;
+  // Scaled weights go to f16 times 2^(29 - vexp): 2^15 over a power of two above the scales seen so far, so that none
+  // exceeds f16 and those down to 2^-39 of the largest count; O follows when a larger scale comes, as it follows the maximum.
+  // vexp: the f16 exponent field of that scale (-1: none yet)
+  int vexp = -1;
+
+  auto start_fragment = [&](int q_buf) {
+    const bool mine_row = gid < G;
+    float top = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint2 w = mine_row ? *reinterpret_cast<const uint2*>(mine + Tr::OFF_Q + q_buf * Tr::Q_BYTES + (gid * D + 32 * tig + 4 * s) * 2) : make_uint2(0u, 0u);
+      qa0[s] = w.x;
+      qa1[s] = w.y;
+      const float2 a = widen2<QT>(w.x), b = widen2<QT>(w.y);
+      top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // The products run in f16: the group's rows are multiplied by the power of two that puts their largest element at 2^14 ..
+    // 2^15, and the columns whose codes are in units of 2^-20, not 2^-24, by 2^-4 of it.  Exact for elements within 2^24 of
+    // the largest; smaller ones may round as subnormals.
+    const int ebits = (__float_as_int(top) >> 23) & 0xff;
+    const int qexp = top > 0.f ? min(100, max(-100, 141 - ebits)) : 0;
+    const float by = __int_as_float((127 + qexp) << 23);
+    float sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const float2 a = widen2<QT>(qa0[s]), b = widen2<QT>(qa1[s]);
+      qa0[s] = pack2<false>(a.x * by, a.y * by);
+      qa1[s] = pack2<false>(b.x * by * 0.0625f, b.y * by * 0.0625f);
+      const float2 x = widen2<f16_t>(qa0[s]), y = widen2<f16_t>(qa1[s]);  // as they enter the products
+      sum += fmaf(16.f, y.x + y.y, x.x + x.y);
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    const float scale = p.qk_scale_log2 * __int_as_float((127 - qexp) << 23);
+    sum *= scale;
+    q_sum[0] = __shfl_sync(0xffffffffu, sum, 8 * tig);
+    q_sum[1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4);
+    score_unit = scale * kCodeUnit;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[e] = -INFINITY;
+      l[e] = z_sum[e] = 0.f;
+    }
+    vexp = -1;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  };
+
+  // One unit.  FULL: every position is attended.
+  auto unit_step = [&](auto full_tag, uint32_t stage) {
+    constexpr bool FULL = decltype(full_tag)::value;
+    const Int4Frag& f = frags[cur];
+    const int t0 = j << Tr::UR_SHIFT;
+    auto attended = [&](int t) { return FULL || (t < f.T && (t >= f.lo || t < f.sinks)); };
+    float sc[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      sc[mt][0] = sc[mt][1] = sc[mt][2] = sc[mt][3] = 0.f;
+      const uint4 w0 = lds128(stage + k_at + mt * 1024), w1 = lds128(stage + k_at + mt * 1024 + 512);
+      const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {  // word r: k-steps 2 r and 2 r + 1
+        uint32_t n0[4], n1[4];
+        nibbles4(x0[r], n0);
+        nibbles4(x1[r], n1);
+        mma16816<false>(sc[mt], n0[0], n1[0], n0[1], n1[1], qa0[2 * r], qa1[2 * r]);
+        mma16816<false>(sc[mt], n0[2], n1[2], n0[3], n1[3], qa0[2 * r + 1], qa1[2 * r + 1]);
+      }
+      const float2 p0 = widen2<f16_t>(lds32(stage + Tr::OFF_KP + mt * 64 + gid * 4));
+      const float2 p1 = widen2<f16_t>(lds32(stage + Tr::OFF_KP + mt * 64 + gid * 4 + 32));
+      const float s0 = p0.x * score_unit, s1 = p1.x * score_unit;
+      sc[mt][0] = fmaf(sc[mt][0], s0, p0.y * q_sum[0]);
+      sc[mt][1] = fmaf(sc[mt][1], s0, p0.y * q_sum[1]);
+      sc[mt][2] = fmaf(sc[mt][2], s1, p1.y * q_sum[0]);
+      sc[mt][3] = fmaf(sc[mt][3], s1, p1.y * q_sum[1]);
+    }
+    uint32_t v_pair[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) v_pair[mt][x] = lds32(stage + Tr::OFF_VP + mt * 64 + gid * 4 + x * 32);
+    }
+    // ---- online softmax of rows 2t (elements 0, 2) and 2t + 1 (1, 3), over the 8 lanes of equal t
+    // (scores in the log2 domain)
+    if (p.att.softcap > 0.f) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[mt][e] = cap2 - __fdividef(2.f * cap2, 1.f + fast_exp2(sc[mt][e] * capk));
+      }
+    }
+    if (p.att.slopes) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float slope2 = 2 * tig + e < G ? __ldg(p.att.slopes + f.kvh * G + 2 * tig + e) * kLog2e : 0.f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          sc[mt][e] -= slope2 * static_cast<float>(f.T - 1 - (t0 + 16 * mt + gid));
+          sc[mt][2 + e] -= slope2 * static_cast<float>(f.T - 1 - (t0 + 16 * mt + 8 + gid));
+        }
+      }
+    }
+    if constexpr (!FULL) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (attended(t0 + 16 * mt + 8 * x + gid)) continue;
+          sc[mt][2 * x] = sc[mt][2 * x + 1] = -INFINITY;
+          v_pair[mt][x] = 0u;  // (it may hold anything)
+        }
+      }
+    }
+    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      mx0 = fmaxf(mx0, fmaxf(sc[mt][0], sc[mt][2]));
+      mx1 = fmaxf(mx1, fmaxf(sc[mt][1], sc[mt][3]));
+    }
+    if (p.att.mass && 2 * tig < G) {  // both rows of a position stand side by side: [position][query head of the group]
+      float* const row = p.att.scores + (static_cast<int64_t>(f.s) * Hkv + f.kvh) * p.att.score_stride * G + 2 * tig;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const int t = t0 + 16 * mt + 4 * e + gid;
+          if (!attended(t)) continue;
+          float* const at = row + static_cast<int64_t>(t) * G;
+          if ((G & 1) == 0) {
+            *reinterpret_cast<float2*>(at) = make_float2(sc[mt][e], sc[mt][e + 1]);
+          } else {
+            at[0] = sc[mt][e];
+            if (2 * tig + 1 < G) at[1] = sc[mt][e + 1];
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+    }
+    // the V rows' scales in units of the weights: none above 2^15
+    float v_scale[MT][2], most = 0.f, unit = __int_as_float((127 + 29 - vexp) << 23);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        v_scale[mt][x] = widen2<f16_t>(v_pair[mt][x]).x * unit;
+        most = fmaxf(most, fabsf(v_scale[mt][x]));
+      }
+    }
+    // every row sees a position in every unit it processes: the new maxima are finite
+    if (__any_sync(0xffffffffu, mx0 > m[0] || mx1 > m[1] || most > 32768.f)) {
+      const float mn0 = fmaxf(m[0], mx0), mn1 = fmaxf(m[1], mx1);
+      float a0 = fast_exp2(m[0] - mn0), a1 = fast_exp2(m[1] - mn1);
+      m[0] = mn0;
+      m[1] = mn1;
+      l[0] *= a0;
+      l[1] *= a1;
+      z_sum[0] *= a0;
+      z_sum[1] *= a1;
+      int bits = 0;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        bits = max(bits, max(static_cast<int>(v_pair[mt][0] & 0x7fffu), static_cast<int>(v_pair[mt][1] & 0x7fffu)));
+      const int e = max(vexp, __reduce_max_sync(0xffffffffu, bits) >> 10);
+      const float down = __int_as_float((127 + vexp - e) << 23);
+      vexp = e;
+      unit *= down;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        v_scale[mt][0] *= down;
+        v_scale[mt][1] *= down;
+      }
+      a0 *= down;
+      a1 *= down;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        acc[i][0] *= a0;
+        acc[i][1] *= a1;
+        acc[i][2] *= a0;
+        acc[i][3] *= a1;
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float p0 = fast_exp2(sc[mt][0] - m[0]), p1 = fast_exp2(sc[mt][1] - m[1]);
+      float p2 = fast_exp2(sc[mt][2] - m[0]), p3 = fast_exp2(sc[mt][3] - m[1]);
+      l[0] += p0 + p2;
+      l[1] += p1 + p3;
+      const float z0 = widen2<f16_t>(v_pair[mt][0]).y, z1 = widen2<f16_t>(v_pair[mt][1]).y;
+      z_sum[0] = fmaf(p0, z0, fmaf(p2, z1, z_sum[0]));
+      z_sum[1] = fmaf(p1, z0, fmaf(p3, z1, z_sum[1]));
+      p0 *= v_scale[mt][0];
+      p1 *= v_scale[mt][0];
+      p2 *= v_scale[mt][1];
+      p3 *= v_scale[mt][1];
+      // P^T as the B operand of this k-step, hi + lo: positions g (8 + g) become k-rows 2t, 2t + 1 (+ 8)
+      const uint32_t h01 = pack2<false>(p0, p1), h23 = pack2<false>(p2, p3);
+      const uint32_t hi0 = movmatrix_trans(h01), hi1 = movmatrix_trans(h23);
+      uint32_t lo0 = 0u, lo1 = 0u;
+      if constexpr (SPLIT) {
+        const float2 f01 = unpack2<false>(h01), f23 = unpack2<false>(h23);
+        lo0 = movmatrix_trans(pack2<false>(p0 - f01.x, p1 - f01.y));
+        lo1 = movmatrix_trans(pack2<false>(p2 - f23.x, p3 - f23.y));
+      }
+      // a nibble of two positions' words side by side is an operand register: even columns from the words' lower halves, odd
+      // ones from the upper
+      const uint2 v00 = lds64(stage + v_at + mt * 1024), v01 = lds64(stage + (v_at ^ 64u) + mt * 1024);
+      const uint2 v10 = lds64(stage + v_at + mt * 1024 + 512), v11 = lds64(stage + (v_at ^ 64u) + mt * 1024 + 512);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t n0[4], n1[4], n2[4], n3[4];
+        const uint32_t a0 = w ? v00.y : v00.x, b0 = w ? v01.y : v01.x, a1 = w ? v10.y : v10.x, b1 = w ? v11.y : v11.x;
+        nibbles4(prmt(a0, b0, 0x5410u), n0);
+        nibbles4(prmt(a0, b0, 0x7632u), n1);
+        nibbles4(prmt(a1, b1, 0x5410u), n2);
+        nibbles4(prmt(a1, b1, 0x7632u), n3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mma16816<false>(acc[4 * w + j], n0[j], n1[j], n2[j], n3[j], hi0, hi1);
+          if constexpr (SPLIT) mma16816<false>(acc[4 * w + j], n0[j], n1[j], n2[j], n3[j], lo0, lo1);
+        }
+      }
+    }
+  };
+
+  // ---- split segments: an arrival is looked at only at the next one, so that it stalls nothing (as in paged_decode_kernel)
+  int arr_old = 0, arr_x = -1, arr_first = 0, arr_nfr = 0;
+  auto settle = [&] {
+    if (lane == 0 && arr_x >= 0 && arr_old == arr_nfr - 1) {  // last to arrive
+      int* const at = won + 1 + 3 * atomicAdd(won, 1);
+      at[0] = arr_x;
+      at[1] = arr_first;
+      at[2] = arr_nfr;
+    }
+    arr_x = -1;
+  };
+
+  auto end_fragment = [&] {
+    const Int4Frag& f = frags[cur];
+    // sums of rows 2t, 2t + 1 over the 8 lanes of equal t
+    float lt[2], z[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      lt[e] = l[e];
+      z[e] = z_sum[e];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        lt[e] += __shfl_xor_sync(0xffffffffu, lt[e], off);
+        z[e] += __shfl_xor_sync(0xffffffffu, z[e], off);
+      }
+    }
+    // O out of the units of the codes (2^-24, odd nibbles 2^-20) and of the weights, with the zeros' part
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      const float u = __int_as_float((127 + ((i & 1) ? 20 : 24) - 29 + vexp) << 23);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(acc[i][e], u, z[e & 1]);
+    }
+    if (f.slot < 0) {
+      const int64_t row0 = static_cast<int64_t>(f.rows0) * p.num_heads + static_cast<int64_t>(f.kvh) * G;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 2 * tig + e;
+        if (row >= G) continue;
+        const float inv = lt[e] > 0.f ? 1.f / lt[e] : 0.f;
+        const int64_t o = (row0 + row) * D + 16 * gid;
+#pragma unroll
+        for (int i = 0; i < KS; i += 2)
+          store_out4(p.out, p.out_dtype, o + 2 * i,
+                     make_float4(acc[i][e] * inv, acc[i][2 + e] * inv, acc[i + 1][e] * inv, acc[i + 1][2 + e] * inv), true);
+        if (p.att.mass && gid == 0)
+          p.att.row_stats[static_cast<int64_t>(f.s) * p.num_heads + f.kvh * G + row] = make_float2(m[e], lt[e]);
+      }
+      return;
+    }
+    float* const rec = p.part_records + static_cast<int64_t>(f.slot) * Tr::REC;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+        *reinterpret_cast<float2*>(rec + (16 * gid + 2 * i + hf) * GM + 2 * tig) = make_float2(acc[i][2 * hf], acc[i][2 * hf + 1]);
+    }
+    if (gid == 0) {
+      *reinterpret_cast<float2*>(rec + GM * D + 2 * tig) = make_float2(m[0], m[1]);
+      *reinterpret_cast<float2*>(rec + GM * D + GM + 2 * tig) = make_float2(lt[0], lt[1]);
+    }
+    const long long seg_start = prefix[f.s] + static_cast<long long>(f.kvh) * (f.nu + p.frag_cost);
+    const int first_w = ring_of(seg_start + p.frag_cost, U, nw_eff);
+    const int nfr = ring_of(seg_start + p.frag_cost + f.nu - 1, U, nw_eff) - first_w + 1;
+    settle();
+    __syncwarp();  // every lane's stores come before lane 0's release
+    int* const ctr = p.seg_counters + f.s * Hkv + f.kvh;
+    if (lane == 0) arr_old = atom_add_release_gpu(ctr, 1);
+    arr_x = f.s * Hkv + f.kvh;
+    arr_first = first_w;
+    arr_nfr = nfr;
+  };
+
+  // ---- units.  Unit aj of fragment af is the next to be fetched (while a_more), into stage as; its table entry is on its
+  // way.  A fragment's first unit (a_first) brings its query rows, into buffer aq: a buffer's last rows were read at the
+  // start of a fragment that is over by then.
+  int aj = j, af = 0, as = 0, aq = 0, ahead = 0;  // ahead: units fetched and not done with
+  bool a_more = true, a_first = true;
+  int entry = any ? entry_of(frags[0], j) : 0;
+  auto fetch_next = [&] {
+    if (a_more) {
+      const Int4Frag& f = frags[af];
+      fetch_unit(mine_u32 + as * Tr::STAGE, tile_of(f, entry), aj);
+      if (a_first) {
+        fetch_q(f, aq);
+        aq = aq + 1 == Tr::NS ? 0 : aq + 1;
+      }
+      as = as + 1 == Tr::NS ? 0 : as + 1;
+      ++ahead;
+      a_first = aj + 1 == f.jend;
+      if (a_first) {
+        WorkIter w = *walk;
+        iter_next_fragment<ATT, SINKS>(w, prefix, p, false, Tr::UR_SHIFT);
+        __syncwarp();  // every lane has read it
+        af = af + 1 == Tr::NFRAG ? 0 : af + 1;
+        note(w, af);
+        a_more = w.valid;
+        aj = w.j;
+      } else {
+        aj = aj + 1 == f.su ? aj + 1 + f.skip : aj + 1;
+      }
+      if (a_more) entry = entry_of(frags[af], aj);
+    }
+    cp_async_commit();  // a group per unit, empty ones behind the last
+  };
+  if (any) {
+#pragma unroll
+    for (int i = 0; i + 1 < Tr::NS; ++i) fetch_next();
+  }
+  bool first = true;  // the current unit is its fragment's first
+  for (int st = 0, q_buf = 0; any;) {
+    fetch_next();  // (into the stage of the unit before)
+    cp_async_wait<Tr::NS - 1>();
+    __syncwarp();
+    if (first) {
+      start_fragment(q_buf);
+      q_buf = q_buf + 1 == Tr::NS ? 0 : q_buf + 1;
+    }
+    const Int4Frag& f = frags[cur];
+    const int t0 = j << Tr::UR_SHIFT;
+    const uint32_t stage = mine_u32 + st * Tr::STAGE;
+    if (t0 + UR <= f.T && (t0 >= f.lo || t0 + UR <= f.sinks)) unit_step(std::true_type{}, stage);
+    else unit_step(std::false_type{}, stage);
+    st = st + 1 == Tr::NS ? 0 : st + 1;
+    first = j + 1 == f.jend;
+    if (first) {
+      end_fragment();
+      if (--ahead == 0) break;
+      cur = cur + 1 == Tr::NFRAG ? 0 : cur + 1;
+      j = frags[cur].j0;
+    } else {
+      --ahead;
+      j = j + 1 == f.su ? j + 1 + f.skip : j + 1;
+    }
+    __syncwarp();  // every lane has read the stage
+  }
+  cp_async_wait<0>();  // (empty groups)
+
+  // ---- segments whose last record came from this CTA: its warps join them, 16 columns at a time, the records in the
+  // order of the fragments (16 bytes per lane: 4 rows of one column).  Every warp is past its units then, and so are
+  // the other CTAs' warps that left records.
+  settle();
+  if (arr_nfr > 0) fence_acq_rel_gpu();  // what this warp's arrivals saw released
+  __syncthreads();
+  const int n_won = won[0];
+  // NP of a segment's eight 16-column parts by one warp, the loads of N records' under way at once
+  auto join = [&](auto parts) {
+    constexpr int NP = decltype(parts)::value, N = NP == 1 ? 8 : NP == 2 ? 4 : 2;
+    for (int g = warp; g < n_won * (8 / NP); g += W) {
+      const int* const w = won + 1 + 3 * (g / (8 / NP));
+      const int x = w[0], first_w = w[1], nfr = w[2], s = x / Hkv, kvh = x - s * Hkv;
+      const long long seg_start = prefix[s] + static_cast<long long>(kvh) * ((prefix[s + 1] - prefix[s]) / Hkv);
+      // the records: each share's first one, but the second of a share that starts before the segment
+      const int slot0 = 2 * first_w + (first_w * U < seg_start * nw_eff ? 1 : 0);
+      const int d0 = (g % (8 / NP)) * NP * 16 + (lane >> 1), r0 = 4 * (lane & 1);
+      const int64_t row0 = first_row(s) * p.num_heads + static_cast<int64_t>(kvh) * G;
+      auto load4 = [](const float* at) { return __ldcg(reinterpret_cast<const float4*>(at)); };
+      auto at = [](const float4& v, int e) { return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w; };
+      float M[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, L[4] = {}, o[NP][4] = {};
+#pragma unroll 1
+      for (int k0 = 0; k0 < nfr; k0 += N) {
+        float4 a[N][NP], mk[N], lk[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          // (behind the last: its record again, with a maximum of minus infinity)
+          const int kk = min(k0 + k, nfr - 1);
+          const float* const rec = p.part_records + static_cast<int64_t>(kk == 0 ? slot0 : 2 * (first_w + kk)) * Tr::REC;
+          mk[k] = load4(rec + GM * D + r0);
+          lk[k] = load4(rec + GM * D + GM + r0);
+#pragma unroll
+          for (int q = 0; q < NP; ++q) a[k][q] = load4(rec + (d0 + 16 * q) * GM + r0);
+          if (k0 + k >= nfr) mk[k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float mx = M[e];
+#pragma unroll
+          for (int k = 0; k < N; ++k) mx = fmaxf(mx, at(mk[k], e));
+          const float down = M[e] == -INFINITY ? 0.f : exp2f(M[e] - mx);  // (nothing joined yet)
+          M[e] = mx;
+          L[e] *= down;
+#pragma unroll
+          for (int q = 0; q < NP; ++q) o[q][e] *= down;
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const float wk = at(mk[k], e) == -INFINITY ? 0.f : exp2f(at(mk[k], e) - mx);
+            if (k0 + k >= nfr) continue;  // (a weight of zero would not leave infinities as they are)
+            L[e] = fmaf(wk, at(lk[k], e), L[e]);
+#pragma unroll
+            for (int q = 0; q < NP; ++q) o[q][e] = fmaf(wk, at(a[k][q], e), o[q][e]);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (r0 + e >= G) continue;
+        const float inv = L[e] > 0.f ? 1.f / L[e] : 0.f;
+#pragma unroll
+        for (int q = 0; q < NP; ++q) store_out(p.out, p.out_dtype, (row0 + r0 + e) * D + d0 + 16 * q, o[q][e] * inv);
+        if (p.att.mass && d0 == 0)
+          p.att.row_stats[static_cast<int64_t>(s) * p.num_heads + kvh * G + r0 + e] = make_float2(M[e], L[e]);
+      }
+      if (d0 == 0 && lane == 0) p.seg_counters[x] = 0;
+    }
+  };
+  // few segments: all warps on each; many: a warp each
+  if (n_won == 1) join(std::integral_constant<int, 1>());
+  else if (n_won == 2) join(std::integral_constant<int, 2>());
+  else if (n_won > 2) join(std::integral_constant<int, 8>());
+}
+
+}  // namespace pa

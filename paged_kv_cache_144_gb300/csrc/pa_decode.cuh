@@ -64,13 +64,9 @@
 //    same recurrence after its own unit loop, one row per lane, writes
 //    out[s, kvh*G .. kvh*G+G-1] and resets the counter.  Nothing waits on
 //    another warp, so the kernel cannot deadlock.
-//  * 4-bit caches (pa_attend only): a tile of one block, codes then pairs, comes
-//    in one bulk copy.  Codes enter the products as f16 subnormals, in the order
-//    of a word's nibbles: five instructions for eight of them, and no constant
-//    added that would have to be taken off again (with 64 + code and 16 + code the
-//    average of 32768 rows lost four bits to it: error 3.6e-3 against 1.7e-3 in a
-//    bf16 output).  A row's scale multiplies its score, or its weight; what the
-//    zeros contribute is added up apart in float32 (q_sum, z_sum).
+//  * 4-bit caches (pa_attend with several queries per sequence; one query:
+//    pa_attend_int4.cuh, which has the mathematics): a tile of one block, codes
+//    then pairs, comes in one bulk copy.
 //  * The variants of pa_attend (AP = 2; 3: with sinks) add the score modifiers, masks, ragged
 //    query rows and stored scores of include/pa.h; every difference is behind
 //    `if constexpr`, so the decode's own variants compile to what they were.
@@ -113,8 +109,8 @@ struct DecodeTraits {
   static constexpr bool B4 = std::is_same<KVT, i4_t>::value;  // 4-bit cache: rows of 64 bytes of codes, and 4 of their pair
   static constexpr int ROW = B4 ? int4_row_bytes(D) : D * KVB;  // bytes of one cache row
   static_assert(B4 || ROW == 128 || ROW == 256, "cache rows must be 128 or 256 bytes");
-  static constexpr int UR = UR_;                 // rows per work unit (32; 64 for 8- and 4-bit caches)
-  static_assert(UR == 32 || (UR == 64 && KVB <= 1), "unit rows");
+  static constexpr int UR = UR_;                 // rows per work unit (32; 64 for 8-bit caches)
+  static_assert(UR == 32 || (UR == 64 && KVB == 1), "unit rows");
   static constexpr int UR_SHIFT = UR == 64 ? 6 : 5;
   static constexpr int NSUB = B4 ? 1 : ROW / 128;  // 128-byte halves per row
   static constexpr int TILE = UR * ROW;          // bytes of one unit of K (or V)
@@ -139,7 +135,7 @@ struct DecodeTraits {
   static constexpr int OFF_EMPTY = OFF_FULL + MAX_NS * 8;
   static constexpr int OFF_MERGE = OFF_EMPTY + MAX_NS * 8;  // one barrier per warp of the ring: its merge copies
   static constexpr int OFF_QEMPTY = OFF_MERGE + 4 * 8;      // several queries: the ring's query buffer is free
-  static constexpr int OFF_STAGES = 1024;
+  static constexpr int OFF_STAGES = B4 ? 256 : 1024;
   static_assert(OFF_QEMPTY + 8 <= OFF_STAGES, "barriers");
   // Several queries per sequence (16-row variants): the query rows of a
   // fragment (16 per consumer warp of the ring) live in one buffer per ring,
@@ -439,7 +435,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                     const DecodeParams p) {
   using Tr = DecodeTraits<QT, KVT, D, GM, UR_>;
   constexpr bool k8bit = elem<KVT>::bytes == 1, k4bit = Tr::B4;
-  static_assert(!k4bit || AP == 3, "4-bit caches: pa_attend");
+  static_assert(!k4bit || (AP == 3 && GM == 16), "4-bit caches: pa_attend, several queries (pa_attend_int4.cuh: one)");
   constexpr int UR = Tr::UR;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -1007,31 +1003,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       float sc[NMT][4];
 #pragma unroll
       for (int mt = 0; mt < NMT; ++mt) sc[mt][0] = sc[mt][1] = sc[mt][2] = sc[mt][3] = 0.f;
-      if constexpr (k4bit) {
-#pragma unroll
-        for (int mt = 0; mt < NMT; ++mt) {
-          // 32 values of tokens tau(g) and 8 + tau(g): word r holds those of k-steps 2 r and 2 r + 1
-          const uint4 w0 = lds128(kt + codes_of(2 * mt) + tau(gid) * 64 + tig * 16);
-          const uint4 w1 = lds128(kt + codes_of(2 * mt + 1) + tau(gid) * 64 + tig * 16);
-          const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w};
-          const uint32_t x1[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            uint32_t n0[4], n1[4];
-            nibbles4(x0[r], n0);
-            nibbles4(x1[r], n1);
-            mma16816<false>(sc[mt], n0[0], n1[0], n0[1], n1[1], qa0[2 * r], qa1[2 * r]);
-            mma16816<false>(sc[mt], n0[2], n1[2], n0[3], n1[3], qa0[2 * r + 1], qa1[2 * r + 1]);
-          }
-          const float2 p0 = widen2<f16_t>(lds32(kt + pairs_of(2 * mt) + tau(gid) * 4));
-          const float2 p1 = widen2<f16_t>(lds32(kt + pairs_of(2 * mt + 1) + tau(gid) * 4));
-          const float s0 = p0.x * kCodeUnit, s1 = p1.x * kCodeUnit;
-          sc[mt][0] = fmaf(sc[mt][0], s0, p0.y * q_sum[0]);
-          sc[mt][1] = fmaf(sc[mt][1], s0, p0.y * q_sum[1]);
-          sc[mt][2] = fmaf(sc[mt][2], s1, p1.y * q_sum[0]);
-          sc[mt][3] = fmaf(sc[mt][3], s1, p1.y * q_sum[1]);
-        }
-      } else if constexpr (!k8bit) {
+      if constexpr (!k8bit) {
 #pragma unroll
         for (int mt = 0; mt < NMT; ++mt) {
 #pragma unroll
@@ -1109,38 +1081,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
       }
-      // 4-bit: the V rows' pairs (of one that is not attended, which may hold anything: zero), their largest scale
-      [[maybe_unused]] uint32_t vpair[NMT][2];
-      [[maybe_unused]] int vbits = 0;
-      if constexpr (k4bit) {
-#pragma unroll
-        for (int mt = 0; mt < NMT; ++mt) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            vpair[mt][x] = lds32(vt + pairs_of(2 * mt + x) + tau(gid) * 4);
-            if constexpr (!FULL) {
-              const int tok = 16 * mt + 8 * x + tau(gid);
-              if (tok >= n_valid || (tok < lo_rel && tok >= sink_rel)) vpair[mt][x] = 0u;
-            }
-            vbits = scale_bits(vbits, vpair[mt][x]);
-          }
-        }
-      }
       // every row sees a token in every unit it processes: the new maxima are finite
-      if (__any_sync(0xffffffffu, mx0 > m[0] || mx1 > m[1] || (k4bit && (vbits >> 10) > vexp))) {
+      if (__any_sync(0xffffffffu, mx0 > m[0] || mx1 > m[1])) {
         const float mn0 = fmaxf(m[0], mx0), mn1 = fmaxf(m[1], mx1);
-        float a0 = fast_exp2(m[0] - mn0), a1 = fast_exp2(m[1] - mn1);
+        const float a0 = fast_exp2(m[0] - mn0), a1 = fast_exp2(m[1] - mn1);
         m[0] = mn0;
         m[1] = mn1;
         l[0] *= a0;
         l[1] *= a1;
-        if constexpr (k4bit) {
-          z_sum[0] *= a0;
-          z_sum[1] *= a1;
-          const float f = larger_scale(vbits);
-          a0 *= f;
-          a1 *= f;
-        }
 #pragma unroll
         for (int i = 0; i < Tr::KS; ++i) {
           acc[i][0][0] *= a0;
@@ -1149,28 +1097,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
           acc[i][0][3] *= a1;
         }
       }
-      [[maybe_unused]] float wunit = 0.f;
-      if constexpr (k4bit) wunit = weight_unit();
       // P, then its transposes: m-rows g (g + 8) of S become k-rows 2t, 2t + 1
       // (2t + 8, 2t + 9) of P^T, the token order the V loads use
 #pragma unroll
       for (int mt = 0; mt < NMT; ++mt) {
-        float p0 = fast_exp2(sc[mt][0] - m[0]);
-        float p1 = fast_exp2(sc[mt][1] - m[1]);
-        float p2 = fast_exp2(sc[mt][2] - m[0]);
-        float p3 = fast_exp2(sc[mt][3] - m[1]);
+        const float p0 = fast_exp2(sc[mt][0] - m[0]);
+        const float p1 = fast_exp2(sc[mt][1] - m[1]);
+        const float p2 = fast_exp2(sc[mt][2] - m[0]);
+        const float p3 = fast_exp2(sc[mt][3] - m[1]);
         l[0] += p0 + p2;
         l[1] += p1 + p3;
-        if constexpr (k4bit) {
-          const float2 v0 = widen2<f16_t>(vpair[mt][0]), v1 = widen2<f16_t>(vpair[mt][1]);
-          z_sum[0] = fmaf(p0, v0.y, fmaf(p2, v1.y, z_sum[0]));
-          z_sum[1] = fmaf(p1, v0.y, fmaf(p3, v1.y, z_sum[1]));
-          const float s0 = v0.x * wunit, s1 = v1.x * wunit;
-          p0 *= s0;
-          p1 *= s0;
-          p2 *= s1;
-          p3 *= s1;
-        }
         const uint32_t h01 = pack2<MB>(p0, p1), h23 = pack2<MB>(p2, p3);
         const float2 f01 = unpack2<MB>(h01), f23 = unpack2<MB>(h23);
         ph[mt][0][0] = movmatrix_trans(h01);
@@ -1722,7 +1658,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     }
     if constexpr (k4bit) {
       vexp = -1;
-      // the sums of query rows g (and g + 8), as they enter the products; one query: then of this lane's rows 2t, 2t + 1
+      // the sums of query rows g and g + 8, as they enter the products
       auto sum_row = [&](const uint32_t(&a)[Tr::KS], const uint32_t(&b)[Tr::KS]) {
         float x = 0.f;
 #pragma unroll
@@ -1733,14 +1669,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         return x + __shfl_xor_sync(0xffffffffu, x, 2);
       };
-      const float sg = sum_row(qa0, qa1);
-      if constexpr (MQ) {
-        q_sum[0] = sg;
-        q_sum[1] = sum_row(qb0, qb1);
-      } else {
-        q_sum[0] = __shfl_sync(0xffffffffu, sg, 8 * tig);
-        q_sum[1] = __shfl_sync(0xffffffffu, sg, 8 * tig + 4);
-      }
+      q_sum[0] = sum_row(qa0, qa1);
+      q_sum[1] = sum_row(qb0, qb1);
     }
     score_scale = p.qk_scale_log2;
     if constexpr (k8bit) score_scale *= hp_ks[it.kvh];
@@ -1821,21 +1751,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       if constexpr (k4bit) {  // the rows' share of the zeros joins their products
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          float z0, z1;  // of rows 8h + 2t, 8h + 2t + 1
-          if constexpr (MQ) {
-            float z = z_sum[h] + __shfl_xor_sync(0xffffffffu, z_sum[h], 1);
-            z += __shfl_xor_sync(0xffffffffu, z, 2);
-            z0 = __shfl_sync(0xffffffffu, z, 8 * tig);
-            z1 = __shfl_sync(0xffffffffu, z, 8 * tig + 4);
-          } else {
-            z0 = z_sum[0];
-            z1 = z_sum[1];
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-              z0 += __shfl_xor_sync(0xffffffffu, z0, off);
-              z1 += __shfl_xor_sync(0xffffffffu, z1, off);
-            }
-          }
+          float z = z_sum[h] + __shfl_xor_sync(0xffffffffu, z_sum[h], 1);
+          z += __shfl_xor_sync(0xffffffffu, z, 2);
+          const float z0 = __shfl_sync(0xffffffffu, z, 8 * tig), z1 = __shfl_sync(0xffffffffu, z, 8 * tig + 4);  // of rows 8h + 2t (+ 1)
 #pragma unroll
           for (int i = 0; i < Tr::KS; ++i) {
             // O in units of the codes (2^-24, odd nibbles 2^-20) and of the weights

@@ -78,10 +78,8 @@
   X(f16_t, i8_t, 128, 8, 32, 3) X(f16_t, i8_t, 128, 8, 64, 3) X(bf16_t, e4m3_t, 128, 16, 32, 3) \
   X(bf16_t, i8_t, 128, 16, 32, 3) X(f16_t, e4m3_t, 128, 16, 32, 3) X(f16_t, i8_t, 128, 16, 32, 3)
 
-// 4-bit caches
-#define PA_DECODE_VARIANTS_INT4(X) \
-  X(bf16_t, i4_t, 128, 8, 32, 3) X(bf16_t, i4_t, 128, 8, 64, 3) X(f16_t, i4_t, 128, 8, 32, 3) \
-  X(f16_t, i4_t, 128, 8, 64, 3) X(bf16_t, i4_t, 128, 16, 32, 3) X(f16_t, i4_t, 128, 16, 32, 3)
+// 4-bit caches: several queries (one query per sequence: attend_int4_kernel)
+#define PA_DECODE_VARIANTS_INT4(X) X(bf16_t, i4_t, 128, 16, 32, 3) X(f16_t, i4_t, 128, 16, 32, 3)
 
 #define PA_DECODE_VARIANTS(X) \
   PA_DECODE_VARIANTS_F16(X) PA_DECODE_VARIANTS_BF16(X) PA_DECODE_VARIANTS_FP8(X) PA_DECODE_VARIANTS_INT8(X) \

@@ -6,7 +6,8 @@ as AttendCase.tolerance has it.  But the codes' part and the zeros' part of an o
 is at most R = 3 times the largest value (zero is the row's smallest value, code * scale at most the difference to the
 largest).  The first is off by 2^-22 R for its weights; either by 2^-23 R for each addition to its accumulator (the tensor
 cores cut off, two products per 16 positions; a float32 addition per 8), of which there are at most min(T, 2048) / 8 in a
-warp: longer sequences are split over the device, here to shares far below that.
+warp: longer sequences are split over the device, here to shares far below that.  With one query per sequence and a bfloat16
+output a scaled weight is one float16 value: 2^-11 R, a quarter of the output's own half step for values near R.
 
 In calls of many rows K and V are rounded to float16 once: half a step, 2^-11 of a value, at most.  A score then is off by
 the sum of 128 independent errors q_i k_i 2^-11, uniform: a standard deviation of 2^-11 / sqrt(3) * sqrt(sum q_i^2 k_i^2) /
@@ -79,7 +80,8 @@ class Case(AttendCase):
         mult = max(1.0, float(self.q.float().abs().max()) / 4.5)
         if max(self.qlens) * group <= 16:                  # always on the decode kernel
             steps = 1 + 2 * min(max(self.lens), 2048) // 8
-            return tol + (2.0 ** -22 + steps * 2.0 ** -23) * 3 * float(self.v64.abs().max())
+            weight = 2.0 ** -11 if out_fmt == "bf16" and max(self.qlens) == 1 else 2.0 ** -22
+            return tol + (weight + steps * 2.0 ** -23) * 3 * float(self.v64.abs().max())
         return tol + (2 * 6 * 2.9e-4 * mult + 2.0 ** -11) * wabs
 
 

@@ -150,6 +150,40 @@ def test_nan_shows_where_it_is_seen():
             assert not torch.isnan(got[i, 4:]).any()
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_not_finite_in_a_segment_split_over_many_warps(value, which):
+    """One pair of 9000 positions that is not finite: KV head 0's rows show it, through the join of their records; the others
+    do not."""
+    c = Case([9000], [1], kv="i4", seed=31)
+    plain, _ = run(c)
+    b, r = c.row_of(0, 4321)
+    pool = getattr(c, which)
+    pool[..., c.block * 64:].view(torch.float16).view(c.blocks, c.kv_heads, c.block, 2)[b, 0, r, 1] = value
+    got, err = run(c)
+    assert err == 0
+    if which == "v" and value == float("inf"):
+        assert torch.all(got[0, :4] == value)                # every column of that row is infinite
+    elif which == "v":
+        assert torch.isnan(got[0, :4]).all()
+    else:                                                    # a score of either infinity, by the sign of sum(q), or NaN
+        q = c.q[0, :4].to(F64).sum(-1)
+        for h in range(4):
+            if value == float("inf") and q[h] < 0:
+                assert torch.isfinite(got[0, h]).all()       # that position has no weight
+            else:
+                assert torch.isnan(got[0, h]).all()
+    assert torch.equal(got[0, 4:], plain[0, 4:])
+
+
+def test_many_segments_joined_by_few_blocks():
+    """More segments than CTAs, each cut in two or three: CTAs that join several of them."""
+    g = torch.Generator().manual_seed(32)
+    lens = torch.randint(900, 1300, (90,), generator=g).tolist()
+    check(Case(lens, [1] * 90, kv="i4", heads=16, kv_heads=4, seed=32), spoil=False)
+    check(Case(lens, [1] * 90, kv="i4", heads=16, kv_heads=4, seed=33, window=700, sinks=70), "bf16", spoil=False)
+
+
 def test_bad_block_is_reported():
     c = Case([40], [1], kv="i4", seed=27)
     c.tables[0, 1] = c.blocks + 3
