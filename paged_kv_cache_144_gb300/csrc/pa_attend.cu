@@ -15,10 +15,13 @@ namespace {
 //   bf16, 2^20 positions: 32 rows 120 / 153, 48 rows 162 / 156, 64 rows 236 / 157;  2^21: 32 rows 241 / 201, 64 rows 456 / 204
 //   bf16, 2^19 positions: 32 rows 72 / 103, 48 rows 90 / 101, 64 rows 127 / 105;  2^16: 64 rows 27 / 63
 //   e4m3, 2^20 positions: 32 rows 135 / 254, 48 rows 192 / 255, 64 rows 281 / 257;  2^19: 64 rows 134 / 131
+//   4 bits, 2^22 positions: 32 rows 788 / 785;  2^20: 32 rows 217 / 270, 48 rows 311 / 275;  2^19: 48 rows 169 / 185, 64 rows
+//   248 / 190;  2^16: 64 rows 62 / 138
 constexpr int kFewRows = 64;
-bool few_rows(int64_t rows, int64_t positions, bool q8) {
+bool few_rows(int64_t rows, int64_t positions, bool q8, bool q4) {
   const int64_t row_groups = (rows + 15) / 16;
-  return rows <= 16 || (rows <= kFewRows && positions <= int64_t{1} << ((q8 ? 23 : 22) - row_groups));
+  const int64_t bits = q4 ? (row_groups == 2 ? 22 : 22 - row_groups) : (q8 ? 23 : 22) - row_groups;
+  return rows <= 16 || (rows <= kFewRows && positions <= int64_t{1} << bits);
 }
 // Units charged per fragment in their balanced split, as in pa_decode.  4 trees of 5 to 16 nodes over 20 to 300 tokens with
 // 1 / 2 / 3 / 5 units: 27.5 / 23.5 / 26.8 / 30.7 us with the commit (fewer, longer pieces against joins); 32 x 4K decode steps
@@ -68,7 +71,7 @@ bool make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
   pl->seg_rows = rps * pl->cg * (pl->paired ? 2 : 1);
   const int few = tuning_override("PA_ATTEND_FEW_ROWS");  // tuning
   const int64_t positions = static_cast<int64_t>(num_seqs) * num_kv_heads * span;
-  const bool chosen = prefer >= 0 ? prefer == Plan::kFew : few >= 0 ? rows <= few : few_rows(rows, positions, q8);
+  const bool chosen = prefer >= 0 ? prefer == Plan::kFew : few >= 0 ? rows <= few : few_rows(rows, positions, q8, q4);
   const bool is_few = rows <= kFewRows && (accumulate || chosen);
   pl->kind = is_few ? Plan::kFew : Plan::kTensor;
   size_t records = 0, pending = 0;

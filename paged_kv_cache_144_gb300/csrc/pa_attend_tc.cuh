@@ -491,7 +491,7 @@ struct TcTraits {
   static constexpr int STAGE = TILE_BYTES / CG;    // bytes of a K or V stage
   static constexpr int NST = CODES ? 3 : (D == 128 ? 2 : 4) * CG;  // stages of K and of V
   // 8-bit caches: stages of codes as they come, [rows][128 / CG bytes] for V; 4-bit: [box][rows of codes, their pairs]
-  static constexpr int NR = CODES ? 2 : 0;
+  static constexpr int NR = B4 ? 3 : B8 ? 2 : 0;
   static constexpr int RAW_K = B8 ? STAGE / 2 : B4 ? KROWS * int4_row_bytes(D) : 0;
   static constexpr int RAW_V = B8 ? STAGE / 2 : B4 ? kTile * int4_row_bytes(D) : 0;
   static_assert(RAW_K % 128 == 0 && RAW_V % 128 == 0, "alignment");
@@ -1067,19 +1067,20 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       [[maybe_unused]] auto codes_at = [&](int r, int box_rows) { return r * (D / 2) + 4 * (r & ~(box_rows - 1)); };
       [[maybe_unused]] auto pair_at = [&](int r, int box_rows) { return 4 * r + (D / 2) * ((r & ~(box_rows - 1)) + box_rows); };
       [[maybe_unused]] auto widen8 = [&](uint32_t w, uint32_t pair) {
-        const uint32_t s2 = prmt(pair, pair, 0x1010u), z2 = prmt(pair, pair, 0x3232u);
-        uint4 o;
-        auto two = [&](uint32_t x) {  // f16x2 64 + code -> value
+        const uint32_t s2 = prmt(pair, pair, 0x1010u), z2 = prmt(pair, pair, 0x3232u), u = w >> 8;
+        // f16x2 of a pair of codes with a constant above them (1024 + code, or 64 + code) -> values
+        auto two = [&](uint32_t x, uint32_t constant) {
           uint32_t y;
           asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tfma.rn.f16x2 %0, t, %3, %4;\n\t}"
               : "=r"(y)
-              : "r"(x), "r"(0x54005400u), "r"(s2), "r"(z2));
+              : "r"(x), "r"(constant), "r"(s2), "r"(z2));
           return y;
         };
-        o.x = two(nibbles_f16_64<0>(w));
-        o.y = two(nibbles_f16_64<1>(w));
-        o.z = two(nibbles_f16_64<2>(w));
-        o.w = two(nibbles_f16_64<3>(w));
+        uint4 o;
+        o.x = two((w & 0x000f000fu) | 0x64006400u, 0x64006400u);
+        o.y = two((w & 0x00f000f0u) | 0x54005400u, 0x54005400u);
+        o.z = two((u & 0x000f000fu) | 0x64006400u, 0x64006400u);
+        o.w = two((u & 0x00f000f0u) | 0x54005400u, 0x54005400u);
         return o;
       };
       // 16 codes to two 16-byte chunks of f16

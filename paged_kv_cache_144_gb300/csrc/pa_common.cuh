@@ -417,13 +417,6 @@ __device__ __forceinline__ void nibbles4(uint32_t w, uint32_t (&n)[4]) {
   n[2] = u & 0x000f000fu;
   n[3] = u & 0x00f000f0u;
 }
-// Nibble J of each half as f16x2 64 + code, exact.
-template <int J>
-__device__ __forceinline__ uint32_t nibbles_f16_64(uint32_t w) {
-  const uint32_t x = J == 0 ? w << 4 : w >> (4 * J - 4);
-  return (x & 0x00f000f0u) | 0x54005400u;
-}
-
 // float32 y (= x * inv_scale, already rounded to float32) -> INT8 code:
 // nearest integer (ties to even) plus the zero point, saturated to the int8
 // range; NaN saturates upward.

@@ -574,7 +574,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   const long long U = prefix[S];  // partitions (fixed) or cost positions (balanced) of the batch
   // pa_attend: row of q and out of the sequence's first query (q_starts validated above; unused otherwise)
   auto first_row = [&](int s) -> int64_t { return p.att.q_starts ? __ldg(p.att.q_starts + s) : s; };
-  const int min_share = kMinUnitsPerWarp + (fixed ? 0 : p.frag_cost);
+  // (4-bit units are small, and a segment's records are joined by one warp: 65536 positions over 8 segments, 64 rows, 62 us with
+  // the others' smallest share)
+  const int min_share = (k4bit ? 8 : kMinUnitsPerWarp) + (fixed ? 0 : p.frag_cost);
   long long want = (U + min_share - 1) / min_share;
   const int nw_eff = fixed ? nw_total : static_cast<int>(want < 1 ? 1 : (want < nw_total ? want : nw_total));
   // (pa_attend: a batch of few rings has them on as many SMs)
