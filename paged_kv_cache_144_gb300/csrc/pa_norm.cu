@@ -13,6 +13,17 @@
 // pairs, else two neighbouring ones: every pair lies in one thread and the row is
 // read and written in 16-byte pieces (a 4-bit row: a word of 8 codes per chunk).
 // A CTA takes kTokens tokens and a slice of their heads, as in pa_rope.cu.
+//
+// What bounds it: instructions, next to memory traffic (device times, caches cold).
+// 8192 tokens of 32 + 2 x 8 heads of 128: to a bf16 cache 38 us, 5.3 TB/s (78 % of
+// a plain copy); to 4 bits 47 us (bounds, quotients and packing of a third of the
+// rows).  2049 tokens to FP8, half the columns turned: 13 us.  32 tokens: 5 us, the
+// latency of a launch, the tokens' loads and one store.  Taken for 8192 tokens to
+// 16 / 4 bits: angles and weights laid out for the threads' 16-byte reads 43.9 -> 38.0
+// / 62 -> 55 us; quotients by the reciprocal but near halves, a register limit
+// for eight CTAs per SM in the 4-bit variant 55 -> 47 (the others lose by it: 38 ->
+// 40).  Other shapes, 16 bits: 64 threads 42, 256 threads 58, one row in flight 40,
+// three 39.
 #include "pa_rope.cuh"
 
 namespace pa {
@@ -30,6 +41,33 @@ constexpr unsigned kFillCtas = 1024;  // CTAs below which a token's heads are sp
 __device__ __forceinline__ float load_weight(const void* w, int dtype, int i) {
   return dtype == PA_F32 ? static_cast<const float*>(w)[i]
                          : (dtype == PA_BF16 ? load_scalar<bf16_t>(w, i) : load_scalar<f16_t>(w, i));
+}
+
+// A turn's fraction, times 2^64, that a position adds at this frequency: inv_freq / 2 pi modulo 1.  As in pa_rope.cuh, but by
+// integers: the float's mantissa times 1 / 2 pi in 128 bits, shifted by its exponent (exact to 2^-62 of a turn for frequencies
+// below 2^24; 64-bit floating point runs at 2 operations per cycle and SM here, and took an eighth of the time of a long
+// prompt).
+__device__ __forceinline__ unsigned long long turn_step(float inv_freq) {
+  const uint32_t bits = __float_as_uint(inv_freq);
+  const int e = static_cast<int>((bits >> 23) & 0xffu);
+  const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
+  constexpr unsigned long long kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;  // 2^128 / 2 pi
+  // m * 2^128 / 2 pi in 192 bits (the lowest 64 only carry), then the bits of weight 2^-1 .. 2^-64 of m * 2^(e - 150) / 2 pi
+  const unsigned long long carry = __umul64hi(m, kLo), mid = m * kHi + carry;
+  const unsigned long long top = __umul64hi(m, kHi) + (mid < carry ? 1ull : 0ull);
+  const int n = 214 - max(e, 1) - 64;  // right shift of top : mid
+  unsigned long long step;
+  if (n < 0) step = n > -64 ? (mid << -n) | ((m * kLo) >> (64 + n)) : 0ull;
+  else if (n < 64) step = n == 0 ? mid : (mid >> n) | (top << (64 - n));
+  else step = n < 128 ? top >> (n - 64) : 0ull;
+  return (bits >> 31) ? 0ull - step : step;
+}
+__device__ __forceinline__ float2 turn_of(unsigned long long step, int64_t position, float scale) {
+  const unsigned long long phase = step * static_cast<unsigned long long>(position);
+  const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
+  float sn, c;
+  sincospif(half_turns, &sn, &c);
+  return make_float2(c * scale, sn * scale);
 }
 
 // One 4-bit row by `lanes` neighbouring threads (a power of two), 16 values each,
@@ -59,31 +97,53 @@ __device__ __forceinline__ void store_int4(uint8_t* codes, uint8_t* pair, int l,
   const float zero = __half2float(hz);
   const __half hs = __float2half_rn(fmaxf(__fdiv_rn(hi - zero, 15.f), 0.f));
   const float scale = __half2float(hs);
-  const float step = scale > 0.f ? scale : INFINITY;  // a row of one value: code 0
-  auto word = [&](const float (&x)[8]) {
-    uint32_t w = 0u;
+  // A product with the reciprocal is off by at most 2^-22 of a quotient of 15 or so: it rounds as the quotient does unless it
+  // is that close to a half.
+  const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;  // a row of one value: code 0
+  constexpr float kRound = 12582912.f;                    // 1.5 2^23: added and taken off, it leaves the nearest whole number
+  float off = 0.f;                                         // the largest distance from a whole number
+  auto near = [&](float x) {
+    const float y = x - zero, n = fmaf(y, inv, kRound) - kRound;
+    off = fmaxf(off, fabsf(fmaf(y, inv, -n)));
+    return fminf(fmaxf(n, 0.f), 15.f);
+  };
+  auto exact = [&](float x) { return fminf(fmaxf(rintf(__fdiv_rn(x - zero, scale > 0.f ? scale : INFINITY)), 0.f), 15.f); };
+  // 8 codes to a word: even values to its lower half, odd ones to the upper, four bits each
+  auto word = [](const float (&c)[8]) {
+    const float even = fmaf(fmaf(fmaf(c[6], 16.f, c[4]), 16.f, c[2]), 16.f, c[0]);
+    const float odd = fmaf(fmaf(fmaf(c[7], 16.f, c[5]), 16.f, c[3]), 16.f, c[1]);
+    return static_cast<uint32_t>(even) | (static_cast<uint32_t>(odd) << 16);
+  };
+  float cp[8], cq[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    cp[i] = near(p[i]);
+    cq[i] = near(q[i]);
+  }
+  if (!(off < 0.49999f)) {  // (NaN and values beyond the clip too)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float c = fminf(fmaxf(rintf(__fdiv_rn(x[i] - zero, step)), 0.f), 15.f);
-      w |= static_cast<uint32_t>(c) << (16 * (i & 1) + 4 * (i >> 1));
+      cp[i] = exact(p[i]);
+      cq[i] = exact(q[i]);
     }
-    return w;
-  };
-  reinterpret_cast<uint32_t*>(codes)[ca] = word(p);
-  reinterpret_cast<uint32_t*>(codes)[cb] = word(q);
+  }
+  reinterpret_cast<uint32_t*>(codes)[ca] = word(cp);
+  reinterpret_cast<uint32_t*>(codes)[cb] = word(cq);
   if (l == 0)
     *reinterpret_cast<uint32_t*>(pair) =
         static_cast<uint32_t>(__half_as_ushort(hs)) | (static_cast<uint32_t>(__half_as_ushort(hz)) << 16);
 }
 
 template <typename SRC, int MODE, int D, int LAYOUT>
-__global__ void __launch_bounds__(kThreads) norm_rope_and_cache_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kThreads, MODE == kToInt4 ? 8 : 1) norm_rope_and_cache_kernel(const NormArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int L = D / 16;                  // threads of a row
   constexpr int PASS = kThreads / L;         // rows of a pass over the CTA
-  __shared__ float2 cs[kTokens][D / 2];
-  __shared__ __align__(16) float weights[2][D];
+  // Both as the threads read them, 16 bytes each: pairs 8 l + 2 x, 8 l + 2 x + 1 of thread l at [x][l], weights 8 c + 4 x .. of
+  // chunk c at [x][c] (as [l][8 pairs] and [c][8 weights] the reads met in a quarter of the banks).
+  __shared__ float4 cs[kTokens][4][D / 16];
+  __shared__ float4 weights[2][2][D / 8];
   __shared__ int64_t block_of[kTokens];
   __shared__ int row_of[kTokens];
   __shared__ float row_buf[LAYOUT == kHalfAny ? PASS : 1][LAYOUT == kHalfAny ? D + 1 : 1];
@@ -128,11 +188,13 @@ __global__ void __launch_bounds__(kThreads) norm_rope_and_cache_kernel(const Nor
     if (!ready) {
       for (int x = threadIdx.x; x < nt * half; x += kThreads) {
         const int t = x >= half ? 1 : 0, i = x - t * half;
-        cs[t][i] = rope_turn(__ldg(r.inv_freq + i), r.positions[n0 + t], r.rope_scale);
+        reinterpret_cast<float2*>(&cs[t][(i & 7) >> 1][i >> 3])[i & 1] =
+            turn_of(turn_step(__ldg(r.inv_freq + i)), r.positions[n0 + t], r.rope_scale);
       }
       for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
         const void* g = x < D ? a.q_weight : a.k_weight;
-        if (g) weights[x / D][x % D] = load_weight(g, a.weight_dtype, x % D) + a.weight_offset;
+        const int i = x % D;
+        if (g) reinterpret_cast<float*>(&weights[x / D][(i & 7) >> 2][i >> 3])[i & 3] = load_weight(g, a.weight_dtype, i) + a.weight_offset;
       }
       if (threadIdx.x < nt) {
         const int64_t slot = w.slot_mapping[n0 + threadIdx.x];
@@ -165,41 +227,48 @@ __global__ void __launch_bounds__(kThreads) norm_rope_and_cache_kernel(const Nor
         for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (g) {
           const float inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-          const float* const gw = weights[wh];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            p[i] *= inv * gw[8 * ca + i];
-            q[i] *= inv * gw[8 * cb + i];
+          for (int x = 0; x < 2; ++x) {
+            const float4 u = weights[wh][x][ca], v = weights[wh][x][cb];
+            const float uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              p[4 * x + i] *= inv * uw[i];
+              q[4 * x + i] *= inv * vw[i];
+            }
           }
         }
       }
       if (half > 0) {
-        const float2* const c2 = cs[tok[k] > 0 ? 1 : 0];
+        const float4(&c4)[4][D / 16] = cs[tok[k] > 0 ? 1 : 0];
         if constexpr (LAYOUT == kHalf) {
           if (paired && wh != 2) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 f = c2[8 * l + i];
-              const float y = p[i], z = q[i];
-              p[i] = y * f.x - z * f.y;
-              q[i] = z * f.x + y * f.y;
+            for (int x = 0; x < 4; ++x) {
+              const float4 f = c4[x][l];
+              const float y0 = p[2 * x], z0 = q[2 * x], y1 = p[2 * x + 1], z1 = q[2 * x + 1];
+              p[2 * x] = y0 * f.x - z0 * f.y;
+              q[2 * x] = z0 * f.x + y0 * f.y;
+              p[2 * x + 1] = y1 * f.z - z1 * f.w;
+              q[2 * x + 1] = z1 * f.z + y1 * f.w;
             }
           }
         } else if constexpr (LAYOUT == kInterleaved) {
           if (wh != 2) {
+            // pairs 8 l .. 8 l + 3 lie in the first chunk, 8 l + 4 .. in the second
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (8 * l + i < half) {
-                const float2 f = c2[8 * l + i];
-                const float y = p[2 * i], z = p[2 * i + 1];
-                p[2 * i] = y * f.x - z * f.y;
-                p[2 * i + 1] = z * f.x + y * f.y;
+            for (int x = 0; x < 4; ++x) {
+              const float4 f = c4[x][l];
+              float* const at = (x < 2 ? p : q) + 4 * (x & 1);
+              if (8 * l + 2 * x < half) {
+                const float y = at[0], z = at[1];
+                at[0] = y * f.x - z * f.y;
+                at[1] = z * f.x + y * f.y;
               }
-              if (8 * l + 4 + i < half) {
-                const float2 f = c2[8 * l + 4 + i];
-                const float y = q[2 * i], z = q[2 * i + 1];
-                q[2 * i] = y * f.x - z * f.y;
-                q[2 * i + 1] = z * f.x + y * f.y;
+              if (8 * l + 2 * x + 1 < half) {
+                const float y = at[2], z = at[3];
+                at[2] = y * f.z - z * f.w;
+                at[3] = z * f.z + y * f.w;
               }
             }
           }
@@ -213,9 +282,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_and_cache_kernel(const Nor
           }
           __syncwarp();
           if (wh != 2) {
+            auto pair = [&](int i) { return reinterpret_cast<const float2*>(&c4[(i & 7) >> 1][i >> 3])[i & 1]; };
             auto turn = [&](int c, float x) {
-              if (c < half) return x * c2[c].x - buf[c + half] * c2[c].y;
-              if (c < 2 * half) return x * c2[c - half].x + buf[c - half] * c2[c - half].y;
+              if (c < half) return x * pair(c).x - buf[c + half] * pair(c).y;
+              if (c < 2 * half) return x * pair(c - half).x + buf[c - half] * pair(c - half).y;
               return x;
             };
 #pragma unroll
@@ -251,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_and_cache_kernel(const Nor
         }
       }
       if constexpr (MODE == kToInt4) {
-        store_int4<L>(d.row, pair, l, ca, cb, p, q, live && d.cache);  // (exchanges within the warp)
+        if (__any_sync(0xffffffffu, d.cache)) store_int4<L>(d.row, pair, l, ca, cb, p, q, live && d.cache);  // (exchanges within the warp)
         if (live && !d.cache) {
           store8<SRC, kCopy>(d, 8 * ca, p);
           store8<SRC, kCopy>(d, 8 * cb, q);

@@ -222,6 +222,7 @@ PA_EXPORT int pa_read_cache(void* k_out, void* v_out, pa_dtype out_dtype, int64_
   if (ps != PA_OK) return ps;
   const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
   if (k_out_stride < row || v_out_stride < row) return PA_ERR_SHAPE;
+  if (num_tokens * static_cast<int64_t>(num_kv_heads) >= (int64_t{1} << 35)) return PA_ERR_SHAPE;  // CTAs of 32 rows
   const int64_t piece = out_dtype == PA_F32 ? 4 : 8;  // elements of 16 bytes
   if (!aligned16(k_out) || !aligned16(v_out) || k_out_stride % piece != 0 || v_out_stride % piece != 0) return PA_ERR_ALIGN;
   const int64_t bytes = out_dtype == PA_F32 ? 4 : 2;
