@@ -349,7 +349,7 @@ def decode(out, q, k_cache, v_cache, block_tables, seq_lens, num_kv_heads, scale
     NB = k_cache.shape[0]
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (_ptr(out), dtype_code(out), _ptr(q), dtype_code(q), q.stride(0),
-            _ptr(k_cache), _ptr(v_cache), dtype_code(k_cache), NB,
+            _ptr(k_cache), _ptr(v_cache), cache_dtype_code(k_cache), NB,
             _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
             S, Hq, int(num_kv_heads), D, float(scale), int(block_size), int(partition_size),
             _ptr(workspace), ws_bytes)
@@ -377,7 +377,7 @@ def decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_lens, num_kv_head
         raise ValueError("q rows must be contiguous per sequence")
     S, Hq, D = q.shape
     st = pa_decode_noalloc(_ptr(out), dtype_code(out), _ptr(q), dtype_code(q), q.stride(0),
-                           _ptr(k_cache), _ptr(v_cache), dtype_code(k_cache), k_cache.shape[0],
+                           _ptr(k_cache), _ptr(v_cache), cache_dtype_code(k_cache), k_cache.shape[0],
                            _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
                            S, Hq, int(num_kv_heads), D, float(scale), int(block_size), int(partition_size),
                            _stream(stream))

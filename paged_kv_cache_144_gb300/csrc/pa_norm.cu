@@ -44,9 +44,8 @@ __device__ __forceinline__ float load_weight(const void* w, int dtype, int i) {
 }
 
 // A turn's fraction, times 2^64, that a position adds at this frequency: inv_freq / 2 pi modulo 1.  As in pa_rope.cuh, but by
-// integers: the float's mantissa times 1 / 2 pi in 128 bits, shifted by its exponent (exact to 2^-62 of a turn for frequencies
-// below 2^24; 64-bit floating point runs at 2 operations per cycle and SM here, and took an eighth of the time of a long
-// prompt).
+// integers, since 64-bit floating point is slow here: the float's mantissa times 1 / 2 pi in 128 bits, shifted by its exponent
+// (exact to 2^-62 of a turn for frequencies below 2^24).
 __device__ __forceinline__ unsigned long long turn_step(float inv_freq) {
   const uint32_t bits = __float_as_uint(inv_freq);
   const int e = static_cast<int>((bits >> 23) & 0xffu);

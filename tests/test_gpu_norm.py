@@ -173,7 +173,7 @@ def _write_rows(x):
     """The 4-bit rows of x [N, d] (as V of one head) through reshape_and_cache."""
     n = x.shape[0]
     c = torch.zeros(pa.int4_cache_shape(-(-n // 8), 1, 8), dtype=torch.uint8, device="cuda")
-    d = x.view(n, 1, 128).cuda()
+    d = x.reshape(n, 1, 128).contiguous().cuda()
     pa.reshape_and_cache(d, d, torch.zeros_like(c), c, torch.arange(n, device="cuda"), 8)
     assert pa.get_device_error() == 0
     codes, scale, zero = int4_cases.unpack(c.cpu(), 8)
@@ -252,3 +252,49 @@ def test_captured_and_replayed():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("where", ["far", "far_negative", "edges", "large_frequencies"])
+def test_far_positions_and_large_frequencies(interleaved, where):
+    """Angles against exact ones: at most 2^-26 turns for the float32 nearest to the fraction, 2^-32 for the bits below it, and
+    2^-62 for the step, times |p| <= 2^31.  The rest as in test_gpu_rope_far.py, whose exact angles these are: p = 2^16 h + l,
+    both times a float32 of at most 24 bits exact in 64."""
+    import math
+    from test_gpu_rope_far import exact_cos_sin
+    g = torch.Generator().manual_seed(60)
+    n = 64
+    near = torch.randint(0, 5000, (n,), generator=g)
+    pos = {"far": (1 << 31) - 1 - near, "far_negative": near - (1 << 31), "large_frequencies": near - 2500,
+           "edges": torch.tensor([0, 1, -1, (1 << 31) - 1, -(1 << 31), 1 << 30, -(1 << 30), 65535] * 8)}[where]
+    inv = pa.rope_frequencies(128)
+    if where == "large_frequencies":                       # 2^-140 .. 2^20 and both signs (exact in 64 bits with such positions)
+        inv = torch.exp2(torch.linspace(-140, 20, 64, dtype=F64)).float() * torch.where(torch.arange(64) % 2 == 0, 1.0, -1.0)
+    q = torch.randn((n, 3, 128), generator=g).to(torch.float16)
+    c = torch.zeros((n // 16, 3, 16, 128), dtype=torch.float16, device="cuda")
+    got = pa.norm_rope_and_cache(q.cuda(), q.cuda(), q.cuda(), c, c.clone(), pos.cuda(), torch.arange(n, device="cuda"), inv.cuda(),
+                                 16, q_out=torch.empty_like(q, device="cuda"), interleaved=interleaved).cpu().to(F64)
+    assert pa.get_device_error() == 0
+    cos, sin = exact_cos_sin(pos, inv)
+    i = torch.arange(64)
+    lo, hi = (2 * i, 2 * i + 1) if interleaved else (i, i + 64)
+    x = q.to(F64)
+    a, b = x[..., lo], x[..., hi]
+    turns = 2.0 ** -26 + 2.0 ** -32 + 2.0 ** -31
+    size = (2 * math.pi * turns + 2.0 ** -21) * (a.abs() + b.abs())
+    for column, want in ((lo, a * cos[:, None] - b * sin[:, None]), (hi, b * cos[:, None] + a * sin[:, None])):
+        assert torch.all((got[..., column] - want).abs() <= HALF_STEP["f16"] * (want.abs() + size) + size)
+
+
+def test_halves_between_16_bit_values_go_to_the_even_code():
+    """Rows whose quotients are whole numbers and halves of a scale that is no power of two: (x - zero) / scale is exact."""
+    scale = torch.tensor([3.0, 5.0, 7.0, 0.375, 1.25])
+    rows = []
+    for s in scale.tolist():
+        y = torch.arange(128) % 31 * 0.5                   # 0, 0.5 .. 15
+        rows.append(y * s)
+    x = torch.stack(rows).to(torch.float16)                # exact: 5 bits times 3
+    codes, sc, zero = _write_rows(x)
+    assert torch.equal(sc, scale.to(F64)) and torch.all(zero == 0)
+    want = torch.round(torch.arange(128) % 31 * 0.5).to(torch.int64)
+    assert torch.equal(codes, want.expand(5, -1))
