@@ -599,6 +599,7 @@ typedef struct pa_attend_options {
   int64_t mass_stride_seq;
   int64_t mass_stride_head;
   int32_t pdl;
+  int32_t reserved; /* not read (padding of callers built before `sinks`) */
   int32_t sinks;
 } pa_attend_options;
 

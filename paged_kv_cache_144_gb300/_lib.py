@@ -60,7 +60,8 @@ class AttendOptions(ctypes.Structure):
                 ("v_zero_point", ctypes.c_void_p), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
                 ("window", ctypes.c_int32), ("prefix_lens", ctypes.c_void_p), ("tree_mask", ctypes.c_void_p),
                 ("tree_words", ctypes.c_int32), ("mass", ctypes.c_void_p), ("mass_stride_seq", ctypes.c_int64),
-                ("mass_stride_head", ctypes.c_int64), ("pdl", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+                ("mass_stride_head", ctypes.c_int64), ("pdl", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("sinks", ctypes.c_int32)]
 
     def __init__(self, *args, **kw):
         if args:                                   # every field in order, struct_size first
@@ -245,10 +246,11 @@ def dtype_code(t) -> int:
     return code
 
 
-def cache_dtype_code(cache) -> int:
-    """The type of a cache pool: 4-bit pools are uint8 [blocks, H_kv, tile bytes] (int4_cache_shape), the others
-    [blocks, H_kv, block_size, d] of their own type."""
-    if cache.dim() == 3 and cache.dtype is _torch().uint8:
+def cache_dtype_code(cache, block_size=None, head_dim=128) -> int:
+    """The type of a cache pool: 4-bit pools are uint8 [blocks, H_kv, tile bytes] (with block_size: of int4_cache_shape),
+    the others hold rows of their own type (uint8: E4M3)."""
+    if cache.dim() == 3 and cache.dtype is _torch().uint8 and (
+            block_size is None or tuple(cache.shape[1:]) == int4_cache_shape(0, cache.shape[1], block_size, head_dim)[1:]):
         return PA_INT4
     return dtype_code(cache)
 
@@ -349,7 +351,7 @@ def decode(out, q, k_cache, v_cache, block_tables, seq_lens, num_kv_heads, scale
     NB = k_cache.shape[0]
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (_ptr(out), dtype_code(out), _ptr(q), dtype_code(q), q.stride(0),
-            _ptr(k_cache), _ptr(v_cache), cache_dtype_code(k_cache), NB,
+            _ptr(k_cache), _ptr(v_cache), cache_dtype_code(k_cache, block_size, D), NB,
             _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
             S, Hq, int(num_kv_heads), D, float(scale), int(block_size), int(partition_size),
             _ptr(workspace), ws_bytes)
@@ -377,7 +379,7 @@ def decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_lens, num_kv_head
         raise ValueError("q rows must be contiguous per sequence")
     S, Hq, D = q.shape
     st = pa_decode_noalloc(_ptr(out), dtype_code(out), _ptr(q), dtype_code(q), q.stride(0),
-                           _ptr(k_cache), _ptr(v_cache), cache_dtype_code(k_cache), k_cache.shape[0],
+                           _ptr(k_cache), _ptr(v_cache), cache_dtype_code(k_cache, block_size, D), k_cache.shape[0],
                            _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
                            S, Hq, int(num_kv_heads), D, float(scale), int(block_size), int(partition_size),
                            _stream(stream))
@@ -404,11 +406,9 @@ def reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, block_size, *, k_inv
     for t in (k, v):
         if t.stride(2) != 1 or t.stride(1) != D:
             raise ValueError("k/v rows must be contiguous per token")
-    code = cache_dtype_code(k_cache)
-    if code == PA_INT4:
-        for t in (k_cache, v_cache):
-            if t.dtype is not k_cache.dtype or tuple(t.shape) != int4_cache_shape(k_cache.shape[0], Hkv, block_size, D):
-                raise ValueError("4-bit caches must be uint8 of int4_cache_shape(blocks, H_kv, block_size, d)")
+    code = cache_dtype_code(k_cache, block_size, D)
+    if code == PA_INT4 and (v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape or k_cache.shape[1] != Hkv):
+        raise ValueError("4-bit caches must both be uint8 of int4_cache_shape(blocks, H_kv, block_size, d)")
     args = (_ptr(k), _ptr(v), dtype_code(k), k.stride(0), v.stride(0),
             _ptr(k_cache), _ptr(v_cache), code, k_cache.shape[0],
             _ptr(slot_mapping), N, Hkv, D, int(block_size), _ptr(k_inv_scale), _ptr(v_inv_scale))

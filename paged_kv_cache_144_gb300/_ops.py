@@ -318,7 +318,7 @@ def _attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_le
                 raise ValueError("mass rows must hold block_tables.shape[1] * block_size positions")
         opt = ctypes.byref(AttendOptions(_OPT_SIZE, _ptr(k_zero_point), _ptr(v_zero_point), softcap, _ptr(slopes), int(window),
                                          _ptr(prefix_lens), _ptr(tree_mask), words, _ptr(mass), mseq, mhead,
-                                         1 if pdl else 0, int(sinks)))
+                                         1 if pdl else 0, 0, int(sinks)))
     _issue(load().pa_attend, dev, stream, out.data_ptr(), _code(out), q.data_ptr(), _code(q), qs, k_cache.data_ptr(),
            v_cache.data_ptr(), _cache_code(k_cache), blocks, _ptr(k_scale), _ptr(v_scale), block_tables.data_ptr(), width,
            seq_lens.data_ptr(), starts, int(max_q_len), N, S, Hq, Hkv, D, scale, int(block_size), ws, wb, opt)
@@ -342,7 +342,8 @@ def attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_len
     q, out [N, H_q, d]: sequence s owns rows q_starts[s] .. q_starts[s + 1] - 1 (q_starts int32 [S + 1]; None: one
     query per sequence), its newest positions; max_q_len >= the most queries of one sequence.
     softcap > 0: scores softcap * tanh(score / softcap).  slopes [H_q]: - slopes[h] * distance is added.
-    window > 0: the last `window` positions only, and the first `sinks`.  prefix_lens int32 [S]: the first positions are seen by all queries.
+    window > 0: the last `window` positions only, and the first `sinks` of the sequence.  prefix_lens int32 [S]: the
+    first positions are seen by all queries.
     workspace: new_workspace(attend_workspace_bytes(...)), not shared by calls that may overlap.
     """
     return _attend(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_len, num_kv_heads, scale,

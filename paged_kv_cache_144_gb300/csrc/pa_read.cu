@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) read_cache_kernel(const ReadArgs a) 
     head[k] = 0;
     if (x >= total) continue;
     const int64_t n = x < (int64_t{1} << 32) ? static_cast<uint32_t>(x) / static_cast<uint32_t>(Hk) : x / Hk;
-    const int64_t slot = __ldg(a.slots + n);
+    const int64_t slot = a.slots[n];
     head[k] = static_cast<int>(x - n * Hk);
     if (slot < 0) continue;  // padding
     if (slot >= a.num_blocks * B) {
@@ -65,10 +65,10 @@ __global__ void __launch_bounds__(kThreads) read_cache_kernel(const ReadArgs a) 
       const uint8_t* const cache = static_cast<const uint8_t*>(v ? a.v_cache : a.k_cache);
       if constexpr (std::is_same<KVT, i4_t>::value) {
         const uint8_t* const at = cache + tile * (static_cast<int64_t>(B) * int4_row_bytes(D));
-        code[k][v] = __ldg(reinterpret_cast<const uint32_t*>(at + row * (D / 2)) + l);
-        pair[k][v] = __ldg(reinterpret_cast<const uint32_t*>(at + B * (D / 2)) + row);
+        code[k][v] = reinterpret_cast<const uint32_t*>(at + row * (D / 2))[l];
+        pair[k][v] = reinterpret_cast<const uint32_t*>(at + B * (D / 2))[row];
       } else {
-        code[k][v] = __ldg(reinterpret_cast<const C*>(cache + (tile * B + row) * (D * elem<KVT>::bytes)) + l);
+        code[k][v] = reinterpret_cast<const C*>(cache + (tile * B + row) * (D * elem<KVT>::bytes))[l];
       }
     }
   }

@@ -109,6 +109,29 @@ def test_option_struct_layout():
     assert pa.NormOptions().struct_size == 40
 
 
+def test_options_of_callers_built_before_sinks(lib):
+    """Their struct ends with 4 bytes of padding, whose contents mean nothing."""
+    o = pa.AttendOptions(window=8)
+    old = pa.AttendOptions.sinks.offset
+    assert old % 8 == 0
+    o.struct_size, o.reserved, o.sinks = old, -1, -1
+    args = (A, pa.PA_F32, A, pa.PA_BF16, 1024, A, A2, pa.PA_BF16, 100, None, None, A, 16, A, A, 4, 0, 3, 8, 2, 128, 0.1, 16,
+            None, 0)
+    assert lib.pa_attend(*args, ctypes.byref(o), None) == pa.PA_OK
+    o.struct_size = ctypes.sizeof(o)
+    assert lib.pa_attend(*args, ctypes.byref(o), None) == pa.PA_ERR_SHAPE
+    o.sinks = 4
+    assert lib.pa_attend(*args, ctypes.byref(o), None) == pa.PA_OK
+
+
+def test_uint8_pools_of_three_dimensions(lib):
+    """An E4M3 pool whose rows are flattened stays one."""
+    four, eight = (torch.zeros(s, dtype=torch.uint8) for s in (pa.int4_cache_shape(3, 2, 16), (3, 2, 16 * 128)))
+    assert pa.cache_dtype_code(four, 16) == pa.PA_INT4
+    assert pa.cache_dtype_code(eight, 16) == pa.PA_FP8_E4M3
+    assert pa.cache_dtype_code(four, 16, 64) == pa.PA_FP8_E4M3
+
+
 def test_binding_refusals():
     q = torch.zeros((2, 4, 128), dtype=torch.bfloat16)
     c = torch.zeros(pa.int4_cache_shape(3, 2, 16), dtype=torch.uint8)
