@@ -33,7 +33,8 @@
  *    "PagedAttentionのメモリ管理": the block table maps logical blocks to
  *    physical blocks of B tokens).
  *  - Supported shapes: head_dim in {64, 128} for 16-bit caches, 128 for the
- *    8-bit (FP8, INT8) caches, which also take at most 256 KV heads; block_size a power of two from 8 to 1024 (16
+ *    8-bit (FP8, INT8) caches, which also take at most 256 KV heads, and for the
+ *    4-bit ones (pa_attend, pa_read_cache, the cache writes); block_size a power of two from 8 to 1024 (16
  *    and 32 are the usual sizes); num_heads = G * num_kv_heads with
  *    1 <= G <= 8; with q_len queries per sequence (pa_decode_ex),
  *    q_len * G <= 64.
@@ -541,7 +542,13 @@ int pa_read_cache(void* k_out, void* v_out, pa_dtype out_dtype, int64_t k_out_st
  * twice that with 8-bit caches or head_dim 128 - as one, off by up to 2^-8
  * (bf16 caches) or 2^-11 (others) of it: up to the size of a rounding of out
  * itself.  Ask for a float32 out where a prompt's rows have to be as exact as a
- * decode step's.
+ * decode step's.  Over 4-bit caches calls of few rows (max_q_len * G <= 16, and
+ * up to 64 where the cache is short) multiply the codes as they are; a weight
+ * times its row's scale enters as one float16 value (off by up to 2^-11 of it)
+ * with a bf16 out and max_q_len 1 (G <= 8), else as two.  Calls of more rows
+ * round each K and V value to float16 first, whatever out's type: scores of
+ * normal q and k are off by about 3e-4, and a float16 or float32 out by about
+ * 4e-4 of its size, twice float16's own rounding.
  *
  *   out            [num_tokens][num_heads][head_dim], out_dtype F32/F16/BF16,
  *                  16-byte aligned, not overlapping q (rows are read by

@@ -95,15 +95,15 @@ def _row_stride(name, t, tokens, heads, dim):
 def _cache(k_cache, v_cache, block_size):
     """(blocks, KV heads, head size) of the two pools."""
     shape = k_cache.shape
-    if len(shape) == 3 and k_cache.dtype is _U8:  # 4 bits
+    if len(shape) == 4 and shape[2] == block_size and k_cache.is_contiguous():
+        dim = shape[3]
+    elif len(shape) == 3 and k_cache.dtype is _U8:  # 4 bits
         dim = 2 * (shape[2] // block_size - 4) if block_size > 0 else 0
         if dim <= 0 or shape != int4_cache_shape(shape[0], shape[1], block_size, dim) or not k_cache.is_contiguous():
             raise ValueError(f"a 4-bit k_cache must be contiguous, of int4_cache_shape(blocks, H_kv, {block_size}), not "
                              f"{tuple(shape)}")
     else:
-        if len(shape) != 4 or shape[2] != block_size or not k_cache.is_contiguous():
-            raise ValueError(f"k_cache must be contiguous [blocks, H_kv, {block_size}, d], not {tuple(shape)}")
-        dim = shape[3]
+        raise ValueError(f"k_cache must be contiguous [blocks, H_kv, {block_size}, d], not {tuple(shape)}")
     if v_cache.shape != shape or v_cache.dtype is not k_cache.dtype or not v_cache.is_contiguous():
         raise ValueError("v_cache must be contiguous, of the shape and type of k_cache")
     return shape[0], shape[1], dim
@@ -151,16 +151,21 @@ def rope_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, orig
     return f.float()
 
 
-def _write_rotated(norm, q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, block_size, q_out, interleaved,
-                   rope_scale, k_inv_scale, v_inv_scale, k_zero_point, v_zero_point, pdl, stream):
-    """rope_and_cache (norm None) and norm_rope_and_cache (norm: q_weight, k_weight, eps, weight_offset)."""
+def rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, block_size, *, q_out=None,
+                   interleaved=False, rope_scale=1.0, k_inv_scale=None, v_inv_scale=None, k_zero_point=None,
+                   v_zero_point=None, pdl=False, stream=None, _norm=None):
+    """Rotary positions of q and k, and the cache write of k and v (pa_rope_and_cache).
+
+    q [N, H_q, d], k / v [N, H_kv, d]; positions and slot_mapping int64 [N]; inv_freq float32 [rotary_dim / 2].
+    The turned q goes to q_out (default: q itself), the turned k and v into their slots; tokens with a negative slot
+    are padding and left alone.  pdl as in reshape_and_cache.  Returns q_out.
+    """
+    # (_norm: q_weight, k_weight, eps and weight_offset of norm_rope_and_cache, which has these checks too)
+    _torch or _t()
     if q_out is None:
         q_out = q
-    qw = kw = None
-    if norm is not None:
-        qw, kw = norm[:2]
     dev = _on_one_device(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, q_out, k_inv_scale, v_inv_scale,
-                         k_zero_point, v_zero_point, qw, kw)
+                         k_zero_point, v_zero_point)
     N, Hq, D = q.shape
     blocks, Hkv, dim = _cache(k_cache, v_cache, block_size)
     if dim != D:
@@ -173,18 +178,11 @@ def _write_rotated(norm, q, k, v, k_cache, v_cache, positions, slot_mapping, inv
     ks, vs = _row_stride("k", k, N, Hkv, D), _row_stride("v", v, N, Hkv, D)
     tokens = (N,)
     _need("slot_mapping", slot_mapping, _I64, tokens)
-    pos = freq = None
-    pairs = 0
-    if inv_freq is not None:
+    if _norm is None or inv_freq is not None:
+        if inv_freq is None or positions is None:
+            raise ValueError("inv_freq needs positions, and they it")
         _need("inv_freq", inv_freq, _F32, inv_freq.shape[:1])
-        pairs = inv_freq.shape[0]
-    if positions is not None:
         _need("positions", positions, _I64, tokens)
-        pos = positions.data_ptr()
-    elif pairs:
-        raise ValueError("inv_freq needs positions")
-    if pairs:
-        freq = inv_freq.data_ptr()
     opt = ki = vi = None
     if k_inv_scale is not None or v_inv_scale is not None:
         _heads_params(Hkv, (k_inv_scale, v_inv_scale), (k_zero_point, v_zero_point))
@@ -192,37 +190,29 @@ def _write_rotated(norm, q, k, v, k_cache, v_cache, positions, slot_mapping, inv
     if k_zero_point is not None or v_zero_point is not None or pdl:
         opt = ctypes.byref(CacheWriteOptions(k_zero_point=_ptr(k_zero_point), v_zero_point=_ptr(v_zero_point),
                                              pdl=1 if pdl else 0))
-    args = (q_out.data_ptr(), qos, q.data_ptr(), qs, Hq, k.data_ptr(), v.data_ptr(), _code(q), ks, vs, k_cache.data_ptr(),
-            v_cache.data_ptr(), _cache_code(k_cache), blocks, pos, slot_mapping.data_ptr(), freq, 2 * pairs,
-            1 if interleaved else 0, rope_scale, N, Hkv, D, int(block_size))
-    if norm is None:
-        _issue(load().pa_rope_and_cache, dev, stream, *args, ki, vi, opt)
+    if _norm is None:
+        _issue(load().pa_rope_and_cache, dev, stream, q_out.data_ptr(), qos, q.data_ptr(), qs, Hq, k.data_ptr(),
+               v.data_ptr(), _code(q), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), _cache_code(k_cache), blocks,
+               positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0],
+               1 if interleaved else 0, rope_scale, N, Hkv, D, int(block_size), ki, vi, opt)
         return q_out
+    qw, kw, eps, offset = _norm
     wd = 0
     for name, w in (("q_weight", qw), ("k_weight", kw)):
         if w is not None:
+            _on_one_device(q, w)
             _need(name, w, w.dtype, (D,))
             wd = _code(w)
     if qw is not None and kw is not None and qw.dtype is not kw.dtype:
         raise ValueError("q_weight and k_weight must have one type")
-    _issue(load().pa_norm_rope_and_cache, dev, stream, *args,
-           ctypes.byref(NormOptions(q_weight=_ptr(qw), k_weight=_ptr(kw), weight_dtype=wd, weight_offset=norm[3],
-                                    eps=norm[2])), ki, vi, opt)
+    pairs = 0 if inv_freq is None else inv_freq.shape[0]
+    _issue(load().pa_norm_rope_and_cache, dev, stream, q_out.data_ptr(), qos, q.data_ptr(), qs, Hq, k.data_ptr(),
+           v.data_ptr(), _code(q), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), _cache_code(k_cache), blocks,
+           _ptr(positions) if pairs else None, slot_mapping.data_ptr(), inv_freq.data_ptr() if pairs else None, 2 * pairs,
+           1 if interleaved else 0, rope_scale, N, Hkv, D, int(block_size),
+           ctypes.byref(NormOptions(q_weight=_ptr(qw), k_weight=_ptr(kw), weight_dtype=wd, weight_offset=offset, eps=eps)),
+           ki, vi, opt)
     return q_out
-
-
-def rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, block_size, *, q_out=None,
-                   interleaved=False, rope_scale=1.0, k_inv_scale=None, v_inv_scale=None, k_zero_point=None,
-                   v_zero_point=None, pdl=False, stream=None):
-    """Rotary positions of q and k, and the cache write of k and v (pa_rope_and_cache).
-
-    q [N, H_q, d], k / v [N, H_kv, d]; positions and slot_mapping int64 [N]; inv_freq float32 [rotary_dim / 2].
-    The turned q goes to q_out (default: q itself), the turned k and v into their slots; tokens with a negative slot
-    are padding and left alone.  pdl as in reshape_and_cache.  Returns q_out.
-    """
-    _torch or _t()
-    return _write_rotated(None, q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, block_size, q_out,
-                          interleaved, rope_scale, k_inv_scale, v_inv_scale, k_zero_point, v_zero_point, pdl, stream)
 
 
 def norm_rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, block_size, *, q_weight=None,
@@ -234,10 +224,10 @@ def norm_rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_
     q_weight / k_weight [d] (float32, float16 or bfloat16); None: that tensor is not normalised.  positions and inv_freq
     may be None: nothing is turned.  4-bit caches (int4_cache_shape) need no scales.  Returns q_out.
     """
-    _torch or _t()
-    return _write_rotated((q_weight, k_weight, float(eps), float(weight_offset)), q, k, v, k_cache, v_cache, positions,
-                          slot_mapping, inv_freq, block_size, q_out, interleaved, rope_scale, k_inv_scale, v_inv_scale,
-                          k_zero_point, v_zero_point, pdl, stream)
+    return rope_and_cache(q, k, v, k_cache, v_cache, positions, slot_mapping, inv_freq, block_size, q_out=q_out,
+                          interleaved=interleaved, rope_scale=rope_scale, k_inv_scale=k_inv_scale, v_inv_scale=v_inv_scale,
+                          k_zero_point=k_zero_point, v_zero_point=v_zero_point, pdl=pdl, stream=stream,
+                          _norm=(q_weight, k_weight, float(eps), float(weight_offset)))
 
 
 def read_cache(k_out, v_out, k_cache, v_cache, slot_mapping, block_size, *, k_scale=None, v_scale=None,

@@ -1302,6 +1302,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       // (a negative scale would turn the maximum of raw products into a minimum)
       const bool modified = a.softcap > 0.f || a.slopes || !(sc2 >= 0.f);
       float m = -INFINITY, l = 0.f;
+      // (as first_of, from registers: 187 -> 183 us where 1-2K queries see 1024 + 4 positions)
+      [[maybe_unused]] const int lo_tile = f.lo / kTile, seg_lo = f.seg_lo;
 
       for (int j = j0; ok && j < f.t1; j += step, ++jobs) {
         // Half a tile at a time: while one half's weights are computed, the tensor cores multiply the other's and compute the
@@ -1318,7 +1320,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           }
           if (warp_on) {
             // positions of the half: 32 from tb, 32 from tb + gap on
-            const int tb = first_of(j) + half * (CG == 1 ? kHalfTile : 32);
+            const int tb = (!SINKS || j >= lo_tile ? j : j - seg_lo) * kTile + half * (CG == 1 ? kHalfTile : 32);
             constexpr int kGap = CG == 1 ? 32 : kHalfTile;
             const uint32_t ps = ts + half * kHalfTile;  // the half's scores; its weights replace them (hi, then lo)
             float z[kHalfTile];
@@ -1350,7 +1352,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                   z[c] = fmaf(-slope2, fabsf(d0 + static_cast<float>((c >> 5) * kGap + (c & 31))), z[c]);
               }
             }
+            // SINKS: chunks of 32 that some row of the warp sees, and whether this row sees any: the others get no exponentials
+            // (the window's edges, the sinks and the end lie in a third of a segment's tiles there: 192 -> 187 us)
+            [[maybe_unused]] uint32_t on = 3u;
+            [[maybe_unused]] bool sees = true;
             if (masked) {
+              if constexpr (SINKS) sees = false;
 #pragma unroll
               for (int c = 0; c < kHalfTile / 32; ++c) {
                 const int b0 = tb + kGap * c;
@@ -1363,6 +1370,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 }
                 uint32_t see = (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & from;
                 if (tree && valid) see &= tree_bits(tree, a.tree_words, first, b0);
+                if constexpr (SINKS) {
+                  sees |= see != 0u;
+                  if (!__any_sync(0xffffffffu, see != 0u)) on &= ~(1u << c);
+                  if (__all_sync(0xffffffffu, see == 0xffffffffu || !valid)) continue;
+                }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) z[32 * c + k] = (see >> k) & 1u ? z[32 * c + k] : -INFINITY;
               }
@@ -1404,6 +1416,15 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
               for (int c = 0; c < kHalfTile / 32; ++c) {
                 float2 w[16];
                 uint32_t hi[16];
+                if constexpr (SINKS) {
+                  if (!(on >> c & 1u)) {  // nothing seen: no weights
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) hi[k] = 0u;
+                    tmem_st16(ps + 16 * c, hi);
+                    if constexpr (SPLIT) tmem_st16(ps + kHalfTile / 2 + 16 * c, hi);
+                    continue;
+                  }
+                }
 #pragma unroll
                 for (int k = 0; k < 16; ++k) w[k] = ffma2(make_float2(z[32 * c + 2 * k], z[32 * c + 2 * k + 1]), mul2, neg);
 #pragma unroll
@@ -1428,7 +1449,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
               }
               sum0 = fadd2(sum0, sum1);
               lt = sum0.x + sum0.y;
-              if (again || !__any_sync(0xffffffffu, valid && (lt > kMost || m == -INFINITY))) break;
+              if constexpr (SINKS) {
+                if (again || !__any_sync(0xffffffffu, valid && (lt > kMost || (sees && m == -INFINITY)))) break;
+              } else {
+                if (again || !__any_sync(0xffffffffu, valid && (lt > kMost || m == -INFINITY))) break;
+              }
             }
             l += lt;
             tmem_wait_st();
