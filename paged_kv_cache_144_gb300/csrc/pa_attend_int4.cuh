@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(Int4Traits::WARPS * 32, 1) attend_int4_kernel(
   float q_sum[2], z_sum[2];    // of rows 2t, 2t + 1
   float m[2], l[2];
   float acc[KS][4];            // O^T: columns 16 g + 2 i (+ 1: elements 2, 3) of rows 2t, 2t + 1
-  float score_unit = 0.f;      // what a K scale is multiplied by: units of the codes and the queries, the softmax's scale
+  float score_unit[2] = {};    // of rows 2t, 2t + 1, what a K scale is multiplied by: units of the codes and the row, the softmax's scale
   const float cap2 = p.att.softcap * kLog2e, capk = p.att.softcap > 0.f ? 2.f / p.att.softcap : 0.f;
   // Scaled weights go to f16 times 2^(29 - vexp): 2^15 over a power of two above the scales seen so far, so that none
   // exceeds f16 and those down to 2^-39 of the largest count; O follows when a larger scale comes, as it follows the maximum.
@@ -258,11 +258,11 @@ __global__ void __launch_bounds__(Int4Traits::WARPS * 32, 1) attend_int4_kernel(
       const float2 a = widen2<QT>(w.x), b = widen2<QT>(w.y);
       top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // The products run in f16: the group's rows are multiplied by the power of two that puts their largest element at 2^14 ..
-    // 2^15, and the columns whose codes are in units of 2^-20, not 2^-24, by 2^-4 of it.  Exact for elements within 2^24 of
-    // the largest; smaller ones may round as subnormals.
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // The products run in f16: each row is multiplied by the power of two that puts its largest element at 2^14 .. 2^15, and
+    // the columns whose codes are in units of 2^-20, not 2^-24, by 2^-4 of it.  Exact for elements within 2^24 of the row's
+    // largest; smaller ones may round as subnormals.
     const int ebits = (__float_as_int(top) >> 23) & 0xff;
     const int qexp = top > 0.f ? min(100, max(-100, 141 - ebits)) : 0;
     const float by = __int_as_float((127 + qexp) << 23);
@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(Int4Traits::WARPS * 32, 1) attend_int4_kernel(
     sum *= scale;
     q_sum[0] = __shfl_sync(0xffffffffu, sum, 8 * tig);
     q_sum[1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4);
-    score_unit = scale * kCodeUnit;
+    score_unit[0] = __shfl_sync(0xffffffffu, scale, 8 * tig) * kCodeUnit;
+    score_unit[1] = __shfl_sync(0xffffffffu, scale, 8 * tig + 4) * kCodeUnit;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       m[e] = -INFINITY;
@@ -314,11 +315,11 @@ __global__ void __launch_bounds__(Int4Traits::WARPS * 32, 1) attend_int4_kernel(
       }
       const float2 p0 = widen2<f16_t>(lds32(stage + Tr::OFF_KP + mt * 64 + gid * 4));
       const float2 p1 = widen2<f16_t>(lds32(stage + Tr::OFF_KP + mt * 64 + gid * 4 + 32));
-      const float s0 = p0.x * score_unit, s1 = p1.x * score_unit;
-      sc[mt][0] = fmaf(sc[mt][0], s0, p0.y * q_sum[0]);
-      sc[mt][1] = fmaf(sc[mt][1], s0, p0.y * q_sum[1]);
-      sc[mt][2] = fmaf(sc[mt][2], s1, p1.y * q_sum[0]);
-      sc[mt][3] = fmaf(sc[mt][3], s1, p1.y * q_sum[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sc[mt][e] = fmaf(sc[mt][e], p0.x * score_unit[e], p0.y * q_sum[e]);
+        sc[mt][2 + e] = fmaf(sc[mt][2 + e], p1.x * score_unit[e], p1.y * q_sum[e]);
+      }
     }
     uint32_t v_pair[MT][2];
 #pragma unroll

@@ -977,7 +977,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
   // scale, and lacks sum(weight zero), which is added up apart in float32.  Scaled weights go to f16 times 2^(29 - vexp), which
   // is 2^15 over a power of two above the scales seen so far, so that none exceeds f16 and those down to 2^-39 of the largest
   // count; O follows when a larger scale comes, as it follows the maximum.  vexp: that scale's f16 exponent field (-1: none).
-  [[maybe_unused]] float q_sum[NR], z_sum[NR];  // of this lane's softmax rows
+  [[maybe_unused]] float q_sum[NR], q_unit[NR], z_sum[NR];  // of this lane's softmax rows (q_unit: units of the codes and the row)
   [[maybe_unused]] int vexp = -1;
   // the larger of the scales' bits so far and those of pair word w
   [[maybe_unused]] auto scale_bits = [](int most, uint32_t w) { return max(most, static_cast<int>(w & 0x7fffu)); };
@@ -1139,9 +1139,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float2 kp = widen2<f16_t>(lds32(kt + pairs_of(nt) + tau(2 * tig + e) * 4));
-            const float ks = kp.x * kCodeUnit;
 #pragma unroll
-            for (int h = 0; h < NH; ++h) sc[nt][2 * h + e] = fmaf(sc[nt][2 * h + e], ks, kp.y * q_sum[h]);
+            for (int h = 0; h < NH; ++h) sc[nt][2 * h + e] = fmaf(sc[nt][2 * h + e], kp.x * q_unit[h], kp.y * q_sum[h]);
           }
         }
       } else if constexpr (!k8bit) {
@@ -1543,9 +1542,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     // rounding of every element within 2^28 of the group's largest (bf16 has 8
     // significant bits, f16 11); smaller elements can lose bits as f16
     // subnormals, an absolute error below 2^-38 of the largest element.
-    // 4-bit caches: f16 queries too, since the codes' units (nibbles4) put half of each row's elements 2^4 below the others: exact
-    // within 2^24 of the largest.
-    constexpr bool q_rescale = (k8bit && std::is_same<QT, bf16_t>::value) || k4bit;
+    // (4-bit caches: each row for itself, f16 queries too, since the codes' units (nibbles4) put half of a row's elements 2^4
+    // below the others: exact within 2^24 of the row's largest.)
+    constexpr bool q_rescale = k8bit && std::is_same<QT, bf16_t>::value;
     int qexp = 0;
     [[maybe_unused]] int64_t row_base = 0;  // pa_attend: the sequence's first row of q and out
     if constexpr (ATT) {
@@ -1625,10 +1624,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     if constexpr (q_rescale) {
       // largest |q| of the group (bf16 halves read as floats), over the warp
       auto amax2 = [](float a, uint32_t w) {
-        if constexpr (std::is_same<QT, f16_t>::value) {
-          const float2 f = widen2<f16_t>(w);
-          return fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
         return fmaxf(a, fmaxf(__uint_as_float((w << 16) & 0x7fffffffu), __uint_as_float(w & 0x7fff0000u)));
       };
       float qmax = 0.f;
@@ -1644,36 +1639,51 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
       const int ebits = (__float_as_int(qmax) >> 23) & 0xff;
       qexp = qmax > 0.f ? min(100, max(-100, 141 - ebits)) : 0;
       const float mul = __int_as_float((127 + qexp) << 23);
-      const float mul1 = k4bit ? mul * 0.0625f : mul;  // (4-bit: the codes of these columns are in units of 2^-20, not 2^-24)
-      auto narrow = [](uint32_t w, float by) {
-        const float2 f = widen2<QT>(w);
-        return pack2<false>(f.x * by, f.y * by);
+      auto narrow = [&](uint32_t w) {
+        const float2 f = widen2<bf16_t>(w);
+        return pack2<false>(f.x * mul, f.y * mul);
       };
 #pragma unroll
       for (int s = 0; s < Tr::KS; ++s) {
-        qa0[s] = narrow(qa0[s], mul);
-        qa1[s] = narrow(qa1[s], mul1);
+        qa0[s] = narrow(qa0[s]);
+        qa1[s] = narrow(qa1[s]);
         if constexpr (NH == 2) {
-          qb0[s] = narrow(qb0[s], mul);
-          qb1[s] = narrow(qb1[s], mul1);
+          qb0[s] = narrow(qb0[s]);
+          qb1[s] = narrow(qb1[s]);
         }
       }
     }
     if constexpr (k4bit) {
       vexp = -1;
-      // the sums of query rows g and g + 8, as they enter the products
-      auto sum_row = [&](const uint32_t(&a)[Tr::KS], const uint32_t(&b)[Tr::KS]) {
-        float x = 0.f;
+      // query rows g and g + 8, each with a power of two of its own: its largest element to 2^14 .. 2^15; and their sums as
+      // they enter the products
+      auto take_row = [&](uint32_t(&a)[Tr::KS], uint32_t(&b)[Tr::KS], int h) {
+        float top = 0.f, x = 0.f;
 #pragma unroll
         for (int s = 0; s < Tr::KS; ++s) {
-          const float2 f = widen2<f16_t>(a[s]), g = widen2<f16_t>(b[s]);
-          x += fmaf(16.f, g.x + g.y, f.x + f.y);
+          const float2 f = widen2<QT>(a[s]), g = widen2<QT>(b[s]);
+          top = fmaxf(fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(g.x), fabsf(g.y)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = top > 0.f ? min(100, max(-100, 141 - ((__float_as_int(top) >> 23) & 0xff))) : 0;
+        const float by = __int_as_float((127 + e) << 23);
+#pragma unroll
+        for (int s = 0; s < Tr::KS; ++s) {
+          const float2 f = widen2<QT>(a[s]), g = widen2<QT>(b[s]);
+          a[s] = pack2<false>(f.x * by, f.y * by);
+          b[s] = pack2<false>(g.x * by * 0.0625f, g.y * by * 0.0625f);  // (the codes of these columns are in units of 2^-20)
+          const float2 y = widen2<f16_t>(a[s]), z = widen2<f16_t>(b[s]);
+          x += fmaf(16.f, z.x + z.y, y.x + y.y);
         }
         x += __shfl_xor_sync(0xffffffffu, x, 1);
-        return x + __shfl_xor_sync(0xffffffffu, x, 2);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        const float back = __int_as_float((127 - e) << 23);
+        q_sum[h] = x * back;
+        q_unit[h] = back * kCodeUnit;
       };
-      q_sum[0] = sum_row(qa0, qa1);
-      q_sum[1] = sum_row(qb0, qb1);
+      take_row(qa0, qa1, 0);
+      take_row(qb0, qb1, 1);
     }
     score_scale = p.qk_scale_log2;
     if constexpr (k8bit) score_scale *= hp_ks[it.kvh];

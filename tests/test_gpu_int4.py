@@ -123,6 +123,23 @@ def test_queries_beyond_the_range_of_float16(mult):
         assert torch.equal(got, plain)
 
 
+@pytest.mark.parametrize("value", [2.0 ** 60, float("inf"), float("nan")])
+@pytest.mark.parametrize("qlens", [[1, 1], [3, 2], [40, 64]])
+def test_a_head_out_of_range_does_not_disturb_the_others(qlens, value):
+    """Each query row enters the f16 products times a power of two of its own."""
+    c = Case([300, 77], qlens, kv="i4", seed=29)
+    ref, wabs, _ = c.reference()
+    tol = c.tolerance("f32", ref, wabs)
+    c.q_wide = c.q_wide.clone()
+    c.q_wide[:, 1, 5] = value
+    c.q = c.q_wide[:, :c.heads]
+    got, err = run(c)
+    assert err == 0
+    rest = [0] + list(range(2, c.heads))
+    n = sum(qlens)
+    assert torch.all((got - ref).abs()[:n, rest] <= tol[:n, rest])
+
+
 @pytest.mark.parametrize("spread,shift", [(2.0 ** -12, 0.0), (0.05, 40.0), (300.0, -1000.0)])
 def test_rows_of_other_sizes(spread, shift):
     """Small values, rows far from zero, large ones.  Queries and scale are chosen so that the scores stay near one; K's size
