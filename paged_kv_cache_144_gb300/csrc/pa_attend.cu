@@ -16,7 +16,7 @@ namespace {
 //   bf16, 2^19 positions: 32 rows 72 / 103, 48 rows 90 / 101, 64 rows 127 / 105;  2^16: 64 rows 27 / 63
 //   e4m3, 2^20 positions: 32 rows 135 / 254, 48 rows 192 / 255, 64 rows 281 / 257;  2^19: 64 rows 134 / 131
 //   4 bits, 2^22 positions: 32 rows 788 / 785;  2^20: 32 rows 217 / 270, 48 rows 311 / 275;  2^19: 48 rows 169 / 185, 64 rows
-//   248 / 190;  2^16: 64 rows 62 / 138
+//   248 / 190;  2^16: 64 rows 54 / 138
 constexpr int kFewRows = 64;
 bool few_rows(int64_t rows, int64_t positions, bool q8, bool q4) {
   const int64_t row_groups = (rows + 15) / 16;

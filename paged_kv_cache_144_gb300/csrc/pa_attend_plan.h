@@ -27,7 +27,6 @@ cudaError_t launch_tc_fp8(const AttendParams& a, const Plan& pl, uint8_t* ws, cu
 cudaError_t launch_tc_int8(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream);
 cudaError_t launch_tc_int4(const AttendParams& a, const Plan& pl, uint8_t* ws, cudaStream_t stream);
 
-
 // One query per sequence over a 4-bit cache, up to 8 heads per KV head: attend_int4_kernel.
 bool int4_geometry(int num_seqs, DecodeGeometry* geo);
 cudaError_t launch_int4(const DecodeGeometry& geo, const DecodeParams& p, int q_dtype, cudaStream_t stream, bool pdl);

@@ -814,7 +814,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     const uint32_t vt = base + Tr::OFF_V + st * Tr::STAGE;
     for (int x = lane; x < kTile * Tr::VH * 8; x += 32) {
       const int r = x / (Tr::VH * 8), c = x % (Tr::VH * 8);
-      if (r >= n_hi || (r < n_lo && !(SINKS && r < n_sinks))) sts128_zero(vt + (r >> 3) * Tr::VGROUP + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16);
+      if (r >= n_hi || (r < n_lo && !(SINKS && r < n_sinks)))
+        sts128_zero(vt + (r >> 3) * Tr::VGROUP + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -1233,7 +1234,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 const int x = k * 128 + tid, row = x >> 2, c = 2 * (x & 3);
                 uint4 lo, hi;
                 widen16(w[k], zv2, lo, hi);
-                if (row >= n_hi || (row < n_lo && !(SINKS && row < n_sinks))) lo = hi = make_uint4(0u, 0u, 0u, 0u);  // outside the sequence or the window
+                if (row >= n_hi || (row < n_lo && !(SINKS && row < n_sinks)))  // outside the sequence or the window
+                  lo = hi = make_uint4(0u, 0u, 0u, 0u);
                 uint8_t* const to = sm + Tr::OFF_V + st * Tr::STAGE + (row >> 3) * Tr::VGROUP + (row & 7) * 128;
                 *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) = lo;
                 *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) << 4)) = hi;

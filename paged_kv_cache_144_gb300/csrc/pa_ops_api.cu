@@ -1,7 +1,7 @@
 // pa_ops_api.cu - the extern "C" entry points of the operators around the
 // cache (rotary cache write with and without norms, rows read back, attention
-// with score modifiers, tree commit, eviction): argument validation and dispatch.  No call here allocates device
-// memory.
+// with score modifiers, tree commit, eviction): argument validation and
+// dispatch.  No call here allocates device memory.
 #include <cmath>
 #include <cstring>
 
